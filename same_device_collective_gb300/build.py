@@ -23,7 +23,7 @@ STEP_TOOL = os.path.join(PKG, "rank_local_step")
 
 SOURCES = ["dt_group.cpp", "dt_reduce.cu", "dt_reduce_shift.cu", "dt_copy.cu", "dt_bucket.cu",
            "dt_barrier.cu", "dt_static.cu"]
-HEADERS = ["dt_internal.h", "dt_group.h", "dt_math.cuh", "dt_device.cuh", "dt_shift.cuh",
+HEADERS = ["dt_internal.h", "dt_group.h", "dt_host.h", "dt_math.cuh", "dt_device.cuh", "dt_shift.cuh",
            "dt_reduce_shift.h", "dt_timeline.cuh", "dt_timeline.h", "dt_bounds.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
