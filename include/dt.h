@@ -312,6 +312,56 @@ dt_status dt_bucket_allreduce_static(int world_size, void *const *grads, const s
                                      size_t n_tensors, int dtype, int op,
                                      size_t bucket_cap_bytes, void *stream);
 
+/* ------------------------------------------------ layer norm, group-wide */
+
+/* Layer norm over the last dimension of every rank's rows, as a
+ * sequence-parallel model has it: the activations are S(0) (rank r holds its
+ * own rows), the weights R (one copy serves every rank on this GPU), and the
+ * weights' gradients P, reduced over the ranks by the backward call itself.
+ * Like the bucket all-reduce, these calls are group-wide only.
+ *   x[r], y[r]     rank r's rows (rows[r], or rows_equal when rows is NULL) of
+ *                  cols elements of dtype (DT_F32 or DT_BF16), dense; y[r] may
+ *                  equal x[r] (in place).  A rank may have no rows.
+ *   weight, bias   cols elements of weight_dtype (DT_F32 or DT_BF16), shared
+ *                  by all ranks; NULL: ones, zeros
+ *   mean, rstd     per rank rows[r] floats, written: what the backward call
+ *                  reads; either array, or any entry, may be NULL
+ *   eps            finite, >= 0
+ * With mu the mean of a row and v the mean of (x - mu)^2, both fp32 and v from
+ * the differences: rstd = 1 / sqrt(v + eps), y = (x - mu) * rstd * weight +
+ * bias, rounded once.  A NaN or an infinity in a row makes that row NaN.
+ * Every pointer must be a multiple of its element size; rows that all start on
+ * 16-byte boundaries move as vectors, others element by element.  cols is
+ * 1..2^24.  A buffer may otherwise overlap no output. */
+dt_status dt_layer_norm(dt_group_t g, const void *const *x, const void *weight, const void *bias,
+                        void *const *y, float *const *mean, float *const *rstd, const size_t *rows,
+                        size_t rows_equal, size_t cols, float eps, int dtype, int weight_dtype,
+                        void *stream);
+
+/* The backward pass.  With h = (x - mean) * rstd and q = dy * weight:
+ *   dx[r]     = rstd * (q - mean(q) - h * mean(q * h)), of dtype; may equal
+ *               dy[r] (in place)
+ *   dweight   = the sum over every row of every rank of dy * h, of
+ *               weight_dtype; dbias the same of dy; either may be NULL.  op
+ *               DT_SUM, or DT_AVG: divided by the number of ranks, the mean
+ *               of the ranks' gradients.  With no rows at all they are 0.
+ *   mean, rstd  as the forward call wrote them
+ *   workspace   at least dt_layer_norm_workspace(g, cols) bytes of device
+ *               memory, 16-byte aligned, free for other use once `stream` has
+ *               passed the call; NULL when neither gradient is wanted
+ * The sums over rows are fp32 and their order depends on the GPU and the
+ * shapes only: repeated calls give the same bits. */
+dt_status dt_layer_norm_backward(dt_group_t g, const void *const *x, const void *const *dy,
+                                 const void *weight, const float *const *mean,
+                                 const float *const *rstd, void *const *dx, void *dweight,
+                                 void *dbias, const size_t *rows, size_t rows_equal, size_t cols,
+                                 int dtype, int weight_dtype, int op, void *workspace,
+                                 size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of dt_layer_norm_backward for rows of cols elements, any
+ * number of them; 0 for an invalid argument. */
+size_t dt_layer_norm_workspace(dt_group_t g, size_t cols);
+
 /* ----------------------------------------------------------- async work */
 
 /* Asynchronous collectives, after the async mode of "通信与互联（05）" §四.3
@@ -382,6 +432,7 @@ dt_status dt_debug_barrier_expect(dt_group_t g, int extra, uint32_t timeout_ms, 
 #define DT_TL_BUCKET_BARRIER 8  /* bucket all-reduce, the barrier block after a bucket */
 #define DT_TL_BARRIER 9         /* signal-window barrier kernel */
 #define DT_TL_MARK 10           /* dt_timeline_mark: block = the caller's tag */
+#define DT_TL_NORM 11           /* layer norm, either pass, and the join of its weight gradients */
 typedef struct {
     uint64_t grid;       /* the launch's %gridid */
     uint32_t kind;       /* DT_TL_* */
@@ -433,6 +484,7 @@ dt_status dt_timeline_mark(void *stream, uint32_t tag);
 #define DT_BOUNDS_COPY_SHIFT 6
 #define DT_BOUNDS_COPY_2D 7
 #define DT_BOUNDS_BUCKET 8
+#define DT_BOUNDS_NORM 9         /* layer norm; buffers: x r, dy 16 + r, y or dx 32 + r, mean 48 + r, rstd 64 + r */
 uint32_t dt_build_flags(void);
 
 #ifdef __cplusplus

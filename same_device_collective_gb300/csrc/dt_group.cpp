@@ -27,6 +27,7 @@
 
 #include "dt_group.h"
 #include "dt_host.h"
+#include "dt_ops.h"
 #include "dt_reduce_shift.h"
 #include "dt_timeline.h"
 
@@ -1452,6 +1453,7 @@ dt_status dt_timeline_start(size_t max_records)
     dt::bind_timeline_copy(&sink);
     dt::bind_timeline_bucket(&sink);
     dt::bind_timeline_barrier(&sink);
+    dt::bind_timeline_norm(&sink);
     return cudaDeviceSynchronize() == cudaSuccess ? DT_OK : DT_ERR_CUDA;
 #else
     (void)max_records;

@@ -38,7 +38,7 @@ DT_SHARED_OUTPUT = 0x1
 DT_DEFAULT_BUCKET_CAP_BYTES = 25 << 20
 DT_BUILD_NVTX, DT_BUILD_TIMELINE, DT_BUILD_BOUNDS = 1, 2, 4
 BOUNDS_KERNELS = {1: "reduce", 2: "reduce_shift", 3: "copy_bulk", 4: "copy_vec", 5: "copy_edge",
-                  6: "copy_shift", 7: "copy_2d", 8: "bucket"}
+                  6: "copy_shift", 7: "copy_2d", 8: "bucket", 9: "norm"}
 
 DTYPES = {"f32": DT_F32, "bf16": DT_BF16, "i32": DT_I32}
 OPS = {"sum": DT_SUM, "avg": DT_AVG, "max": DT_MAX, "min": DT_MIN,
@@ -50,6 +50,7 @@ _sz = ctypes.c_size_t
 _szp = ctypes.POINTER(ctypes.c_size_t)
 _i = ctypes.c_int
 _u = ctypes.c_uint
+_f = ctypes.c_float
 _u32 = ctypes.c_uint32
 
 _SIGS = {
@@ -71,6 +72,10 @@ _SIGS = {
     "dt_bucket_plan": ([_szp, _sz, _sz, _sz, _szp, _szp], _i),
     "dt_bucket_allreduce_static": ([_i, _vpp, _szp, _sz, _i, _i, _sz, _vp], _i),
     "dt_barrier": ([_vp, _i, _vp], _i),
+    "dt_layer_norm": ([_vp, _vpp, _vp, _vp, _vpp, _vpp, _vpp, _szp, _sz, _sz, _f, _i, _i, _vp], _i),
+    "dt_layer_norm_backward": ([_vp, _vpp, _vpp, _vp, _vpp, _vpp, _vpp, _vp, _vp, _szp, _sz, _sz, _i, _i,
+                                _i, _vp, _sz, _vp], _i),
+    "dt_layer_norm_workspace": ([_vp, _sz], _sz),
     "dt_replicate_to_shard": ([_vp, _i, _vpp, _vpp, ctypes.POINTER(_i), _sz, _sz, _vp], _i),
     "dt_all_gather_into_vec": ([_vp, _i, _vpp, _vpp, _szp, _sz, _sz, _vp], _i),
     "dt_all_to_all_2d": ([_vp, _i, _vpp, _vpp, _sz, _sz, _sz, _i, _i, _vp], _i),
@@ -98,7 +103,8 @@ TIMELINE_DTYPE = np.dtype([("grid", np.uint64), ("kind", np.uint32), ("block", n
                            ("sm", np.uint32), ("pad", np.uint32), ("t_start", np.uint64),
                            ("t_waited", np.uint64), ("t_end", np.uint64)])
 TIMELINE_KINDS = {1: "reduce", 2: "reduce_shift", 3: "copy_bulk", 4: "copy_vec", 5: "copy_shift",
-                  6: "copy_2d", 7: "bucket", 8: "bucket_barrier", 9: "barrier", 10: "mark"}
+                  6: "copy_2d", 7: "bucket", 8: "bucket_barrier", 9: "barrier", 10: "mark",
+                  11: "norm"}
 
 
 class DtError(RuntimeError):
@@ -343,6 +349,55 @@ def _m_barrier(g: int, rank: int = DT_ALL_RANKS, stream=None) -> tuple:
     return (g, rank, _stream(stream))
 
 
+def _dense(*xs) -> None:
+    """The layer norm and loss calls describe dense buffers: refuse a tensor that is not one
+    (its address alone would be read as if it were)."""
+    for x in xs:
+        for t in x if isinstance(x, (list, tuple)) else (x,):
+            if hasattr(t, "is_contiguous") and not t.is_contiguous():
+                raise ValueError(f"tensor of shape {tuple(t.shape)} and strides {t.stride()} is not contiguous")
+
+
+def _workspace(ws) -> tuple:
+    """(address, bytes) of a workspace: a tensor, an (address, bytes) pair, or None."""
+    if ws is None:
+        return 0, 0
+    if isinstance(ws, tuple):
+        return ws
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _rows_array(rows):
+    return None if rows is None else (ctypes.c_size_t * max(len(rows), 1))(*rows)
+
+
+def _opt_ptr_array(xs):
+    return None if xs is None else _ptr_array(xs)
+
+
+def _m_layer_norm(g: int, x: Sequence, weight, bias, y: Sequence, mean, rstd, rows: Sequence | None,
+                  rows_equal: int, cols: int, eps: float, dtype, weight_dtype, stream=None) -> tuple:
+    """Layer norm of every rank's rows: x[r], y[r] are rank r's [rows[r], cols] (or rows_equal
+    rows); weight and bias (or None) serve all ranks; mean and rstd, lists of f32 tensors or
+    None, receive what dt_layer_norm_backward reads."""
+    _dense(x, weight, bias, y, mean, rstd)
+    return (g, _ptr_array(x), _ptr(weight), _ptr(bias), _ptr_array(y), _opt_ptr_array(mean),
+            _opt_ptr_array(rstd), _rows_array(rows), rows_equal, cols, eps, _code(DTYPES, dtype),
+            _code(DTYPES, weight_dtype), _stream(stream))
+
+
+def _m_layer_norm_backward(g: int, x: Sequence, dy: Sequence, weight, mean: Sequence, rstd: Sequence,
+                           dx: Sequence, dweight, dbias, rows: Sequence | None, rows_equal: int,
+                           cols: int, dtype, weight_dtype, op, workspace, stream=None) -> tuple:
+    """Backward pass: dx per rank, dweight and dbias (or None) reduced over every rank's rows
+    (op "sum" or "avg").  workspace: a device tensor of dt_layer_norm_workspace(g, cols) bytes."""
+    _dense(x, dy, weight, mean, rstd, dx, dweight, dbias, workspace)
+    return (g, _ptr_array(x), _ptr_array(dy), _ptr(weight), _ptr_array(mean), _ptr_array(rstd),
+            _ptr_array(dx), _ptr(dweight), _ptr(dbias), _rows_array(rows), rows_equal, cols,
+            _code(DTYPES, dtype), _code(DTYPES, weight_dtype), _code(OPS, op), *_workspace(workspace),
+            _stream(stream))
+
+
 _MARSHAL: dict = {}
 
 
@@ -369,6 +424,13 @@ dt_all_to_all_2d = _entry("dt_all_to_all_2d", _m_all_to_all_2d)
 dt_bucket_allreduce = _entry("dt_bucket_allreduce", _m_bucket_allreduce)
 dt_bucket_allreduce_static = _entry("dt_bucket_allreduce_static", _m_bucket_allreduce_static)
 dt_barrier = _entry("dt_barrier", _m_barrier)
+dt_layer_norm = _entry("dt_layer_norm", _m_layer_norm)
+dt_layer_norm_backward = _entry("dt_layer_norm_backward", _m_layer_norm_backward)
+
+
+def dt_layer_norm_workspace(g: int, cols: int) -> int:
+    """Workspace bytes of dt_layer_norm_backward (0: invalid argument)."""
+    return int(_lib.dt_layer_norm_workspace(g, cols))
 
 
 class Prepared:

@@ -234,3 +234,10 @@ def test_header_is_plain_c_and_links(tmp_path):
     run = subprocess.run([str(exe)], capture_output=True, text=True, timeout=120)
     assert run.returncode == 0, (run.returncode, run.stderr)
     assert run.stdout.strip().isdigit()
+
+
+def test_operator_calls_without_a_group_are_invalid(dt):
+    lib = dt.library()
+    assert lib.dt_layer_norm(None, *[None] * 7, 0, 0, 1e-5, 0, 0, None) == dt.DT_ERR_INVALID
+    assert lib.dt_layer_norm_backward(None, *[None] * 9, 0, 0, 0, 0, 0, None, 0, None) == dt.DT_ERR_INVALID
+    assert lib.dt_layer_norm_workspace(None, 64) == 0
