@@ -362,6 +362,66 @@ dt_status dt_layer_norm_backward(dt_group_t g, const void *const *x, const void 
  * number of them; 0 for an invalid argument. */
 size_t dt_layer_norm_workspace(dt_group_t g, size_t cols);
 
+/* ------------------------------------------- vocabulary loss, group-wide */
+
+/* Softmax cross entropy of `tokens` hidden rows under a vocabulary whose rows
+ * are S(0) over the ranks (rank r holds weight[r]), computed from the hidden
+ * rows and the weights in one call: the logits are never stored, and the
+ * reductions over the ranks (the maximum and the sum of exponentials here,
+ * dhidden below) are part of it.  Group-wide only, like the layer norm.
+ *   hidden       [tokens, dim], one copy for all ranks
+ *   weight[r]    rank r's vocabulary rows, [vocab[r], dim] (vocab_equal rows
+ *                each when vocab is NULL); rank r's first row has the index
+ *                vocab[0] + ... + vocab[r - 1].  A rank may have none, all
+ *                ranks together need one.
+ *   targets      [tokens] int32 vocabulary indices on the device, or
+ *                ignore_index: that token's loss and gradient are 0 and it is
+ *                not counted.  Any other value outside the vocabulary is
+ *                treated the same way and recorded as DT_ERR_INVALID in the
+ *                group's error word (dt_group_error_detail: rank -1, peer =
+ *                the token, generation = the value).
+ *   dtype        of hidden and weight: DT_BF16 (products in the tensor cores,
+ *                fp32 sums); DT_F32 is DT_ERR_UNSUPPORTED
+ *   op           DT_SUM, or DT_AVG: the mean over the counted tokens (0 where
+ *                none is counted)
+ *   losses, lse  [tokens] floats: each token's loss, and log(sum(exp(logits)))
+ *                for the backward call;  loss: one float.  Each may be NULL.
+ *   workspace    dt_vocab_loss_workspace bytes (backward = 0) of device memory,
+ *                256-byte aligned, free once `stream` has passed the call
+ * hidden, weight are 2-byte aligned; rows of whole 16-byte vectors that start
+ * on 16-byte boundaries are read in place, others are laid out again in the
+ * workspace first.  tokens, the vocabulary and dim are at most 2^30, 2^30 and
+ * 2^20.  No output may overlap another buffer. */
+dt_status dt_vocab_loss(dt_group_t g, const void *hidden, const void *const *weight,
+                        const size_t *vocab, size_t vocab_equal, const int32_t *targets,
+                        size_t tokens, size_t dim, int dtype, int op, int32_t ignore_index,
+                        float *losses, float *lse, float *loss, void *workspace,
+                        size_t workspace_bytes, void *stream);
+
+/* The gradient of that loss.  With p = exp(logit - lse) and c = grad_loss
+ * (one float on the device; NULL: 1), divided by the counted tokens for DT_AVG:
+ *   dhidden      [tokens, dim] of dtype: c * sum over the whole vocabulary of
+ *                (p - [target]) * weight, the ranks' parts already reduced
+ *   dweight[r]   [vocab[r], dim] of dtype: c * sum over the tokens of
+ *                (p - [target]) * hidden; entries of ranks without rows may be
+ *                NULL
+ *   lse          as dt_vocab_loss wrote it
+ *   workspace    dt_vocab_loss_workspace bytes with backward = 1
+ * The logits are computed again, a piece of the vocabulary at a time; p -
+ * [target] is held in bf16 for that piece (at most 512 MiB, or 256 vocabulary
+ * rows' worth), every sum in fp32, and results are rounded once.  Repeated
+ * calls give the same bits. */
+dt_status dt_vocab_loss_backward(dt_group_t g, const void *hidden, const void *const *weight,
+                                 const size_t *vocab, size_t vocab_equal, const int32_t *targets,
+                                 const float *lse, const float *grad_loss, size_t tokens,
+                                 size_t dim, int dtype, int op, int32_t ignore_index,
+                                 void *dhidden, void *const *dweight, void *workspace,
+                                 size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of either call; 0 for an invalid argument. */
+size_t dt_vocab_loss_workspace(dt_group_t g, const size_t *vocab, size_t vocab_equal,
+                               size_t tokens, size_t dim, int dtype, int backward);
+
 /* ----------------------------------------------------------- async work */
 
 /* Asynchronous collectives, after the async mode of "通信与互联（05）" §四.3
@@ -432,6 +492,7 @@ dt_status dt_debug_barrier_expect(dt_group_t g, int extra, uint32_t timeout_ms, 
 #define DT_TL_BUCKET_BARRIER 8  /* bucket all-reduce, the barrier block after a bucket */
 #define DT_TL_BARRIER 9         /* signal-window barrier kernel */
 #define DT_TL_MARK 10           /* dt_timeline_mark: block = the caller's tag */
+#define DT_TL_VOCAB 12          /* vocabulary loss, either pass */
 #define DT_TL_NORM 11           /* layer norm, either pass, and the join of its weight gradients */
 typedef struct {
     uint64_t grid;       /* the launch's %gridid */
@@ -484,6 +545,7 @@ dt_status dt_timeline_mark(void *stream, uint32_t tag);
 #define DT_BOUNDS_COPY_SHIFT 6
 #define DT_BOUNDS_COPY_2D 7
 #define DT_BOUNDS_BUCKET 8
+#define DT_BOUNDS_VOCAB 10       /* vocabulary loss; buffers: p - [target] 0, dhidden 1, dweight 16 + r, rows laid out again 32 + r */
 #define DT_BOUNDS_NORM 9         /* layer norm; buffers: x r, dy 16 + r, y or dx 32 + r, mean 48 + r, rstd 64 + r */
 uint32_t dt_build_flags(void);
 

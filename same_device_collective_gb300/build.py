@@ -22,9 +22,9 @@ LIB = os.path.join(PKG, "libdt.so")
 STEP_TOOL = os.path.join(PKG, "rank_local_step")
 
 SOURCES = ["dt_group.cpp", "dt_reduce.cu", "dt_reduce_shift.cu", "dt_copy.cu", "dt_bucket.cu",
-           "dt_barrier.cu", "dt_static.cu", "dt_norm.cu", "dt_ops.cpp"]
+           "dt_barrier.cu", "dt_static.cu", "dt_norm.cu", "dt_vocab.cu", "dt_ops.cpp"]
 HEADERS = ["dt_internal.h", "dt_group.h", "dt_host.h", "dt_math.cuh", "dt_device.cuh", "dt_shift.cuh",
-           "dt_reduce_shift.h", "dt_timeline.cuh", "dt_timeline.h", "dt_bounds.cuh", "dt_ops.h"]
+           "dt_reduce_shift.h", "dt_timeline.cuh", "dt_timeline.h", "dt_bounds.cuh", "dt_ops.h", "dt_tc.cuh", "dt_vocab.h"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 # -fmad=false: no multiply-add contraction anywhere (the reductions use

@@ -1454,6 +1454,7 @@ dt_status dt_timeline_start(size_t max_records)
     dt::bind_timeline_bucket(&sink);
     dt::bind_timeline_barrier(&sink);
     dt::bind_timeline_norm(&sink);
+    dt::bind_timeline_vocab(&sink);
     return cudaDeviceSynchronize() == cudaSuccess ? DT_OK : DT_ERR_CUDA;
 #else
     (void)max_records;

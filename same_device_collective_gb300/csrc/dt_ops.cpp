@@ -2,12 +2,14 @@
 // checks and launch planning.  They follow the collectives' conventions: every
 // argument error is reported before anything is enqueued, device memory is the
 // caller's, no call waits for the GPU and none throws.
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 
 #include "dt_group.h"
 #include "dt_host.h"
 #include "dt_ops.h"
+#include "dt_vocab.h"
 
 namespace {
 
@@ -89,6 +91,216 @@ dt_status norm_common(dt_group *g, const void *const *x, void *const *out, const
     p.weight_bf16 = weight_dtype == DT_BF16;
     p.sink = error_sink(g);
     return DT_OK;
+}
+
+// ---- vocabulary loss --------------------------------------------------------
+
+constexpr size_t kMaxTokens = (size_t)1 << 30, kMaxVocab = (size_t)1 << 30, kMaxDim = (size_t)1 << 20;
+// A piece of the vocabulary: its p - [target], and its rows where they have to
+// be laid out again, take at most this much.
+constexpr uint64_t kPieceBytes = (uint64_t)512 << 20, kPackBytes = (uint64_t)128 << 20;
+// Vocabulary tiles next to one another in the order of tiles: with 16, the
+// 152 tiles in flight are about 10 x 16, nearly as many rows as columns.
+constexpr uint32_t kGroup = 16;
+
+uint64_t up(uint64_t n, uint64_t to) { return (n + to - 1) / to * to; }
+
+// How a call is cut up, and where its parts of the workspace lie.  Sizes that
+// the workspace query knows decide everything but `packed`.
+struct VocabPlan {
+    size_t rows[DT_MAX_RANKS];
+    uint32_t units, pieces, piece;      // units of 256 rows; pieces of at most `piece` units
+    uint32_t bn;                        // width of the logits' tiles
+    uint32_t pitch;                     // of rows laid out again
+    uint32_t splits, apitch;
+    bool packed;
+    uint64_t part, logit, sums, kept, ticket, scale, g, acc, pack_h, pack_w, bytes;
+};
+
+// The widest tile that still gives every SM one: a wide tile reads its
+// operands from L2 less often, but 32768 weights of few tokens are 128 tiles
+// of 256 for 152 SMs and 512 of 64.
+uint32_t tile_width(uint64_t mt, uint64_t units, uint64_t sms)
+{
+    for (uint32_t bn = 256; bn > 64; bn /= 2)
+        if (mt * units * (dt::kVocabUnit / bn) >= sms) return bn;
+    return 64;
+}
+
+bool vocab_plan(dt_group *g, const size_t *vocab, size_t vocab_equal, size_t tokens, size_t dim, bool back, bool packed,
+                VocabPlan &v)
+{
+    if (tokens > kMaxTokens || dim == 0 || dim > kMaxDim) return false;
+    size_t total = 0;
+    v.units = 0;
+    for (int r = 0; r < g->P; ++r) {
+        v.rows[r] = vocab ? vocab[r] : vocab_equal;
+        if (v.rows[r] > kMaxVocab || (total += v.rows[r]) > kMaxVocab) return false;
+        v.units += (uint32_t)((v.rows[r] + dt::kVocabUnit - 1) / dt::kVocabUnit);
+    }
+    if (total == 0) return false;
+    const uint64_t sms = (uint64_t)dt::sm_count(g->device), mt = (tokens + 127) / 128;
+    v.packed = packed;
+    v.pitch = (uint32_t)up(dim, 8);
+    const uint64_t pack_units = std::max<uint64_t>(1, kPackBytes / (dt::kVocabUnit * 2ull * v.pitch));
+    uint64_t most = v.units;
+    if (packed) most = std::min(most, pack_units);
+    if (back && tokens) most = std::min(most, std::max<uint64_t>(1, kPieceBytes / (dt::kVocabUnit * 2ull * tokens)));
+    v.pieces = (uint32_t)((v.units + most - 1) / most);
+    v.piece = (v.units + v.pieces - 1) / v.pieces;
+    v.pieces = (v.units + v.piece - 1) / v.piece;
+    v.bn = tile_width(mt, v.piece, sms);
+    // few tokens: the vocabulary is split over the SMs that dh's tiles leave idle
+    v.apitch = (uint32_t)up(dim, 4);
+    const uint64_t tiles = mt * ((dim + 255) / 256), kblocks = 4ull * (v.units - (v.pieces - 1) * v.piece);
+    v.splits = 1;
+    if (back && tiles && tiles < sms) v.splits = (uint32_t)std::max<uint64_t>(1, std::min(sms / tiles, kblocks / 4));
+
+    uint64_t at = 0;
+    auto take = [&at](uint64_t n) {
+        const uint64_t from = at;
+        at = up(at + n, 256);
+        return from;
+    };
+    v.ticket = take(4);
+    v.scale = take(4);
+    v.part = v.logit = v.sums = v.kept = v.g = v.acc = 0;
+    if (!back) {
+        const uint64_t blocks = dt::vocab_finish_blocks((uint32_t)tokens);
+        v.part = take((uint64_t)v.units * (dt::kVocabUnit / v.bn) * tokens * sizeof(float2));
+        v.logit = take(tokens * 4);
+        v.sums = take(blocks * 8);
+        v.kept = take(blocks * 4);
+    } else {
+        v.g = take((uint64_t)v.piece * dt::kVocabUnit * 2 * tokens);
+        if (v.splits > 1 || v.pieces > 1) v.acc = take((uint64_t)v.splits * tokens * v.apitch * 4);
+    }
+    v.pack_h = v.pack_w = 0;
+    if (packed) {
+        v.pack_h = take((uint64_t)tokens * v.pitch * 2);
+        v.pack_w = take((uint64_t)v.piece * dt::kVocabUnit * 2 * v.pitch);
+    }
+    v.bytes = at;
+    return true;
+}
+
+// Bytes for either form: a call finds out from its pointers whether rows have
+// to be laid out again.
+uint64_t vocab_bytes(dt_group *g, const size_t *vocab, size_t vocab_equal, size_t tokens, size_t dim, bool back)
+{
+    VocabPlan a, b;
+    if (!vocab_plan(g, vocab, vocab_equal, tokens, dim, back, true, a)) return 0;
+    if (dim % 8) return a.bytes;
+    vocab_plan(g, vocab, vocab_equal, tokens, dim, back, false, b);
+    return std::max(a.bytes, b.bytes);
+}
+
+// Checks what both passes share and fills in the parameters and the plan.
+dt_status vocab_common(dt_group *g, const void *hidden, const void *const *weight, const size_t *vocab,
+                       size_t vocab_equal, const int32_t *targets, size_t tokens, size_t dim, int dtype, int op,
+                       int32_t ignore_index, void *workspace, size_t workspace_bytes, bool back, Buffers &b,
+                       VocabPlan &v, dt::VocabParams &p)
+{
+    if (!valid_dtype(dtype) || !valid_op(op)) return DT_ERR_INVALID;
+    if (dtype != DT_BF16 || (op != DT_SUM && op != DT_AVG)) return DT_ERR_UNSUPPORTED;
+    if (!weight || !vocab_plan(g, vocab, vocab_equal, tokens, dim, back, false, v)) return DT_ERR_INVALID;
+    if (tokens && (!hidden || !targets)) return DT_ERR_INVALID;
+    if (!multiple(hidden, 2) || !multiple(targets, 4)) return DT_ERR_INVALID;
+    bool in_place = dim % 8 == 0 && aligned16(hidden);
+    b.read(hidden, tokens * dim * 2);
+    b.read(targets, tokens * 4);
+    memset(&p, 0, sizeof p);
+    uint32_t unit = 0, first = 0;
+    for (int r = 0; r < g->P; ++r) {
+        p.unit_end[r] = unit += (uint32_t)((v.rows[r] + dt::kVocabUnit - 1) / dt::kVocabUnit);
+        p.rows[r] = (uint32_t)v.rows[r];
+        p.first[r] = first;
+        first += (uint32_t)v.rows[r];
+        if (v.rows[r] == 0) continue;
+        if (!weight[r] || !multiple(weight[r], 2)) return DT_ERR_INVALID;
+        in_place = in_place && aligned16(weight[r]);
+        b.read(weight[r], v.rows[r] * dim * 2);
+    }
+    if (!in_place) vocab_plan(g, vocab, vocab_equal, tokens, dim, back, true, v);
+    if (tokens && (!workspace || !multiple(workspace, 256) ||
+                   workspace_bytes < vocab_bytes(g, vocab, vocab_equal, tokens, dim, back)))
+        return DT_ERR_INVALID;
+    b.write(workspace, workspace_bytes);
+    p.vocab = first;
+    p.P = g->P;
+    p.packed = !in_place;
+    p.tokens = (uint32_t)tokens;
+    p.dim = (uint32_t)dim;
+    p.ignore = ignore_index;
+    p.avg = op == DT_AVG;
+    p.targets = targets;
+    p.sink = error_sink(g);
+    unsigned char *ws = static_cast<unsigned char *>(workspace);
+    p.ticket = reinterpret_cast<uint32_t *>(ws + v.ticket);
+    p.scale = reinterpret_cast<float *>(ws + v.scale);
+    p.part = reinterpret_cast<float2 *>(ws + v.part);
+    p.logit = reinterpret_cast<float *>(ws + v.logit);
+    p.gbuf = reinterpret_cast<uint16_t *>(ws + v.g);
+    p.acc = reinterpret_cast<float *>(ws + v.acc);
+    p.gpitch = v.piece * dt::kVocabUnit;
+    p.apitch = v.apitch;
+    return DT_OK;
+}
+
+// The tensor maps of the operands; where they have to be laid out again, the
+// hidden rows are, now, and w[0] is the map of a piece's rows to come.
+cudaError_t vocab_operands(dt_group *g, const void *hidden, const void *const *weight, void *workspace,
+                           const VocabPlan &v, dt::VocabParams &p, dt::VocabPack &pack, cudaStream_t s)
+{
+    cudaError_t e = cudaSuccess;
+    if (!v.packed) {
+        e = dt::vocab_map(&p.h, hidden, p.dim, p.tokens, p.dim);
+        for (int r = 0; r < g->P && e == cudaSuccess; ++r)
+            if (p.rows[r]) e = dt::vocab_map(&p.w[r], weight[r], p.dim, p.rows[r], p.dim);
+        return e;
+    }
+    uint16_t *h = reinterpret_cast<uint16_t *>(static_cast<unsigned char *>(workspace) + v.pack_h);
+    uint16_t *w = reinterpret_cast<uint16_t *>(static_cast<unsigned char *>(workspace) + v.pack_w);
+    memset(&pack, 0, sizeof pack);
+    pack.src[0] = static_cast<const uint16_t *>(hidden);
+    pack.dst = h;
+    pack.rows = p.tokens;
+    pack.dim = p.dim;
+    pack.pitch = v.pitch;
+    pack.sink = p.sink;
+    e = dt::launch_vocab_pack(pack, g->device, s);
+    if (e == cudaSuccess) e = dt::vocab_map(&p.h, h, p.dim, p.tokens, v.pitch);
+    if (e == cudaSuccess) e = dt::vocab_map(&p.w[0], w, p.dim, (uint64_t)v.piece * dt::kVocabUnit, v.pitch);
+    for (int r = 0; r < g->P; ++r) {
+        pack.src[r] = static_cast<const uint16_t *>(weight[r]);
+        pack.src_rows[r] = p.rows[r];
+        pack.unit_end[r] = p.unit_end[r];
+    }
+    pack.dst = w;
+    pack.P = g->P;
+    return e;
+}
+
+// The piece's first unit and, where needed, its rows laid out again.
+cudaError_t vocab_piece(dt_group *g, const VocabPlan &v, uint32_t piece, dt::VocabParams &p, dt::VocabPack &pack,
+                        uint32_t *units, cudaStream_t s)
+{
+    p.unit0 = piece * v.piece;
+    *units = std::min(v.piece, v.units - p.unit0);
+    if (!v.packed) return cudaSuccess;
+    pack.unit0 = p.unit0;
+    pack.rows = *units * dt::kVocabUnit;
+    return dt::launch_vocab_pack(pack, g->device, s);
+}
+
+void logits_tiles(const VocabPlan &v, uint32_t units, dt::VocabParams &p)
+{
+    p.bn = v.bn;
+    p.mt = (p.tokens + 127) / 128;
+    p.nt = units * (dt::kVocabUnit / v.bn);
+    p.splits = 1;
+    p.group = kGroup;
+    p.kblocks = (p.dim + 63) / 64;
 }
 
 }  // namespace
@@ -191,6 +403,143 @@ size_t dt_layer_norm_workspace(dt_group_t g, size_t cols)
 {
     if (!g || cols == 0 || cols > kMaxCols) return 0;
     return dt::norm_workspace((uint32_t)cols, g->device);
+}
+
+dt_status dt_vocab_loss(dt_group_t g, const void *hidden, const void *const *weight, const size_t *vocab,
+                        size_t vocab_equal, const int32_t *targets, size_t tokens, size_t dim, int dtype, int op,
+                        int32_t ignore_index, float *losses, float *lse, float *loss, void *workspace,
+                        size_t workspace_bytes, void *stream)
+{
+    DT_TRACE();
+    if (!g) return DT_ERR_INVALID;
+    std::lock_guard<std::mutex> lock(g->mu);
+    dt_status st = take_device_error(g);
+    if (st != DT_OK) return st;
+    Buffers b;
+    VocabPlan v;
+    dt::VocabParams p;
+    dt::VocabPack pack;
+    st = vocab_common(g, hidden, weight, vocab, vocab_equal, targets, tokens, dim, dtype, op, ignore_index, workspace,
+                      workspace_bytes, false, b, v, p);
+    if (st != DT_OK) return st;
+    if (!multiple(losses, 4) || !multiple(lse, 4) || !multiple(loss, 4)) return DT_ERR_INVALID;
+    b.write(losses, tokens * 4);
+    b.write(lse, tokens * 4);
+    b.write(loss, 4);
+    if (b.clash()) return DT_ERR_INVALID;
+    DeviceScope scope(g->device);
+    if (!scope.ok) return DT_ERR_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (tokens == 0) return loss ? cuda_status(cudaMemsetAsync(loss, 0, 4, s)) : DT_OK;
+
+    cudaError_t e = vocab_operands(g, hidden, weight, workspace, v, p, pack, s);
+    for (uint32_t k = 0; k < v.pieces && e == cudaSuccess; ++k) {
+        uint32_t units = 0;
+        e = vocab_piece(g, v, k, p, pack, &units, s);
+        logits_tiles(v, units, p);
+        if (e == cudaSuccess) e = dt::launch_vocab_lse(p, g->device, s);
+    }
+    if (e != cudaSuccess) return cuda_status(e);
+    unsigned char *ws = static_cast<unsigned char *>(workspace);
+    dt::VocabFinish f;
+    memset(&f, 0, sizeof f);
+    f.part = p.part;
+    f.logit = p.logit;
+    f.targets = targets;
+    f.losses = losses;
+    f.lse = lse;
+    f.loss = loss;
+    f.block_sum = reinterpret_cast<double *>(ws + v.sums);
+    f.block_kept = reinterpret_cast<uint32_t *>(ws + v.kept);
+    f.ticket = p.ticket;
+    f.tokens = p.tokens;
+    f.tiles = v.units * (dt::kVocabUnit / v.bn);
+    f.vocab = p.vocab;
+    f.ignore = ignore_index;
+    f.avg = p.avg;
+    f.sink = p.sink;
+    return cuda_status(dt::launch_vocab_finish(f, s));
+}
+
+dt_status dt_vocab_loss_backward(dt_group_t g, const void *hidden, const void *const *weight, const size_t *vocab,
+                                 size_t vocab_equal, const int32_t *targets, const float *lse, const float *grad_loss,
+                                 size_t tokens, size_t dim, int dtype, int op, int32_t ignore_index, void *dhidden,
+                                 void *const *dweight, void *workspace, size_t workspace_bytes, void *stream)
+{
+    DT_TRACE();
+    if (!g) return DT_ERR_INVALID;
+    std::lock_guard<std::mutex> lock(g->mu);
+    dt_status st = take_device_error(g);
+    if (st != DT_OK) return st;
+    Buffers b;
+    VocabPlan v;
+    dt::VocabParams p;
+    dt::VocabPack pack;
+    st = vocab_common(g, hidden, weight, vocab, vocab_equal, targets, tokens, dim, dtype, op, ignore_index, workspace,
+                      workspace_bytes, true, b, v, p);
+    if (st != DT_OK) return st;
+    if (!dweight || !multiple(lse, 4) || !multiple(grad_loss, 4) || !multiple(dhidden, 2)) return DT_ERR_INVALID;
+    if (tokens && (!lse || !dhidden)) return DT_ERR_INVALID;
+    b.read(lse, tokens * 4);
+    b.read(grad_loss, 4);
+    b.write(dhidden, tokens * dim * 2);
+    p.dw_vec = dim % 8 == 0;
+    for (int r = 0; r < g->P; ++r) {
+        if (p.rows[r] == 0) continue;
+        if (!dweight[r] || !multiple(dweight[r], 2)) return DT_ERR_INVALID;
+        p.dw[r] = static_cast<uint16_t *>(dweight[r]);
+        p.dw_vec = p.dw_vec && aligned16(dweight[r]);
+        b.write(dweight[r], v.rows[r] * dim * 2);
+    }
+    if (b.clash()) return DT_ERR_INVALID;
+    p.dh_vec = dim % 4 == 0 && multiple(dhidden, 8);
+    p.dh = static_cast<uint16_t *>(dhidden);
+    p.lse = lse;
+    p.grad = grad_loss;
+    DeviceScope scope(g->device);
+    if (!scope.ok) return DT_ERR_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaSuccess;
+    if (tokens == 0) {
+        for (int r = 0; r < g->P && e == cudaSuccess; ++r)
+            if (p.rows[r]) e = cudaMemsetAsync(dweight[r], 0, v.rows[r] * dim * 2, s);
+        return cuda_status(e);
+    }
+
+    e = vocab_operands(g, hidden, weight, workspace, v, p, pack, s);
+    if (e == cudaSuccess) e = dt::vocab_map(&p.g, p.gbuf, p.gpitch, p.tokens, p.gpitch);
+    const uint32_t wide = (uint32_t)((dim + 255) / 256);
+    for (uint32_t k = 0; k < v.pieces && e == cudaSuccess; ++k) {
+        uint32_t units = 0;
+        e = vocab_piece(g, v, k, p, pack, &units, s);
+        logits_tiles(v, units, p);
+        if (e == cudaSuccess) e = dt::launch_vocab_grad(p, g->device, s);
+        if (e != cudaSuccess) break;
+        p.bn = 256;
+        p.nt = p.group = wide;
+        p.splits = v.splits;
+        p.kblocks = units * (dt::kVocabUnit / 64);
+        p.acc_in = k > 0;
+        p.final = v.splits == 1 && k + 1 == v.pieces;
+        e = dt::launch_vocab_dh(p, g->device, s);
+        if (e != cudaSuccess) break;
+        p.mt = units * (dt::kVocabUnit / 128);
+        p.splits = 1;
+        p.kblocks = (p.tokens + 63) / 64;
+        e = dt::launch_vocab_dw(p, g->device, s);
+    }
+    if (e == cudaSuccess && v.splits > 1) {
+        p.splits = v.splits;
+        e = dt::launch_vocab_join(p, g->device, s);
+    }
+    return cuda_status(e);
+}
+
+size_t dt_vocab_loss_workspace(dt_group_t g, const size_t *vocab, size_t vocab_equal, size_t tokens, size_t dim,
+                               int dtype, int backward)
+{
+    if (!g || dtype != DT_BF16) return 0;
+    return (size_t)vocab_bytes(g, vocab, vocab_equal, tokens, dim, backward != 0);
 }
 
 }  // extern "C"

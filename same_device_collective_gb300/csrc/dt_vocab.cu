@@ -1,0 +1,671 @@
+// Softmax cross entropy of tokens under a vocabulary whose rows are split over
+// the ranks, without ever holding the logits, and its gradient.
+//
+//   l_tv = <h_t, w_v>      lse_t = log sum_v exp(l_tv)      loss_t = lse_t - l_t,target
+//   g_tv = s (exp(l_tv - lse_t) - [v = target_t])    dh_t = sum_v g_tv w_v    dw_v = sum_t g_tv h_t
+//
+// Each of these is a product on the tensor cores, and one persistent kernel
+// serves all four (Mode): tiles of 128 x bn outputs, operands brought by TMA
+// into a ring of shared memory stages by one thread, multiplied by one thread
+// that issues tcgen05.mma into tensor memory, and finished by four warps that
+// read the accumulator while the next tile's is being made in the other half
+// of tensor memory.
+//   kLse   logits; the finish reduces a tile's columns to a maximum and a sum
+//          of exponentials for each token: 8 bytes for bn logits.
+//   kGrad  the same logits again; the finish makes p - [target] and stores it
+//          as bf16 for a piece of the vocabulary at a time.  That is the one
+//          rounding on the way (2^-9 of each term, as the outputs' own): the
+//          two products below need it in the operands' type.  The scale s is
+//          applied to their fp32 sums.
+//   kDh    the piece's g times its rows of w.  Over several pieces, or when
+//          the vocabulary is split over blocks because there are few tokens,
+//          the sums stay in fp32 and are joined in a fixed order.
+//   kDw    the piece's g, transposed, times h: final for these rows of w.
+// Rank boundaries are no more than an offset: the ranks' rows are numbered
+// through in units of 256 (the last unit of a rank is padded by zeros that TMA
+// fills in), so the reductions over the ranks (of the maximum, the sum and dh)
+// are the sums over units.
+//
+// With n tokens the work is 2 n flops for each byte of w: below about 280
+// tokens HBM bounds it, above it the tensor cores do.
+#include <cudaTypedefs.h>
+
+#include "dt_ops.h"
+
+#include "dt_bounds.cuh"
+#include "dt_device.cuh"
+#include "dt_math.cuh"
+#include "dt_tc.cuh"
+#include "dt_timeline.cuh"
+#include "dt_vocab.h"
+
+namespace dt {
+namespace {
+
+enum Mode { kLse, kGrad, kDh, kDw };
+
+constexpr float kLog2e = 1.44269504088896340736f;
+
+constexpr uint32_t kM = 128;                       // rows of a tile
+constexpr uint32_t kABytes = 2 * kBoxBytes;        // 128 x 64 operand A of a stage
+constexpr uint32_t kRingBytes = 192 * 1024;
+constexpr uint32_t kMaxStages = 8;
+constexpr uint32_t kTmemColumns = 512;             // two accumulators of 128 x 256 fp32
+constexpr int kTcThreads = 7 * 32;                 // 4 finishing warps, TMA, MMA, side work
+constexpr uint32_t kStageOut = 4096;               // a finishing warp's 32 rows x 128 bytes
+constexpr uint32_t kBarBytes = 1024;
+constexpr size_t kTcSmem = 1024 + kRingBytes + 4 * kStageOut + kBarBytes;
+
+// Where a tile's operands and outputs are.
+struct Tile {
+    uint32_t m0, n0;     // first row and column of the output
+    uint32_t kb0, kb1;   // blocks of 64 of the inner dimension
+    uint32_t split;
+    int r;               // rank and row there of the vocabulary rows that the tile covers (kLse, kGrad: n; kDw: m)
+    uint32_t vrow;
+};
+
+// The rank of a unit of 256 vocabulary rows, and the unit's first row there.
+__device__ __forceinline__ int unit_rank(const VocabParams &p, uint32_t unit, uint32_t &row)
+{
+    int r = 0;
+    uint32_t begin = 0;
+    while (r + 1 < p.P && unit >= p.unit_end[r]) begin = p.unit_end[r++];
+    row = (unit - begin) * kVocabUnit;
+    return r;
+}
+
+template <int MODE>
+__device__ __forceinline__ Tile tile_of(const VocabParams &p, uint32_t i)
+{
+    Tile t;
+    const uint32_t per_split = p.mt * p.nt;
+    t.split = i / per_split;
+    i -= t.split * per_split;
+    // columns in groups of `group`, rows slowest within a group: the tiles in
+    // flight share few rows and columns, so that operands come from L2
+    const uint32_t g = i / (p.group * p.mt), in = i - g * p.group * p.mt;
+    const uint32_t width = min(p.group, p.nt - g * p.group);
+    const uint32_t m = in / width, n = g * p.group + in % width;
+    t.m0 = m * kM;
+    t.n0 = n * p.bn;
+    t.kb0 = (uint32_t)((uint64_t)p.kblocks * t.split / p.splits);
+    t.kb1 = (uint32_t)((uint64_t)p.kblocks * (t.split + 1) / p.splits);
+    t.r = 0;
+    t.vrow = 0;
+    if (MODE != kDh) {
+        const uint32_t v = MODE == kDw ? t.m0 : t.n0;
+        t.r = unit_rank(p, p.unit0 + v / kVocabUnit, t.vrow);
+        t.vrow += v % kVocabUnit;
+    }
+    return t;
+}
+
+// Vocabulary rows of rank r from `row` on that exist, at most `most`.
+__device__ __forceinline__ uint32_t rows_left(const VocabParams &p, int r, uint32_t row, uint32_t most)
+{
+    return row >= p.rows[r] ? 0 : min(p.rows[r] - row, most);
+}
+
+// Boxes of 64 that cover `left` rows or columns, of `most`: at least one, so
+// that every stage has a load for each operand.
+__device__ __forceinline__ uint32_t boxes(uint32_t left, uint32_t most)
+{
+    const uint32_t n = (min(left, most) + 63) / 64;
+    return n ? n : 1;
+}
+
+template <int MODE>
+__device__ __forceinline__ void load_stage(const VocabParams &p, const Tile &t, uint32_t kb, uint32_t a, uint32_t bar)
+{
+    const uint32_t b = a + kABytes, k = kb * 64;
+    const uint32_t na = MODE == kDw ? 2 : boxes(p.tokens - t.m0, kM);
+    uint32_t nb;
+    if (MODE == kLse || MODE == kGrad) nb = p.packed ? p.bn / 64 : boxes(rows_left(p, t.r, t.vrow, p.bn), p.bn);
+    else nb = boxes(p.dim - t.n0, p.bn);
+    mbar_expect_tx(bar, (na + nb) * kBoxBytes);
+    if (MODE == kLse || MODE == kGrad) {
+        const CUtensorMap *w = &p.w[p.packed ? 0 : t.r];
+        const uint32_t row = p.packed ? t.n0 : t.vrow;
+        for (uint32_t i = 0; i < na; ++i) tma_box(a + i * kBoxBytes, &p.h, k, t.m0 + 64 * i, bar);
+        for (uint32_t i = 0; i < nb; ++i) tma_box(b + i * kBoxBytes, w, k, row + 64 * i, bar);
+    } else if (MODE == kDh) {
+        uint32_t row;
+        const int r = unit_rank(p, p.unit0 + k / kVocabUnit, row);
+        row += k % kVocabUnit;
+        const CUtensorMap *w = &p.w[p.packed ? 0 : r];
+        if (p.packed) row = k;
+        for (uint32_t i = 0; i < na; ++i) tma_box(a + i * kBoxBytes, &p.g, k, t.m0 + 64 * i, bar);
+        for (uint32_t i = 0; i < nb; ++i) tma_box(b + i * kBoxBytes, w, t.n0 + 64 * i, row, bar);
+    } else {
+        for (uint32_t i = 0; i < na; ++i) tma_box(a + i * kBoxBytes, &p.g, t.m0 + 64 * i, k, bar);
+        for (uint32_t i = 0; i < nb; ++i) tma_box(b + i * kBoxBytes, &p.h, t.n0 + 64 * i, k, bar);
+    }
+}
+
+// A finishing warp's 32 rows x 128 bytes in shared memory, 16-byte chunk c of
+// row r at chunk c ^ (r mod 8): a thread writes its row, and eight threads
+// read a row, without bank conflicts.
+__device__ __forceinline__ uint4 *out_chunk(unsigned char *buf, uint32_t row, uint32_t c)
+{
+    return reinterpret_cast<uint4 *>(buf + row * 128 + ((c ^ (row & 7)) << 4));
+}
+
+#ifdef DT_BOUNDS
+#define VOCAB_OK(a, n, lo, bytes, buffer)                                                                     \
+    DT_IN_BOUNDS(span_in((a), (n), (uint64_t)(lo), (uint64_t)(lo) + (bytes)), p.sink, DT_BOUNDS_VOCAB, (buffer), (a), \
+                 (uint64_t)(lo))
+#else
+#define VOCAB_OK(a, n, lo, bytes, buffer) true
+#endif
+
+// 64 columns of bf16, packed two to a word: this thread's row into `buf`,
+// then the warp's rows to memory, whole lines at a time where rows are
+// vectors (vec), else element by element.
+__device__ __forceinline__ void store_rows_bf16(const VocabParams &p, unsigned char *buf, const uint32_t (&w)[32],
+                                                uint16_t *out, uint64_t pitch, uint32_t rows, uint32_t cols, bool vec,
+                                                const void *lo, uint64_t bytes, int buffer)
+{
+    (void)p, (void)lo, (void)bytes, (void)buffer;
+    const uint32_t lane = threadIdx.x & 31;
+    __syncwarp();
+#pragma unroll
+    for (uint32_t c = 0; c < 8; ++c)
+        *out_chunk(buf, lane, c) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+    __syncwarp();
+    if (vec) {
+        const uint32_t c = lane & 7;
+        for (uint32_t row = lane >> 3; row < rows && c * 8 < cols; row += 4) {
+            uint16_t *to = out + row * pitch + c * 8;
+            if (VOCAB_OK(to, 16, lo, bytes, buffer)) *reinterpret_cast<uint4 *>(to) = *out_chunk(buf, row, c);
+        }
+    } else {
+        for (uint32_t row = 0; row < rows; ++row)
+            for (uint32_t e = lane; e < cols; e += 32) {
+                const uint16_t v = reinterpret_cast<const uint16_t *>(out_chunk(buf, row, e >> 3))[e & 7];
+                uint16_t *to = out + row * pitch + e;
+                if (VOCAB_OK(to, 2, lo, bytes, buffer)) *to = v;
+            }
+    }
+}
+
+// The state of the pipeline's waits: a wait that runs out is recorded once,
+// and every role then leaves its loop.
+struct Waits {
+    const ErrorSink &sink;
+    volatile uint32_t *gave_up;
+    __device__ bool operator()(uint32_t bar, uint32_t parity) const
+    {
+        if (mbar_wait_bounded(bar, parity, sink.timeout_ns)) return true;
+        *gave_up = 1;
+        record_error(sink, DT_ERR_TIMEOUT, -1, blockIdx.x, 0);
+        return false;
+    }
+};
+
+template <int MODE>
+__global__ void __launch_bounds__(kTcThreads, 1) vocab_kernel(const __grid_constant__ VocabParams p)
+{
+    constexpr bool kAMn = MODE == kDw, kBMn = MODE == kDh || MODE == kDw;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
+    const uint32_t ring = smem_addr(smem);
+    unsigned char *out_buf = smem + kRingBytes;
+    unsigned char *ctl = out_buf + 4 * kStageOut;
+    const uint32_t bars = smem_addr(ctl);
+    const uint32_t full = bars, empty = bars + 8 * kMaxStages;         // stage loaded; stage consumed
+    const uint32_t acc_full = bars + 16 * kMaxStages, acc_empty = acc_full + 16, drained = acc_empty + 16;
+    volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(ctl + 256);
+    volatile uint32_t *gave_up = tmem_slot + 1;
+    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    DT_TL_BEGIN();
+    if (threadIdx.x == 0) {
+        for (uint32_t s = 0; s < p.stages; ++s) {
+            mbar_init(full + 8 * s, 1);
+            mbar_init(empty + 8 * s, 1);
+        }
+        for (uint32_t s = 0; s < 2; ++s) {
+            mbar_init(acc_full + 8 * s, 1);
+            mbar_init(acc_empty + 8 * s, 4);
+        }
+        mbar_init(drained, 1);
+        *gave_up = 0;
+        mbar_init_fence();
+    }
+    if (warp == 5) tmem_alloc(smem_addr(const_cast<uint32_t *>(tmem_slot)), kTmemColumns);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_begin();
+    DT_TL_WAITED();
+    const Waits wait{p.sink, gave_up};
+    const uint32_t stage_bytes = kABytes + p.bn * 128;
+
+    if (warp == 4) {
+        if (lane == 0) {
+            uint32_t n = 0;   // loads issued
+            bool ok = true;
+            for (uint32_t i = blockIdx.x; ok && i < p.tiles; i += gridDim.x) {
+                const Tile t = tile_of<MODE>(p, i);
+                for (uint32_t kb = t.kb0; kb < t.kb1; ++kb, ++n) {
+                    const uint32_t s = n % p.stages, round = n / p.stages;
+                    if (!(ok = wait(empty + 8 * s, (round & 1) ^ 1))) break;
+                    load_stage<MODE>(p, t, kb, ring + s * stage_bytes, full + 8 * s);
+                }
+            }
+            // leave nothing in flight: the stages are consumed, or at least loaded
+            for (uint32_t k = n > p.stages ? n - p.stages : 0; k < n; ++k) {
+                const uint32_t s = k % p.stages, parity = (k / p.stages) & 1;
+                if (*gave_up || !wait(empty + 8 * s, parity)) wait(full + 8 * s, parity);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 5) {
+        if (lane == 0) {
+            const uint32_t desc = mma_desc(kM, p.bn, kAMn, kBMn);
+            uint32_t n = 0, done = 0;
+            bool ok = true;
+            for (uint32_t i = blockIdx.x; ok && i < p.tiles; i += gridDim.x, ++done) {
+                const Tile t = tile_of<MODE>(p, i);
+                const uint32_t half = done & 1, acc = tmem + half * 256;
+                if (!(ok = wait(acc_empty + 8 * half, ((done >> 1) & 1) ^ 1))) break;
+                tc_fence_after();
+                for (uint32_t kb = t.kb0; kb < t.kb1; ++kb, ++n) {
+                    const uint32_t s = n % p.stages;
+                    if (!(ok = wait(full + 8 * s, (n / p.stages) & 1))) break;
+                    tc_fence_after();
+                    const uint32_t a = ring + s * stage_bytes, b = a + kABytes;
+#pragma unroll
+                    for (uint32_t k = 0; k < 4; ++k)
+                        mma_bf16(acc, smem_desc(a + k * k_step_bytes(kAMn), kAMn),
+                                 smem_desc(b + k * k_step_bytes(kBMn), kBMn), desc, kb != t.kb0 || k != 0);
+                    mma_commit(empty + 8 * s);
+                }
+                if (ok) mma_commit(acc_full + 8 * half);
+            }
+            if (!ok) {   // the MMAs issued so far end before tensor memory is freed
+                mma_commit(drained);
+                wait(drained, 0);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 6) {
+        // what the block's tiles do not wait for
+        if (MODE == kLse && blockIdx.x == 0 && lane == 0) *p.ticket = 0;
+        if (MODE == kGrad && blockIdx.x == 0 && p.unit0 == 0) {
+            uint32_t kept = 0;
+            for (uint32_t k = lane; k < p.tokens; k += 32) {
+                const int32_t v = p.targets[k];
+                const bool in = v >= 0 && (uint32_t)v < p.vocab;
+                if (v != p.ignore && !in) record_error(p.sink, DT_ERR_INVALID, -1, (int)k, v);
+                kept += v != p.ignore && in;
+            }
+            kept = __reduce_add_sync(0xFFFFFFFFu, kept);
+            if (lane == 0) {
+                const float grad = p.grad ? *p.grad : 1.0f;
+                *p.scale = kept == 0 ? 0.0f : p.avg ? __fdiv_rn(grad, (float)kept) : grad;
+            }
+        }
+    } else {
+        unsigned char *buf = out_buf + warp * kStageOut;
+        const float scale = MODE == kDh || MODE == kDw ? *p.scale : 0.0f;
+        uint32_t done = 0;
+        for (uint32_t i = blockIdx.x; i < p.tiles; i += gridDim.x, ++done) {
+            const Tile t = tile_of<MODE>(p, i);
+            const uint32_t half = done & 1;
+            const uint32_t acc = tmem + half * 256 + (warp * 32 << 16);   // this warp's 32 rows
+            const uint32_t row0 = t.m0 + warp * 32, row = row0 + lane;
+            bool ok = wait(acc_full + 8 * half, (done >> 1) & 1);
+            if (__any_sync(0xFFFFFFFFu, !ok)) break;
+            tc_fence_after();
+
+            if (MODE == kLse || MODE == kGrad) {
+                const uint32_t valid = rows_left(p, t.r, t.vrow, p.bn);
+                const int32_t target = row < p.tokens ? p.targets[row] : p.ignore;
+                // the column of this row's target in the tile, if it is there
+                const int64_t at = (int64_t)target - (int64_t)(p.first[t.r] + t.vrow);
+                const bool here = target != p.ignore && target >= 0 && at >= 0 && at < (int64_t)valid;
+                if (MODE == kLse) {
+                    float top = -INFINITY, sum = 0.0f;
+                    for (uint32_t c = 0; c < p.bn; c += 32) {
+                        float v[32];
+                        tmem_load32(acc + c, v);
+#pragma unroll
+                        for (uint32_t j = 0; j < 32; ++j) top = fmaxf(top, c + j < valid ? v[j] : -INFINITY);
+                    }
+                    const float top2 = top == -INFINITY ? 0.0f : top * kLog2e;   // no 0 times infinity where all are -inf
+                    for (uint32_t c = 0; c < p.bn; c += 32) {
+                        float v[32];
+                        tmem_load32(acc + c, v);
+#pragma unroll
+                        for (uint32_t j = 0; j < 32; ++j)
+                            if (c + j < valid) sum += exp2_fast(fmaf(v[j], kLog2e, -top2));
+                    }
+                    // few rows have their target here: one column read for each
+                    float logit = 0.0f;
+                    for (uint32_t rest = __ballot_sync(0xFFFFFFFFu, here); rest; rest &= rest - 1) {
+                        const uint32_t who = __ffs(rest) - 1;
+                        const uint32_t col = __shfl_sync(0xFFFFFFFFu, (uint32_t)at, who);
+                        const float v = tmem_load1(acc + col);
+                        if (lane == who) logit = v;
+                    }
+                    if (row < p.tokens) {
+                        p.part[(uint64_t)(p.unit0 * (kVocabUnit / p.bn) + t.n0 / p.bn) * p.tokens + row] =
+                            make_float2(top, sum);
+                        if (here) p.logit[row] = logit;
+                    }
+                } else {
+                    const bool keep = row < p.tokens && target != p.ignore && target >= 0 && (uint32_t)target < p.vocab;
+                    const float lse2 = keep ? p.lse[row] * kLog2e : 0.0f;
+                    const uint32_t col = here ? (uint32_t)at : 0xFFFFFFFFu;
+                    const uint32_t rows = row0 < p.tokens ? min(p.tokens - row0, 32u) : 0;
+                    for (uint32_t c = 0; c < p.bn; c += 64) {
+                        uint32_t w[32];
+#pragma unroll
+                        for (uint32_t q = 0; q < 2; ++q) {
+                            float v[32];
+                            tmem_load32(acc + c + 32 * q, v);
+#pragma unroll
+                            for (uint32_t j = 0; j < 32; ++j) {
+                                const uint32_t e = c + 32 * q + j;
+                                float x = exp2_fast(fmaf(v[j], kLog2e, -lse2));
+                                if (e == col) x -= 1.0f;
+                                v[j] = keep && e < valid ? x : 0.0f;
+                            }
+#pragma unroll
+                            for (uint32_t j = 0; j < 16; ++j) w[16 * q + j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+                        }
+                        store_rows_bf16(p, buf, w, p.gbuf + (uint64_t)row0 * p.gpitch + t.n0 + c, p.gpitch, rows, 64,
+                                        true, p.gbuf, (uint64_t)p.tokens * p.gpitch * 2, 0);
+                    }
+                }
+            } else if (MODE == kDh) {
+                // fp32 sums: 32 columns a step, four to a thread on the way out
+                const uint32_t rows = row0 < p.tokens ? min(p.tokens - row0, 32u) : 0;
+                float *part = p.acc + ((uint64_t)t.split * p.tokens + row0) * p.apitch + t.n0;
+                for (uint32_t c = 0; c < p.bn && t.n0 + c < p.dim; c += 32) {
+                    float v[32];
+                    tmem_load32(acc + c, v);
+                    __syncwarp();
+#pragma unroll
+                    for (uint32_t q = 0; q < 8; ++q)
+                        *out_chunk(buf, lane, q) =
+                            make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
+                                       __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3]));
+                    __syncwarp();
+                    const uint32_t q = lane & 7, e = t.n0 + c + 4 * q;
+                    for (uint32_t k = lane >> 3; k < rows && e < p.dim; k += 4) {
+                        const uint4 u = *out_chunk(buf, k, q);
+                        float4 f = make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z),
+                                               __uint_as_float(u.w));
+                        float4 *at = reinterpret_cast<float4 *>(part + (uint64_t)k * p.apitch + c + 4 * q);
+                        if (p.acc_in) {
+                            const float4 o = *at;
+                            f.x += o.x, f.y += o.y, f.z += o.z, f.w += o.w;
+                        }
+                        if (!p.final) {
+                            *at = f;
+                            continue;
+                        }
+                        uint16_t *to = p.dh + (uint64_t)(row0 + k) * p.dim + e;
+                        const uint64_t all = (uint64_t)p.tokens * p.dim * 2;
+                        (void)all;
+                        const uint2 h = make_uint2(pack_bf16x2(f.x * scale, f.y * scale),
+                                                   pack_bf16x2(f.z * scale, f.w * scale));
+                        if (p.dh_vec) {
+                            if (VOCAB_OK(to, 8, p.dh, all, 1)) *reinterpret_cast<uint2 *>(to) = h;
+                        } else {
+                            const uint16_t x[4] = {(uint16_t)h.x, (uint16_t)(h.x >> 16), (uint16_t)h.y,
+                                                   (uint16_t)(h.y >> 16)};
+                            for (uint32_t j = 0; j < 4 && e + j < p.dim; ++j)
+                                if (VOCAB_OK(to + j, 2, p.dh, all, 1)) to[j] = x[j];
+                        }
+                    }
+                }
+            } else {
+                const uint32_t rows = rows_left(p, t.r, t.vrow + warp * 32, 32);
+                uint16_t *out = p.dw[t.r] + (uint64_t)(t.vrow + warp * 32) * p.dim + t.n0;
+                for (uint32_t c = 0; c < p.bn && t.n0 + c < p.dim; c += 64) {
+                    uint32_t w[32];
+#pragma unroll
+                    for (uint32_t q = 0; q < 2; ++q) {
+                        float v[32];
+                        tmem_load32(acc + c + 32 * q, v);
+#pragma unroll
+                        for (uint32_t j = 0; j < 16; ++j)
+                            w[16 * q + j] = pack_bf16x2(v[2 * j] * scale, v[2 * j + 1] * scale);
+                    }
+                    store_rows_bf16(p, buf, w, out + c, p.dim, rows, min(p.dim - t.n0 - c, 64u), p.dw_vec, p.dw[t.r],
+                                    (uint64_t)p.rows[t.r] * p.dim * 2, 16 + t.r);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(acc_empty + 8 * half);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 5) tmem_free(tmem, kTmemColumns);
+    DT_TL_END_BLOCK(DT_TL_VOCAB);
+}
+
+// Joins the tiles' maxima and sums: thread (t, s) takes every 32nd tile of
+// token t, the 32 are joined in shared memory in ascending order, and block
+// sums of the losses are added by the last block to finish, in block order.
+constexpr int kTokens = 32, kSlices = 32;
+
+__global__ void __launch_bounds__(kTokens *kSlices) vocab_finish_kernel(const __grid_constant__ VocabFinish p)
+{
+    __shared__ float2 part[kSlices][kTokens];
+    __shared__ bool last;
+    DT_TL_BEGIN();
+    pdl_begin();
+    DT_TL_WAITED();
+    const uint32_t c = threadIdx.x % kTokens, s = threadIdx.x / kTokens;
+    const uint32_t t = blockIdx.x * kTokens + c;
+    // joins (m, x) into (top, sum), both relative to their own maximum
+    auto join = [](float &top, float &sum, float m, float x) {
+        const float most = fmaxf(top, m);
+        if (most == -INFINITY) {
+            // nothing but minus infinities so far (a unit's padding): no mass, but
+            // a NaN in a sum must stay
+            sum += x;
+        } else {
+            sum = sum * exp2_fast((top - most) * kLog2e) + x * exp2_fast((m - most) * kLog2e);
+            top = most;
+        }
+    };
+    float top = -INFINITY, sum = 0.0f;
+    if (t < p.tokens)
+        for (uint32_t k = s; k < p.tiles; k += kSlices) {
+            const float2 v = p.part[(uint64_t)k * p.tokens + t];
+            join(top, sum, v.x, v.y);
+        }
+    part[s][c] = make_float2(top, sum);
+    __syncthreads();
+    if (s == 0) {
+        for (int k = 1; k < kSlices; ++k) join(top, sum, part[k][c].x, part[k][c].y);
+        float loss = 0.0f;
+        uint32_t kept = 0;
+        if (t < p.tokens) {
+            const float lse = top + logf(sum);
+            const int32_t v = p.targets[t];
+            if (v != p.ignore) {
+                if (v >= 0 && (uint32_t)v < p.vocab) {
+                    loss = lse - p.logit[t];
+                    kept = 1;
+                } else {
+                    record_error(p.sink, DT_ERR_INVALID, -1, (int)t, v);
+                }
+            }
+            if (p.lse) p.lse[t] = lse;
+            if (p.losses) p.losses[t] = loss;
+        }
+        double all = loss;
+        for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
+        kept = __reduce_add_sync(0xFFFFFFFFu, kept);
+        if (c == 0) {
+            p.block_sum[blockIdx.x] = all;
+            p.block_kept[blockIdx.x] = kept;
+            __threadfence();
+            last = atomicAdd(p.ticket, 1u) == gridDim.x - 1;
+        }
+    }
+    __syncthreads();
+    if (last && s == 0) {
+        __threadfence();
+        double all = 0.0;
+        uint64_t kept = 0;
+        for (uint32_t b = c; b < gridDim.x; b += kTokens) {
+            all += __ldcg(p.block_sum + b);
+            kept += __ldcg(p.block_kept + b);
+        }
+        for (int o = 16; o > 0; o >>= 1) {
+            all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
+            kept += __shfl_xor_sync(0xFFFFFFFFu, kept, o);
+        }
+        if (c == 0 && p.loss) *p.loss = kept == 0 ? 0.0f : (float)(p.avg ? all / (double)kept : all);
+    }
+    DT_TL_END_BLOCK(DT_TL_VOCAB);
+}
+
+// dh = s * (the sum of the splits), four elements a thread.
+__global__ void __launch_bounds__(kThreads) vocab_join_kernel(const __grid_constant__ VocabParams p)
+{
+    DT_TL_BEGIN();
+    pdl_begin();
+    DT_TL_WAITED();
+    const float scale = *p.scale;
+    const uint32_t quads = p.apitch / 4;
+    const uint64_t all = (uint64_t)p.tokens * quads, step = (uint64_t)gridDim.x * kThreads;
+    for (uint64_t i = (uint64_t)blockIdx.x * kThreads + threadIdx.x; i < all; i += step) {
+        const uint32_t row = (uint32_t)(i / quads), e = (uint32_t)(i % quads) * 4;
+        float4 f = make_float4(0, 0, 0, 0);
+#pragma unroll 4
+        for (uint32_t k = 0; k < p.splits; ++k) {
+            const float4 o = *reinterpret_cast<const float4 *>(p.acc + ((uint64_t)k * p.tokens + row) * p.apitch + e);
+            f.x += o.x, f.y += o.y, f.z += o.z, f.w += o.w;
+        }
+        const float v[4] = {f.x * scale, f.y * scale, f.z * scale, f.w * scale};
+        uint16_t *to = p.dh + (uint64_t)row * p.dim + e;
+        for (uint32_t j = 0; j < 4 && e + j < p.dim; ++j)
+            if (VOCAB_OK(to + j, 2, p.dh, (uint64_t)p.tokens * p.dim * 2, 1)) to[j] = f32_to_bf16(v[j]);
+    }
+    DT_TL_END_BLOCK(DT_TL_VOCAB);
+}
+
+// Rows that TMA cannot address (a width that is not a multiple of 8, or a
+// buffer off a 16-byte boundary), laid out again: `rows` rows at a pitch of
+// whole vectors.  Source rows are the vocabulary units [unit0, ...) or, with
+// P = 0, the one matrix src[0].  Rows past a rank's last are zeros.
+__global__ void __launch_bounds__(kThreads) vocab_pack_kernel(const __grid_constant__ VocabPack p)
+{
+    DT_TL_BEGIN();
+    pdl_begin();
+    DT_TL_WAITED();
+    const uint32_t vecs = p.pitch / 8;
+    const uint64_t all = (uint64_t)p.rows * vecs, step = (uint64_t)gridDim.x * kThreads;
+    for (uint64_t i = (uint64_t)blockIdx.x * kThreads + threadIdx.x; i < all; i += step) {
+        const uint32_t row = (uint32_t)(i / vecs), e = (uint32_t)(i % vecs) * 8;
+        int r = 0;
+        uint32_t at = row, have = p.rows;
+        if (p.P) {
+            const uint32_t unit = p.unit0 + row / kVocabUnit;
+            uint32_t begin = 0;
+            while (r + 1 < p.P && unit >= p.unit_end[r]) begin = p.unit_end[r++];
+            at = (unit - begin) * kVocabUnit + row % kVocabUnit;
+            have = p.src_rows[r];
+        }
+        uint32_t w[4] = {0, 0, 0, 0};
+        if (at < have) {
+            const uint16_t *src = p.src[r] + (uint64_t)at * p.dim + e;
+#pragma unroll
+            for (uint32_t j = 0; j < 8; ++j)
+                if (e + j < p.dim && VOCAB_OK(src + j, 2, p.src[r], (uint64_t)have * p.dim * 2, 32 + r))
+                    w[j / 2] |= (uint32_t)src[j] << (16 * (j & 1));
+        }
+        reinterpret_cast<uint4 *>(p.dst)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    DT_TL_END_BLOCK(DT_TL_VOCAB);
+}
+
+template <int MODE>
+cudaError_t launch_mode(VocabParams &p, int device, cudaStream_t s)
+{
+    static std::atomic<uint64_t> ready{0};   // devices whose shared memory limit is set
+    const uint64_t bit = device < 64 ? 1ull << device : 0;
+    if (!(ready.load(std::memory_order_acquire) & bit) || !bit) {
+        const cudaError_t e = cudaFuncSetAttribute(vocab_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   (int)kTcSmem);
+        if (e != cudaSuccess) return e;
+        ready.fetch_or(bit, std::memory_order_release);
+    }
+    p.stages = kRingBytes / (kABytes + p.bn * 128);
+    if (p.stages > kMaxStages) p.stages = kMaxStages;
+    const uint64_t tiles = (uint64_t)p.mt * p.nt * p.splits;
+    if (tiles > 0x7FFFFFFFu) return cudaErrorInvalidValue;
+    p.tiles = (uint32_t)tiles;
+    const uint32_t sms = (uint32_t)sm_count(device);
+    return launch_kernel(vocab_kernel<MODE>, dim3(p.tiles < sms ? p.tiles : sms), dim3(kTcThreads), kTcSmem, s, false, p);
+}
+
+unsigned elementwise_grid(uint64_t items, int device)
+{
+    const uint64_t want = (items + kThreads - 1) / kThreads, cap = (uint64_t)sm_count(device) * 16;
+    return (unsigned)(want < cap ? (want ? want : 1) : cap);
+}
+
+}  // namespace
+
+DT_TL_BINDER(bind_timeline_vocab)
+
+cudaError_t launch_vocab_lse(VocabParams &p, int device, cudaStream_t s) { return launch_mode<kLse>(p, device, s); }
+cudaError_t launch_vocab_grad(VocabParams &p, int device, cudaStream_t s) { return launch_mode<kGrad>(p, device, s); }
+cudaError_t launch_vocab_dh(VocabParams &p, int device, cudaStream_t s) { return launch_mode<kDh>(p, device, s); }
+cudaError_t launch_vocab_dw(VocabParams &p, int device, cudaStream_t s) { return launch_mode<kDw>(p, device, s); }
+
+cudaError_t launch_vocab_finish(const VocabFinish &p, cudaStream_t s)
+{
+    return launch_kernel(vocab_finish_kernel, dim3(vocab_finish_blocks(p.tokens)), dim3(kTokens * kSlices), 0, s, false, p);
+}
+
+uint32_t vocab_finish_blocks(uint32_t tokens) { return (tokens + kTokens - 1) / kTokens; }
+
+cudaError_t launch_vocab_join(const VocabParams &p, int device, cudaStream_t s)
+{
+    return launch_kernel(vocab_join_kernel, dim3(elementwise_grid((uint64_t)p.tokens * (p.apitch / 4), device)),
+                         dim3(kThreads), 0, s, false, p);
+}
+
+cudaError_t launch_vocab_pack(const VocabPack &p, int device, cudaStream_t s)
+{
+    return launch_kernel(vocab_pack_kernel, dim3(elementwise_grid((uint64_t)p.rows * (p.pitch / 8), device)),
+                         dim3(kThreads), 0, s, false, p);
+}
+
+cudaError_t vocab_map(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows, uint64_t pitch)
+{
+    static std::atomic<void *> entry{nullptr};
+    void *fn = entry.load(std::memory_order_acquire);
+    if (!fn) {
+        cudaDriverEntryPointQueryResult found;
+        const cudaError_t e =
+            cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found);
+        if (e != cudaSuccess) return e;
+        if (found != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
+        entry.store(fn, std::memory_order_release);
+    }
+    const cuuint64_t dims[2] = {cols, rows}, strides[1] = {pitch * 2};
+    const cuuint32_t box[2] = {64, 64}, steps[2] = {1, 1};
+    const CUresult r = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn)(
+        map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, steps,
+        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+}  // namespace dt

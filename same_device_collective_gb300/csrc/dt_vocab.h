@@ -1,0 +1,90 @@
+// Parameter blocks and launchers of the vocabulary loss.  Not part of the C ABI.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cstdint>
+
+#include "dt.h"
+#include "dt_internal.h"
+
+namespace dt {
+
+// The ranks' vocabulary rows are numbered through in units of this many rows:
+// rank r has units [unit_end[r - 1], unit_end[r]), its last one padded.
+constexpr uint32_t kVocabUnit = 256;
+
+struct VocabParams {
+    CUtensorMap h;                     // [tokens, dim]
+    CUtensorMap g;                     // [tokens, gpitch]: a piece's p - [target]
+    CUtensorMap w[DT_MAX_RANKS];       // rank r's rows; packed: w[0] holds the piece's units
+    uint32_t unit_end[DT_MAX_RANKS];
+    uint32_t rows[DT_MAX_RANKS];       // vocabulary rows of each rank
+    uint32_t first[DT_MAX_RANKS];      // the vocabulary index of its first row
+    uint32_t vocab;
+    int32_t P;
+    uint32_t packed;
+    uint32_t unit0;                    // the piece's first unit
+    uint32_t tokens, dim;
+    uint32_t bn;                       // tile width: 64, 128 or 256
+    uint32_t stages;
+    uint32_t mt, nt, splits, group;    // tiles of the output, splits of the inner dimension, tile order
+    uint32_t kblocks;                  // blocks of 64 of the inner dimension
+    uint32_t tiles;
+    uint32_t gpitch, apitch;
+    uint32_t acc_in, final;            // dh: add to the sums so far; store the result
+    uint32_t dh_vec, dw_vec;           // rows start on 8- and 16-byte boundaries
+    int32_t ignore;
+    int32_t avg;
+    const int32_t *targets;
+    const float *lse;
+    const float *grad;
+    float2 *part;                      // [tiles of the vocabulary][tokens]: maximum, sum of exponentials
+    float *logit;                      // the target's logit of each token
+    uint32_t *ticket;
+    float *scale;                      // grad, or grad / counted tokens
+    uint16_t *gbuf;                    // [tokens, gpitch] bf16
+    float *acc;                        // [splits][tokens][apitch]
+    uint16_t *dh;
+    uint16_t *dw[DT_MAX_RANKS];
+    ErrorSink sink;
+};
+
+struct VocabFinish {
+    const float2 *part;
+    const float *logit;
+    const int32_t *targets;
+    float *losses, *lse, *loss;        // each may be NULL
+    double *block_sum;
+    uint32_t *block_kept;
+    uint32_t *ticket;
+    uint32_t tokens, tiles, vocab;
+    int32_t ignore, avg;
+    ErrorSink sink;
+};
+
+struct VocabPack {
+    const uint16_t *src[DT_MAX_RANKS];
+    uint32_t src_rows[DT_MAX_RANKS];
+    uint32_t unit_end[DT_MAX_RANKS];
+    uint16_t *dst;
+    int32_t P;                         // 0: one matrix of `rows` rows
+    uint32_t unit0;
+    uint32_t rows, dim, pitch;
+    ErrorSink sink;
+};
+
+cudaError_t launch_vocab_lse(VocabParams &p, int device, cudaStream_t s);
+cudaError_t launch_vocab_grad(VocabParams &p, int device, cudaStream_t s);
+cudaError_t launch_vocab_dh(VocabParams &p, int device, cudaStream_t s);
+cudaError_t launch_vocab_dw(VocabParams &p, int device, cudaStream_t s);
+cudaError_t launch_vocab_join(const VocabParams &p, int device, cudaStream_t s);
+cudaError_t launch_vocab_finish(const VocabFinish &p, cudaStream_t s);
+uint32_t vocab_finish_blocks(uint32_t tokens);
+cudaError_t launch_vocab_pack(const VocabPack &p, int device, cudaStream_t s);
+// The tensor map of a row-major bf16 matrix, read in boxes of 64 x 64.
+cudaError_t vocab_map(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows, uint64_t pitch);
+
+}  // namespace dt

@@ -38,7 +38,8 @@ DT_SHARED_OUTPUT = 0x1
 DT_DEFAULT_BUCKET_CAP_BYTES = 25 << 20
 DT_BUILD_NVTX, DT_BUILD_TIMELINE, DT_BUILD_BOUNDS = 1, 2, 4
 BOUNDS_KERNELS = {1: "reduce", 2: "reduce_shift", 3: "copy_bulk", 4: "copy_vec", 5: "copy_edge",
-                  6: "copy_shift", 7: "copy_2d", 8: "bucket", 9: "norm"}
+                  6: "copy_shift", 7: "copy_2d", 8: "bucket", 9: "norm",
+                  10: "vocab"}
 
 DTYPES = {"f32": DT_F32, "bf16": DT_BF16, "i32": DT_I32}
 OPS = {"sum": DT_SUM, "avg": DT_AVG, "max": DT_MAX, "min": DT_MIN,
@@ -51,6 +52,7 @@ _szp = ctypes.POINTER(ctypes.c_size_t)
 _i = ctypes.c_int
 _u = ctypes.c_uint
 _f = ctypes.c_float
+_i32 = ctypes.c_int32
 _u32 = ctypes.c_uint32
 
 _SIGS = {
@@ -76,6 +78,11 @@ _SIGS = {
     "dt_layer_norm_backward": ([_vp, _vpp, _vpp, _vp, _vpp, _vpp, _vpp, _vp, _vp, _szp, _sz, _sz, _i, _i,
                                 _i, _vp, _sz, _vp], _i),
     "dt_layer_norm_workspace": ([_vp, _sz], _sz),
+    "dt_vocab_loss": ([_vp, _vp, _vpp, _szp, _sz, _vp, _sz, _sz, _i, _i, _i32, _vp, _vp, _vp, _vp, _sz,
+                       _vp], _i),
+    "dt_vocab_loss_backward": ([_vp, _vp, _vpp, _szp, _sz, _vp, _vp, _vp, _sz, _sz, _i, _i, _i32, _vp,
+                                _vpp, _vp, _sz, _vp], _i),
+    "dt_vocab_loss_workspace": ([_vp, _szp, _sz, _sz, _sz, _i, _i], _sz),
     "dt_replicate_to_shard": ([_vp, _i, _vpp, _vpp, ctypes.POINTER(_i), _sz, _sz, _vp], _i),
     "dt_all_gather_into_vec": ([_vp, _i, _vpp, _vpp, _szp, _sz, _sz, _vp], _i),
     "dt_all_to_all_2d": ([_vp, _i, _vpp, _vpp, _sz, _sz, _sz, _i, _i, _vp], _i),
@@ -104,7 +111,7 @@ TIMELINE_DTYPE = np.dtype([("grid", np.uint64), ("kind", np.uint32), ("block", n
                            ("t_waited", np.uint64), ("t_end", np.uint64)])
 TIMELINE_KINDS = {1: "reduce", 2: "reduce_shift", 3: "copy_bulk", 4: "copy_vec", 5: "copy_shift",
                   6: "copy_2d", 7: "bucket", 8: "bucket_barrier", 9: "barrier", 10: "mark",
-                  11: "norm"}
+                  11: "norm", 12: "vocab"}
 
 
 class DtError(RuntimeError):
@@ -398,6 +405,29 @@ def _m_layer_norm_backward(g: int, x: Sequence, dy: Sequence, weight, mean: Sequ
             _stream(stream))
 
 
+def _m_vocab_loss(g: int, hidden, weight: Sequence, vocab: Sequence | None, vocab_equal: int, targets,
+                  tokens: int, dim: int, dtype, op, ignore_index: int, losses, lse, loss, workspace,
+                  stream=None) -> tuple:
+    """Softmax cross entropy of hidden [tokens, dim] under the ranks' vocabulary rows weight[r]
+    [vocab[r], dim] (or vocab_equal rows each): losses and lse [tokens], loss [1], f32, or None.
+    targets: int32 [tokens].  workspace: a device tensor of dt_vocab_loss_workspace bytes."""
+    _dense(hidden, weight, targets, losses, lse, loss, workspace)
+    return (g, _ptr(hidden), _ptr_array(weight), _rows_array(vocab), vocab_equal, _ptr(targets), tokens,
+            dim, _code(DTYPES, dtype), _code(OPS, op), ignore_index, _ptr(losses), _ptr(lse), _ptr(loss),
+            *_workspace(workspace), _stream(stream))
+
+
+def _m_vocab_loss_backward(g: int, hidden, weight: Sequence, vocab: Sequence | None, vocab_equal: int,
+                           targets, lse, grad_loss, tokens: int, dim: int, dtype, op, ignore_index: int,
+                           dhidden, dweight: Sequence, workspace, stream=None) -> tuple:
+    """The gradient of that loss: dhidden [tokens, dim], reduced over the ranks, and dweight[r]
+    [vocab[r], dim].  lse as dt_vocab_loss wrote it; grad_loss: one f32 on the device, or None (1)."""
+    _dense(hidden, weight, targets, lse, grad_loss, dhidden, dweight, workspace)
+    return (g, _ptr(hidden), _ptr_array(weight), _rows_array(vocab), vocab_equal, _ptr(targets), _ptr(lse),
+            _ptr(grad_loss), tokens, dim, _code(DTYPES, dtype), _code(OPS, op), ignore_index,
+            _ptr(dhidden), _ptr_array(dweight), *_workspace(workspace), _stream(stream))
+
+
 _MARSHAL: dict = {}
 
 
@@ -426,6 +456,15 @@ dt_bucket_allreduce_static = _entry("dt_bucket_allreduce_static", _m_bucket_allr
 dt_barrier = _entry("dt_barrier", _m_barrier)
 dt_layer_norm = _entry("dt_layer_norm", _m_layer_norm)
 dt_layer_norm_backward = _entry("dt_layer_norm_backward", _m_layer_norm_backward)
+dt_vocab_loss = _entry("dt_vocab_loss", _m_vocab_loss)
+dt_vocab_loss_backward = _entry("dt_vocab_loss_backward", _m_vocab_loss_backward)
+
+
+def dt_vocab_loss_workspace(g: int, vocab: Sequence | None, vocab_equal: int, tokens: int, dim: int,
+                            dtype, backward: bool) -> int:
+    """Workspace bytes of dt_vocab_loss, or of dt_vocab_loss_backward (0: invalid argument)."""
+    return int(_lib.dt_vocab_loss_workspace(g, _rows_array(vocab), vocab_equal, tokens, dim,
+                                            _code(DTYPES, dtype), int(bool(backward))))
 
 
 def dt_layer_norm_workspace(g: int, cols: int) -> int:

@@ -241,3 +241,7 @@ def test_operator_calls_without_a_group_are_invalid(dt):
     assert lib.dt_layer_norm(None, *[None] * 7, 0, 0, 1e-5, 0, 0, None) == dt.DT_ERR_INVALID
     assert lib.dt_layer_norm_backward(None, *[None] * 9, 0, 0, 0, 0, 0, None, 0, None) == dt.DT_ERR_INVALID
     assert lib.dt_layer_norm_workspace(None, 64) == 0
+    assert lib.dt_vocab_loss(None, None, None, None, 0, None, 0, 0, 1, 0, 0, *[None] * 4, 0, None) == dt.DT_ERR_INVALID
+    assert lib.dt_vocab_loss_backward(None, None, None, None, 0, None, None, None, 0, 0, 1, 0, 0, None, None, None, 0,
+                                      None) == dt.DT_ERR_INVALID
+    assert lib.dt_vocab_loss_workspace(None, None, 8, 8, 8, 1, 0) == 0
