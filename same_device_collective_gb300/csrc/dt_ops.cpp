@@ -100,7 +100,7 @@ constexpr size_t kMaxTokens = (size_t)1 << 30, kMaxVocab = (size_t)1 << 30, kMax
 // be laid out again, take at most this much.
 constexpr uint64_t kPieceBytes = (uint64_t)512 << 20, kPackBytes = (uint64_t)128 << 20;
 // Vocabulary tiles next to one another in the order of tiles: with 16, the
-// 152 tiles in flight are about 10 x 16, nearly as many rows as columns.
+// 76 pairs of CTAs work on about 5 x 16 tiles of 256 x 256.
 constexpr uint32_t kGroup = 16;
 
 uint64_t up(uint64_t n, uint64_t to) { return (n + to - 1) / to * to; }
@@ -110,21 +110,23 @@ uint64_t up(uint64_t n, uint64_t to) { return (n + to - 1) / to * to; }
 struct VocabPlan {
     size_t rows[DT_MAX_RANKS];
     uint32_t units, pieces, piece;      // units of 256 rows; pieces of at most `piece` units
+    bool pairs;                         // two CTAs share a tile
     uint32_t bn;                        // width of the logits' tiles
+    uint32_t parts;                     // partial sums of a unit
     uint32_t pitch;                     // of rows laid out again
     uint32_t splits, apitch;
     bool packed;
     uint64_t part, logit, sums, kept, ticket, scale, g, acc, pack_h, pack_w, bytes;
 };
 
-// The widest tile that still gives every SM one: a wide tile reads its
+// The widest tile that still gives every worker one: a wide tile reads its
 // operands from L2 less often, but 32768 weights of few tokens are 128 tiles
 // of 256 for 152 SMs and 512 of 64.
-uint32_t tile_width(uint64_t mt, uint64_t units, uint64_t sms)
+uint32_t tile_width(uint64_t mt, uint64_t units, uint64_t workers, uint32_t least)
 {
-    for (uint32_t bn = 256; bn > 64; bn /= 2)
-        if (mt * units * (dt::kVocabUnit / bn) >= sms) return bn;
-    return 64;
+    for (uint32_t bn = 256; bn > least; bn /= 2)
+        if (mt * units * (dt::kVocabUnit / bn) >= workers) return bn;
+    return least;
 }
 
 bool vocab_plan(dt_group *g, const size_t *vocab, size_t vocab_equal, size_t tokens, size_t dim, bool back, bool packed,
@@ -139,7 +141,9 @@ bool vocab_plan(dt_group *g, const size_t *vocab, size_t vocab_equal, size_t tok
         v.units += (uint32_t)((v.rows[r] + dt::kVocabUnit - 1) / dt::kVocabUnit);
     }
     if (total == 0) return false;
-    const uint64_t sms = (uint64_t)dt::sm_count(g->device), mt = (tokens + 127) / 128;
+    v.pairs = tokens > 128;
+    const uint64_t workers = dt::vocab_workers(v.pairs, g->device), high = v.pairs ? 256 : 128;
+    const uint64_t mt = (tokens + high - 1) / high;
     v.packed = packed;
     v.pitch = (uint32_t)up(dim, 8);
     const uint64_t pack_units = std::max<uint64_t>(1, kPackBytes / (dt::kVocabUnit * 2ull * v.pitch));
@@ -149,12 +153,18 @@ bool vocab_plan(dt_group *g, const size_t *vocab, size_t vocab_equal, size_t tok
     v.pieces = (uint32_t)((v.units + most - 1) / most);
     v.piece = (v.units + v.pieces - 1) / v.pieces;
     v.pieces = (v.units + v.piece - 1) / v.piece;
-    v.bn = tile_width(mt, v.piece, sms);
-    // few tokens: the vocabulary is split over the SMs that dh's tiles leave idle
+    // a pair's halves of a tile, and a tile that is stored, are boxes of 64 columns
+    v.bn = tile_width(mt, v.piece, workers, v.pairs ? 128 : 64);
+    v.parts = v.bn == 64 ? 4 : dt::kVocabUnit / (v.bn / 2);
+    // few tokens: the vocabulary is split over the workers that dh's tiles leave idle
     v.apitch = (uint32_t)up(dim, 4);
     const uint64_t tiles = mt * ((dim + 255) / 256), kblocks = 4ull * (v.units - (v.pieces - 1) * v.piece);
     v.splits = 1;
-    if (back && tiles && tiles < sms) v.splits = (uint32_t)std::max<uint64_t>(1, std::min(sms / tiles, kblocks / 4));
+    if (back && tiles && tiles < workers)
+        v.splits = (uint32_t)std::max<uint64_t>(1, std::min(workers / tiles, kblocks / 4));
+
+    // tiles are counted in 32 bits
+    if (mt * v.piece * 4 > 0x7FFFFFFF || tiles * v.splits + 2ull * v.piece * ((dim + 255) / 256) > 0x7FFFFFFF) return false;
 
     uint64_t at = 0;
     auto take = [&at](uint64_t n) {
@@ -167,7 +177,7 @@ bool vocab_plan(dt_group *g, const size_t *vocab, size_t vocab_equal, size_t tok
     v.part = v.logit = v.sums = v.kept = v.g = v.acc = 0;
     if (!back) {
         const uint64_t blocks = dt::vocab_finish_blocks((uint32_t)tokens);
-        v.part = take((uint64_t)v.units * (dt::kVocabUnit / v.bn) * tokens * sizeof(float2));
+        v.part = take((uint64_t)v.units * v.parts * tokens * sizeof(float2));
         v.logit = take(tokens * 4);
         v.sums = take(blocks * 8);
         v.kept = take(blocks * 4);
@@ -295,12 +305,15 @@ cudaError_t vocab_piece(dt_group *g, const VocabPlan &v, uint32_t piece, dt::Voc
 
 void logits_tiles(const VocabPlan &v, uint32_t units, dt::VocabParams &p)
 {
+    const uint32_t high = v.pairs ? 256 : 128;
+    p.pairs = v.pairs;
     p.bn = v.bn;
-    p.mt = (p.tokens + 127) / 128;
+    p.mt = (p.tokens + high - 1) / high;
     p.nt = units * (dt::kVocabUnit / v.bn);
     p.splits = 1;
     p.group = kGroup;
     p.kblocks = (p.dim + 63) / 64;
+    p.tiles = p.mt * p.nt;
 }
 
 }  // namespace
@@ -453,7 +466,7 @@ dt_status dt_vocab_loss(dt_group_t g, const void *hidden, const void *const *wei
     f.block_kept = reinterpret_cast<uint32_t *>(ws + v.kept);
     f.ticket = p.ticket;
     f.tokens = p.tokens;
-    f.tiles = v.units * (dt::kVocabUnit / v.bn);
+    f.tiles = v.units * v.parts;
     f.vocab = p.vocab;
     f.ignore = ignore_index;
     f.avg = p.avg;
@@ -516,22 +529,17 @@ dt_status dt_vocab_loss_backward(dt_group_t g, const void *hidden, const void *c
         if (e == cudaSuccess) e = dt::launch_vocab_grad(p, g->device, s);
         if (e != cudaSuccess) break;
         p.bn = 256;
-        p.nt = p.group = wide;
+        p.nt = wide;
         p.splits = v.splits;
         p.kblocks = units * (dt::kVocabUnit / 64);
+        p.tiles = p.mt * p.nt * p.splits;
+        p.dw_tiles = units * (v.pairs ? 1 : 2) * wide;
+        p.dw_kblocks = (p.tokens + 63) / 64;
         p.acc_in = k > 0;
         p.final = v.splits == 1 && k + 1 == v.pieces;
-        e = dt::launch_vocab_dh(p, g->device, s);
-        if (e != cudaSuccess) break;
-        p.mt = units * (dt::kVocabUnit / 128);
-        p.splits = 1;
-        p.kblocks = (p.tokens + 63) / 64;
-        e = dt::launch_vocab_dw(p, g->device, s);
+        e = dt::launch_vocab_back(p, g->device, s);
     }
-    if (e == cudaSuccess && v.splits > 1) {
-        p.splits = v.splits;
-        e = dt::launch_vocab_join(p, g->device, s);
-    }
+    if (e == cudaSuccess && v.splits > 1) e = dt::launch_vocab_join(p, g->device, s);
     return cuda_status(e);
 }
 

@@ -42,34 +42,89 @@ __host__ __device__ constexpr uint32_t mma_desc(uint32_t m, uint32_t n, bool a_m
            (m / 16) << 24;
 }
 
+// The forms below take the number of CTAs that share a tile, CG: 1, or 2 for
+// the two CTAs of a cluster.  As a pair each CTA holds its half of the rows of
+// A and of the columns of B in its own shared memory, and its rows of the
+// accumulator in its own tensor memory; the first one issues the products.
+
 // One M x N x 16 product into tensor memory; `add` false overwrites.
+template <int CG>
 __device__ __forceinline__ void mma_bf16(uint32_t tmem, uint64_t a, uint64_t b, uint32_t desc, bool add)
 {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem),
-        "l"(a), "l"(b), "r"(desc), "r"((uint32_t)add)
-        : "memory");
+    if constexpr (CG == 1)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem),
+            "l"(a), "l"(b), "r"(desc), "r"((uint32_t)add)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem),
+            "l"(a), "l"(b), "r"(desc), "r"((uint32_t)add)
+            : "memory");
 }
 
-// The barrier gets one arrival once every MMA this thread issued has finished.
+// The barrier (of a pair: the barrier at this place in both CTAs) gets one
+// arrival once every MMA this thread issued has finished.
+template <int CG>
 __device__ __forceinline__ void mma_commit(uint32_t bar)
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+    if constexpr (CG == 1)
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+                     : "memory");
+    else
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+            "h"((uint16_t)3)
+            : "memory");
 }
 
-// A whole warp allocates and frees tensor memory columns; the address is
-// written to shared memory.
+// A whole warp (of a pair: one of each CTA) allocates and frees tensor memory
+// columns; the address is written to shared memory.
+template <int CG>
 __device__ __forceinline__ void tmem_alloc(uint32_t smem_slot, uint32_t columns)
 {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_slot), "r"(columns)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    if constexpr (CG == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_slot), "r"(columns)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_slot), "r"(columns)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
 }
 
+template <int CG>
 __device__ __forceinline__ void tmem_free(uint32_t tmem, uint32_t columns)
 {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(columns) : "memory");
+    if constexpr (CG == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(columns) : "memory");
+    else
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(columns) : "memory");
+}
+
+// Both CTAs of a pair; every thread of them calls it.
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+// Arrival at the barrier at this place in the pair's first CTA.
+__device__ __forceinline__ void mbar_arrive_first(uint32_t bar)
+{
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\t"
+        "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(bar)
+        : "memory");
 }
 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -104,20 +159,25 @@ __device__ __forceinline__ float tmem_load1(uint32_t tmem)
     return __uint_as_float(r);
 }
 
-// One box of a row-major matrix at (column, row); what lies outside the matrix
-// is filled with zeros and counts towards the barrier's bytes.  The column is
-// a multiple of 64, so the copy starts on a 16-byte boundary.
+// One box of a row-major matrix at (column, row) into this CTA's shared
+// memory; what lies outside the matrix is filled with zeros and counts towards
+// the barrier's bytes.  Of a pair, both CTAs' loads complete on the first
+// CTA's barrier (its address is the own one with bit 24 cleared).  The column
+// is a multiple of 64, so the copy starts on a 16-byte boundary.
+template <int CG>
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap *map, int32_t col, int32_t row, uint32_t bar)
 {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-        ::"r"(dst), "l"(map), "r"(col), "r"(row), "r"(bar)
-        : "memory");
-}
-
-__device__ __forceinline__ void tma_prefetch_map(const CUtensorMap *map)
-{
-    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+    if constexpr (CG == 1)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+            ::"r"(dst), "l"(map), "r"(col), "r"(row), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+            "[%0], [%1, {%2, %3}], [%4];"
+            ::"r"(dst), "l"(map), "r"(col), "r"(row), "r"(bar & 0xFEFFFFFFu)
+            : "memory");
 }
 
 __device__ __forceinline__ void mbar_arrive(uint32_t bar)

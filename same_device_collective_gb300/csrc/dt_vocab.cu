@@ -5,22 +5,27 @@
 //   g_tv = s (exp(l_tv - lse_t) - [v = target_t])    dh_t = sum_v g_tv w_v    dw_v = sum_t g_tv h_t
 //
 // Each of these is a product on the tensor cores, and one persistent kernel
-// serves all four (Mode): tiles of 128 x bn outputs, operands brought by TMA
-// into a ring of shared memory stages by one thread, multiplied by one thread
-// that issues tcgen05.mma into tensor memory, and finished by four warps that
-// read the accumulator while the next tile's is being made in the other half
-// of tensor memory.
-//   kLse   logits; the finish reduces a tile's columns to a maximum and a sum
-//          of exponentials for each token: 8 bytes for bn logits.
+// serves all (Mode): tiles of 128 x bn outputs, or of 256 x bn for two CTAs of
+// a cluster, operands brought by TMA into a ring of shared memory stages by
+// one thread, multiplied by one thread that issues tcgen05.mma into tensor
+// memory, and finished by eight warps that read the accumulator while the next
+// tile's is being made in the other half of tensor memory.
+//   kLse   logits; the finish reduces half a tile's columns to a maximum and a
+//          sum of exponentials for each token: 8 bytes for 128 logits.
 //   kGrad  the same logits again; the finish makes p - [target] and stores it
 //          as bf16 for a piece of the vocabulary at a time.  That is the one
-//          rounding on the way (2^-9 of each term, as the outputs' own): the
-//          two products below need it in the operands' type.  The scale s is
-//          applied to their fp32 sums.
-//   kDh    the piece's g times its rows of w.  Over several pieces, or when
+//          rounding on the way (2^-8 of each term at most, as the outputs'
+//          own): the two products below need it in the operands' type.  The
+//          scale s is applied to their fp32 sums.
+//   kBack  dh, the piece's g times its rows of w, and dw, the piece's g
+//          transposed times h, in one launch: a tile of dh takes as long as
+//          many of dw, so the tiles of dw fill what dh leaves of the last wave.
+//          dw is final for these rows of w.  dh over several pieces, or when
 //          the vocabulary is split over blocks because there are few tokens,
-//          the sums stay in fp32 and are joined in a fixed order.
-//   kDw    the piece's g, transposed, times h: final for these rows of w.
+//          stays in fp32 and is joined in a fixed order.
+// A pair of CTAs halves what each reads of B: a stage is 32 KB instead of 48,
+// six of them fit instead of four, and L2 feeds a third less.  It takes 256
+// rows of A, so up to 128 tokens a CTA works alone.
 // Rank boundaries are no more than an offset: the ranks' rows are numbered
 // through in units of 256 (the last unit of a rank is padded by zeros that TMA
 // fills in), so the reductions over the ranks (of the maximum, the sum and dh)
@@ -29,6 +34,8 @@
 // With n tokens the work is 2 n flops for each byte of w: below about 280
 // tokens HBM bounds it, above it the tensor cores do.
 #include <cudaTypedefs.h>
+
+#include <algorithm>
 
 #include "dt_ops.h"
 
@@ -42,26 +49,29 @@
 namespace dt {
 namespace {
 
-enum Mode { kLse, kGrad, kDh, kDw };
+enum Mode { kLse, kGrad, kBack };
 
 constexpr float kLog2e = 1.44269504088896340736f;
 
-constexpr uint32_t kM = 128;                       // rows of a tile
+constexpr uint32_t kM = 128;                       // rows of a tile in a CTA
 constexpr uint32_t kABytes = 2 * kBoxBytes;        // 128 x 64 operand A of a stage
 constexpr uint32_t kRingBytes = 192 * 1024;
 constexpr uint32_t kMaxStages = 8;
 constexpr uint32_t kTmemColumns = 512;             // two accumulators of 128 x 256 fp32
-constexpr int kTcThreads = 7 * 32;                 // 4 finishing warps, TMA, MMA, side work
+constexpr uint32_t kFinishWarps = 8;
+constexpr int kTcThreads = (kFinishWarps + 3) * 32;   // and TMA, MMA, side work
 constexpr uint32_t kStageOut = 4096;               // a finishing warp's 32 rows x 128 bytes
 constexpr uint32_t kBarBytes = 1024;
-constexpr size_t kTcSmem = 1024 + kRingBytes + 4 * kStageOut + kBarBytes;
+constexpr size_t kTcSmem = 1024 + kRingBytes + kFinishWarps * kStageOut + kBarBytes;
+static_assert(kTcSmem <= 227 * 1024, "shared memory above the per-block limit");
 
 // Where a tile's operands and outputs are.
 struct Tile {
+    bool dw;             // kBack: a tile of dw, not of dh
     uint32_t m0, n0;     // first row and column of the output
     uint32_t kb0, kb1;   // blocks of 64 of the inner dimension
     uint32_t split;
-    int r;               // rank and row there of the vocabulary rows that the tile covers (kLse, kGrad: n; kDw: m)
+    int r;               // rank and row there of the vocabulary rows that the tile covers (logits: n; dw: m)
     uint32_t vrow;
 };
 
@@ -75,30 +85,64 @@ __device__ __forceinline__ int unit_rank(const VocabParams &p, uint32_t unit, ui
     return r;
 }
 
-template <int MODE>
-__device__ __forceinline__ Tile tile_of(const VocabParams &p, uint32_t i)
+// The k-th tile of worker q (a CTA or a pair) of W; false when it has no more.
+// Logits: tile q + k W, columns in groups of 16, rows slowest within a group,
+// so that the tiles in flight share few rows and columns and their operands
+// come from L2.
+// kBack: first the tiles of dh, one by one to the workers.  While the first
+// dh_rest workers still have one more of them, the others take dw_early tiles
+// of dw each; then all take the rest of dw in turn.
+template <int MODE, int CG>
+__device__ __forceinline__ bool next_tile(const VocabParams &p, uint32_t q, uint32_t W, uint32_t k, Tile &t)
 {
-    Tile t;
-    const uint32_t per_split = p.mt * p.nt;
-    t.split = i / per_split;
-    i -= t.split * per_split;
-    // columns in groups of `group`, rows slowest within a group: the tiles in
-    // flight share few rows and columns, so that operands come from L2
-    const uint32_t g = i / (p.group * p.mt), in = i - g * p.group * p.mt;
-    const uint32_t width = min(p.group, p.nt - g * p.group);
-    const uint32_t m = in / width, n = g * p.group + in % width;
-    t.m0 = m * kM;
-    t.n0 = n * p.bn;
-    t.kb0 = (uint32_t)((uint64_t)p.kblocks * t.split / p.splits);
-    t.kb1 = (uint32_t)((uint64_t)p.kblocks * (t.split + 1) / p.splits);
+    uint32_t i, width;
+    t.dw = false;
+    t.split = 0;
     t.r = 0;
     t.vrow = 0;
-    if (MODE != kDh) {
-        const uint32_t v = MODE == kDw ? t.m0 : t.n0;
-        t.r = unit_rank(p, p.unit0 + v / kVocabUnit, t.vrow);
-        t.vrow += v % kVocabUnit;
+    if (MODE != kBack) {
+        i = q + k * W;
+        if (i >= p.tiles) return false;
+        const uint32_t g = i / (p.group * p.mt);
+        i -= g * p.group * p.mt;
+        width = min(p.group, p.nt - g * p.group);
+        t.m0 = i / width * (kM * CG);
+        t.n0 = (g * p.group + i % width) * p.bn;
+        t.kb0 = 0;
+        t.kb1 = p.kblocks;
+        t.r = unit_rank(p, p.unit0 + t.n0 / kVocabUnit, t.vrow);
+        t.vrow += t.n0 % kVocabUnit;
+        return true;
     }
-    return t;
+    const uint32_t mine = q < p.tiles ? (p.tiles - q + W - 1) / W : 0;   // tiles of dh
+    if (k < mine) {
+        i = q + k * W;
+        const uint32_t per_split = p.mt * p.nt;
+        t.split = i / per_split;
+        i -= t.split * per_split;
+        t.m0 = i / p.nt * (kM * CG);
+        t.n0 = i % p.nt * p.bn;
+        t.kb0 = (uint32_t)((uint64_t)p.kblocks * t.split / p.splits);
+        t.kb1 = (uint32_t)((uint64_t)p.kblocks * (t.split + 1) / p.splits);
+        return true;
+    }
+    k -= mine;
+    const uint32_t others = W - p.dh_rest;
+    if (q >= p.dh_rest && k < p.dw_early) {
+        i = q - p.dh_rest + k * others;
+    } else {
+        if (q >= p.dh_rest) k -= p.dw_early;
+        i = p.dw_early * others + k * W + (q >= p.dh_rest ? q - p.dh_rest : q + others);
+    }
+    if (i >= p.dw_tiles) return false;
+    t.dw = true;
+    t.m0 = i / p.nt * (kM * CG);
+    t.n0 = i % p.nt * p.bn;
+    t.kb0 = 0;
+    t.kb1 = p.dw_kblocks;
+    t.r = unit_rank(p, p.unit0 + t.m0 / kVocabUnit, t.vrow);
+    t.vrow += t.m0 % kVocabUnit;
+    return true;
 }
 
 // Vocabulary rows of rank r from `row` on that exist, at most `most`.
@@ -107,39 +151,58 @@ __device__ __forceinline__ uint32_t rows_left(const VocabParams &p, int r, uint3
     return row >= p.rows[r] ? 0 : min(p.rows[r] - row, most);
 }
 
-// Boxes of 64 that cover `left` rows or columns, of `most`: at least one, so
-// that every stage has a load for each operand.
-__device__ __forceinline__ uint32_t boxes(uint32_t left, uint32_t most)
+// Boxes of 64 that cover the rows or columns [from, end), of `most`: at least
+// one, so that every stage has a load for each operand.  What a stage holds
+// beyond them is left over from earlier loads and reaches only rows and
+// columns of the accumulator that are not stored.
+__device__ __forceinline__ uint32_t boxes(uint32_t from, uint32_t end, uint32_t most)
 {
-    const uint32_t n = (min(left, most) + 63) / 64;
+    const uint32_t n = from < end ? (min(end - from, most) + 63) / 64 : 0;
     return n ? n : 1;
 }
 
-template <int MODE>
-__device__ __forceinline__ void load_stage(const VocabParams &p, const Tile &t, uint32_t kb, uint32_t a, uint32_t bar)
+// The boxes of A and B that CTA `half` of the tile loads for a stage.
+template <int MODE, int CG>
+__device__ __forceinline__ void stage_boxes(const VocabParams &p, const Tile &t, uint32_t half, uint32_t &na, uint32_t &nb)
 {
-    const uint32_t b = a + kABytes, k = kb * 64;
-    const uint32_t na = MODE == kDw ? 2 : boxes(p.tokens - t.m0, kM);
-    uint32_t nb;
-    if (MODE == kLse || MODE == kGrad) nb = p.packed ? p.bn / 64 : boxes(rows_left(p, t.r, t.vrow, p.bn), p.bn);
-    else nb = boxes(p.dim - t.n0, p.bn);
-    mbar_expect_tx(bar, (na + nb) * kBoxBytes);
-    if (MODE == kLse || MODE == kGrad) {
+    const uint32_t bn = p.bn / CG, m = t.m0 + half * kM, n = half * bn;
+    na = MODE == kBack && t.dw ? 2 : boxes(m, p.tokens, kM);
+    if (MODE != kBack) nb = p.packed ? bn / 64 : boxes(t.vrow + n, p.rows[t.r], bn);
+    else nb = boxes(t.n0 + n, p.dim, bn);
+}
+
+template <int MODE, int CG>
+__device__ __forceinline__ void load_stage(const VocabParams &p, const Tile &t, uint32_t half, uint32_t kb, uint32_t a,
+                                           uint32_t bar)
+{
+    const uint32_t b = a + kABytes, k = kb * 64, m = t.m0 + half * kM, n = half * (p.bn / CG);
+    uint32_t na, nb;
+    stage_boxes<MODE, CG>(p, t, half, na, nb);
+    if (half == 0) {
+        uint32_t all = na + nb;
+        if (CG == 2) {
+            uint32_t na1, nb1;
+            stage_boxes<MODE, CG>(p, t, 1, na1, nb1);
+            all += na1 + nb1;
+        }
+        mbar_expect_tx(bar, all * kBoxBytes);
+    }
+    if (MODE != kBack) {
         const CUtensorMap *w = &p.w[p.packed ? 0 : t.r];
-        const uint32_t row = p.packed ? t.n0 : t.vrow;
-        for (uint32_t i = 0; i < na; ++i) tma_box(a + i * kBoxBytes, &p.h, k, t.m0 + 64 * i, bar);
-        for (uint32_t i = 0; i < nb; ++i) tma_box(b + i * kBoxBytes, w, k, row + 64 * i, bar);
-    } else if (MODE == kDh) {
+        const uint32_t row = (p.packed ? t.n0 : t.vrow) + n;
+        for (uint32_t i = 0; i < na; ++i) tma_box<CG>(a + i * kBoxBytes, &p.h, k, m + 64 * i, bar);
+        for (uint32_t i = 0; i < nb; ++i) tma_box<CG>(b + i * kBoxBytes, w, k, row + 64 * i, bar);
+    } else if (!t.dw) {
         uint32_t row;
         const int r = unit_rank(p, p.unit0 + k / kVocabUnit, row);
         row += k % kVocabUnit;
         const CUtensorMap *w = &p.w[p.packed ? 0 : r];
         if (p.packed) row = k;
-        for (uint32_t i = 0; i < na; ++i) tma_box(a + i * kBoxBytes, &p.g, k, t.m0 + 64 * i, bar);
-        for (uint32_t i = 0; i < nb; ++i) tma_box(b + i * kBoxBytes, w, t.n0 + 64 * i, row, bar);
+        for (uint32_t i = 0; i < na; ++i) tma_box<CG>(a + i * kBoxBytes, &p.g, k, m + 64 * i, bar);
+        for (uint32_t i = 0; i < nb; ++i) tma_box<CG>(b + i * kBoxBytes, w, t.n0 + n + 64 * i, row, bar);
     } else {
-        for (uint32_t i = 0; i < na; ++i) tma_box(a + i * kBoxBytes, &p.g, t.m0 + 64 * i, k, bar);
-        for (uint32_t i = 0; i < nb; ++i) tma_box(b + i * kBoxBytes, &p.h, t.n0 + 64 * i, k, bar);
+        for (uint32_t i = 0; i < na; ++i) tma_box<CG>(a + i * kBoxBytes, &p.g, m + 64 * i, k, bar);
+        for (uint32_t i = 0; i < nb; ++i) tma_box<CG>(b + i * kBoxBytes, &p.h, t.n0 + n + 64 * i, k, bar);
     }
 }
 
@@ -203,21 +266,23 @@ struct Waits {
     }
 };
 
-template <int MODE>
-__global__ void __launch_bounds__(kTcThreads, 1) vocab_kernel(const __grid_constant__ VocabParams p)
+template <int MODE, int CG>
+__global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(kTcThreads, 1)
+vocab_kernel(const __grid_constant__ VocabParams p)
 {
-    constexpr bool kAMn = MODE == kDw, kBMn = MODE == kDh || MODE == kDw;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
     const uint32_t ring = smem_addr(smem);
     unsigned char *out_buf = smem + kRingBytes;
-    unsigned char *ctl = out_buf + 4 * kStageOut;
+    unsigned char *ctl = out_buf + kFinishWarps * kStageOut;
     const uint32_t bars = smem_addr(ctl);
     const uint32_t full = bars, empty = bars + 8 * kMaxStages;         // stage loaded; stage consumed
     const uint32_t acc_full = bars + 16 * kMaxStages, acc_empty = acc_full + 16, drained = acc_empty + 16;
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(ctl + 256);
     volatile uint32_t *gave_up = tmem_slot + 1;
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t half = CG == 2 ? cluster_rank() : 0;                // of the tile's rows
+    const uint32_t worker = blockIdx.x / CG, workers = gridDim.x / CG;
 
     DT_TL_BEGIN();
     if (threadIdx.x == 0) {
@@ -227,50 +292,55 @@ __global__ void __launch_bounds__(kTcThreads, 1) vocab_kernel(const __grid_const
         }
         for (uint32_t s = 0; s < 2; ++s) {
             mbar_init(acc_full + 8 * s, 1);
-            mbar_init(acc_empty + 8 * s, 4);
+            mbar_init(acc_empty + 8 * s, kFinishWarps * CG);
         }
         mbar_init(drained, 1);
         *gave_up = 0;
         mbar_init_fence();
     }
-    if (warp == 5) tmem_alloc(smem_addr(const_cast<uint32_t *>(tmem_slot)), kTmemColumns);
+    if (warp == kFinishWarps + 1) tmem_alloc<CG>(smem_addr(const_cast<uint32_t *>(tmem_slot)), kTmemColumns);
     tc_fence_before();
-    __syncthreads();
+    __syncwarp();
+    if (CG == 2) cluster_sync();
+    else __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     pdl_begin();
     DT_TL_WAITED();
     const Waits wait{p.sink, gave_up};
-    const uint32_t stage_bytes = kABytes + p.bn * 128;
+    const uint32_t stage_bytes = kABytes + p.bn / CG * 128;
+    Tile t;
 
-    if (warp == 4) {
+    if (warp == kFinishWarps) {
         if (lane == 0) {
             uint32_t n = 0;   // loads issued
             bool ok = true;
-            for (uint32_t i = blockIdx.x; ok && i < p.tiles; i += gridDim.x) {
-                const Tile t = tile_of<MODE>(p, i);
+            for (uint32_t k = 0; ok && next_tile<MODE, CG>(p, worker, workers, k, t); ++k) {
                 for (uint32_t kb = t.kb0; kb < t.kb1; ++kb, ++n) {
                     const uint32_t s = n % p.stages, round = n / p.stages;
                     if (!(ok = wait(empty + 8 * s, (round & 1) ^ 1))) break;
-                    load_stage<MODE>(p, t, kb, ring + s * stage_bytes, full + 8 * s);
+                    load_stage<MODE, CG>(p, t, half, kb, ring + s * stage_bytes, full + 8 * s);
                 }
             }
-            // leave nothing in flight: the stages are consumed, or at least loaded
+            // leave nothing in flight: the stages are consumed or, where that
+            // was given up, at least loaded (a pair's loads complete on its
+            // first CTA's barriers, and neither CTA leaves before the other)
             for (uint32_t k = n > p.stages ? n - p.stages : 0; k < n; ++k) {
                 const uint32_t s = k % p.stages, parity = (k / p.stages) & 1;
-                if (*gave_up || !wait(empty + 8 * s, parity)) wait(full + 8 * s, parity);
+                if ((*gave_up || !wait(empty + 8 * s, parity)) && half == 0) wait(full + 8 * s, parity);
             }
         }
         __syncwarp();
-    } else if (warp == 5) {
-        if (lane == 0) {
-            const uint32_t desc = mma_desc(kM, p.bn, kAMn, kBMn);
-            uint32_t n = 0, done = 0;
+    } else if (warp == kFinishWarps + 1) {
+        if (lane == 0 && half == 0) {
+            uint32_t n = 0;
             bool ok = true;
-            for (uint32_t i = blockIdx.x; ok && i < p.tiles; i += gridDim.x, ++done) {
-                const Tile t = tile_of<MODE>(p, i);
-                const uint32_t half = done & 1, acc = tmem + half * 256;
-                if (!(ok = wait(acc_empty + 8 * half, ((done >> 1) & 1) ^ 1))) break;
+            for (uint32_t i = 0; ok && next_tile<MODE, CG>(p, worker, workers, i, t); ++i) {
+                const bool a_mn = MODE == kBack && t.dw;
+                constexpr bool b_mn = MODE == kBack;
+                const uint32_t desc = mma_desc(kM * CG, p.bn, a_mn, b_mn), a_step = k_step_bytes(a_mn);
+                const uint32_t acc = tmem + (i & 1) * 256;
+                if (!(ok = wait(acc_empty + 8 * (i & 1), ((i >> 1) & 1) ^ 1))) break;
                 tc_fence_after();
                 for (uint32_t kb = t.kb0; kb < t.kb1; ++kb, ++n) {
                     const uint32_t s = n % p.stages;
@@ -279,20 +349,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) vocab_kernel(const __grid_const
                     const uint32_t a = ring + s * stage_bytes, b = a + kABytes;
 #pragma unroll
                     for (uint32_t k = 0; k < 4; ++k)
-                        mma_bf16(acc, smem_desc(a + k * k_step_bytes(kAMn), kAMn),
-                                 smem_desc(b + k * k_step_bytes(kBMn), kBMn), desc, kb != t.kb0 || k != 0);
-                    mma_commit(empty + 8 * s);
+                        mma_bf16<CG>(acc, smem_desc(a + k * a_step, a_mn), smem_desc(b + k * k_step_bytes(b_mn), b_mn),
+                                     desc, kb != t.kb0 || k != 0);
+                    mma_commit<CG>(empty + 8 * s);
                 }
-                if (ok) mma_commit(acc_full + 8 * half);
+                if (ok) mma_commit<CG>(acc_full + 8 * (i & 1));
             }
             if (!ok) {   // the MMAs issued so far end before tensor memory is freed
-                mma_commit(drained);
+                mma_commit<CG>(drained);
                 wait(drained, 0);
             }
         }
         __syncwarp();
-    } else if (warp == 6) {
-        // what the block's tiles do not wait for
+    } else if (warp == kFinishWarps + 2) {
+        // what the tiles do not wait for
         if (MODE == kLse && blockIdx.x == 0 && lane == 0) *p.ticket = 0;
         if (MODE == kGrad && blockIdx.x == 0 && p.unit0 == 0) {
             uint32_t kept = 0;
@@ -309,34 +379,36 @@ __global__ void __launch_bounds__(kTcThreads, 1) vocab_kernel(const __grid_const
             }
         }
     } else {
+        // Warps w and w + 4 read the same 32 rows (a warp reaches the tensor
+        // memory lanes of its number modulo 4) and take half of the columns
+        // each; tiles of 64 columns are the first four warps'.
         unsigned char *buf = out_buf + warp * kStageOut;
-        const float scale = MODE == kDh || MODE == kDw ? *p.scale : 0.0f;
-        uint32_t done = 0;
-        for (uint32_t i = blockIdx.x; i < p.tiles; i += gridDim.x, ++done) {
-            const Tile t = tile_of<MODE>(p, i);
-            const uint32_t half = done & 1;
-            const uint32_t acc = tmem + half * 256 + (warp * 32 << 16);   // this warp's 32 rows
-            const uint32_t row0 = t.m0 + warp * 32, row = row0 + lane;
-            bool ok = wait(acc_full + 8 * half, (done >> 1) & 1);
+        const float scale = MODE == kBack ? *p.scale : 0.0f;
+        const uint32_t width = p.bn >= 128 ? p.bn / 2 : p.bn, c0 = (warp >> 2) * width, c1 = min(c0 + width, p.bn);
+        for (uint32_t i = 0; next_tile<MODE, CG>(p, worker, workers, i, t); ++i) {
+            const uint32_t acc = tmem + (i & 1) * 256 + ((warp & 3) * 32 << 16);
+            const uint32_t quad = half * kM + (warp & 3) * 32;   // first of this warp's rows in the tile
+            const uint32_t row0 = t.m0 + quad, row = row0 + lane;
+            const bool ok = wait(acc_full + 8 * (i & 1), (i >> 1) & 1);
             if (__any_sync(0xFFFFFFFFu, !ok)) break;
             tc_fence_after();
 
-            if (MODE == kLse || MODE == kGrad) {
+            if (MODE != kBack) {
                 const uint32_t valid = rows_left(p, t.r, t.vrow, p.bn);
                 const int32_t target = row < p.tokens ? p.targets[row] : p.ignore;
                 // the column of this row's target in the tile, if it is there
                 const int64_t at = (int64_t)target - (int64_t)(p.first[t.r] + t.vrow);
-                const bool here = target != p.ignore && target >= 0 && at >= 0 && at < (int64_t)valid;
+                const bool here = target != p.ignore && target >= 0 && at >= (int64_t)c0 && at < (int64_t)min(c1, valid);
                 if (MODE == kLse) {
                     float top = -INFINITY, sum = 0.0f;
-                    for (uint32_t c = 0; c < p.bn; c += 32) {
+                    for (uint32_t c = c0; c < c1; c += 32) {
                         float v[32];
                         tmem_load32(acc + c, v);
 #pragma unroll
                         for (uint32_t j = 0; j < 32; ++j) top = fmaxf(top, c + j < valid ? v[j] : -INFINITY);
                     }
                     const float top2 = top == -INFINITY ? 0.0f : top * kLog2e;   // no 0 times infinity where all are -inf
-                    for (uint32_t c = 0; c < p.bn; c += 32) {
+                    for (uint32_t c = c0; c < c1; c += 32) {
                         float v[32];
                         tmem_load32(acc + c, v);
 #pragma unroll
@@ -351,9 +423,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) vocab_kernel(const __grid_const
                         const float v = tmem_load1(acc + col);
                         if (lane == who) logit = v;
                     }
-                    if (row < p.tokens) {
-                        p.part[(uint64_t)(p.unit0 * (kVocabUnit / p.bn) + t.n0 / p.bn) * p.tokens + row] =
-                            make_float2(top, sum);
+                    if (row < p.tokens && c0 < c1) {
+                        const uint64_t part = (uint64_t)p.unit0 * (kVocabUnit / width) + (t.n0 + c0) / width;
+                        p.part[part * p.tokens + row] = make_float2(top, sum);
                         if (here) p.logit[row] = logit;
                     }
                 } else {
@@ -361,7 +433,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) vocab_kernel(const __grid_const
                     const float lse2 = keep ? p.lse[row] * kLog2e : 0.0f;
                     const uint32_t col = here ? (uint32_t)at : 0xFFFFFFFFu;
                     const uint32_t rows = row0 < p.tokens ? min(p.tokens - row0, 32u) : 0;
-                    for (uint32_t c = 0; c < p.bn; c += 64) {
+                    for (uint32_t c = c0; c < c1; c += 64) {
                         uint32_t w[32];
 #pragma unroll
                         for (uint32_t q = 0; q < 2; ++q) {
@@ -381,11 +453,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) vocab_kernel(const __grid_const
                                         true, p.gbuf, (uint64_t)p.tokens * p.gpitch * 2, 0);
                     }
                 }
-            } else if (MODE == kDh) {
+            } else if (!t.dw) {
                 // fp32 sums: 32 columns a step, four to a thread on the way out
                 const uint32_t rows = row0 < p.tokens ? min(p.tokens - row0, 32u) : 0;
                 float *part = p.acc + ((uint64_t)t.split * p.tokens + row0) * p.apitch + t.n0;
-                for (uint32_t c = 0; c < p.bn && t.n0 + c < p.dim; c += 32) {
+                for (uint32_t c = c0; c < c1 && t.n0 + c < p.dim; c += 32) {
                     float v[32];
                     tmem_load32(acc + c, v);
                     __syncwarp();
@@ -425,9 +497,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) vocab_kernel(const __grid_const
                     }
                 }
             } else {
-                const uint32_t rows = rows_left(p, t.r, t.vrow + warp * 32, 32);
-                uint16_t *out = p.dw[t.r] + (uint64_t)(t.vrow + warp * 32) * p.dim + t.n0;
-                for (uint32_t c = 0; c < p.bn && t.n0 + c < p.dim; c += 64) {
+                const uint32_t rows = rows_left(p, t.r, t.vrow + quad, 32);
+                uint16_t *out = p.dw[t.r] + (uint64_t)(t.vrow + quad) * p.dim + t.n0;
+                for (uint32_t c = c0; c < c1 && t.n0 + c < p.dim; c += 64) {
                     uint32_t w[32];
 #pragma unroll
                     for (uint32_t q = 0; q < 2; ++q) {
@@ -443,13 +515,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) vocab_kernel(const __grid_const
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(acc_empty + 8 * half);
+            if (lane == 0) {
+                if (CG == 2) mbar_arrive_first(acc_empty + 8 * (i & 1));
+                else mbar_arrive(acc_empty + 8 * (i & 1));
+            }
         }
     }
     tc_fence_before();
-    __syncthreads();
+    __syncwarp();
+    if (CG == 2) cluster_sync();
+    else __syncthreads();
     tc_fence_after();
-    if (warp == 5) tmem_free(tmem, kTmemColumns);
+    if (warp == kFinishWarps + 1) tmem_free<CG>(tmem, kTmemColumns);
     DT_TL_END_BLOCK(DT_TL_VOCAB);
 }
 
@@ -593,24 +670,26 @@ __global__ void __launch_bounds__(kThreads) vocab_pack_kernel(const __grid_const
     DT_TL_END_BLOCK(DT_TL_VOCAB);
 }
 
-template <int MODE>
+template <int MODE, int CG>
 cudaError_t launch_mode(VocabParams &p, int device, cudaStream_t s)
 {
     static std::atomic<uint64_t> ready{0};   // devices whose shared memory limit is set
     const uint64_t bit = device < 64 ? 1ull << device : 0;
     if (!(ready.load(std::memory_order_acquire) & bit) || !bit) {
-        const cudaError_t e = cudaFuncSetAttribute(vocab_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        const cudaError_t e = cudaFuncSetAttribute(vocab_kernel<MODE, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    (int)kTcSmem);
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit, std::memory_order_release);
     }
-    p.stages = kRingBytes / (kABytes + p.bn * 128);
-    if (p.stages > kMaxStages) p.stages = kMaxStages;
-    const uint64_t tiles = (uint64_t)p.mt * p.nt * p.splits;
-    if (tiles > 0x7FFFFFFFu) return cudaErrorInvalidValue;
-    p.tiles = (uint32_t)tiles;
-    const uint32_t sms = (uint32_t)sm_count(device);
-    return launch_kernel(vocab_kernel<MODE>, dim3(p.tiles < sms ? p.tiles : sms), dim3(kTcThreads), kTcSmem, s, false, p);
+    p.stages = std::min(kMaxStages, kRingBytes / (kABytes + p.bn / CG * 128));
+    return launch_kernel(vocab_kernel<MODE, CG>, dim3(std::min(p.workers, vocab_workers(CG == 2, device)) * CG),
+                         dim3(kTcThreads), kTcSmem, s, false, p);
+}
+
+template <int MODE>
+cudaError_t launch_mode(VocabParams &p, int device, cudaStream_t s)
+{
+    return p.pairs ? launch_mode<MODE, 2>(p, device, s) : launch_mode<MODE, 1>(p, device, s);
 }
 
 unsigned elementwise_grid(uint64_t items, int device)
@@ -623,10 +702,36 @@ unsigned elementwise_grid(uint64_t items, int device)
 
 DT_TL_BINDER(bind_timeline_vocab)
 
-cudaError_t launch_vocab_lse(VocabParams &p, int device, cudaStream_t s) { return launch_mode<kLse>(p, device, s); }
-cudaError_t launch_vocab_grad(VocabParams &p, int device, cudaStream_t s) { return launch_mode<kGrad>(p, device, s); }
-cudaError_t launch_vocab_dh(VocabParams &p, int device, cudaStream_t s) { return launch_mode<kDh>(p, device, s); }
-cudaError_t launch_vocab_dw(VocabParams &p, int device, cudaStream_t s) { return launch_mode<kDw>(p, device, s); }
+uint32_t vocab_workers(bool pairs, int device) { return (uint32_t)std::max(1, sm_count(device) / (pairs ? 2 : 1)); }
+
+cudaError_t launch_vocab_lse(VocabParams &p, int device, cudaStream_t s)
+{
+    p.workers = p.tiles;
+    return launch_mode<kLse>(p, device, s);
+}
+
+cudaError_t launch_vocab_grad(VocabParams &p, int device, cudaStream_t s)
+{
+    p.workers = p.tiles;
+    return launch_mode<kGrad>(p, device, s);
+}
+
+// A finished tile costs a worker about two blocks of 64 of the inner dimension
+// more than its products.
+constexpr uint32_t kTileCost = 2;
+
+cudaError_t launch_vocab_back(VocabParams &p, int device, cudaStream_t s)
+{
+    const uint32_t W = vocab_workers(p.pairs, device);
+    p.workers = std::min(W, p.tiles + p.dw_tiles);
+    p.dh_rest = p.tiles % p.workers;
+    p.dw_early = 0;
+    if (p.dh_rest) {
+        const uint32_t others = p.workers - p.dh_rest;
+        p.dw_early = std::min((p.kblocks / p.splits + kTileCost) / (p.dw_kblocks + kTileCost), p.dw_tiles / others);
+    }
+    return launch_mode<kBack>(p, device, s);
+}
 
 cudaError_t launch_vocab_finish(const VocabFinish &p, cudaStream_t s)
 {

@@ -30,9 +30,13 @@ struct VocabParams {
     uint32_t tokens, dim;
     uint32_t bn;                       // tile width: 64, 128 or 256
     uint32_t stages;
-    uint32_t mt, nt, splits, group;    // tiles of the output, splits of the inner dimension, tile order
+    uint32_t pairs;                    // two CTAs share a tile
+    uint32_t workers;                  // CTAs or pairs that have a tile
+    uint32_t mt, nt, splits, group;    // tiles of the logits or dh, splits of the inner dimension, tile order
     uint32_t kblocks;                  // blocks of 64 of the inner dimension
-    uint32_t tiles;
+    uint32_t tiles;                    // mt * nt * splits
+    uint32_t dw_tiles, dw_kblocks;     // the same of dw, whose tiles have the width of dh's
+    uint32_t dh_rest, dw_early;        // the order of both (next_tile)
     uint32_t gpitch, apitch;
     uint32_t acc_in, final;            // dh: add to the sums so far; store the result
     uint32_t dh_vec, dw_vec;           // rows start on 8- and 16-byte boundaries
@@ -41,7 +45,7 @@ struct VocabParams {
     const int32_t *targets;
     const float *lse;
     const float *grad;
-    float2 *part;                      // [tiles of the vocabulary][tokens]: maximum, sum of exponentials
+    float2 *part;                      // [half tiles of the vocabulary][tokens]: maximum, sum of exponentials
     float *logit;                      // the target's logit of each token
     uint32_t *ticket;
     float *scale;                      // grad, or grad / counted tokens
@@ -78,8 +82,9 @@ struct VocabPack {
 
 cudaError_t launch_vocab_lse(VocabParams &p, int device, cudaStream_t s);
 cudaError_t launch_vocab_grad(VocabParams &p, int device, cudaStream_t s);
-cudaError_t launch_vocab_dh(VocabParams &p, int device, cudaStream_t s);
-cudaError_t launch_vocab_dw(VocabParams &p, int device, cudaStream_t s);
+cudaError_t launch_vocab_back(VocabParams &p, int device, cudaStream_t s);
+// CTAs, or pairs of them, that run at once.
+uint32_t vocab_workers(bool pairs, int device);
 cudaError_t launch_vocab_join(const VocabParams &p, int device, cudaStream_t s);
 cudaError_t launch_vocab_finish(const VocabFinish &p, cudaStream_t s);
 uint32_t vocab_finish_blocks(uint32_t tokens);
