@@ -119,14 +119,13 @@ struct VocabPlan {
     uint64_t part, logit, sums, kept, ticket, scale, g, acc, pack_h, pack_w, bytes;
 };
 
-// The widest tile that still gives every worker one: a wide tile reads its
-// operands from L2 less often, but 32768 weights of few tokens are 128 tiles
-// of 256 for 152 SMs and 512 of 64.
-uint32_t tile_width(uint64_t mt, uint64_t units, uint64_t workers, uint32_t least)
+// The wider of two tiles, where that still gives every worker one: a wide tile
+// reads its operands from L2 less often, but 8192 weights of few tokens are 64
+// tiles of 128 for 152 SMs and 128 of 64.
+uint32_t tile_width(uint64_t mt, uint64_t units, uint64_t workers, bool pairs)
 {
-    for (uint32_t bn = 256; bn > least; bn /= 2)
-        if (mt * units * (dt::kVocabUnit / bn) >= workers) return bn;
-    return least;
+    const uint32_t bn = pairs ? 256 : 128;
+    return mt * units * (dt::kVocabUnit / bn) >= workers ? bn : bn / 2;
 }
 
 bool vocab_plan(dt_group *g, const size_t *vocab, size_t vocab_equal, size_t tokens, size_t dim, bool back, bool packed,
@@ -153,18 +152,18 @@ bool vocab_plan(dt_group *g, const size_t *vocab, size_t vocab_equal, size_t tok
     v.pieces = (uint32_t)((v.units + most - 1) / most);
     v.piece = (v.units + v.pieces - 1) / v.pieces;
     v.pieces = (v.units + v.piece - 1) / v.piece;
-    // a pair's halves of a tile, and a tile that is stored, are boxes of 64 columns
-    v.bn = tile_width(mt, v.piece, workers, v.pairs ? 128 : 64);
+    v.bn = tile_width(mt, v.piece, workers, v.pairs);
     v.parts = v.bn == 64 ? 4 : dt::kVocabUnit / (v.bn / 2);
     // few tokens: the vocabulary is split over the workers that dh's tiles leave idle
     v.apitch = (uint32_t)up(dim, 4);
-    const uint64_t tiles = mt * ((dim + 255) / 256), kblocks = 4ull * (v.units - (v.pieces - 1) * v.piece);
+    const uint64_t wide = v.pairs ? 256 : 128, across = (dim + wide - 1) / wide, tiles = mt * across;
+    const uint64_t kblocks = dt::vocab_blocks(dt::kVocabUnit * (uint64_t)(v.units - (v.pieces - 1) * v.piece));
     v.splits = 1;
     if (back && tiles && tiles < workers)
-        v.splits = (uint32_t)std::max<uint64_t>(1, std::min(workers / tiles, kblocks / 4));
+        v.splits = (uint32_t)std::max<uint64_t>(1, std::min(workers / tiles, kblocks / 2));
 
     // tiles are counted in 32 bits
-    if (mt * v.piece * 4 > 0x7FFFFFFF || tiles * v.splits + 2ull * v.piece * ((dim + 255) / 256) > 0x7FFFFFFF) return false;
+    if (mt * v.piece * 4 > 0x7FFFFFFF || tiles * v.splits + 2ull * v.piece * across > 0x7FFFFFFF) return false;
 
     uint64_t at = 0;
     auto take = [&at](uint64_t n) {
@@ -257,20 +256,29 @@ dt_status vocab_common(dt_group *g, const void *hidden, const void *const *weigh
     return DT_OK;
 }
 
-// The tensor maps of the operands; where they have to be laid out again, the
-// hidden rows are, now, and w[0] is the map of a piece's rows to come.
+// The tensor maps of the ranks' rows, or of a piece's rows laid out again, in
+// boxes of box_rows.
+cudaError_t vocab_weight_maps(dt_group *g, const void *const *weight, void *workspace, const VocabPlan &v,
+                              dt::VocabParams &p, uint32_t box_rows)
+{
+    if (v.packed)
+        return dt::vocab_map(&p.w[0], static_cast<unsigned char *>(workspace) + v.pack_w, p.dim,
+                             (uint64_t)v.piece * dt::kVocabUnit, v.pitch, box_rows);
+    cudaError_t e = cudaSuccess;
+    for (int r = 0; r < g->P && e == cudaSuccess; ++r)
+        if (p.rows[r]) e = dt::vocab_map(&p.w[r], weight[r], p.dim, p.rows[r], p.dim, box_rows);
+    return e;
+}
+
+// The tensor maps of the operands as the logits' tiles read them; where rows
+// have to be laid out again, the hidden rows are, now.
 cudaError_t vocab_operands(dt_group *g, const void *hidden, const void *const *weight, void *workspace,
                            const VocabPlan &v, dt::VocabParams &p, dt::VocabPack &pack, cudaStream_t s)
 {
-    cudaError_t e = cudaSuccess;
-    if (!v.packed) {
-        e = dt::vocab_map(&p.h, hidden, p.dim, p.tokens, p.dim);
-        for (int r = 0; r < g->P && e == cudaSuccess; ++r)
-            if (p.rows[r]) e = dt::vocab_map(&p.w[r], weight[r], p.dim, p.rows[r], p.dim);
-        return e;
-    }
+    cudaError_t e = vocab_weight_maps(g, weight, workspace, v, p, v.bn / (v.pairs ? 2 : 1));
+    if (e != cudaSuccess) return e;
+    if (!v.packed) return dt::vocab_map(&p.h, hidden, p.dim, p.tokens, p.dim, 128);
     uint16_t *h = reinterpret_cast<uint16_t *>(static_cast<unsigned char *>(workspace) + v.pack_h);
-    uint16_t *w = reinterpret_cast<uint16_t *>(static_cast<unsigned char *>(workspace) + v.pack_w);
     memset(&pack, 0, sizeof pack);
     pack.src[0] = static_cast<const uint16_t *>(hidden);
     pack.dst = h;
@@ -279,14 +287,13 @@ cudaError_t vocab_operands(dt_group *g, const void *hidden, const void *const *w
     pack.pitch = v.pitch;
     pack.sink = p.sink;
     e = dt::launch_vocab_pack(pack, g->device, s);
-    if (e == cudaSuccess) e = dt::vocab_map(&p.h, h, p.dim, p.tokens, v.pitch);
-    if (e == cudaSuccess) e = dt::vocab_map(&p.w[0], w, p.dim, (uint64_t)v.piece * dt::kVocabUnit, v.pitch);
+    if (e == cudaSuccess) e = dt::vocab_map(&p.h, h, p.dim, p.tokens, v.pitch, 128);
     for (int r = 0; r < g->P; ++r) {
         pack.src[r] = static_cast<const uint16_t *>(weight[r]);
         pack.src_rows[r] = p.rows[r];
         pack.unit_end[r] = p.unit_end[r];
     }
-    pack.dst = w;
+    pack.dst = reinterpret_cast<uint16_t *>(static_cast<unsigned char *>(workspace) + v.pack_w);
     pack.P = g->P;
     return e;
 }
@@ -312,7 +319,7 @@ void logits_tiles(const VocabPlan &v, uint32_t units, dt::VocabParams &p)
     p.nt = units * (dt::kVocabUnit / v.bn);
     p.splits = 1;
     p.group = kGroup;
-    p.kblocks = (p.dim + 63) / 64;
+    p.kblocks = dt::vocab_blocks(p.dim);
     p.tiles = p.mt * p.nt;
 }
 
@@ -520,21 +527,24 @@ dt_status dt_vocab_loss_backward(dt_group_t g, const void *hidden, const void *c
     }
 
     e = vocab_operands(g, hidden, weight, workspace, v, p, pack, s);
-    if (e == cudaSuccess) e = dt::vocab_map(&p.g, p.gbuf, p.gpitch, p.tokens, p.gpitch);
-    const uint32_t wide = (uint32_t)((dim + 255) / 256);
+    if (e == cudaSuccess) e = dt::vocab_map(&p.g, p.gbuf, p.gpitch, p.tokens, p.gpitch, 128);
+    const uint32_t rows = v.bn / (v.pairs ? 2 : 1);   // of w in a CTA's tile of logits
     for (uint32_t k = 0; k < v.pieces && e == cudaSuccess; ++k) {
         uint32_t units = 0;
-        e = vocab_piece(g, v, k, p, pack, &units, s);
+        if (k > 0 && rows != 128) e = vocab_weight_maps(g, weight, workspace, v, p, rows);
+        if (e == cudaSuccess) e = vocab_piece(g, v, k, p, pack, &units, s);
         logits_tiles(v, units, p);
         if (e == cudaSuccess) e = dt::launch_vocab_grad(p, g->device, s);
         if (e != cudaSuccess) break;
-        p.bn = 256;
-        p.nt = wide;
+        if (e == cudaSuccess && rows != 128) e = vocab_weight_maps(g, weight, workspace, v, p, 128);
+        if (e != cudaSuccess) break;
+        p.bn = v.pairs ? 256 : 128;
+        p.nt = (p.dim + p.bn - 1) / p.bn;
         p.splits = v.splits;
-        p.kblocks = units * (dt::kVocabUnit / 64);
+        p.kblocks = dt::vocab_blocks(units * dt::kVocabUnit);
         p.tiles = p.mt * p.nt * p.splits;
-        p.dw_tiles = units * (v.pairs ? 1 : 2) * wide;
-        p.dw_kblocks = (p.tokens + 63) / 64;
+        p.dw_tiles = units * (v.pairs ? 1 : 2) * p.nt;
+        p.dw_kblocks = dt::vocab_blocks(p.tokens);
         p.acc_in = k > 0;
         p.final = v.splits == 1 && k + 1 == v.pieces;
         e = dt::launch_vocab_back(p, g->device, s);

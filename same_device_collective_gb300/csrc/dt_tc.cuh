@@ -1,13 +1,13 @@
 // Thin wrappers over the fifth-generation tensor core instructions (tcgen05),
 // tensor memory and tiled TMA loads, and the descriptors they take.
 //
-// Operands are bf16 tiles in shared memory, cut into boxes of 64 x 64
-// elements: 64 rows of 128 bytes, in the 128-byte swizzle that the TMA load
+// Operands are bf16 tiles in shared memory, cut into boxes of 64 columns and up
+// to 128 rows: rows of 128 bytes, in the 128-byte swizzle that the TMA load
 // applies (16-byte chunk c of row r lies at chunk c ^ (r mod 8)).  A box
 // begins on a 1024-byte boundary.  An operand whose rows run along K ("K
-// major") stacks boxes of 64 rows of M or N; one whose rows run along M or N
-// ("MN major") stacks boxes of 64 columns of M or N, each 64 deep in K.  Both
-// are what a TMA load of a row-major matrix leaves, so no operand is ever
+// major") is boxes of 64 of K and all of its M or N; one whose rows run along
+// M or N ("MN major") is boxes of 64 of M or N, each 128 deep in K.  Both are
+// what a TMA load of a row-major matrix leaves, so no operand is ever
 // transposed in memory.
 #pragma once
 
@@ -17,7 +17,7 @@
 
 namespace dt {
 
-constexpr uint32_t kBoxBytes = 64 * 128;
+constexpr uint32_t kBoxBytes = 128 * 128;   // a box of 128 rows
 
 // Shared memory matrix descriptor: address, leading and stride byte offsets
 // (in 16-byte units), the descriptor version of this architecture (bit 46)
@@ -30,9 +30,6 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, bool mn_major)
     const uint64_t lead = mn_major ? kBoxBytes / 16 : 1, stride = 1024 / 16;
     return (uint64_t)((addr >> 4) & 0x3FFF) | lead << 16 | stride << 32 | 1ull << 46 | 2ull << 61;
 }
-
-// Bytes from one K step of 16 to the next within a box.
-__host__ __device__ constexpr uint32_t k_step_bytes(bool mn_major) { return mn_major ? 16 * 128 : 32; }
 
 // Instruction descriptor of kind::f16: fp32 accumulator, bf16 operands, the
 // operands' major-ness, N / 8 and M / 16.

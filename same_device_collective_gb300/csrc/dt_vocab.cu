@@ -23,9 +23,11 @@
 //          dw is final for these rows of w.  dh over several pieces, or when
 //          the vocabulary is split over blocks because there are few tokens,
 //          stays in fp32 and is joined in a fixed order.
-// A pair of CTAs halves what each reads of B: a stage is 32 KB instead of 48,
-// six of them fit instead of four, and L2 feeds a third less.  It takes 256
-// rows of A, so up to 128 tokens a CTA works alone.
+// A pair of CTAs halves what each reads of B, so that L2 feeds a third less.
+// It takes 256 rows of A, so up to 128 tokens a CTA works alone, on tiles of at
+// most 128 columns.  A stage is 128 deep: four TMA boxes of 16 KB, which the
+// copy engine serves faster than eight of 8 KB (2048 tokens of 32768 x 4096:
+// 397 -> 328 us).
 // Rank boundaries are no more than an offset: the ranks' rows are numbered
 // through in units of 256 (the last unit of a rank is padded by zeros that TMA
 // fills in), so the reductions over the ranks (of the maximum, the sum and dh)
@@ -54,9 +56,10 @@ enum Mode { kLse, kGrad, kBack };
 constexpr float kLog2e = 1.44269504088896340736f;
 
 constexpr uint32_t kM = 128;                       // rows of a tile in a CTA
-constexpr uint32_t kABytes = 2 * kBoxBytes;        // 128 x 64 operand A of a stage
-constexpr uint32_t kRingBytes = 192 * 1024;
-constexpr uint32_t kMaxStages = 8;
+constexpr uint32_t kK = 128;                       // depth of a stage
+constexpr uint32_t kABytes = 2 * kBoxBytes;        // operand A of a stage
+constexpr uint32_t kRingBytes = 192 * 1024;        // three stages with 128 columns of B, four with 64
+constexpr uint32_t kMaxStages = 4;
 constexpr uint32_t kTmemColumns = 512;             // two accumulators of 128 x 256 fp32
 constexpr uint32_t kFinishWarps = 8;
 constexpr int kTcThreads = (kFinishWarps + 3) * 32;   // and TMA, MMA, side work
@@ -69,7 +72,7 @@ static_assert(kTcSmem <= 227 * 1024, "shared memory above the per-block limit");
 struct Tile {
     bool dw;             // kBack: a tile of dw, not of dh
     uint32_t m0, n0;     // first row and column of the output
-    uint32_t kb0, kb1;   // blocks of 64 of the inner dimension
+    uint32_t kb0, kb1;   // blocks of 128 of the inner dimension
     uint32_t split;
     int r;               // rank and row there of the vocabulary rows that the tile covers (logits: n; dw: m)
     uint32_t vrow;
@@ -151,32 +154,14 @@ __device__ __forceinline__ uint32_t rows_left(const VocabParams &p, int r, uint3
     return row >= p.rows[r] ? 0 : min(p.rows[r] - row, most);
 }
 
-// Boxes of 64 that cover the rows or columns [from, end), of `most`: at least
-// one, so that every stage has a load for each operand.  What a stage holds
-// beyond them is left over from earlier loads and reaches only rows and
-// columns of the accumulator that are not stored.
-__device__ __forceinline__ uint32_t boxes(uint32_t from, uint32_t end, uint32_t most)
-{
-    const uint32_t n = from < end ? (min(end - from, most) + 63) / 64 : 0;
-    return n ? n : 1;
-}
-
-// The boxes of A and B that CTA `half` of the tile loads for a stage.
-template <int MODE, int CG>
-__device__ __forceinline__ void stage_boxes(const VocabParams &p, const Tile &t, uint32_t half, uint32_t &na, uint32_t &nb)
-{
-    const uint32_t bn = p.bn / CG, m = t.m0 + half * kM, n = half * bn;
-    na = MODE == kBack && t.dw ? 2 : boxes(m, p.tokens, kM);
-    if (MODE != kBack) nb = p.packed ? bn / 64 : boxes(t.vrow + n, p.rows[t.r], bn);
-    else nb = boxes(t.n0 + n, p.dim, bn);
-}
-
 // What a CTA's loads of a tile have in common, worked out once a tile.  The
 // inner dimension is the column of a K-major operand and the row of an
-// MN-major one.
+// MN-major one.  An operand is two boxes, but columns of B past the width of
+// w or h are not loaded: what a stage holds there is left over from earlier
+// loads and reaches only columns of the accumulator that are not stored.
 struct Loads {
     const CUtensorMap *a, *b;
-    uint32_t na, nb, bytes;          // bytes: of both CTAs
+    uint32_t nb, bytes;              // boxes of B; bytes of both CTAs
     uint32_t am, bn;                 // first row or column along M and N
 };
 
@@ -184,23 +169,23 @@ template <int MODE, int CG>
 __device__ __forceinline__ Loads tile_loads(const VocabParams &p, const Tile &t, uint32_t half)
 {
     Loads l;
-    stage_boxes<MODE, CG>(p, t, half, l.na, l.nb);
-    l.bytes = (l.na + l.nb) * kBoxBytes;
-    if (CG == 2) {
-        uint32_t na, nb;
-        stage_boxes<MODE, CG>(p, t, half ^ 1, na, nb);
-        l.bytes += (na + nb) * kBoxBytes;
-    }
+    const uint32_t bn = p.bn / CG;   // columns of B in a CTA
     l.am = t.m0 + half * kM;
-    l.bn = half * (p.bn / CG);
+    l.bn = half * bn;
     if (MODE != kBack) {
         l.a = &p.h;
         l.b = &p.w[p.packed ? 0 : t.r];
         l.bn += p.packed ? t.n0 : t.vrow;
+        l.nb = 2;
+        l.bytes = CG * (kABytes + 2 * bn * 128);
     } else {
         l.a = &p.g;
         l.b = &p.h;
         l.bn += t.n0;
+        l.nb = l.bn + 64 < p.dim && bn > 64 ? 2 : 1;
+        const uint32_t other = t.n0 + (half ^ 1) * bn;
+        const uint32_t all = l.nb + (CG == 2 ? (other + 64 < p.dim && bn > 64 ? 2 : 1) : 0);
+        l.bytes = CG * kABytes + all * kBoxBytes;
     }
     return l;
 }
@@ -209,13 +194,20 @@ template <int MODE, int CG>
 __device__ __forceinline__ void load_stage(const VocabParams &p, const Tile &t, Loads &l, uint32_t half, uint32_t kb,
                                            uint32_t a, uint32_t bar)
 {
-    const uint32_t b = a + kABytes, k = kb * 64;
+    const uint32_t b = a + kABytes, k = kb * kK;
     if (half == 0) mbar_expect_tx(bar, l.bytes);
     if (MODE != kBack) {
-        for (uint32_t i = 0; i < l.na; ++i) tma_box<CG>(a + i * kBoxBytes, l.a, k, l.am + 64 * i, bar);
-        for (uint32_t i = 0; i < l.nb; ++i) tma_box<CG>(b + i * kBoxBytes, l.b, k, l.bn + 64 * i, bar);
-    } else if (!t.dw) {
-        uint32_t row = k;
+        const uint32_t b_box = p.bn / CG * 128;
+        tma_box<CG>(a, l.a, k, l.am, bar);
+        tma_box<CG>(b, l.b, k, l.bn, bar);
+        tma_box<CG>(a + kBoxBytes, l.a, k + 64, l.am, bar);
+        tma_box<CG>(b + b_box, l.b, k + 64, l.bn, bar);
+        return;
+    }
+    uint32_t row = k;
+    if (!t.dw) {
+        tma_box<CG>(a, l.a, k, l.am, bar);
+        tma_box<CG>(a + kBoxBytes, l.a, k + 64, l.am, bar);
         if (!p.packed) {
             const int r = unit_rank(p, p.unit0 + k / kVocabUnit, row);
             row += k % kVocabUnit;
@@ -223,12 +215,12 @@ __device__ __forceinline__ void load_stage(const VocabParams &p, const Tile &t, 
         } else {
             l.b = &p.w[0];
         }
-        for (uint32_t i = 0; i < l.na; ++i) tma_box<CG>(a + i * kBoxBytes, l.a, k, l.am + 64 * i, bar);
-        for (uint32_t i = 0; i < l.nb; ++i) tma_box<CG>(b + i * kBoxBytes, l.b, l.bn + 64 * i, row, bar);
     } else {
-        for (uint32_t i = 0; i < l.na; ++i) tma_box<CG>(a + i * kBoxBytes, l.a, l.am + 64 * i, k, bar);
-        for (uint32_t i = 0; i < l.nb; ++i) tma_box<CG>(b + i * kBoxBytes, l.b, l.bn + 64 * i, k, bar);
+        tma_box<CG>(a, l.a, l.am, k, bar);
+        tma_box<CG>(a + kBoxBytes, l.a, l.am + 64, k, bar);
     }
+    tma_box<CG>(b, l.b, l.bn, row, bar);
+    if (l.nb == 2) tma_box<CG>(b + kBoxBytes, l.b, l.bn + 64, row, bar);
 }
 
 // A finishing warp's 32 rows x 128 bytes in shared memory, 16-byte chunk c of
@@ -345,7 +337,7 @@ vocab_kernel(const __grid_constant__ VocabParams p)
     pdl_begin();
     DT_TL_WAITED();
     const Waits wait{p.sink, gave_up};
-    const uint32_t stage_bytes = kABytes + p.bn / CG * 128;
+    const uint32_t stage_bytes = kABytes + p.bn / CG * 256;
     Tile t;
 
     if (warp == kFinishWarps) {
@@ -376,18 +368,23 @@ vocab_kernel(const __grid_constant__ VocabParams p)
             for (uint32_t i = 0; ok && next_tile<MODE, CG>(p, worker, workers, i, t); ++i) {
                 const bool a_mn = MODE == kBack && t.dw;
                 constexpr bool b_mn = MODE == kBack;
-                const uint32_t desc = mma_desc(kM * CG, p.bn, a_mn, b_mn), a_step = k_step_bytes(a_mn);
+                const uint32_t desc = mma_desc(kM * CG, p.bn, a_mn, b_mn);
+                // from a K step of 16 to the next: 16 rows of an MN-major box;
+                // 32 bytes of a K-major one, and from its fourth to the next box
+                const uint32_t a_step = a_mn ? 16 * 128 : 32, a_next = a_mn ? 4 * a_step : kBoxBytes;
+                const uint32_t b_step = b_mn ? 16 * 128 : 32, b_next = b_mn ? 4 * b_step : p.bn / CG * 128;
                 const uint32_t acc = tmem + (i & 1) * 256;
                 if (!(ok = wait(acc_empty + 8 * (i & 1), ((i >> 1) & 1) ^ 1))) break;
                 tc_fence_after();
                 for (uint32_t kb = t.kb0; kb < t.kb1; ++kb) {
                     if (!(ok = wait(full + 8 * s, round))) break;
                     tc_fence_after();
-                    const uint32_t a = ring + s * stage_bytes, b = a + kABytes;
+                    const uint32_t at = ring + s * stage_bytes;
+                    const uint64_t a = smem_desc(at, a_mn), b = smem_desc(at + kABytes, b_mn);
 #pragma unroll
-                    for (uint32_t k = 0; k < 4; ++k)
-                        mma_bf16<CG>(acc, smem_desc(a + k * a_step, a_mn), smem_desc(b + k * k_step_bytes(b_mn), b_mn),
-                                     desc, kb != t.kb0 || k != 0);
+                    for (uint32_t k = 0; k < 8; ++k)
+                        mma_bf16<CG>(acc, a + ((k / 4 * a_next + k % 4 * a_step) >> 4),
+                                     b + ((k / 4 * b_next + k % 4 * b_step) >> 4), desc, kb != t.kb0 || k != 0);
                     mma_commit<CG>(empty + 8 * s);
                     if (++s == p.stages) s = 0, round ^= 1;
                 }
@@ -719,7 +716,7 @@ cudaError_t launch_mode(VocabParams &p, int device, cudaStream_t s)
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit, std::memory_order_release);
     }
-    p.stages = std::min(kMaxStages, kRingBytes / (kABytes + p.bn / CG * 128));
+    p.stages = std::min(kMaxStages, kRingBytes / (kABytes + p.bn / CG * 256));
     return launch_kernel(vocab_kernel<MODE, CG>, dim3(std::min(p.workers, vocab_workers(CG == 2, device)) * CG),
                          dim3(kTcThreads), kTcSmem, s, false, p);
 }
@@ -740,6 +737,8 @@ unsigned elementwise_grid(uint64_t items, int device)
 
 DT_TL_BINDER(bind_timeline_vocab)
 
+uint32_t vocab_blocks(uint64_t inner) { return (uint32_t)((inner + kK - 1) / kK); }
+
 uint32_t vocab_workers(bool pairs, int device) { return (uint32_t)std::max(1, sm_count(device) / (pairs ? 2 : 1)); }
 
 cudaError_t launch_vocab_lse(VocabParams &p, int device, cudaStream_t s)
@@ -754,9 +753,9 @@ cudaError_t launch_vocab_grad(VocabParams &p, int device, cudaStream_t s)
     return launch_mode<kGrad>(p, device, s);
 }
 
-// A finished tile costs a worker about two blocks of 64 of the inner dimension
-// more than its products.
-constexpr uint32_t kTileCost = 2;
+// A finished tile costs a worker about a block of the inner dimension more than
+// its products.
+constexpr uint32_t kTileCost = 1;
 
 cudaError_t launch_vocab_back(VocabParams &p, int device, cudaStream_t s)
 {
@@ -790,7 +789,7 @@ cudaError_t launch_vocab_pack(const VocabPack &p, int device, cudaStream_t s)
                          dim3(kThreads), 0, s, false, p);
 }
 
-cudaError_t vocab_map(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows, uint64_t pitch)
+cudaError_t vocab_map(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows, uint64_t pitch, uint32_t box_rows)
 {
     static std::atomic<void *> entry{nullptr};
     void *fn = entry.load(std::memory_order_acquire);
@@ -803,7 +802,7 @@ cudaError_t vocab_map(CUtensorMap *map, const void *base, uint64_t cols, uint64_
         entry.store(fn, std::memory_order_release);
     }
     const cuuint64_t dims[2] = {cols, rows}, strides[1] = {pitch * 2};
-    const cuuint32_t box[2] = {64, 64}, steps[2] = {1, 1};
+    const cuuint32_t box[2] = {64, box_rows}, steps[2] = {1, 1};
     const CUresult r = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn)(
         map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, steps,
         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

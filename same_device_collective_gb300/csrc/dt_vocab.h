@@ -28,12 +28,12 @@ struct VocabParams {
     uint32_t packed;
     uint32_t unit0;                    // the piece's first unit
     uint32_t tokens, dim;
-    uint32_t bn;                       // tile width: 64, 128 or 256
+    uint32_t bn;                       // tile width: 64 or 128, of pairs 128 or 256
     uint32_t stages;
     uint32_t pairs;                    // two CTAs share a tile
     uint32_t workers;                  // CTAs or pairs that have a tile
     uint32_t mt, nt, splits, group;    // tiles of the logits or dh, splits of the inner dimension, tile order
-    uint32_t kblocks;                  // blocks of 64 of the inner dimension
+    uint32_t kblocks;                  // blocks of the inner dimension
     uint32_t tiles;                    // mt * nt * splits
     uint32_t dw_tiles, dw_kblocks;     // the same of dw, whose tiles have the width of dh's
     uint32_t dh_rest, dw_early;        // the order of both (next_tile)
@@ -89,7 +89,10 @@ cudaError_t launch_vocab_join(const VocabParams &p, int device, cudaStream_t s);
 cudaError_t launch_vocab_finish(const VocabFinish &p, cudaStream_t s);
 uint32_t vocab_finish_blocks(uint32_t tokens);
 cudaError_t launch_vocab_pack(const VocabPack &p, int device, cudaStream_t s);
-// The tensor map of a row-major bf16 matrix, read in boxes of 64 x 64.
-cudaError_t vocab_map(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows, uint64_t pitch);
+// Blocks of an inner dimension of `inner`.
+uint32_t vocab_blocks(uint64_t inner);
+// The tensor map of a row-major bf16 matrix, read in boxes of 64 columns.
+cudaError_t vocab_map(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows, uint64_t pitch,
+                      uint32_t box_rows);
 
 }  // namespace dt
