@@ -119,13 +119,15 @@ struct VocabPlan {
     uint64_t part, logit, sums, kept, ticket, scale, g, acc, pack_h, pack_w, bytes;
 };
 
-// The wider of two tiles, where that still gives every worker one: a wide tile
-// reads its operands from L2 less often, but 8192 weights of few tokens are 64
-// tiles of 128 for 152 SMs and 128 of 64.
+// The wider of two tiles, unless the narrower one leaves the workers less to
+// do one after the other; a tile costs about 64 columns more than it has.  82
+// tiles of 128 for 152 SMs take less time than 164 of 64, but 128 of 64 less
+// than 64 of 128.
 uint32_t tile_width(uint64_t mt, uint64_t units, uint64_t workers, bool pairs)
 {
-    const uint32_t bn = pairs ? 256 : 128;
-    return mt * units * (dt::kVocabUnit / bn) >= workers ? bn : bn / 2;
+    const uint32_t wide = pairs ? 256 : 128;
+    auto cost = [&](uint32_t bn) { return (mt * units * (dt::kVocabUnit / bn) + workers - 1) / workers * (bn + 64); };
+    return cost(wide / 2) < cost(wide) ? wide / 2 : wide;
 }
 
 bool vocab_plan(dt_group *g, const size_t *vocab, size_t vocab_equal, size_t tokens, size_t dim, bool back, bool packed,
@@ -160,7 +162,7 @@ bool vocab_plan(dt_group *g, const size_t *vocab, size_t vocab_equal, size_t tok
     const uint64_t kblocks = dt::vocab_blocks(dt::kVocabUnit * (uint64_t)(v.units - (v.pieces - 1) * v.piece));
     v.splits = 1;
     if (back && tiles && tiles < workers)
-        v.splits = (uint32_t)std::max<uint64_t>(1, std::min(workers / tiles, kblocks / 2));
+        v.splits = (uint32_t)std::max<uint64_t>(1, std::min(workers / tiles, kblocks / 8));
 
     // tiles are counted in 32 bits
     if (mt * v.piece * 4 > 0x7FFFFFFF || tiles * v.splits + 2ull * v.piece * across > 0x7FFFFFFF) return false;
@@ -257,43 +259,58 @@ dt_status vocab_common(dt_group *g, const void *hidden, const void *const *weigh
 }
 
 // The tensor maps of the ranks' rows, or of a piece's rows laid out again, in
-// boxes of box_rows.
-cudaError_t vocab_weight_maps(dt_group *g, const void *const *weight, void *workspace, const VocabPlan &v,
-                              dt::VocabParams &p, uint32_t box_rows)
+// boxes of rows_w rows, and of the hidden rows in boxes of rows_h.
+cudaError_t vocab_maps(dt_group *g, const void *hidden, const void *const *weight, void *workspace, const VocabPlan &v,
+                       dt::VocabParams &p, uint32_t rows_h, uint32_t rows_w)
 {
-    if (v.packed)
-        return dt::vocab_map(&p.w[0], static_cast<unsigned char *>(workspace) + v.pack_w, p.dim,
-                             (uint64_t)v.piece * dt::kVocabUnit, v.pitch, box_rows);
-    cudaError_t e = cudaSuccess;
-    for (int r = 0; r < g->P && e == cudaSuccess; ++r)
-        if (p.rows[r]) e = dt::vocab_map(&p.w[r], weight[r], p.dim, p.rows[r], p.dim, box_rows);
+    if (p.rows_h == rows_h && p.rows_w == rows_w) return cudaSuccess;   // as they are
+    p.rows_h = rows_h;
+    p.rows_w = rows_w;
+    unsigned char *ws = static_cast<unsigned char *>(workspace);
+    if (v.packed) {
+        p.w_maps = 1;
+        const cudaError_t e = dt::vocab_map(&p.h, ws + v.pack_h, p.dim, p.tokens, v.pitch, rows_h);
+        if (e != cudaSuccess) return e;
+        return dt::vocab_map(&p.w[0], ws + v.pack_w, p.dim, (uint64_t)v.piece * dt::kVocabUnit, v.pitch, rows_w);
+    }
+    cudaError_t e = dt::vocab_map(&p.h, hidden, p.dim, p.tokens, p.dim, rows_h);
+    for (int r = 0; r < g->P && e == cudaSuccess; ++r) {
+        if (p.rows[r] == 0) continue;
+        p.w_maps |= 1u << r;
+        e = dt::vocab_map(&p.w[r], weight[r], p.dim, p.rows[r], p.dim, rows_w);
+    }
     return e;
 }
 
-// The tensor maps of the operands as the logits' tiles read them; where rows
-// have to be laid out again, the hidden rows are, now.
+// ... as the logits' tiles read them.
+cudaError_t vocab_logit_maps(dt_group *g, const void *hidden, const void *const *weight, void *workspace,
+                             const VocabPlan &v, dt::VocabParams &p)
+{
+    const uint32_t rows_h = v.pairs ? 128 : (uint32_t)up(p.tokens, 8);
+    return vocab_maps(g, hidden, weight, workspace, v, p, rows_h, v.bn / (v.pairs ? 2 : 1));
+}
+
+// Where rows have to be laid out again, the hidden rows are, now, and `pack`
+// is prepared for the vocabulary's.
 cudaError_t vocab_operands(dt_group *g, const void *hidden, const void *const *weight, void *workspace,
                            const VocabPlan &v, dt::VocabParams &p, dt::VocabPack &pack, cudaStream_t s)
 {
-    cudaError_t e = vocab_weight_maps(g, weight, workspace, v, p, v.bn / (v.pairs ? 2 : 1));
-    if (e != cudaSuccess) return e;
-    if (!v.packed) return dt::vocab_map(&p.h, hidden, p.dim, p.tokens, p.dim, 128);
-    uint16_t *h = reinterpret_cast<uint16_t *>(static_cast<unsigned char *>(workspace) + v.pack_h);
+    if (!v.packed) return cudaSuccess;
+    unsigned char *ws = static_cast<unsigned char *>(workspace);
     memset(&pack, 0, sizeof pack);
     pack.src[0] = static_cast<const uint16_t *>(hidden);
-    pack.dst = h;
+    pack.dst = reinterpret_cast<uint16_t *>(ws + v.pack_h);
     pack.rows = p.tokens;
     pack.dim = p.dim;
     pack.pitch = v.pitch;
     pack.sink = p.sink;
-    e = dt::launch_vocab_pack(pack, g->device, s);
-    if (e == cudaSuccess) e = dt::vocab_map(&p.h, h, p.dim, p.tokens, v.pitch, 128);
+    const cudaError_t e = dt::launch_vocab_pack(pack, g->device, s);
     for (int r = 0; r < g->P; ++r) {
         pack.src[r] = static_cast<const uint16_t *>(weight[r]);
         pack.src_rows[r] = p.rows[r];
         pack.unit_end[r] = p.unit_end[r];
     }
-    pack.dst = reinterpret_cast<uint16_t *>(static_cast<unsigned char *>(workspace) + v.pack_w);
+    pack.dst = reinterpret_cast<uint16_t *>(ws + v.pack_w);
     pack.P = g->P;
     return e;
 }
@@ -453,6 +470,7 @@ dt_status dt_vocab_loss(dt_group_t g, const void *hidden, const void *const *wei
     if (tokens == 0) return loss ? cuda_status(cudaMemsetAsync(loss, 0, 4, s)) : DT_OK;
 
     cudaError_t e = vocab_operands(g, hidden, weight, workspace, v, p, pack, s);
+    if (e == cudaSuccess) e = vocab_logit_maps(g, hidden, weight, workspace, v, p);
     for (uint32_t k = 0; k < v.pieces && e == cudaSuccess; ++k) {
         uint32_t units = 0;
         e = vocab_piece(g, v, k, p, pack, &units, s);
@@ -503,12 +521,12 @@ dt_status dt_vocab_loss_backward(dt_group_t g, const void *hidden, const void *c
     b.read(lse, tokens * 4);
     b.read(grad_loss, 4);
     b.write(dhidden, tokens * dim * 2);
-    p.dw_vec = dim % 8 == 0;
+    p.dw_align = dim % 8 == 0 ? 8 : dim % 4 == 0 ? 4 : dim % 2 == 0 ? 2 : 1;
     for (int r = 0; r < g->P; ++r) {
         if (p.rows[r] == 0) continue;
         if (!dweight[r] || !multiple(dweight[r], 2)) return DT_ERR_INVALID;
         p.dw[r] = static_cast<uint16_t *>(dweight[r]);
-        p.dw_vec = p.dw_vec && aligned16(dweight[r]);
+        while (!multiple(dweight[r], 2 * p.dw_align)) p.dw_align /= 2;
         b.write(dweight[r], v.rows[r] * dim * 2);
     }
     if (b.clash()) return DT_ERR_INVALID;
@@ -527,16 +545,17 @@ dt_status dt_vocab_loss_backward(dt_group_t g, const void *hidden, const void *c
     }
 
     e = vocab_operands(g, hidden, weight, workspace, v, p, pack, s);
-    if (e == cudaSuccess) e = dt::vocab_map(&p.g, p.gbuf, p.gpitch, p.tokens, p.gpitch, 128);
-    const uint32_t rows = v.bn / (v.pairs ? 2 : 1);   // of w in a CTA's tile of logits
+    // few tokens: boxes of as many as there are, in whole K steps of 16
+    p.rows_g = v.pairs ? 128 : (uint32_t)up(p.tokens, 16);
+    if (e == cudaSuccess) e = dt::vocab_map(&p.g, p.gbuf, p.gpitch, p.tokens, p.gpitch, p.rows_g);
     for (uint32_t k = 0; k < v.pieces && e == cudaSuccess; ++k) {
         uint32_t units = 0;
-        if (k > 0 && rows != 128) e = vocab_weight_maps(g, weight, workspace, v, p, rows);
+        e = vocab_logit_maps(g, hidden, weight, workspace, v, p);
         if (e == cudaSuccess) e = vocab_piece(g, v, k, p, pack, &units, s);
         logits_tiles(v, units, p);
         if (e == cudaSuccess) e = dt::launch_vocab_grad(p, g->device, s);
         if (e != cudaSuccess) break;
-        if (e == cudaSuccess && rows != 128) e = vocab_weight_maps(g, weight, workspace, v, p, 128);
+        if (e == cudaSuccess) e = vocab_maps(g, hidden, weight, workspace, v, p, p.rows_g, 128);
         if (e != cudaSuccess) break;
         p.bn = v.pairs ? 256 : 128;
         p.nt = (p.dim + p.bn - 1) / p.bn;

@@ -17,13 +17,13 @@
 
 namespace dt {
 
-constexpr uint32_t kBoxBytes = 128 * 128;   // a box of 128 rows
+constexpr uint32_t kBoxBytes = 128 * 128;   // a box of 128 rows; MN-major boxes lie this far apart
 
 // Shared memory matrix descriptor: address, leading and stride byte offsets
 // (in 16-byte units), the descriptor version of this architecture (bit 46)
 // and the 128-byte swizzle (2 at bit 61).
 //   K major: stride offset = 8 rows of 128 bytes; the leading offset is not used.
-//   MN major: leading offset = from 64 columns to the next (one box), stride
+//   MN major: leading offset = from 64 columns to the next (kBoxBytes), stride
 //   offset = 8 rows of K.
 __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, bool mn_major)
 {
@@ -175,6 +175,11 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap *map, in
             "[%0], [%1, {%2, %3}], [%4];"
             ::"r"(dst), "l"(map), "r"(col), "r"(row), "r"(bar & 0xFEFFFFFFu)
             : "memory");
+}
+
+__device__ __forceinline__ void tma_prefetch_map(const CUtensorMap *map)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
 __device__ __forceinline__ void mbar_arrive(uint32_t bar)

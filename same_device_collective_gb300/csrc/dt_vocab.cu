@@ -25,7 +25,9 @@
 //          stays in fp32 and is joined in a fixed order.
 // A pair of CTAs halves what each reads of B, so that L2 feeds a third less.
 // It takes 256 rows of A, so up to 128 tokens a CTA works alone, on tiles of at
-// most 128 columns.  A stage is 128 deep: four TMA boxes of 16 KB, which the
+// most 128 columns, and loads only the rows there are of A: for one token 72
+// KB of w are under way at a time, in eight stages, instead of 64 in four.
+// A stage is 128 deep: four TMA boxes of 16 KB, which the
 // copy engine serves faster than eight of 8 KB (2048 tokens of 32768 x 4096:
 // 397 -> 328 us).
 // Rank boundaries are no more than an offset: the ranks' rows are numbered
@@ -57,9 +59,8 @@ constexpr float kLog2e = 1.44269504088896340736f;
 
 constexpr uint32_t kM = 128;                       // rows of a tile in a CTA
 constexpr uint32_t kK = 128;                       // depth of a stage
-constexpr uint32_t kABytes = 2 * kBoxBytes;        // operand A of a stage
-constexpr uint32_t kRingBytes = 192 * 1024;        // three stages with 128 columns of B, four with 64
-constexpr uint32_t kMaxStages = 4;
+constexpr uint32_t kRingBytes = 192 * 1024;        // three stages of 128 rows and columns of A and B
+constexpr uint32_t kMaxStages = 8;
 constexpr uint32_t kTmemColumns = 512;             // two accumulators of 128 x 256 fp32
 constexpr uint32_t kFinishWarps = 8;
 constexpr int kTcThreads = (kFinishWarps + 3) * 32;   // and TMA, MMA, side work
@@ -156,9 +157,10 @@ __device__ __forceinline__ uint32_t rows_left(const VocabParams &p, int r, uint3
 
 // What a CTA's loads of a tile have in common, worked out once a tile.  The
 // inner dimension is the column of a K-major operand and the row of an
-// MN-major one.  An operand is two boxes, but columns of B past the width of
-// w or h are not loaded: what a stage holds there is left over from earlier
-// loads and reaches only columns of the accumulator that are not stored.
+// MN-major one.  An operand is two boxes of as many rows as its map says, but
+// columns of B past the width of w or h are not loaded.  What a stage holds
+// beside its boxes is left over from earlier loads and reaches only rows and
+// columns of the accumulator that are not stored.
 struct Loads {
     const CUtensorMap *a, *b;
     uint32_t nb, bytes;              // boxes of B; bytes of both CTAs
@@ -177,37 +179,36 @@ __device__ __forceinline__ Loads tile_loads(const VocabParams &p, const Tile &t,
         l.b = &p.w[p.packed ? 0 : t.r];
         l.bn += p.packed ? t.n0 : t.vrow;
         l.nb = 2;
-        l.bytes = CG * (kABytes + 2 * bn * 128);
+        l.bytes = CG * 2 * (p.rows_h + p.rows_w) * 128;
     } else {
         l.a = &p.g;
         l.b = &p.h;
         l.bn += t.n0;
-        l.nb = l.bn + 64 < p.dim && bn > 64 ? 2 : 1;
-        const uint32_t other = t.n0 + (half ^ 1) * bn;
-        const uint32_t all = l.nb + (CG == 2 ? (other + 64 < p.dim && bn > 64 ? 2 : 1) : 0);
-        l.bytes = CG * kABytes + all * kBoxBytes;
+        l.nb = l.bn + 64 < p.dim ? 2 : 1;
+        const uint32_t all = l.nb + (CG == 2 ? (t.n0 + (half ^ 1) * bn + 64 < p.dim ? 2 : 1) : 0);
+        l.bytes = (CG * 2 * p.rows_g + all * (t.dw ? p.rows_h : p.rows_w)) * 128;
     }
     return l;
 }
 
+// a_box: from operand A's first box to its second.
 template <int MODE, int CG>
 __device__ __forceinline__ void load_stage(const VocabParams &p, const Tile &t, Loads &l, uint32_t half, uint32_t kb,
-                                           uint32_t a, uint32_t bar)
+                                           uint32_t a, uint32_t a_box, uint32_t bar)
 {
-    const uint32_t b = a + kABytes, k = kb * kK;
+    const uint32_t b = a + 2 * a_box, k = kb * kK;
     if (half == 0) mbar_expect_tx(bar, l.bytes);
     if (MODE != kBack) {
-        const uint32_t b_box = p.bn / CG * 128;
         tma_box<CG>(a, l.a, k, l.am, bar);
         tma_box<CG>(b, l.b, k, l.bn, bar);
-        tma_box<CG>(a + kBoxBytes, l.a, k + 64, l.am, bar);
-        tma_box<CG>(b + b_box, l.b, k + 64, l.bn, bar);
+        tma_box<CG>(a + a_box, l.a, k + 64, l.am, bar);
+        tma_box<CG>(b + p.rows_w * 128, l.b, k + 64, l.bn, bar);
         return;
     }
     uint32_t row = k;
     if (!t.dw) {
         tma_box<CG>(a, l.a, k, l.am, bar);
-        tma_box<CG>(a + kBoxBytes, l.a, k + 64, l.am, bar);
+        tma_box<CG>(a + a_box, l.a, k + 64, l.am, bar);
         if (!p.packed) {
             const int r = unit_rank(p, p.unit0 + k / kVocabUnit, row);
             row += k % kVocabUnit;
@@ -217,7 +218,7 @@ __device__ __forceinline__ void load_stage(const VocabParams &p, const Tile &t, 
         }
     } else {
         tma_box<CG>(a, l.a, l.am, k, bar);
-        tma_box<CG>(a + kBoxBytes, l.a, l.am + 64, k, bar);
+        tma_box<CG>(a + a_box, l.a, l.am + 64, k, bar);
     }
     tma_box<CG>(b, l.b, l.bn, row, bar);
     if (l.nb == 2) tma_box<CG>(b + kBoxBytes, l.b, l.bn + 64, row, bar);
@@ -239,34 +240,84 @@ __device__ __forceinline__ uint4 *out_chunk(unsigned char *buf, uint32_t row, ui
 #define VOCAB_OK(a, n, lo, bytes, buffer) true
 #endif
 
-// 64 columns of bf16, packed two to a word: this thread's row into `buf`,
-// then the warp's rows to memory, whole lines at a time where rows are
-// vectors (vec), else element by element.
-__device__ __forceinline__ void store_rows_bf16(const VocabParams &p, unsigned char *buf, const uint32_t (&w)[32],
-                                                uint16_t *out, uint64_t pitch, uint32_t rows, uint32_t cols, bool vec,
-                                                const void *lo, uint64_t bytes, int buffer)
+// One instruction's worth of a row: N 16-bit elements.
+template <int N> struct Words;
+template <> struct Words<8> { using type = uint4; };
+template <> struct Words<4> { using type = uint2; };
+template <> struct Words<2> { using type = uint32_t; };
+
+// A warp's rows from `buf` to memory, N elements of a row to a lane and as
+// many rows at a time as that leaves lanes for.
+template <int N>
+__device__ __forceinline__ void store_rows(const VocabParams &p, const unsigned char *buf, uint16_t *out, uint64_t pitch,
+                                           uint32_t rows, uint32_t cols, const void *lo, uint64_t bytes, int buffer)
+{
+    using W = typename Words<N>::type;
+    (void)p, (void)lo, (void)bytes, (void)buffer;
+    constexpr uint32_t kLanes = 64 / N, kRows = 32 / kLanes;
+    const uint32_t lane = threadIdx.x & 31, e = lane % kLanes * N, first = lane / kLanes;
+    if (e >= cols) return;
+#pragma unroll 8
+    for (uint32_t k = 0; k < 32; k += kRows) {
+        const uint32_t row = k + first;
+        const W v = *reinterpret_cast<const W *>(buf + row * 128 + ((((e >> 3) ^ row) & 7) << 4) + (e & 7) * 2);
+        uint16_t *to = out + row * pitch + e;
+        if (row < rows && VOCAB_OK(to, 2 * N, lo, bytes, buffer)) *reinterpret_cast<W *>(to) = v;
+    }
+}
+
+// The same for rows of an odd width, every other one of which starts between
+// two words: a lane's word is then made of its neighbour's halves, and the
+// row's first and last elements go by themselves.
+__device__ __forceinline__ void store_rows_odd(const VocabParams &p, const unsigned char *buf, uint16_t *out,
+                                               uint64_t pitch, uint32_t rows, uint32_t cols, const void *lo,
+                                               uint64_t bytes, int buffer)
 {
     (void)p, (void)lo, (void)bytes, (void)buffer;
+    const uint32_t lane = threadIdx.x & 31;
+#pragma unroll 8
+    for (uint32_t row = 0; row < 32; ++row) {
+        const uint32_t w = *reinterpret_cast<const uint32_t *>(buf + row * 128 + ((((lane >> 2) ^ row) & 7) << 4) +
+                                                               (lane & 3) * 4);
+        const uint32_t next = __shfl_down_sync(0xFFFFFFFFu, w, 1);
+        if (row >= rows) continue;
+        uint16_t *at = out + row * pitch;
+        const uint32_t odd = (reinterpret_cast<uintptr_t>(at) >> 1) & 1, e = 2 * lane + odd;
+        const uint32_t v = odd ? __funnelshift_r(w, next, 16) : w;
+        if (e + 1 < cols) {
+            if (VOCAB_OK(at + e, 4, lo, bytes, buffer)) *reinterpret_cast<uint32_t *>(at + e) = v;
+        } else if (e < cols) {
+            if (VOCAB_OK(at + e, 2, lo, bytes, buffer)) at[e] = (uint16_t)v;
+        }
+        if (odd && lane == 0 && VOCAB_OK(at, 2, lo, bytes, buffer)) at[0] = (uint16_t)w;
+    }
+}
+
+// 64 columns of bf16, packed two to a word: this thread's row into `buf`,
+// then the warp's rows to memory in the widest words that their alignment
+// allows (2 * align bytes).  Element by element a tile of dw 500 columns wide
+// took 9700 cycles, against 1000 of its products.
+__device__ __forceinline__ void store_rows_bf16(const VocabParams &p, unsigned char *buf, const uint32_t (&w)[32],
+                                                uint16_t *out, uint64_t pitch, uint32_t rows, uint32_t cols,
+                                                uint32_t align, const void *lo, uint64_t bytes, int buffer)
+{
     const uint32_t lane = threadIdx.x & 31;
     __syncwarp();
 #pragma unroll
     for (uint32_t c = 0; c < 8; ++c)
         *out_chunk(buf, lane, c) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
     __syncwarp();
-    if (vec) {
-        const uint32_t c = lane & 7;
-        for (uint32_t row = lane >> 3; row < rows && c * 8 < cols; row += 4) {
-            uint16_t *to = out + row * pitch + c * 8;
-            if (VOCAB_OK(to, 16, lo, bytes, buffer)) *reinterpret_cast<uint4 *>(to) = *out_chunk(buf, row, c);
-        }
-    } else {
-        for (uint32_t row = 0; row < rows; ++row)
-            for (uint32_t e = lane; e < cols; e += 32) {
-                const uint16_t v = reinterpret_cast<const uint16_t *>(out_chunk(buf, row, e >> 3))[e & 7];
-                uint16_t *to = out + row * pitch + e;
-                if (VOCAB_OK(to, 2, lo, bytes, buffer)) *to = v;
-            }
-    }
+    if (align == 8) store_rows<8>(p, buf, out, pitch, rows, cols, lo, bytes, buffer);
+    else if (align == 4) store_rows<4>(p, buf, out, pitch, rows, cols, lo, bytes, buffer);
+    else if (align == 2) store_rows<2>(p, buf, out, pitch, rows, cols, lo, bytes, buffer);
+    else store_rows_odd(p, buf, out, pitch, rows, cols, lo, bytes, buffer);
+}
+
+// From operand A's first box to its second: K-major boxes of few tokens' rows
+// lie closer, MN-major ones are a fixed way apart.
+__host__ __device__ constexpr uint32_t a_box_bytes(bool back, uint32_t rows)
+{
+    return back ? kBoxBytes : (rows * 128 + 1023) / 1024 * 1024;
 }
 
 // The state of the pipeline's waits: a wait that runs out is recorded once,
@@ -327,6 +378,11 @@ vocab_kernel(const __grid_constant__ VocabParams p)
         *gave_up = 0;
         mbar_init_fence();
     }
+    if (warp == kFinishWarps) {
+        if (lane < DT_MAX_RANKS && p.w_maps >> lane & 1) tma_prefetch_map(&p.w[lane]);
+        if (lane == DT_MAX_RANKS) tma_prefetch_map(&p.h);
+        if (MODE == kBack && lane == DT_MAX_RANKS + 1) tma_prefetch_map(&p.g);
+    }
     if (warp == kFinishWarps + 1) tmem_alloc<CG>(smem_addr(const_cast<uint32_t *>(tmem_slot)), kTmemColumns);
     tc_fence_before();
     __syncwarp();
@@ -337,7 +393,7 @@ vocab_kernel(const __grid_constant__ VocabParams p)
     pdl_begin();
     DT_TL_WAITED();
     const Waits wait{p.sink, gave_up};
-    const uint32_t stage_bytes = kABytes + p.bn / CG * 256;
+    const uint32_t a_box = a_box_bytes(MODE == kBack, p.rows_h), stage_bytes = 2 * a_box + p.bn / CG * 256;
     Tile t;
 
     if (warp == kFinishWarps) {
@@ -348,7 +404,7 @@ vocab_kernel(const __grid_constant__ VocabParams p)
                 Loads l = tile_loads<MODE, CG>(p, t, half);
                 for (uint32_t kb = t.kb0; kb < t.kb1; ++kb, ++n) {
                     if (!(ok = wait(empty + 8 * s, round ^ 1))) break;
-                    load_stage<MODE, CG>(p, t, l, half, kb, ring + s * stage_bytes, full + 8 * s);
+                    load_stage<MODE, CG>(p, t, l, half, kb, ring + s * stage_bytes, a_box, full + 8 * s);
                     if (++s == p.stages) s = 0, round ^= 1;
                 }
             }
@@ -371,8 +427,11 @@ vocab_kernel(const __grid_constant__ VocabParams p)
                 const uint32_t desc = mma_desc(kM * CG, p.bn, a_mn, b_mn);
                 // from a K step of 16 to the next: 16 rows of an MN-major box;
                 // 32 bytes of a K-major one, and from its fourth to the next box
-                const uint32_t a_step = a_mn ? 16 * 128 : 32, a_next = a_mn ? 4 * a_step : kBoxBytes;
-                const uint32_t b_step = b_mn ? 16 * 128 : 32, b_next = b_mn ? 4 * b_step : p.bn / CG * 128;
+                const uint32_t a_step = a_mn ? 16 * 128 : 32, a_next = a_mn ? 4 * a_step : a_box;
+                const uint32_t b_step = b_mn ? 16 * 128 : 32, b_next = b_mn ? 4 * b_step : p.rows_w * 128;
+                // K steps of 16 that the last block has
+                const uint32_t inner = MODE != kBack ? p.dim : t.dw ? p.tokens : p.kblocks * kK;
+                const uint32_t last = min((inner - (t.kb1 - 1) * kK + 15) / 16, 8u);
                 const uint32_t acc = tmem + (i & 1) * 256;
                 if (!(ok = wait(acc_empty + 8 * (i & 1), ((i >> 1) & 1) ^ 1))) break;
                 tc_fence_after();
@@ -380,11 +439,13 @@ vocab_kernel(const __grid_constant__ VocabParams p)
                     if (!(ok = wait(full + 8 * s, round))) break;
                     tc_fence_after();
                     const uint32_t at = ring + s * stage_bytes;
-                    const uint64_t a = smem_desc(at, a_mn), b = smem_desc(at + kABytes, b_mn);
+                    const uint64_t a = smem_desc(at, a_mn), b = smem_desc(at + 2 * a_box, b_mn);
+                    const uint32_t steps = kb + 1 == t.kb1 ? last : 8;
 #pragma unroll
                     for (uint32_t k = 0; k < 8; ++k)
-                        mma_bf16<CG>(acc, a + ((k / 4 * a_next + k % 4 * a_step) >> 4),
-                                     b + ((k / 4 * b_next + k % 4 * b_step) >> 4), desc, kb != t.kb0 || k != 0);
+                        if (k < steps) mma_bf16<CG>(acc, a + ((k / 4 * a_next + k % 4 * a_step) >> 4),
+                                                    b + ((k / 4 * b_next + k % 4 * b_step) >> 4), desc,
+                                                    kb != t.kb0 || k != 0);
                     mma_commit<CG>(empty + 8 * s);
                     if (++s == p.stages) s = 0, round ^= 1;
                 }
@@ -484,8 +545,8 @@ vocab_kernel(const __grid_constant__ VocabParams p)
 #pragma unroll
                             for (uint32_t j = 0; j < 16; ++j) w[16 * q + j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
                         }
-                        store_rows_bf16(p, buf, w, p.gbuf + (uint64_t)row0 * p.gpitch + t.n0 + c, p.gpitch, rows, 64,
-                                        true, p.gbuf, (uint64_t)p.tokens * p.gpitch * 2, 0);
+                        store_rows_bf16(p, buf, w, p.gbuf + (uint64_t)row0 * p.gpitch + t.n0 + c, p.gpitch, rows, 64, 8,
+                                         p.gbuf, (uint64_t)p.tokens * p.gpitch * 2, 0);
                     }
                 }
             } else if (!t.dw) {
@@ -503,7 +564,9 @@ vocab_kernel(const __grid_constant__ VocabParams p)
                                        __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3]));
                     __syncwarp();
                     const uint32_t q = lane & 7, e = t.n0 + c + 4 * q;
-                    for (uint32_t k = lane >> 3; k < rows && e < p.dim; k += 4) {
+                    if (e >= p.dim) continue;
+#pragma unroll 4
+                    for (uint32_t k = lane >> 3; k < rows; k += 4) {
                         const uint4 u = *out_chunk(buf, k, q);
                         float4 f = make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z),
                                                __uint_as_float(u.w));
@@ -544,7 +607,7 @@ vocab_kernel(const __grid_constant__ VocabParams p)
                         for (uint32_t j = 0; j < 16; ++j)
                             w[16 * q + j] = pack_bf16x2(v[2 * j] * scale, v[2 * j + 1] * scale);
                     }
-                    store_rows_bf16(p, buf, w, out + c, p.dim, rows, min(p.dim - t.n0 - c, 64u), p.dw_vec, p.dw[t.r],
+                    store_rows_bf16(p, buf, w, out + c, p.dim, rows, min(p.dim - t.n0 - c, 64u), p.dw_align, p.dw[t.r],
                                     (uint64_t)p.rows[t.r] * p.dim * 2, 16 + t.r);
                 }
             }
@@ -565,82 +628,96 @@ vocab_kernel(const __grid_constant__ VocabParams p)
     DT_TL_END_BLOCK(DT_TL_VOCAB);
 }
 
-// Joins the tiles' maxima and sums: thread (t, s) takes every 32nd tile of
-// token t, the 32 are joined in shared memory in ascending order, and block
-// sums of the losses are added by the last block to finish, in block order.
+// Joins the partial maxima and sums of 32 tokens: thread (c, s) takes every
+// 32nd of token c (loads of 32 tokens are whole lines), then warp c joins
+// token c's 32 in a tree.  The block's sum of losses goes to memory, and the
+// last block to finish adds the blocks' in block order.
 constexpr int kTokens = 32, kSlices = 32;
 
 __global__ void __launch_bounds__(kTokens *kSlices) vocab_finish_kernel(const __grid_constant__ VocabFinish p)
 {
-    __shared__ float2 part[kSlices][kTokens];
+    __shared__ float2 part[kSlices][kTokens + 1];
+    __shared__ float loss_of[kTokens];
+    __shared__ uint32_t keeps[kTokens];
     __shared__ bool last;
     DT_TL_BEGIN();
     pdl_begin();
     DT_TL_WAITED();
-    const uint32_t c = threadIdx.x % kTokens, s = threadIdx.x / kTokens;
-    const uint32_t t = blockIdx.x * kTokens + c;
-    // joins (m, x) into (top, sum), both relative to their own maximum
-    auto join = [](float &top, float &sum, float m, float x) {
-        const float most = fmaxf(top, m);
-        if (most == -INFINITY) {
-            // nothing but minus infinities so far (a unit's padding): no mass, but
-            // a NaN in a sum must stay
-            sum += x;
-        } else {
-            sum = sum * exp2_fast((top - most) * kLog2e) + x * exp2_fast((m - most) * kLog2e);
+    const uint32_t lane = threadIdx.x % kTokens, warp = threadIdx.x / kTokens;
+    // (m, x) and (top, sum), both relative to their own maximum, into one.  No
+    // mass is left of minus infinities, but a NaN in a sum stays.
+    auto scaled = [](float m, float x, float most) { return x * (m == -INFINITY ? 0.0f : exp2_fast((m - most) * kLog2e)); };
+    float top = -INFINITY, sum = 0.0f;
+    const uint32_t column = blockIdx.x * kTokens + lane;
+    if (column < p.tokens) {
+#pragma unroll 4
+        for (uint32_t k = warp; k < p.tiles; k += kSlices) {
+            const float2 v = p.part[(uint64_t)k * p.tokens + column];
+            const float most = fmaxf(top, v.x);
+            sum = scaled(top, sum, most) + scaled(v.x, v.y, most);
             top = most;
         }
-    };
-    float top = -INFINITY, sum = 0.0f;
-    if (t < p.tokens)
-        for (uint32_t k = s; k < p.tiles; k += kSlices) {
-            const float2 v = p.part[(uint64_t)k * p.tokens + t];
-            join(top, sum, v.x, v.y);
-        }
-    part[s][c] = make_float2(top, sum);
+    }
+    part[warp][lane] = make_float2(top, sum);
     __syncthreads();
-    if (s == 0) {
-        for (int k = 1; k < kSlices; ++k) join(top, sum, part[k][c].x, part[k][c].y);
+    const float2 v = part[lane][warp];
+    float most = v.x;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+    sum = scaled(v.x, v.y, most);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    const uint32_t t = blockIdx.x * kTokens + warp;
+    if (lane == 0) {
         float loss = 0.0f;
         uint32_t kept = 0;
         if (t < p.tokens) {
-            const float lse = top + logf(sum);
-            const int32_t v = p.targets[t];
-            if (v != p.ignore) {
-                if (v >= 0 && (uint32_t)v < p.vocab) {
+            const float lse = most + logf(sum);
+            const int32_t target = p.targets[t];
+            if (target != p.ignore) {
+                if (target >= 0 && (uint32_t)target < p.vocab) {
                     loss = lse - p.logit[t];
                     kept = 1;
                 } else {
-                    record_error(p.sink, DT_ERR_INVALID, -1, (int)t, v);
+                    record_error(p.sink, DT_ERR_INVALID, -1, (int)t, target);
                 }
             }
             if (p.lse) p.lse[t] = lse;
             if (p.losses) p.losses[t] = loss;
         }
-        double all = loss;
-        for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
-        kept = __reduce_add_sync(0xFFFFFFFFu, kept);
-        if (c == 0) {
-            p.block_sum[blockIdx.x] = all;
-            p.block_kept[blockIdx.x] = kept;
-            __threadfence();
-            last = atomicAdd(p.ticket, 1u) == gridDim.x - 1;
-        }
+        loss_of[warp] = loss;
+        keeps[warp] = kept;
     }
     __syncthreads();
-    if (last && s == 0) {
-        __threadfence();
-        double all = 0.0;
-        uint64_t kept = 0;
-        for (uint32_t b = c; b < gridDim.x; b += kTokens) {
-            all += __ldcg(p.block_sum + b);
-            kept += __ldcg(p.block_kept + b);
+    if (warp == 0 && p.loss) {
+        double all = loss_of[lane];
+        for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
+        uint64_t kept = __reduce_add_sync(0xFFFFFFFFu, keeps[lane]);
+        bool end = true;
+        if (gridDim.x > 1) {
+            if (lane == 0) {
+                p.block_sum[blockIdx.x] = all;
+                p.block_kept[blockIdx.x] = (uint32_t)kept;
+                __threadfence();
+                last = atomicAdd(p.ticket, 1u) == gridDim.x - 1;
+            }
+            __syncwarp();
+            end = last;
+            if (end) {
+                __threadfence();
+                all = 0.0;
+                kept = 0;
+                for (uint32_t b = lane; b < gridDim.x; b += 32) {
+                    all += __ldcg(p.block_sum + b);
+                    kept += __ldcg(p.block_kept + b);
+                }
+                for (int o = 16; o > 0; o >>= 1) {
+                    all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
+                    kept += __shfl_xor_sync(0xFFFFFFFFu, kept, o);
+                }
+            }
         }
-        for (int o = 16; o > 0; o >>= 1) {
-            all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
-            kept += __shfl_xor_sync(0xFFFFFFFFu, kept, o);
-        }
-        if (c == 0 && p.loss) *p.loss = kept == 0 ? 0.0f : (float)(p.avg ? all / (double)kept : all);
+        if (end && lane == 0) *p.loss = kept == 0 ? 0.0f : (float)(p.avg ? all / (double)kept : all);
     }
     DT_TL_END_BLOCK(DT_TL_VOCAB);
 }
@@ -657,7 +734,7 @@ __global__ void __launch_bounds__(kThreads) vocab_join_kernel(const __grid_const
     for (uint64_t i = (uint64_t)blockIdx.x * kThreads + threadIdx.x; i < all; i += step) {
         const uint32_t row = (uint32_t)(i / quads), e = (uint32_t)(i % quads) * 4;
         float4 f = make_float4(0, 0, 0, 0);
-#pragma unroll 4
+#pragma unroll 8
         for (uint32_t k = 0; k < p.splits; ++k) {
             const float4 o = *reinterpret_cast<const float4 *>(p.acc + ((uint64_t)k * p.tokens + row) * p.apitch + e);
             f.x += o.x, f.y += o.y, f.z += o.z, f.w += o.w;
@@ -716,7 +793,7 @@ cudaError_t launch_mode(VocabParams &p, int device, cudaStream_t s)
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit, std::memory_order_release);
     }
-    p.stages = std::min(kMaxStages, kRingBytes / (kABytes + p.bn / CG * 256));
+    p.stages = std::min(kMaxStages, kRingBytes / (2 * a_box_bytes(MODE == kBack, p.rows_h) + p.bn / CG * 256));
     return launch_kernel(vocab_kernel<MODE, CG>, dim3(std::min(p.workers, vocab_workers(CG == 2, device)) * CG),
                          dim3(kTcThreads), kTcSmem, s, false, p);
 }

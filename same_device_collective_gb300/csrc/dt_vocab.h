@@ -39,7 +39,10 @@ struct VocabParams {
     uint32_t dh_rest, dw_early;        // the order of both (next_tile)
     uint32_t gpitch, apitch;
     uint32_t acc_in, final;            // dh: add to the sums so far; store the result
-    uint32_t dh_vec, dw_vec;           // rows start on 8- and 16-byte boundaries
+    uint32_t rows_h, rows_g, rows_w;   // of the maps' boxes
+    uint32_t w_maps;                   // bit r: w[r] is a map
+    uint32_t dh_vec;                   // rows of dh start on 8-byte boundaries
+    uint32_t dw_align;                 // elements that rows of every dw are a multiple of, address and width: 1, 2, 4, 8
     int32_t ignore;
     int32_t avg;
     const int32_t *targets;
