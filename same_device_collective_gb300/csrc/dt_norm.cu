@@ -8,17 +8,28 @@
 //
 // The ranks' rows are one list, so that a call is one launch (two for the
 // backward pass) whatever the number of ranks.  Both directions are bound by
-// HBM: about 4 and 5 flops per byte.  A row is read once: its elements stay
-// in the registers of the `tpr` threads that share it, the variance is the
-// mean of the squared distances from the mean (a second pass over registers,
-// not E[x^2] - mu^2, which loses every digit where |mu| is large), and all
-// sums are fp32.  Results are rounded once, at the store.
+// HBM (about 4 and 5 flops per byte), and close behind by the instructions an
+// SM can issue, so a row crosses few threads: sums cost shuffles and barriers
+// per warp that shares a row, not per element.  A row is read once, by a bulk
+// copy into shared memory; every group of threads that shares rows has a ring
+// of stages of its own, so that 100 to 200 KB an SM are always under way, which
+// registers alone cannot hold.  A stage is one row, or as many short ones as
+// make 4 KB; rows of any alignment are copied with the 16-byte blocks that
+// their ends lie in, and then read element by element.
 //
-// Blocks stay resident and walk over the rows; each loads its next row before
-// it works on the present one, so that loads are always in flight.  The
-// backward pass keeps its share of dw and db in registers over all of its
-// rows and writes it once; a second kernel adds the shares in a fixed order,
-// so the result depends on the device and the shapes alone, not on timing.
+// The variance is the mean of the squared distances from the mean, not
+// E[x^2] - mu^2, which loses every digit where |mu| is large.  All sums are
+// fp32, and results are rounded once, at the store.
+//
+// Forward, a row is one warp's (of 4 x 2048 rows of 4096 bf16: 00 us, against
+// 94 us with 256 threads to a row and 44 with one row ahead in registers and no
+// ring), and several warps' where there are few rows or long ones.  Backward, a
+// thread keeps its columns' shares of dw and db in registers over all of its
+// rows, eight columns where it can, and up to four rows are summed at a time; a second
+// kernel adds the shares in a fixed order, so the result depends on the device
+// and the shapes alone, not on timing.
+#include <algorithm>
+
 #include "dt_ops.h"
 
 #include "dt_bounds.cuh"
@@ -29,56 +40,125 @@
 namespace dt {
 namespace {
 
-constexpr int kNormThreads = 512;    // most threads of a block, and of a row
+constexpr int kRowThreads = 512;     // most threads of a row
+constexpr int kForwardThreads = 768; // most threads of a block, forward: 85 registers a thread
+constexpr int kNormThreads = 512;    // and backward: 128, for the sums of dw and db
+constexpr uint32_t kSmemBytes = 208 * 1024;    // of the SM's 227 KB: weights and rings
+constexpr uint32_t kMaxStages = 8;
+constexpr uint32_t kStageTarget = 4096;
+constexpr uint32_t kMostParams = 64 * 1024;    // longer weights and biases, as floats, stay in global memory
 constexpr int kLongThreads = 512;    // rows too long for registers
 constexpr int kLongSlices = 32;      // row slices of the column sums there
 constexpr int kJoinCols = 32;        // columns and row slices of a block that adds the shares
 constexpr int kJoinSlices = 16;
 
-// VEC elements as they lie in memory: one 16-byte vector, or one element.
-template <typename T, int VEC>
-struct Chunk {
-    static_assert(VEC * sizeof(T) == 16, "a vector is 16 bytes");
-    uint4 v;
-    __device__ __forceinline__ void load(const T *p) { v = *reinterpret_cast<const uint4 *>(p); }
-    __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ void get(float (&f)[VEC]) const
-    {
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if constexpr (VEC == 8) {
-                f[2 * i] = bf16_lo(w[i]);
-                f[2 * i + 1] = bf16_hi(w[i]);
-            } else {
-                f[i] = __uint_as_float(w[i]);
-            }
-        }
-    }
-    static __device__ __forceinline__ void store(T *p, const float (&f)[VEC])
-    {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if constexpr (VEC == 8) w[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
-            else w[i] = __float_as_uint(f[i]);
-        }
-        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
+// Two fp32 values in a pair of registers, for the instructions that work on
+// both at once: the kernels are nearly bound by issue, and these halve the
+// arithmetic's share of it.  The same functions on one float serve rows that
+// are read element by element.
+struct F2 {
+    uint64_t v;
 };
+__device__ __forceinline__ F2 pair(float a, float b)
+{
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void split(F2 x, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x.v)); }
+__device__ __forceinline__ F2 add(F2 a, F2 b)
+{
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 mul(F2 a, F2 b)
+{
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c)
+{
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ float both(F2 x)
+{
+    float a, b;
+    split(x, a, b);
+    return a + b;
+}
+__device__ __forceinline__ float add(float a, float b) { return a + b; }
+__device__ __forceinline__ float mul(float a, float b) { return a * b; }
+__device__ __forceinline__ float fma(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float both(float x) { return x; }
 
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(uint16_t x) { return bf16_to_f32(x); }
 __device__ __forceinline__ void from_f32(float f, float *p) { *p = f; }
 __device__ __forceinline__ void from_f32(float f, uint16_t *p) { *p = f32_to_bf16(f); }
 
+// VEC elements as they lie in memory: one 16-byte vector, or one element; in
+// registers K values of V, pairs of floats or one float.
+template <typename T, int VEC>
+struct Chunk {
+    static_assert(VEC * sizeof(T) == 16, "a vector is 16 bytes");
+    using V = F2;
+    static constexpr int K = VEC / 2;
+    uint4 v;
+    __device__ __forceinline__ void load(const T *p) { v = *reinterpret_cast<const uint4 *>(p); }
+    __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void get(V (&f)[K]) const
+    {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+            if constexpr (VEC == 8) f[i] = pair(bf16_lo(w[i]), bf16_hi(w[i]));
+            else f[i] = pair(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+        }
+    }
+    static __device__ __forceinline__ void store(T *p, const V (&f)[K])
+    {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+            float a, b;
+            split(f[i], a, b);
+            if constexpr (VEC == 8) {
+                w[i] = pack_bf16x2(a, b);
+            } else {
+                w[2 * i] = __float_as_uint(a);
+                w[2 * i + 1] = __float_as_uint(b);
+            }
+        }
+        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    // the same elements of f32 values, from a 16-byte boundary on
+    static __device__ __forceinline__ void floats(const float *p, V (&f)[K])
+    {
+#pragma unroll
+        for (int i = 0; i < K; i += 2) {
+            const ulonglong2 u = *reinterpret_cast<const ulonglong2 *>(p + 2 * i);
+            f[i].v = u.x;
+            f[i + 1].v = u.y;
+        }
+    }
+    static __device__ __forceinline__ V all(float x) { return pair(x, x); }
+};
+
 template <typename T>
 struct Chunk<T, 1> {
+    using V = float;
+    static constexpr int K = 1;
     T v;
     __device__ __forceinline__ void load(const T *p) { v = *p; }
     __device__ __forceinline__ void zero() { v = 0; }
-    __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = to_f32(v); }
-    static __device__ __forceinline__ void store(T *p, const float (&f)[1]) { from_f32(f[0], p); }
+    __device__ __forceinline__ void get(V (&f)[1]) const { f[0] = to_f32(v); }
+    static __device__ __forceinline__ void store(T *p, const V (&f)[1]) { from_f32(f[0], p); }
+    static __device__ __forceinline__ void floats(const float *p, V (&f)[1]) { f[0] = *p; }
+    static __device__ __forceinline__ V all(float x) { return x; }
 };
 
 // Element j of the weight or bias, `none` where there is none.
@@ -86,6 +166,18 @@ __device__ __forceinline__ float param(const void *p, int bf16, uint32_t j, floa
 {
     if (!p) return none;
     return bf16 ? bf16_to_f32(static_cast<const uint16_t *>(p)[j]) : static_cast<const float *>(p)[j];
+}
+
+// A thread's weights or biases from element e on.
+template <typename C, int VEC>
+__device__ __forceinline__ void params(const void *p, int bf16, uint32_t e, float none, typename C::V (&f)[C::K])
+{
+    if constexpr (VEC == 1) {
+        f[0] = param(p, bf16, e, none);
+    } else {
+#pragma unroll
+        for (int i = 0; i < C::K; ++i) f[i] = pair(param(p, bf16, e + 2 * i, none), param(p, bf16, e + 2 * i + 1, none));
+    }
 }
 
 // The rank that row belongs to, and the row's number there.
@@ -115,229 +207,506 @@ __device__ __forceinline__ bool in_rank(const NormParams &p, const void *const *
 #define NORM_OK(base, kind, r, a, n, row_bytes) true
 #endif
 
-// Sums of K values over the tpr threads of a row; every thread gets the same
-// sums, in the same order of addition.  `red` is double-buffered by the
-// caller's `phase`: a buffer is written again only after the barrier of the
-// sum in between, which every reader of it has passed.
-template <int K>
-__device__ __forceinline__ void row_sum(float (&v)[K], float (*red)[32][2], uint32_t &phase, uint32_t tpr,
-                                        uint32_t group)
+// Values of each warp of a row to all of its threads: `red` is
+// double-buffered by the caller's `phase`, and a buffer is written again only
+// after the barrier of the exchange in between, which every reader of it has
+// passed.  The result is the row's first entry.
+using Exchange = float4[2][kForwardThreads / 32];
+__device__ __forceinline__ const float4 *exchange(float4 v, Exchange &red, uint32_t &phase, uint32_t tpr, uint32_t group)
 {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-        for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], o);
-    if (tpr == 32) return;
-    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uint32_t first = group * (tpr >> 5), warps = tpr >> 5;
-    if (lane == 0)
-#pragma unroll
-        for (int k = 0; k < K; ++k) red[phase][warp][k] = v[k];
+    if ((threadIdx.x & 31) == 0) red[phase][threadIdx.x >> 5] = v;
     asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(tpr) : "memory");
-#pragma unroll
-    for (int k = 0; k < K; ++k) v[k] = lane < warps ? red[phase][first + lane][k] : 0.0f;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-        for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], o);
+    const float4 *first = &red[phase][group * (tpr >> 5)];
     phase ^= 1;
+    return first;
 }
 
-// A row in registers: chunk c of thread t is elements [(c * tpr + t) * VEC,
-// + VEC).
-template <typename T, int VEC, int N>
-__device__ __forceinline__ void load_row(Chunk<T, VEC> (&c)[N], const NormParams &p, const void *const *base,
-                                         int kind, uint64_t row, uint32_t t)
+template <int K>
+__device__ __forceinline__ void warp_sum(float (&v)[K])
 {
-    uint64_t local;
-    const int r = find_rank(p, row, local);
-    const T *src = static_cast<const T *>(base[r]) + local * p.cols;
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-        const uint32_t e = (n * p.tpr + t) * VEC;
-        if (e < p.cols && NORM_OK(base, kind, r, src + e, VEC * sizeof(T), p.cols * sizeof(T))) c[n].load(src + e);
-        else c[n].zero();
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], o);
+}
+
+// Sums of V values (2, 4 or 8) over the tpr threads that share a row; every
+// thread gets the same sums, added in the same order.  Within a warp each step
+// halves the values a lane still carries as well as the lanes that share one:
+// 9 shuffles for 8 values, where one value after the other takes 40.  `red` is
+// double-buffered like exchange()'s.
+template <int V>
+__device__ __forceinline__ void row_sum(float (&v)[V], float (*red)[V][kNormThreads / 32], uint32_t &phase, uint32_t tpr,
+                                        uint32_t group)
+{
+    constexpr uint32_t kLanes = 32 / V;   // lanes that hold the same value in the end
+    const uint32_t lane = threadIdx.x & 31;
+#pragma unroll
+    for (int have = V, o = 16; o > 0; o >>= 1) {
+        if (have > 1) {
+            have /= 2;
+            const bool up = lane & o;
+#pragma unroll
+            for (int i = 0; i < have; ++i) {
+                const float send = up ? v[i] : v[i + have], keep = up ? v[i + have] : v[i];
+                v[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, send, o);
+            }
+        } else {
+            v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], o);
+        }
+    }
+    float sum = v[0];                     // of value lane / kLanes
+    if (tpr > 32) {
+        const uint32_t warps = tpr >> 5, j = lane % kLanes;
+        if (j == 0) red[phase][lane / kLanes][threadIdx.x >> 5] = sum;
+        asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(tpr) : "memory");
+        const float *of = &red[phase][lane / kLanes][group * warps];
+        sum = 0.0f;
+#pragma unroll
+        for (uint32_t k = 0; k < kNormThreads / 32; k += kLanes)
+            if (k + j < warps) sum += of[k + j];
+#pragma unroll
+        for (uint32_t o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        phase ^= 1;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = __shfl_sync(0xFFFFFFFFu, sum, i * kLanes);
+}
+
+// A group's walk over the rows: chunk c of the call is up to p.chunk_rows rows
+// of one rank; group number `part` has chunks part, part + parts, ...  Its
+// first thread starts the copies; the rest is the same in all of its threads.
+// Dynamic shared memory holds the weights, the groups' rings and their barriers.
+template <typename T, int ARRAYS>
+struct Ring {
+    const NormParams &p;
+    uint32_t base, bars;             // the group's stages and their barriers in shared memory
+    unsigned char *mem;
+    uint32_t s = 0, parity = 0;
+    bool late = false;               // a wait ran out: wait no more, and keep to the barriers
+
+    // The rows of chunk c: rank, first row there, how many.
+    __device__ __forceinline__ void chunk(uint64_t c, int &r, uint64_t &row, uint32_t &n) const
+    {
+        uint64_t begin = 0, rows = 0;
+        r = 0;
+        while (r + 1 < p.P && c >= p.chunk_end[r]) begin = p.chunk_end[r++];
+        row = (c - begin) * p.chunk_rows;
+        rows = p.row_end[r] - (r ? p.row_end[r - 1] : 0);
+        n = rows - row < p.chunk_rows ? (uint32_t)(rows - row) : p.chunk_rows;
+    }
+    // The 16-byte blocks that hold rows [row, row + n) of one buffer.
+    __device__ __forceinline__ void copy(const void *base_ptr, int kind, int r, uint64_t row, uint32_t n, uint32_t dst,
+                                         uint32_t bar, uint32_t &bytes) const
+    {
+        (void)kind, (void)r;
+        const uint64_t lo = reinterpret_cast<uint64_t>(base_ptr) + row * p.cols * sizeof(T);
+        const uint64_t hi = lo + (uint64_t)n * p.cols * sizeof(T);
+        const uint64_t from = lo & ~15ull, to = (hi + 15) & ~15ull;
+        bytes = (uint32_t)(to - from);
+        if (!NORM_OK(kind ? p.dy : p.x, kind, r, reinterpret_cast<const void *>(lo), hi - lo, p.cols * sizeof(T))) bytes = 0;
+        if (bytes) bulk_load(dst, reinterpret_cast<const void *>(from), bytes, bar);
+    }
+    __device__ __forceinline__ void load(uint64_t c, uint32_t stage) const
+    {
+        int r;
+        uint64_t row;
+        uint32_t n, bytes[2] = {0, 0};
+        chunk(c, r, row, n);
+        const uint32_t bar = bars + 8 * stage, dst = base + stage * p.stage_bytes * ARRAYS;
+        copy(p.x[r], 0, r, row, n, dst, bar, bytes[0]);
+        if constexpr (ARRAYS == 2) copy(p.dy[r], 1, r, row, n, dst + p.stage_bytes, bar, bytes[1]);
+        mbar_expect_tx(bar, bytes[0] + bytes[1]);
+    }
+    __device__ __forceinline__ void wait()
+    {
+        const uint32_t bar = bars + 8 * s;
+        for (int k = 0; k < 64 && !late; ++k)
+            if (mbar_try_wait(bar, parity)) return;
+        if (late || mbar_wait_bounded(bar, parity, p.sink.timeout_ns)) return;
+        late = true;
+        record_error(p.sink, DT_ERR_TIMEOUT, -1, blockIdx.x, 0);
+    }
+    // Array a's first row in the present stage, where `src` is its address in memory.
+    __device__ __forceinline__ const T *row0(int a, const T *src) const
+    {
+        return reinterpret_cast<const T *>(mem + (s * ARRAYS + a) * p.stage_bytes + (reinterpret_cast<uint64_t>(src) & 15));
+    }
+    __device__ __forceinline__ void next()
+    {
+        if (++s == p.stages) s = 0, parity ^= 1;
+    }
+};
+
+// The start of both kernels: the group's ring, with its first copies under way.
+template <typename T, int ARRAYS>
+__device__ __forceinline__ Ring<T, ARRAYS> start_ring(const NormParams &p, unsigned char *smem, uint32_t group, uint32_t t,
+                                                      uint64_t part)
+{
+    const uint32_t groups = blockDim.x / p.tpr, mine = p.stages * p.stage_bytes * ARRAYS;
+    smem += p.param_bytes;
+    const uint32_t bars = smem_addr(smem) + groups * mine;
+    if (threadIdx.x == 0) {
+        for (uint32_t k = 0; k < groups * p.stages; ++k) mbar_init(bars + 8 * k, 1);
+        mbar_init_fence();
+    }
+    __syncthreads();
+    unsigned char *mem = smem + (size_t)group * mine;
+    Ring<T, ARRAYS> ring{p, smem_addr(mem), bars + 8 * group * p.stages, mem};
+    pdl_begin();
+    if (t == 0)
+        for (uint32_t k = 0; k < p.stages; ++k) {
+            const uint64_t c = part + (uint64_t)k * p.parts;
+            if (c < p.chunks) ring.load(c, k);
+        }
+    return ring;
+}
+
+// The mean and the sum of squared distances from it, of all warps that share a
+// row from each one's own: M2 = sum of M2_w + n_w (mean_w - mean)^2.
+__device__ __forceinline__ void row_moments(float sum, float &mean, float &m2, uint32_t mine, uint32_t cols,
+                                            Exchange &red, uint32_t &phase, uint32_t tpr, uint32_t group)
+{
+    if (tpr == 32) return;
+    const float4 *of = exchange(make_float4(sum, m2, mean, (float)mine), red, phase, tpr, group);
+    float all = 0.0f;
+    for (uint32_t q = 0; q < tpr >> 5; ++q) all += of[q].x;
+    mean = __fdiv_rn(all, (float)cols);
+    m2 = 0.0f;
+    for (uint32_t q = 0; q < tpr >> 5; ++q) {
+        const float4 v = of[q];
+        m2 += fmaf(v.w * (v.z - mean), v.z - mean, v.y);
     }
 }
 
-template <typename T, int VEC, int N>
-__global__ void __launch_bounds__(kNormThreads) norm_kernel(const __grid_constant__ NormParams p)
+__device__ __forceinline__ float rstd_of(float m2, uint32_t cols, float eps)
 {
-    // weights of up to 16 elements a thread stay in registers over all rows;
-    // wider rows read them again from L1
-    constexpr bool kHold = N * VEC <= 16;
-    __shared__ float red[2][32][2];
+    return __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(m2, (float)cols) + eps));
+}
+
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kForwardThreads, 1) norm_kernel(const __grid_constant__ NormParams p)
+{
+    using C = Chunk<T, VEC>;
+    using V = typename C::V;
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ Exchange red;
     DT_TL_BEGIN();
-    pdl_begin();
+    const uint32_t tpr = p.tpr, group = threadIdx.x / tpr, t = threadIdx.x % tpr, cols = p.cols;
+    const uint64_t part = (uint64_t)group * gridDim.x + blockIdx.x;
+    Ring<T, 1> ring = start_ring<T, 1>(p, smem, group, t, part);
     DT_TL_WAITED();
-    const uint32_t tpr = p.tpr, groups = blockDim.x / tpr, group = threadIdx.x / tpr, t = threadIdx.x % tpr;
-    const uint64_t step = (uint64_t)gridDim.x * groups;
-    uint64_t row = (uint64_t)blockIdx.x * groups + group;
+    // as floats, so that no row spends instructions on widening them
+    float *weight = reinterpret_cast<float *>(smem), *bias = reinterpret_cast<float *>(smem + p.param_bytes / 2);
+    if (p.param_bytes) {
+#pragma unroll 4
+        for (uint32_t e = threadIdx.x; e < cols; e += blockDim.x) {
+            weight[e] = param(p.weight, p.weight_bf16, e, 1.0f);
+            bias[e] = param(p.bias, p.weight_bf16, e, 0.0f);
+        }
+        __syncthreads();
+    }
+    // this thread's elements of a row are [e0, + VEC), and every `step` on; the
+    // warp's number of them
+    const uint32_t e0 = t * VEC, step = tpr * VEC;
+    uint32_t mine = 0;
+    for (uint32_t e = e0 - (t & 31) * VEC; e < cols; e += step) mine += min(cols - e, 32u * VEC);
+    const float inv_mine = mine ? __fdiv_rn(1.0f, (float)mine) : 0.0f;
     uint32_t phase = 0;
-    Chunk<T, VEC> next[N];
-    if (row < p.rows) load_row<T, VEC, N>(next, p, p.x, 0, row, t);
 
-    float w[kHold ? N * VEC : 1], b[kHold ? N * VEC : 1];
-    if constexpr (kHold)
+    for (uint64_t c = part; c < p.chunks; c += p.parts) {
+        int r;
+        uint64_t row;
+        uint32_t rows;
+        ring.chunk(c, r, row, rows);
+        const T *src = ring.row0(0, static_cast<const T *>(p.x[r]) + row * cols);
+        T *y = static_cast<T *>(p.out[r]) + row * cols;
+        ring.wait();
+        for (uint32_t k = 0; k < rows; ++k, ++row, src += cols, y += cols) {
+            // the warp's mean and the squared distances from it; two sums, so
+            // that an addition does not wait for the one before
+            V s[2] = {C::all(0.0f), C::all(0.0f)}, m[2] = {C::all(0.0f), C::all(0.0f)};
+#pragma unroll 4
+            for (uint32_t e = e0; e < cols; e += step) {
+                C x;
+                x.load(src + e);
+                V f[C::K];
+                x.get(f);
 #pragma unroll
-        for (int n = 0; n < N; ++n)
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const uint32_t e = (n * tpr + t) * VEC + i;
-                w[n * VEC + i] = e < p.cols ? param(p.weight, p.weight_bf16, e, 1.0f) : 0.0f;
-                b[n * VEC + i] = e < p.cols ? param(p.bias, p.weight_bf16, e, 0.0f) : 0.0f;
+                for (int i = 0; i < C::K; ++i) s[i & 1] = add(s[i & 1], f[i]);
             }
-
-    for (; row < p.rows; row += step) {
-        Chunk<T, VEC> x[N];
+            float sum[1] = {both(add(s[0], s[1]))};
+            warp_sum<1>(sum);
+            float mean = sum[0] * inv_mine;
+            const V minus_warp = C::all(-mean);
+#pragma unroll 4
+            for (uint32_t e = e0; e < cols; e += step) {
+                C x;
+                x.load(src + e);
+                V f[C::K];
+                x.get(f);
 #pragma unroll
-        for (int n = 0; n < N; ++n) x[n] = next[n];
-        if (row + step < p.rows) load_row<T, VEC, N>(next, p, p.x, 0, row + step, t);
-
-        float s[1] = {0.0f};
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-            float f[VEC];
-            x[n].get(f);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) s[0] += f[i];
-        }
-        row_sum<1>(s, red, phase, tpr, group);
-        const float mean = __fdiv_rn(s[0], (float)p.cols);
-        float m2[1] = {0.0f};
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-            if ((n * tpr + t) * VEC >= p.cols) continue;
-            float f[VEC];
-            x[n].get(f);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) m2[0] = fmaf(f[i] - mean, f[i] - mean, m2[0]);
-        }
-        row_sum<1>(m2, red, phase, tpr, group);
-        const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(m2[0], (float)p.cols) + p.eps));
-
-        uint64_t local;
-        const int r = find_rank(p, row, local);
-        T *y = static_cast<T *>(p.out[r]) + local * p.cols;
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-            const uint32_t e = (n * tpr + t) * VEC;
-            if (e >= p.cols) continue;
-            float f[VEC];
-            x[n].get(f);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const float wi = kHold ? w[kHold ? n * VEC + i : 0] : param(p.weight, p.weight_bf16, e + i, 1.0f);
-                const float bi = kHold ? b[kHold ? n * VEC + i : 0] : param(p.bias, p.weight_bf16, e + i, 0.0f);
-                f[i] = fmaf((f[i] - mean) * rstd, wi, bi);
+                for (int i = 0; i < C::K; ++i) {
+                    f[i] = add(f[i], minus_warp);
+                    m[i & 1] = fma(f[i], f[i], m[i & 1]);
+                }
             }
-            if (NORM_OK(p.out, 2, r, y + e, VEC * sizeof(T), p.cols * sizeof(T))) Chunk<T, VEC>::store(y + e, f);
+            float m2[1] = {both(add(m[0], m[1]))};
+            warp_sum<1>(m2);
+            row_moments(sum[0], mean, m2[0], mine, cols, red, phase, tpr, group);
+            const float rstd = rstd_of(m2[0], cols, p.eps);
+            const V minus = C::all(-mean), scale = C::all(rstd);
+#pragma unroll 4
+            for (uint32_t e = e0; e < cols; e += step) {
+                C x;
+                x.load(src + e);
+                V f[C::K], w[C::K], b[C::K];
+                x.get(f);
+                if (p.param_bytes) {
+                    C::floats(weight + e, w);
+                    C::floats(bias + e, b);
+                } else {
+                    params<C, VEC>(p.weight, p.weight_bf16, e, 1.0f, w);
+                    params<C, VEC>(p.bias, p.weight_bf16, e, 0.0f, b);
+                }
+#pragma unroll
+                for (int i = 0; i < C::K; ++i) f[i] = fma(mul(add(f[i], minus), scale), w[i], b[i]);
+                if (NORM_OK(p.out, 2, r, y + e, VEC * sizeof(T), cols * sizeof(T))) C::store(y + e, f);
+            }
+            if (t == 0) {
+                if (p.mean[r] && NORM_OK(p.mean, 3, r, p.mean[r] + row, 4, 4)) p.mean[r][row] = mean;
+                if (p.rstd[r] && NORM_OK(p.rstd, 4, r, p.rstd[r] + row, 4, 4)) p.rstd[r][row] = rstd;
+            }
         }
-        if (t == 0) {
-            if (p.mean[r] && NORM_OK(p.mean, 3, r, p.mean[r] + local, 4, 4)) p.mean[r][local] = mean;
-            if (p.rstd[r] && NORM_OK(p.rstd, 4, r, p.rstd[r] + local, 4, 4)) p.rstd[r][local] = rstd;
-        }
+        // the stage is free once every thread of the group has read it
+        if (tpr > 32) asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(tpr) : "memory");
+        else __syncwarp();
+        if (t == 0 && c + (uint64_t)p.stages * p.parts < p.chunks) ring.load(c + (uint64_t)p.stages * p.parts, ring.s);
+        ring.next();
     }
     DT_TL_END_BLOCK(DT_TL_NORM);
 }
 
+// One row to a block, for calls of few rows, where only the time from the
+// first load to the last store counts: the row, the weights and the bias are
+// all loaded to registers at once (1 row on each of 4 ranks, 4096 bf16: 0.0 us
+// a call, against 5.3 through a ring and shared memory).
 template <typename T, int VEC, int N>
-__global__ void __launch_bounds__(kNormThreads) norm_backward_kernel(const __grid_constant__ NormParams p)
+__global__ void __launch_bounds__(kRowThreads) norm_few_kernel(const __grid_constant__ NormParams p)
 {
-    constexpr bool kAhead = N * VEC * sizeof(T) <= 32;   // the next row's registers fit beside the sums
-    constexpr bool kHold = N * VEC <= 16;
-    __shared__ float red[2][32][2];
+    using C = Chunk<T, VEC>;
+    using V = typename C::V;
+    __shared__ Exchange red;
     DT_TL_BEGIN();
     pdl_begin();
     DT_TL_WAITED();
-    const uint32_t tpr = p.tpr, groups = blockDim.x / tpr, group = threadIdx.x / tpr, t = threadIdx.x % tpr;
-    const uint64_t step = (uint64_t)gridDim.x * groups;
-    const uint64_t part = (uint64_t)blockIdx.x * groups + group;
-    uint64_t row = part;
-    uint32_t phase = 0;
-    Chunk<T, VEC> xn[N], gn[N];
-    if (kAhead && row < p.rows) {
-        load_row<T, VEC, N>(xn, p, p.x, 0, row, t);
-        load_row<T, VEC, N>(gn, p, p.dy, 1, row, t);
+    const uint32_t tpr = blockDim.x, t = threadIdx.x, cols = p.cols;
+    uint64_t row;
+    const int r = find_rank(p, blockIdx.x, row);
+    const T *src = static_cast<const T *>(p.x[r]) + row * cols;
+    T *y = static_cast<T *>(p.out[r]) + row * cols;
+    V f[N][C::K], w[N][C::K], b[N][C::K];
+    C x[N];
+    uint32_t mine = 0, phase = 0;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const uint32_t first = (n * tpr + (t & ~31u)) * VEC, e = (n * tpr + t) * VEC;
+        mine += first < cols ? min(cols - first, 32u * VEC) : 0;
+        if (e < cols && NORM_OK(p.x, 0, r, src + e, VEC * sizeof(T), cols * sizeof(T))) x[n].load(src + e);
+        else x[n].zero();
     }
-    float dw[N * VEC], db[N * VEC], w[kHold ? N * VEC : 1];
 #pragma unroll
-    for (int n = 0; n < N; ++n)
+    for (int n = 0; n < N; ++n) {
+        const uint32_t e = (n * tpr + t) * VEC;
+        if (e >= cols) continue;
+        params<C, VEC>(p.weight, p.weight_bf16, e, 1.0f, w[n]);
+        params<C, VEC>(p.bias, p.weight_bf16, e, 0.0f, b[n]);
+    }
+    V s = C::all(0.0f), m = C::all(0.0f);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            const uint32_t e = (n * tpr + t) * VEC + i;
-            dw[n * VEC + i] = db[n * VEC + i] = 0.0f;
-            if constexpr (kHold) w[n * VEC + i] = e < p.cols ? param(p.weight, p.weight_bf16, e, 1.0f) : 0.0f;
+    for (int n = 0; n < N; ++n) {
+        x[n].get(f[n]);
+#pragma unroll
+        for (int i = 0; i < C::K; ++i) s = add(s, f[n][i]);
+    }
+    float sum[1] = {both(s)};
+    warp_sum<1>(sum);
+    float mean = mine ? __fdiv_rn(sum[0], (float)mine) : 0.0f;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        if ((n * tpr + t) * VEC >= cols) continue;
+#pragma unroll
+        for (int i = 0; i < C::K; ++i) {
+            const V d = add(f[n][i], C::all(-mean));
+            m = fma(d, d, m);
         }
+    }
+    float m2[1] = {both(m)};
+    warp_sum<1>(m2);
+    row_moments(sum[0], mean, m2[0], mine, cols, red, phase, tpr, 0);
+    const float rstd = rstd_of(m2[0], cols, p.eps);
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const uint32_t e = (n * tpr + t) * VEC;
+        if (e >= cols) continue;
+#pragma unroll
+        for (int i = 0; i < C::K; ++i)
+            f[n][i] = fma(mul(add(f[n][i], C::all(-mean)), C::all(rstd)), w[n][i], b[n][i]);
+        if (NORM_OK(p.out, 2, r, y + e, VEC * sizeof(T), cols * sizeof(T))) C::store(y + e, f[n]);
+    }
+    if (t == 0) {
+        if (p.mean[r] && NORM_OK(p.mean, 3, r, p.mean[r] + row, 4, 4)) p.mean[r][row] = mean;
+        if (p.rstd[r] && NORM_OK(p.rstd, 4, r, p.rstd[r] + row, 4, 4)) p.rstd[r][row] = rstd;
+    }
+    DT_TL_END_BLOCK(DT_TL_NORM);
+}
 
-    for (; row < p.rows; row += step) {
-        Chunk<T, VEC> x[N], g[N];
-        uint64_t local;
-        const int r = find_rank(p, row, local);
-        const float mean = NORM_OK(p.mean, 3, r, p.mean[r] + local, 4, 4) ? p.mean[r][local] : 0.0f;
-        const float rstd = NORM_OK(p.rstd, 4, r, p.rstd[r] + local, 4, 4) ? p.rstd[r][local] : 0.0f;
-        if constexpr (kAhead) {
+// A row of a stage in registers: chunk c of thread t is elements [(c * tpr +
+// t) * VEC, + VEC).
+template <typename T, int VEC, int N>
+__device__ __forceinline__ void read_row(Chunk<T, VEC> (&c)[N], const NormParams &p, const T *row, uint32_t t)
+{
 #pragma unroll
-            for (int n = 0; n < N; ++n) {
-                x[n] = xn[n];
-                g[n] = gn[n];
-            }
-            if (row + step < p.rows) {
-                load_row<T, VEC, N>(xn, p, p.x, 0, row + step, t);
-                load_row<T, VEC, N>(gn, p, p.dy, 1, row + step, t);
-            }
-        } else {
-            load_row<T, VEC, N>(x, p, p.x, 0, row, t);
-            load_row<T, VEC, N>(g, p, p.dy, 1, row, t);
-        }
-        float s[2] = {0.0f, 0.0f};
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-            const uint32_t e = (n * tpr + t) * VEC;
-            if (e >= p.cols) continue;
-            float f[VEC], d[VEC];
-            x[n].get(f);
-            g[n].get(d);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const float h = (f[i] - mean) * rstd;
-                const float q = d[i] * (kHold ? w[kHold ? n * VEC + i : 0] : param(p.weight, p.weight_bf16, e + i, 1.0f));
-                s[0] += q;
-                s[1] = fmaf(q, h, s[1]);
-                dw[n * VEC + i] = fmaf(d[i], h, dw[n * VEC + i]);
-                db[n * VEC + i] += d[i];
-            }
-        }
-        row_sum<2>(s, red, phase, tpr, group);
-        const float mq = __fdiv_rn(s[0], (float)p.cols), mqh = __fdiv_rn(s[1], (float)p.cols);
-        T *dx = static_cast<T *>(p.out[r]) + local * p.cols;
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-            const uint32_t e = (n * tpr + t) * VEC;
-            if (e >= p.cols) continue;
-            float f[VEC], d[VEC];
-            x[n].get(f);
-            g[n].get(d);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const float h = (f[i] - mean) * rstd;
-                const float q = d[i] * (kHold ? w[kHold ? n * VEC + i : 0] : param(p.weight, p.weight_bf16, e + i, 1.0f));
-                f[i] = rstd * (q - mq - h * mqh);
-            }
-            if (NORM_OK(p.out, 2, r, dx + e, VEC * sizeof(T), p.cols * sizeof(T))) Chunk<T, VEC>::store(dx + e, f);
-        }
+    for (int n = 0; n < N; ++n) {
+        const uint32_t e = (n * p.tpr + t) * VEC;
+        if (e < p.cols) c[n].load(row + e);
+        else c[n].zero();
     }
-    if (p.partial && part < p.parts) {
-        float *out = p.partial + part * 2 * p.cols;
+}
+
+// Rows that the backward pass sums at a time, so that a barrier serves several:
+// as many as fit in registers beside the columns' sums.
+__host__ __device__ constexpr int back_rows(int elem_bytes, int elems) { return elem_bytes * elems <= 16 ? 4 : elem_bytes * elems <= 32 ? 2 : 1; }
+
+template <typename T, int VEC, int N>
+__global__ void __launch_bounds__(kNormThreads, 1) norm_backward_kernel(const __grid_constant__ NormParams p)
+{
+    constexpr bool kHold = N * VEC <= 16;   // wider rows read their weights again from L1
+    constexpr int B = back_rows(VEC == 1 ? 4 : sizeof(T), N * VEC);
+    using C = Chunk<T, VEC>;
+    using V = typename C::V;
+    constexpr int K = C::K;
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ float red[2][2 * B][kNormThreads / 32];
+    DT_TL_BEGIN();
+    const uint32_t tpr = p.tpr, group = threadIdx.x / tpr, t = threadIdx.x % tpr, cols = p.cols;
+    const uint64_t part = (uint64_t)group * gridDim.x + blockIdx.x;
+    Ring<T, 2> ring = start_ring<T, 2>(p, smem, group, t, part);
+    DT_TL_WAITED();
+    const float inv = __fdiv_rn(1.0f, (float)cols);
+    uint32_t phase = 0;
+    V dw[N][K], db[N][K], w[N][K];
+    auto weights = [&](int n) {
+        const uint32_t e = (n * tpr + t) * VEC;
+        if (e < cols) params<C, VEC>(p.weight, p.weight_bf16, e, 1.0f, w[n]);
+    };
 #pragma unroll
-        for (int n = 0; n < N; ++n)
+    for (int n = 0; n < N; ++n) {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const uint32_t e = (n * tpr + t) * VEC + i;
-                if (e >= p.cols) continue;
-                out[e] = dw[n * VEC + i];
-                out[p.cols + e] = db[n * VEC + i];
+        for (int i = 0; i < K; ++i) dw[n][i] = db[n][i] = w[n][i] = C::all(0.0f);
+        if constexpr (kHold) weights(n);
+    }
+
+    for (uint64_t c = part; c < p.chunks; c += p.parts) {
+        int r;
+        uint64_t row;
+        uint32_t rows;
+        ring.chunk(c, r, row, rows);
+        const T *xs = ring.row0(0, static_cast<const T *>(p.x[r]) + row * cols);
+        const T *gs = ring.row0(1, static_cast<const T *>(p.dy[r]) + row * cols);
+        T *dx = static_cast<T *>(p.out[r]) + row * cols;
+        // B rows at a time; the last ones of a stage may stand beside rows of zeros
+        float mean[B], rstd[B];
+        auto stats = [&](uint32_t k) {
+#pragma unroll
+            for (int j = 0; j < B; ++j) {
+                const bool in = k + j < rows;
+                mean[j] = in && NORM_OK(p.mean, 3, r, p.mean[r] + row + j, 4, 4) ? p.mean[r][row + j] : 0.0f;
+                rstd[j] = in && NORM_OK(p.rstd, 4, r, p.rstd[r] + row + j, 4, 4) ? p.rstd[r][row + j] : 0.0f;
             }
+        };
+        stats(0);
+        ring.wait();
+        for (uint32_t k = 0; k < rows; k += B, row += B, xs += B * cols, gs += B * cols, dx += B * (uint64_t)cols) {
+            if (k) stats(k);
+            C x[B][N], g[B][N];
+            float s[2 * B];
+#pragma unroll
+            for (int j = 0; j < B; ++j) {
+                if (k + j < rows) {
+                    read_row<T, VEC, N>(x[j], p, xs + j * cols, t);
+                    read_row<T, VEC, N>(g[j], p, gs + j * cols, t);
+                } else {
+#pragma unroll
+                    for (int n = 0; n < N; ++n) x[j][n].zero(), g[j][n].zero();
+                }
+                V sq = C::all(0.0f), sh = C::all(0.0f);
+                const V minus = C::all(-mean[j]), scale = C::all(rstd[j]);
+#pragma unroll
+                for (int n = 0; n < N; ++n) {
+                    if ((n * tpr + t) * VEC >= cols) continue;
+                    if constexpr (!kHold) weights(n);
+                    V f[K], d[K];
+                    x[j][n].get(f);
+                    g[j][n].get(d);
+#pragma unroll
+                    for (int i = 0; i < K; ++i) {
+                        const V a = add(f[i], minus), q = mul(d[i], w[n][i]);   // h = a * rstd
+                        sq = add(sq, q);
+                        sh = fma(q, a, sh);
+                        dw[n][i] = fma(mul(d[i], scale), a, dw[n][i]);
+                        db[n][i] = add(db[n][i], d[i]);
+                    }
+                }
+                s[2 * j] = both(sq);
+                s[2 * j + 1] = both(sh);
+            }
+            row_sum<2 * B>(s, red, phase, tpr, group);
+            if (tpr == 32) __syncwarp();
+            // every thread has read its part of the stage's last rows
+            if (k + B >= rows && t == 0 && c + (uint64_t)p.stages * p.parts < p.chunks)
+                ring.load(c + (uint64_t)p.stages * p.parts, ring.s);
+#pragma unroll
+            for (int j = 0; j < B; ++j) {
+                if (k + j >= rows) continue;
+                // dx = rstd (q - mean(q)) - a rstd^2 mean(q h), h = a rstd
+                const V c0 = C::all(-s[2 * j] * inv * rstd[j]);
+                const V c1 = C::all(-s[2 * j + 1] * inv * rstd[j] * rstd[j] * rstd[j]);
+                const V minus = C::all(-mean[j]), scale = C::all(rstd[j]);
+                T *to = dx + j * (uint64_t)cols;
+#pragma unroll
+                for (int n = 0; n < N; ++n) {
+                    const uint32_t e = (n * tpr + t) * VEC;
+                    if (e >= cols) continue;
+                    if constexpr (!kHold) weights(n);
+                    V f[K], d[K];
+                    x[j][n].get(f);
+                    g[j][n].get(d);
+#pragma unroll
+                    for (int i = 0; i < K; ++i) f[i] = fma(add(f[i], minus), c1, fma(mul(d[i], w[n][i]), scale, c0));
+                    if (NORM_OK(p.out, 2, r, to + e, VEC * sizeof(T), cols * sizeof(T))) C::store(to + e, f);
+                }
+            }
+        }
+        ring.next();
+    }
+    if (p.partial && part < p.chunks) {
+        float *out = p.partial + part * 2 * cols;
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const uint32_t e = (n * tpr + t) * VEC;
+            if (e >= cols) continue;
+            if constexpr (VEC == 1) {
+                out[e] = dw[n][0];
+                out[cols + e] = db[n][0];
+            } else {
+#pragma unroll
+                for (int i = 0; i < K; ++i) {   // cols is even here
+                    *reinterpret_cast<uint64_t *>(out + e + 2 * i) = dw[n][i].v;
+                    *reinterpret_cast<uint64_t *>(out + cols + e + 2 * i) = db[n][i].v;
+                }
+            }
+        }
     }
     DT_TL_END_BLOCK(DT_TL_NORM);
 }
@@ -377,7 +746,7 @@ __global__ void __launch_bounds__(kJoinCols *kJoinSlices) norm_join_kernel(const
 template <typename T>
 __global__ void __launch_bounds__(kLongThreads) norm_long_kernel(const __grid_constant__ NormParams p)
 {
-    __shared__ float red[2][32][2];
+    __shared__ float red[2][2][kNormThreads / 32];
     DT_TL_BEGIN();
     pdl_begin();
     DT_TL_WAITED();
@@ -390,15 +759,15 @@ __global__ void __launch_bounds__(kLongThreads) norm_long_kernel(const __grid_co
         auto at = [&](uint32_t e) {
             return NORM_OK(p.x, 0, r, x + e, sizeof(T), p.cols * sizeof(T)) ? to_f32(x[e]) : 0.0f;
         };
-        float s[1] = {0.0f}, m2[1] = {0.0f};
+        float s[2] = {0.0f, 0.0f}, m2[2] = {0.0f, 0.0f};
         for (uint32_t e = threadIdx.x; e < p.cols; e += kLongThreads) s[0] += at(e);
-        row_sum<1>(s, red, phase, kLongThreads, 0);
+        row_sum<2>(s, red, phase, kLongThreads, 0);
         const float mean = __fdiv_rn(s[0], (float)p.cols);
         for (uint32_t e = threadIdx.x; e < p.cols; e += kLongThreads) {
             const float d = at(e) - mean;
             m2[0] = fmaf(d, d, m2[0]);
         }
-        row_sum<1>(m2, red, phase, kLongThreads, 0);
+        row_sum<2>(m2, red, phase, kLongThreads, 0);
         const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(m2[0], (float)p.cols) + p.eps));
         for (uint32_t e = threadIdx.x; e < p.cols; e += kLongThreads) {
             const float f = fmaf((at(e) - mean) * rstd, param(p.weight, p.weight_bf16, e, 1.0f),
@@ -416,7 +785,7 @@ __global__ void __launch_bounds__(kLongThreads) norm_long_kernel(const __grid_co
 template <typename T>
 __global__ void __launch_bounds__(kLongThreads) norm_backward_long_kernel(const __grid_constant__ NormParams p)
 {
-    __shared__ float red[2][32][2];
+    __shared__ float red[2][2][kNormThreads / 32];
     DT_TL_BEGIN();
     pdl_begin();
     DT_TL_WAITED();
@@ -484,51 +853,110 @@ __global__ void __launch_bounds__(kThreads) norm_columns_long_kernel(const __gri
 
 using NormFn = void (*)(NormParams);
 
-// The kernel for rows of `chunks` chunks, and the threads that share a row.
-// The fewest chunks a thread that keep a row within 256 threads: 4096 bf16
-// elements are 2 x 16 bytes of 256 threads.  Backward instances stop where
-// two sums for each element no longer fit in registers.
+// The backward kernel for rows of `cols` elements, and the threads that share
+// a row: eight columns a thread, or as many more as keep a row within 512
+// threads.  Instances stop at 32 columns, where two sums for each no longer
+// fit in registers.
 struct NormPick {
     NormFn fn = nullptr;
-    uint32_t tpr = 0;
+    uint32_t tpr = 0, rows = 0;   // rows it sums at a time
 };
 
-template <typename T, int VEC, int N, bool BACK>
-bool try_pick(NormPick &k, uint32_t chunks, uint32_t most)
+template <typename T, int VEC, int N>
+void try_pick(NormPick &k, uint32_t chunks)
 {
     const uint32_t tpr = ((chunks + N - 1) / N + 31) / 32 * 32;
-    if (tpr > most) return false;
-    if constexpr (BACK) k.fn = norm_backward_kernel<T, VEC, N>;
-    else k.fn = norm_kernel<T, VEC, N>;
+    if (k.fn || tpr > kNormThreads) return;
+    k.fn = norm_backward_kernel<T, VEC, N>;
     k.tpr = tpr;
-    return true;
+    k.rows = back_rows(VEC == 1 ? 4 : sizeof(T), N * VEC);
 }
 
-template <typename T, int VEC, bool BACK>
-NormPick pick_norm(uint32_t cols)
+template <typename T, int VEC>
+NormPick pick_backward(uint32_t cols)
 {
     NormPick k;
     const uint32_t chunks = (cols + VEC - 1) / VEC;
-    constexpr int kMost = VEC == 1 ? 16 : BACK ? 16 / VEC * 2 : 8;   // chunks a thread
-    if (try_pick<T, VEC, 1, BACK>(k, chunks, 32) || try_pick<T, VEC, 2, BACK>(k, chunks, 256) ||
-        try_pick<T, VEC, 4, BACK>(k, chunks, 256))
-        return k;
-    if constexpr (kMost >= 8)
-        if (try_pick<T, VEC, 8, BACK>(k, chunks, 256)) return k;
-    try_pick<T, VEC, kMost, BACK>(k, chunks, kNormThreads);
+    if constexpr (VEC > 1)
+        if (chunks <= 32) try_pick<T, VEC, 1>(k, chunks);
+    try_pick<T, VEC, 8 / VEC>(k, chunks);
+    try_pick<T, VEC, 16 / VEC>(k, chunks);
+    if constexpr (VEC > 1) try_pick<T, VEC, 32 / VEC>(k, chunks);
     return k;
 }
 
-template <bool BACK>
-NormPick pick_norm(int dtype, bool vec, uint32_t cols)
+NormPick pick_backward(int dtype, bool vec, uint32_t cols)
 {
-    if (dtype == DT_BF16) return vec ? pick_norm<uint16_t, 8, BACK>(cols) : pick_norm<uint16_t, 1, BACK>(cols);
-    return vec ? pick_norm<float, 4, BACK>(cols) : pick_norm<float, 1, BACK>(cols);
+    if (dtype == DT_BF16) return vec ? pick_backward<uint16_t, 8>(cols) : pick_backward<uint16_t, 1>(cols);
+    return vec ? pick_backward<float, 4>(cols) : pick_backward<float, 1>(cols);
 }
 
-constexpr int kBackBlocks = 2;   // blocks per SM of the backward pass, at most: each writes a share of dw and db
+// The same for one row to a block, which every thread has up to 4 vectors or 8
+// single elements of.
+template <typename T, int VEC>
+NormPick pick_few(uint32_t cols)
+{
+    NormPick k;
+    const uint32_t chunks = (cols + VEC - 1) / VEC;
+    auto try_few = [&](NormFn fn, uint32_t n) {
+        const uint32_t tpr = ((chunks + n - 1) / n + 31) / 32 * 32;
+        if (k.fn || tpr > kRowThreads) return;
+        k.fn = fn;
+        k.tpr = tpr;
+    };
+    try_few(norm_few_kernel<T, VEC, 1>, 1);
+    try_few(norm_few_kernel<T, VEC, 2>, 2);
+    try_few(norm_few_kernel<T, VEC, 4>, 4);
+    if constexpr (VEC == 1) try_few(norm_few_kernel<T, VEC, 8>, 8);
+    return k;
+}
 
-uint32_t groups_of(uint32_t tpr, uint32_t threads) { return tpr >= threads ? 1 : threads / tpr; }
+NormPick pick_few(int dtype, bool vec, uint32_t cols)
+{
+    if (dtype == DT_BF16) return vec ? pick_few<uint16_t, 8>(cols) : pick_few<uint16_t, 1>(cols);
+    return vec ? pick_few<float, 4>(cols) : pick_few<float, 1>(cols);
+}
+
+// The grid, the groups and the rings of a call.
+struct NormShape {
+    uint32_t grid, threads;
+    size_t smem;
+};
+
+// Rows of a call over blocks of up to `groups` groups of p.tpr threads, with
+// `room` bytes of shared memory for their rings; at least `least` rows to a
+// stage where there are enough of them.
+NormShape norm_shape(NormParams &p, uint64_t row_bytes, bool vec, uint32_t arrays, uint64_t blocks, uint64_t groups,
+                     uint64_t least, uint64_t room)
+{
+    if (p.tpr > 32) groups = std::min<uint64_t>(groups, 15);   // named barriers
+    // short rows share a stage, but not so many that groups go without
+    uint64_t per = std::max(kStageTarget / row_bytes, least);
+    per = std::max<uint64_t>(1, std::min(per, p.rows / (groups * blocks)));
+    p.chunk_rows = (uint32_t)per;
+    p.chunks = 0;
+    for (int r = 0; r < p.P; ++r)
+        p.chunk_end[r] = p.chunks += (p.row_end[r] - (r ? p.row_end[r - 1] : 0) + per - 1) / per;
+    const uint64_t grid = std::min(blocks, p.chunks);
+    groups = std::min(groups, (p.chunks + grid - 1) / grid);
+    p.parts = (uint32_t)(grid * groups);
+    // rows at other offsets are copied with up to 15 bytes at either end
+    p.stage_bytes = (uint32_t)((per * row_bytes + (vec ? 0 : 32) + 127) / 128 * 128);
+    const uint64_t depth = (p.chunks + p.parts - 1) / p.parts;
+    p.stages = (uint32_t)std::max<uint64_t>(
+        1, std::min({(uint64_t)kMaxStages, room / (groups * arrays * p.stage_bytes), depth}));
+    return {(uint32_t)grid, (uint32_t)(groups * p.tpr), p.param_bytes + groups * p.stages * (arrays * p.stage_bytes + 8)};
+}
+
+cudaError_t launch_rows(NormFn fn, const NormShape &n, const NormParams &p, cudaStream_t s)
+{
+    if (n.smem > 48 * 1024) {   // what a kernel may have without asking
+        const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(fn),
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_kernel(fn, dim3(n.grid), dim3(n.threads), n.smem, s, false, p);
+}
 
 }  // namespace
 
@@ -536,55 +964,60 @@ DT_TL_BINDER(bind_timeline_norm)
 
 size_t norm_workspace(uint32_t cols, int device)
 {
-    // at least 32 threads a row, and at most 32 elements a thread
+    // a thread has at least 8 columns, or a warp the row: shares of that many groups
     uint32_t tpr = (cols + 31) / 32;
     tpr = tpr < 32 ? 32 : (tpr + 31) / 32 * 32;
-    const uint64_t parts = (uint64_t)sm_count(device) * kBackBlocks * groups_of(tpr, kNormThreads);
+    const uint64_t groups = tpr >= kNormThreads ? 1 : kNormThreads / tpr;
+    const uint64_t parts = (uint64_t)sm_count(device) * groups;
     return (size_t)((parts > kLongSlices ? parts : kLongSlices) * 2 * cols * sizeof(float));
 }
 
-cudaError_t launch_norm(const NormParams &p0, int dtype, bool vec, int device, cudaStream_t s)
+cudaError_t launch_norm(NormParams p, int dtype, bool vec, int device, cudaStream_t s)
 {
-    NormParams p = p0;
-    const NormPick k = pick_norm<false>(dtype, vec, p.cols);
-    uint32_t threads = kLongThreads, groups = 1;
-    NormFn fn = k.fn;
-    if (fn) {
-        p.tpr = k.tpr;
-        groups = groups_of(k.tpr, 256);
-        threads = groups * k.tpr;
-    } else {
-        fn = dtype == DT_BF16 ? norm_long_kernel<uint16_t> : norm_long_kernel<float>;
+    const uint64_t row_bytes = (uint64_t)p.cols * (dtype == DT_BF16 ? 2 : 4), sms = (uint64_t)sm_count(device);
+    if (p.rows <= 2 * sms) {
+        const NormPick k = pick_few(dtype, vec, p.cols);
+        if (k.fn) return launch_kernel(k.fn, dim3((unsigned)p.rows), dim3(k.tpr), 0, s, false, p);
     }
+    const uint64_t params = ((uint64_t)p.cols * sizeof(float) + 127) / 128 * 256;
+    p.param_bytes = params <= kMostParams ? (uint32_t)params : 0;
+    const uint64_t room = kSmemBytes - p.param_bytes, warps = kForwardThreads / 32;
+    if (row_bytes + 160 <= room) {
+        // two stages for each row that is worked on, and all the warps that a
+        // block may have shared out among them
+        const uint64_t most = std::max<uint64_t>(1, std::min(warps, room / (2 * (row_bytes + 160))));
+        const uint64_t rows = std::min(most, (p.rows + sms - 1) / sms);
+        p.tpr = (uint32_t)std::min<uint64_t>(warps / rows * 32, kRowThreads);
+        const NormShape n = norm_shape(p, row_bytes, vec, 1, sms, rows, 1, room);
+        const NormFn fn = dtype == DT_BF16 ? (vec ? norm_kernel<uint16_t, 8> : norm_kernel<uint16_t, 1>)
+                                           : (vec ? norm_kernel<float, 4> : norm_kernel<float, 1>);
+        return launch_rows(fn, n, p, s);
+    }
+    const NormFn fn = dtype == DT_BF16 ? norm_long_kernel<uint16_t> : norm_long_kernel<float>;
     int resident = 0;
-    cudaError_t e = resident_blocks(reinterpret_cast<const void *>(fn), (int)threads, device, &resident);
+    const cudaError_t e = resident_blocks(reinterpret_cast<const void *>(fn), kLongThreads, device, &resident);
     if (e != cudaSuccess) return e;
-    const uint64_t want = (p.rows + groups - 1) / groups;
-    const unsigned grid = (unsigned)(want < (uint64_t)resident ? want : (uint64_t)resident);
-    return launch_kernel(fn, dim3(grid), dim3(threads), 0, s, false, p);
+    const uint64_t grid = std::min(p.rows, (uint64_t)resident);
+    return launch_kernel(fn, dim3((unsigned)grid), dim3(kLongThreads), 0, s, false, p);
 }
 
 cudaError_t launch_norm_backward(NormParams p, int dtype, bool vec, int device, cudaStream_t s)
 {
-    const NormPick k = pick_norm<true>(dtype, vec, p.cols);
+    const NormPick k = pick_backward(dtype, vec, p.cols);
     cudaError_t e = cudaSuccess;
     if (p.rows == 0) {
         p.parts = 0;
     } else if (k.fn) {
+        const uint64_t row_bytes = (uint64_t)p.cols * (dtype == DT_BF16 ? 2 : 4), sms = (uint64_t)sm_count(device);
         p.tpr = k.tpr;
-        const uint32_t groups = groups_of(k.tpr, kNormThreads), threads = groups * k.tpr;
-        int resident = 0;
-        e = resident_blocks(reinterpret_cast<const void *>(k.fn), (int)threads, device, &resident);
-        if (e != cudaSuccess) return e;
-        const uint64_t want = (p.rows + groups - 1) / groups, cap = (uint64_t)sm_count(device) * kBackBlocks;
-        uint64_t grid = want < (uint64_t)resident ? want : (uint64_t)resident;
-        if (grid > cap) grid = cap;
-        p.parts = (uint32_t)(grid * groups < p.rows ? grid * groups : p.rows);
-        e = launch_kernel(k.fn, dim3((unsigned)grid), dim3(threads), 0, s, false, p);
+        p.param_bytes = 0;
+        const NormShape n = norm_shape(p, row_bytes, vec, 2, sms, kNormThreads / k.tpr, k.rows, kSmemBytes);
+        e = launch_rows(k.fn, n, p, s);
+        p.parts = (uint32_t)std::min<uint64_t>(p.parts, p.chunks);
     } else {
         const bool bf16 = dtype == DT_BF16;
         if (p.partial) {
-            p.parts = p.rows < kLongSlices ? (uint32_t)p.rows : kLongSlices;
+            p.parts = (uint32_t)std::min<uint64_t>(p.rows, kLongSlices);
             e = launch_kernel(bf16 ? norm_columns_long_kernel<uint16_t> : norm_columns_long_kernel<float>,
                               dim3((p.cols + kThreads - 1) / kThreads, p.parts), dim3(kThreads), 0, s, false, p);
             if (e != cudaSuccess) return e;
@@ -593,7 +1026,7 @@ cudaError_t launch_norm_backward(NormParams p, int dtype, bool vec, int device, 
         int resident = 0;
         e = resident_blocks(reinterpret_cast<const void *>(fn), kLongThreads, device, &resident);
         if (e != cudaSuccess) return e;
-        const uint64_t grid = p.rows < (uint64_t)resident ? p.rows : (uint64_t)resident;
+        const uint64_t grid = std::min(p.rows, (uint64_t)resident);
         e = launch_kernel(fn, dim3((unsigned)grid), dim3(kLongThreads), 0, s, false, p);
     }
     if (e != cudaSuccess || !p.partial) return e;

@@ -28,7 +28,13 @@ struct NormParams {
     uint64_t rows;
     uint32_t cols;
     uint32_t tpr;                      // threads that share a row, a multiple of 32
-    uint32_t parts;
+    uint32_t parts;                    // groups of them that walk over the rows; shares of dw and db
+    // rings: chunks of up to chunk_rows rows of one rank (rank r's end at
+    // chunk_end[r]), stages of stage_bytes for each array that is read
+    uint32_t chunk_rows, stages, stage_bytes;
+    uint32_t param_bytes;              // of weights and bias in shared memory, half of it each (0: not there)
+    uint64_t chunks;
+    uint64_t chunk_end[DT_MAX_RANKS];
     int32_t P;
     int32_t weight_bf16;               // of both
     float eps;
@@ -42,7 +48,7 @@ struct NormParams {
 // writes at most on this device.
 size_t norm_workspace(uint32_t cols, int device);
 // vec: every row of every buffer starts on a 16-byte boundary
-cudaError_t launch_norm(const NormParams &p, int dtype, bool vec, int device, cudaStream_t s);
+cudaError_t launch_norm(NormParams p, int dtype, bool vec, int device, cudaStream_t s);
 cudaError_t launch_norm_backward(NormParams p, int dtype, bool vec, int device, cudaStream_t s);
 
 #ifdef DT_TIMELINE
