@@ -21,11 +21,11 @@
 // E[x^2] - mu^2, which loses every digit where |mu| is large.  All sums are
 // fp32, and results are rounded once, at the store.
 //
-// Forward, a row is one warp's (of 4 x 2048 rows of 4096 bf16: 00 us, against
-// 94 us with 256 threads to a row and 44 with one row ahead in registers and no
-// ring), and several warps' where there are few rows or long ones.  Backward, a
-// thread keeps its columns' shares of dw and db in registers over all of its
-// rows, eight columns where it can, and up to four rows are summed at a time; a second
+// A thread keeps its columns, eight where it can, over all of its rows, and
+// with them their weights and, backward, their shares of dw and db; up to four
+// rows are summed at a time (4 x 2048 rows of 4096 bf16 took 94 us forward with
+// a ring and one row at a time, 40 with a warp or two to a row and the weights
+// in shared memory, whose reads then bound it, and 00 so).  A second
 // kernel adds the shares in a fixed order, so the result depends on the device
 // and the shapes alone, not on timing.
 #include <algorithm>
@@ -40,13 +40,10 @@
 namespace dt {
 namespace {
 
-constexpr int kRowThreads = 512;     // most threads of a row
-constexpr int kForwardThreads = 768; // most threads of a block, forward: 85 registers a thread
-constexpr int kNormThreads = 512;    // and backward: 128, for the sums of dw and db
-constexpr uint32_t kSmemBytes = 208 * 1024;    // of the SM's 227 KB: weights and rings
+constexpr int kNormThreads = 512;    // most threads of a block, and of a row
+constexpr uint32_t kSmemBytes = 208 * 1024;    // of the SM's 227 KB: rings
 constexpr uint32_t kMaxStages = 8;
 constexpr uint32_t kStageTarget = 4096;
-constexpr uint32_t kMostParams = 64 * 1024;    // longer weights and biases, as floats, stay in global memory
 constexpr int kLongThreads = 512;    // rows too long for registers
 constexpr int kLongSlices = 32;      // row slices of the column sums there
 constexpr int kJoinCols = 32;        // columns and row slices of a block that adds the shares
@@ -135,16 +132,6 @@ struct Chunk {
         }
         *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    // the same elements of f32 values, from a 16-byte boundary on
-    static __device__ __forceinline__ void floats(const float *p, V (&f)[K])
-    {
-#pragma unroll
-        for (int i = 0; i < K; i += 2) {
-            const ulonglong2 u = *reinterpret_cast<const ulonglong2 *>(p + 2 * i);
-            f[i].v = u.x;
-            f[i + 1].v = u.y;
-        }
-    }
     static __device__ __forceinline__ V all(float x) { return pair(x, x); }
 };
 
@@ -157,7 +144,6 @@ struct Chunk<T, 1> {
     __device__ __forceinline__ void zero() { v = 0; }
     __device__ __forceinline__ void get(V (&f)[1]) const { f[0] = to_f32(v); }
     static __device__ __forceinline__ void store(T *p, const V (&f)[1]) { from_f32(f[0], p); }
-    static __device__ __forceinline__ void floats(const float *p, V (&f)[1]) { f[0] = *p; }
     static __device__ __forceinline__ V all(float x) { return x; }
 };
 
@@ -211,7 +197,7 @@ __device__ __forceinline__ bool in_rank(const NormParams &p, const void *const *
 // double-buffered by the caller's `phase`, and a buffer is written again only
 // after the barrier of the exchange in between, which every reader of it has
 // passed.  The result is the row's first entry.
-using Exchange = float4[2][kForwardThreads / 32];
+using Exchange = float4[2][kNormThreads / 32];
 __device__ __forceinline__ const float4 *exchange(float4 v, Exchange &red, uint32_t &phase, uint32_t tpr, uint32_t group)
 {
     if ((threadIdx.x & 31) == 0) red[phase][threadIdx.x >> 5] = v;
@@ -276,8 +262,8 @@ __device__ __forceinline__ void row_sum(float (&v)[V], float (*red)[V][kNormThre
 // A group's walk over the rows: chunk c of the call is up to p.chunk_rows rows
 // of one rank; group number `part` has chunks part, part + parts, ...  Its
 // first thread starts the copies; the rest is the same in all of its threads.
-// Dynamic shared memory holds the weights, the groups' rings and their barriers.
-template <typename T, int ARRAYS>
+// Dynamic shared memory holds the groups' rings and their barriers.
+template <typename T, bool BACK>
 struct Ring {
     const NormParams &p;
     uint32_t base, bars;             // the group's stages and their barriers in shared memory
@@ -295,28 +281,33 @@ struct Ring {
         rows = p.row_end[r] - (r ? p.row_end[r - 1] : 0);
         n = rows - row < p.chunk_rows ? (uint32_t)(rows - row) : p.chunk_rows;
     }
-    // The 16-byte blocks that hold rows [row, row + n) of one buffer.
-    __device__ __forceinline__ void copy(const void *base_ptr, int kind, int r, uint64_t row, uint32_t n, uint32_t dst,
-                                         uint32_t bar, uint32_t &bytes) const
+    // The 16-byte blocks that hold rows [row, row + n) of `bytes` bytes of one buffer.
+    __device__ __forceinline__ uint32_t copy(const void *const *bases, int kind, int r, uint64_t row, uint32_t n,
+                                             uint64_t row_bytes, uint32_t dst, uint32_t bar) const
     {
-        (void)kind, (void)r;
-        const uint64_t lo = reinterpret_cast<uint64_t>(base_ptr) + row * p.cols * sizeof(T);
-        const uint64_t hi = lo + (uint64_t)n * p.cols * sizeof(T);
+        (void)kind;
+        const uint64_t lo = reinterpret_cast<uint64_t>(bases[r]) + row * row_bytes, hi = lo + n * row_bytes;
         const uint64_t from = lo & ~15ull, to = (hi + 15) & ~15ull;
-        bytes = (uint32_t)(to - from);
-        if (!NORM_OK(kind ? p.dy : p.x, kind, r, reinterpret_cast<const void *>(lo), hi - lo, p.cols * sizeof(T))) bytes = 0;
-        if (bytes) bulk_load(dst, reinterpret_cast<const void *>(from), bytes, bar);
+        if (!NORM_OK(bases, kind, r, reinterpret_cast<const void *>(lo), hi - lo, row_bytes)) return 0;
+        bulk_load(dst, reinterpret_cast<const void *>(from), (uint32_t)(to - from), bar);
+        return (uint32_t)(to - from);
     }
     __device__ __forceinline__ void load(uint64_t c, uint32_t stage) const
     {
         int r;
         uint64_t row;
-        uint32_t n, bytes[2] = {0, 0};
+        uint32_t n;
         chunk(c, r, row, n);
-        const uint32_t bar = bars + 8 * stage, dst = base + stage * p.stage_bytes * ARRAYS;
-        copy(p.x[r], 0, r, row, n, dst, bar, bytes[0]);
-        if constexpr (ARRAYS == 2) copy(p.dy[r], 1, r, row, n, dst + p.stage_bytes, bar, bytes[1]);
-        mbar_expect_tx(bar, bytes[0] + bytes[1]);
+        const uint32_t bar = bars + 8 * stage, dst = base + stage * p.stage_bytes;
+        const uint64_t row_bytes = p.cols * sizeof(T);
+        uint32_t bytes = copy(p.x, 0, r, row, n, row_bytes, dst, bar);
+        if constexpr (BACK) {
+            bytes += copy(p.dy, 1, r, row, n, row_bytes, dst + p.array_bytes, bar);
+            const uint32_t stat = dst + 2 * p.array_bytes;
+            bytes += copy(reinterpret_cast<const void *const *>(p.mean), 3, r, row, n, 4, stat, bar);
+            bytes += copy(reinterpret_cast<const void *const *>(p.rstd), 4, r, row, n, 4, stat + p.stat_bytes, bar);
+        }
+        mbar_expect_tx(bar, bytes);
     }
     __device__ __forceinline__ void wait()
     {
@@ -327,10 +318,11 @@ struct Ring {
         late = true;
         record_error(p.sink, DT_ERR_TIMEOUT, -1, blockIdx.x, 0);
     }
-    // Array a's first row in the present stage, where `src` is its address in memory.
-    __device__ __forceinline__ const T *row0(int a, const T *src) const
+    // What was copied to `offset` bytes into the present stage from `src` on.
+    template <typename E>
+    __device__ __forceinline__ const E *at(uint32_t offset, const E *src) const
     {
-        return reinterpret_cast<const T *>(mem + (s * ARRAYS + a) * p.stage_bytes + (reinterpret_cast<uint64_t>(src) & 15));
+        return reinterpret_cast<const E *>(mem + s * p.stage_bytes + offset + (reinterpret_cast<uint64_t>(src) & 15));
     }
     __device__ __forceinline__ void next()
     {
@@ -338,13 +330,11 @@ struct Ring {
     }
 };
 
-// The start of both kernels: the group's ring, with its first copies under way.
-template <typename T, int ARRAYS>
-__device__ __forceinline__ Ring<T, ARRAYS> start_ring(const NormParams &p, unsigned char *smem, uint32_t group, uint32_t t,
-                                                      uint64_t part)
+// The group's ring; the waits of the next kernel and for the one before.
+template <typename T, bool BACK>
+__device__ __forceinline__ Ring<T, BACK> make_ring(const NormParams &p, unsigned char *smem, uint32_t group)
 {
-    const uint32_t groups = blockDim.x / p.tpr, mine = p.stages * p.stage_bytes * ARRAYS;
-    smem += p.param_bytes;
+    const uint32_t groups = blockDim.x / p.tpr, mine = p.stages * p.stage_bytes;
     const uint32_t bars = smem_addr(smem) + groups * mine;
     if (threadIdx.x == 0) {
         for (uint32_t k = 0; k < groups * p.stages; ++k) mbar_init(bars + 8 * k, 1);
@@ -352,14 +342,40 @@ __device__ __forceinline__ Ring<T, ARRAYS> start_ring(const NormParams &p, unsig
     }
     __syncthreads();
     unsigned char *mem = smem + (size_t)group * mine;
-    Ring<T, ARRAYS> ring{p, smem_addr(mem), bars + 8 * group * p.stages, mem};
     pdl_begin();
+    return Ring<T, BACK>{p, smem_addr(mem), bars + 8 * group * p.stages, mem};
+}
+
+// Its first copies.  They come after the loads of the weights, which would
+// otherwise wait behind 25 MB of rows (6 us).
+template <typename T, bool BACK>
+__device__ __forceinline__ void first_loads(const Ring<T, BACK> &ring, const NormParams &p, uint32_t t, uint64_t part)
+{
     if (t == 0)
         for (uint32_t k = 0; k < p.stages; ++k) {
             const uint64_t c = part + (uint64_t)k * p.parts;
             if (c < p.chunks) ring.load(c, k);
         }
-    return ring;
+}
+
+// A row of a stage in registers: chunk c of thread t is elements [(c * tpr +
+// t) * VEC, + VEC).
+template <typename T, int VEC, int N>
+__device__ __forceinline__ void read_row(Chunk<T, VEC> (&c)[N], const NormParams &p, const T *row, uint32_t t, bool there)
+{
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const uint32_t e = (n * p.tpr + t) * VEC;
+        if (there && e < p.cols) c[n].load(row + e);
+        else c[n].zero();
+    }
+}
+
+// Rows that are summed at a time, so that a barrier serves several: as many as
+// fit in registers beside what a thread keeps for its columns.
+__host__ __device__ constexpr int rows_at_once(int elem_bytes, int elems)
+{
+    return elem_bytes * elems <= 16 ? 4 : elem_bytes * elems <= 32 ? 2 : 1;
 }
 
 // The mean and the sum of squared distances from it, of all warps that share a
@@ -384,104 +400,107 @@ __device__ __forceinline__ float rstd_of(float m2, uint32_t cols, float eps)
     return __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(m2, (float)cols) + eps));
 }
 
-template <typename T, int VEC>
-__global__ void __launch_bounds__(kForwardThreads, 1) norm_kernel(const __grid_constant__ NormParams p)
+template <typename T, int VEC, int N>
+__global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(const __grid_constant__ NormParams p)
 {
+    constexpr bool kHold = N * VEC <= 16;   // wider rows read their weights again from L1
+    constexpr int B = rows_at_once(VEC == 1 ? 4 : sizeof(T), N * VEC);
     using C = Chunk<T, VEC>;
     using V = typename C::V;
+    constexpr int K = C::K;
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ Exchange red;
+    __shared__ float red[2][B][kNormThreads / 32];
     DT_TL_BEGIN();
     const uint32_t tpr = p.tpr, group = threadIdx.x / tpr, t = threadIdx.x % tpr, cols = p.cols;
     const uint64_t part = (uint64_t)group * gridDim.x + blockIdx.x;
-    Ring<T, 1> ring = start_ring<T, 1>(p, smem, group, t, part);
+    Ring<T, false> ring = make_ring<T, false>(p, smem, group);
     DT_TL_WAITED();
-    // as floats, so that no row spends instructions on widening them
-    float *weight = reinterpret_cast<float *>(smem), *bias = reinterpret_cast<float *>(smem + p.param_bytes / 2);
-    if (p.param_bytes) {
-#pragma unroll 4
-        for (uint32_t e = threadIdx.x; e < cols; e += blockDim.x) {
-            weight[e] = param(p.weight, p.weight_bf16, e, 1.0f);
-            bias[e] = param(p.bias, p.weight_bf16, e, 0.0f);
-        }
-        __syncthreads();
-    }
-    // this thread's elements of a row are [e0, + VEC), and every `step` on; the
-    // warp's number of them
-    const uint32_t e0 = t * VEC, step = tpr * VEC;
-    uint32_t mine = 0;
-    for (uint32_t e = e0 - (t & 31) * VEC; e < cols; e += step) mine += min(cols - e, 32u * VEC);
-    const float inv_mine = mine ? __fdiv_rn(1.0f, (float)mine) : 0.0f;
+    const float inv = __fdiv_rn(1.0f, (float)cols);
     uint32_t phase = 0;
+    V w[N][K], b[N][K];
+    auto weights = [&](int n) {
+        const uint32_t e = (n * tpr + t) * VEC;
+        if (e >= cols) return;
+        params<C, VEC>(p.weight, p.weight_bf16, e, 1.0f, w[n]);
+        params<C, VEC>(p.bias, p.weight_bf16, e, 0.0f, b[n]);
+    };
+    if constexpr (kHold)
+#pragma unroll
+        for (int n = 0; n < N; ++n) weights(n);
+    first_loads(ring, p, t, part);
 
     for (uint64_t c = part; c < p.chunks; c += p.parts) {
         int r;
         uint64_t row;
         uint32_t rows;
         ring.chunk(c, r, row, rows);
-        const T *src = ring.row0(0, static_cast<const T *>(p.x[r]) + row * cols);
+        const T *src = ring.at(0, static_cast<const T *>(p.x[r]) + row * cols);
         T *y = static_cast<T *>(p.out[r]) + row * cols;
         ring.wait();
-        for (uint32_t k = 0; k < rows; ++k, ++row, src += cols, y += cols) {
-            // the warp's mean and the squared distances from it; two sums, so
-            // that an addition does not wait for the one before
-            V s[2] = {C::all(0.0f), C::all(0.0f)}, m[2] = {C::all(0.0f), C::all(0.0f)};
-#pragma unroll 4
-            for (uint32_t e = e0; e < cols; e += step) {
-                C x;
-                x.load(src + e);
-                V f[C::K];
-                x.get(f);
+        for (uint32_t k = 0; k < rows; k += B, row += B, src += B * cols, y += B * (uint64_t)cols) {
+            // B rows at a time; the last ones of a stage may stand beside rows of zeros
+            C x[B][N];
+            float s[B], m2[B];
 #pragma unroll
-                for (int i = 0; i < C::K; ++i) s[i & 1] = add(s[i & 1], f[i]);
-            }
-            float sum[1] = {both(add(s[0], s[1]))};
-            warp_sum<1>(sum);
-            float mean = sum[0] * inv_mine;
-            const V minus_warp = C::all(-mean);
-#pragma unroll 4
-            for (uint32_t e = e0; e < cols; e += step) {
-                C x;
-                x.load(src + e);
-                V f[C::K];
-                x.get(f);
+            for (int j = 0; j < B; ++j) {
+                read_row<T, VEC, N>(x[j], p, src + j * cols, t, k + j < rows);
+                V sum = C::all(0.0f);
 #pragma unroll
-                for (int i = 0; i < C::K; ++i) {
-                    f[i] = add(f[i], minus_warp);
-                    m[i & 1] = fma(f[i], f[i], m[i & 1]);
+                for (int n = 0; n < N; ++n) {
+                    V f[K];
+                    x[j][n].get(f);
+#pragma unroll
+                    for (int i = 0; i < K; ++i) sum = add(sum, f[i]);
                 }
+                s[j] = both(sum);
             }
-            float m2[1] = {both(add(m[0], m[1]))};
-            warp_sum<1>(m2);
-            row_moments(sum[0], mean, m2[0], mine, cols, red, phase, tpr, group);
-            const float rstd = rstd_of(m2[0], cols, p.eps);
-            const V minus = C::all(-mean), scale = C::all(rstd);
-#pragma unroll 4
-            for (uint32_t e = e0; e < cols; e += step) {
-                C x;
-                x.load(src + e);
-                V f[C::K], w[C::K], b[C::K];
-                x.get(f);
-                if (p.param_bytes) {
-                    C::floats(weight + e, w);
-                    C::floats(bias + e, b);
-                } else {
-                    params<C, VEC>(p.weight, p.weight_bf16, e, 1.0f, w);
-                    params<C, VEC>(p.bias, p.weight_bf16, e, 0.0f, b);
-                }
+            row_sum<B>(s, red, phase, tpr, group);
+            if (tpr == 32) __syncwarp();
+            // every thread has read its part of the stage's last rows
+            if (k + B >= rows && t == 0 && c + (uint64_t)p.stages * p.parts < p.chunks)
+                ring.load(c + (uint64_t)p.stages * p.parts, ring.s);
 #pragma unroll
-                for (int i = 0; i < C::K; ++i) f[i] = fma(mul(add(f[i], minus), scale), w[i], b[i]);
-                if (NORM_OK(p.out, 2, r, y + e, VEC * sizeof(T), cols * sizeof(T))) C::store(y + e, f);
+            for (int j = 0; j < B; ++j) {
+                s[j] *= inv;
+                V sum = C::all(0.0f);
+                const V minus = C::all(-s[j]);
+#pragma unroll
+                for (int n = 0; n < N; ++n) {
+                    if ((n * tpr + t) * VEC >= cols) continue;
+                    V f[K];
+                    x[j][n].get(f);
+#pragma unroll
+                    for (int i = 0; i < K; ++i) {
+                        f[i] = add(f[i], minus);
+                        sum = fma(f[i], f[i], sum);
+                    }
+                }
+                m2[j] = both(sum);
             }
-            if (t == 0) {
-                if (p.mean[r] && NORM_OK(p.mean, 3, r, p.mean[r] + row, 4, 4)) p.mean[r][row] = mean;
-                if (p.rstd[r] && NORM_OK(p.rstd, 4, r, p.rstd[r] + row, 4, 4)) p.rstd[r][row] = rstd;
+            row_sum<B>(m2, red, phase, tpr, group);
+#pragma unroll
+            for (int j = 0; j < B; ++j) {
+                if (k + j >= rows) continue;
+                const float rstd = rstd_of(m2[j], cols, p.eps);
+                const V minus = C::all(-s[j]), scale = C::all(rstd);
+                T *to = y + j * (uint64_t)cols;
+#pragma unroll
+                for (int n = 0; n < N; ++n) {
+                    const uint32_t e = (n * tpr + t) * VEC;
+                    if (e >= cols) continue;
+                    if constexpr (!kHold) weights(n);
+                    V f[K];
+                    x[j][n].get(f);
+#pragma unroll
+                    for (int i = 0; i < K; ++i) f[i] = fma(mul(add(f[i], minus), scale), w[n][i], b[n][i]);
+                    if (NORM_OK(p.out, 2, r, to + e, VEC * sizeof(T), cols * sizeof(T))) C::store(to + e, f);
+                }
+                if (t == 0) {
+                    if (p.mean[r] && NORM_OK(p.mean, 3, r, p.mean[r] + row + j, 4, 4)) p.mean[r][row + j] = s[j];
+                    if (p.rstd[r] && NORM_OK(p.rstd, 4, r, p.rstd[r] + row + j, 4, 4)) p.rstd[r][row + j] = rstd;
+                }
             }
         }
-        // the stage is free once every thread of the group has read it
-        if (tpr > 32) asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(tpr) : "memory");
-        else __syncwarp();
-        if (t == 0 && c + (uint64_t)p.stages * p.parts < p.chunks) ring.load(c + (uint64_t)p.stages * p.parts, ring.s);
         ring.next();
     }
     DT_TL_END_BLOCK(DT_TL_NORM);
@@ -492,7 +511,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1) norm_kernel(const __grid_c
 // all loaded to registers at once (1 row on each of 4 ranks, 4096 bf16: 0.0 us
 // a call, against 5.3 through a ring and shared memory).
 template <typename T, int VEC, int N>
-__global__ void __launch_bounds__(kRowThreads) norm_few_kernel(const __grid_constant__ NormParams p)
+__global__ void __launch_bounds__(kNormThreads) norm_few_kernel(const __grid_constant__ NormParams p)
 {
     using C = Chunk<T, VEC>;
     using V = typename C::V;
@@ -561,28 +580,11 @@ __global__ void __launch_bounds__(kRowThreads) norm_few_kernel(const __grid_cons
     DT_TL_END_BLOCK(DT_TL_NORM);
 }
 
-// A row of a stage in registers: chunk c of thread t is elements [(c * tpr +
-// t) * VEC, + VEC).
-template <typename T, int VEC, int N>
-__device__ __forceinline__ void read_row(Chunk<T, VEC> (&c)[N], const NormParams &p, const T *row, uint32_t t)
-{
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-        const uint32_t e = (n * p.tpr + t) * VEC;
-        if (e < p.cols) c[n].load(row + e);
-        else c[n].zero();
-    }
-}
-
-// Rows that the backward pass sums at a time, so that a barrier serves several:
-// as many as fit in registers beside the columns' sums.
-__host__ __device__ constexpr int back_rows(int elem_bytes, int elems) { return elem_bytes * elems <= 16 ? 4 : elem_bytes * elems <= 32 ? 2 : 1; }
-
 template <typename T, int VEC, int N>
 __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_kernel(const __grid_constant__ NormParams p)
 {
     constexpr bool kHold = N * VEC <= 16;   // wider rows read their weights again from L1
-    constexpr int B = back_rows(VEC == 1 ? 4 : sizeof(T), N * VEC);
+    constexpr int B = rows_at_once(VEC == 1 ? 4 : sizeof(T), N * VEC);
     using C = Chunk<T, VEC>;
     using V = typename C::V;
     constexpr int K = C::K;
@@ -591,7 +593,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_kernel(const __
     DT_TL_BEGIN();
     const uint32_t tpr = p.tpr, group = threadIdx.x / tpr, t = threadIdx.x % tpr, cols = p.cols;
     const uint64_t part = (uint64_t)group * gridDim.x + blockIdx.x;
-    Ring<T, 2> ring = start_ring<T, 2>(p, smem, group, t, part);
+    Ring<T, true> ring = make_ring<T, true>(p, smem, group);
     DT_TL_WAITED();
     const float inv = __fdiv_rn(1.0f, (float)cols);
     uint32_t phase = 0;
@@ -606,40 +608,33 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_kernel(const __
         for (int i = 0; i < K; ++i) dw[n][i] = db[n][i] = w[n][i] = C::all(0.0f);
         if constexpr (kHold) weights(n);
     }
+    first_loads(ring, p, t, part);
 
     for (uint64_t c = part; c < p.chunks; c += p.parts) {
         int r;
         uint64_t row;
         uint32_t rows;
         ring.chunk(c, r, row, rows);
-        const T *xs = ring.row0(0, static_cast<const T *>(p.x[r]) + row * cols);
-        const T *gs = ring.row0(1, static_cast<const T *>(p.dy[r]) + row * cols);
+        const T *xs = ring.at(0, static_cast<const T *>(p.x[r]) + row * cols);
+        const T *gs = ring.at(p.array_bytes, static_cast<const T *>(p.dy[r]) + row * cols);
+        const float *means = ring.at(2 * p.array_bytes, p.mean[r] + row);
+        const float *rstds = ring.at(2 * p.array_bytes + p.stat_bytes, p.rstd[r] + row);
         T *dx = static_cast<T *>(p.out[r]) + row * cols;
-        // B rows at a time; the last ones of a stage may stand beside rows of zeros
-        float mean[B], rstd[B];
-        auto stats = [&](uint32_t k) {
+        ring.wait();
+        for (uint32_t k = 0; k < rows; k += B, xs += B * cols, gs += B * cols, dx += B * (uint64_t)cols) {
+            // B rows at a time; the last ones of a stage may stand beside rows of zeros
+            float mean[B], rstd[B];
 #pragma unroll
             for (int j = 0; j < B; ++j) {
-                const bool in = k + j < rows;
-                mean[j] = in && NORM_OK(p.mean, 3, r, p.mean[r] + row + j, 4, 4) ? p.mean[r][row + j] : 0.0f;
-                rstd[j] = in && NORM_OK(p.rstd, 4, r, p.rstd[r] + row + j, 4, 4) ? p.rstd[r][row + j] : 0.0f;
+                mean[j] = k + j < rows ? means[k + j] : 0.0f;
+                rstd[j] = k + j < rows ? rstds[k + j] : 0.0f;
             }
-        };
-        stats(0);
-        ring.wait();
-        for (uint32_t k = 0; k < rows; k += B, row += B, xs += B * cols, gs += B * cols, dx += B * (uint64_t)cols) {
-            if (k) stats(k);
             C x[B][N], g[B][N];
             float s[2 * B];
 #pragma unroll
             for (int j = 0; j < B; ++j) {
-                if (k + j < rows) {
-                    read_row<T, VEC, N>(x[j], p, xs + j * cols, t);
-                    read_row<T, VEC, N>(g[j], p, gs + j * cols, t);
-                } else {
-#pragma unroll
-                    for (int n = 0; n < N; ++n) x[j][n].zero(), g[j][n].zero();
-                }
+                read_row<T, VEC, N>(x[j], p, xs + j * cols, t, k + j < rows);
+                read_row<T, VEC, N>(g[j], p, gs + j * cols, t, k + j < rows);
                 V sq = C::all(0.0f), sh = C::all(0.0f);
                 const V minus = C::all(-mean[j]), scale = C::all(rstd[j]);
 #pragma unroll
@@ -853,7 +848,7 @@ __global__ void __launch_bounds__(kThreads) norm_columns_long_kernel(const __gri
 
 using NormFn = void (*)(NormParams);
 
-// The backward kernel for rows of `cols` elements, and the threads that share
+// The kernel for rows of `cols` elements, either way, and the threads that share
 // a row: eight columns a thread, or as many more as keep a row within 512
 // threads.  Instances stop at 32 columns, where two sums for each no longer
 // fit in registers.
@@ -862,33 +857,35 @@ struct NormPick {
     uint32_t tpr = 0, rows = 0;   // rows it sums at a time
 };
 
-template <typename T, int VEC, int N>
+template <typename T, int VEC, int N, bool BACK>
 void try_pick(NormPick &k, uint32_t chunks)
 {
     const uint32_t tpr = ((chunks + N - 1) / N + 31) / 32 * 32;
     if (k.fn || tpr > kNormThreads) return;
-    k.fn = norm_backward_kernel<T, VEC, N>;
+    if constexpr (BACK) k.fn = norm_backward_kernel<T, VEC, N>;
+    else k.fn = norm_kernel<T, VEC, N>;
     k.tpr = tpr;
-    k.rows = back_rows(VEC == 1 ? 4 : sizeof(T), N * VEC);
+    k.rows = rows_at_once(VEC == 1 ? 4 : sizeof(T), N * VEC);
 }
 
-template <typename T, int VEC>
-NormPick pick_backward(uint32_t cols)
+template <typename T, int VEC, bool BACK>
+NormPick pick_norm(uint32_t cols)
 {
     NormPick k;
     const uint32_t chunks = (cols + VEC - 1) / VEC;
     if constexpr (VEC > 1)
-        if (chunks <= 32) try_pick<T, VEC, 1>(k, chunks);
-    try_pick<T, VEC, 8 / VEC>(k, chunks);
-    try_pick<T, VEC, 16 / VEC>(k, chunks);
-    if constexpr (VEC > 1) try_pick<T, VEC, 32 / VEC>(k, chunks);
+        if (chunks <= 32) try_pick<T, VEC, 1, BACK>(k, chunks);
+    try_pick<T, VEC, 8 / VEC, BACK>(k, chunks);
+    try_pick<T, VEC, 16 / VEC, BACK>(k, chunks);
+    if constexpr (VEC > 1) try_pick<T, VEC, 32 / VEC, BACK>(k, chunks);
     return k;
 }
 
-NormPick pick_backward(int dtype, bool vec, uint32_t cols)
+template <bool BACK>
+NormPick pick_norm(int dtype, bool vec, uint32_t cols)
 {
-    if (dtype == DT_BF16) return vec ? pick_backward<uint16_t, 8>(cols) : pick_backward<uint16_t, 1>(cols);
-    return vec ? pick_backward<float, 4>(cols) : pick_backward<float, 1>(cols);
+    if (dtype == DT_BF16) return vec ? pick_norm<uint16_t, 8, BACK>(cols) : pick_norm<uint16_t, 1, BACK>(cols);
+    return vec ? pick_norm<float, 4, BACK>(cols) : pick_norm<float, 1, BACK>(cols);
 }
 
 // The same for one row to a block, which every thread has up to 4 vectors or 8
@@ -900,7 +897,7 @@ NormPick pick_few(uint32_t cols)
     const uint32_t chunks = (cols + VEC - 1) / VEC;
     auto try_few = [&](NormFn fn, uint32_t n) {
         const uint32_t tpr = ((chunks + n - 1) / n + 31) / 32 * 32;
-        if (k.fn || tpr > kRowThreads) return;
+        if (k.fn || tpr > kNormThreads) return;
         k.fn = fn;
         k.tpr = tpr;
     };
@@ -923,29 +920,30 @@ struct NormShape {
     size_t smem;
 };
 
-// Rows of a call over blocks of up to `groups` groups of p.tpr threads, with
-// `room` bytes of shared memory for their rings; at least `least` rows to a
-// stage where there are enough of them.
-NormShape norm_shape(NormParams &p, uint64_t row_bytes, bool vec, uint32_t arrays, uint64_t blocks, uint64_t groups,
-                     uint64_t least, uint64_t room)
+NormShape norm_shape(NormParams &p, const NormPick &k, int dtype, bool vec, bool back, int device)
 {
-    if (p.tpr > 32) groups = std::min<uint64_t>(groups, 15);   // named barriers
-    // short rows share a stage, but not so many that groups go without
-    uint64_t per = std::max(kStageTarget / row_bytes, least);
-    per = std::max<uint64_t>(1, std::min(per, p.rows / (groups * blocks)));
+    const uint64_t row_bytes = (uint64_t)p.cols * (dtype == DT_BF16 ? 2 : 4), sms = (uint64_t)sm_count(device);
+    p.tpr = k.tpr;
+    uint64_t groups = kNormThreads / k.tpr;
+    if (k.tpr > 32) groups = std::min<uint64_t>(groups, 15);   // named barriers
+    // rows of a stage: those summed at once, and more where they are short,
+    // but not so many that groups go without
+    uint64_t per = std::max<uint64_t>(kStageTarget / row_bytes, k.rows);
+    per = std::max<uint64_t>(1, std::min(per, p.rows / (groups * sms)));
     p.chunk_rows = (uint32_t)per;
     p.chunks = 0;
     for (int r = 0; r < p.P; ++r)
         p.chunk_end[r] = p.chunks += (p.row_end[r] - (r ? p.row_end[r - 1] : 0) + per - 1) / per;
-    const uint64_t grid = std::min(blocks, p.chunks);
+    const uint64_t grid = std::min(sms, p.chunks);
     groups = std::min(groups, (p.chunks + grid - 1) / grid);
     p.parts = (uint32_t)(grid * groups);
     // rows at other offsets are copied with up to 15 bytes at either end
-    p.stage_bytes = (uint32_t)((per * row_bytes + (vec ? 0 : 32) + 127) / 128 * 128);
+    p.array_bytes = (uint32_t)((per * row_bytes + (vec ? 0 : 32) + 127) / 128 * 128);
+    p.stat_bytes = back ? (uint32_t)((per * 4 + 32 + 63) / 64 * 64) : 0;
+    p.stage_bytes = back ? 2 * (p.array_bytes + p.stat_bytes) : p.array_bytes;
     const uint64_t depth = (p.chunks + p.parts - 1) / p.parts;
-    p.stages = (uint32_t)std::max<uint64_t>(
-        1, std::min({(uint64_t)kMaxStages, room / (groups * arrays * p.stage_bytes), depth}));
-    return {(uint32_t)grid, (uint32_t)(groups * p.tpr), p.param_bytes + groups * p.stages * (arrays * p.stage_bytes + 8)};
+    p.stages = (uint32_t)std::max<uint64_t>(1, std::min({(uint64_t)kMaxStages, kSmemBytes / (groups * p.stage_bytes), depth}));
+    return {(uint32_t)grid, (uint32_t)(groups * p.tpr), groups * p.stages * (p.stage_bytes + 8)};
 }
 
 cudaError_t launch_rows(NormFn fn, const NormShape &n, const NormParams &p, cudaStream_t s)
@@ -974,25 +972,12 @@ size_t norm_workspace(uint32_t cols, int device)
 
 cudaError_t launch_norm(NormParams p, int dtype, bool vec, int device, cudaStream_t s)
 {
-    const uint64_t row_bytes = (uint64_t)p.cols * (dtype == DT_BF16 ? 2 : 4), sms = (uint64_t)sm_count(device);
-    if (p.rows <= 2 * sms) {
+    if (p.rows <= 2 * (uint64_t)sm_count(device)) {
         const NormPick k = pick_few(dtype, vec, p.cols);
         if (k.fn) return launch_kernel(k.fn, dim3((unsigned)p.rows), dim3(k.tpr), 0, s, false, p);
     }
-    const uint64_t params = ((uint64_t)p.cols * sizeof(float) + 127) / 128 * 256;
-    p.param_bytes = params <= kMostParams ? (uint32_t)params : 0;
-    const uint64_t room = kSmemBytes - p.param_bytes, warps = kForwardThreads / 32;
-    if (row_bytes + 160 <= room) {
-        // two stages for each row that is worked on, and all the warps that a
-        // block may have shared out among them
-        const uint64_t most = std::max<uint64_t>(1, std::min(warps, room / (2 * (row_bytes + 160))));
-        const uint64_t rows = std::min(most, (p.rows + sms - 1) / sms);
-        p.tpr = (uint32_t)std::min<uint64_t>(warps / rows * 32, kRowThreads);
-        const NormShape n = norm_shape(p, row_bytes, vec, 1, sms, rows, 1, room);
-        const NormFn fn = dtype == DT_BF16 ? (vec ? norm_kernel<uint16_t, 8> : norm_kernel<uint16_t, 1>)
-                                           : (vec ? norm_kernel<float, 4> : norm_kernel<float, 1>);
-        return launch_rows(fn, n, p, s);
-    }
+    const NormPick k = pick_norm<false>(dtype, vec, p.cols);
+    if (k.fn) return launch_rows(k.fn, norm_shape(p, k, dtype, vec, false, device), p, s);
     const NormFn fn = dtype == DT_BF16 ? norm_long_kernel<uint16_t> : norm_long_kernel<float>;
     int resident = 0;
     const cudaError_t e = resident_blocks(reinterpret_cast<const void *>(fn), kLongThreads, device, &resident);
@@ -1003,16 +988,12 @@ cudaError_t launch_norm(NormParams p, int dtype, bool vec, int device, cudaStrea
 
 cudaError_t launch_norm_backward(NormParams p, int dtype, bool vec, int device, cudaStream_t s)
 {
-    const NormPick k = pick_backward(dtype, vec, p.cols);
+    const NormPick k = pick_norm<true>(dtype, vec, p.cols);
     cudaError_t e = cudaSuccess;
     if (p.rows == 0) {
         p.parts = 0;
     } else if (k.fn) {
-        const uint64_t row_bytes = (uint64_t)p.cols * (dtype == DT_BF16 ? 2 : 4), sms = (uint64_t)sm_count(device);
-        p.tpr = k.tpr;
-        p.param_bytes = 0;
-        const NormShape n = norm_shape(p, row_bytes, vec, 2, sms, kNormThreads / k.tpr, k.rows, kSmemBytes);
-        e = launch_rows(k.fn, n, p, s);
+        e = launch_rows(k.fn, norm_shape(p, k, dtype, vec, true, device), p, s);
         p.parts = (uint32_t)std::min<uint64_t>(p.parts, p.chunks);
     } else {
         const bool bf16 = dtype == DT_BF16;

@@ -30,9 +30,9 @@ struct NormParams {
     uint32_t tpr;                      // threads that share a row, a multiple of 32
     uint32_t parts;                    // groups of them that walk over the rows; shares of dw and db
     // rings: chunks of up to chunk_rows rows of one rank (rank r's end at
-    // chunk_end[r]), stages of stage_bytes for each array that is read
-    uint32_t chunk_rows, stages, stage_bytes;
-    uint32_t param_bytes;              // of weights and bias in shared memory, half of it each (0: not there)
+    // chunk_end[r]); a stage holds a chunk of x, and backward of dy, in
+    // array_bytes each, then of mean and rstd in stat_bytes each
+    uint32_t chunk_rows, stages, stage_bytes, array_bytes, stat_bytes;
     uint64_t chunks;
     uint64_t chunk_end[DT_MAX_RANKS];
     int32_t P;
