@@ -21,7 +21,7 @@
 // E[x^2] - mu^2, which loses every digit where |mu| is large.  All sums are
 // fp32, and results are rounded once, at the store.
 //
-// A thread keeps its columns, eight where it can, over all of its rows, and
+// A thread keeps its columns, 8 to 32 of them, over all of its rows, and
 // with them their weights and, backward, their shares of dw and db; up to four
 // rows are summed at a time (4 x 2048 rows of 4096 bf16 took 94 us forward with
 // a ring and one row at a time, 40 with a warp or two to a row and the weights
@@ -154,15 +154,30 @@ __device__ __forceinline__ float param(const void *p, int bf16, uint32_t j, floa
     return bf16 ? bf16_to_f32(static_cast<const uint16_t *>(p)[j]) : static_cast<const float *>(p)[j];
 }
 
-// A thread's weights or biases from element e on.
+// A thread's weights or biases from element e on.  All of them are loaded
+// before the first is converted: one after the other they took 3 us.
 template <typename C, int VEC>
 __device__ __forceinline__ void params(const void *p, int bf16, uint32_t e, float none, typename C::V (&f)[C::K])
 {
-    if constexpr (VEC == 1) {
-        f[0] = param(p, bf16, e, none);
+    float v[VEC];
+    if (!p) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[i] = none;
+    } else if (bf16) {
+        uint16_t u[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) u[i] = static_cast<const uint16_t *>(p)[e + i];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[i] = bf16_to_f32(u[i]);
     } else {
 #pragma unroll
-        for (int i = 0; i < C::K; ++i) f[i] = pair(param(p, bf16, e + 2 * i, none), param(p, bf16, e + 2 * i + 1, none));
+        for (int i = 0; i < VEC; ++i) v[i] = static_cast<const float *>(p)[e + i];
+    }
+    if constexpr (VEC == 1) {
+        f[0] = v[0];
+    } else {
+#pragma unroll
+        for (int i = 0; i < C::K; ++i) f[i] = pair(v[2 * i], v[2 * i + 1]);
     }
 }
 
@@ -330,7 +345,7 @@ struct Ring {
     }
 };
 
-// The group's ring; the waits of the next kernel and for the one before.
+// The group's ring; the waits for the kernel before and of the one after.
 template <typename T, bool BACK>
 __device__ __forceinline__ Ring<T, BACK> make_ring(const NormParams &p, unsigned char *smem, uint32_t group)
 {
@@ -346,8 +361,7 @@ __device__ __forceinline__ Ring<T, BACK> make_ring(const NormParams &p, unsigned
     return Ring<T, BACK>{p, smem_addr(mem), bars + 8 * group * p.stages, mem};
 }
 
-// Its first copies.  They come after the loads of the weights, which would
-// otherwise wait behind 25 MB of rows (6 us).
+// Its first copies.
 template <typename T, bool BACK>
 __device__ __forceinline__ void first_loads(const Ring<T, BACK> &ring, const NormParams &p, uint32_t t, uint64_t part)
 {
@@ -371,11 +385,13 @@ __device__ __forceinline__ void read_row(Chunk<T, VEC> (&c)[N], const NormParams
     }
 }
 
-// Rows that are summed at a time, so that a barrier serves several: as many as
-// fit in registers beside what a thread keeps for its columns.
-__host__ __device__ constexpr int rows_at_once(int elem_bytes, int elems)
+// Rows that are summed at a time, so that a barrier serves several: up to four,
+// as long as they take at most 32 registers of a thread.
+template <typename T, int VEC, int N, bool BACK>
+__host__ __device__ constexpr int rows_at_once()
 {
-    return elem_bytes * elems <= 16 ? 4 : elem_bytes * elems <= 32 ? 2 : 1;
+    constexpr int regs = N * (VEC == 1 ? 1 : 4) * (BACK ? 2 : 1);
+    return regs <= 8 ? 4 : regs <= 16 ? 2 : 1;
 }
 
 // The mean and the sum of squared distances from it, of all warps that share a
@@ -404,7 +420,7 @@ template <typename T, int VEC, int N>
 __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(const __grid_constant__ NormParams p)
 {
     constexpr bool kHold = N * VEC <= 16;   // wider rows read their weights again from L1
-    constexpr int B = rows_at_once(VEC == 1 ? 4 : sizeof(T), N * VEC);
+    constexpr int B = rows_at_once<T, VEC, N, false>();
     using C = Chunk<T, VEC>;
     using V = typename C::V;
     constexpr int K = C::K;
@@ -415,6 +431,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(const __grid_cons
     const uint64_t part = (uint64_t)group * gridDim.x + blockIdx.x;
     Ring<T, false> ring = make_ring<T, false>(p, smem, group);
     DT_TL_WAITED();
+    first_loads(ring, p, t, part);
     const float inv = __fdiv_rn(1.0f, (float)cols);
     uint32_t phase = 0;
     V w[N][K], b[N][K];
@@ -427,7 +444,6 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(const __grid_cons
     if constexpr (kHold)
 #pragma unroll
         for (int n = 0; n < N; ++n) weights(n);
-    first_loads(ring, p, t, part);
 
     for (uint64_t c = part; c < p.chunks; c += p.parts) {
         int r;
@@ -436,8 +452,9 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(const __grid_cons
         ring.chunk(c, r, row, rows);
         const T *src = ring.at(0, static_cast<const T *>(p.x[r]) + row * cols);
         T *y = static_cast<T *>(p.out[r]) + row * cols;
+        float *means = p.mean[r] ? p.mean[r] + row : nullptr, *rstds = p.rstd[r] ? p.rstd[r] + row : nullptr;
         ring.wait();
-        for (uint32_t k = 0; k < rows; k += B, row += B, src += B * cols, y += B * (uint64_t)cols) {
+        for (uint32_t k = 0; k < rows; k += B, src += B * cols, y += B * (uint64_t)cols) {
             // B rows at a time; the last ones of a stage may stand beside rows of zeros
             C x[B][N];
             float s[B], m2[B];
@@ -481,8 +498,8 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(const __grid_cons
 #pragma unroll
             for (int j = 0; j < B; ++j) {
                 if (k + j >= rows) continue;
-                const float rstd = rstd_of(m2[j], cols, p.eps);
-                const V minus = C::all(-s[j]), scale = C::all(rstd);
+                m2[j] = rstd_of(m2[j], cols, p.eps);
+                const V minus = C::all(-s[j]), scale = C::all(m2[j]);
                 T *to = y + j * (uint64_t)cols;
 #pragma unroll
                 for (int n = 0; n < N; ++n) {
@@ -495,10 +512,16 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(const __grid_cons
                     for (int i = 0; i < K; ++i) f[i] = fma(mul(add(f[i], minus), scale), w[n][i], b[n][i]);
                     if (NORM_OK(p.out, 2, r, to + e, VEC * sizeof(T), cols * sizeof(T))) C::store(to + e, f);
                 }
-                if (t == 0) {
-                    if (p.mean[r] && NORM_OK(p.mean, 3, r, p.mean[r] + row + j, 4, 4)) p.mean[r][row + j] = s[j];
-                    if (p.rstd[r] && NORM_OK(p.rstd, 4, r, p.rstd[r] + row + j, 4, 4)) p.rstd[r][row + j] = rstd;
-                }
+            }
+            // one lane to a row, of the group's last warp
+            const uint32_t lane = t - (tpr - 32);
+            if (lane < B && k + lane < rows) {
+                float mean = s[0], rstd = m2[0];
+#pragma unroll
+                for (int j = 1; j < B; ++j)
+                    if (lane == j) mean = s[j], rstd = m2[j];
+                if (means && NORM_OK(p.mean, 3, r, means + k + lane, 4, 4)) means[k + lane] = mean;
+                if (rstds && NORM_OK(p.rstd, 4, r, rstds + k + lane, 4, 4)) rstds[k + lane] = rstd;
             }
         }
         ring.next();
@@ -584,7 +607,7 @@ template <typename T, int VEC, int N>
 __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_kernel(const __grid_constant__ NormParams p)
 {
     constexpr bool kHold = N * VEC <= 16;   // wider rows read their weights again from L1
-    constexpr int B = rows_at_once(VEC == 1 ? 4 : sizeof(T), N * VEC);
+    constexpr int B = rows_at_once<T, VEC, N, true>();
     using C = Chunk<T, VEC>;
     using V = typename C::V;
     constexpr int K = C::K;
@@ -595,6 +618,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_kernel(const __
     const uint64_t part = (uint64_t)group * gridDim.x + blockIdx.x;
     Ring<T, true> ring = make_ring<T, true>(p, smem, group);
     DT_TL_WAITED();
+    first_loads(ring, p, t, part);
     const float inv = __fdiv_rn(1.0f, (float)cols);
     uint32_t phase = 0;
     V dw[N][K], db[N][K], w[N][K];
@@ -608,7 +632,6 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_kernel(const __
         for (int i = 0; i < K; ++i) dw[n][i] = db[n][i] = w[n][i] = C::all(0.0f);
         if constexpr (kHold) weights(n);
     }
-    first_loads(ring, p, t, part);
 
     for (uint64_t c = part; c < p.chunks; c += p.parts) {
         int r;
@@ -848,24 +871,26 @@ __global__ void __launch_bounds__(kThreads) norm_columns_long_kernel(const __gri
 
 using NormFn = void (*)(NormParams);
 
-// The kernel for rows of `cols` elements, either way, and the threads that share
-// a row: eight columns a thread, or as many more as keep a row within 512
-// threads.  Instances stop at 32 columns, where two sums for each no longer
-// fit in registers.
+// The kernel for rows of `cols` elements, either way, and the threads that
+// share a row: 8 columns a thread, or 16 or 32 where that keeps the row within
+// 256 threads, so that two groups or more share an SM and one computes while
+// another waits at its barrier (4096 columns over 512 threads: 39 us forward,
+// over 256: 37).  Past 256 threads of 32 columns a row may have 512; beyond
+// that, a thread's sums for its columns would not fit in registers.
 struct NormPick {
     NormFn fn = nullptr;
     uint32_t tpr = 0, rows = 0;   // rows it sums at a time
 };
 
 template <typename T, int VEC, int N, bool BACK>
-void try_pick(NormPick &k, uint32_t chunks)
+void try_pick(NormPick &k, uint32_t chunks, uint32_t most)
 {
     const uint32_t tpr = ((chunks + N - 1) / N + 31) / 32 * 32;
-    if (k.fn || tpr > kNormThreads) return;
+    if (k.fn || tpr > most) return;
     if constexpr (BACK) k.fn = norm_backward_kernel<T, VEC, N>;
     else k.fn = norm_kernel<T, VEC, N>;
     k.tpr = tpr;
-    k.rows = rows_at_once(VEC == 1 ? 4 : sizeof(T), N * VEC);
+    k.rows = rows_at_once<T, VEC, N, BACK>();
 }
 
 template <typename T, int VEC, bool BACK>
@@ -874,10 +899,13 @@ NormPick pick_norm(uint32_t cols)
     NormPick k;
     const uint32_t chunks = (cols + VEC - 1) / VEC;
     if constexpr (VEC > 1)
-        if (chunks <= 32) try_pick<T, VEC, 1, BACK>(k, chunks);
-    try_pick<T, VEC, 8 / VEC, BACK>(k, chunks);
-    try_pick<T, VEC, 16 / VEC, BACK>(k, chunks);
-    if constexpr (VEC > 1) try_pick<T, VEC, 32 / VEC, BACK>(k, chunks);
+        if (chunks <= 32) try_pick<T, VEC, 1, BACK>(k, chunks, 32);
+    try_pick<T, VEC, 8 / VEC, BACK>(k, chunks, 256);
+    try_pick<T, VEC, 16 / VEC, BACK>(k, chunks, VEC == 1 ? kNormThreads : 256);
+    if constexpr (VEC > 1) {
+        try_pick<T, VEC, 16 / VEC, BACK>(k, chunks, kNormThreads);
+        try_pick<T, VEC, 32 / VEC, BACK>(k, chunks, kNormThreads);
+    }
     return k;
 }
 
