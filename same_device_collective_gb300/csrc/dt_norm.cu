@@ -23,12 +23,11 @@
 //
 // A thread keeps its columns, 8 to 32 of them, over all of its rows, and
 // with them their weights and, backward, their shares of dw and db; up to four
-// rows are summed at a time (4 x 2048 rows of 4096 bf16 took 94 us forward with
-// a ring and one row at a time, 40 with a warp or two to a row and the weights
-// in shared memory, whose reads then bound it, and 00 so).  A second
+// rows are summed at a time.  A second
 // kernel adds the shares in a fixed order, so the result depends on the device
 // and the shapes alone, not on timing.
 #include <algorithm>
+#include <type_traits>
 
 #include "dt_ops.h"
 
@@ -154,24 +153,37 @@ __device__ __forceinline__ float param(const void *p, int bf16, uint32_t j, floa
     return bf16 ? bf16_to_f32(static_cast<const uint16_t *>(p)[j]) : static_cast<const float *>(p)[j];
 }
 
-// A thread's weights or biases from element e on.  All of them are loaded
-// before the first is converted: one after the other they took 3 us.
+// A thread's weights or biases from element e on: whole vectors where they lie
+// on 16-byte boundaries.
 template <typename C, int VEC>
 __device__ __forceinline__ void params(const void *p, int bf16, uint32_t e, float none, typename C::V (&f)[C::K])
 {
     float v[VEC];
+    const bool vec = VEC > 1 && (reinterpret_cast<uint64_t>(p) & 15) == 0;
     if (!p) {
 #pragma unroll
         for (int i = 0; i < VEC; ++i) v[i] = none;
     } else if (bf16) {
-        uint16_t u[VEC];
+        const uint16_t *q = static_cast<const uint16_t *>(p) + e;
+        uint32_t u[VEC > 1 ? VEC / 2 : 1];
+        if (VEC > 1 && vec) {
+            if constexpr (VEC == 8) *reinterpret_cast<uint4 *>(u) = *reinterpret_cast<const uint4 *>(q);
+            if constexpr (VEC == 4) *reinterpret_cast<uint2 *>(u) = *reinterpret_cast<const uint2 *>(q);
+        } else {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) u[i] = static_cast<const uint16_t *>(p)[e + i];
+            for (int i = 0; i < VEC; i += 2) u[i / 2] = q[i] | (VEC > 1 ? (uint32_t)q[i + (VEC > 1)] << 16 : 0u);
+        }
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) v[i] = bf16_to_f32(u[i]);
+        for (int i = 0; i < VEC; ++i) v[i] = i & 1 ? bf16_hi(u[i / 2]) : bf16_lo(u[i / 2]);
     } else {
+        const float *q = static_cast<const float *>(p) + e;
+        if (VEC > 1 && vec) {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) v[i] = static_cast<const float *>(p)[e + i];
+            for (int i = 0; i < VEC / 4; ++i) *reinterpret_cast<float4 *>(v + 4 * i) = *reinterpret_cast<const float4 *>(q + 4 * i);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) v[i] = q[i];
+        }
     }
     if constexpr (VEC == 1) {
         f[0] = v[0];
@@ -181,12 +193,19 @@ __device__ __forceinline__ void params(const void *p, int bf16, uint32_t e, floa
     }
 }
 
-// The rank that row belongs to, and the row's number there.
+// The rank that row belongs to, and the row's number there.  Every bound is a
+// constant operand, so nothing waits for the one before: a search took 700
+// cycles of a row's 6000.
 __device__ __forceinline__ int find_rank(const NormParams &p, uint64_t row, uint64_t &local)
 {
     int r = 0;
     uint64_t begin = 0;
-    while (r + 1 < p.P && row >= p.row_end[r]) begin = p.row_end[r++];
+#pragma unroll
+    for (int k = 0; k + 1 < DT_MAX_RANKS; ++k)
+        if (k + 1 < p.P && row >= p.row_end[k]) {
+            r = k + 1;
+            begin = p.row_end[k];
+        }
     local = row - begin;
     return r;
 }
@@ -361,7 +380,8 @@ __device__ __forceinline__ Ring<T, BACK> make_ring(const NormParams &p, unsigned
     return Ring<T, BACK>{p, smem_addr(mem), bars + 8 * group * p.stages, mem};
 }
 
-// Its first copies.
+// Its first copies.  They come after the weights' loads, which behind 25 MB of
+// rows would take 6 us.
 template <typename T, bool BACK>
 __device__ __forceinline__ void first_loads(const Ring<T, BACK> &ring, const NormParams &p, uint32_t t, uint64_t part)
 {
@@ -431,7 +451,6 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(const __grid_cons
     const uint64_t part = (uint64_t)group * gridDim.x + blockIdx.x;
     Ring<T, false> ring = make_ring<T, false>(p, smem, group);
     DT_TL_WAITED();
-    first_loads(ring, p, t, part);
     const float inv = __fdiv_rn(1.0f, (float)cols);
     uint32_t phase = 0;
     V w[N][K], b[N][K];
@@ -444,6 +463,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(const __grid_cons
     if constexpr (kHold)
 #pragma unroll
         for (int n = 0; n < N; ++n) weights(n);
+    first_loads(ring, p, t, part);
 
     for (uint64_t c = part; c < p.chunks; c += p.parts) {
         int r;
@@ -529,12 +549,40 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(const __grid_cons
     DT_TL_END_BLOCK(DT_TL_NORM);
 }
 
-// One row to a block, for calls of few rows, where only the time from the
-// first load to the last store counts: the row, the weights and the bias are
-// all loaded to registers at once (1 row on each of 4 ranks, 4096 bf16: 0.0 us
-// a call, against 5.3 through a ring and shared memory).
-template <typename T, int VEC, int N>
-__global__ void __launch_bounds__(kNormThreads) norm_few_kernel(const __grid_constant__ NormParams p)
+// How a call's weights and biases are read; the kernel takes it as a constant
+// within its loops, so that loads are not kept apart by branches.
+enum ParamKind { kParamBf16, kParamF32, kParamAny };   // whole vectors of either type, or whatever there is
+
+template <typename C, int VEC, int KIND>
+__device__ __forceinline__ void read_param(const NormParams &p, const void *q, uint32_t e, float none, typename C::V (&f)[C::K])
+{
+    if constexpr (KIND == kParamBf16 && VEC == 8) {
+        const uint4 u = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(q) + e));
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = pair(bf16_lo(w[i]), bf16_hi(w[i]));
+    } else if constexpr (KIND == kParamF32 && VEC > 1) {
+#pragma unroll
+        for (int i = 0; i < C::K; i += 2) {
+            const float4 u = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(q) + e + 2 * i));
+            f[i] = pair(u.x, u.y);
+            f[i + 1] = pair(u.z, u.w);
+        }
+    } else {
+        params<C, VEC>(q, p.weight_bf16, e, none, f);
+    }
+}
+
+// A row in the registers of tpr threads, up to 4 vectors each, and blocks of a
+// few rows that the hardware hands to the SMs as they come free (4 x 2048 rows
+// of 4096 bf16: 31 us, against 37 with the resident blocks and rings above, of
+// which 6 pass before the last SM has its first row and 8 between the first
+// SM's end and the last's).  What bounds it is the time of a row, 3 us, over
+// the eight rows that an SM's registers hold.
+// EARLY: the weights are loaded along with the row, for calls of few rows,
+// where only the time from the first load to the last store counts.
+template <typename T, int VEC, int N, bool EARLY>
+__global__ void __launch_bounds__(EARLY || N < 4 ? kNormThreads : 256, EARLY || N < 4 ? 1 : 4) norm_rows_kernel(const __grid_constant__ NormParams p)
 {
     using C = Chunk<T, VEC>;
     using V = typename C::V;
@@ -542,63 +590,86 @@ __global__ void __launch_bounds__(kNormThreads) norm_few_kernel(const __grid_con
     DT_TL_BEGIN();
     pdl_begin();
     DT_TL_WAITED();
-    const uint32_t tpr = blockDim.x, t = threadIdx.x, cols = p.cols;
-    uint64_t row;
-    const int r = find_rank(p, blockIdx.x, row);
-    const T *src = static_cast<const T *>(p.x[r]) + row * cols;
-    T *y = static_cast<T *>(p.out[r]) + row * cols;
-    V f[N][C::K], w[N][C::K], b[N][C::K];
-    C x[N];
-    uint32_t mine = 0, phase = 0;
+    const uint32_t tpr = p.tpr, group = threadIdx.x / tpr, t = threadIdx.x % tpr, cols = p.cols;
+    const uint64_t at = (uint64_t)blockIdx.x * (blockDim.x / tpr) + group;
+    if (at < p.rows) {
+        uint64_t row;
+        const int r = find_rank(p, at, row);
+        const T *src = static_cast<const T *>(p.x[r]) + row * cols;
+        T *y = static_cast<T *>(p.out[r]) + row * cols;
+        C x[N];
+        V w[EARLY ? N : 1][C::K], b[EARLY ? N : 1][C::K];
+        uint32_t mine = 0, phase = 0;
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-        const uint32_t first = (n * tpr + (t & ~31u)) * VEC, e = (n * tpr + t) * VEC;
-        mine += first < cols ? min(cols - first, 32u * VEC) : 0;
-        if (e < cols && NORM_OK(p.x, 0, r, src + e, VEC * sizeof(T), cols * sizeof(T))) x[n].load(src + e);
-        else x[n].zero();
-    }
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-        const uint32_t e = (n * tpr + t) * VEC;
-        if (e >= cols) continue;
-        params<C, VEC>(p.weight, p.weight_bf16, e, 1.0f, w[n]);
-        params<C, VEC>(p.bias, p.weight_bf16, e, 0.0f, b[n]);
-    }
-    V s = C::all(0.0f), m = C::all(0.0f);
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-        x[n].get(f[n]);
-#pragma unroll
-        for (int i = 0; i < C::K; ++i) s = add(s, f[n][i]);
-    }
-    float sum[1] = {both(s)};
-    warp_sum<1>(sum);
-    float mean = mine ? __fdiv_rn(sum[0], (float)mine) : 0.0f;
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-        if ((n * tpr + t) * VEC >= cols) continue;
-#pragma unroll
-        for (int i = 0; i < C::K; ++i) {
-            const V d = add(f[n][i], C::all(-mean));
-            m = fma(d, d, m);
+        for (int n = 0; n < N; ++n) {
+            const uint32_t first = (n * tpr + (t & ~31u)) * VEC, e = (n * tpr + t) * VEC;
+            mine += first < cols ? min(cols - first, 32u * VEC) : 0;
+            if (e < cols && NORM_OK(p.x, 0, r, src + e, VEC * sizeof(T), cols * sizeof(T))) x[n].load(src + e);
+            else x[n].zero();
         }
-    }
-    float m2[1] = {both(m)};
-    warp_sum<1>(m2);
-    row_moments(sum[0], mean, m2[0], mine, cols, red, phase, tpr, 0);
-    const float rstd = rstd_of(m2[0], cols, p.eps);
+        if constexpr (EARLY)
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-        const uint32_t e = (n * tpr + t) * VEC;
-        if (e >= cols) continue;
+            for (int n = 0; n < N; ++n) {
+                const uint32_t e = (n * tpr + t) * VEC;
+                if (e >= cols) continue;
+                params<C, VEC>(p.weight, p.weight_bf16, e, 1.0f, w[n]);
+                params<C, VEC>(p.bias, p.weight_bf16, e, 0.0f, b[n]);
+            }
+        const float inv_mine = mine ? __fdiv_rn(1.0f, (float)mine) : 0.0f;
+        // four sums, so that an addition does not wait for the one before
+        V s[4] = {C::all(0.0f), C::all(0.0f), C::all(0.0f), C::all(0.0f)}, m[4] = {s[0], s[0], s[0], s[0]};
 #pragma unroll
-        for (int i = 0; i < C::K; ++i)
-            f[n][i] = fma(mul(add(f[n][i], C::all(-mean)), C::all(rstd)), w[n][i], b[n][i]);
-        if (NORM_OK(p.out, 2, r, y + e, VEC * sizeof(T), cols * sizeof(T))) C::store(y + e, f[n]);
-    }
-    if (t == 0) {
-        if (p.mean[r] && NORM_OK(p.mean, 3, r, p.mean[r] + row, 4, 4)) p.mean[r][row] = mean;
-        if (p.rstd[r] && NORM_OK(p.rstd, 4, r, p.rstd[r] + row, 4, 4)) p.rstd[r][row] = rstd;
+        for (int n = 0; n < N; ++n) {
+            V f[C::K];
+            x[n].get(f);
+#pragma unroll
+            for (int i = 0; i < C::K; ++i) s[(n * C::K + i) & 3] = add(s[(n * C::K + i) & 3], f[i]);
+        }
+        float sum[1] = {both(add(add(s[0], s[1]), add(s[2], s[3])))};
+        warp_sum<1>(sum);
+        float mean = sum[0] * inv_mine;
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            if ((n * tpr + t) * VEC >= cols) continue;
+            V f[C::K];
+            x[n].get(f);
+#pragma unroll
+            for (int i = 0; i < C::K; ++i) {
+                const V d = add(f[i], C::all(-mean));
+                m[(n * C::K + i) & 3] = fma(d, d, m[(n * C::K + i) & 3]);
+            }
+        }
+        float m2[1] = {both(add(add(m[0], m[1]), add(m[2], m[3])))};
+        warp_sum<1>(m2);
+        row_moments(sum[0], mean, m2[0], mine, cols, red, phase, tpr, group);
+        const float rstd = rstd_of(m2[0], cols, p.eps);
+        const V minus = C::all(-mean), scale = C::all(rstd);
+        auto finish = [&](auto kind) {
+            constexpr int KIND = decltype(kind)::value;
+            (void)KIND;
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                const uint32_t e = (n * tpr + t) * VEC;
+                if (e >= cols) continue;
+                constexpr int k = EARLY ? 1 : 0;
+                if constexpr (!EARLY) {
+                    read_param<C, VEC, KIND>(p, p.weight, e, 1.0f, w[0]);
+                    read_param<C, VEC, KIND>(p, p.bias, e, 0.0f, b[0]);
+                }
+                V f[C::K];
+                x[n].get(f);
+#pragma unroll
+                for (int i = 0; i < C::K; ++i) f[i] = fma(mul(add(f[i], minus), scale), w[n * k][i], b[n * k][i]);
+                if (NORM_OK(p.out, 2, r, y + e, VEC * sizeof(T), cols * sizeof(T))) C::store(y + e, f);
+            }
+        };
+        if (EARLY || p.param_kind == kParamAny) finish(std::integral_constant<int, kParamAny>());
+        else if (p.param_kind == kParamBf16) finish(std::integral_constant<int, kParamBf16>());
+        else finish(std::integral_constant<int, kParamF32>());
+        if (t == 0) {
+            if (p.mean[r] && NORM_OK(p.mean, 3, r, p.mean[r] + row, 4, 4)) p.mean[r][row] = mean;
+            if (p.rstd[r] && NORM_OK(p.rstd, 4, r, p.rstd[r] + row, 4, 4)) p.rstd[r][row] = rstd;
+        }
     }
     DT_TL_END_BLOCK(DT_TL_NORM);
 }
@@ -618,7 +689,6 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_kernel(const __
     const uint64_t part = (uint64_t)group * gridDim.x + blockIdx.x;
     Ring<T, true> ring = make_ring<T, true>(p, smem, group);
     DT_TL_WAITED();
-    first_loads(ring, p, t, part);
     const float inv = __fdiv_rn(1.0f, (float)cols);
     uint32_t phase = 0;
     V dw[N][K], db[N][K], w[N][K];
@@ -632,6 +702,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_kernel(const __
         for (int i = 0; i < K; ++i) dw[n][i] = db[n][i] = w[n][i] = C::all(0.0f);
         if constexpr (kHold) weights(n);
     }
+    first_loads(ring, p, t, part);
 
     for (uint64_t c = part; c < p.chunks; c += p.parts) {
         int r;
@@ -916,30 +987,37 @@ NormPick pick_norm(int dtype, bool vec, uint32_t cols)
     return vec ? pick_norm<float, 4, BACK>(cols) : pick_norm<float, 1, BACK>(cols);
 }
 
-// The same for one row to a block, which every thread has up to 4 vectors or 8
-// single elements of.
+// The kernel that has a row in registers, and the threads of a row.  Few rows:
+// as many threads as a row has vectors.  Else, for rows of whole vectors, a
+// warp to a row or 4 vectors a thread (16384 bf16 rows of 512: 1, 2, 4 vectors
+// 29, 19, 23 us).
 template <typename T, int VEC>
-NormPick pick_few(uint32_t cols)
+NormPick pick_rows(uint32_t cols, bool few)
 {
     NormPick k;
     const uint32_t chunks = (cols + VEC - 1) / VEC;
-    auto try_few = [&](NormFn fn, uint32_t n) {
+    auto try_rows = [&](NormFn fn, uint32_t n, uint32_t most) {
         const uint32_t tpr = ((chunks + n - 1) / n + 31) / 32 * 32;
-        if (k.fn || tpr > kNormThreads) return;
+        if (k.fn || tpr > most) return;
         k.fn = fn;
         k.tpr = tpr;
     };
-    try_few(norm_few_kernel<T, VEC, 1>, 1);
-    try_few(norm_few_kernel<T, VEC, 2>, 2);
-    try_few(norm_few_kernel<T, VEC, 4>, 4);
-    if constexpr (VEC == 1) try_few(norm_few_kernel<T, VEC, 8>, 8);
+    if (few) {
+        try_rows(norm_rows_kernel<T, VEC, 1, true>, 1, kNormThreads);
+        try_rows(norm_rows_kernel<T, VEC, 2, true>, 2, kNormThreads);
+    }
+    if constexpr (VEC > 1) {
+        try_rows(norm_rows_kernel<T, VEC, 1, false>, 1, 32);
+        try_rows(norm_rows_kernel<T, VEC, 2, false>, 2, 32);
+        try_rows(norm_rows_kernel<T, VEC, 4, false>, 4, 256);
+    }
     return k;
 }
 
-NormPick pick_few(int dtype, bool vec, uint32_t cols)
+NormPick pick_rows(int dtype, bool vec, uint32_t cols, bool few)
 {
-    if (dtype == DT_BF16) return vec ? pick_few<uint16_t, 8>(cols) : pick_few<uint16_t, 1>(cols);
-    return vec ? pick_few<float, 4>(cols) : pick_few<float, 1>(cols);
+    if (dtype == DT_BF16) return vec ? pick_rows<uint16_t, 8>(cols, few) : pick_rows<uint16_t, 1>(cols, few);
+    return vec ? pick_rows<float, 4>(cols, few) : pick_rows<float, 1>(cols, few);
 }
 
 // The grid, the groups and the rings of a call.
@@ -1000,9 +1078,17 @@ size_t norm_workspace(uint32_t cols, int device)
 
 cudaError_t launch_norm(NormParams p, int dtype, bool vec, int device, cudaStream_t s)
 {
-    if (p.rows <= 2 * (uint64_t)sm_count(device)) {
-        const NormPick k = pick_few(dtype, vec, p.cols);
-        if (k.fn) return launch_kernel(k.fn, dim3((unsigned)p.rows), dim3(k.tpr), 0, s, false, p);
+    const bool few = p.rows <= 2 * (uint64_t)sm_count(device);
+    const NormPick rows = pick_rows(dtype, vec, p.cols, few);
+    if (rows.fn) {
+        const uint32_t threads = few ? rows.tpr : std::max(rows.tpr, 256 / rows.tpr * rows.tpr), per = threads / rows.tpr;
+        const uint64_t blocks = (p.rows + per - 1) / per;
+        if (blocks <= 0x7FFFFFFF) {
+            p.tpr = rows.tpr;
+            const bool whole = p.weight && p.bias && ((uintptr_t)p.weight & 15) == 0 && ((uintptr_t)p.bias & 15) == 0;
+            p.param_kind = !vec || !whole ? kParamAny : !p.weight_bf16 ? kParamF32 : dtype == DT_BF16 ? kParamBf16 : kParamAny;
+            return launch_kernel(rows.fn, dim3((unsigned)blocks), dim3(threads), 0, s, false, p);
+        }
     }
     const NormPick k = pick_norm<false>(dtype, vec, p.cols);
     if (k.fn) return launch_rows(k.fn, norm_shape(p, k, dtype, vec, false, device), p, s);

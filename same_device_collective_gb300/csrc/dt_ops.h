@@ -37,6 +37,7 @@ struct NormParams {
     uint64_t chunk_end[DT_MAX_RANKS];
     int32_t P;
     int32_t weight_bf16;               // of both
+    int32_t param_kind;                // how the forward kernel reads them
     float eps;
     float avg_scale;
     int32_t avg;                       // 0: sum; 1: divide the gradients by P
