@@ -362,6 +362,15 @@ struct Ring {
     {
         if (++s == p.stages) s = 0, parity ^= 1;
     }
+    // Before the block goes on after a wait that ran out, a last, bounded wait
+    // for what is still under way: each stage's last copy of group `part`.
+    __device__ __forceinline__ void drain(uint32_t t, uint64_t part) const
+    {
+        if (!late || t != 0) return;
+        const uint64_t n = (p.chunks - part + p.parts - 1) / p.parts;
+        for (uint32_t k = 0; k < p.stages && k < n; ++k)
+            mbar_wait_bounded(bars + 8 * k, (uint32_t)((n - k + p.stages - 1) / p.stages - 1) & 1, p.sink.timeout_ns);
+    }
 };
 
 // The group's ring; the waits for the kernel before and of the one after.
@@ -546,6 +555,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(const __grid_cons
         }
         ring.next();
     }
+    ring.drain(t, part);
     DT_TL_END_BLOCK(DT_TL_NORM);
 }
 
@@ -779,23 +789,29 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_kernel(const __
         }
         ring.next();
     }
-    if (p.partial && part < p.chunks) {
-        float *out = p.partial + part * 2 * cols;
+    ring.drain(t, part);
+    if (p.partial) {
+        // the groups' shares are added in the rings' place, in ascending order
+        __syncthreads();
+        float *all = reinterpret_cast<float *>(smem);
+        const uint32_t groups = blockDim.x / tpr;
+        for (uint32_t k = 0; k < groups; ++k) {
+            if (group == k)
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-            const uint32_t e = (n * tpr + t) * VEC;
-            if (e >= cols) continue;
-            if constexpr (VEC == 1) {
-                out[e] = dw[n][0];
-                out[cols + e] = db[n][0];
-            } else {
+                for (int n = 0; n < N; ++n) {
+                    const uint32_t e = (n * tpr + t) * VEC;
+                    if (e >= cols) continue;
 #pragma unroll
-                for (int i = 0; i < K; ++i) {   // cols is even here
-                    *reinterpret_cast<uint64_t *>(out + e + 2 * i) = dw[n][i].v;
-                    *reinterpret_cast<uint64_t *>(out + cols + e + 2 * i) = db[n][i].v;
+                    for (int i = 0; i < K; ++i) {   // cols is even where there are pairs
+                        V *w0 = reinterpret_cast<V *>(all + e) + i, *b0 = reinterpret_cast<V *>(all + cols + e) + i;
+                        *w0 = k ? add(*w0, dw[n][i]) : dw[n][i];
+                        *b0 = k ? add(*b0, db[n][i]) : db[n][i];
+                    }
                 }
-            }
+            __syncthreads();
         }
+        float *out = p.partial + (uint64_t)blockIdx.x * 2 * cols;
+        for (uint32_t e = threadIdx.x; e < 2 * cols; e += blockDim.x) out[e] = all[e];
     }
     DT_TL_END_BLOCK(DT_TL_NORM);
 }
@@ -813,7 +829,7 @@ __global__ void __launch_bounds__(kJoinCols *kJoinSlices) norm_join_kernel(const
     float v = 0.0f;
     if (col < p.cols) {
         const float *in = p.partial + blockIdx.y * (uint64_t)p.cols + col;
-#pragma unroll 4
+#pragma unroll 10
         for (uint32_t k = s; k < p.parts; k += kJoinSlices) v += in[(uint64_t)k * 2 * p.cols];
     }
     sum[s][c] = v;
@@ -1049,7 +1065,8 @@ NormShape norm_shape(NormParams &p, const NormPick &k, int dtype, bool vec, bool
     p.stage_bytes = back ? 2 * (p.array_bytes + p.stat_bytes) : p.array_bytes;
     const uint64_t depth = (p.chunks + p.parts - 1) / p.parts;
     p.stages = (uint32_t)std::max<uint64_t>(1, std::min({(uint64_t)kMaxStages, kSmemBytes / (groups * p.stage_bytes), depth}));
-    return {(uint32_t)grid, (uint32_t)(groups * p.tpr), groups * p.stages * (p.stage_bytes + 8)};
+    const size_t rings = groups * p.stages * (p.stage_bytes + 8), sums = back ? 2 * (size_t)p.cols * sizeof(float) : 0;
+    return {(uint32_t)grid, (uint32_t)(groups * p.tpr), std::max(rings, sums)};
 }
 
 cudaError_t launch_rows(NormFn fn, const NormShape &n, const NormParams &p, cudaStream_t s)
@@ -1068,12 +1085,8 @@ DT_TL_BINDER(bind_timeline_norm)
 
 size_t norm_workspace(uint32_t cols, int device)
 {
-    // a thread has at least 8 columns, or a warp the row: shares of that many groups
-    uint32_t tpr = (cols + 31) / 32;
-    tpr = tpr < 32 ? 32 : (tpr + 31) / 32 * 32;
-    const uint64_t groups = tpr >= kNormThreads ? 1 : kNormThreads / tpr;
-    const uint64_t parts = (uint64_t)sm_count(device) * groups;
-    return (size_t)((parts > kLongSlices ? parts : kLongSlices) * 2 * cols * sizeof(float));
+    // a share to a block, or to a slice of rows that are too long for that
+    return (size_t)std::max(sm_count(device), kLongSlices) * 2 * cols * sizeof(float);
 }
 
 cudaError_t launch_norm(NormParams p, int dtype, bool vec, int device, cudaStream_t s)
@@ -1107,8 +1120,9 @@ cudaError_t launch_norm_backward(NormParams p, int dtype, bool vec, int device, 
     if (p.rows == 0) {
         p.parts = 0;
     } else if (k.fn) {
-        e = launch_rows(k.fn, norm_shape(p, k, dtype, vec, true, device), p, s);
-        p.parts = (uint32_t)std::min<uint64_t>(p.parts, p.chunks);
+        const NormShape n = norm_shape(p, k, dtype, vec, true, device);
+        e = launch_rows(k.fn, n, p, s);
+        p.parts = n.grid;   // a share to a block
     } else {
         const bool bf16 = dtype == DT_BF16;
         if (p.partial) {

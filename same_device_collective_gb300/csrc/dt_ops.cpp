@@ -290,29 +290,26 @@ cudaError_t vocab_logit_maps(dt_group *g, const void *hidden, const void *const 
     return vocab_maps(g, hidden, weight, workspace, v, p, rows_h, v.bn / (v.pairs ? 2 : 1));
 }
 
-// Where rows have to be laid out again, the hidden rows are, now, and `pack`
-// is prepared for the vocabulary's.
-cudaError_t vocab_operands(dt_group *g, const void *hidden, const void *const *weight, void *workspace,
-                           const VocabPlan &v, dt::VocabParams &p, dt::VocabPack &pack, cudaStream_t s)
+// Where rows have to be laid out again: what the pieces' launches share.  The
+// first one does the hidden rows too.
+void vocab_prepare_pack(dt_group *g, const void *hidden, const void *const *weight, void *workspace, const VocabPlan &v,
+                        const dt::VocabParams &p, dt::VocabPack &pack)
 {
-    if (!v.packed) return cudaSuccess;
+    if (!v.packed) return;
     unsigned char *ws = static_cast<unsigned char *>(workspace);
     memset(&pack, 0, sizeof pack);
-    pack.src[0] = static_cast<const uint16_t *>(hidden);
-    pack.dst = reinterpret_cast<uint16_t *>(ws + v.pack_h);
-    pack.rows = p.tokens;
-    pack.dim = p.dim;
-    pack.pitch = v.pitch;
-    pack.sink = p.sink;
-    const cudaError_t e = dt::launch_vocab_pack(pack, g->device, s);
     for (int r = 0; r < g->P; ++r) {
         pack.src[r] = static_cast<const uint16_t *>(weight[r]);
         pack.src_rows[r] = p.rows[r];
         pack.unit_end[r] = p.unit_end[r];
     }
+    pack.hidden = static_cast<const uint16_t *>(hidden);
+    pack.hidden_dst = reinterpret_cast<uint16_t *>(ws + v.pack_h);
     pack.dst = reinterpret_cast<uint16_t *>(ws + v.pack_w);
     pack.P = g->P;
-    return e;
+    pack.dim = p.dim;
+    pack.pitch = v.pitch;
+    pack.sink = p.sink;
 }
 
 // The piece's first unit and, where needed, its rows laid out again.
@@ -323,6 +320,7 @@ cudaError_t vocab_piece(dt_group *g, const VocabPlan &v, uint32_t piece, dt::Voc
     *units = std::min(v.piece, v.units - p.unit0);
     if (!v.packed) return cudaSuccess;
     pack.unit0 = p.unit0;
+    pack.tokens = piece == 0 ? p.tokens : 0;
     pack.rows = *units * dt::kVocabUnit;
     return dt::launch_vocab_pack(pack, g->device, s);
 }
@@ -469,8 +467,8 @@ dt_status dt_vocab_loss(dt_group_t g, const void *hidden, const void *const *wei
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (tokens == 0) return loss ? cuda_status(cudaMemsetAsync(loss, 0, 4, s)) : DT_OK;
 
-    cudaError_t e = vocab_operands(g, hidden, weight, workspace, v, p, pack, s);
-    if (e == cudaSuccess) e = vocab_logit_maps(g, hidden, weight, workspace, v, p);
+    vocab_prepare_pack(g, hidden, weight, workspace, v, p, pack);
+    cudaError_t e = vocab_logit_maps(g, hidden, weight, workspace, v, p);
     for (uint32_t k = 0; k < v.pieces && e == cudaSuccess; ++k) {
         uint32_t units = 0;
         e = vocab_piece(g, v, k, p, pack, &units, s);
@@ -521,6 +519,7 @@ dt_status dt_vocab_loss_backward(dt_group_t g, const void *hidden, const void *c
     b.read(lse, tokens * 4);
     b.read(grad_loss, 4);
     b.write(dhidden, tokens * dim * 2);
+    p.dh_vec = dim % 4 == 0 && multiple(dhidden, 8);
     p.dw_align = dim % 8 == 0 ? 8 : dim % 4 == 0 ? 4 : dim % 2 == 0 ? 2 : 1;
     for (int r = 0; r < g->P; ++r) {
         if (p.rows[r] == 0) continue;
@@ -530,7 +529,6 @@ dt_status dt_vocab_loss_backward(dt_group_t g, const void *hidden, const void *c
         b.write(dweight[r], v.rows[r] * dim * 2);
     }
     if (b.clash()) return DT_ERR_INVALID;
-    p.dh_vec = dim % 4 == 0 && multiple(dhidden, 8);
     p.dh = static_cast<uint16_t *>(dhidden);
     p.lse = lse;
     p.grad = grad_loss;
@@ -544,10 +542,10 @@ dt_status dt_vocab_loss_backward(dt_group_t g, const void *hidden, const void *c
         return cuda_status(e);
     }
 
-    e = vocab_operands(g, hidden, weight, workspace, v, p, pack, s);
+    vocab_prepare_pack(g, hidden, weight, workspace, v, p, pack);
     // few tokens: boxes of as many as there are, in whole K steps of 16
     p.rows_g = v.pairs ? 128 : (uint32_t)up(p.tokens, 16);
-    if (e == cudaSuccess) e = dt::vocab_map(&p.g, p.gbuf, p.gpitch, p.tokens, p.gpitch, p.rows_g);
+    e = dt::vocab_map(&p.g, p.gbuf, p.gpitch, p.tokens, p.gpitch, p.rows_g);
     for (uint32_t k = 0; k < v.pieces && e == cudaSuccess; ++k) {
         uint32_t units = 0;
         e = vocab_logit_maps(g, hidden, weight, workspace, v, p);

@@ -28,7 +28,7 @@ struct NormParams {
     uint64_t rows;
     uint32_t cols;
     uint32_t tpr;                      // threads that share a row, a multiple of 32
-    uint32_t parts;                    // groups of them that walk over the rows; shares of dw and db
+    uint32_t parts;                    // groups of them that walk over the rows; to the join, shares of dw and db
     // rings: chunks of up to chunk_rows rows of one rank (rank r's end at
     // chunk_end[r]); a stage holds a chunk of x, and backward of dy, in
     // array_bytes each, then of mean and rstd in stat_bytes each

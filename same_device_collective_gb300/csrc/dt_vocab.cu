@@ -267,30 +267,36 @@ __device__ __forceinline__ void store_rows(const VocabParams &p, const unsigned 
 }
 
 // The same for rows of an odd width, every other one of which starts between
-// two words: a lane's word is then made of its neighbour's halves, and the
-// row's first and last elements go by themselves.
+// two words: a lane's word is then made of its neighbour's halves.  The first
+// element of such a row, and a last one that no word takes, go afterwards, a
+// row to a lane.
 __device__ __forceinline__ void store_rows_odd(const VocabParams &p, const unsigned char *buf, uint16_t *out,
                                                uint64_t pitch, uint32_t rows, uint32_t cols, const void *lo,
                                                uint64_t bytes, int buffer)
 {
     (void)p, (void)lo, (void)bytes, (void)buffer;
     const uint32_t lane = threadIdx.x & 31;
+    const uint32_t odd0 = (uint32_t)(reinterpret_cast<uintptr_t>(out) >> 1) & 1, odd_step = (uint32_t)pitch & 1;
+    uint16_t *at = out + 2 * lane;
+    uint32_t odd = odd0;
 #pragma unroll 8
-    for (uint32_t row = 0; row < 32; ++row) {
+    for (uint32_t row = 0; row < 32; ++row, at += pitch, odd ^= odd_step) {
         const uint32_t w = *reinterpret_cast<const uint32_t *>(buf + row * 128 + ((((lane >> 2) ^ row) & 7) << 4) +
                                                                (lane & 3) * 4);
         const uint32_t next = __shfl_down_sync(0xFFFFFFFFu, w, 1);
-        if (row >= rows) continue;
-        uint16_t *at = out + row * pitch;
-        const uint32_t odd = (reinterpret_cast<uintptr_t>(at) >> 1) & 1, e = 2 * lane + odd;
-        const uint32_t v = odd ? __funnelshift_r(w, next, 16) : w;
-        if (e + 1 < cols) {
-            if (VOCAB_OK(at + e, 4, lo, bytes, buffer)) *reinterpret_cast<uint32_t *>(at + e) = v;
-        } else if (e < cols) {
-            if (VOCAB_OK(at + e, 2, lo, bytes, buffer)) at[e] = (uint16_t)v;
-        }
-        if (odd && lane == 0 && VOCAB_OK(at, 2, lo, bytes, buffer)) at[0] = (uint16_t)w;
+        uint16_t *to = at + odd;
+        if (row < rows && 2 * lane + odd + 1 < cols && VOCAB_OK(to, 4, lo, bytes, buffer))
+            *reinterpret_cast<uint32_t *>(to) = odd ? __funnelshift_r(w, next, 16) : w;
     }
+    if (lane >= rows) return;
+    auto element = [&](uint32_t e) {
+        const uint16_t v = *reinterpret_cast<const uint16_t *>(buf + lane * 128 + ((((e >> 3) ^ lane) & 7) << 4) + (e & 7) * 2);
+        uint16_t *to = out + lane * pitch + e;
+        if (VOCAB_OK(to, 2, lo, bytes, buffer)) *to = v;
+    };
+    odd = odd0 ^ (odd_step & lane);
+    if (odd) element(0);
+    if ((cols - odd) & 1) element(cols - 1);
 }
 
 // 64 columns of bf16, packed two to a word: this thread's row into `buf`,
@@ -390,11 +396,11 @@ vocab_kernel(const __grid_constant__ VocabParams p)
     else __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    Tile t;
     pdl_begin();
     DT_TL_WAITED();
     const Waits wait{p.sink, gave_up};
     const uint32_t a_box = a_box_bytes(MODE == kBack, p.rows_h), stage_bytes = 2 * a_box + p.bn / CG * 256;
-    Tile t;
 
     if (warp == kFinishWarps) {
         if (lane == 0) {
@@ -485,32 +491,53 @@ vocab_kernel(const __grid_constant__ VocabParams p)
             const uint32_t acc = tmem + (i & 1) * 256 + ((warp & 3) * 32 << 16);
             const uint32_t quad = half * kM + (warp & 3) * 32;   // first of this warp's rows in the tile
             const uint32_t row0 = t.m0 + quad, row = row0 + lane;
+            // what does not depend on the accumulator, before the wait for it
+            int32_t target = p.ignore;
+            float lse2 = 0.0f;
+            if (MODE != kBack && row < p.tokens) {
+                target = p.targets[row];
+                if (MODE == kGrad) lse2 = p.lse[row] * kLog2e;
+            }
             const bool ok = wait(acc_full + 8 * (i & 1), (i >> 1) & 1);
             if (__any_sync(0xFFFFFFFFu, !ok)) break;
             tc_fence_after();
 
             if (MODE != kBack) {
                 const uint32_t valid = rows_left(p, t.r, t.vrow, p.bn);
-                const int32_t target = row < p.tokens ? p.targets[row] : p.ignore;
                 // the column of this row's target in the tile, if it is there
                 const int64_t at = (int64_t)target - (int64_t)(p.first[t.r] + t.vrow);
                 const bool here = target != p.ignore && target >= 0 && at >= (int64_t)c0 && at < (int64_t)min(c1, valid);
                 if (MODE == kLse) {
-                    float top = -INFINITY, sum = 0.0f;
+                    // four running values each, so that none waits for the one before
+                    float tops[4], sums[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (uint32_t j = 0; j < 4; ++j) tops[j] = -INFINITY;
                     for (uint32_t c = c0; c < c1; c += 32) {
                         float v[32];
                         tmem_load32(acc + c, v);
+                        if (c + 32 <= valid) {
 #pragma unroll
-                        for (uint32_t j = 0; j < 32; ++j) top = fmaxf(top, c + j < valid ? v[j] : -INFINITY);
+                            for (uint32_t j = 0; j < 32; ++j) tops[j & 3] = fmaxf(tops[j & 3], v[j]);
+                        } else {
+#pragma unroll
+                            for (uint32_t j = 0; j < 32; ++j) tops[j & 3] = fmaxf(tops[j & 3], c + j < valid ? v[j] : -INFINITY);
+                        }
                     }
+                    const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
                     const float top2 = top == -INFINITY ? 0.0f : top * kLog2e;   // no 0 times infinity where all are -inf
                     for (uint32_t c = c0; c < c1; c += 32) {
                         float v[32];
                         tmem_load32(acc + c, v);
+                        if (c + 32 <= valid) {
 #pragma unroll
-                        for (uint32_t j = 0; j < 32; ++j)
-                            if (c + j < valid) sum += exp2_fast(fmaf(v[j], kLog2e, -top2));
+                            for (uint32_t j = 0; j < 32; ++j) sums[j & 3] += exp2_fast(fmaf(v[j], kLog2e, -top2));
+                        } else {
+#pragma unroll
+                            for (uint32_t j = 0; j < 32; ++j)
+                                if (c + j < valid) sums[j & 3] += exp2_fast(fmaf(v[j], kLog2e, -top2));
+                        }
                     }
+                    const float sum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
                     // few rows have their target here: one column read for each
                     float logit = 0.0f;
                     for (uint32_t rest = __ballot_sync(0xFFFFFFFFu, here); rest; rest &= rest - 1) {
@@ -526,31 +553,37 @@ vocab_kernel(const __grid_constant__ VocabParams p)
                     }
                 } else {
                     const bool keep = row < p.tokens && target != p.ignore && target >= 0 && (uint32_t)target < p.vocab;
-                    const float lse2 = keep ? p.lse[row] * kLog2e : 0.0f;
                     const uint32_t col = here ? (uint32_t)at : 0xFFFFFFFFu;
                     const uint32_t rows = row0 < p.tokens ? min(p.tokens - row0, 32u) : 0;
+                    const uint32_t mask = keep ? 0xFFFFFFFFu : 0u;   // of a row's results, two at a time
                     for (uint32_t c = c0; c < c1; c += 64) {
                         uint32_t w[32];
+                        // most steps have every column there and no row's target
+                        const bool plain = c + 64 <= valid && !__any_sync(0xFFFFFFFFu, col - c < 64);
 #pragma unroll
                         for (uint32_t q = 0; q < 2; ++q) {
                             float v[32];
                             tmem_load32(acc + c + 32 * q, v);
 #pragma unroll
-                            for (uint32_t j = 0; j < 32; ++j) {
-                                const uint32_t e = c + 32 * q + j;
-                                float x = exp2_fast(fmaf(v[j], kLog2e, -lse2));
-                                if (e == col) x -= 1.0f;
-                                v[j] = keep && e < valid ? x : 0.0f;
+                            for (uint32_t j = 0; j < 32; ++j) v[j] = exp2_fast(fmaf(v[j], kLog2e, -lse2));
+                            if (!plain) {
+#pragma unroll
+                                for (uint32_t j = 0; j < 32; ++j) {
+                                    const uint32_t e = c + 32 * q + j;
+                                    if (e == col) v[j] -= 1.0f;
+                                    v[j] = e < valid ? v[j] : 0.0f;
+                                }
                             }
 #pragma unroll
-                            for (uint32_t j = 0; j < 16; ++j) w[16 * q + j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+                            for (uint32_t j = 0; j < 16; ++j) w[16 * q + j] = pack_bf16x2(v[2 * j], v[2 * j + 1]) & mask;
                         }
                         store_rows_bf16(p, buf, w, p.gbuf + (uint64_t)row0 * p.gpitch + t.n0 + c, p.gpitch, rows, 64, 8,
                                          p.gbuf, (uint64_t)p.tokens * p.gpitch * 2, 0);
                     }
                 }
             } else if (!t.dw) {
-                // fp32 sums: 32 columns a step, four to a thread on the way out
+                // fp32 sums: 32 columns a step, through shared memory so that
+                // eight threads take a row's line
                 const uint32_t rows = row0 < p.tokens ? min(p.tokens - row0, 32u) : 0;
                 float *part = p.acc + ((uint64_t)t.split * p.tokens + row0) * p.apitch + t.n0;
                 for (uint32_t c = c0; c < c1 && t.n0 + c < p.dim; c += 32) {
@@ -563,34 +596,42 @@ vocab_kernel(const __grid_constant__ VocabParams p)
                             make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
                                        __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3]));
                     __syncwarp();
-                    const uint32_t q = lane & 7, e = t.n0 + c + 4 * q;
+                    const uint32_t q = lane & 7, first = lane >> 3, e = t.n0 + c + 4 * q;
                     if (e >= p.dim) continue;
-#pragma unroll 4
-                    for (uint32_t k = lane >> 3; k < rows; k += 4) {
-                        const uint4 u = *out_chunk(buf, k, q);
-                        float4 f = make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z),
-                                               __uint_as_float(u.w));
-                        float4 *at = reinterpret_cast<float4 *>(part + (uint64_t)k * p.apitch + c + 4 * q);
-                        if (p.acc_in) {
-                            const float4 o = *at;
-                            f.x += o.x, f.y += o.y, f.z += o.z, f.w += o.w;
-                        }
-                        if (!p.final) {
-                            *at = f;
-                            continue;
-                        }
-                        uint16_t *to = p.dh + (uint64_t)(row0 + k) * p.dim + e;
-                        const uint64_t all = (uint64_t)p.tokens * p.dim * 2;
-                        (void)all;
-                        const uint2 h = make_uint2(pack_bf16x2(f.x * scale, f.y * scale),
-                                                   pack_bf16x2(f.z * scale, f.w * scale));
+                    float4 f[8];   // rows first, first + 4, ... of the warp's 32
+#pragma unroll
+                    for (uint32_t k = 0; k < 8; ++k) f[k] = *reinterpret_cast<const float4 *>(out_chunk(buf, first + 4 * k, q));
+                    float4 *at = reinterpret_cast<float4 *>(part + (uint64_t)first * p.apitch + c + 4 * q);
+                    if (p.acc_in) {
+#pragma unroll
+                        for (uint32_t k = 0; k < 8; ++k)
+                            if (first + 4 * k < rows) {
+                                const float4 o = at[(uint64_t)k * p.apitch];
+                                f[k].x += o.x, f[k].y += o.y, f[k].z += o.z, f[k].w += o.w;
+                            }
+                    }
+                    if (!p.final) {
+#pragma unroll
+                        for (uint32_t k = 0; k < 8; ++k)
+                            if (first + 4 * k < rows) at[(uint64_t)k * p.apitch] = f[k];
+                        continue;
+                    }
+                    const uint64_t all = (uint64_t)p.tokens * p.dim * 2;
+                    (void)all;
+#pragma unroll
+                    for (uint32_t k = 0; k < 8; ++k) {
+                        if (first + 4 * k >= rows) continue;
+                        uint16_t *to = p.dh + (uint64_t)(row0 + first + 4 * k) * p.dim + e;
+                        const uint2 h = make_uint2(pack_bf16x2(f[k].x * scale, f[k].y * scale),
+                                                   pack_bf16x2(f[k].z * scale, f[k].w * scale));
                         if (p.dh_vec) {
                             if (VOCAB_OK(to, 8, p.dh, all, 1)) *reinterpret_cast<uint2 *>(to) = h;
                         } else {
                             const uint16_t x[4] = {(uint16_t)h.x, (uint16_t)(h.x >> 16), (uint16_t)h.y,
                                                    (uint16_t)(h.y >> 16)};
-                            for (uint32_t j = 0; j < 4 && e + j < p.dim; ++j)
-                                if (VOCAB_OK(to + j, 2, p.dh, all, 1)) to[j] = x[j];
+#pragma unroll
+                            for (uint32_t j = 0; j < 4; ++j)
+                                if (e + j < p.dim && VOCAB_OK(to + j, 2, p.dh, all, 1)) to[j] = x[j];
                         }
                     }
                 }
@@ -647,6 +688,13 @@ __global__ void __launch_bounds__(kTokens *kSlices) vocab_finish_kernel(const __
     // (m, x) and (top, sum), both relative to their own maximum, into one.  No
     // mass is left of minus infinities, but a NaN in a sum stays.
     auto scaled = [](float m, float x, float most) { return x * (m == -INFINITY ? 0.0f : exp2_fast((m - most) * kLog2e)); };
+    const uint32_t t = blockIdx.x * kTokens + warp;   // the token that this warp finishes
+    int32_t target = p.ignore;
+    float logit = 0.0f;
+    if (t < p.tokens) {
+        target = p.targets[t];
+        logit = p.logit[t];   // nobody's where the target is not in the vocabulary: not used then
+    }
     float top = -INFINITY, sum = 0.0f;
     const uint32_t column = blockIdx.x * kTokens + lane;
     if (column < p.tokens) {
@@ -667,16 +715,14 @@ __global__ void __launch_bounds__(kTokens *kSlices) vocab_finish_kernel(const __
     sum = scaled(v.x, v.y, most);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    const uint32_t t = blockIdx.x * kTokens + warp;
     if (lane == 0) {
         float loss = 0.0f;
         uint32_t kept = 0;
         if (t < p.tokens) {
             const float lse = most + logf(sum);
-            const int32_t target = p.targets[t];
             if (target != p.ignore) {
                 if (target >= 0 && (uint32_t)target < p.vocab) {
-                    loss = lse - p.logit[t];
+                    loss = lse - logit;
                     kept = 1;
                 } else {
                     record_error(p.sink, DT_ERR_INVALID, -1, (int)t, target);
@@ -722,62 +768,104 @@ __global__ void __launch_bounds__(kTokens *kSlices) vocab_finish_kernel(const __
     DT_TL_END_BLOCK(DT_TL_VOCAB);
 }
 
-// dh = s * (the sum of the splits), four elements a thread.
+// dh = s * (the sum of the splits), four elements a thread, 16 splits' loads
+// under way at a time.
 __global__ void __launch_bounds__(kThreads) vocab_join_kernel(const __grid_constant__ VocabParams p)
 {
     DT_TL_BEGIN();
     pdl_begin();
     DT_TL_WAITED();
-    const float scale = *p.scale;
     const uint32_t quads = p.apitch / 4;
     const uint64_t all = (uint64_t)p.tokens * quads, step = (uint64_t)gridDim.x * kThreads;
     for (uint64_t i = (uint64_t)blockIdx.x * kThreads + threadIdx.x; i < all; i += step) {
-        const uint32_t row = (uint32_t)(i / quads), e = (uint32_t)(i % quads) * 4;
+        const float scale = *p.scale;
+        const float4 *from = reinterpret_cast<const float4 *>(p.acc) + i;   // rows of quads, one split after the other
         float4 f = make_float4(0, 0, 0, 0);
-#pragma unroll 8
-        for (uint32_t k = 0; k < p.splits; ++k) {
-            const float4 o = *reinterpret_cast<const float4 *>(p.acc + ((uint64_t)k * p.tokens + row) * p.apitch + e);
-            f.x += o.x, f.y += o.y, f.z += o.z, f.w += o.w;
+        for (uint32_t k = 0; k < p.splits; k += 16) {
+            float4 o[16];
+#pragma unroll
+            for (uint32_t j = 0; j < 16; ++j) o[j] = k + j < p.splits ? from[(k + j) * all] : make_float4(0, 0, 0, 0);
+#pragma unroll
+            for (uint32_t j = 0; j < 16; ++j) f.x += o[j].x, f.y += o[j].y, f.z += o[j].z, f.w += o[j].w;
         }
         const float v[4] = {f.x * scale, f.y * scale, f.z * scale, f.w * scale};
+        const uint32_t row = (uint32_t)(i / quads), e = (uint32_t)(i - (uint64_t)row * quads) * 4;
         uint16_t *to = p.dh + (uint64_t)row * p.dim + e;
-        for (uint32_t j = 0; j < 4 && e + j < p.dim; ++j)
-            if (VOCAB_OK(to + j, 2, p.dh, (uint64_t)p.tokens * p.dim * 2, 1)) to[j] = f32_to_bf16(v[j]);
+        if (p.dh_vec) {
+            if (VOCAB_OK(to, 8, p.dh, (uint64_t)p.tokens * p.dim * 2, 1))
+                *reinterpret_cast<uint2 *>(to) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+        } else {
+            for (uint32_t j = 0; j < 4 && e + j < p.dim; ++j)
+                if (VOCAB_OK(to + j, 2, p.dh, (uint64_t)p.tokens * p.dim * 2, 1)) to[j] = f32_to_bf16(v[j]);
+        }
     }
     DT_TL_END_BLOCK(DT_TL_VOCAB);
 }
 
 // Rows that TMA cannot address (a width that is not a multiple of 8, or a
-// buffer off a 16-byte boundary), laid out again: `rows` rows at a pitch of
-// whole vectors.  Source rows are the vocabulary units [unit0, ...) or, with
-// P = 0, the one matrix src[0].  Rows past a rank's last are zeros.
+// buffer off a 16-byte boundary), laid out again at a pitch of whole vectors:
+// the hidden rows (`tokens` of them, in the call's first launch, else 0), then
+// the vocabulary units [unit0, ...), whose rows past a rank's last are zeros.
+// A warp takes a row; a lane makes a vector from the two aligned ones that its
+// elements lie in, neither of which reaches past the 16-byte block of an
+// element of its row.
 __global__ void __launch_bounds__(kThreads) vocab_pack_kernel(const __grid_constant__ VocabPack p)
 {
     DT_TL_BEGIN();
     pdl_begin();
     DT_TL_WAITED();
-    const uint32_t vecs = p.pitch / 8;
-    const uint64_t all = (uint64_t)p.rows * vecs, step = (uint64_t)gridDim.x * kThreads;
-    for (uint64_t i = (uint64_t)blockIdx.x * kThreads + threadIdx.x; i < all; i += step) {
-        const uint32_t row = (uint32_t)(i / vecs), e = (uint32_t)(i % vecs) * 8;
-        int r = 0;
-        uint32_t at = row, have = p.rows;
-        if (p.P) {
+    const uint32_t vecs = p.pitch / 8, lane = threadIdx.x & 31, step = gridDim.x * (kThreads / 32);
+    for (uint32_t i = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); i < p.tokens + p.rows; i += step) {
+        const bool h = i < p.tokens;
+        const uint32_t row = h ? i : i - p.tokens;
+        const uint16_t *base = p.hidden;
+        uint32_t at = row, have = p.tokens;
+        int r = -1;
+        if (!h) {
             const uint32_t unit = p.unit0 + row / kVocabUnit;
             uint32_t begin = 0;
-            while (r + 1 < p.P && unit >= p.unit_end[r]) begin = p.unit_end[r++];
+            r = 0;
+#pragma unroll
+            for (int q = 0; q + 1 < DT_MAX_RANKS; ++q)
+                if (q + 1 < p.P && unit >= p.unit_end[q]) {
+                    r = q + 1;
+                    begin = p.unit_end[q];
+                }
             at = (unit - begin) * kVocabUnit + row % kVocabUnit;
             have = p.src_rows[r];
+            base = p.src[r];
         }
-        uint32_t w[4] = {0, 0, 0, 0};
-        if (at < have) {
-            const uint16_t *src = p.src[r] + (uint64_t)at * p.dim + e;
+        uint4 *dst = reinterpret_cast<uint4 *>(h ? p.hidden_dst : p.dst) + (uint64_t)row * vecs;
+        if (at >= have) {
+            for (uint32_t k = lane; k < vecs; k += 32) dst[k] = make_uint4(0, 0, 0, 0);
+            continue;
+        }
+        const uint16_t *src = base + (uint64_t)at * p.dim;
+        const uint32_t off = (uint32_t)reinterpret_cast<uintptr_t>(src) & 15, words = off / 4, bits = off % 4 * 8;
+        const uint4 *blocks = reinterpret_cast<const uint4 *>(reinterpret_cast<uintptr_t>(src) & ~(uintptr_t)15);
+#pragma unroll 4
+        for (uint32_t k = lane; k < vecs; k += 32) {
+            const uint32_t n = min(p.dim - 8 * k, 8u);   // elements of this vector
+            uint32_t w[4] = {0, 0, 0, 0};
+            if (VOCAB_OK(src + 8 * k, 2 * n, base, (uint64_t)have * p.dim * 2, 32 + r)) {
+                const uint4 a = __ldg(blocks + k), b = off + 2 * n > 16 ? __ldg(blocks + k + 1) : make_uint4(0, 0, 0, 0);
+                const uint32_t v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-            for (uint32_t j = 0; j < 8; ++j)
-                if (e + j < p.dim && VOCAB_OK(src + j, 2, p.src[r], (uint64_t)have * p.dim * 2, 32 + r))
-                    w[j / 2] |= (uint32_t)src[j] << (16 * (j & 1));
+                for (uint32_t q = 0; q < 4; ++q) {
+                    uint32_t lo = 0, hi = 0;   // words words + q and the next, by selection: no indexing of registers
+#pragma unroll
+                    for (uint32_t z = 0; z < 4; ++z) {
+                        lo = words == z ? v[q + z] : lo;
+                        hi = words == z ? (q + z + 1 < 8 ? v[q + z + 1] : 0u) : hi;
+                    }
+                    w[q] = __funnelshift_r(lo, hi, bits);
+                    // elements past the row's end
+                    if (2 * q >= n) w[q] = 0;
+                    else if (2 * q + 1 >= n) w[q] &= 0xFFFFu;
+                }
+            }
+            dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        reinterpret_cast<uint4 *>(p.dst)[i] = make_uint4(w[0], w[1], w[2], w[3]);
     }
     DT_TL_END_BLOCK(DT_TL_VOCAB);
 }
@@ -862,7 +950,7 @@ cudaError_t launch_vocab_join(const VocabParams &p, int device, cudaStream_t s)
 
 cudaError_t launch_vocab_pack(const VocabPack &p, int device, cudaStream_t s)
 {
-    return launch_kernel(vocab_pack_kernel, dim3(elementwise_grid((uint64_t)p.rows * (p.pitch / 8), device)),
+    return launch_kernel(vocab_pack_kernel, dim3(elementwise_grid(((uint64_t)p.tokens + p.rows) * 32, device)),
                          dim3(kThreads), 0, s, false, p);
 }
 

@@ -53,7 +53,7 @@ struct VocabParams {
     uint32_t *ticket;
     float *scale;                      // grad, or grad / counted tokens
     uint16_t *gbuf;                    // [tokens, gpitch] bf16
-    float *acc;                        // [splits][tokens][apitch]
+    float *acc;                        // dh's sums [splits][tokens][apitch]
     uint16_t *dh;
     uint16_t *dw[DT_MAX_RANKS];
     ErrorSink sink;
@@ -76,10 +76,12 @@ struct VocabPack {
     const uint16_t *src[DT_MAX_RANKS];
     uint32_t src_rows[DT_MAX_RANKS];
     uint32_t unit_end[DT_MAX_RANKS];
-    uint16_t *dst;
-    int32_t P;                         // 0: one matrix of `rows` rows
+    const uint16_t *hidden;
+    uint16_t *hidden_dst, *dst;
+    int32_t P;
     uint32_t unit0;
-    uint32_t rows, dim, pitch;
+    uint32_t tokens, rows;             // hidden rows and vocabulary rows of this launch
+    uint32_t dim, pitch;
     ErrorSink sink;
 };
 
