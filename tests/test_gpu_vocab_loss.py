@@ -121,7 +121,9 @@ CASES = [
     (65, [257, 1], 72, 0), (128, [512, 512], 128, 0), (129, [100, 900, 0, 24], 200, 0), (77, [1000, 3000, 6007], 500, 0),
     (300, [2048] * 4, 256, 0), (300, [2048] * 4, 256, 1), (200, [1111, 2222], 333, 0), (40, [64] * 16, 1000, 3),
     (1000, [6000, 6001], 128, 0), (1, [40000], 1024, 0), (17, [20000, 12000], 768, 0), (513, [4096] * 8, 1024, 0),
-    (2500, [3000], 96, 0),
+    (2500, [3000], 96, 0), (256, [700, 800], 256, 0), (257, [700, 800], 264, 0), (192, [50, 3000], 129, 0),
+    # the vocabulary in several pieces: by p - [target]'s size, and by that of rows laid out again
+    (2048, [70000, 70001], 64, 0), (300, [9000, 11000], 4100, 0),
 ]
 
 
