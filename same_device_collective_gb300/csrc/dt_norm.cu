@@ -193,19 +193,12 @@ __device__ __forceinline__ void params(const void *p, int bf16, uint32_t e, floa
     }
 }
 
-// The rank that row belongs to, and the row's number there.  Every bound is a
-// constant operand, so nothing waits for the one before: a search took 700
-// cycles of a row's 6000.
+// The rank that row belongs to, and the row's number there.
 __device__ __forceinline__ int find_rank(const NormParams &p, uint64_t row, uint64_t &local)
 {
     int r = 0;
     uint64_t begin = 0;
-#pragma unroll
-    for (int k = 0; k + 1 < DT_MAX_RANKS; ++k)
-        if (k + 1 < p.P && row >= p.row_end[k]) {
-            r = k + 1;
-            begin = p.row_end[k];
-        }
+    while (r + 1 < p.P && row >= p.row_end[r]) begin = p.row_end[r++];
     local = row - begin;
     return r;
 }
@@ -425,25 +418,25 @@ __host__ __device__ constexpr int rows_at_once()
 
 // The mean and the sum of squared distances from it, of all warps that share a
 // row from each one's own: M2 = sum of M2_w + n_w (mean_w - mean)^2.
-__device__ __forceinline__ void row_moments(float sum, float &mean, float &m2, uint32_t mine, uint32_t cols,
+__device__ __forceinline__ void row_moments(float sum, float &mean, float &m2, uint32_t mine, float inv_cols,
                                             Exchange &red, uint32_t &phase, uint32_t tpr, uint32_t group)
 {
     if (tpr == 32) return;
     const float4 *of = exchange(make_float4(sum, m2, mean, (float)mine), red, phase, tpr, group);
     float all = 0.0f;
+#pragma unroll 4
     for (uint32_t q = 0; q < tpr >> 5; ++q) all += of[q].x;
-    mean = __fdiv_rn(all, (float)cols);
+    mean = all * inv_cols;
     m2 = 0.0f;
+#pragma unroll 4
     for (uint32_t q = 0; q < tpr >> 5; ++q) {
         const float4 v = of[q];
         m2 += fmaf(v.w * (v.z - mean), v.z - mean, v.y);
     }
 }
 
-__device__ __forceinline__ float rstd_of(float m2, uint32_t cols, float eps)
-{
-    return __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(m2, (float)cols) + eps));
-}
+// 1 / sqrt(v + eps), at most 2 ulp off.
+__device__ __forceinline__ float rstd_of(float m2, float inv_cols, float eps) { return rsqrtf(fmaf(m2, inv_cols, eps)); }
 
 template <typename T, int VEC, int N>
 __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(const __grid_constant__ NormParams p)
@@ -460,7 +453,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(const __grid_cons
     const uint64_t part = (uint64_t)group * gridDim.x + blockIdx.x;
     Ring<T, false> ring = make_ring<T, false>(p, smem, group);
     DT_TL_WAITED();
-    const float inv = __fdiv_rn(1.0f, (float)cols);
+    const float inv = p.inv_cols;
     uint32_t phase = 0;
     V w[N][K], b[N][K];
     auto weights = [&](int n) {
@@ -527,7 +520,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(const __grid_cons
 #pragma unroll
             for (int j = 0; j < B; ++j) {
                 if (k + j >= rows) continue;
-                m2[j] = rstd_of(m2[j], cols, p.eps);
+                m2[j] = rstd_of(m2[j], inv, p.eps);
                 const V minus = C::all(-s[j]), scale = C::all(m2[j]);
                 T *to = y + j * (uint64_t)cols;
 #pragma unroll
@@ -601,10 +594,9 @@ __global__ void __launch_bounds__(EARLY || N < 4 ? kNormThreads : 256, EARLY || 
     pdl_begin();
     DT_TL_WAITED();
     const uint32_t tpr = p.tpr, group = threadIdx.x / tpr, t = threadIdx.x % tpr, cols = p.cols;
-    const uint64_t at = (uint64_t)blockIdx.x * (blockDim.x / tpr) + group;
-    if (at < p.rows) {
-        uint64_t row;
-        const int r = find_rank(p, at, row);
+    const int r = blockIdx.y;   // a search for the rank took a tenth of a row's instructions
+    const uint64_t row = (uint64_t)blockIdx.x * (blockDim.x / tpr) + group;
+    if (row < p.row_end[r] - (r ? p.row_end[r - 1] : 0)) {
         const T *src = static_cast<const T *>(p.x[r]) + row * cols;
         T *y = static_cast<T *>(p.out[r]) + row * cols;
         C x[N];
@@ -625,7 +617,7 @@ __global__ void __launch_bounds__(EARLY || N < 4 ? kNormThreads : 256, EARLY || 
                 params<C, VEC>(p.weight, p.weight_bf16, e, 1.0f, w[n]);
                 params<C, VEC>(p.bias, p.weight_bf16, e, 0.0f, b[n]);
             }
-        const float inv_mine = mine ? __fdiv_rn(1.0f, (float)mine) : 0.0f;
+        const float inv_mine = mine ? __frcp_rn((float)mine) : 0.0f;
         // four sums, so that an addition does not wait for the one before
         V s[4] = {C::all(0.0f), C::all(0.0f), C::all(0.0f), C::all(0.0f)}, m[4] = {s[0], s[0], s[0], s[0]};
 #pragma unroll
@@ -651,8 +643,8 @@ __global__ void __launch_bounds__(EARLY || N < 4 ? kNormThreads : 256, EARLY || 
         }
         float m2[1] = {both(add(add(m[0], m[1]), add(m[2], m[3])))};
         warp_sum<1>(m2);
-        row_moments(sum[0], mean, m2[0], mine, cols, red, phase, tpr, group);
-        const float rstd = rstd_of(m2[0], cols, p.eps);
+        row_moments(sum[0], mean, m2[0], mine, p.inv_cols, red, phase, tpr, group);
+        const float rstd = rstd_of(m2[0], p.inv_cols, p.eps);
         const V minus = C::all(-mean), scale = C::all(rstd);
         auto finish = [&](auto kind) {
             constexpr int KIND = decltype(kind)::value;
@@ -699,7 +691,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_kernel(const __
     const uint64_t part = (uint64_t)group * gridDim.x + blockIdx.x;
     Ring<T, true> ring = make_ring<T, true>(p, smem, group);
     DT_TL_WAITED();
-    const float inv = __fdiv_rn(1.0f, (float)cols);
+    const float inv = p.inv_cols;
     uint32_t phase = 0;
     V dw[N][K], db[N][K], w[N][K];
     auto weights = [&](int n) {
@@ -867,13 +859,13 @@ __global__ void __launch_bounds__(kLongThreads) norm_long_kernel(const __grid_co
         float s[2] = {0.0f, 0.0f}, m2[2] = {0.0f, 0.0f};
         for (uint32_t e = threadIdx.x; e < p.cols; e += kLongThreads) s[0] += at(e);
         row_sum<2>(s, red, phase, kLongThreads, 0);
-        const float mean = __fdiv_rn(s[0], (float)p.cols);
+        const float mean = s[0] * p.inv_cols;
         for (uint32_t e = threadIdx.x; e < p.cols; e += kLongThreads) {
             const float d = at(e) - mean;
             m2[0] = fmaf(d, d, m2[0]);
         }
         row_sum<2>(m2, red, phase, kLongThreads, 0);
-        const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(m2[0], (float)p.cols) + p.eps));
+        const float rstd = rstd_of(m2[0], p.inv_cols, p.eps);
         for (uint32_t e = threadIdx.x; e < p.cols; e += kLongThreads) {
             const float f = fmaf((at(e) - mean) * rstd, param(p.weight, p.weight_bf16, e, 1.0f),
                                  param(p.bias, p.weight_bf16, e, 0.0f));
@@ -917,7 +909,7 @@ __global__ void __launch_bounds__(kLongThreads) norm_backward_long_kernel(const 
             s[1] = fmaf(q, h_at(e), s[1]);
         }
         row_sum<2>(s, red, phase, kLongThreads, 0);
-        const float mq = __fdiv_rn(s[0], (float)p.cols), mqh = __fdiv_rn(s[1], (float)p.cols);
+        const float mq = s[0] * p.inv_cols, mqh = s[1] * p.inv_cols;
         for (uint32_t e = threadIdx.x; e < p.cols; e += kLongThreads) {
             const float f = rstd * (q_at(e) - mq - h_at(e) * mqh);
             if (NORM_OK(p.out, 2, r, dx + e, sizeof(T), p.cols * sizeof(T))) from_f32(f, dx + e);
@@ -1095,12 +1087,14 @@ cudaError_t launch_norm(NormParams p, int dtype, bool vec, int device, cudaStrea
     const NormPick rows = pick_rows(dtype, vec, p.cols, few);
     if (rows.fn) {
         const uint32_t threads = few ? rows.tpr : std::max(rows.tpr, 256 / rows.tpr * rows.tpr), per = threads / rows.tpr;
-        const uint64_t blocks = (p.rows + per - 1) / per;
+        uint64_t most = 0;   // rows of a rank
+        for (int r = 0; r < p.P; ++r) most = std::max(most, p.row_end[r] - (r ? p.row_end[r - 1] : 0));
+        const uint64_t blocks = (most + per - 1) / per;
         if (blocks <= 0x7FFFFFFF) {
             p.tpr = rows.tpr;
             const bool whole = p.weight && p.bias && ((uintptr_t)p.weight & 15) == 0 && ((uintptr_t)p.bias & 15) == 0;
             p.param_kind = !vec || !whole ? kParamAny : !p.weight_bf16 ? kParamF32 : dtype == DT_BF16 ? kParamBf16 : kParamAny;
-            return launch_kernel(rows.fn, dim3((unsigned)blocks), dim3(threads), 0, s, false, p);
+            return launch_kernel(rows.fn, dim3((unsigned)blocks, (unsigned)p.P), dim3(threads), 0, s, false, p);
         }
     }
     const NormPick k = pick_norm<false>(dtype, vec, p.cols);

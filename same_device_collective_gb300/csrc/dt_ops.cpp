@@ -86,6 +86,7 @@ dt_status norm_common(dt_group *g, const void *const *x, void *const *out, const
     }
     p.rows = total;
     p.cols = (uint32_t)cols;
+    p.inv_cols = 1.0f / (float)cols;
     p.P = g->P;
     p.weight = weight;
     p.weight_bf16 = weight_dtype == DT_BF16;
@@ -180,7 +181,7 @@ bool vocab_plan(dt_group *g, const size_t *vocab, size_t vocab_equal, size_t tok
         const uint64_t blocks = dt::vocab_finish_blocks((uint32_t)tokens);
         v.part = take((uint64_t)v.units * v.parts * tokens * sizeof(float2));
         v.logit = take(tokens * 4);
-        v.sums = take(blocks * 8);
+        v.sums = take(blocks * 4);
         v.kept = take(blocks * 4);
     } else {
         v.g = take((uint64_t)v.piece * dt::kVocabUnit * 2 * tokens);
@@ -485,7 +486,7 @@ dt_status dt_vocab_loss(dt_group_t g, const void *hidden, const void *const *wei
     f.losses = losses;
     f.lse = lse;
     f.loss = loss;
-    f.block_sum = reinterpret_cast<double *>(ws + v.sums);
+    f.block_sum = reinterpret_cast<float *>(ws + v.sums);
     f.block_kept = reinterpret_cast<uint32_t *>(ws + v.kept);
     f.ticket = p.ticket;
     f.tokens = p.tokens;

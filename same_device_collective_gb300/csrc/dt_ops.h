@@ -38,7 +38,7 @@ struct NormParams {
     int32_t P;
     int32_t weight_bf16;               // of both
     int32_t param_kind;                // how the forward kernel reads them
-    float eps;
+    float eps, inv_cols;
     float avg_scale;
     int32_t avg;                       // 0: sum; 1: divide the gradients by P
     int32_t avg_pow2;

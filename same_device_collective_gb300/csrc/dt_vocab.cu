@@ -736,13 +736,16 @@ __global__ void __launch_bounds__(kTokens *kSlices) vocab_finish_kernel(const __
     }
     __syncthreads();
     if (warp == 0 && p.loss) {
-        double all = loss_of[lane];
-        for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
+        // 32 losses in fp32; the blocks' sums, of which there may be many, in
+        // 64 bits (a rare unit here, and slow: not for a single block)
+        float sum32 = loss_of[lane];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum32 += __shfl_xor_sync(0xFFFFFFFFu, sum32, o);
         uint64_t kept = __reduce_add_sync(0xFFFFFFFFu, keeps[lane]);
         bool end = true;
         if (gridDim.x > 1) {
             if (lane == 0) {
-                p.block_sum[blockIdx.x] = all;
+                p.block_sum[blockIdx.x] = sum32;
                 p.block_kept[blockIdx.x] = (uint32_t)kept;
                 __threadfence();
                 last = atomicAdd(p.ticket, 1u) == gridDim.x - 1;
@@ -751,8 +754,9 @@ __global__ void __launch_bounds__(kTokens *kSlices) vocab_finish_kernel(const __
             end = last;
             if (end) {
                 __threadfence();
-                all = 0.0;
+                double all = 0.0;
                 kept = 0;
+#pragma unroll 4
                 for (uint32_t b = lane; b < gridDim.x; b += 32) {
                     all += __ldcg(p.block_sum + b);
                     kept += __ldcg(p.block_kept + b);
@@ -761,9 +765,10 @@ __global__ void __launch_bounds__(kTokens *kSlices) vocab_finish_kernel(const __
                     all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
                     kept += __shfl_xor_sync(0xFFFFFFFFu, kept, o);
                 }
+                sum32 = (float)all;
             }
         }
-        if (end && lane == 0) *p.loss = kept == 0 ? 0.0f : (float)(p.avg ? all / (double)kept : all);
+        if (end && lane == 0) *p.loss = kept == 0 ? 0.0f : p.avg ? __fdiv_rn(sum32, (float)kept) : sum32;
     }
     DT_TL_END_BLOCK(DT_TL_VOCAB);
 }

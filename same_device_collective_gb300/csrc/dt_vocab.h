@@ -64,7 +64,7 @@ struct VocabFinish {
     const float *logit;
     const int32_t *targets;
     float *losses, *lse, *loss;        // each may be NULL
-    double *block_sum;
+    float *block_sum;
     uint32_t *block_kept;
     uint32_t *ticket;
     uint32_t tokens, tiles, vocab;
