@@ -6,26 +6,37 @@
 //   q_j = dy_j w_j       dx_j = r (q_j - mean(q) - h_j mean(q h))
 //   dw_j = sum_rows dy_j h_j      db_j = sum_rows dy_j
 //
-// The ranks' rows are one list, so that a call is one launch (two for the
-// backward pass) whatever the number of ranks.  Both directions are bound by
-// HBM (about 4 and 5 flops per byte), and close behind by the instructions an
-// SM can issue, so a row crosses few threads: sums cost shuffles and barriers
-// per warp that shares a row, not per element.  A row is read once, by a bulk
-// copy into shared memory; every group of threads that shares rows has a ring
-// of stages of its own, so that 100 to 200 KB an SM are always under way, which
-// registers alone cannot hold.  A stage is one row, or as many short ones as
-// make 4 KB; rows of any alignment are copied with the 16-byte blocks that
-// their ends lie in, and then read element by element.
+// A call is one launch (two for the backward pass) whatever the number of
+// ranks.  HBM bounds both directions (about 4 and 5 flops per byte), and close
+// behind it the instructions an SM can issue and the time that one row takes,
+// so every row is read once and crosses few threads: sums cost shuffles and
+// barriers per warp that shares a row, not per element.
+//
+// norm_rows_kernel  forward, rows of whole vectors: a row in the registers of
+//                   its threads, blocks handed out by the hardware (4 x 2048
+//                   rows of 4096 bf16: 27.7 us, 4.8 TB/s; PyTorch's copy of
+//                   the same bytes 23.2)
+// norm_kernel       forward, rows at other offsets or too long for that, and
+// norm_backward_kernel: resident blocks whose groups of threads each have a
+//                   ring of shared memory stages that bulk copies fill, so that
+//                   100 to 200 KB an SM are always under way.  A stage is a few
+//                   rows; rows of any alignment are copied with the 16-byte
+//                   blocks that their ends lie in, and then read element by
+//                   element (3 x 5000 rows of 1021 f32: 25.8 us, 4.8 TB/s; with
+//                   loads to registers 36).  A thread keeps its columns, 8 to
+//                   32 of them, over all of its rows, and with them their
+//                   weights and, backward, their shares of dw and db; up to four
+//                   rows are summed at a time.  Backward 4 x 2048 x 4096 bf16
+//                   44 us, 4.6 TB/s; 8 x 8192 x 4096 275 us, 5.9 TB/s: the
+//                   smaller call's blocks spend 6 us on their way to the first
+//                   row and 8 between the first SM's end and the last's.
+// norm_join_kernel  adds the blocks' shares of dw and db in a fixed order, so
+//                   that the result depends on the device and the shapes alone,
+//                   not on timing.
 //
 // The variance is the mean of the squared distances from the mean, not
 // E[x^2] - mu^2, which loses every digit where |mu| is large.  All sums are
 // fp32, and results are rounded once, at the store.
-//
-// A thread keeps its columns, 8 to 32 of them, over all of its rows, and
-// with them their weights and, backward, their shares of dw and db; up to four
-// rows are summed at a time.  A second
-// kernel adds the shares in a fixed order, so the result depends on the device
-// and the shapes alone, not on timing.
 #include <algorithm>
 #include <type_traits>
 
@@ -577,15 +588,17 @@ __device__ __forceinline__ void read_param(const NormParams &p, const void *q, u
 }
 
 // A row in the registers of tpr threads, up to 4 vectors each, and blocks of a
-// few rows that the hardware hands to the SMs as they come free (4 x 2048 rows
-// of 4096 bf16: 31 us, against 37 with the resident blocks and rings above, of
-// which 6 pass before the last SM has its first row and 8 between the first
-// SM's end and the last's).  What bounds it is the time of a row, 3 us, over
-// the eight rows that an SM's registers hold.
+// few rows that the hardware hands to the SMs as they come free: resident
+// blocks that share the rows out evenly took 37 us for 4 x 2048 rows of 4096
+// bf16, this 27.7.  64 registers a thread leave room for eight rows an SM; a
+// row takes 3 us, of which 1 is its loads'.  Tried: 1, 2, 8, 16 vectors a
+// thread 66, 43, 35, 38 us (with 4: 34 at that stage); the rows' weights in
+// shared memory 40, bound by reading them there.
 // EARLY: the weights are loaded along with the row, for calls of few rows,
 // where only the time from the first load to the last store counts.
 template <typename T, int VEC, int N, bool EARLY>
-__global__ void __launch_bounds__(EARLY || N < 4 ? kNormThreads : 256, EARLY || N < 4 ? 1 : 4) norm_rows_kernel(const __grid_constant__ NormParams p)
+__global__ void __launch_bounds__(EARLY || N < 4 ? kNormThreads : 256, EARLY || N < 4 ? 1 : 4)
+norm_rows_kernel(const __grid_constant__ NormParams p)
 {
     using C = Chunk<T, VEC>;
     using V = typename C::V;
@@ -953,8 +966,8 @@ using NormFn = void (*)(NormParams);
 // The kernel for rows of `cols` elements, either way, and the threads that
 // share a row: 8 columns a thread, or 16 or 32 where that keeps the row within
 // 256 threads, so that two groups or more share an SM and one computes while
-// another waits at its barrier (4096 columns over 512 threads: 39 us forward,
-// over 256: 37).  Past 256 threads of 32 columns a row may have 512; beyond
+// another waits at its barrier (4 x 2048 x 4096 backward: over 512 threads 47.0
+// us, over 256 46.6).  Past 256 threads of 32 columns a row may have 512; beyond
 // that, a thread's sums for its columns would not fit in registers.
 struct NormPick {
     NormFn fn = nullptr;
@@ -977,11 +990,15 @@ NormPick pick_norm(uint32_t cols)
 {
     NormPick k;
     const uint32_t chunks = (cols + VEC - 1) / VEC;
-    if constexpr (VEC > 1)
-        if (chunks <= 32) try_pick<T, VEC, 1, BACK>(k, chunks, 32);
-    try_pick<T, VEC, 8 / VEC, BACK>(k, chunks, 256);
-    try_pick<T, VEC, 16 / VEC, BACK>(k, chunks, VEC == 1 ? kNormThreads : 256);
-    if constexpr (VEC > 1) {
+    if constexpr (VEC == 1) {
+        try_pick<T, VEC, 8, BACK>(k, chunks, 256);
+        try_pick<T, VEC, 16, BACK>(k, chunks, kNormThreads);
+    } else if constexpr (!BACK) {   // what is left to this kernel is longer than 256 threads of 4 vectors
+        try_pick<T, VEC, 32 / VEC, BACK>(k, chunks, kNormThreads);
+    } else {
+        try_pick<T, VEC, 1, BACK>(k, chunks, 32);
+        try_pick<T, VEC, 8 / VEC, BACK>(k, chunks, 256);
+        try_pick<T, VEC, 16 / VEC, BACK>(k, chunks, 256);
         try_pick<T, VEC, 16 / VEC, BACK>(k, chunks, kNormThreads);
         try_pick<T, VEC, 32 / VEC, BACK>(k, chunks, kNormThreads);
     }
