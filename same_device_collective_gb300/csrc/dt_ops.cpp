@@ -113,7 +113,7 @@ struct VocabPlan {
     uint32_t units, pieces, piece;      // units of 256 rows; pieces of at most `piece` units
     bool pairs;                         // two CTAs share a tile
     uint32_t bn;                        // width of the logits' tiles
-    uint32_t parts;                     // partial sums of a unit
+    uint32_t parts;                     // tiles, and partial sums, of a unit
     uint32_t pitch;                     // of rows laid out again
     uint32_t splits, apitch;
     bool packed;
@@ -156,7 +156,7 @@ bool vocab_plan(dt_group *g, const size_t *vocab, size_t vocab_equal, size_t tok
     v.piece = (v.units + v.pieces - 1) / v.pieces;
     v.pieces = (v.units + v.piece - 1) / v.piece;
     v.bn = tile_width(mt, v.piece, workers, v.pairs);
-    v.parts = v.bn == 64 ? 4 : dt::kVocabUnit / (v.bn / 2);
+    v.parts = dt::kVocabUnit / v.bn;
     // few tokens: the vocabulary is split over the workers that dh's tiles leave idle
     v.apitch = (uint32_t)up(dim, 4);
     const uint64_t wide = v.pairs ? 256 : 128, across = (dim + wide - 1) / wide, tiles = mt * across;

@@ -8,10 +8,10 @@
 // serves all (Mode): tiles of 128 x bn outputs, or of 256 x bn for two CTAs of
 // a cluster, operands brought by TMA into a ring of shared memory stages by
 // one thread, multiplied by one thread that issues tcgen05.mma into tensor
-// memory, and finished by eight warps that read the accumulator while the next
-// tile's is being made in the other half of tensor memory.
-//   kLse   logits; the finish reduces half a tile's columns to a maximum and a
-//          sum of exponentials for each token: 8 bytes for 128 logits.
+// memory, and finished by 8 or 16 warps that read the accumulator while the
+// next tile's is being made in the other half of tensor memory.
+//   kLse   logits; the finish reduces a tile's columns to a maximum and a
+//          sum of exponentials for each token: 8 bytes for 256 logits.
 //   kGrad  the same logits again; the finish makes p - [target] and stores it
 //          as bf16 for a piece of the vocabulary at a time.  That is the one
 //          rounding on the way (2^-8 of each term at most, as the outputs'
@@ -61,12 +61,22 @@ constexpr uint32_t kM = 128;                       // rows of a tile in a CTA
 constexpr uint32_t kK = 128;                       // depth of a stage
 constexpr uint32_t kRingBytes = 192 * 1024;        // three stages of 128 rows and columns of A and B
 constexpr uint32_t kMaxStages = 8;
+// kLse: blocks of the inner dimension whose sum the tensor cores make; the sums
+// of further ones are added in registers.  The tensor cores round towards zero
+// at every step of 16: whole sums of 4096 products came out 4e-6 of themselves
+// too small, and losses 8e-7 off; with sums of 1024 that is 9e-7 and 2e-7, for
+// 2% of the time (2048 tokens of 32768 x 4096: 332 -> 338 us).
+constexpr uint32_t kSumBlocks = 8;
 constexpr uint32_t kTmemColumns = 512;             // two accumulators of 128 x 256 fp32
-constexpr uint32_t kFinishWarps = 8;
-constexpr int kTcThreads = (kFinishWarps + 3) * 32;   // and TMA, MMA, side work
+// Finishing warps: of logits that are only reduced 16, each with 64 columns of a
+// tile in registers; else 8 with 128.  And one for TMA, one for the products,
+// and kGrad's one for the tokens' count.
+__host__ __device__ constexpr uint32_t finish_warps(int mode) { return mode == kLse ? 16 : 8; }
+__host__ __device__ constexpr int tc_threads(int mode) { return (finish_warps(mode) + (mode == kGrad ? 3 : 2)) * 32; }
 constexpr uint32_t kStageOut = 4096;               // a finishing warp's 32 rows x 128 bytes
 constexpr uint32_t kBarBytes = 1024;
-constexpr size_t kTcSmem = 1024 + kRingBytes + kFinishWarps * kStageOut + kBarBytes;
+constexpr uint32_t kOutBytes = 8 * kStageOut;      // or kLse: 2 tiles x 4 column groups x 128 rows x 8 bytes
+constexpr size_t kTcSmem = 1024 + kRingBytes + kOutBytes + kBarBytes;
 static_assert(kTcSmem <= 227 * 1024, "shared memory above the per-block limit");
 
 // Where a tile's operands and outputs are.
@@ -326,6 +336,21 @@ __host__ __device__ constexpr uint32_t a_box_bytes(bool back, uint32_t rows)
     return back ? kBoxBytes : (rows * 128 + 1023) / 1024 * 1024;
 }
 
+// A sum of exponentials relative to m, relative to `most` >= m.  No mass is
+// left of minus infinities, but a NaN in a sum stays.
+__device__ __forceinline__ float scaled(float m, float x, float most)
+{
+    return x * (m == -INFINITY ? 0.0f : exp2_fast((m - most) * kLog2e));
+}
+
+// A maximum and a sum relative to it, and another such pair, into one.
+__device__ __forceinline__ void join(float &top, float &sum, float2 v)
+{
+    const float most = fmaxf(top, v.x);
+    sum = scaled(top, sum, most) + scaled(v.x, v.y, most);
+    top = most;
+}
+
 // The state of the pipeline's waits: a wait that runs out is recorded once,
 // and every role then leaves its loop.
 struct Waits {
@@ -353,14 +378,15 @@ struct Waits {
 };
 
 template <int MODE, int CG>
-__global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(kTcThreads, 1)
+__global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(tc_threads(MODE), 1)
 vocab_kernel(const __grid_constant__ VocabParams p)
 {
+    constexpr uint32_t kFinishWarps = finish_warps(MODE);
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
     const uint32_t ring = smem_addr(smem);
     unsigned char *out_buf = smem + kRingBytes;
-    unsigned char *ctl = out_buf + kFinishWarps * kStageOut;
+    unsigned char *ctl = out_buf + kOutBytes;
     const uint32_t bars = smem_addr(ctl);
     const uint32_t full = bars, empty = bars + 8 * kMaxStages;         // stage loaded; stage consumed
     const uint32_t acc_full = bars + 16 * kMaxStages, acc_empty = acc_full + 16, drained = acc_empty + 16;
@@ -404,6 +430,7 @@ vocab_kernel(const __grid_constant__ VocabParams p)
 
     if (warp == kFinishWarps) {
         if (lane == 0) {
+            if (MODE == kLse && blockIdx.x == 0) *p.ticket = 0;   // for the kernel that joins the partial sums
             uint32_t n = 0, s = 0, round = 0;   // loads issued; the next one's stage and its parity
             bool ok = true;
             for (uint32_t k = 0; ok && next_tile<MODE, CG>(p, worker, workers, k, t); ++k) {
@@ -425,7 +452,7 @@ vocab_kernel(const __grid_constant__ VocabParams p)
         __syncwarp();
     } else if (warp == kFinishWarps + 1) {
         if (lane == 0 && half == 0) {
-            uint32_t s = 0, round = 0;
+            uint32_t s = 0, round = 0, u = 0;   // u: accumulators handed over
             bool ok = true;
             for (uint32_t i = 0; ok && next_tile<MODE, CG>(p, worker, workers, i, t); ++i) {
                 const bool a_mn = MODE == kBack && t.dw;
@@ -438,24 +465,27 @@ vocab_kernel(const __grid_constant__ VocabParams p)
                 // K steps of 16 that the last block has
                 const uint32_t inner = MODE != kBack ? p.dim : t.dw ? p.tokens : p.kblocks * kK;
                 const uint32_t last = min((inner - (t.kb1 - 1) * kK + 15) / 16, 8u);
-                const uint32_t acc = tmem + (i & 1) * 256;
-                if (!(ok = wait(acc_empty + 8 * (i & 1), ((i >> 1) & 1) ^ 1))) break;
-                tc_fence_after();
-                for (uint32_t kb = t.kb0; kb < t.kb1; ++kb) {
-                    if (!(ok = wait(full + 8 * s, round))) break;
+                for (uint32_t kb = t.kb0; ok && kb < t.kb1; ++u) {
+                    const uint32_t first = kb, end = MODE == kLse ? min(kb + kSumBlocks, t.kb1) : t.kb1;
+                    const uint32_t acc = tmem + (u & 1) * 256;
+                    if (!(ok = wait(acc_empty + 8 * (u & 1), ((u >> 1) & 1) ^ 1))) break;
                     tc_fence_after();
-                    const uint32_t at = ring + s * stage_bytes;
-                    const uint64_t a = smem_desc(at, a_mn), b = smem_desc(at + 2 * a_box, b_mn);
-                    const uint32_t steps = kb + 1 == t.kb1 ? last : 8;
+                    for (; kb < end; ++kb) {
+                        if (!(ok = wait(full + 8 * s, round))) break;
+                        tc_fence_after();
+                        const uint32_t at = ring + s * stage_bytes;
+                        const uint64_t a = smem_desc(at, a_mn), b = smem_desc(at + 2 * a_box, b_mn);
+                        const uint32_t steps = kb + 1 == t.kb1 ? last : 8;
 #pragma unroll
-                    for (uint32_t k = 0; k < 8; ++k)
-                        if (k < steps) mma_bf16<CG>(acc, a + ((k / 4 * a_next + k % 4 * a_step) >> 4),
-                                                    b + ((k / 4 * b_next + k % 4 * b_step) >> 4), desc,
-                                                    kb != t.kb0 || k != 0);
-                    mma_commit<CG>(empty + 8 * s);
-                    if (++s == p.stages) s = 0, round ^= 1;
+                        for (uint32_t k = 0; k < 8; ++k)
+                            if (k < steps)
+                                mma_bf16<CG>(acc, a + ((k / 4 * a_next + k % 4 * a_step) >> 4),
+                                             b + ((k / 4 * b_next + k % 4 * b_step) >> 4), desc, kb != first || k != 0);
+                        mma_commit<CG>(empty + 8 * s);
+                        if (++s == p.stages) s = 0, round ^= 1;
+                    }
+                    if (ok) mma_commit<CG>(acc_full + 8 * (u & 1));
                 }
-                if (ok) mma_commit<CG>(acc_full + 8 * (i & 1));
             }
             if (!ok) {   // the MMAs issued so far end before tensor memory is freed
                 mma_commit<CG>(drained);
@@ -463,10 +493,9 @@ vocab_kernel(const __grid_constant__ VocabParams p)
             }
         }
         __syncwarp();
-    } else if (warp == kFinishWarps + 2) {
-        // what the tiles do not wait for
-        if (MODE == kLse && blockIdx.x == 0 && lane == 0) *p.ticket = 0;
-        if (MODE == kGrad && blockIdx.x == 0 && p.unit0 == 0) {
+    } else if (MODE == kGrad && warp == kFinishWarps + 2) {
+        // the scale, which the tiles of this launch do not wait for
+        if (blockIdx.x == 0 && p.unit0 == 0) {
             uint32_t kept = 0;
             for (uint32_t k = lane; k < p.tokens; k += 32) {
                 const int32_t v = p.targets[k];
@@ -481,14 +510,31 @@ vocab_kernel(const __grid_constant__ VocabParams p)
             }
         }
     } else {
-        // Warps w and w + 4 read the same 32 rows (a warp reaches the tensor
-        // memory lanes of its number modulo 4) and take half of the columns
-        // each; tiles of 64 columns are the first four warps'.
-        unsigned char *buf = out_buf + warp * kStageOut;
+        // Warps w, w + 4, ... read the same 32 rows (a warp reaches the tensor
+        // memory lanes of its number modulo 4) and take an equal part of the
+        // columns each, in kGrad and kBack at least 64.
+        unsigned char *buf = out_buf + (MODE == kLse ? 0 : warp * kStageOut);
         const float scale = MODE == kBack ? *p.scale : 0.0f;
-        const uint32_t width = p.bn >= 128 ? p.bn / 2 : p.bn, c0 = (warp >> 2) * width, c1 = min(c0 + width, p.bn);
+        constexpr uint32_t kParts = kFinishWarps / 4;
+        const uint32_t width = MODE == kLse || p.bn >= 128 ? p.bn / kParts : p.bn;
+        const uint32_t c0 = (warp >> 2) * width, c1 = min(c0 + width, p.bn);
+        bool late = false;
+        uint32_t u = 0;   // accumulators taken over
+        auto take = [&] {
+            const bool ok = wait(acc_full + 8 * (u & 1), (u >> 1) & 1);
+            tc_fence_after();
+            return !__any_sync(0xFFFFFFFFu, !ok);
+        };
+        auto give_back = [&] {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (CG == 2) mbar_arrive_first(acc_empty + 8 * (u & 1));
+                else mbar_arrive(acc_empty + 8 * (u & 1));
+            }
+            ++u;
+        };
         for (uint32_t i = 0; next_tile<MODE, CG>(p, worker, workers, i, t); ++i) {
-            const uint32_t acc = tmem + (i & 1) * 256 + ((warp & 3) * 32 << 16);
             const uint32_t quad = half * kM + (warp & 3) * 32;   // first of this warp's rows in the tile
             const uint32_t row0 = t.m0 + quad, row = row0 + lane;
             // what does not depend on the accumulator, before the wait for it
@@ -498,9 +544,8 @@ vocab_kernel(const __grid_constant__ VocabParams p)
                 target = p.targets[row];
                 if (MODE == kGrad) lse2 = p.lse[row] * kLog2e;
             }
-            const bool ok = wait(acc_full + 8 * (i & 1), (i >> 1) & 1);
-            if (__any_sync(0xFFFFFFFFu, !ok)) break;
-            tc_fence_after();
+            const uint32_t lanes = (warp & 3) * 32 << 16;   // of tensor memory
+            uint32_t acc = tmem + (u & 1) * 256 + lanes;
 
             if (MODE != kBack) {
                 const uint32_t valid = rows_left(p, t.r, t.vrow, p.bn);
@@ -508,50 +553,68 @@ vocab_kernel(const __grid_constant__ VocabParams p)
                 const int64_t at = (int64_t)target - (int64_t)(p.first[t.r] + t.vrow);
                 const bool here = target != p.ignore && target >= 0 && at >= (int64_t)c0 && at < (int64_t)min(c1, valid);
                 if (MODE == kLse) {
+                    // the logits: one accumulator, or the sum of several.  A wait
+                    // that runs out ends no loop here, as all warps meet below:
+                    // there are just no more waits.
+                    float v[64] = {};
+                    for (uint32_t kb = t.kb0; kb < t.kb1; kb += kSumBlocks) {
+                        if (!late) late = !take();
+                        acc = tmem + (u & 1) * 256 + lanes;
+#pragma unroll
+                        for (uint32_t b = 0; b < 64; b += 8) {
+                            if (b >= width) continue;
+                            float x[8];
+                            tmem_load8(acc + c0 + b, x);
+#pragma unroll
+                            for (uint32_t j = 0; j < 8; ++j) v[b + j] += x[j];
+                        }
+                        give_back();
+                    }
                     // four running values each, so that none waits for the one before
-                    float tops[4], sums[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    float tops[4], sums[4] = {0.0f, 0.0f, 0.0f, 0.0f}, logit = 0.0f;
 #pragma unroll
                     for (uint32_t j = 0; j < 4; ++j) tops[j] = -INFINITY;
-                    for (uint32_t c = c0; c < c1; c += 32) {
-                        float v[32];
-                        tmem_load32(acc + c, v);
-                        if (c + 32 <= valid) {
+                    const uint32_t mine = here ? (uint32_t)at - c0 : 0xFFFFFFFFu;
+                    const bool search = __any_sync(0xFFFFFFFFu, here);
 #pragma unroll
-                            for (uint32_t j = 0; j < 32; ++j) tops[j & 3] = fmaxf(tops[j & 3], v[j]);
-                        } else {
+                    for (uint32_t b = 0; b < 64; b += 16) {
+                        if (b >= width) continue;
+                        if (c0 + b + 16 > valid) {   // columns that are not there count for nothing
 #pragma unroll
-                            for (uint32_t j = 0; j < 32; ++j) tops[j & 3] = fmaxf(tops[j & 3], c + j < valid ? v[j] : -INFINITY);
+                            for (uint32_t j = 0; j < 16; ++j) v[b + j] = c0 + b + j < valid ? v[b + j] : -INFINITY;
                         }
+                        if (search) {
+#pragma unroll
+                            for (uint32_t j = 0; j < 16; ++j) logit = mine == b + j ? v[b + j] : logit;
+                        }
+#pragma unroll
+                        for (uint32_t j = 0; j < 16; ++j) tops[j & 3] = fmaxf(tops[j & 3], v[b + j]);
                     }
-                    const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+                    float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
                     const float top2 = top == -INFINITY ? 0.0f : top * kLog2e;   // no 0 times infinity where all are -inf
-                    for (uint32_t c = c0; c < c1; c += 32) {
-                        float v[32];
-                        tmem_load32(acc + c, v);
-                        if (c + 32 <= valid) {
 #pragma unroll
-                            for (uint32_t j = 0; j < 32; ++j) sums[j & 3] += exp2_fast(fmaf(v[j], kLog2e, -top2));
-                        } else {
+                    for (uint32_t b = 0; b < 64; b += 16) {
+                        if (b >= width) continue;
 #pragma unroll
-                            for (uint32_t j = 0; j < 32; ++j)
-                                if (c + j < valid) sums[j & 3] += exp2_fast(fmaf(v[j], kLog2e, -top2));
-                        }
+                        for (uint32_t j = 0; j < 16; ++j) sums[j & 3] += exp2_fast(fmaf(v[b + j], kLog2e, -top2));
                     }
-                    const float sum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
-                    // few rows have their target here: one column read for each
-                    float logit = 0.0f;
-                    for (uint32_t rest = __ballot_sync(0xFFFFFFFFu, here); rest; rest &= rest - 1) {
-                        const uint32_t who = __ffs(rest) - 1;
-                        const uint32_t col = __shfl_sync(0xFFFFFFFFu, (uint32_t)at, who);
-                        const float v = tmem_load1(acc + col);
-                        if (lane == who) logit = v;
-                    }
-                    if (row < p.tokens && c0 < c1) {
-                        const uint64_t part = (uint64_t)p.unit0 * (kVocabUnit / width) + (t.n0 + c0) / width;
+                    if (here && row < p.tokens) p.logit[row] = logit;
+                    // the four column groups' into one; the other half of `red` may
+                    // still be read from the tile before
+                    float2(*red)[kM] = reinterpret_cast<float2(*)[kM]>(buf) + (i & 1) * kParts;
+                    const uint32_t in = (warp & 3) * 32 + lane;
+                    if (warp >= 4) red[warp >> 2][in] = make_float2(top, (sums[0] + sums[1]) + (sums[2] + sums[3]));
+                    asm volatile("bar.sync 1, %0;" ::"n"(kFinishWarps * 32) : "memory");
+                    if (warp < 4 && row < p.tokens) {
+                        float sum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+#pragma unroll
+                        for (uint32_t q = 1; q < kParts; ++q) join(top, sum, red[q][in]);
+                        const uint64_t part = (uint64_t)p.unit0 * (kVocabUnit / p.bn) + t.n0 / p.bn;
                         p.part[part * p.tokens + row] = make_float2(top, sum);
-                        if (here) p.logit[row] = logit;
                     }
+                    continue;
                 } else {
+                    if (!take()) break;
                     const bool keep = row < p.tokens && target != p.ignore && target >= 0 && (uint32_t)target < p.vocab;
                     const uint32_t col = here ? (uint32_t)at : 0xFFFFFFFFu;
                     const uint32_t rows = row0 < p.tokens ? min(p.tokens - row0, 32u) : 0;
@@ -581,6 +644,8 @@ vocab_kernel(const __grid_constant__ VocabParams p)
                                          p.gbuf, (uint64_t)p.tokens * p.gpitch * 2, 0);
                     }
                 }
+            } else if (!take()) {
+                break;
             } else if (!t.dw) {
                 // fp32 sums: 32 columns a step, through shared memory so that
                 // eight threads take a row's line
@@ -652,12 +717,7 @@ vocab_kernel(const __grid_constant__ VocabParams p)
                                     (uint64_t)p.rows[t.r] * p.dim * 2, 16 + t.r);
                 }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                if (CG == 2) mbar_arrive_first(acc_empty + 8 * (i & 1));
-                else mbar_arrive(acc_empty + 8 * (i & 1));
-            }
+            give_back();
         }
     }
     tc_fence_before();
@@ -685,9 +745,6 @@ __global__ void __launch_bounds__(kTokens *kSlices) vocab_finish_kernel(const __
     pdl_begin();
     DT_TL_WAITED();
     const uint32_t lane = threadIdx.x % kTokens, warp = threadIdx.x / kTokens;
-    // (m, x) and (top, sum), both relative to their own maximum, into one.  No
-    // mass is left of minus infinities, but a NaN in a sum stays.
-    auto scaled = [](float m, float x, float most) { return x * (m == -INFINITY ? 0.0f : exp2_fast((m - most) * kLog2e)); };
     const uint32_t t = blockIdx.x * kTokens + warp;   // the token that this warp finishes
     int32_t target = p.ignore;
     float logit = 0.0f;
@@ -700,10 +757,7 @@ __global__ void __launch_bounds__(kTokens *kSlices) vocab_finish_kernel(const __
     if (column < p.tokens) {
 #pragma unroll 4
         for (uint32_t k = warp; k < p.tiles; k += kSlices) {
-            const float2 v = p.part[(uint64_t)k * p.tokens + column];
-            const float most = fmaxf(top, v.x);
-            sum = scaled(top, sum, most) + scaled(v.x, v.y, most);
-            top = most;
+            join(top, sum, p.part[(uint64_t)k * p.tokens + column]);
         }
     }
     part[warp][lane] = make_float2(top, sum);
@@ -888,7 +942,7 @@ cudaError_t launch_mode(VocabParams &p, int device, cudaStream_t s)
     }
     p.stages = std::min(kMaxStages, kRingBytes / (2 * a_box_bytes(MODE == kBack, p.rows_h) + p.bn / CG * 256));
     return launch_kernel(vocab_kernel<MODE, CG>, dim3(std::min(p.workers, vocab_workers(CG == 2, device)) * CG),
-                         dim3(kTcThreads), kTcSmem, s, false, p);
+                         dim3(tc_threads(MODE)), kTcSmem, s, false, p);
 }
 
 template <int MODE>

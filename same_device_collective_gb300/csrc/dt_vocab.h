@@ -48,7 +48,7 @@ struct VocabParams {
     const int32_t *targets;
     const float *lse;
     const float *grad;
-    float2 *part;                      // [half tiles of the vocabulary][tokens]: maximum, sum of exponentials
+    float2 *part;                      // [tiles of the vocabulary][tokens]: maximum, sum of exponentials
     float *logit;                      // the target's logit of each token
     uint32_t *ticket;
     float *scale;                      // grad, or grad / counted tokens
