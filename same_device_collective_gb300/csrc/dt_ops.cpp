@@ -336,6 +336,10 @@ void logits_tiles(const VocabPlan &v, uint32_t units, dt::VocabParams &p)
     p.splits = 1;
     p.group = kGroup;
     p.kblocks = dt::vocab_blocks(p.dim);
+    auto inverse = [](uint32_t d) { return (uint32_t)((1ull << 32) / d + 1); };
+    p.per_group = inverse(p.group * p.mt);
+    p.per_row = inverse(p.group);
+    p.per_last = inverse((p.nt - 1) % p.group + 1);
     p.tiles = p.mt * p.nt;
 }
 

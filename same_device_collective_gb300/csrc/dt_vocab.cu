@@ -25,7 +25,7 @@
 //          stays in fp32 and is joined in a fixed order.
 // A pair of CTAs halves what each reads of B, so that L2 feeds a third less.
 // It takes 256 rows of A, so up to 128 tokens a CTA works alone, on tiles of at
-// most 128 columns, and loads only the rows there are of A: for one token 72
+// most 128 columns, and loads only the rows there are of A: for one token 128
 // KB of w are under way at a time, in eight stages, instead of 64 in four.
 // A stage is 128 deep: four TMA boxes of 16 KB, which the
 // copy engine serves faster than eight of 8 KB (2048 tokens of 32768 x 4096:
@@ -34,6 +34,11 @@
 // through in units of 256 (the last unit of a rank is padded by zeros that TMA
 // fills in), so the reductions over the ranks (of the maximum, the sum and dh)
 // are the sums over units.
+//
+// Where dim is small the finish bounds the logits, not their products: below
+// about 400 a tile of 256 x 256 takes the finishing warps 4000 cycles, half of
+// which issue instructions (8192 tokens of 65536 x 256: 231 us, of which the
+// products need 144).
 //
 // With n tokens the work is 2 n flops for each byte of w: below about 280
 // tokens HBM bounds it, above it the tensor cores do.
@@ -73,9 +78,10 @@ constexpr uint32_t kTmemColumns = 512;             // two accumulators of 128 x 
 // and kGrad's one for the tokens' count.
 __host__ __device__ constexpr uint32_t finish_warps(int mode) { return mode == kLse ? 16 : 8; }
 __host__ __device__ constexpr int tc_threads(int mode) { return (finish_warps(mode) + (mode == kGrad ? 3 : 2)) * 32; }
+constexpr uint32_t kJoins = 3;                     // tiles whose column groups' results there is room for
 constexpr uint32_t kStageOut = 4096;               // a finishing warp's 32 rows x 128 bytes
 constexpr uint32_t kBarBytes = 1024;
-constexpr uint32_t kOutBytes = 8 * kStageOut;      // or kLse: 2 tiles x 4 column groups x 128 rows x 8 bytes
+constexpr uint32_t kOutBytes = 8 * kStageOut;      // or kLse: 3 tiles x 4 column groups x 128 rows x 8 bytes
 constexpr size_t kTcSmem = 1024 + kRingBytes + kOutBytes + kBarBytes;
 static_assert(kTcSmem <= 227 * 1024, "shared memory above the per-block limit");
 
@@ -88,6 +94,15 @@ struct Tile {
     int r;               // rank and row there of the vocabulary rows that the tile covers (logits: n; dw: m)
     uint32_t vrow;
 };
+
+// n / d, where `inverse` is the least whole number above 2^32 / d (0 for 1): the
+// product's high word is at most one too large.
+__device__ __forceinline__ uint32_t quotient(uint32_t n, uint32_t d, uint32_t inverse)
+{
+    if (d == 1) return n;
+    const uint32_t q = __umulhi(n, inverse);
+    return q * d > n ? q - 1 : q;
+}
 
 // The rank of a unit of 256 vocabulary rows, and the unit's first row there.
 __device__ __forceinline__ int unit_rank(const VocabParams &p, uint32_t unit, uint32_t &row)
@@ -117,11 +132,12 @@ __device__ __forceinline__ bool next_tile(const VocabParams &p, uint32_t q, uint
     if (MODE != kBack) {
         i = q + k * W;
         if (i >= p.tiles) return false;
-        const uint32_t g = i / (p.group * p.mt);
-        i -= g * p.group * p.mt;
+        const uint32_t all = p.group * p.mt, g = quotient(i, all, p.per_group);
+        i -= g * all;
         width = min(p.group, p.nt - g * p.group);
-        t.m0 = i / width * (kM * CG);
-        t.n0 = (g * p.group + i % width) * p.bn;
+        const uint32_t m = quotient(i, width, width == p.group ? p.per_row : p.per_last);
+        t.m0 = m * (kM * CG);
+        t.n0 = (g * p.group + i - m * width) * p.bn;
         t.kb0 = 0;
         t.kb1 = p.kblocks;
         t.r = unit_rank(p, p.unit0 + t.n0 / kVocabUnit, t.vrow);
@@ -390,6 +406,7 @@ vocab_kernel(const __grid_constant__ VocabParams p)
     const uint32_t bars = smem_addr(ctl);
     const uint32_t full = bars, empty = bars + 8 * kMaxStages;         // stage loaded; stage consumed
     const uint32_t acc_full = bars + 16 * kMaxStages, acc_empty = acc_full + 16, drained = acc_empty + 16;
+    const uint32_t reduced = drained + 8;                              // kLse: the column groups' results are there
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(ctl + 256);
     volatile uint32_t *gave_up = tmem_slot + 1;
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -407,6 +424,7 @@ vocab_kernel(const __grid_constant__ VocabParams p)
             mbar_init(acc_empty + 8 * s, kFinishWarps * CG);
         }
         mbar_init(drained, 1);
+        for (uint32_t s = 0; MODE == kLse && s < kJoins; ++s) mbar_init(reduced + 8 * s, kFinishWarps - 4);
         *gave_up = 0;
         mbar_init_fence();
     }
@@ -519,7 +537,7 @@ vocab_kernel(const __grid_constant__ VocabParams p)
         const uint32_t width = MODE == kLse || p.bn >= 128 ? p.bn / kParts : p.bn;
         const uint32_t c0 = (warp >> 2) * width, c1 = min(c0 + width, p.bn);
         bool late = false;
-        uint32_t u = 0;   // accumulators taken over
+        uint32_t u = 0, j3 = 0, round = 0;   // accumulators taken over; kLse: the next tile's room for results, its parity
         auto take = [&] {
             const bool ok = wait(acc_full + 8 * (u & 1), (u >> 1) & 1);
             tc_fence_after();
@@ -549,15 +567,17 @@ vocab_kernel(const __grid_constant__ VocabParams p)
 
             if (MODE != kBack) {
                 const uint32_t valid = rows_left(p, t.r, t.vrow, p.bn);
-                // the column of this row's target in the tile, if it is there
-                const int64_t at = (int64_t)target - (int64_t)(p.first[t.r] + t.vrow);
-                const bool here = target != p.ignore && target >= 0 && at >= (int64_t)c0 && at < (int64_t)min(c1, valid);
                 if (MODE == kLse) {
                     // the logits: one accumulator, or the sum of several.  A wait
                     // that runs out ends no loop here, as all warps meet below:
                     // there are just no more waits.
-                    float v[64] = {};
-                    for (uint32_t kb = t.kb0; kb < t.kb1; kb += kSumBlocks) {
+                    float v[64];
+                    if (!late) late = !take();
+#pragma unroll
+                    for (uint32_t b = 0; b < 64; b += 32)
+                        if (b < width) tmem_load32(acc + c0 + b, *reinterpret_cast<float(*)[32]>(v + b));
+                    give_back();
+                    for (uint32_t kb = t.kb0 + kSumBlocks; kb < t.kb1; kb += kSumBlocks) {
                         if (!late) late = !take();
                         acc = tmem + (u & 1) * 256 + lanes;
 #pragma unroll
@@ -571,11 +591,10 @@ vocab_kernel(const __grid_constant__ VocabParams p)
                         give_back();
                     }
                     // four running values each, so that none waits for the one before
-                    float tops[4], sums[4] = {0.0f, 0.0f, 0.0f, 0.0f}, logit = 0.0f;
+                    float tops[4];
+                    float2 sums[4];
 #pragma unroll
-                    for (uint32_t j = 0; j < 4; ++j) tops[j] = -INFINITY;
-                    const uint32_t mine = here ? (uint32_t)at - c0 : 0xFFFFFFFFu;
-                    const bool search = __any_sync(0xFFFFFFFFu, here);
+                    for (uint32_t j = 0; j < 4; ++j) tops[j] = -INFINITY, sums[j] = make_float2(0.0f, 0.0f);
 #pragma unroll
                     for (uint32_t b = 0; b < 64; b += 16) {
                         if (b >= width) continue;
@@ -583,37 +602,59 @@ vocab_kernel(const __grid_constant__ VocabParams p)
 #pragma unroll
                             for (uint32_t j = 0; j < 16; ++j) v[b + j] = c0 + b + j < valid ? v[b + j] : -INFINITY;
                         }
-                        if (search) {
 #pragma unroll
-                            for (uint32_t j = 0; j < 16; ++j) logit = mine == b + j ? v[b + j] : logit;
-                        }
-#pragma unroll
-                        for (uint32_t j = 0; j < 16; ++j) tops[j & 3] = fmaxf(tops[j & 3], v[b + j]);
+                        for (uint32_t j = 0; j < 8; ++j) tops[j & 3] = max3(tops[j & 3], v[b + j], v[b + j + 8]);
                     }
                     float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
                     const float top2 = top == -INFINITY ? 0.0f : top * kLog2e;   // no 0 times infinity where all are -inf
+                    const float2 log2e2 = make_float2(kLog2e, kLog2e), down = make_float2(-top2, -top2);
 #pragma unroll
                     for (uint32_t b = 0; b < 64; b += 16) {
                         if (b >= width) continue;
 #pragma unroll
-                        for (uint32_t j = 0; j < 16; ++j) sums[j & 3] += exp2_fast(fmaf(v[b + j], kLog2e, -top2));
+                        for (uint32_t j = 0; j < 16; j += 2) {
+                            const float2 x = fma2(make_float2(v[b + j], v[b + j + 1]), log2e2, down);
+                            sums[j / 2 & 3] = add2(sums[j / 2 & 3], make_float2(exp2_fast(x.x), exp2_fast(x.y)));
+                        }
                     }
-                    if (here && row < p.tokens) p.logit[row] = logit;
-                    // the four column groups' into one; the other half of `red` may
-                    // still be read from the tile before
-                    float2(*red)[kM] = reinterpret_cast<float2(*)[kM]>(buf) + (i & 1) * kParts;
-                    const uint32_t in = (warp & 3) * 32 + lane;
-                    if (warp >= 4) red[warp >> 2][in] = make_float2(top, (sums[0] + sums[1]) + (sums[2] + sums[3]));
-                    asm volatile("bar.sync 1, %0;" ::"n"(kFinishWarps * 32) : "memory");
-                    if (warp < 4 && row < p.tokens) {
-                        float sum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+                    const float2 both = add2(add2(sums[0], sums[1]), add2(sums[2], sums[3]));
+                    float sum = both.x + both.y;
+                    // the column of this row's target in the tile, if it is there
+                    const int64_t at = (int64_t)target - (int64_t)(p.first[t.r] + t.vrow);
+                    const bool here = target != p.ignore && target >= 0 && at >= (int64_t)c0 && at < (int64_t)min(c1, valid);
+                    if (__any_sync(0xFFFFFFFFu, here)) {
+                        const uint32_t mine = (uint32_t)at - c0;
+                        float logit = 0.0f;
 #pragma unroll
-                        for (uint32_t q = 1; q < kParts; ++q) join(top, sum, red[q][in]);
-                        const uint64_t part = (uint64_t)p.unit0 * (kVocabUnit / p.bn) + t.n0 / p.bn;
-                        p.part[part * p.tokens + row] = make_float2(top, sum);
+                        for (uint32_t j = 0; j < 64; ++j)
+                            if (j < width) logit = mine == j ? v[j] : logit;
+                        if (here && row < p.tokens) p.logit[row] = logit;
                     }
+                    // The four column groups' into one by the first warps; the others go on
+                    // (with a barrier of them all a narrow head's tile took 12% longer).  They
+                    // are at most two tiles ahead then: a third one's logits wait for the first
+                    // warps to have read the second's, so three tiles' results need room.
+                    float2(*red)[kM] = reinterpret_cast<float2(*)[kM]>(buf) + j3 * kParts;
+                    const uint32_t in = (warp & 3) * 32 + lane;
+                    if (warp >= 4) {
+                        red[warp >> 2][in] = make_float2(top, sum);
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(reduced + 8 * j3);
+                    } else {
+                        if (!late) late = __any_sync(0xFFFFFFFFu, !wait(reduced + 8 * j3, round));
+                        if (row < p.tokens) {
+#pragma unroll
+                            for (uint32_t q = 1; q < kParts; ++q) join(top, sum, red[q][in]);
+                            const uint64_t part = (uint64_t)p.unit0 * (kVocabUnit / p.bn) + t.n0 / p.bn;
+                            p.part[part * p.tokens + row] = make_float2(top, sum);
+                        }
+                    }
+                    if (++j3 == kJoins) j3 = 0, round ^= 1;
                     continue;
                 } else {
+                    // the column of this row's target in the tile, if it is there
+                    const int64_t at = (int64_t)target - (int64_t)(p.first[t.r] + t.vrow);
+                    const bool here = target != p.ignore && target >= 0 && at >= (int64_t)c0 && at < (int64_t)min(c1, valid);
                     if (!take()) break;
                     const bool keep = row < p.tokens && target != p.ignore && target >= 0 && (uint32_t)target < p.vocab;
                     const uint32_t col = here ? (uint32_t)at : 0xFFFFFFFFu;

@@ -33,6 +33,7 @@ struct VocabParams {
     uint32_t pairs;                    // two CTAs share a tile
     uint32_t workers;                  // CTAs or pairs that have a tile
     uint32_t mt, nt, splits, group;    // tiles of the logits or dh, splits of the inner dimension, tile order
+    uint32_t per_group, per_row, per_last;   // inverses of group * mt, group and the last group's width (quotient)
     uint32_t kblocks;                  // blocks of the inner dimension
     uint32_t tiles;                    // mt * nt * splits
     uint32_t dw_tiles, dw_kblocks;     // the same of dw, whose tiles have the width of dh's
