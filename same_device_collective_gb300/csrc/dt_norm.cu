@@ -13,21 +13,22 @@
 // barriers per warp that shares a row, not per element.
 //
 // norm_rows_kernel  forward, rows of whole vectors: a row in the registers of
-//                   its threads, blocks handed out by the hardware (4 x 2048
-//                   rows of 4096 bf16: 27.7 us, 4.8 TB/s; PyTorch's copy of
-//                   the same bytes 23.2)
+//                   4, 8 or 16 lanes or of whole warps, blocks handed out by
+//                   the hardware (4 x 2048 rows of 4096 bf16: 27.7 us, 4.8
+//                   TB/s; PyTorch's copy of the same bytes 23.2)
 // norm_kernel       forward, rows at other offsets or too long for that, and
 // norm_backward_kernel: resident blocks whose groups of threads each have a
 //                   ring of shared memory stages that bulk copies fill, so that
-//                   100 to 200 KB an SM are always under way.  A stage is a few
+//                   up to 160 KB an SM are always under way.  A stage is a few
 //                   rows; rows of any alignment are copied with the 16-byte
 //                   blocks that their ends lie in, and then read element by
-//                   element (3 x 5000 rows of 1021 f32: 25.8 us, 4.8 TB/s; with
+//                   element (3 x 5000 rows of 1021 f32: 24.1 us, 5.1 TB/s; with
 //                   loads to registers 36).  A thread keeps its columns, 8 to
 //                   32 of them, over all of its rows, and with them their
 //                   weights and, backward, their shares of dw and db; up to four
-//                   rows are summed at a time.  Backward 4 x 2048 x 4096 bf16
-//                   44 us, 4.6 TB/s; 8 x 8192 x 4096 275 us, 5.9 TB/s: the
+//                   rows are summed at a time, and the rows of a warp's teams of
+//                   lanes where rows are short.  Backward 4 x 2048 x 4096 bf16
+//                   44 us, 4.6 TB/s; 8 x 8192 x 4096 276 us, 5.8 TB/s: the
 //                   smaller call's blocks spend 6 us on their way to the first
 //                   row and 8 between the first SM's end and the last's.
 // norm_join_kernel  adds the blocks' shares of dw and db in a fixed order, so
@@ -51,7 +52,11 @@ namespace dt {
 namespace {
 
 constexpr int kNormThreads = 512;    // most threads of a block, and of a row
-constexpr uint32_t kSmemBytes = 208 * 1024;    // of the SM's 227 KB: rings
+// Rings, of the SM's 227 KB.  With more on its way than keeps HBM busy, some
+// SMs get a larger share of it than others and wait for those at the end
+// (backward, 4 x 8192 rows of 2048 f32: 145 us with 208 KB, the SMs busy for
+// 202000 to 246000 cycles; 133 with 160).
+constexpr uint32_t kSmemBytes = 160 * 1024;
 constexpr uint32_t kMaxStages = 8;
 constexpr uint32_t kStageTarget = 4096;
 constexpr int kLongThreads = 512;    // rows too long for registers
@@ -245,28 +250,44 @@ __device__ __forceinline__ const float4 *exchange(float4 v, Exchange &red, uint3
     return first;
 }
 
-template <int K>
-__device__ __forceinline__ void warp_sum(float (&v)[K])
+// The threads that share a ring: one warp or more of one row, or a warp of 32 / L
+// teams of L lanes, which take the rows of a stage in turn.
+template <int L>
+struct Team {
+    static constexpr uint32_t kTeams = 32 / L;
+    uint32_t tpr, group, team, t;
+    explicit __device__ __forceinline__ Team(uint32_t threads)
+        : tpr(L < 32 ? L : threads), group(threadIdx.x / (tpr * kTeams)), team(threadIdx.x / tpr % kTeams),
+          t(threadIdx.x % tpr)
+    {
+    }
+    __device__ __forceinline__ uint32_t threads() const { return tpr * kTeams; }
+    __device__ __forceinline__ bool first() const { return team == 0 && t == 0; }
+};
+
+// The sum over L lanes.
+template <int L>
+__device__ __forceinline__ float lane_sum(float v)
 {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-        for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], o);
+    for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
 }
 
-// Sums of V values (2, 4 or 8) over the tpr threads that share a row; every
-// thread gets the same sums, added in the same order.  Within a warp each step
-// halves the values a lane still carries as well as the lanes that share one:
-// 9 shuffles for 8 values, where one value after the other takes 40.  `red` is
-// double-buffered like exchange()'s.
-template <int V>
-__device__ __forceinline__ void row_sum(float (&v)[V], float (*red)[V][kNormThreads / 32], uint32_t &phase, uint32_t tpr,
-                                        uint32_t group)
+// Sums of V values (2, 4 or 8) over the threads that share a row, L lanes or
+// several warps; every thread gets the same sums, added in the same order.
+// Within a warp each step halves the values a lane still carries as well as the
+// lanes that share one: 9 shuffles for 8 values, where one value after the
+// other takes 40.  `red` is double-buffered like exchange()'s.
+template <int V, int L>
+__device__ __forceinline__ void row_sum(float (&v)[V], float (*red)[V][kNormThreads / 32], uint32_t &phase,
+                                        const Team<L> &m)
 {
-    constexpr uint32_t kLanes = 32 / V;   // lanes that hold the same value in the end
+    static_assert(V <= L, "a value to a lane at least");
+    constexpr uint32_t kLanes = L / V;   // lanes that hold the same value in the end
     const uint32_t lane = threadIdx.x & 31;
 #pragma unroll
-    for (int have = V, o = 16; o > 0; o >>= 1) {
+    for (int have = V, o = L / 2; o > 0; o >>= 1) {
         if (have > 1) {
             have /= 2;
             const bool up = lane & o;
@@ -279,12 +300,12 @@ __device__ __forceinline__ void row_sum(float (&v)[V], float (*red)[V][kNormThre
             v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], o);
         }
     }
-    float sum = v[0];                     // of value lane / kLanes
-    if (tpr > 32) {
-        const uint32_t warps = tpr >> 5, j = lane % kLanes;
+    float sum = v[0];                     // of value lane % L / kLanes
+    if (L == 32 && m.tpr > 32) {
+        const uint32_t warps = m.tpr >> 5, j = lane % kLanes;
         if (j == 0) red[phase][lane / kLanes][threadIdx.x >> 5] = sum;
-        asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(tpr) : "memory");
-        const float *of = &red[phase][lane / kLanes][group * warps];
+        asm volatile("bar.sync %0, %1;" ::"r"(m.group + 1), "r"(m.tpr) : "memory");
+        const float *of = &red[phase][lane / kLanes][m.group * warps];
         sum = 0.0f;
 #pragma unroll
         for (uint32_t k = 0; k < kNormThreads / 32; k += kLanes)
@@ -294,7 +315,7 @@ __device__ __forceinline__ void row_sum(float (&v)[V], float (*red)[V][kNormThre
         phase ^= 1;
     }
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = __shfl_sync(0xFFFFFFFFu, sum, i * kLanes);
+    for (int i = 0; i < V; ++i) v[i] = __shfl_sync(0xFFFFFFFFu, sum, i * kLanes, L);
 }
 
 // A group's walk over the rows: chunk c of the call is up to p.chunk_rows rows
@@ -368,9 +389,9 @@ struct Ring {
     }
     // Before the block goes on after a wait that ran out, a last, bounded wait
     // for what is still under way: each stage's last copy of group `part`.
-    __device__ __forceinline__ void drain(uint32_t t, uint64_t part) const
+    __device__ __forceinline__ void drain(bool first, uint64_t part) const
     {
-        if (!late || t != 0) return;
+        if (!late || !first) return;
         const uint64_t n = (p.chunks - part + p.parts - 1) / p.parts;
         for (uint32_t k = 0; k < p.stages && k < n; ++k)
             mbar_wait_bounded(bars + 8 * k, (uint32_t)((n - k + p.stages - 1) / p.stages - 1) & 1, p.sink.timeout_ns);
@@ -378,27 +399,27 @@ struct Ring {
 };
 
 // The group's ring; the waits for the kernel before and of the one after.
-template <typename T, bool BACK>
-__device__ __forceinline__ Ring<T, BACK> make_ring(const NormParams &p, unsigned char *smem, uint32_t group)
+template <typename T, bool BACK, int L>
+__device__ __forceinline__ Ring<T, BACK> make_ring(const NormParams &p, unsigned char *smem, const Team<L> &m)
 {
-    const uint32_t groups = blockDim.x / p.tpr, mine = p.stages * p.stage_bytes;
+    const uint32_t groups = blockDim.x / m.threads(), mine = p.stages * p.stage_bytes;
     const uint32_t bars = smem_addr(smem) + groups * mine;
     if (threadIdx.x == 0) {
         for (uint32_t k = 0; k < groups * p.stages; ++k) mbar_init(bars + 8 * k, 1);
         mbar_init_fence();
     }
     __syncthreads();
-    unsigned char *mem = smem + (size_t)group * mine;
+    unsigned char *mem = smem + (size_t)m.group * mine;
     pdl_begin();
-    return Ring<T, BACK>{p, smem_addr(mem), bars + 8 * group * p.stages, mem};
+    return Ring<T, BACK>{p, smem_addr(mem), bars + 8 * m.group * p.stages, mem};
 }
 
 // Its first copies.  They come after the weights' loads, which behind 25 MB of
 // rows would take 6 us.
 template <typename T, bool BACK>
-__device__ __forceinline__ void first_loads(const Ring<T, BACK> &ring, const NormParams &p, uint32_t t, uint64_t part)
+__device__ __forceinline__ void first_loads(const Ring<T, BACK> &ring, const NormParams &p, bool first, uint64_t part)
 {
-    if (t == 0)
+    if (first)
         for (uint32_t k = 0; k < p.stages; ++k) {
             const uint64_t c = part + (uint64_t)k * p.parts;
             if (c < p.chunks) ring.load(c, k);
@@ -408,11 +429,12 @@ __device__ __forceinline__ void first_loads(const Ring<T, BACK> &ring, const Nor
 // A row of a stage in registers: chunk c of thread t is elements [(c * tpr +
 // t) * VEC, + VEC).
 template <typename T, int VEC, int N>
-__device__ __forceinline__ void read_row(Chunk<T, VEC> (&c)[N], const NormParams &p, const T *row, uint32_t t, bool there)
+__device__ __forceinline__ void read_row(Chunk<T, VEC> (&c)[N], const NormParams &p, const T *row, uint32_t tpr, uint32_t t,
+                                         bool there)
 {
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-        const uint32_t e = (n * p.tpr + t) * VEC;
+        const uint32_t e = (n * tpr + t) * VEC;
         if (there && e < p.cols) c[n].load(row + e);
         else c[n].zero();
     }
@@ -449,7 +471,7 @@ __device__ __forceinline__ void row_moments(float sum, float &mean, float &m2, u
 // 1 / sqrt(v + eps), at most 2 ulp off.
 __device__ __forceinline__ float rstd_of(float m2, float inv_cols, float eps) { return rsqrtf(fmaf(m2, inv_cols, eps)); }
 
-template <typename T, int VEC, int N>
+template <typename T, int VEC, int N, int L>
 __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(const __grid_constant__ NormParams p)
 {
     constexpr bool kHold = N * VEC <= 16;   // wider rows read their weights again from L1
@@ -460,9 +482,11 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(const __grid_cons
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ float red[2][B][kNormThreads / 32];
     DT_TL_BEGIN();
-    const uint32_t tpr = p.tpr, group = threadIdx.x / tpr, t = threadIdx.x % tpr, cols = p.cols;
-    const uint64_t part = (uint64_t)group * gridDim.x + blockIdx.x;
-    Ring<T, false> ring = make_ring<T, false>(p, smem, group);
+    const Team<L> team(p.tpr);
+    constexpr uint32_t S = Team<L>::kTeams;
+    const uint32_t tpr = team.tpr, t = team.t, cols = p.cols;
+    const uint64_t part = (uint64_t)team.group * gridDim.x + blockIdx.x;
+    Ring<T, false> ring = make_ring<T, false>(p, smem, team);
     DT_TL_WAITED();
     const float inv = p.inv_cols;
     uint32_t phase = 0;
@@ -476,24 +500,25 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(const __grid_cons
     if constexpr (kHold)
 #pragma unroll
         for (int n = 0; n < N; ++n) weights(n);
-    first_loads(ring, p, t, part);
+    first_loads(ring, p, team.first(), part);
 
     for (uint64_t c = part; c < p.chunks; c += p.parts) {
         int r;
         uint64_t row;
         uint32_t rows;
         ring.chunk(c, r, row, rows);
-        const T *src = ring.at(0, static_cast<const T *>(p.x[r]) + row * cols);
-        T *y = static_cast<T *>(p.out[r]) + row * cols;
+        const T *src = ring.at(0, static_cast<const T *>(p.x[r]) + row * cols) + team.team * cols;
+        T *y = static_cast<T *>(p.out[r]) + (row + team.team) * cols;
         float *means = p.mean[r] ? p.mean[r] + row : nullptr, *rstds = p.rstd[r] ? p.rstd[r] + row : nullptr;
         ring.wait();
-        for (uint32_t k = 0; k < rows; k += B, src += B * cols, y += B * (uint64_t)cols) {
+        // this team's rows are the stage's k, k + S, ...
+        for (uint32_t k = team.team; k - team.team < rows; k += B * S, src += B * S * cols, y += (uint64_t)(B * S) * cols) {
             // B rows at a time; the last ones of a stage may stand beside rows of zeros
             C x[B][N];
             float s[B], m2[B];
 #pragma unroll
             for (int j = 0; j < B; ++j) {
-                read_row<T, VEC, N>(x[j], p, src + j * cols, t, k + j < rows);
+                read_row<T, VEC, N>(x[j], p, src + j * S * cols, tpr, t, k + j * S < rows);
                 V sum = C::all(0.0f);
 #pragma unroll
                 for (int n = 0; n < N; ++n) {
@@ -504,10 +529,10 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(const __grid_cons
                 }
                 s[j] = both(sum);
             }
-            row_sum<B>(s, red, phase, tpr, group);
-            if (tpr == 32) __syncwarp();
+            row_sum<B>(s, red, phase, team);
+            if (tpr <= 32) __syncwarp();
             // every thread has read its part of the stage's last rows
-            if (k + B >= rows && t == 0 && c + (uint64_t)p.stages * p.parts < p.chunks)
+            if (k - team.team + B * S >= rows && team.first() && c + (uint64_t)p.stages * p.parts < p.chunks)
                 ring.load(c + (uint64_t)p.stages * p.parts, ring.s);
 #pragma unroll
             for (int j = 0; j < B; ++j) {
@@ -516,7 +541,8 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(const __grid_cons
                 const V minus = C::all(-s[j]);
 #pragma unroll
                 for (int n = 0; n < N; ++n) {
-                    if ((n * tpr + t) * VEC >= cols) continue;
+                    const uint32_t e = (n * tpr + t) * VEC;
+                    if (e >= cols) continue;
                     V f[K];
                     x[j][n].get(f);
 #pragma unroll
@@ -527,13 +553,13 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(const __grid_cons
                 }
                 m2[j] = both(sum);
             }
-            row_sum<B>(m2, red, phase, tpr, group);
+            row_sum<B>(m2, red, phase, team);
 #pragma unroll
             for (int j = 0; j < B; ++j) {
-                if (k + j >= rows) continue;
+                if (k + j * S >= rows) continue;
                 m2[j] = rstd_of(m2[j], inv, p.eps);
                 const V minus = C::all(-s[j]), scale = C::all(m2[j]);
-                T *to = y + j * (uint64_t)cols;
+                T *to = y + j * S * (uint64_t)cols;
 #pragma unroll
                 for (int n = 0; n < N; ++n) {
                     const uint32_t e = (n * tpr + t) * VEC;
@@ -546,20 +572,20 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(const __grid_cons
                     if (NORM_OK(p.out, 2, r, to + e, VEC * sizeof(T), cols * sizeof(T))) C::store(to + e, f);
                 }
             }
-            // one lane to a row, of the group's last warp
-            const uint32_t lane = t - (tpr - 32);
-            if (lane < B && k + lane < rows) {
+            // one lane to a row, of the team's last warp
+            const uint32_t lane = t - (tpr - L), at = k + lane * S;
+            if (lane < B && at < rows) {
                 float mean = s[0], rstd = m2[0];
 #pragma unroll
                 for (int j = 1; j < B; ++j)
                     if (lane == j) mean = s[j], rstd = m2[j];
-                if (means && NORM_OK(p.mean, 3, r, means + k + lane, 4, 4)) means[k + lane] = mean;
-                if (rstds && NORM_OK(p.rstd, 4, r, rstds + k + lane, 4, 4)) rstds[k + lane] = rstd;
+                if (means && NORM_OK(p.mean, 3, r, means + at, 4, 4)) means[at] = mean;
+                if (rstds && NORM_OK(p.rstd, 4, r, rstds + at, 4, 4)) rstds[at] = rstd;
             }
         }
         ring.next();
     }
-    ring.drain(t, part);
+    ring.drain(team.first(), part);
     DT_TL_END_BLOCK(DT_TL_NORM);
 }
 
@@ -587,16 +613,19 @@ __device__ __forceinline__ void read_param(const NormParams &p, const void *q, u
     }
 }
 
-// A row in the registers of tpr threads, up to 4 vectors each, and blocks of a
+// A row in the registers of tpr threads, mostly 4 vectors each, and blocks of a
 // few rows that the hardware hands to the SMs as they come free: resident
 // blocks that share the rows out evenly took 37 us for 4 x 2048 rows of 4096
 // bf16, this 27.7.  64 registers a thread leave room for eight rows an SM; a
 // row takes 3 us, of which 1 is its loads'.  Tried: 1, 2, 8, 16 vectors a
 // thread 66, 43, 35, 38 us (with 4: 34 at that stage); the rows' weights in
 // shared memory 40, bound by reading them there.
+// L: lanes of a warp that share a row.  Short rows share a warp, four vectors a
+// lane: a warp to a row took 230, 118, 67, 48 us for 100 MB of rows of 64, 128,
+// 256, 512 bf16, this 46, 38, 41, 41.
 // EARLY: the weights are loaded along with the row, for calls of few rows,
 // where only the time from the first load to the last store counts.
-template <typename T, int VEC, int N, bool EARLY>
+template <typename T, int VEC, int N, int L, bool EARLY>
 __global__ void __launch_bounds__(EARLY || N < 4 ? kNormThreads : 256, EARLY || N < 4 ? 1 : 4)
 norm_rows_kernel(const __grid_constant__ NormParams p)
 {
@@ -609,7 +638,8 @@ norm_rows_kernel(const __grid_constant__ NormParams p)
     const uint32_t tpr = p.tpr, group = threadIdx.x / tpr, t = threadIdx.x % tpr, cols = p.cols;
     const int r = blockIdx.y;   // a search for the rank took a tenth of a row's instructions
     const uint64_t row = (uint64_t)blockIdx.x * (blockDim.x / tpr) + group;
-    if (row < p.row_end[r] - (r ? p.row_end[r - 1] : 0)) {
+    const bool there = row < p.row_end[r] - (r ? p.row_end[r - 1] : 0);
+    if (L < 32 || there) {   // all rows of a warp pass through its shuffles
         const T *src = static_cast<const T *>(p.x[r]) + row * cols;
         T *y = static_cast<T *>(p.out[r]) + row * cols;
         C x[N];
@@ -617,9 +647,9 @@ norm_rows_kernel(const __grid_constant__ NormParams p)
         uint32_t mine = 0, phase = 0;
 #pragma unroll
         for (int n = 0; n < N; ++n) {
-            const uint32_t first = (n * tpr + (t & ~31u)) * VEC, e = (n * tpr + t) * VEC;
-            mine += first < cols ? min(cols - first, 32u * VEC) : 0;
-            if (e < cols && NORM_OK(p.x, 0, r, src + e, VEC * sizeof(T), cols * sizeof(T))) x[n].load(src + e);
+            const uint32_t first = (n * tpr + t / L * L) * VEC, e = (n * tpr + t) * VEC;
+            mine += first < cols ? min(cols - first, (uint32_t)(L * VEC)) : 0;
+            if (e < cols && there && NORM_OK(p.x, 0, r, src + e, VEC * sizeof(T), cols * sizeof(T))) x[n].load(src + e);
             else x[n].zero();
         }
         if constexpr (EARLY)
@@ -640,9 +670,8 @@ norm_rows_kernel(const __grid_constant__ NormParams p)
 #pragma unroll
             for (int i = 0; i < C::K; ++i) s[(n * C::K + i) & 3] = add(s[(n * C::K + i) & 3], f[i]);
         }
-        float sum[1] = {both(add(add(s[0], s[1]), add(s[2], s[3])))};
-        warp_sum<1>(sum);
-        float mean = sum[0] * inv_mine;
+        const float sum = lane_sum<L>(both(add(add(s[0], s[1]), add(s[2], s[3]))));
+        float mean = sum * inv_mine;
 #pragma unroll
         for (int n = 0; n < N; ++n) {
             if ((n * tpr + t) * VEC >= cols) continue;
@@ -654,10 +683,9 @@ norm_rows_kernel(const __grid_constant__ NormParams p)
                 m[(n * C::K + i) & 3] = fma(d, d, m[(n * C::K + i) & 3]);
             }
         }
-        float m2[1] = {both(add(add(m[0], m[1]), add(m[2], m[3])))};
-        warp_sum<1>(m2);
-        row_moments(sum[0], mean, m2[0], mine, p.inv_cols, red, phase, tpr, group);
-        const float rstd = rstd_of(m2[0], p.inv_cols, p.eps);
+        float m2 = lane_sum<L>(both(add(add(m[0], m[1]), add(m[2], m[3]))));
+        if constexpr (L == 32) row_moments(sum, mean, m2, mine, p.inv_cols, red, phase, tpr, group);
+        const float rstd = rstd_of(m2, p.inv_cols, p.eps);
         const V minus = C::all(-mean), scale = C::all(rstd);
         auto finish = [&](auto kind) {
             constexpr int KIND = decltype(kind)::value;
@@ -665,7 +693,7 @@ norm_rows_kernel(const __grid_constant__ NormParams p)
 #pragma unroll
             for (int n = 0; n < N; ++n) {
                 const uint32_t e = (n * tpr + t) * VEC;
-                if (e >= cols) continue;
+                if (e >= cols || !there) continue;
                 constexpr int k = EARLY ? 1 : 0;
                 if constexpr (!EARLY) {
                     read_param<C, VEC, KIND>(p, p.weight, e, 1.0f, w[0]);
@@ -681,7 +709,7 @@ norm_rows_kernel(const __grid_constant__ NormParams p)
         if (EARLY || p.param_kind == kParamAny) finish(std::integral_constant<int, kParamAny>());
         else if (p.param_kind == kParamBf16) finish(std::integral_constant<int, kParamBf16>());
         else finish(std::integral_constant<int, kParamF32>());
-        if (t == 0) {
+        if (t == 0 && there) {
             if (p.mean[r] && NORM_OK(p.mean, 3, r, p.mean[r] + row, 4, 4)) p.mean[r][row] = mean;
             if (p.rstd[r] && NORM_OK(p.rstd, 4, r, p.rstd[r] + row, 4, 4)) p.rstd[r][row] = rstd;
         }
@@ -689,7 +717,15 @@ norm_rows_kernel(const __grid_constant__ NormParams p)
     DT_TL_END_BLOCK(DT_TL_NORM);
 }
 
-template <typename T, int VEC, int N>
+__device__ __forceinline__ float from_lane(float x, uint32_t o) { return __shfl_xor_sync(0xFFFFFFFFu, x, o); }
+__device__ __forceinline__ F2 from_lane(F2 x, uint32_t o)
+{
+    float a, b;
+    split(x, a, b);
+    return pair(from_lane(a, o), from_lane(b, o));
+}
+
+template <typename T, int VEC, int N, int L>
 __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_kernel(const __grid_constant__ NormParams p)
 {
     constexpr bool kHold = N * VEC <= 16;   // wider rows read their weights again from L1
@@ -700,9 +736,11 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_kernel(const __
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ float red[2][2 * B][kNormThreads / 32];
     DT_TL_BEGIN();
-    const uint32_t tpr = p.tpr, group = threadIdx.x / tpr, t = threadIdx.x % tpr, cols = p.cols;
-    const uint64_t part = (uint64_t)group * gridDim.x + blockIdx.x;
-    Ring<T, true> ring = make_ring<T, true>(p, smem, group);
+    const Team<L> team(p.tpr);
+    constexpr uint32_t S = Team<L>::kTeams;
+    const uint32_t tpr = team.tpr, t = team.t, cols = p.cols;
+    const uint64_t part = (uint64_t)team.group * gridDim.x + blockIdx.x;
+    Ring<T, true> ring = make_ring<T, true>(p, smem, team);
     DT_TL_WAITED();
     const float inv = p.inv_cols;
     uint32_t phase = 0;
@@ -717,33 +755,35 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_kernel(const __
         for (int i = 0; i < K; ++i) dw[n][i] = db[n][i] = w[n][i] = C::all(0.0f);
         if constexpr (kHold) weights(n);
     }
-    first_loads(ring, p, t, part);
+    first_loads(ring, p, team.first(), part);
 
     for (uint64_t c = part; c < p.chunks; c += p.parts) {
         int r;
         uint64_t row;
         uint32_t rows;
         ring.chunk(c, r, row, rows);
-        const T *xs = ring.at(0, static_cast<const T *>(p.x[r]) + row * cols);
-        const T *gs = ring.at(p.array_bytes, static_cast<const T *>(p.dy[r]) + row * cols);
+        const T *xs = ring.at(0, static_cast<const T *>(p.x[r]) + row * cols) + team.team * cols;
+        const T *gs = ring.at(p.array_bytes, static_cast<const T *>(p.dy[r]) + row * cols) + team.team * cols;
         const float *means = ring.at(2 * p.array_bytes, p.mean[r] + row);
         const float *rstds = ring.at(2 * p.array_bytes + p.stat_bytes, p.rstd[r] + row);
-        T *dx = static_cast<T *>(p.out[r]) + row * cols;
+        T *dx = static_cast<T *>(p.out[r]) + (row + team.team) * cols;
         ring.wait();
-        for (uint32_t k = 0; k < rows; k += B, xs += B * cols, gs += B * cols, dx += B * (uint64_t)cols) {
+        // this team's rows are the stage's k, k + S, ...
+        for (uint32_t k = team.team; k - team.team < rows;
+             k += B * S, xs += B * S * cols, gs += B * S * cols, dx += (uint64_t)(B * S) * cols) {
             // B rows at a time; the last ones of a stage may stand beside rows of zeros
             float mean[B], rstd[B];
 #pragma unroll
             for (int j = 0; j < B; ++j) {
-                mean[j] = k + j < rows ? means[k + j] : 0.0f;
-                rstd[j] = k + j < rows ? rstds[k + j] : 0.0f;
+                mean[j] = k + j * S < rows ? means[k + j * S] : 0.0f;
+                rstd[j] = k + j * S < rows ? rstds[k + j * S] : 0.0f;
             }
             C x[B][N], g[B][N];
             float s[2 * B];
 #pragma unroll
             for (int j = 0; j < B; ++j) {
-                read_row<T, VEC, N>(x[j], p, xs + j * cols, t, k + j < rows);
-                read_row<T, VEC, N>(g[j], p, gs + j * cols, t, k + j < rows);
+                read_row<T, VEC, N>(x[j], p, xs + j * S * cols, tpr, t, k + j * S < rows);
+                read_row<T, VEC, N>(g[j], p, gs + j * S * cols, tpr, t, k + j * S < rows);
                 V sq = C::all(0.0f), sh = C::all(0.0f);
                 const V minus = C::all(-mean[j]), scale = C::all(rstd[j]);
 #pragma unroll
@@ -765,19 +805,19 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_kernel(const __
                 s[2 * j] = both(sq);
                 s[2 * j + 1] = both(sh);
             }
-            row_sum<2 * B>(s, red, phase, tpr, group);
-            if (tpr == 32) __syncwarp();
+            row_sum<2 * B>(s, red, phase, team);
+            if (tpr <= 32) __syncwarp();
             // every thread has read its part of the stage's last rows
-            if (k + B >= rows && t == 0 && c + (uint64_t)p.stages * p.parts < p.chunks)
+            if (k - team.team + B * S >= rows && team.first() && c + (uint64_t)p.stages * p.parts < p.chunks)
                 ring.load(c + (uint64_t)p.stages * p.parts, ring.s);
 #pragma unroll
             for (int j = 0; j < B; ++j) {
-                if (k + j >= rows) continue;
+                if (k + j * S >= rows) continue;
                 // dx = rstd (q - mean(q)) - a rstd^2 mean(q h), h = a rstd
                 const V c0 = C::all(-s[2 * j] * inv * rstd[j]);
                 const V c1 = C::all(-s[2 * j + 1] * inv * rstd[j] * rstd[j] * rstd[j]);
                 const V minus = C::all(-mean[j]), scale = C::all(rstd[j]);
-                T *to = dx + j * (uint64_t)cols;
+                T *to = dx + j * S * (uint64_t)cols;
 #pragma unroll
                 for (int n = 0; n < N; ++n) {
                     const uint32_t e = (n * tpr + t) * VEC;
@@ -794,29 +834,41 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_kernel(const __
         }
         ring.next();
     }
-    ring.drain(t, part);
+    ring.drain(team.first(), part);
     if (p.partial) {
-        // the groups' shares are added in the rings' place, in ascending order
-        __syncthreads();
-        float *all = reinterpret_cast<float *>(smem);
-        const uint32_t groups = blockDim.x / tpr;
-        for (uint32_t k = 0; k < groups; ++k) {
-            if (group == k)
+        // the teams of a warp add theirs, then the block its groups', in ascending
+        // order, in the rings' place (512 threads' columns take at most 128 KB)
 #pragma unroll
-                for (int n = 0; n < N; ++n) {
-                    const uint32_t e = (n * tpr + t) * VEC;
-                    if (e >= cols) continue;
+        for (uint32_t o = 16; o >= (uint32_t)L; o >>= 1)
 #pragma unroll
-                    for (int i = 0; i < K; ++i) {   // cols is even where there are pairs
-                        V *w0 = reinterpret_cast<V *>(all + e) + i, *b0 = reinterpret_cast<V *>(all + cols + e) + i;
-                        *w0 = k ? add(*w0, dw[n][i]) : dw[n][i];
-                        *b0 = k ? add(*b0, db[n][i]) : db[n][i];
-                    }
+            for (int n = 0; n < N; ++n)
+#pragma unroll
+                for (int i = 0; i < K; ++i) {
+                    dw[n][i] = add(dw[n][i], from_lane(dw[n][i], o));
+                    db[n][i] = add(db[n][i], from_lane(db[n][i], o));
                 }
-            __syncthreads();
-        }
+        __syncthreads();
+        float *all = reinterpret_cast<float *>(smem), *mine = all + (size_t)team.group * 2 * cols;
+        if (team.team == 0)
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                const uint32_t e = (n * tpr + t) * VEC;
+                if (e >= cols) continue;
+#pragma unroll
+                for (int i = 0; i < K; ++i) {   // cols is even where there are pairs
+                    reinterpret_cast<V *>(mine + e)[i] = dw[n][i];
+                    reinterpret_cast<V *>(mine + cols + e)[i] = db[n][i];
+                }
+            }
+        __syncthreads();
+        const uint32_t groups = blockDim.x / team.threads();
         float *out = p.partial + (uint64_t)blockIdx.x * 2 * cols;
-        for (uint32_t e = threadIdx.x; e < 2 * cols; e += blockDim.x) out[e] = all[e];
+        for (uint32_t e = threadIdx.x; e < 2 * cols; e += blockDim.x) {
+            float v = all[e];
+#pragma unroll 4
+            for (uint32_t k = 1; k < groups; ++k) v += all[(size_t)k * 2 * cols + e];
+            out[e] = v;
+        }
     }
     DT_TL_END_BLOCK(DT_TL_NORM);
 }
@@ -871,13 +923,13 @@ __global__ void __launch_bounds__(kLongThreads) norm_long_kernel(const __grid_co
         };
         float s[2] = {0.0f, 0.0f}, m2[2] = {0.0f, 0.0f};
         for (uint32_t e = threadIdx.x; e < p.cols; e += kLongThreads) s[0] += at(e);
-        row_sum<2>(s, red, phase, kLongThreads, 0);
+        row_sum<2>(s, red, phase, Team<32>(kLongThreads));
         const float mean = s[0] * p.inv_cols;
         for (uint32_t e = threadIdx.x; e < p.cols; e += kLongThreads) {
             const float d = at(e) - mean;
             m2[0] = fmaf(d, d, m2[0]);
         }
-        row_sum<2>(m2, red, phase, kLongThreads, 0);
+        row_sum<2>(m2, red, phase, Team<32>(kLongThreads));
         const float rstd = rstd_of(m2[0], p.inv_cols, p.eps);
         for (uint32_t e = threadIdx.x; e < p.cols; e += kLongThreads) {
             const float f = fmaf((at(e) - mean) * rstd, param(p.weight, p.weight_bf16, e, 1.0f),
@@ -921,7 +973,7 @@ __global__ void __launch_bounds__(kLongThreads) norm_backward_long_kernel(const 
             s[0] += q;
             s[1] = fmaf(q, h_at(e), s[1]);
         }
-        row_sum<2>(s, red, phase, kLongThreads, 0);
+        row_sum<2>(s, red, phase, Team<32>(kLongThreads));
         const float mq = s[0] * p.inv_cols, mqh = s[1] * p.inv_cols;
         for (uint32_t e = threadIdx.x; e < p.cols; e += kLongThreads) {
             const float f = rstd * (q_at(e) - mq - h_at(e) * mqh);
@@ -964,25 +1016,29 @@ __global__ void __launch_bounds__(kThreads) norm_columns_long_kernel(const __gri
 using NormFn = void (*)(NormParams);
 
 // The kernel for rows of `cols` elements, either way, and the threads that
-// share a row: 8 columns a thread, or 16 or 32 where that keeps the row within
-// 256 threads, so that two groups or more share an SM and one computes while
-// another waits at its barrier (4 x 2048 x 4096 backward: over 512 threads 47.0
-// us, over 256 46.6).  Past 256 threads of 32 columns a row may have 512; beyond
-// that, a thread's sums for its columns would not fit in registers.
+// share a row: 16 columns of bf16 or 8 of f32 a thread (bf16 8 where that leaves
+// fewer threads idle), in as few lanes of a warp as that takes; or 16 where
+// that keeps the row within 256 threads, so that two groups or more share an
+// SM and one computes while another waits at its barrier (4 x 2048 x 4096
+// backward: over 512 threads 47.0 us, over 256 46.6).  Past 256 threads of 32
+// columns a row may have 512; beyond that, a thread's sums for its columns
+// would not fit in registers.  100 MB of rows of 64, 128, 384 bf16 backward: 8
+// columns and a warp to a row 161, 93, 100 us; this 61, 61, 75.
 struct NormPick {
     NormFn fn = nullptr;
-    uint32_t tpr = 0, rows = 0;   // rows it sums at a time
+    uint32_t tpr = 0, threads = 0, rows = 0;   // of a row; of a group, and the rows that it sums at a time
 };
 
-template <typename T, int VEC, int N, bool BACK>
+template <typename T, int VEC, int N, int L, bool BACK>
 void try_pick(NormPick &k, uint32_t chunks, uint32_t most)
 {
-    const uint32_t tpr = ((chunks + N - 1) / N + 31) / 32 * 32;
-    if (k.fn || tpr > most) return;
-    if constexpr (BACK) k.fn = norm_backward_kernel<T, VEC, N>;
-    else k.fn = norm_kernel<T, VEC, N>;
+    const uint32_t tpr = L < 32 ? L : ((chunks + N - 1) / N + 31) / 32 * 32;
+    if (k.fn || tpr > most || chunks > tpr * N) return;
+    if constexpr (BACK) k.fn = norm_backward_kernel<T, VEC, N, L>;
+    else k.fn = norm_kernel<T, VEC, N, L>;
     k.tpr = tpr;
-    k.rows = rows_at_once<T, VEC, N, BACK>();
+    k.threads = L < 32 ? 32 : tpr;
+    k.rows = rows_at_once<T, VEC, N, BACK>() * (32 / L);
 }
 
 template <typename T, int VEC, bool BACK>
@@ -990,17 +1046,23 @@ NormPick pick_norm(uint32_t cols)
 {
     NormPick k;
     const uint32_t chunks = (cols + VEC - 1) / VEC;
-    if constexpr (VEC == 1) {
-        try_pick<T, VEC, 8, BACK>(k, chunks, 256);
-        try_pick<T, VEC, 16, BACK>(k, chunks, kNormThreads);
+    if constexpr (VEC == 1) {   // 65 f32, 100 MB: a warp to a row 87 us forward, 8 lanes' 8 columns 44
+        try_pick<T, VEC, 8, 8, BACK>(k, chunks, 32);
+        try_pick<T, VEC, 8, 16, BACK>(k, chunks, 32);
+        try_pick<T, VEC, 8, 32, BACK>(k, chunks, 256);
+        try_pick<T, VEC, 16, 32, BACK>(k, chunks, kNormThreads);
     } else if constexpr (!BACK) {   // what is left to this kernel is longer than 256 threads of 4 vectors
-        try_pick<T, VEC, 32 / VEC, BACK>(k, chunks, kNormThreads);
+        try_pick<T, VEC, 32 / VEC, 32, BACK>(k, chunks, kNormThreads);
     } else {
-        try_pick<T, VEC, 1, BACK>(k, chunks, 32);
-        try_pick<T, VEC, 8 / VEC, BACK>(k, chunks, 256);
-        try_pick<T, VEC, 16 / VEC, BACK>(k, chunks, 256);
-        try_pick<T, VEC, 16 / VEC, BACK>(k, chunks, kNormThreads);
-        try_pick<T, VEC, 32 / VEC, BACK>(k, chunks, kNormThreads);
+        try_pick<T, VEC, 2, 4, BACK>(k, chunks, 32);
+        try_pick<T, VEC, 2, 8, BACK>(k, chunks, 32);
+        try_pick<T, VEC, 2, 16, BACK>(k, chunks, 32);
+        if constexpr (VEC == 8)
+            if ((chunks + 31) / 32 * 32 * 1.1 < (chunks + 63) / 64 * 64) try_pick<T, VEC, 1, 32, BACK>(k, chunks, 256);
+        try_pick<T, VEC, 2, 32, BACK>(k, chunks, 256);
+        if constexpr (VEC == 4) try_pick<T, VEC, 4, 32, BACK>(k, chunks, 256);
+        try_pick<T, VEC, 16 / VEC, 32, BACK>(k, chunks, kNormThreads);
+        try_pick<T, VEC, 32 / VEC, 32, BACK>(k, chunks, kNormThreads);
     }
     return k;
 }
@@ -1013,28 +1075,38 @@ NormPick pick_norm(int dtype, bool vec, uint32_t cols)
 }
 
 // The kernel that has a row in registers, and the threads of a row.  Few rows:
-// as many threads as a row has vectors.  Else, for rows of whole vectors, a
-// warp to a row or 4 vectors a thread (16384 bf16 rows of 512: 1, 2, 4 vectors
-// 29, 19, 23 us).
+// as many threads as a row has vectors.  Else, for rows of whole vectors, 4
+// vectors a thread in as few lanes of a warp as that takes, or 4 to 6 vectors
+// and whole warps, whichever leaves the fewest threads idle (100 MB of rows of
+// 2056 bf16: 4 and 5 vectors 58, 49 us; of 640 f32 40, 32).
 template <typename T, int VEC>
 NormPick pick_rows(uint32_t cols, bool few)
 {
     NormPick k;
     const uint32_t chunks = (cols + VEC - 1) / VEC;
-    auto try_rows = [&](NormFn fn, uint32_t n, uint32_t most) {
-        const uint32_t tpr = ((chunks + n - 1) / n + 31) / 32 * 32;
-        if (k.fn || tpr > most) return;
+    auto take = [&](NormFn fn, uint32_t tpr) {
         k.fn = fn;
         k.tpr = tpr;
     };
+    auto warps = [&](uint32_t n) { return ((chunks + n - 1) / n + 31) / 32 * 32; };
     if (few) {
-        try_rows(norm_rows_kernel<T, VEC, 1, true>, 1, kNormThreads);
-        try_rows(norm_rows_kernel<T, VEC, 2, true>, 2, kNormThreads);
+        if (warps(1) <= kNormThreads) take(norm_rows_kernel<T, VEC, 1, 32, true>, warps(1));
+        else if (warps(2) <= kNormThreads) take(norm_rows_kernel<T, VEC, 2, 32, true>, warps(2));
+        if (k.fn) return k;
     }
     if constexpr (VEC > 1) {
-        try_rows(norm_rows_kernel<T, VEC, 1, false>, 1, 32);
-        try_rows(norm_rows_kernel<T, VEC, 2, false>, 2, 32);
-        try_rows(norm_rows_kernel<T, VEC, 4, false>, 4, 256);
+        // what a row costs: its threads' vectors, and more where a block has one of an odd number of warps
+        auto cost = [&](uint32_t n, uint32_t most, double factor) {
+            const uint32_t t = warps(n);
+            return t > most ? 1e30 : n * t * factor * (t & (t - 1) ? 1.15 : 1.0);
+        };
+        const double c4 = cost(4, 256, 1.0), c5 = cost(5, 128, 1.08), c6 = cost(6, 128, 1.12);
+        if (chunks <= 16) take(norm_rows_kernel<T, VEC, 4, 4, false>, 4);
+        else if (chunks <= 32) take(norm_rows_kernel<T, VEC, 4, 8, false>, 8);
+        else if (chunks <= 64) take(norm_rows_kernel<T, VEC, 4, 16, false>, 16);
+        else if (c4 <= c5 && c4 <= c6 && c4 < 1e30) take(norm_rows_kernel<T, VEC, 4, 32, false>, warps(4));
+        else if (c5 <= c6 && c5 < 1e30) take(norm_rows_kernel<T, VEC, 5, 32, false>, warps(5));
+        else if (c6 < 1e30) take(norm_rows_kernel<T, VEC, 6, 32, false>, warps(6));
     }
     return k;
 }
@@ -1055,8 +1127,8 @@ NormShape norm_shape(NormParams &p, const NormPick &k, int dtype, bool vec, bool
 {
     const uint64_t row_bytes = (uint64_t)p.cols * (dtype == DT_BF16 ? 2 : 4), sms = (uint64_t)sm_count(device);
     p.tpr = k.tpr;
-    uint64_t groups = kNormThreads / k.tpr;
-    if (k.tpr > 32) groups = std::min<uint64_t>(groups, 15);   // named barriers
+    uint64_t groups = kNormThreads / k.threads;
+    if (k.threads > 32) groups = std::min<uint64_t>(groups, 15);   // named barriers
     // rows of a stage: those summed at once, and more where they are short,
     // but not so many that groups go without
     uint64_t per = std::max<uint64_t>(kStageTarget / row_bytes, k.rows);
@@ -1074,8 +1146,8 @@ NormShape norm_shape(NormParams &p, const NormPick &k, int dtype, bool vec, bool
     p.stage_bytes = back ? 2 * (p.array_bytes + p.stat_bytes) : p.array_bytes;
     const uint64_t depth = (p.chunks + p.parts - 1) / p.parts;
     p.stages = (uint32_t)std::max<uint64_t>(1, std::min({(uint64_t)kMaxStages, kSmemBytes / (groups * p.stage_bytes), depth}));
-    const size_t rings = groups * p.stages * (p.stage_bytes + 8), sums = back ? 2 * (size_t)p.cols * sizeof(float) : 0;
-    return {(uint32_t)grid, (uint32_t)(groups * p.tpr), std::max(rings, sums)};
+    const size_t rings = groups * p.stages * (p.stage_bytes + 8), sums = back ? groups * 2 * (size_t)p.cols * sizeof(float) : 0;
+    return {(uint32_t)grid, (uint32_t)(groups * k.threads), std::max(rings, sums)};
 }
 
 cudaError_t launch_rows(NormFn fn, const NormShape &n, const NormParams &p, cudaStream_t s)

@@ -191,6 +191,40 @@ def test_not_finite_rows_stay_in_their_rows(dt):
             assert torch.equal(y[r][keep], clean[0][r][keep])
 
 
+# Rows that share a warp, four to 32 lanes each, and widths that are taken in 4,
+# 5 and 6 vectors a thread; the last warps have fewer rows than they could.
+@pytest.mark.parametrize("cols", [3, 8, 24, 33, 64, 65, 72, 128, 136, 200, 256, 264, 400, 512, 520, 640, 1280, 2056, 3000])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_many_rows_of_few_columns_and_between_powers_of_two(dt, dtype, cols):
+    rows = [403, 0, 1, 350]
+    x, dy, w, b = make(rows, cols, dtype, "f32", seed=cols)
+    with group(len(rows)) as g:
+        y, mean, rstd = forward(dt, g, x, w, b, rows, cols, dtype, "f32")
+        check_forward(x, w, b, y, mean, rstd, dtype)
+        dx, dw, db = backward(dt, g, x, dy, w, mean, rstd, rows, cols, dtype, "f32")
+        check_backward(x, dy, w, mean, rstd, dx, dw, db, dtype, "f32")
+        again = backward(dt, g, x, dy, w, mean, rstd, rows, cols, dtype, "f32")
+        assert torch.equal(dw, again[1]) and torch.equal(db, again[2])
+        assert dt.dt_group_check(g) == dt.DT_OK
+
+
+@pytest.mark.parametrize("dtype,cols", [("bf16", 64), ("bf16", 40), ("f32", 32), ("f32", 17)])
+def test_not_finite_rows_leave_the_rows_of_their_warp_alone(dt, dtype, cols):
+    rows = [310, 9]
+    x, dy, w, b = make(rows, cols, dtype, "f32", seed=cols)
+    clean = [t.clone() for t in x]
+    with group(2) as g:
+        y0, mean0, rstd0 = forward(dt, g, clean, w, b, rows, cols, dtype, "f32")
+        dx0 = backward(dt, g, clean, dy, w, mean0, rstd0, rows, cols, dtype, "f32")[0]
+        x[0][5, 0], x[0][6, cols - 1], x[0][309, 1], x[1][8, 2] = float("nan"), float("inf"), -float("inf"), float("nan")
+        y, mean, rstd = forward(dt, g, x, w, b, rows, cols, dtype, "f32")
+        dx = backward(dt, g, x, dy, w, mean, rstd, rows, cols, dtype, "f32")[0]
+        for r, bad in ((0, [5, 6, 309]), (1, [8])):
+            keep = [k for k in range(rows[r]) if k not in bad]
+            assert torch.equal(y[r][keep], y0[r][keep]) and torch.equal(dx[r][keep], dx0[r][keep])
+            assert not torch.isfinite(mean[r][bad]).any()
+
+
 @pytest.mark.parametrize("dtype,cols", [("f32", 96), ("f32", 1021), ("bf16", 256)])
 def test_gradients_against_differences(dt, dtype, cols):
     # sum(dy * y) along random directions of x, weight and bias, by central
