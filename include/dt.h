@@ -28,8 +28,8 @@
  * rank's own) or every rank gets DT_ERR_INVALID.  A rank whose partners do
  * not all arrive within the group's time limit gets DT_ERR_TIMEOUT and the
  * group is poisoned until dt_group_reset.  Ranks of one group must not mix
- * rank-local and group-wide calls within a round.  dt_bucket_allreduce is
- * group-wide only.
+ * rank-local and group-wide calls within a round.  dt_bucket_allreduce, the
+ * layer norm and the vocabulary loss are group-wide only.
  *
  * Conventions shared by every entry point:
  *   Streams   `stream` is a cudaStream_t passed as void* (NULL = the legacy
@@ -375,8 +375,9 @@ size_t dt_layer_norm_workspace(dt_group_t g, size_t cols);
  *                vocab[0] + ... + vocab[r - 1].  A rank may have none, all
  *                ranks together need one.
  *   targets      [tokens] int32 vocabulary indices on the device, or
- *                ignore_index: that token's loss and gradient are 0 and it is
- *                not counted.  Any other value outside the vocabulary is
+ *                ignore_index: that token's loss and dhidden are 0, it is not
+ *                counted, and its hidden row enters dweight as a product with
+ *                0 (so a NaN or an infinity there makes dweight NaN).  Any other value outside the vocabulary is
  *                treated the same way and recorded as DT_ERR_INVALID in the
  *                group's error word (dt_group_error_detail: rank -1, peer =
  *                the token, generation = the value).

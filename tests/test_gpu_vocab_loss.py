@@ -235,6 +235,23 @@ def test_not_finite_tokens_stay_in_their_rows(dt):
         assert torch.equal(losses[~bad], clean[0][~bad]) and torch.equal(lse[~bad], clean[1][~bad])
 
 
+@pytest.mark.parametrize("tokens,vocab,dim", [(40, [300, 500], 64), (300, [700, 1000], 200)])
+def test_what_ignored_tokens_hold_reaches_no_other_token(dt, tokens, vocab, dim):
+    h, w, t = make(tokens, vocab, dim, seed=13)
+    drop = torch.nonzero(t == IGNORE)[:, 0]
+    assert len(drop) >= 3
+    bad = h.clone()
+    bad[drop[0]], bad[drop[1], 3], bad[drop[2], 0] = float("nan"), float("inf"), -float("inf")
+    with group(2) as g:
+        losses, lse, loss = forward(dt, g, h, w, t)
+        dh = backward(dt, g, h, w, t, lse)[0]
+        losses_b, lse_b, loss_b = forward(dt, g, bad, w, t)
+        dh_b = backward(dt, g, bad, w, t, lse_b)[0]
+        assert torch.equal(losses, losses_b) and torch.equal(loss, loss_b) and torch.equal(dh, dh_b)
+        assert not dh_b[drop].any() and not losses_b[drop].any()
+        assert dt.dt_group_check(g) == dt.DT_OK
+
+
 def test_gradients_against_differences(dt):
     # the loss along random directions of hidden and weight, by central
     # differences of the definition in 64 bits
