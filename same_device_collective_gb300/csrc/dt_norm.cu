@@ -106,6 +106,19 @@ __device__ __forceinline__ float add(float a, float b) { return a + b; }
 __device__ __forceinline__ float mul(float a, float b) { return a * b; }
 __device__ __forceinline__ float fma(float a, float b, float c) { return fmaf(a, b, c); }
 __device__ __forceinline__ float both(float x) { return x; }
+__device__ __forceinline__ float first_of(F2 x)
+{
+    float a, b;
+    split(x, a, b);
+    return a;
+}
+__device__ __forceinline__ float second_of(F2 x)
+{
+    float a, b;
+    split(x, a, b);
+    return b;
+}
+__device__ __forceinline__ float first_of(float x) { return x; }
 
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(uint16_t x) { return bf16_to_f32(x); }
@@ -449,17 +462,42 @@ __host__ __device__ constexpr int rows_at_once()
     return regs <= 8 ? 4 : regs <= 16 ? 2 : 1;
 }
 
+// sum + low is the sum of what was added, to about twice fp32's digits: `low`
+// collects what each addition rounds off.
+template <typename V>
+__device__ __forceinline__ void exact_add(V &sum, V &low, V x, V minus_one)
+{
+    const V t = add(sum, x), of_x = fma(sum, minus_one, t);
+    low = add(low, add(fma(fma(of_x, minus_one, t), minus_one, sum), fma(of_x, minus_one, x)));
+    sum = t;
+}
+
+// Without it where the sum is no number.
+__device__ __forceinline__ float with_low(float sum, float low) { return sum - sum == 0.0f ? sum + low : sum; }
+
 // The mean and the sum of squared distances from it, of all warps that share a
 // row from each one's own: M2 = sum of M2_w + n_w (mean_w - mean)^2.
 __device__ __forceinline__ void row_moments(float sum, float &mean, float &m2, uint32_t mine, float inv_cols,
-                                            Exchange &red, uint32_t &phase, uint32_t tpr, uint32_t group)
+                                            Exchange &red, uint32_t &phase, uint32_t tpr, uint32_t group,
+                                            float *lows = nullptr, float low = 0.0f)
 {
-    if (tpr == 32) return;
+    if (tpr == 32) {
+        if (lows) mean = with_low(sum, low) * inv_cols;
+        return;
+    }
+    if (lows && (threadIdx.x & 31) == 0) lows[threadIdx.x >> 5] = low;
     const float4 *of = exchange(make_float4(sum, m2, mean, (float)mine), red, phase, tpr, group);
-    float all = 0.0f;
+    float all = 0.0f, rest = 0.0f;
 #pragma unroll 4
-    for (uint32_t q = 0; q < tpr >> 5; ++q) all += of[q].x;
-    mean = all * inv_cols;
+    for (uint32_t q = 0; q < tpr >> 5; ++q) {
+        if (!lows) {
+            all += of[q].x;
+        } else {
+            rest += lows[q];
+            exact_add(all, rest, of[q].x, -1.0f);
+        }
+    }
+    mean = (lows ? with_low(all, rest) : all) * inv_cols;
     m2 = 0.0f;
 #pragma unroll 4
     for (uint32_t q = 0; q < tpr >> 5; ++q) {
@@ -632,6 +670,7 @@ norm_rows_kernel(const __grid_constant__ NormParams p)
     using C = Chunk<T, VEC>;
     using V = typename C::V;
     __shared__ Exchange red;
+    __shared__ float lows[kNormThreads / 32];
     DT_TL_BEGIN();
     pdl_begin();
     DT_TL_WAITED();
@@ -670,7 +709,30 @@ norm_rows_kernel(const __grid_constant__ NormParams p)
 #pragma unroll
             for (int i = 0; i < C::K; ++i) s[(n * C::K + i) & 3] = add(s[(n * C::K + i) & 3], f[i]);
         }
-        const float sum = lane_sum<L>(both(add(add(s[0], s[1]), add(s[2], s[3]))));
+        float sum = both(add(add(s[0], s[1]), add(s[2], s[3]))), low = 0.0f;
+        if constexpr (EARLY) {
+            // A mean near zero keeps few of its sum's digits: of a few rows a
+            // caller sees each, and a sum of twice the digits costs nothing here
+            // (4 x 1 x 4096 bf16: 4.0 us either way).
+            V hi = C::all(0.0f), lo = C::all(0.0f);
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                V f[C::K];
+                x[n].get(f);
+#pragma unroll
+                for (int i = 0; i < C::K; ++i) exact_add(hi, lo, f[i], C::all(-1.0f));
+            }
+            sum = first_of(hi);
+            low = both(lo);
+            if constexpr (VEC > 1) exact_add(sum, low, second_of(hi), -1.0f);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                low += __shfl_xor_sync(0xFFFFFFFFu, low, o);
+                exact_add(sum, low, __shfl_xor_sync(0xFFFFFFFFu, sum, o), -1.0f);
+            }
+        } else {
+            sum = lane_sum<L>(sum);
+        }
         float mean = sum * inv_mine;
 #pragma unroll
         for (int n = 0; n < N; ++n) {
@@ -684,7 +746,8 @@ norm_rows_kernel(const __grid_constant__ NormParams p)
             }
         }
         float m2 = lane_sum<L>(both(add(add(m[0], m[1]), add(m[2], m[3]))));
-        if constexpr (L == 32) row_moments(sum, mean, m2, mine, p.inv_cols, red, phase, tpr, group);
+        if constexpr (L == 32)
+            row_moments(sum, mean, m2, mine, p.inv_cols, red, phase, tpr, group, EARLY ? lows : nullptr, low);
         const float rstd = rstd_of(m2, p.inv_cols, p.eps);
         const V minus = C::all(-mean), scale = C::all(rstd);
         auto finish = [&](auto kind) {
