@@ -28,9 +28,9 @@
 //                   weights and, backward, their shares of dw and db; up to four
 //                   rows are summed at a time, and the rows of a warp's teams of
 //                   lanes where rows are short.  Backward 4 x 2048 x 4096 bf16
-//                   44 us, 4.6 TB/s; 8 x 8192 x 4096 276 us, 5.8 TB/s: the
-//                   smaller call's blocks spend 6 us on their way to the first
-//                   row and 8 between the first SM's end and the last's.
+//                   43 us, 4.7 TB/s; 8 x 8192 x 4096 275 us, 5.9 TB/s: the
+//                   smaller call's blocks spend 5 us on their way to the first
+//                   row and 3 between the first SM's end and the last's.
 // norm_join_kernel  adds the blocks' shares of dw and db in a fixed order, so
 //                   that the result depends on the device and the shapes alone,
 //                   not on timing.
@@ -276,6 +276,7 @@ struct Team {
     }
     __device__ __forceinline__ uint32_t threads() const { return tpr * kTeams; }
     __device__ __forceinline__ bool first() const { return team == 0 && t == 0; }
+    __device__ __forceinline__ bool first_warp() const { return L < 32 || t < 32; }
 };
 
 // The sum over L lanes.
@@ -333,7 +334,7 @@ __device__ __forceinline__ void row_sum(float (&v)[V], float (*red)[V][kNormThre
 
 // A group's walk over the rows: chunk c of the call is up to p.chunk_rows rows
 // of one rank; group number `part` has chunks part, part + parts, ...  Its
-// first thread starts the copies; the rest is the same in all of its threads.
+// first warp starts the copies; the rest is the same in all of its threads.
 // Dynamic shared memory holds the groups' rings and their barriers.
 template <typename T, bool BACK>
 struct Ring {
@@ -353,33 +354,57 @@ struct Ring {
         rows = p.row_end[r] - (r ? p.row_end[r - 1] : 0);
         n = rows - row < p.chunk_rows ? (uint32_t)(rows - row) : p.chunk_rows;
     }
-    // The 16-byte blocks that hold rows [row, row + n) of `bytes` bytes of one buffer.
-    __device__ __forceinline__ uint32_t copy(const void *const *bases, int kind, int r, uint64_t row, uint32_t n,
-                                             uint64_t row_bytes, uint32_t dst, uint32_t bar) const
+    // The copies of a chunk: x, and backward dy, mean, rstd.
+    static constexpr uint32_t kCopies = BACK ? 4 : 1;
+    // Copies the 16-byte blocks of one of its buffers that hold rows [row, row + n) of rank r; how many bytes.
+    __device__ __forceinline__ uint32_t copy(uint32_t which, int r, uint64_t row, uint32_t n, uint32_t stage) const
     {
-        (void)kind;
+        uint32_t dst = base + stage * p.stage_bytes;
+        uint64_t row_bytes = p.cols * sizeof(T);
+        const void *const *bases = p.x;
+        if (BACK && which != 0) {
+            bases = which == 1 ? p.dy : reinterpret_cast<const void *const *>(which == 2 ? p.mean : p.rstd);
+            dst += which == 1 ? p.array_bytes : 2 * p.array_bytes + (which - 2) * p.stat_bytes;
+            if (which >= 2) row_bytes = 4;
+        }
         const uint64_t lo = reinterpret_cast<uint64_t>(bases[r]) + row * row_bytes, hi = lo + n * row_bytes;
         const uint64_t from = lo & ~15ull, to = (hi + 15) & ~15ull;
-        if (!NORM_OK(bases, kind, r, reinterpret_cast<const void *>(lo), hi - lo, row_bytes)) return 0;
-        bulk_load(dst, reinterpret_cast<const void *>(from), (uint32_t)(to - from), bar);
+        if (!NORM_OK(bases, (which < 2 ? which : which + 1), r, reinterpret_cast<const void *>(lo), hi - lo, row_bytes))
+            return 0;
+        bulk_load(dst, reinterpret_cast<const void *>(from), (uint32_t)(to - from), bars + 8 * stage);
         return (uint32_t)(to - from);
     }
+    // All of them by one thread.
     __device__ __forceinline__ void load(uint64_t c, uint32_t stage) const
     {
         int r;
         uint64_t row;
-        uint32_t n;
+        uint32_t n, bytes = 0;
         chunk(c, r, row, n);
-        const uint32_t bar = bars + 8 * stage, dst = base + stage * p.stage_bytes;
-        const uint64_t row_bytes = p.cols * sizeof(T);
-        uint32_t bytes = copy(p.x, 0, r, row, n, row_bytes, dst, bar);
-        if constexpr (BACK) {
-            bytes += copy(p.dy, 1, r, row, n, row_bytes, dst + p.array_bytes, bar);
-            const uint32_t stat = dst + 2 * p.array_bytes;
-            bytes += copy(reinterpret_cast<const void *const *>(p.mean), 3, r, row, n, 4, stat, bar);
-            bytes += copy(reinterpret_cast<const void *const *>(p.rstd), 4, r, row, n, 4, stat + p.stat_bytes, bar);
+#pragma unroll
+        for (uint32_t k = 0; k < kCopies; ++k) bytes += copy(k, r, row, n, stage);
+        mbar_expect_tx(bars + 8 * stage, bytes);
+    }
+    // The ring's first ones, by a warp, a lane to a copy: one after the other they
+    // take 0.6 us a stage.  They come after the weights' loads, which behind 25 MB
+    // of rows would take 6 us.
+    __device__ __forceinline__ void load_first(uint64_t part) const
+    {
+        static_assert(kCopies * kMaxStages <= 32, "a lane to a copy");
+        const uint32_t lane = threadIdx.x & 31, stage = lane / kCopies, which = lane % kCopies;
+        const uint64_t c = part + (uint64_t)stage * p.parts;
+        const bool mine = stage < p.stages && c < p.chunks;
+        uint32_t bytes = 0;
+        if (mine) {
+            int r;
+            uint64_t row;
+            uint32_t n;
+            chunk(c, r, row, n);
+            bytes = copy(which, r, row, n, stage);
         }
-        mbar_expect_tx(bar, bytes);
+#pragma unroll
+        for (uint32_t o = 1; o < kCopies; o *= 2) bytes += __shfl_xor_sync(0xFFFFFFFFu, bytes, o);
+        if (mine && which == 0) mbar_expect_tx(bars + 8 * stage, bytes);
     }
     __device__ __forceinline__ void wait()
     {
@@ -425,18 +450,6 @@ __device__ __forceinline__ Ring<T, BACK> make_ring(const NormParams &p, unsigned
     unsigned char *mem = smem + (size_t)m.group * mine;
     pdl_begin();
     return Ring<T, BACK>{p, smem_addr(mem), bars + 8 * m.group * p.stages, mem};
-}
-
-// Its first copies.  They come after the weights' loads, which behind 25 MB of
-// rows would take 6 us.
-template <typename T, bool BACK>
-__device__ __forceinline__ void first_loads(const Ring<T, BACK> &ring, const NormParams &p, bool first, uint64_t part)
-{
-    if (first)
-        for (uint32_t k = 0; k < p.stages; ++k) {
-            const uint64_t c = part + (uint64_t)k * p.parts;
-            if (c < p.chunks) ring.load(c, k);
-        }
 }
 
 // A row of a stage in registers: chunk c of thread t is elements [(c * tpr +
@@ -528,6 +541,8 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(const __grid_cons
     DT_TL_WAITED();
     const float inv = p.inv_cols;
     uint32_t phase = 0;
+    // the first stage's copies before the weights' loads, and the others, behind
+    // whose 25 MB the weights would take 6 us, after them
     V w[N][K], b[N][K];
     auto weights = [&](int n) {
         const uint32_t e = (n * tpr + t) * VEC;
@@ -538,7 +553,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(const __grid_cons
     if constexpr (kHold)
 #pragma unroll
         for (int n = 0; n < N; ++n) weights(n);
-    first_loads(ring, p, team.first(), part);
+    if (team.first_warp()) ring.load_first(part);
 
     for (uint64_t c = part; c < p.chunks; c += p.parts) {
         int r;
@@ -807,6 +822,8 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_kernel(const __
     DT_TL_WAITED();
     const float inv = p.inv_cols;
     uint32_t phase = 0;
+    // the first stage's copies before the weights' loads, and the others, behind
+    // whose 25 MB the weights would take 6 us, after them
     V dw[N][K], db[N][K], w[N][K];
     auto weights = [&](int n) {
         const uint32_t e = (n * tpr + t) * VEC;
@@ -818,7 +835,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_kernel(const __
         for (int i = 0; i < K; ++i) dw[n][i] = db[n][i] = w[n][i] = C::all(0.0f);
         if constexpr (kHold) weights(n);
     }
-    first_loads(ring, p, team.first(), part);
+    if (team.first_warp()) ring.load_first(part);
 
     for (uint64_t c = part; c < p.chunks; c += p.parts) {
         int r;
@@ -910,8 +927,10 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_kernel(const __
                     dw[n][i] = add(dw[n][i], from_lane(dw[n][i], o));
                     db[n][i] = add(db[n][i], from_lane(db[n][i], o));
                 }
-        __syncthreads();
-        float *all = reinterpret_cast<float *>(smem), *mine = all + (size_t)team.group * 2 * cols;
+        const uint32_t groups = blockDim.x / team.threads();
+        float *out = p.partial + (uint64_t)blockIdx.x * 2 * cols, *all = reinterpret_cast<float *>(smem);
+        if (groups > 1) __syncthreads();
+        float *mine = groups > 1 ? all + (size_t)team.group * 2 * cols : out;
         if (team.team == 0)
 #pragma unroll
             for (int n = 0; n < N; ++n) {
@@ -923,39 +942,52 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_kernel(const __
                     reinterpret_cast<V *>(mine + cols + e)[i] = db[n][i];
                 }
             }
-        __syncthreads();
-        const uint32_t groups = blockDim.x / team.threads();
-        float *out = p.partial + (uint64_t)blockIdx.x * 2 * cols;
-        for (uint32_t e = threadIdx.x; e < 2 * cols; e += blockDim.x) {
-            float v = all[e];
+        if (groups > 1) {
+            __syncthreads();
 #pragma unroll 4
-            for (uint32_t k = 1; k < groups; ++k) v += all[(size_t)k * 2 * cols + e];
-            out[e] = v;
+            for (uint32_t e = threadIdx.x; e < 2 * cols; e += blockDim.x) {
+                float v = all[e];
+#pragma unroll 4
+                for (uint32_t k = 1; k < groups; ++k) v += all[(size_t)k * 2 * cols + e];
+                out[e] = v;
+            }
         }
     }
     DT_TL_END_BLOCK(DT_TL_NORM);
 }
 
 // Adds the shares of dw (blockIdx.y 0) and db (1): thread (c, s) adds shares
-// s, s + 16, ... of its column, then the 16 sums are added in ascending order.
+// s, s + 16, ... of its column, then the 16 sums are added in a tree.
 __global__ void __launch_bounds__(kJoinCols *kJoinSlices) norm_join_kernel(const __grid_constant__ NormParams p)
 {
-    __shared__ float sum[kJoinSlices][kJoinCols];
+    __shared__ float sum[kJoinSlices][kJoinCols + 1];
     DT_TL_BEGIN();
     pdl_begin();
     DT_TL_WAITED();
     const uint32_t c = threadIdx.x % kJoinCols, s = threadIdx.x / kJoinCols;
-    const uint32_t col = blockIdx.x * kJoinCols + c;
+    const uint32_t first = blockIdx.x * kJoinCols;
     float v = 0.0f;
-    if (col < p.cols) {
-        const float *in = p.partial + blockIdx.y * (uint64_t)p.cols + col;
-#pragma unroll 10
-        for (uint32_t k = s; k < p.parts; k += kJoinSlices) v += in[(uint64_t)k * 2 * p.cols];
+    if (first + c < p.cols) {
+        const float *in = p.partial + blockIdx.y * (uint64_t)p.cols + first + c;
+        for (uint32_t k = s; k < p.parts; k += kJoinSlices * 10) {
+            float o[10];   // on their way at the same time: 152 shares are 10 of each slice
+#pragma unroll
+            for (uint32_t j = 0; j < 10; ++j) {
+                const uint32_t at = k + j * kJoinSlices;
+                o[j] = at < p.parts ? in[(uint64_t)at * 2 * p.cols] : 0.0f;
+            }
+#pragma unroll
+            for (uint32_t j = 0; j < 10; ++j) v += o[j];
+        }
     }
     sum[s][c] = v;
     __syncthreads();
-    if (s == 0 && col < p.cols) {
-        for (int k = 1; k < kJoinSlices; ++k) v += sum[k][c];
+    // half a warp to a column, a lane to a slice
+    const uint32_t mine = threadIdx.x / kJoinSlices, col = first + mine;
+    v = sum[threadIdx.x % kJoinSlices][mine];
+#pragma unroll
+    for (int o = kJoinSlices / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    if (threadIdx.x % kJoinSlices == 0 && col < p.cols) {
         if (p.avg) v = avg_of(v, p.P, p.avg_scale, p.avg_pow2);
         void *out = blockIdx.y ? p.dbias : p.dweight;
         if (out) {
