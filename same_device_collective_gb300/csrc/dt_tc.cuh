@@ -115,10 +115,11 @@ __device__ __forceinline__ uint32_t cluster_rank()
     return r;
 }
 
-// Arrival at the barrier at this place in the pair's first CTA, for what was
-// read from tensor memory: the loads have completed and no memory was written,
-// so nothing has to be made visible (a release would wait for all of the
-// thread's stores first).
+// Arrival at the barrier at this place in the pair's first CTA, which says that
+// tensor memory has been read and nothing else: the loads have completed
+// (tcgen05.wait::ld, tc_fence_before), and relaxed as it is it orders neither
+// reads nor writes of shared or global memory.  (A release at cluster scope
+// would wait for all of the thread's stores first.)
 __device__ __forceinline__ void mbar_arrive_first(uint32_t bar)
 {
     asm volatile(

@@ -406,7 +406,8 @@ vocab_kernel(const __grid_constant__ VocabParams p)
     const uint32_t bars = smem_addr(ctl);
     const uint32_t full = bars, empty = bars + 8 * kMaxStages;         // stage loaded; stage consumed
     const uint32_t acc_full = bars + 16 * kMaxStages, acc_empty = acc_full + 16, drained = acc_empty + 16;
-    const uint32_t reduced = drained + 8;                              // kLse: the column groups' results are there
+    const uint32_t reduced = drained + 8;                              // kLse: the column groups' results are there,
+    const uint32_t joined = reduced + 8 * kJoins;                      // and have been read
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(ctl + 256);
     volatile uint32_t *gave_up = tmem_slot + 1;
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -424,7 +425,10 @@ vocab_kernel(const __grid_constant__ VocabParams p)
             mbar_init(acc_empty + 8 * s, kFinishWarps * CG);
         }
         mbar_init(drained, 1);
-        for (uint32_t s = 0; MODE == kLse && s < kJoins; ++s) mbar_init(reduced + 8 * s, kFinishWarps - 4);
+        for (uint32_t s = 0; MODE == kLse && s < kJoins; ++s) {
+            mbar_init(reduced + 8 * s, kFinishWarps - 4);
+            mbar_init(joined + 8 * s, 4);
+        }
         *gave_up = 0;
         mbar_init_fence();
     }
@@ -631,12 +635,15 @@ vocab_kernel(const __grid_constant__ VocabParams p)
                         if (here && row < p.tokens) p.logit[row] = logit;
                     }
                     // The four column groups' into one by the first warps; the others go on
-                    // (with a barrier of them all a narrow head's tile took 12% longer).  They
-                    // are at most two tiles ahead then: a third one's logits wait for the first
-                    // warps to have read the second's, so three tiles' results need room.
+                    // (with a barrier of them all a narrow head's tile took 12% longer), up to
+                    // the tile whose results go where the first warps have yet to read: tensor
+                    // memory lets them be two tiles ahead, so with room for three no warp waits.
+                    // That order needs barriers of its own: the arrivals that give accumulators
+                    // back release nothing (mbar_arrive_first).
                     float2(*red)[kM] = reinterpret_cast<float2(*)[kM]>(buf) + j3 * kParts;
                     const uint32_t in = (warp & 3) * 32 + lane;
                     if (warp >= 4) {
+                        if (!late) late = __any_sync(0xFFFFFFFFu, !wait(joined + 8 * j3, round ^ 1));
                         red[warp >> 2][in] = make_float2(top, sum);
                         __syncwarp();
                         if (lane == 0) mbar_arrive(reduced + 8 * j3);
@@ -648,6 +655,8 @@ vocab_kernel(const __grid_constant__ VocabParams p)
                             const uint64_t part = (uint64_t)p.unit0 * (kVocabUnit / p.bn) + t.n0 / p.bn;
                             p.part[part * p.tokens + row] = make_float2(top, sum);
                         }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(joined + 8 * j3);
                     }
                     if (++j3 == kJoins) j3 = 0, round ^= 1;
                     continue;

@@ -370,3 +370,17 @@ def test_refusals(dt):
         assert dt.dt_vocab_loss_workspace(g, vocab, 0, 16, 0, "bf16", False) == 0
         torch.cuda.synchronize()
         assert not dh.any() and not losses.any() and dt.dt_group_check(g) == dt.DT_OK
+
+
+# Narrow heads give every CTA or pair many short tiles in a row, so that the
+# warps that hand their column group's results on run ahead of those that join
+# them: as many tiles as the results have room for, and several times that.
+@pytest.mark.parametrize("tokens,vocab,dim", [(2048, [40000, 3], 64), (700, [90001, 40000], 16), (100, [131072], 64)])
+def test_many_short_tiles_in_a_row_keep_their_results_apart(dt, tokens, vocab, dim):
+    h, w, t = make(tokens, vocab, dim, seed=tokens + 1)
+    with group(len(vocab)) as g:
+        first = forward(dt, g, h, w, t)
+        check_forward(h, w, t, *first)
+        for _ in range(20):
+            assert all(torch.equal(a, b) for a, b in zip(first, forward(dt, g, h, w, t)))
+        assert dt.dt_group_check(g) == dt.DT_OK
