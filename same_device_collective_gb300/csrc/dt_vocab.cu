@@ -610,7 +610,15 @@ vocab_kernel(const __grid_constant__ VocabParams p)
                         for (uint32_t j = 0; j < 8; ++j) tops[j & 3] = max3(tops[j & 3], v[b + j], v[b + j + 8]);
                     }
                     float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-                    const float top2 = top == -INFINITY ? 0.0f : top * kLog2e;   // no 0 times infinity where all are -inf
+                    // v log2e - top2 is one fma, with top2 the rounded top * log2e: the sum comes
+                    // out 2^rest too large, rest being what was rounded off, and is set right
+                    // afterwards.  Relative to the maximum it is 1 at least, so that no loss is
+                    // below zero.  From 2^30 on, where rest may be more than fp32 has powers for,
+                    // it is as good as 1: other logits are 64 away, and the logarithm of how many
+                    // are equal is less than half an ulp of them.
+                    // (The distance first, then its scale: 8192 tokens of 65536 x 64 223 -> 244 us; this 226.)
+                    const float from = top == -INFINITY ? 0.0f : top;   // no infinity from itself where all are -inf
+                    const float top2 = from * kLog2e, rest = fmaf(from, kLog2e, -top2);
                     const float2 log2e2 = make_float2(kLog2e, kLog2e), down = make_float2(-top2, -top2);
 #pragma unroll
                     for (uint32_t b = 0; b < 64; b += 16) {
@@ -623,6 +631,8 @@ vocab_kernel(const __grid_constant__ VocabParams p)
                     }
                     const float2 both = add2(add2(sums[0], sums[1]), add2(sums[2], sums[3]));
                     float sum = both.x + both.y;
+                    const float right = fabsf(top) < 1073741824.0f ? sum * exp2_fast(-rest) : 1.0f;
+                    sum = sum != sum ? sum : fmaxf(right, 1.0f);
                     // the column of this row's target in the tile, if it is there
                     const int64_t at = (int64_t)target - (int64_t)(p.first[t.r] + t.vrow);
                     const bool here = target != p.ignore && target >= 0 && at >= (int64_t)c0 && at < (int64_t)min(c1, valid);

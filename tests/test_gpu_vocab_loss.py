@@ -384,3 +384,40 @@ def test_many_short_tiles_in_a_row_keep_their_results_apart(dt, tokens, vocab, d
         for _ in range(20):
             assert all(torch.equal(a, b) for a, b in zip(first, forward(dt, g, h, w, t)))
         assert dt.dt_group_check(g) == dt.DT_OK
+
+
+# Tokens of a trained model: one word takes nearly all.  Every logit is a single
+# product of two bf16 numbers or the exact sum of two, so that logits are exact.
+# Relative to the maximum the sum of exponentials is 1 + s; s is off by 2^-18 of
+# itself (exponents up to 64 rounded to fp32, the powers, the additions), the
+# sum and its logarithm by 2^-22, and lse, where it is rounded, by 2^-24 of
+# itself.  As the sum is 1 at least, no loss is negative.
+def confident(top, tokens, words, down):
+    """Word t has the logit `top` for token t (bf16 products near it), every other one `down` less of itself."""
+    gen = torch.Generator("cuda").manual_seed(17)
+    dim = tokens + 1
+    a = (torch.rand(tokens, generator=gen, device="cuda") + 1).bfloat16()
+    h = torch.zeros(tokens, dim, dtype=torch.bfloat16, device="cuda")
+    h[torch.arange(tokens), torch.arange(tokens)] = a
+    h[:, tokens] = 1
+    w = torch.zeros(words, dim, dtype=torch.bfloat16, device="cuda")
+    w[torch.arange(tokens), torch.arange(tokens)] = (top / a.float()).bfloat16()
+    w[:, tokens] = -down
+    t = torch.arange(tokens, device="cuda", dtype=torch.int32)
+    return h, [w[:words // 3].contiguous(), w[words // 3:].contiguous()], t
+
+
+@pytest.mark.parametrize("tokens", [100, 300])
+@pytest.mark.parametrize("top,down", [(0.75, 80), (15.0, 0), (15.0, 40), (30.0, 4), (120.0, 0), (3000.0, 0), (3e9, 0), (1e30, 0)])
+def test_losses_of_confident_tokens_are_not_negative(dt, tokens, top, down):
+    h, w, t = confident(top, tokens, 900, down)
+    with group(2) as g:
+        losses, lse, loss = forward(dt, g, h, w, t)
+    l = h.double() @ torch.cat(w).double().t()
+    want = torch.logsumexp(l, 1)
+    each = torch.log1p((l - l.gather(1, t.long()[:, None])).exp().sum(1) - 1)
+    assert (losses >= 0).all() and float(loss) >= 0
+    tol = 2.0 ** -22 + 2.0 ** -18 * (1 - torch.exp(-each)) + 2.0 ** -24 * want.abs()
+    assert ((lse.double() - want).abs() <= tol).all()
+    # lse and the logit cancel; the difference is rounded once more
+    assert ((losses.double() - each).abs() <= tol + 2.0 ** -24 * each).all()
