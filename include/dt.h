@@ -408,10 +408,12 @@ dt_status dt_vocab_loss(dt_group_t g, const void *hidden, const void *const *wei
  *                NULL
  *   lse          as dt_vocab_loss wrote it
  *   workspace    dt_vocab_loss_workspace bytes with backward = 1
- * The logits are computed again, a piece of the vocabulary at a time; p -
- * [target] is held in bf16 for that piece (at most 512 MiB, or 256 vocabulary
- * rows' worth), every sum in fp32, and results are rounded once.  Repeated
- * calls give the same bits. */
+ * The logits are computed again as the loss computes them, a piece of the
+ * vocabulary at a time; p - [target] is held in bf16 for that piece (at most 512
+ * MiB, or 256 vocabulary rows' worth), every sum in fp32, and results are
+ * rounded once.  The tensor cores add 16 products at a time and round towards
+ * zero: sums of n terms are up to n * 2e-9 of themselves too small beside that.
+ * Repeated calls give the same bits. */
 dt_status dt_vocab_loss_backward(dt_group_t g, const void *hidden, const void *const *weight,
                                  const size_t *vocab, size_t vocab_equal, const int32_t *targets,
                                  const float *lse, const float *grad_loss, size_t tokens,

@@ -227,6 +227,17 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
     return f;
 }
 
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    uint64_t x, y, z;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(z) : "l"(x), "l"(y));
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(z));
+    return f;
+}
+
 // 2^x, at most 2 ulp off.
 __device__ __forceinline__ float exp2_fast(float x)
 {

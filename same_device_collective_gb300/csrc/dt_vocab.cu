@@ -12,8 +12,9 @@
 // next tile's is being made in the other half of tensor memory.
 //   kLse   logits; the finish reduces a tile's columns to a maximum and a
 //          sum of exponentials for each token: 8 bytes for 256 logits.
-//   kGrad  the same logits again; the finish makes p - [target] and stores it
-//          as bf16 for a piece of the vocabulary at a time.  That is the one
+//   kGrad  the same logits again (kGradLong: as sums of several accumulators);
+//          the finish makes p - [target] and stores it as bf16 for a piece of
+//          the vocabulary at a time.  That is the one
 //          rounding on the way (2^-8 of each term at most, as the outputs'
 //          own): the two products below need it in the operands' type.  The
 //          scale s is applied to their fp32 sums.
@@ -22,7 +23,10 @@
 //          many of dw, so the tiles of dw fill what dh leaves of the last wave.
 //          dw is final for these rows of w.  dh over several pieces, or when
 //          the vocabulary is split over blocks because there are few tokens,
-//          stays in fp32 and is joined in a fixed order.
+//          stays in fp32 and is joined in a fixed order.  These sums, over a
+//          piece of the vocabulary or all tokens, stay in one accumulator, which
+//          cuts off up to 3e-8 of its value at each step of 16: 3e-4 of 131072
+//          terms of one sign, where bf16 results are rounded by up to 4e-3.
 // A pair of CTAs halves what each reads of B, so that L2 feeds a third less.
 // It takes 256 rows of A, so up to 128 tokens a CTA works alone, on tiles of at
 // most 128 columns, and loads only the rows there are of A: for one token 128
@@ -58,7 +62,7 @@
 namespace dt {
 namespace {
 
-enum Mode { kLse, kGrad, kBack };
+enum Mode { kLse, kGrad, kGradLong, kBack };
 
 constexpr float kLog2e = 1.44269504088896340736f;
 
@@ -66,18 +70,22 @@ constexpr uint32_t kM = 128;                       // rows of a tile in a CTA
 constexpr uint32_t kK = 128;                       // depth of a stage
 constexpr uint32_t kRingBytes = 192 * 1024;        // three stages of 128 rows and columns of A and B
 constexpr uint32_t kMaxStages = 8;
-// kLse: blocks of the inner dimension whose sum the tensor cores make; the sums
-// of further ones are added in registers.  The tensor cores round towards zero
-// at every step of 16: whole sums of 4096 products came out 4e-6 of themselves
-// too small, and losses 8e-7 off; with sums of 1024 that is 9e-7 and 2e-7, for
-// 2% of the time (2048 tokens of 32768 x 4096: 332 -> 338 us).
+// The logits: blocks of the inner dimension whose sum the tensor cores make; the
+// sums of further ones are added in registers.  The tensor cores round towards
+// zero at every step of 16: whole sums of 4096 products came out 4e-6 of
+// themselves too small, and losses 8e-7 off; with sums of 1024 that is 9e-7 and
+// 2e-7, for 2% of the time (2048 tokens of 32768 x 4096: 332 -> 338 us).  The
+// gradient's logits are summed alike, for up to 1% (2048 x 32768 x 4096: 977 ->
+// 986 us): p is exp(l - lse), and with other logits than lse was made of, p - 1 of
+// a confident token was mostly their difference (at 4096 columns, a logit of 17.5
+// and p = 1 - 1e-4, 0.7 of it).
 constexpr uint32_t kSumBlocks = 8;
 constexpr uint32_t kTmemColumns = 512;             // two accumulators of 128 x 256 fp32
 // Finishing warps: of logits that are only reduced 16, each with 64 columns of a
 // tile in registers; else 8 with 128.  And one for TMA, one for the products,
-// and kGrad's one for the tokens' count.
+// and the gradient's one for the tokens' count.
 __host__ __device__ constexpr uint32_t finish_warps(int mode) { return mode == kLse ? 16 : 8; }
-__host__ __device__ constexpr int tc_threads(int mode) { return (finish_warps(mode) + (mode == kGrad ? 3 : 2)) * 32; }
+__host__ __device__ constexpr int tc_threads(int mode) { return (finish_warps(mode) + (mode == kGrad || mode == kGradLong ? 3 : 2)) * 32; }
 constexpr uint32_t kJoins = 3;                     // tiles whose column groups' results there is room for
 constexpr uint32_t kStageOut = 4096;               // a finishing warp's 32 rows x 128 bytes
 constexpr uint32_t kBarBytes = 1024;
@@ -488,7 +496,7 @@ vocab_kernel(const __grid_constant__ VocabParams p)
                 const uint32_t inner = MODE != kBack ? p.dim : t.dw ? p.tokens : p.kblocks * kK;
                 const uint32_t last = min((inner - (t.kb1 - 1) * kK + 15) / 16, 8u);
                 for (uint32_t kb = t.kb0; ok && kb < t.kb1; ++u) {
-                    const uint32_t first = kb, end = MODE == kLse ? min(kb + kSumBlocks, t.kb1) : t.kb1;
+                    const uint32_t first = kb, end = MODE != kBack ? min(kb + kSumBlocks, t.kb1) : t.kb1;
                     const uint32_t acc = tmem + (u & 1) * 256;
                     if (!(ok = wait(acc_empty + 8 * (u & 1), ((u >> 1) & 1) ^ 1))) break;
                     tc_fence_after();
@@ -515,7 +523,7 @@ vocab_kernel(const __grid_constant__ VocabParams p)
             }
         }
         __syncwarp();
-    } else if (MODE == kGrad && warp == kFinishWarps + 2) {
+    } else if ((MODE == kGrad || MODE == kGradLong) && warp == kFinishWarps + 2) {
         // the scale, which the tiles of this launch do not wait for
         if (blockIdx.x == 0 && p.unit0 == 0) {
             uint32_t kept = 0;
@@ -534,7 +542,7 @@ vocab_kernel(const __grid_constant__ VocabParams p)
     } else {
         // Warps w, w + 4, ... read the same 32 rows (a warp reaches the tensor
         // memory lanes of its number modulo 4) and take an equal part of the
-        // columns each, in kGrad and kBack at least 64.
+        // columns each, but for kLse at least 64.
         unsigned char *buf = out_buf + (MODE == kLse ? 0 : warp * kStageOut);
         const float scale = MODE == kBack ? *p.scale : 0.0f;
         constexpr uint32_t kParts = kFinishWarps / 4;
@@ -561,10 +569,10 @@ vocab_kernel(const __grid_constant__ VocabParams p)
             const uint32_t row0 = t.m0 + quad, row = row0 + lane;
             // what does not depend on the accumulator, before the wait for it
             int32_t target = p.ignore;
-            float lse2 = 0.0f;
+            float lse = 0.0f;
             if (MODE != kBack && row < p.tokens) {
                 target = p.targets[row];
-                if (MODE == kGrad) lse2 = p.lse[row] * kLog2e;
+                if (MODE != kLse) lse = p.lse[row];
             }
             const uint32_t lanes = (warp & 3) * 32 << 16;   // of tensor memory
             uint32_t acc = tmem + (u & 1) * 256 + lanes;
@@ -674,35 +682,70 @@ vocab_kernel(const __grid_constant__ VocabParams p)
                     // the column of this row's target in the tile, if it is there
                     const int64_t at = (int64_t)target - (int64_t)(p.first[t.r] + t.vrow);
                     const bool here = target != p.ignore && target >= 0 && at >= (int64_t)c0 && at < (int64_t)min(c1, valid);
-                    if (!take()) break;
+                    // the logits, summed as the loss sums them: of one accumulator 64 columns at a
+                    // time below (8192 tokens of 65536 x 64: 655 us, 807 with all of them here)
+                    constexpr bool kLong = MODE == kGradLong;
+                    float v[kLong ? 128 : 64];
+                    bool ok = take();
+                    if constexpr (kLong) {
+#pragma unroll
+                        for (uint32_t b = 0; b < 128; b += 32)
+                            if (c0 + b < c1) tmem_load32(acc + c0 + b, *reinterpret_cast<float(*)[32]>(v + b));
+                        give_back();
+                        for (uint32_t kb = t.kb0 + kSumBlocks; ok && kb < t.kb1; kb += kSumBlocks) {
+                            ok = take();
+                            acc = tmem + (u & 1) * 256 + lanes;
+#pragma unroll
+                            for (uint32_t b = 0; b < 128; b += 8) {
+                                if (c0 + b >= c1) continue;
+                                float x[8];
+                                tmem_load8(acc + c0 + b, x);
+#pragma unroll
+                                for (uint32_t j = 0; j < 8; ++j) v[b + j] += x[j];
+                            }
+                            give_back();
+                        }
+                    }
+                    if (!ok) break;
                     const bool keep = row < p.tokens && target != p.ignore && target >= 0 && (uint32_t)target < p.vocab;
                     const uint32_t col = here ? (uint32_t)at : 0xFFFFFFFFu;
                     const uint32_t rows = row0 < p.tokens ? min(p.tokens - row0, 32u) : 0;
                     const uint32_t mask = keep ? 0xFFFFFFFFu : 0u;   // of a row's results, two at a time
-                    for (uint32_t c = c0; c < c1; c += 64) {
+                    // the distance from lse first, which of a confident token is nearly all
+                    // of its p - 1
+                    const float2 down = make_float2(-lse, -lse), log2e2 = make_float2(kLog2e, kLog2e);
+                    auto step = [&](uint32_t c, float *v) {   // 64 columns
                         uint32_t w[32];
                         // most steps have every column there and no row's target
                         const bool plain = c + 64 <= valid && !__any_sync(0xFFFFFFFFu, col - c < 64);
 #pragma unroll
-                        for (uint32_t q = 0; q < 2; ++q) {
-                            float v[32];
-                            tmem_load32(acc + c + 32 * q, v);
+                        for (uint32_t q = 0; q < 64; q += 32) {
+                            if constexpr (!kLong) tmem_load32(acc + c + q, *reinterpret_cast<float(*)[32]>(v + q));
 #pragma unroll
-                            for (uint32_t j = 0; j < 32; ++j) v[j] = exp2_fast(fmaf(v[j], kLog2e, -lse2));
+                            for (uint32_t j = q; j < q + 32; j += 2) {
+                                const float2 x = mul2(add2(make_float2(v[j], v[j + 1]), down), log2e2);
+                                v[j] = exp2_fast(x.x);
+                                v[j + 1] = exp2_fast(x.y);
+                            }
                             if (!plain) {
 #pragma unroll
-                                for (uint32_t j = 0; j < 32; ++j) {
-                                    const uint32_t e = c + 32 * q + j;
-                                    if (e == col) v[j] -= 1.0f;
-                                    v[j] = e < valid ? v[j] : 0.0f;
+                                for (uint32_t j = q; j < q + 32; ++j) {
+                                    if (c + j == col) v[j] -= 1.0f;
+                                    v[j] = c + j < valid ? v[j] : 0.0f;
                                 }
                             }
 #pragma unroll
-                            for (uint32_t j = 0; j < 16; ++j) w[16 * q + j] = pack_bf16x2(v[2 * j], v[2 * j + 1]) & mask;
+                            for (uint32_t j = q; j < q + 32; j += 2) w[j / 2] = pack_bf16x2(v[j], v[j + 1]) & mask;
                         }
                         store_rows_bf16(p, buf, w, p.gbuf + (uint64_t)row0 * p.gpitch + t.n0 + c, p.gpitch, rows, 64, 8,
                                          p.gbuf, (uint64_t)p.tokens * p.gpitch * 2, 0);
+                    };
+                    if constexpr (kLong) {
+                        if (c0 < c1) step(c0, v);
+                        if (c0 + 64 < c1) step(c0 + 64, v + 64);
+                        continue;   // given back above
                     }
+                    for (uint32_t c = c0; c < c1; c += 64) step(c, v);
                 }
             } else if (!take()) {
                 break;
@@ -1034,7 +1077,7 @@ cudaError_t launch_vocab_lse(VocabParams &p, int device, cudaStream_t s)
 cudaError_t launch_vocab_grad(VocabParams &p, int device, cudaStream_t s)
 {
     p.workers = p.tiles;
-    return launch_mode<kGrad>(p, device, s);
+    return p.kblocks > kSumBlocks ? launch_mode<kGradLong>(p, device, s) : launch_mode<kGrad>(p, device, s);
 }
 
 // A finished tile costs a worker about a block of the inner dimension more than

@@ -421,3 +421,109 @@ def test_losses_of_confident_tokens_are_not_negative(dt, tokens, top, down):
     assert ((lse.double() - want).abs() <= tol).all()
     # lse and the logit cancel; the difference is rounded once more
     assert ((losses.double() - each).abs() <= tol + 2.0 ** -24 * each).all()
+
+
+# Confident tokens of a wide head: word t is a multiple of token t's hidden row,
+# so that its logit is a sum of `dim` products of one sign.  Both passes make
+# the same logits, so what their sums cut off is nearly the same in l and in
+# lse: with e the error of a logit, (1 - p) * 2e is left of it in l - lse.
+# Beside that lse is rounded once (2^-24 of it), and the distance, its power and
+# their product by 2^-21.
+def wide_head(tokens, vocab, dim, target):
+    gen = torch.Generator("cuda").manual_seed(dim + tokens)
+    h = torch.randn(tokens, dim, generator=gen, device="cuda").bfloat16()
+    w = torch.randn(vocab, dim, generator=gen, device="cuda") * dim ** -0.5
+    w[:tokens] = h.float() * (target / h.float().square().sum(1, keepdim=True))
+    w = w.bfloat16()
+    t = torch.arange(tokens, device="cuda", dtype=torch.int32)
+    return h, [w[:vocab // 2].contiguous(), w[vocab // 2:].contiguous()], t
+
+
+@pytest.mark.parametrize("tokens,dim", [(1, 4096), (7, 1032), (100, 4096), (128, 2056), (300, 4096), (257, 1100), (300, 4100)])
+def test_confident_tokens_of_wide_heads(dt, tokens, dim):
+    vocab = 2000
+    h, w, t = wide_head(tokens, vocab, dim, 17.5)
+    with group(2) as g:
+        losses, lse, loss = forward(dt, g, h, w, t)
+        dh, dw = backward(dt, g, h, w, t, lse)
+    hd, wd = h.double(), torch.cat(w).double()
+    l, size = hd @ wd.t(), hd.abs() @ wd.abs().t()
+    want, at = torch.logsumexp(l, 1), l.gather(1, t.long()[:, None])[:, 0]
+    p = torch.exp(l - want[:, None])
+    gone = 1 - p.gather(1, t.long()[:, None])[:, 0]
+    assert 1e-5 < float(gone.min()) and float(gone.max()) < 1e-2
+    e = (sum_error(1024) * size + 4 * 2.0 ** -24 * size).amax(1)   # sums of 1024, and those added in fp32
+    near = 2.0 ** -24 * want.abs() + 2.0 ** -21
+    assert ((losses.double() - (want - at)).abs() <= near + 2 * e * gone).all()
+    check_forward(h, w, t, losses, lse, loss)
+    g = p.clone()
+    g[torch.arange(tokens), t.long()] -= 1
+    off = 2.0 ** -8 * g.abs() + p * ((1 - p) * 2 * e[:, None] + near[:, None])
+    for got, g, off, x in ((dh, g, off, wd), (torch.cat(dw), g.t(), off.t(), hd)):
+        want = g @ x / tokens
+        tol = (off @ x.abs() + sum_error(len(x)) * (g.abs() @ x.abs())) / tokens + 2.0 ** -8 * want.abs()
+        assert ((got.double() - want).abs() <= tol).all(), float(((got.double() - want).abs() / tol).max())
+
+
+# With a single word its logit is lse itself, p is 1 and there is no gradient,
+# however long the sum: both passes have the same logits.
+@pytest.mark.parametrize("tokens,vocab,dim", [(1, [1], 64), (5, [0, 1], 4096), (128, [1], 1500), (129, [1, 0], 4096),
+                                              (300, [1], 4100), (1000, [1], 2048)])
+def test_a_single_word_has_no_gradient(dt, tokens, vocab, dim):
+    h, w, t = make(tokens, vocab, dim, seed=dim, std=1.0)
+    with group(len(vocab)) as g:
+        losses, lse, loss = forward(dt, g, h, w, t)
+        check_forward(h, w, t, losses, lse, loss)
+        dh, dw = backward(dt, g, h, w, t, lse)
+        assert not losses.any() and not loss.any() and not dh.any() and not any(x.any() for x in dw)
+
+
+# ... and a long sum is those of 1024 products each, added in fp32 in their order.
+@pytest.mark.parametrize("tokens,dim", [(1, 4096), (50, 2048), (128, 3000), (300, 4096), (200, 1100)])
+def test_logits_are_sums_of_1024_products(dt, tokens, dim):
+    h, w, t = make(tokens, [1], dim, seed=dim + 1, std=1.0)
+    with group(1) as g:
+        lse = forward(dt, g, h, w, t)[1]
+        want = torch.zeros_like(lse)
+        for k in range(0, dim, 1024):
+            part = forward(dt, g, h[:, k:k + 1024].contiguous(), [w[0][:, k:k + 1024].contiguous()], t)[1]
+            want = part if k == 0 else want + part
+        assert torch.equal(lse, want)
+
+
+# Logits past 100 with sharp and flat tokens in one batch.  With d = l - lse, of
+# the lse that is given: the distance, its product with log2(e) and that
+# constant are off by 2^-24 of d each, the power by 2^-22, and powers under
+# 2^-126 are zero.
+@pytest.mark.parametrize("tokens,vocab", [(130, [500, 600]), (40, [500, 600]), (300, [4000, 3001])])
+def test_gradients_of_peaked_distributions(dt, tokens, vocab):
+    h, w, t = make(tokens, vocab, 256, seed=3, std=4.0)
+    with group(2) as g:
+        losses, lse, loss = forward(dt, g, h, w, t)
+        dh, dw = backward(dt, g, h, w, t, lse)
+    assert float(lse.max()) > 100
+    l, dl = logits(h, w)
+    keep = (t != IGNORE)[:, None]
+    d = l - lse.double()[:, None]
+    p = torch.exp(d)
+    g = p.clone()
+    g[torch.arange(tokens), torch.where(keep[:, 0], t, 0).long()] -= 1
+    g *= keep
+    off = (2.0 ** -8 * g.abs() + 1.01 * p * (dl + 2.0 ** -22 * (1 + d.abs())) + 2.0 ** -126) * keep
+    c = 1 / int(keep.sum())
+    for got, g, off, x in ((dh, g, off, torch.cat(w).double()), (torch.cat(dw), g.t(), off.t(), h.double())):
+        want = c * (g @ x)
+        tol = c * (off @ x.abs() + sum_error(len(x)) * (g.abs() @ x.abs())) + 2.0 ** -8 * want.abs()
+        assert ((got.double() - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("tokens,vocab,dim", [(1, [9000], 4096), (100, [700, 800], 2056), (128, [512], 1032),
+                                              (300, [2000], 4096), (33, [100, 30], 1025), (64, [5000], 3000)])
+def test_sums_of_several_accumulators(dt, tokens, vocab, dim):
+    h, w, t = make(tokens, vocab, dim, seed=dim)
+    with group(len(vocab)) as g:
+        losses, lse, loss = forward(dt, g, h, w, t)
+        check_forward(h, w, t, losses, lse, loss)
+        dh, dw = backward(dt, g, h, w, t, lse)
+        check_backward(h, w, t, lse, dh, dw)
+        assert dt.dt_group_check(g) == dt.DT_OK
