@@ -184,6 +184,7 @@ bool vocab_plan(dt_group *g, const size_t *vocab, size_t vocab_equal, size_t tok
         v.sums = take(blocks * 4);
         v.kept = take(blocks * 4);
     } else {
+        v.kept = take(workers * (v.pairs ? 2 : 1) * 4);
         v.g = take((uint64_t)v.piece * dt::kVocabUnit * 2 * tokens);
         if (v.splits > 1 || v.pieces > 1) v.acc = take((uint64_t)v.splits * tokens * v.apitch * 4);
     }
@@ -250,6 +251,7 @@ dt_status vocab_common(dt_group *g, const void *hidden, const void *const *weigh
     unsigned char *ws = static_cast<unsigned char *>(workspace);
     p.ticket = reinterpret_cast<uint32_t *>(ws + v.ticket);
     p.scale = reinterpret_cast<float *>(ws + v.scale);
+    p.kept = reinterpret_cast<uint32_t *>(ws + v.kept);
     p.part = reinterpret_cast<float2 *>(ws + v.part);
     p.logit = reinterpret_cast<float *>(ws + v.logit);
     p.gbuf = reinterpret_cast<uint16_t *>(ws + v.g);

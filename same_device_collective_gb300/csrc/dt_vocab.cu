@@ -524,27 +524,45 @@ vocab_kernel(const __grid_constant__ VocabParams p)
         }
         __syncwarp();
     } else if ((MODE == kGrad || MODE == kGradLong) && warp == kFinishWarps + 2) {
-        // the scale, which the tiles of this launch do not wait for
-        if (blockIdx.x == 0 && p.unit0 == 0) {
+        // how many tokens count: a part of them to a CTA, 256 or more, which kBack adds.
+        // (One warp for all tokens, whose loads waited for one another, outlasted the
+        // tiles: 65536 tokens of 1000 x 64 910 us; this 355.)
+        if (p.unit0 == 0 && blockIdx.x < p.kept_parts) {
+            const uint32_t each = (p.tokens + p.kept_parts - 1) / p.kept_parts;
+            const uint32_t begin = min(blockIdx.x * each, p.tokens), end = min(begin + each, p.tokens);
             uint32_t kept = 0;
-            for (uint32_t k = lane; k < p.tokens; k += 32) {
-                const int32_t v = p.targets[k];
-                const bool in = v >= 0 && (uint32_t)v < p.vocab;
-                if (v != p.ignore && !in) record_error(p.sink, DT_ERR_INVALID, -1, (int)k, v);
-                kept += v != p.ignore && in;
+            for (uint32_t first = begin; first < end; first += 256) {
+                int32_t v[8];
+#pragma unroll
+                for (uint32_t j = 0; j < 8; ++j) {
+                    const uint32_t k = first + 32 * j + lane;
+                    v[j] = k < end ? p.targets[k] : p.ignore;
+                }
+#pragma unroll
+                for (uint32_t j = 0; j < 8; ++j) {
+                    const bool in = v[j] >= 0 && (uint32_t)v[j] < p.vocab;
+                    if (v[j] != p.ignore && !in) record_error(p.sink, DT_ERR_INVALID, -1, (int)(first + 32 * j + lane), v[j]);
+                    kept += v[j] != p.ignore && in;
+                }
             }
             kept = __reduce_add_sync(0xFFFFFFFFu, kept);
-            if (lane == 0) {
-                const float grad = p.grad ? *p.grad : 1.0f;
-                *p.scale = kept == 0 ? 0.0f : p.avg ? __fdiv_rn(grad, (float)kept) : grad;
-            }
+            if (lane == 0) p.kept[blockIdx.x] = kept;
         }
     } else {
         // Warps w, w + 4, ... read the same 32 rows (a warp reaches the tensor
         // memory lanes of its number modulo 4) and take an equal part of the
         // columns each, but for kLse at least 64.
         unsigned char *buf = out_buf + (MODE == kLse ? 0 : warp * kStageOut);
-        const float scale = MODE == kBack ? *p.scale : 0.0f;
+        float scale = 0.0f;
+        if (MODE == kBack) {
+            const float grad = p.grad ? *p.grad : 1.0f;
+            uint32_t kept = 0;
+#pragma unroll 4
+            for (uint32_t k = lane; k < p.kept_parts; k += 32) kept += p.kept[k];
+            kept = __reduce_add_sync(0xFFFFFFFFu, kept);
+            scale = kept == 0 ? 0.0f : p.avg ? __fdiv_rn(grad, (float)kept) : grad;
+            if (blockIdx.x == 0 && threadIdx.x == 0) *p.scale = scale;   // for the kernel that joins dh's splits
+        }
         constexpr uint32_t kParts = kFinishWarps / 4;
         const uint32_t width = MODE == kLse || p.bn >= 128 ? p.bn / kParts : p.bn;
         const uint32_t c0 = (warp >> 2) * width, c1 = min(c0 + width, p.bn);
@@ -1032,6 +1050,11 @@ __global__ void __launch_bounds__(kThreads) vocab_pack_kernel(const __grid_const
     DT_TL_END_BLOCK(DT_TL_VOCAB);
 }
 
+uint32_t tc_blocks(const VocabParams &p, int device)
+{
+    return std::min(p.workers, vocab_workers(p.pairs, device)) * (p.pairs ? 2 : 1);
+}
+
 template <int MODE, int CG>
 cudaError_t launch_mode(VocabParams &p, int device, cudaStream_t s)
 {
@@ -1044,8 +1067,7 @@ cudaError_t launch_mode(VocabParams &p, int device, cudaStream_t s)
         ready.fetch_or(bit, std::memory_order_release);
     }
     p.stages = std::min(kMaxStages, kRingBytes / (2 * a_box_bytes(MODE == kBack, p.rows_h) + p.bn / CG * 256));
-    return launch_kernel(vocab_kernel<MODE, CG>, dim3(std::min(p.workers, vocab_workers(CG == 2, device)) * CG),
-                         dim3(tc_threads(MODE)), kTcSmem, s, false, p);
+    return launch_kernel(vocab_kernel<MODE, CG>, dim3(tc_blocks(p, device)), dim3(tc_threads(MODE)), kTcSmem, s, false, p);
 }
 
 template <int MODE>
@@ -1077,6 +1099,7 @@ cudaError_t launch_vocab_lse(VocabParams &p, int device, cudaStream_t s)
 cudaError_t launch_vocab_grad(VocabParams &p, int device, cudaStream_t s)
 {
     p.workers = p.tiles;
+    if (p.unit0 == 0) p.kept_parts = std::min(tc_blocks(p, device), (p.tokens + 255) / 256);
     return p.kblocks > kSumBlocks ? launch_mode<kGradLong>(p, device, s) : launch_mode<kGrad>(p, device, s);
 }
 

@@ -52,7 +52,9 @@ struct VocabParams {
     float2 *part;                      // [tiles of the vocabulary][tokens]: maximum, sum of exponentials
     float *logit;                      // the target's logit of each token
     uint32_t *ticket;
-    float *scale;                      // grad, or grad / counted tokens
+    uint32_t *kept;                    // gradient: counted tokens, a part to a CTA of the first launch
+    uint32_t kept_parts;
+    float *scale;                      // gradient: grad, or grad / counted tokens
     uint16_t *gbuf;                    // [tokens, gpitch] bf16
     float *acc;                        // dh's sums [splits][tokens][apitch]
     uint16_t *dh;

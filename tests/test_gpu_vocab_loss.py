@@ -527,3 +527,57 @@ def test_sums_of_several_accumulators(dt, tokens, vocab, dim):
         dh, dw = backward(dt, g, h, w, t, lse)
         check_backward(h, w, t, lse, dh, dw)
         assert dt.dt_group_check(g) == dt.DT_OK
+
+
+# The counted tokens are added over every CTA's part of them.
+@pytest.mark.parametrize("tokens,vocab,dim", [(5000, [300, 41], 32), (20001, [77], 16), (600, [70000, 70001], 64), (31, [9000], 16)])
+def test_many_tokens_of_a_small_head_are_counted(dt, tokens, vocab, dim):
+    h, w, t = make(tokens, vocab, dim, seed=tokens, drop=0.9)
+    t[0], t[-1] = 1, 2
+    grad = torch.tensor([3.0], device="cuda")
+    with group(len(vocab)) as g:
+        losses, lse, loss = forward(dt, g, h, w, t)
+        check_forward(h, w, t, losses, lse, loss)
+        dh, dw = backward(dt, g, h, w, t, lse, grad)
+        check_backward(h, w, t, lse, dh, dw, 3.0)
+        for bad in (0, tokens // 2, tokens - 1):
+            wrong = t.clone()
+            wrong[bad] = 1 << 30
+            kept = t.clone()
+            kept[bad] = IGNORE
+            dh, dw = backward(dt, g, h, w, wrong, lse, grad)
+            check_backward(h, w, kept, lse, dh, dw, 3.0)
+            torch.cuda.synchronize()
+            assert dt.dt_group_error_detail(g) == (dt.DT_ERR_INVALID, -1, bad, 1 << 30)
+            dt.dt_group_reset(g)
+
+
+def test_counting_tokens_does_not_outlast_the_products(dt):
+    # the gradient makes the loss's products three times and moves p - [target]
+    # through memory; a count that ran beside them on one warp took 15 times the loss
+    h, w, t = make(65536, [250] * 4, 64, seed=1)
+    n, dim, vocab = 65536, 64, [250] * 4
+    out = [torch.empty(k, device="cuda") for k in (n, n, 1)]
+    dh, dw = torch.empty_like(h), [torch.empty_like(x) for x in w]
+    with group(4) as g:
+        ws = torch.empty(max(dt.dt_vocab_loss_workspace(g, vocab, 0, n, dim, "bf16", b) for b in (False, True)),
+                         dtype=torch.uint8, device="cuda")
+        calls = (dt.prepare(dt.dt_vocab_loss, g, h, w, vocab, 0, t, n, dim, "bf16", "avg", IGNORE, *out, ws),
+                 dt.prepare(dt.dt_vocab_loss_backward, g, h, w, vocab, 0, t, out[1], None, n, dim, "bf16", "avg", IGNORE,
+                            dh, dw, ws))
+
+        def best(call):
+            took = []
+            for _ in range(8):
+                a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+                torch.cuda._sleep(200_000)
+                a.record()
+                for _ in range(4):
+                    call()
+                b.record()
+                torch.cuda.synchronize()
+                took.append(a.elapsed_time(b))
+            return min(took)
+
+        loss, back = best(calls[0]), best(calls[1])
+        assert back <= 8 * loss, (loss, back)
