@@ -166,9 +166,9 @@ __device__ __forceinline__ void tmem_load8(uint32_t tmem, float (&v)[8])
 
 // One box of a row-major matrix at (column, row) into this CTA's shared
 // memory; what lies outside the matrix is filled with zeros and counts towards
-// the barrier's bytes.  Of a pair, both CTAs' loads complete on the first
-// CTA's barrier (its address is the own one with bit 24 cleared).  The column
-// is a multiple of 64, so the copy starts on a 16-byte boundary.
+// the barrier's bytes.  Of a pair, both CTAs' loads complete on the barrier
+// at this place in the first CTA.  The column is a multiple of 64, so the copy
+// starts on a 16-byte boundary.
 template <int CG>
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap *map, int32_t col, int32_t row, uint32_t bar)
 {
@@ -179,9 +179,10 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap *map, in
             : "memory");
     else
         asm volatile(
+            "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %4, 0;\n\t"
             "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
-            "[%0], [%1, {%2, %3}], [%4];"
-            ::"r"(dst), "l"(map), "r"(col), "r"(row), "r"(bar & 0xFEFFFFFFu)
+            "[%0], [%1, {%2, %3}], [a];\n\t}"
+            ::"r"(dst), "l"(map), "r"(col), "r"(row), "r"(bar)
             : "memory");
 }
 
