@@ -59,6 +59,7 @@ constexpr int kNormThreads = 512;    // most threads of a block, and of a row
 constexpr uint32_t kSmemBytes = 160 * 1024;
 constexpr uint32_t kMaxStages = 8;
 constexpr uint32_t kStageTarget = 4096;
+constexpr uint32_t kMostColumns = kNormThreads * 32;   // of a row in registers
 constexpr int kLongThreads = 512;    // rows too long for registers
 constexpr int kLongSlices = 32;      // row slices of the column sums there
 constexpr int kJoinCols = 32;        // columns and row slices of a block that adds the shares
@@ -1261,8 +1262,10 @@ DT_TL_BINDER(bind_timeline_norm)
 
 size_t norm_workspace(uint32_t cols, int device)
 {
-    // a share to a block, or to a slice of rows that are too long for that
-    return (size_t)std::max(sm_count(device), kLongSlices) * 2 * cols * sizeof(float);
+    // a share to a block, or to a slice of the rows where a row is too long for
+    // any block's registers (and may be for those of one that takes it element by element)
+    const int blocks = cols > kMostColumns ? 0 : sm_count(device);
+    return (size_t)std::max(blocks, kLongSlices) * 2 * cols * sizeof(float);
 }
 
 cudaError_t launch_norm(NormParams p, int dtype, bool vec, int device, cudaStream_t s)

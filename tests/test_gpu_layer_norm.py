@@ -338,3 +338,25 @@ def test_refusals(dt):
         assert dt.dt_layer_norm_workspace(g, 0) == 0
         torch.cuda.synchronize()
         assert not any(t.any() for t in y) and dt.dt_group_check(g) == dt.DT_OK
+
+
+# Rows too long for registers have 32 shares of the weights' gradients, whatever
+# the number of SMs; no share lies outside the workspace that was asked for.
+@pytest.mark.parametrize("cols,dtype", [(16384, "bf16"), (16384, "f32"), (16385, "bf16"), (16388, "f32"), (1 << 20, "f32")])
+def test_workspace_of_long_rows(dt, cols, dtype):
+    rows = [37, 3]
+    x, dy, w, b = make(rows, cols, dtype, "f32", seed=cols)
+    with group(2) as g:
+        assert dt.dt_layer_norm_workspace(g, 1 << 24) == 32 * 2 * 4 << 24
+        size = dt.dt_layer_norm_workspace(g, cols)
+        assert size >= 32 * 2 * 4 * cols and (cols <= 16384 or size == 32 * 2 * 4 * cols)
+        _, mean, rstd = forward(dt, g, x, w, b, rows, cols, dtype, "f32")
+        dx, dw, db = [torch.empty_like(t) for t in x], torch.empty(cols, device="cuda"), torch.empty(cols, device="cuda")
+        base = torch.full((size + 8192,), 0xA5, dtype=torch.uint8, device="cuda")
+        dt.dt_layer_norm_backward(g, x, dy, w, mean, rstd, dx, dw, db, rows, 0, cols, dtype, "f32", "sum",
+                                  base[4096:4096 + size])
+        check_backward(x, dy, w, mean, rstd, dx, dw, db, dtype, "f32")
+        assert (base[:4096] == 0xA5).all() and (base[4096 + size:] == 0xA5).all()
+        with pytest.raises(dt.DtError):
+            dt.dt_layer_norm_backward(g, x, dy, w, mean, rstd, dx, dw, db, rows, 0, cols, dtype, "f32", "sum",
+                                      base[4096:4096 + size - 16])
