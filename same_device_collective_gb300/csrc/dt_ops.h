@@ -34,7 +34,7 @@ struct NormParams {
     // array_bytes each, then of mean and rstd in stat_bytes each
     uint32_t chunk_rows, stages, stage_bytes, array_bytes, stat_bytes;
     uint64_t chunks;
-    uint64_t chunk_end[DT_MAX_RANKS];
+    uint64_t chunk_end[DT_MAX_RANKS];  // rows in registers: the ranks' blocks in one row of `chunks` of them, or chunks 0
     int32_t P;
     int32_t weight_bf16;               // of both
     int32_t param_kind;                // how the forward kernel reads them

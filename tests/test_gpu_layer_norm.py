@@ -360,3 +360,46 @@ def test_workspace_of_long_rows(dt, cols, dtype):
         with pytest.raises(dt.DtError):
             dt.dt_layer_norm_backward(g, x, dy, w, mean, rstd, dx, dw, db, rows, 0, cols, dtype, "f32", "sum",
                                       base[4096:4096 + size - 16])
+
+
+# One row of blocks for all ranks where their rows are uneven, a row to a rank
+# where they are not: every rank has its own rows' results either way.
+@pytest.mark.parametrize("rows", [[900] + [0] * 15, [0] * 15 + [900], [1] * 7 + [700] + [2] * 8, [0, 0, 1000], [500, 0, 500],
+                                  [400, 300, 350], [3, 900, 0, 0, 40]])
+@pytest.mark.parametrize("dtype,cols", [("bf16", 64), ("bf16", 1024), ("f32", 640), ("f32", 31), ("bf16", 4096)])
+def test_rows_of_uneven_ranks(dt, rows, dtype, cols):
+    x, dy, w, b = make(rows, cols, dtype, "f32", seed=cols + len(rows))
+    with group(len(rows)) as g, group(1) as one:
+        y, mean, rstd = forward(dt, g, x, w, b, rows, cols, dtype, "f32")
+        check_forward(x, w, b, y, mean, rstd, dtype)
+        # the same rows as those of a single rank, bit for bit
+        ya, ma, ra = forward(dt, one, [torch.cat(x)], w, b, [sum(rows)], cols, dtype, "f32")
+        assert torch.equal(torch.cat(y), ya[0]) and torch.equal(torch.cat(mean), ma[0]) and torch.equal(torch.cat(rstd), ra[0])
+        assert dt.dt_group_check(g) == dt.DT_OK
+
+
+def test_a_rank_with_all_rows_costs_no_more_than_one_rank(dt):
+    cols, n = 64, 1 << 19
+    x = torch.randn(n, cols, device="cuda").bfloat16()
+    y, w = torch.empty_like(x), torch.ones(cols, device="cuda")
+    none = torch.empty(0, cols, dtype=torch.bfloat16, device="cuda")
+
+    def best(P):
+        rest = [none] * (P - 1)
+        with group(P) as g:
+            call = dt.prepare(dt.dt_layer_norm, g, [x, *rest], w, w, [y, *rest], None, None, [n] + [0] * (P - 1), 0, cols,
+                              1e-5, "bf16", "f32")
+            took = []
+            for _ in range(8):
+                a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+                torch.cuda._sleep(200_000)
+                a.record()
+                for _ in range(4):
+                    call()
+                b.record()
+                torch.cuda.synchronize()
+                took.append(a.elapsed_time(b))
+            return min(took)
+
+    one, many = best(1), best(16)
+    assert many <= 2 * one, (one, many)
