@@ -548,8 +548,13 @@ dt_status dt_timeline_mark(void *stream, uint32_t tag);
 #define DT_BOUNDS_COPY_SHIFT 6
 #define DT_BOUNDS_COPY_2D 7
 #define DT_BOUNDS_BUCKET 8
-#define DT_BOUNDS_VOCAB 10       /* vocabulary loss; buffers: p - [target] 0, dhidden 1, dweight 16 + r, rows laid out again 32 + r */
-#define DT_BOUNDS_NORM 9         /* layer norm; buffers: x r, dy 16 + r, y or dx 32 + r, mean 48 + r, rstd 64 + r */
+/* Layer norm; buffers: x r, dy 16 + r, y or dx 32 + r, mean 48 + r, rstd 64 + r,
+ * weight 80, bias 81, dweight 82, dbias 83, workspace 84. */
+#define DT_BOUNDS_NORM 9
+/* Vocabulary loss; buffers: p - [target] 0, dhidden 1, targets 2, lse 3, losses 4,
+ * loss 5, grad_loss 6, workspace 7, hidden rows laid out again 8, dweight 16 + r,
+ * rank r's rows laid out again 32 + r.  (TMA's own loads stay in their tensor maps.) */
+#define DT_BOUNDS_VOCAB 10
 uint32_t dt_build_flags(void);
 
 #ifdef __cplusplus

@@ -24,6 +24,8 @@ enum BoundsKernel : int {
     kBoundsCopyShift = DT_BOUNDS_COPY_SHIFT,
     kBoundsCopy2d = DT_BOUNDS_COPY_2D,
     kBoundsBucket = DT_BOUNDS_BUCKET,
+    kBoundsNorm = DT_BOUNDS_NORM,
+    kBoundsVocab = DT_BOUNDS_VOCAB,
 };
 
 #ifdef DT_BOUNDS
@@ -54,6 +56,16 @@ static __device__ __noinline__ void bounds_fail(const ErrorSink &s, int kernel, 
 #define DT_IN_BOUNDS(ok, sink, kernel, buffer, addr, lo) \
     ((ok) ? true : (::dt::bounds_fail((sink), (kernel), (buffer), (addr), (lo)), false))
 
+// [a, a + n) lies in buffer number `buffer` of the parameters.
+template <typename Params>
+__device__ __forceinline__ bool in_extent(const Params &p, int kernel, int buffer, const void *a, uint64_t n)
+{
+    const Extent e = p.extent[buffer];
+    return DT_IN_BOUNDS(span_in(a, n, e.lo, e.hi), p.sink, kernel, buffer, a, e.lo);
+}
+
+#define DT_IN_EXTENT(p, kernel, buffer, a, n) ::dt::in_extent((p), (kernel), (buffer), (a), (n))
+
 // Element i of job j's reduction (reduce_elem's operands): every input's
 // element in_off + i and every output's element i lie in their buffers.
 template <int ES>
@@ -80,6 +92,7 @@ __device__ bool reduce_elem_in_bounds(const ReduceParams &p, int kernel, int64_t
 #else
 
 #define DT_IN_BOUNDS(ok, sink, kernel, buffer, addr, lo) true
+#define DT_IN_EXTENT(p, kernel, buffer, a, n) true
 #define DT_REDUCE_ELEM_OK(ES, p, kernel, in_off, i, dst, ndst, job) true
 
 #endif

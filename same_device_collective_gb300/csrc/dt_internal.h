@@ -114,6 +114,24 @@ inline uint64_t trimmed_end(uint64_t lo, uint64_t bytes)
 }
 #endif
 
+// A buffer as the call's arguments give it, for kernels that number theirs
+// (checked in DT_BOUNDS builds only).
+#ifdef DT_BOUNDS
+struct Extent {
+    uint64_t lo, hi;
+};
+#endif
+template <typename Params>
+void set_extent(Params &p, int buffer, const void *a, uint64_t bytes, bool output)
+{
+#ifdef DT_BOUNDS
+    const uint64_t lo = reinterpret_cast<uint64_t>(a);
+    p.extent[buffer] = Extent{lo, output ? trimmed_end(lo, bytes) : lo + bytes};
+#else
+    (void)p; (void)buffer; (void)a; (void)bytes; (void)output;
+#endif
+}
+
 // The buffers a reduction reads and writes, as the call's arguments give
 // them (checked in DT_BOUNDS builds only).
 inline void set_reduce_bounds(ReduceParams &p, const void *const *in, uint64_t in_bytes,

@@ -176,43 +176,63 @@ struct Chunk<T, 1> {
     static __device__ __forceinline__ V all(float x) { return x; }
 };
 
-// Element j of the weight or bias, `none` where there is none.
-__device__ __forceinline__ float param(const void *p, int bf16, uint32_t j, float none)
+// Bounds-checked builds: [a, a + n) lies in buffer `kind` (x 0, dy 1, y or dx 2,
+// mean 3, rstd 4) of rank r, in the weight or bias, or in one of the others.
+#define NORM_OK(kind, r, a, n) DT_IN_EXTENT(p, kBoundsNorm, (kind) * DT_MAX_RANKS + (r), (a), (n))
+#define NORM_PARAM_OK(bias, q, n) DT_IN_EXTENT(p, kBoundsNorm, (bias) ? kNormBias : kNormWeight, (q), (n) * sizeof *(q))
+#define NORM_BUFFER_OK(buffer, a, n) DT_IN_EXTENT(p, kBoundsNorm, (buffer), (a), (n))
+
+// Element j of the weight (bias 0) or the bias (1), or what they are where the
+// caller has none: 1 and 0.
+template <int BIAS>
+__device__ __forceinline__ float param(const NormParams &p, uint32_t j)
 {
-    if (!p) return none;
-    return bf16 ? bf16_to_f32(static_cast<const uint16_t *>(p)[j]) : static_cast<const float *>(p)[j];
+    const void *base = BIAS ? p.bias : p.weight;
+    const float none = BIAS ? 0.0f : 1.0f;
+    if (!base) return none;
+    if (p.weight_bf16) {
+        const uint16_t *q = static_cast<const uint16_t *>(base) + j;
+        return NORM_PARAM_OK(BIAS, q, 1) ? bf16_to_f32(*q) : none;
+    }
+    const float *q = static_cast<const float *>(base) + j;
+    return NORM_PARAM_OK(BIAS, q, 1) ? *q : none;
 }
 
 // A thread's weights or biases from element e on: whole vectors where they lie
 // on 16-byte boundaries.
-template <typename C, int VEC>
-__device__ __forceinline__ void params(const void *p, int bf16, uint32_t e, float none, typename C::V (&f)[C::K])
+template <typename C, int VEC, int BIAS>
+__device__ __forceinline__ void params(const NormParams &p, uint32_t e, typename C::V (&f)[C::K])
 {
+    const void *base = BIAS ? p.bias : p.weight;
     float v[VEC];
-    const bool vec = VEC > 1 && (reinterpret_cast<uint64_t>(p) & 15) == 0;
-    if (!p) {
+    const bool vec = VEC > 1 && (reinterpret_cast<uint64_t>(base) & 15) == 0;
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) v[i] = none;
-    } else if (bf16) {
-        const uint16_t *q = static_cast<const uint16_t *>(p) + e;
-        uint32_t u[VEC > 1 ? VEC / 2 : 1];
-        if (VEC > 1 && vec) {
-            if constexpr (VEC == 8) *reinterpret_cast<uint4 *>(u) = *reinterpret_cast<const uint4 *>(q);
-            if constexpr (VEC == 4) *reinterpret_cast<uint2 *>(u) = *reinterpret_cast<const uint2 *>(q);
-        } else {
+    for (int i = 0; i < VEC; ++i) v[i] = BIAS ? 0.0f : 1.0f;
+    if (base && p.weight_bf16) {
+        const uint16_t *q = static_cast<const uint16_t *>(base) + e;
+        if (NORM_PARAM_OK(BIAS, q, VEC)) {
+            uint32_t u[VEC > 1 ? VEC / 2 : 1];
+            if (VEC > 1 && vec) {
+                if constexpr (VEC == 8) *reinterpret_cast<uint4 *>(u) = *reinterpret_cast<const uint4 *>(q);
+                if constexpr (VEC == 4) *reinterpret_cast<uint2 *>(u) = *reinterpret_cast<const uint2 *>(q);
+            } else {
 #pragma unroll
-            for (int i = 0; i < VEC; i += 2) u[i / 2] = q[i] | (VEC > 1 ? (uint32_t)q[i + (VEC > 1)] << 16 : 0u);
+                for (int i = 0; i < VEC; i += 2) u[i / 2] = q[i] | (VEC > 1 ? (uint32_t)q[i + (VEC > 1)] << 16 : 0u);
+            }
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) v[i] = i & 1 ? bf16_hi(u[i / 2]) : bf16_lo(u[i / 2]);
         }
+    } else if (base) {
+        const float *q = static_cast<const float *>(base) + e;
+        if (NORM_PARAM_OK(BIAS, q, VEC)) {
+            if (VEC > 1 && vec) {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) v[i] = i & 1 ? bf16_hi(u[i / 2]) : bf16_lo(u[i / 2]);
-    } else {
-        const float *q = static_cast<const float *>(p) + e;
-        if (VEC > 1 && vec) {
+                for (int i = 0; i < VEC / 4; ++i)
+                    *reinterpret_cast<float4 *>(v + 4 * i) = *reinterpret_cast<const float4 *>(q + 4 * i);
+            } else {
 #pragma unroll
-            for (int i = 0; i < VEC / 4; ++i) *reinterpret_cast<float4 *>(v + 4 * i) = *reinterpret_cast<const float4 *>(q + 4 * i);
-        } else {
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) v[i] = q[i];
+                for (int i = 0; i < VEC; ++i) v[i] = q[i];
+            }
         }
     }
     if constexpr (VEC == 1) {
@@ -232,23 +252,6 @@ __device__ __forceinline__ int find_rank(const NormParams &p, uint64_t row, uint
     local = row - begin;
     return r;
 }
-
-#ifdef DT_BOUNDS
-// [a, a + n) lies in rank r's buffer of `elem` bytes for each of its rows'
-// elements (mean and rstd: cols = 1).
-__device__ __forceinline__ bool in_rank(const NormParams &p, const void *const *base, int kind, int r,
-                                        const void *a, uint64_t n, uint64_t row_bytes)
-{
-    const uint64_t lo = reinterpret_cast<uint64_t>(base[r]);
-    const uint64_t rows = p.row_end[r] - (r ? p.row_end[r - 1] : 0);
-    return DT_IN_BOUNDS(span_in(a, n, lo, lo + rows * row_bytes), p.sink, DT_BOUNDS_NORM,
-                        kind * DT_MAX_RANKS + r, a, lo);
-}
-#define NORM_OK(base, kind, r, a, n, row_bytes) \
-    in_rank(p, reinterpret_cast<const void *const *>(base), (kind), (r), (a), (n), (row_bytes))
-#else
-#define NORM_OK(base, kind, r, a, n, row_bytes) true
-#endif
 
 // Values of each warp of a row to all of its threads: `red` is
 // double-buffered by the caller's `phase`, and a buffer is written again only
@@ -370,8 +373,7 @@ struct Ring {
         }
         const uint64_t lo = reinterpret_cast<uint64_t>(bases[r]) + row * row_bytes, hi = lo + n * row_bytes;
         const uint64_t from = lo & ~15ull, to = (hi + 15) & ~15ull;
-        if (!NORM_OK(bases, (which < 2 ? which : which + 1), r, reinterpret_cast<const void *>(lo), hi - lo, row_bytes))
-            return 0;
+        if (!NORM_OK(which < 2 ? which : which + 1, r, reinterpret_cast<const void *>(lo), hi - lo)) return 0;
         bulk_load(dst, reinterpret_cast<const void *>(from), (uint32_t)(to - from), bars + 8 * stage);
         return (uint32_t)(to - from);
     }
@@ -548,8 +550,8 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(const __grid_cons
     auto weights = [&](int n) {
         const uint32_t e = (n * tpr + t) * VEC;
         if (e >= cols) return;
-        params<C, VEC>(p.weight, p.weight_bf16, e, 1.0f, w[n]);
-        params<C, VEC>(p.bias, p.weight_bf16, e, 0.0f, b[n]);
+        params<C, VEC, 0>(p, e, w[n]);
+        params<C, VEC, 1>(p, e, b[n]);
     };
     if constexpr (kHold)
 #pragma unroll
@@ -623,7 +625,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(const __grid_cons
                     x[j][n].get(f);
 #pragma unroll
                     for (int i = 0; i < K; ++i) f[i] = fma(mul(add(f[i], minus), scale), w[n][i], b[n][i]);
-                    if (NORM_OK(p.out, 2, r, to + e, VEC * sizeof(T), cols * sizeof(T))) C::store(to + e, f);
+                    if (NORM_OK(2, r, to + e, VEC * sizeof(T))) C::store(to + e, f);
                 }
             }
             // one lane to a row, of the team's last warp
@@ -633,8 +635,8 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(const __grid_cons
 #pragma unroll
                 for (int j = 1; j < B; ++j)
                     if (lane == j) mean = s[j], rstd = m2[j];
-                if (means && NORM_OK(p.mean, 3, r, means + at, 4, 4)) means[at] = mean;
-                if (rstds && NORM_OK(p.rstd, 4, r, rstds + at, 4, 4)) rstds[at] = rstd;
+                if (means && NORM_OK(3, r, means + at, 4)) means[at] = mean;
+                if (rstds && NORM_OK(4, r, rstds + at, 4)) rstds[at] = rstd;
             }
         }
         ring.next();
@@ -647,23 +649,25 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(const __grid_cons
 // within its loops, so that loads are not kept apart by branches.
 enum ParamKind { kParamBf16, kParamF32, kParamAny };   // whole vectors of either type, or whatever there is
 
-template <typename C, int VEC, int KIND>
-__device__ __forceinline__ void read_param(const NormParams &p, const void *q, uint32_t e, float none, typename C::V (&f)[C::K])
+template <typename C, int VEC, int KIND, int BIAS>
+__device__ __forceinline__ void read_param(const NormParams &p, uint32_t e, typename C::V (&f)[C::K])
 {
     if constexpr (KIND == kParamBf16 && VEC == 8) {
-        const uint4 u = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(q) + e));
+        const uint16_t *q = static_cast<const uint16_t *>(BIAS ? p.bias : p.weight) + e;
+        const uint4 u = NORM_PARAM_OK(BIAS, q, VEC) ? __ldg(reinterpret_cast<const uint4 *>(q)) : make_uint4(0, 0, 0, 0);
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) f[i] = pair(bf16_lo(w[i]), bf16_hi(w[i]));
     } else if constexpr (KIND == kParamF32 && VEC > 1) {
 #pragma unroll
         for (int i = 0; i < C::K; i += 2) {
-            const float4 u = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(q) + e + 2 * i));
+            const float *q = static_cast<const float *>(BIAS ? p.bias : p.weight) + e + 2 * i;
+            const float4 u = NORM_PARAM_OK(BIAS, q, 4) ? __ldg(reinterpret_cast<const float4 *>(q)) : make_float4(0, 0, 0, 0);
             f[i] = pair(u.x, u.y);
             f[i + 1] = pair(u.z, u.w);
         }
     } else {
-        params<C, VEC>(q, p.weight_bf16, e, none, f);
+        params<C, VEC, BIAS>(p, e, f);
     }
 }
 
@@ -712,7 +716,7 @@ norm_rows_kernel(const __grid_constant__ NormParams p)
         for (int n = 0; n < N; ++n) {
             const uint32_t first = (n * tpr + t / L * L) * VEC, e = (n * tpr + t) * VEC;
             mine += first < cols ? min(cols - first, (uint32_t)(L * VEC)) : 0;
-            if (e < cols && there && NORM_OK(p.x, 0, r, src + e, VEC * sizeof(T), cols * sizeof(T))) x[n].load(src + e);
+            if (e < cols && there && NORM_OK(0, r, src + e, VEC * sizeof(T))) x[n].load(src + e);
             else x[n].zero();
         }
         if constexpr (EARLY)
@@ -720,8 +724,8 @@ norm_rows_kernel(const __grid_constant__ NormParams p)
             for (int n = 0; n < N; ++n) {
                 const uint32_t e = (n * tpr + t) * VEC;
                 if (e >= cols) continue;
-                params<C, VEC>(p.weight, p.weight_bf16, e, 1.0f, w[n]);
-                params<C, VEC>(p.bias, p.weight_bf16, e, 0.0f, b[n]);
+                params<C, VEC, 0>(p, e, w[n]);
+                params<C, VEC, 1>(p, e, b[n]);
             }
         const float inv_mine = mine ? __frcp_rn((float)mine) : 0.0f;
         // four sums, so that an addition does not wait for the one before
@@ -783,22 +787,22 @@ norm_rows_kernel(const __grid_constant__ NormParams p)
                 if (e >= cols || !there) continue;
                 constexpr int k = EARLY ? 1 : 0;
                 if constexpr (!EARLY) {
-                    read_param<C, VEC, KIND>(p, p.weight, e, 1.0f, w[0]);
-                    read_param<C, VEC, KIND>(p, p.bias, e, 0.0f, b[0]);
+                    read_param<C, VEC, KIND, 0>(p, e, w[0]);
+                    read_param<C, VEC, KIND, 1>(p, e, b[0]);
                 }
                 V f[C::K];
                 x[n].get(f);
 #pragma unroll
                 for (int i = 0; i < C::K; ++i) f[i] = fma(mul(add(f[i], minus), scale), w[n * k][i], b[n * k][i]);
-                if (NORM_OK(p.out, 2, r, y + e, VEC * sizeof(T), cols * sizeof(T))) C::store(y + e, f);
+                if (NORM_OK(2, r, y + e, VEC * sizeof(T))) C::store(y + e, f);
             }
         };
         if (EARLY || p.param_kind == kParamAny) finish(std::integral_constant<int, kParamAny>());
         else if (p.param_kind == kParamBf16) finish(std::integral_constant<int, kParamBf16>());
         else finish(std::integral_constant<int, kParamF32>());
         if (t == 0 && there) {
-            if (p.mean[r] && NORM_OK(p.mean, 3, r, p.mean[r] + row, 4, 4)) p.mean[r][row] = mean;
-            if (p.rstd[r] && NORM_OK(p.rstd, 4, r, p.rstd[r] + row, 4, 4)) p.rstd[r][row] = rstd;
+            if (p.mean[r] && NORM_OK(3, r, p.mean[r] + row, 4)) p.mean[r][row] = mean;
+            if (p.rstd[r] && NORM_OK(4, r, p.rstd[r] + row, 4)) p.rstd[r][row] = rstd;
         }
     }
     DT_TL_END_BLOCK(DT_TL_NORM);
@@ -836,7 +840,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_kernel(const __
     V dw[N][K], db[N][K], w[N][K];
     auto weights = [&](int n) {
         const uint32_t e = (n * tpr + t) * VEC;
-        if (e < cols) params<C, VEC>(p.weight, p.weight_bf16, e, 1.0f, w[n]);
+        if (e < cols) params<C, VEC, 0>(p, e, w[n]);
     };
 #pragma unroll
     for (int n = 0; n < N; ++n) {
@@ -917,7 +921,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_kernel(const __
                     g[j][n].get(d);
 #pragma unroll
                     for (int i = 0; i < K; ++i) f[i] = fma(add(f[i], minus), c1, fma(mul(d[i], w[n][i]), scale, c0));
-                    if (NORM_OK(p.out, 2, r, to + e, VEC * sizeof(T), cols * sizeof(T))) C::store(to + e, f);
+                    if (NORM_OK(2, r, to + e, VEC * sizeof(T))) C::store(to + e, f);
                 }
             }
         }
@@ -947,8 +951,9 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_kernel(const __
                 if (e >= cols) continue;
 #pragma unroll
                 for (int i = 0; i < K; ++i) {   // cols is even where there are pairs
-                    reinterpret_cast<V *>(mine + e)[i] = dw[n][i];
-                    reinterpret_cast<V *>(mine + cols + e)[i] = db[n][i];
+                    V *a = reinterpret_cast<V *>(mine + e) + i, *c = reinterpret_cast<V *>(mine + cols + e) + i;
+                    if (groups > 1 || NORM_BUFFER_OK(kNormWorkspace, a, sizeof(V))) *a = dw[n][i];
+                    if (groups > 1 || NORM_BUFFER_OK(kNormWorkspace, c, sizeof(V))) *c = db[n][i];
                 }
             }
         if (groups > 1) {
@@ -958,7 +963,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_kernel(const __
                 float v = all[e];
 #pragma unroll 4
                 for (uint32_t k = 1; k < groups; ++k) v += all[(size_t)k * 2 * cols + e];
-                out[e] = v;
+                if (NORM_BUFFER_OK(kNormWorkspace, out + e, 4)) out[e] = v;
             }
         }
     }
@@ -983,7 +988,8 @@ __global__ void __launch_bounds__(kJoinCols *kJoinSlices) norm_join_kernel(const
 #pragma unroll
             for (uint32_t j = 0; j < 10; ++j) {
                 const uint32_t at = k + j * kJoinSlices;
-                o[j] = at < p.parts ? in[(uint64_t)at * 2 * p.cols] : 0.0f;
+                const float *from = in + (uint64_t)at * 2 * p.cols;
+                o[j] = at < p.parts && NORM_BUFFER_OK(kNormWorkspace, from, 4) ? *from : 0.0f;
             }
 #pragma unroll
             for (uint32_t j = 0; j < 10; ++j) v += o[j];
@@ -999,9 +1005,12 @@ __global__ void __launch_bounds__(kJoinCols *kJoinSlices) norm_join_kernel(const
     if (threadIdx.x % kJoinSlices == 0 && col < p.cols) {
         if (p.avg) v = avg_of(v, p.P, p.avg_scale, p.avg_pow2);
         void *out = blockIdx.y ? p.dbias : p.dweight;
-        if (out) {
-            if (p.weight_bf16) static_cast<uint16_t *>(out)[col] = f32_to_bf16(v);
-            else static_cast<float *>(out)[col] = v;
+        if (out && p.weight_bf16) {
+            uint16_t *to = static_cast<uint16_t *>(out) + col;
+            if (NORM_BUFFER_OK(blockIdx.y ? kNormDbias : kNormDweight, to, 2)) *to = f32_to_bf16(v);
+        } else if (out) {
+            float *to = static_cast<float *>(out) + col;
+            if (NORM_BUFFER_OK(blockIdx.y ? kNormDbias : kNormDweight, to, 4)) *to = v;
         }
     }
     DT_TL_END_BLOCK(DT_TL_NORM);
@@ -1023,7 +1032,7 @@ __global__ void __launch_bounds__(kLongThreads) norm_long_kernel(const __grid_co
         const T *x = static_cast<const T *>(p.x[r]) + local * p.cols;
         T *y = static_cast<T *>(p.out[r]) + local * p.cols;
         auto at = [&](uint32_t e) {
-            return NORM_OK(p.x, 0, r, x + e, sizeof(T), p.cols * sizeof(T)) ? to_f32(x[e]) : 0.0f;
+            return NORM_OK(0, r, x + e, sizeof(T)) ? to_f32(x[e]) : 0.0f;
         };
         float s[2] = {0.0f, 0.0f}, m2[2] = {0.0f, 0.0f};
         for (uint32_t e = threadIdx.x; e < p.cols; e += kLongThreads) s[0] += at(e);
@@ -1036,13 +1045,12 @@ __global__ void __launch_bounds__(kLongThreads) norm_long_kernel(const __grid_co
         row_sum<2>(m2, red, phase, Team<32>(kLongThreads));
         const float rstd = rstd_of(m2[0], p.inv_cols, p.eps);
         for (uint32_t e = threadIdx.x; e < p.cols; e += kLongThreads) {
-            const float f = fmaf((at(e) - mean) * rstd, param(p.weight, p.weight_bf16, e, 1.0f),
-                                 param(p.bias, p.weight_bf16, e, 0.0f));
-            if (NORM_OK(p.out, 2, r, y + e, sizeof(T), p.cols * sizeof(T))) from_f32(f, y + e);
+            const float f = fmaf((at(e) - mean) * rstd, param<0>(p, e), param<1>(p, e));
+            if (NORM_OK(2, r, y + e, sizeof(T))) from_f32(f, y + e);
         }
         if (threadIdx.x == 0) {
-            if (p.mean[r] && NORM_OK(p.mean, 3, r, p.mean[r] + local, 4, 4)) p.mean[r][local] = mean;
-            if (p.rstd[r] && NORM_OK(p.rstd, 4, r, p.rstd[r] + local, 4, 4)) p.rstd[r][local] = rstd;
+            if (p.mean[r] && NORM_OK(3, r, p.mean[r] + local, 4)) p.mean[r][local] = mean;
+            if (p.rstd[r] && NORM_OK(4, r, p.rstd[r] + local, 4)) p.rstd[r][local] = rstd;
         }
     }
     DT_TL_END_BLOCK(DT_TL_NORM);
@@ -1062,14 +1070,13 @@ __global__ void __launch_bounds__(kLongThreads) norm_backward_long_kernel(const 
         const T *x = static_cast<const T *>(p.x[r]) + local * p.cols;
         const T *dy = static_cast<const T *>(p.dy[r]) + local * p.cols;
         T *dx = static_cast<T *>(p.out[r]) + local * p.cols;
-        const float mean = NORM_OK(p.mean, 3, r, p.mean[r] + local, 4, 4) ? p.mean[r][local] : 0.0f;
-        const float rstd = NORM_OK(p.rstd, 4, r, p.rstd[r] + local, 4, 4) ? p.rstd[r][local] : 0.0f;
+        const float mean = NORM_OK(3, r, p.mean[r] + local, 4) ? p.mean[r][local] : 0.0f;
+        const float rstd = NORM_OK(4, r, p.rstd[r] + local, 4) ? p.rstd[r][local] : 0.0f;
         auto h_at = [&](uint32_t e) {
-            return NORM_OK(p.x, 0, r, x + e, sizeof(T), p.cols * sizeof(T)) ? (to_f32(x[e]) - mean) * rstd : 0.0f;
+            return NORM_OK(0, r, x + e, sizeof(T)) ? (to_f32(x[e]) - mean) * rstd : 0.0f;
         };
         auto q_at = [&](uint32_t e) {
-            return NORM_OK(p.dy, 1, r, dy + e, sizeof(T), p.cols * sizeof(T))
-                       ? to_f32(dy[e]) * param(p.weight, p.weight_bf16, e, 1.0f) : 0.0f;
+            return NORM_OK(1, r, dy + e, sizeof(T)) ? to_f32(dy[e]) * param<0>(p, e) : 0.0f;
         };
         float s[2] = {0.0f, 0.0f};
         for (uint32_t e = threadIdx.x; e < p.cols; e += kLongThreads) {
@@ -1081,7 +1088,7 @@ __global__ void __launch_bounds__(kLongThreads) norm_backward_long_kernel(const 
         const float mq = s[0] * p.inv_cols, mqh = s[1] * p.inv_cols;
         for (uint32_t e = threadIdx.x; e < p.cols; e += kLongThreads) {
             const float f = rstd * (q_at(e) - mq - h_at(e) * mqh);
-            if (NORM_OK(p.out, 2, r, dx + e, sizeof(T), p.cols * sizeof(T))) from_f32(f, dx + e);
+            if (NORM_OK(2, r, dx + e, sizeof(T))) from_f32(f, dx + e);
         }
     }
     DT_TL_END_BLOCK(DT_TL_NORM);
@@ -1104,15 +1111,16 @@ __global__ void __launch_bounds__(kThreads) norm_columns_long_kernel(const __gri
             const int r = find_rank(p, row, local);
             const uint64_t at = local * p.cols + e;
             const T *x = static_cast<const T *>(p.x[r]) + at, *dy = static_cast<const T *>(p.dy[r]) + at;
-            if (!NORM_OK(p.x, 0, r, x, sizeof(T), p.cols * sizeof(T)) ||
-                !NORM_OK(p.dy, 1, r, dy, sizeof(T), p.cols * sizeof(T)))
+            if (!NORM_OK(0, r, x, sizeof(T)) || !NORM_OK(1, r, dy, sizeof(T)) || !NORM_OK(3, r, p.mean[r] + local, 4) ||
+                !NORM_OK(4, r, p.rstd[r] + local, 4))
                 continue;
             const float d = to_f32(*dy);
             dw = fmaf(d, (to_f32(*x) - p.mean[r][local]) * p.rstd[r][local], dw);
             db += d;
         }
-        p.partial[(uint64_t)blockIdx.y * 2 * p.cols + e] = dw;
-        p.partial[(uint64_t)blockIdx.y * 2 * p.cols + p.cols + e] = db;
+        float *out = p.partial + (uint64_t)blockIdx.y * 2 * p.cols + e;
+        if (NORM_BUFFER_OK(kNormWorkspace, out, 4)) *out = dw;
+        if (NORM_BUFFER_OK(kNormWorkspace, out + p.cols, 4)) out[p.cols] = db;
     }
     DT_TL_END_BLOCK(DT_TL_NORM);
 }

@@ -82,6 +82,8 @@ dt_status norm_common(dt_group *g, const void *const *x, void *const *out, const
         if (!x[r] || !out[r] || !multiple(x[r], es) || !multiple(out[r], es)) return DT_ERR_INVALID;
         p.x[r] = x[r];
         p.out[r] = out[r];
+        dt::set_extent(p, r, x[r], n[r] * cols * es, false);
+        dt::set_extent(p, 2 * DT_MAX_RANKS + r, out[r], n[r] * cols * es, true);
         vec = vec && aligned16(x[r]) && aligned16(out[r]);
     }
     p.rows = total;
@@ -91,6 +93,7 @@ dt_status norm_common(dt_group *g, const void *const *x, void *const *out, const
     p.weight = weight;
     p.weight_bf16 = weight_dtype == DT_BF16;
     p.sink = error_sink(g);
+    dt::set_extent(p, dt::kNormWeight, weight, cols * ws, false);
     return DT_OK;
 }
 
@@ -258,6 +261,9 @@ dt_status vocab_common(dt_group *g, const void *hidden, const void *const *weigh
     p.acc = reinterpret_cast<float *>(ws + v.acc);
     p.gpitch = v.piece * dt::kVocabUnit;
     p.apitch = v.apitch;
+    dt::set_extent(p, dt::kVocabG, p.gbuf, back ? (uint64_t)tokens * p.gpitch * 2 : 0, false);
+    dt::set_extent(p, dt::kVocabTargets, targets, tokens * 4, false);
+    dt::set_extent(p, dt::kVocabWorkspace, workspace, v.bytes, false);
     return DT_OK;
 }
 
@@ -313,6 +319,10 @@ void vocab_prepare_pack(dt_group *g, const void *hidden, const void *const *weig
     pack.dim = p.dim;
     pack.pitch = v.pitch;
     pack.sink = p.sink;
+    for (int r = 0; r < g->P; ++r)
+        dt::set_extent(pack, dt::kVocabRows + r, weight[r], (uint64_t)p.rows[r] * p.dim * 2, false);
+    dt::set_extent(pack, dt::kVocabHidden, hidden, (uint64_t)p.tokens * p.dim * 2, false);
+    dt::set_extent(pack, dt::kVocabWorkspace, workspace, v.bytes, false);
 }
 
 // The piece's first unit and, where needed, its rows laid out again.
@@ -377,11 +387,14 @@ dt_status dt_layer_norm(dt_group_t g, const void *const *x, const void *weight, 
         b.write(y[r], n[r] * row_bytes, r);
         b.write(p.mean[r], n[r] * 4);
         b.write(p.rstd[r], n[r] * 4);
+        dt::set_extent(p, 3 * DT_MAX_RANKS + r, p.mean[r], n[r] * 4, true);
+        dt::set_extent(p, 4 * DT_MAX_RANKS + r, p.rstd[r], n[r] * 4, true);
     }
     if (b.clash()) return DT_ERR_INVALID;
     if (p.rows == 0) return DT_OK;
     p.bias = bias;
     p.eps = eps;
+    dt::set_extent(p, dt::kNormBias, bias, w_bytes, false);
     DeviceScope scope(g->device);
     if (!scope.ok) return DT_ERR_CUDA;
     return cuda_status(dt::launch_norm(p, dtype, vec, g->device, static_cast<cudaStream_t>(stream)));
@@ -424,6 +437,9 @@ dt_status dt_layer_norm_backward(dt_group_t g, const void *const *x, const void 
         b.read(mean[r], n[r] * 4);
         b.read(rstd[r], n[r] * 4);
         b.write(dx[r], n[r] * cols * es, r);
+        dt::set_extent(p, DT_MAX_RANKS + r, dy[r], n[r] * cols * es, false);
+        dt::set_extent(p, 3 * DT_MAX_RANKS + r, mean[r], n[r] * 4, false);
+        dt::set_extent(p, 4 * DT_MAX_RANKS + r, rstd[r], n[r] * 4, false);
     }
     b.write(dweight, cols * ws);
     b.write(dbias, cols * ws);
@@ -432,6 +448,9 @@ dt_status dt_layer_norm_backward(dt_group_t g, const void *const *x, const void 
     if (p.rows == 0 && !sums) return DT_OK;
     p.dweight = dweight;
     p.dbias = dbias;
+    dt::set_extent(p, dt::kNormDweight, dweight, cols * ws, true);
+    dt::set_extent(p, dt::kNormDbias, dbias, cols * ws, true);
+    dt::set_extent(p, dt::kNormWorkspace, workspace, workspace_bytes, false);
     p.partial = sums ? static_cast<float *>(workspace) : nullptr;
     p.avg = op == DT_AVG;
     p.avg_pow2 = (g->P & (g->P - 1)) == 0;
@@ -501,6 +520,11 @@ dt_status dt_vocab_loss(dt_group_t g, const void *hidden, const void *const *wei
     f.ignore = ignore_index;
     f.avg = p.avg;
     f.sink = p.sink;
+    dt::set_extent(f, dt::kVocabTargets, targets, tokens * 4, false);
+    dt::set_extent(f, dt::kVocabLse, lse, tokens * 4, true);
+    dt::set_extent(f, dt::kVocabLosses, losses, tokens * 4, true);
+    dt::set_extent(f, dt::kVocabLoss, loss, 4, true);
+    dt::set_extent(f, dt::kVocabWorkspace, workspace, v.bytes, false);
     return cuda_status(dt::launch_vocab_finish(f, s));
 }
 
@@ -534,11 +558,15 @@ dt_status dt_vocab_loss_backward(dt_group_t g, const void *hidden, const void *c
         p.dw[r] = static_cast<uint16_t *>(dweight[r]);
         while (!multiple(dweight[r], 2 * p.dw_align)) p.dw_align /= 2;
         b.write(dweight[r], v.rows[r] * dim * 2);
+        dt::set_extent(p, dt::kVocabDw + r, dweight[r], v.rows[r] * dim * 2, true);
     }
     if (b.clash()) return DT_ERR_INVALID;
     p.dh = static_cast<uint16_t *>(dhidden);
     p.lse = lse;
     p.grad = grad_loss;
+    dt::set_extent(p, dt::kVocabDh, dhidden, tokens * dim * 2, true);
+    dt::set_extent(p, dt::kVocabLse, lse, tokens * 4, false);
+    dt::set_extent(p, dt::kVocabGrad, grad_loss, 4, false);
     DeviceScope scope(g->device);
     if (!scope.ok) return DT_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);

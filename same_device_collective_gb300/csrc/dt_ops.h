@@ -13,6 +13,10 @@
 namespace dt {
 
 // ---- layer norm -------------------------------------------------------------
+// Buffers, as bounds-checked builds number them: x r, dy 16 + r, y or dx 32 + r,
+// mean 48 + r, rstd 64 + r, then these.
+enum NormBuffer : int { kNormWeight = 5 * DT_MAX_RANKS, kNormBias, kNormDweight, kNormDbias, kNormWorkspace, kNormBuffers };
+
 // The ranks' rows are numbered through: rank r has rows [row_end[r - 1],
 // row_end[r]) of the call.
 struct NormParams {
@@ -42,7 +46,10 @@ struct NormParams {
     float avg_scale;
     int32_t avg;                       // 0: sum; 1: divide the gradients by P
     int32_t avg_pow2;
-    ErrorSink sink;                    // bounds-checked builds
+    ErrorSink sink;
+#ifdef DT_BOUNDS
+    Extent extent[kNormBuffers];
+#endif
 };
 
 // Bytes of partial sums that the backward pass of rows of `cols` elements

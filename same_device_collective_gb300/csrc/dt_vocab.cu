@@ -266,13 +266,7 @@ __device__ __forceinline__ uint4 *out_chunk(unsigned char *buf, uint32_t row, ui
     return reinterpret_cast<uint4 *>(buf + row * 128 + ((c ^ (row & 7)) << 4));
 }
 
-#ifdef DT_BOUNDS
-#define VOCAB_OK(a, n, lo, bytes, buffer)                                                                     \
-    DT_IN_BOUNDS(span_in((a), (n), (uint64_t)(lo), (uint64_t)(lo) + (bytes)), p.sink, DT_BOUNDS_VOCAB, (buffer), (a), \
-                 (uint64_t)(lo))
-#else
-#define VOCAB_OK(a, n, lo, bytes, buffer) true
-#endif
+#define VOCAB_OK(buffer, a, n) DT_IN_EXTENT(p, kBoundsVocab, (buffer), (a), (n))
 
 // One instruction's worth of a row: N 16-bit elements.
 template <int N> struct Words;
@@ -284,10 +278,10 @@ template <> struct Words<2> { using type = uint32_t; };
 // many rows at a time as that leaves lanes for.
 template <int N>
 __device__ __forceinline__ void store_rows(const VocabParams &p, const unsigned char *buf, uint16_t *out, uint64_t pitch,
-                                           uint32_t rows, uint32_t cols, const void *lo, uint64_t bytes, int buffer)
+                                           uint32_t rows, uint32_t cols, int buffer)
 {
     using W = typename Words<N>::type;
-    (void)p, (void)lo, (void)bytes, (void)buffer;
+    (void)p, (void)buffer;
     constexpr uint32_t kLanes = 64 / N, kRows = 32 / kLanes;
     const uint32_t lane = threadIdx.x & 31, e = lane % kLanes * N, first = lane / kLanes;
     if (e >= cols) return;
@@ -296,7 +290,7 @@ __device__ __forceinline__ void store_rows(const VocabParams &p, const unsigned 
         const uint32_t row = k + first;
         const W v = *reinterpret_cast<const W *>(buf + row * 128 + ((((e >> 3) ^ row) & 7) << 4) + (e & 7) * 2);
         uint16_t *to = out + row * pitch + e;
-        if (row < rows && VOCAB_OK(to, 2 * N, lo, bytes, buffer)) *reinterpret_cast<W *>(to) = v;
+        if (row < rows && VOCAB_OK(buffer, to, 2 * N)) *reinterpret_cast<W *>(to) = v;
     }
 }
 
@@ -305,10 +299,9 @@ __device__ __forceinline__ void store_rows(const VocabParams &p, const unsigned 
 // element of such a row, and a last one that no word takes, go afterwards, a
 // row to a lane.
 __device__ __forceinline__ void store_rows_odd(const VocabParams &p, const unsigned char *buf, uint16_t *out,
-                                               uint64_t pitch, uint32_t rows, uint32_t cols, const void *lo,
-                                               uint64_t bytes, int buffer)
+                                               uint64_t pitch, uint32_t rows, uint32_t cols, int buffer)
 {
-    (void)p, (void)lo, (void)bytes, (void)buffer;
+    (void)p, (void)buffer;
     const uint32_t lane = threadIdx.x & 31;
     const uint32_t odd0 = (uint32_t)(reinterpret_cast<uintptr_t>(out) >> 1) & 1, odd_step = (uint32_t)pitch & 1;
     uint16_t *at = out + 2 * lane;
@@ -319,14 +312,14 @@ __device__ __forceinline__ void store_rows_odd(const VocabParams &p, const unsig
                                                                (lane & 3) * 4);
         const uint32_t next = __shfl_down_sync(0xFFFFFFFFu, w, 1);
         uint16_t *to = at + odd;
-        if (row < rows && 2 * lane + odd + 1 < cols && VOCAB_OK(to, 4, lo, bytes, buffer))
+        if (row < rows && 2 * lane + odd + 1 < cols && VOCAB_OK(buffer, to, 4))
             *reinterpret_cast<uint32_t *>(to) = odd ? __funnelshift_r(w, next, 16) : w;
     }
     if (lane >= rows) return;
     auto element = [&](uint32_t e) {
         const uint16_t v = *reinterpret_cast<const uint16_t *>(buf + lane * 128 + ((((e >> 3) ^ lane) & 7) << 4) + (e & 7) * 2);
         uint16_t *to = out + lane * pitch + e;
-        if (VOCAB_OK(to, 2, lo, bytes, buffer)) *to = v;
+        if (VOCAB_OK(buffer, to, 2)) *to = v;
     };
     odd = odd0 ^ (odd_step & lane);
     if (odd) element(0);
@@ -339,7 +332,7 @@ __device__ __forceinline__ void store_rows_odd(const VocabParams &p, const unsig
 // took 9700 cycles, against 1000 of its products.
 __device__ __forceinline__ void store_rows_bf16(const VocabParams &p, unsigned char *buf, const uint32_t (&w)[32],
                                                 uint16_t *out, uint64_t pitch, uint32_t rows, uint32_t cols,
-                                                uint32_t align, const void *lo, uint64_t bytes, int buffer)
+                                                uint32_t align, int buffer)
 {
     const uint32_t lane = threadIdx.x & 31;
     __syncwarp();
@@ -347,10 +340,10 @@ __device__ __forceinline__ void store_rows_bf16(const VocabParams &p, unsigned c
     for (uint32_t c = 0; c < 8; ++c)
         *out_chunk(buf, lane, c) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
     __syncwarp();
-    if (align == 8) store_rows<8>(p, buf, out, pitch, rows, cols, lo, bytes, buffer);
-    else if (align == 4) store_rows<4>(p, buf, out, pitch, rows, cols, lo, bytes, buffer);
-    else if (align == 2) store_rows<2>(p, buf, out, pitch, rows, cols, lo, bytes, buffer);
-    else store_rows_odd(p, buf, out, pitch, rows, cols, lo, bytes, buffer);
+    if (align == 8) store_rows<8>(p, buf, out, pitch, rows, cols, buffer);
+    else if (align == 4) store_rows<4>(p, buf, out, pitch, rows, cols, buffer);
+    else if (align == 2) store_rows<2>(p, buf, out, pitch, rows, cols, buffer);
+    else store_rows_odd(p, buf, out, pitch, rows, cols, buffer);
 }
 
 // From operand A's first box to its second: K-major boxes of few tokens' rows
@@ -460,7 +453,7 @@ vocab_kernel(const __grid_constant__ VocabParams p)
 
     if (warp == kFinishWarps) {
         if (lane == 0) {
-            if (MODE == kLse && blockIdx.x == 0) *p.ticket = 0;   // for the kernel that joins the partial sums
+            if (MODE == kLse && blockIdx.x == 0 && VOCAB_OK(kVocabWorkspace, p.ticket, 4)) *p.ticket = 0;   // for the kernel that joins the partial sums
             uint32_t n = 0, s = 0, round = 0;   // loads issued; the next one's stage and its parity
             bool ok = true;
             for (uint32_t k = 0; ok && next_tile<MODE, CG>(p, worker, workers, k, t); ++k) {
@@ -536,7 +529,7 @@ vocab_kernel(const __grid_constant__ VocabParams p)
 #pragma unroll
                 for (uint32_t j = 0; j < 8; ++j) {
                     const uint32_t k = first + 32 * j + lane;
-                    v[j] = k < end ? p.targets[k] : p.ignore;
+                    v[j] = k < end && VOCAB_OK(kVocabTargets, p.targets + k, 4) ? p.targets[k] : p.ignore;
                 }
 #pragma unroll
                 for (uint32_t j = 0; j < 8; ++j) {
@@ -546,7 +539,7 @@ vocab_kernel(const __grid_constant__ VocabParams p)
                 }
             }
             kept = __reduce_add_sync(0xFFFFFFFFu, kept);
-            if (lane == 0) p.kept[blockIdx.x] = kept;
+            if (lane == 0 && VOCAB_OK(kVocabWorkspace, p.kept + blockIdx.x, 4)) p.kept[blockIdx.x] = kept;
         }
     } else {
         // Warps w, w + 4, ... read the same 32 rows (a warp reaches the tensor
@@ -555,13 +548,15 @@ vocab_kernel(const __grid_constant__ VocabParams p)
         unsigned char *buf = out_buf + (MODE == kLse ? 0 : warp * kStageOut);
         float scale = 0.0f;
         if (MODE == kBack) {
-            const float grad = p.grad ? *p.grad : 1.0f;
+            const float grad = p.grad && VOCAB_OK(kVocabGrad, p.grad, 4) ? *p.grad : 1.0f;
             uint32_t kept = 0;
 #pragma unroll 4
-            for (uint32_t k = lane; k < p.kept_parts; k += 32) kept += p.kept[k];
+            for (uint32_t k = lane; k < p.kept_parts; k += 32)
+                if (VOCAB_OK(kVocabWorkspace, p.kept + k, 4)) kept += p.kept[k];
             kept = __reduce_add_sync(0xFFFFFFFFu, kept);
             scale = kept == 0 ? 0.0f : p.avg ? __fdiv_rn(grad, (float)kept) : grad;
-            if (blockIdx.x == 0 && threadIdx.x == 0) *p.scale = scale;   // for the kernel that joins dh's splits
+            // for the kernel that joins dh's splits
+            if (blockIdx.x == 0 && threadIdx.x == 0 && VOCAB_OK(kVocabWorkspace, p.scale, 4)) *p.scale = scale;
         }
         constexpr uint32_t kParts = kFinishWarps / 4;
         const uint32_t width = MODE == kLse || p.bn >= 128 ? p.bn / kParts : p.bn;
@@ -589,8 +584,8 @@ vocab_kernel(const __grid_constant__ VocabParams p)
             int32_t target = p.ignore;
             float lse = 0.0f;
             if (MODE != kBack && row < p.tokens) {
-                target = p.targets[row];
-                if (MODE != kLse) lse = p.lse[row];
+                if (VOCAB_OK(kVocabTargets, p.targets + row, 4)) target = p.targets[row];
+                if (MODE != kLse && VOCAB_OK(kVocabLse, p.lse + row, 4)) lse = p.lse[row];
             }
             const uint32_t lanes = (warp & 3) * 32 << 16;   // of tensor memory
             uint32_t acc = tmem + (u & 1) * 256 + lanes;
@@ -668,7 +663,7 @@ vocab_kernel(const __grid_constant__ VocabParams p)
 #pragma unroll
                         for (uint32_t j = 0; j < 64; ++j)
                             if (j < width) logit = mine == j ? v[j] : logit;
-                        if (here && row < p.tokens) p.logit[row] = logit;
+                        if (here && row < p.tokens && VOCAB_OK(kVocabWorkspace, p.logit + row, 4)) p.logit[row] = logit;
                     }
                     // The four column groups' into one by the first warps; the others go on
                     // (with a barrier of them all a narrow head's tile took 12% longer), up to
@@ -689,7 +684,8 @@ vocab_kernel(const __grid_constant__ VocabParams p)
 #pragma unroll
                             for (uint32_t q = 1; q < kParts; ++q) join(top, sum, red[q][in]);
                             const uint64_t part = (uint64_t)p.unit0 * (kVocabUnit / p.bn) + t.n0 / p.bn;
-                            p.part[part * p.tokens + row] = make_float2(top, sum);
+                            float2 *to = p.part + part * p.tokens + row;
+                            if (VOCAB_OK(kVocabWorkspace, to, 8)) *to = make_float2(top, sum);
                         }
                         __syncwarp();
                         if (lane == 0) mbar_arrive(joined + 8 * j3);
@@ -756,7 +752,7 @@ vocab_kernel(const __grid_constant__ VocabParams p)
                             for (uint32_t j = q; j < q + 32; j += 2) w[j / 2] = pack_bf16x2(v[j], v[j + 1]) & mask;
                         }
                         store_rows_bf16(p, buf, w, p.gbuf + (uint64_t)row0 * p.gpitch + t.n0 + c, p.gpitch, rows, 64, 8,
-                                         p.gbuf, (uint64_t)p.tokens * p.gpitch * 2, 0);
+                                         kVocabG);
                     };
                     if constexpr (kLong) {
                         if (c0 < c1) step(c0, v);
@@ -791,7 +787,7 @@ vocab_kernel(const __grid_constant__ VocabParams p)
                     if (p.acc_in) {
 #pragma unroll
                         for (uint32_t k = 0; k < 8; ++k)
-                            if (first + 4 * k < rows) {
+                            if (first + 4 * k < rows && VOCAB_OK(kVocabWorkspace, at + (uint64_t)k * p.apitch, 16)) {
                                 const float4 o = at[(uint64_t)k * p.apitch];
                                 f[k].x += o.x, f[k].y += o.y, f[k].z += o.z, f[k].w += o.w;
                             }
@@ -799,11 +795,10 @@ vocab_kernel(const __grid_constant__ VocabParams p)
                     if (!p.final) {
 #pragma unroll
                         for (uint32_t k = 0; k < 8; ++k)
-                            if (first + 4 * k < rows) at[(uint64_t)k * p.apitch] = f[k];
+                            if (first + 4 * k < rows && VOCAB_OK(kVocabWorkspace, at + (uint64_t)k * p.apitch, 16))
+                                at[(uint64_t)k * p.apitch] = f[k];
                         continue;
                     }
-                    const uint64_t all = (uint64_t)p.tokens * p.dim * 2;
-                    (void)all;
 #pragma unroll
                     for (uint32_t k = 0; k < 8; ++k) {
                         if (first + 4 * k >= rows) continue;
@@ -811,13 +806,13 @@ vocab_kernel(const __grid_constant__ VocabParams p)
                         const uint2 h = make_uint2(pack_bf16x2(f[k].x * scale, f[k].y * scale),
                                                    pack_bf16x2(f[k].z * scale, f[k].w * scale));
                         if (p.dh_vec) {
-                            if (VOCAB_OK(to, 8, p.dh, all, 1)) *reinterpret_cast<uint2 *>(to) = h;
+                            if (VOCAB_OK(kVocabDh, to, 8)) *reinterpret_cast<uint2 *>(to) = h;
                         } else {
                             const uint16_t x[4] = {(uint16_t)h.x, (uint16_t)(h.x >> 16), (uint16_t)h.y,
                                                    (uint16_t)(h.y >> 16)};
 #pragma unroll
                             for (uint32_t j = 0; j < 4; ++j)
-                                if (e + j < p.dim && VOCAB_OK(to + j, 2, p.dh, all, 1)) to[j] = x[j];
+                                if (e + j < p.dim && VOCAB_OK(kVocabDh, to + j, 2)) to[j] = x[j];
                         }
                     }
                 }
@@ -834,8 +829,7 @@ vocab_kernel(const __grid_constant__ VocabParams p)
                         for (uint32_t j = 0; j < 16; ++j)
                             w[16 * q + j] = pack_bf16x2(v[2 * j] * scale, v[2 * j + 1] * scale);
                     }
-                    store_rows_bf16(p, buf, w, out + c, p.dim, rows, min(p.dim - t.n0 - c, 64u), p.dw_align, p.dw[t.r],
-                                    (uint64_t)p.rows[t.r] * p.dim * 2, 16 + t.r);
+                    store_rows_bf16(p, buf, w, out + c, p.dim, rows, min(p.dim - t.n0 - c, 64u), p.dw_align, kVocabDw + t.r);
                 }
             }
             give_back();
@@ -870,15 +864,17 @@ __global__ void __launch_bounds__(kTokens *kSlices) vocab_finish_kernel(const __
     int32_t target = p.ignore;
     float logit = 0.0f;
     if (t < p.tokens) {
-        target = p.targets[t];
-        logit = p.logit[t];   // nobody's where the target is not in the vocabulary: not used then
+        if (VOCAB_OK(kVocabTargets, p.targets + t, 4)) target = p.targets[t];
+        // nobody's where the target is not in the vocabulary: not used then
+        if (VOCAB_OK(kVocabWorkspace, p.logit + t, 4)) logit = p.logit[t];
     }
     float top = -INFINITY, sum = 0.0f;
     const uint32_t column = blockIdx.x * kTokens + lane;
     if (column < p.tokens) {
 #pragma unroll 4
         for (uint32_t k = warp; k < p.tiles; k += kSlices) {
-            join(top, sum, p.part[(uint64_t)k * p.tokens + column]);
+            const float2 *from = p.part + (uint64_t)k * p.tokens + column;
+            if (VOCAB_OK(kVocabWorkspace, from, 8)) join(top, sum, *from);
         }
     }
     part[warp][lane] = make_float2(top, sum);
@@ -903,8 +899,8 @@ __global__ void __launch_bounds__(kTokens *kSlices) vocab_finish_kernel(const __
                     record_error(p.sink, DT_ERR_INVALID, -1, (int)t, target);
                 }
             }
-            if (p.lse) p.lse[t] = lse;
-            if (p.losses) p.losses[t] = loss;
+            if (p.lse && VOCAB_OK(kVocabLse, p.lse + t, 4)) p.lse[t] = lse;
+            if (p.losses && VOCAB_OK(kVocabLosses, p.losses + t, 4)) p.losses[t] = loss;
         }
         loss_of[warp] = loss;
         keeps[warp] = kept;
@@ -920,8 +916,8 @@ __global__ void __launch_bounds__(kTokens *kSlices) vocab_finish_kernel(const __
         bool end = true;
         if (gridDim.x > 1) {
             if (lane == 0) {
-                p.block_sum[blockIdx.x] = sum32;
-                p.block_kept[blockIdx.x] = (uint32_t)kept;
+                if (VOCAB_OK(kVocabWorkspace, p.block_sum + blockIdx.x, 4)) p.block_sum[blockIdx.x] = sum32;
+                if (VOCAB_OK(kVocabWorkspace, p.block_kept + blockIdx.x, 4)) p.block_kept[blockIdx.x] = (uint32_t)kept;
                 __threadfence();
                 last = atomicAdd(p.ticket, 1u) == gridDim.x - 1;
             }
@@ -933,8 +929,8 @@ __global__ void __launch_bounds__(kTokens *kSlices) vocab_finish_kernel(const __
                 kept = 0;
 #pragma unroll 4
                 for (uint32_t b = lane; b < gridDim.x; b += 32) {
-                    all += __ldcg(p.block_sum + b);
-                    kept += __ldcg(p.block_kept + b);
+                    if (VOCAB_OK(kVocabWorkspace, p.block_sum + b, 4)) all += __ldcg(p.block_sum + b);
+                    if (VOCAB_OK(kVocabWorkspace, p.block_kept + b, 4)) kept += __ldcg(p.block_kept + b);
                 }
                 for (int o = 16; o > 0; o >>= 1) {
                     all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
@@ -943,7 +939,8 @@ __global__ void __launch_bounds__(kTokens *kSlices) vocab_finish_kernel(const __
                 sum32 = (float)all;
             }
         }
-        if (end && lane == 0) *p.loss = kept == 0 ? 0.0f : p.avg ? __fdiv_rn(sum32, (float)kept) : sum32;
+        if (end && lane == 0 && VOCAB_OK(kVocabLoss, p.loss, 4))
+            *p.loss = kept == 0 ? 0.0f : p.avg ? __fdiv_rn(sum32, (float)kept) : sum32;
     }
     DT_TL_END_BLOCK(DT_TL_VOCAB);
 }
@@ -958,13 +955,15 @@ __global__ void __launch_bounds__(kThreads) vocab_join_kernel(const __grid_const
     const uint32_t quads = p.apitch / 4;
     const uint64_t all = (uint64_t)p.tokens * quads, step = (uint64_t)gridDim.x * kThreads;
     for (uint64_t i = (uint64_t)blockIdx.x * kThreads + threadIdx.x; i < all; i += step) {
-        const float scale = *p.scale;
+        const float scale = VOCAB_OK(kVocabWorkspace, p.scale, 4) ? *p.scale : 0.0f;
         const float4 *from = reinterpret_cast<const float4 *>(p.acc) + i;   // rows of quads, one split after the other
         float4 f = make_float4(0, 0, 0, 0);
         for (uint32_t k = 0; k < p.splits; k += 16) {
             float4 o[16];
 #pragma unroll
-            for (uint32_t j = 0; j < 16; ++j) o[j] = k + j < p.splits ? from[(k + j) * all] : make_float4(0, 0, 0, 0);
+            for (uint32_t j = 0; j < 16; ++j)
+                o[j] = k + j < p.splits && VOCAB_OK(kVocabWorkspace, from + (k + j) * all, 16) ? from[(k + j) * all]
+                                                                                             : make_float4(0, 0, 0, 0);
 #pragma unroll
             for (uint32_t j = 0; j < 16; ++j) f.x += o[j].x, f.y += o[j].y, f.z += o[j].z, f.w += o[j].w;
         }
@@ -972,11 +971,11 @@ __global__ void __launch_bounds__(kThreads) vocab_join_kernel(const __grid_const
         const uint32_t row = (uint32_t)(i / quads), e = (uint32_t)(i - (uint64_t)row * quads) * 4;
         uint16_t *to = p.dh + (uint64_t)row * p.dim + e;
         if (p.dh_vec) {
-            if (VOCAB_OK(to, 8, p.dh, (uint64_t)p.tokens * p.dim * 2, 1))
+            if (VOCAB_OK(kVocabDh, to, 8))
                 *reinterpret_cast<uint2 *>(to) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
         } else {
             for (uint32_t j = 0; j < 4 && e + j < p.dim; ++j)
-                if (VOCAB_OK(to + j, 2, p.dh, (uint64_t)p.tokens * p.dim * 2, 1)) to[j] = f32_to_bf16(v[j]);
+                if (VOCAB_OK(kVocabDh, to + j, 2)) to[j] = f32_to_bf16(v[j]);
         }
     }
     DT_TL_END_BLOCK(DT_TL_VOCAB);
@@ -1017,7 +1016,8 @@ __global__ void __launch_bounds__(kThreads) vocab_pack_kernel(const __grid_const
         }
         uint4 *dst = reinterpret_cast<uint4 *>(h ? p.hidden_dst : p.dst) + (uint64_t)row * vecs;
         if (at >= have) {
-            for (uint32_t k = lane; k < vecs; k += 32) dst[k] = make_uint4(0, 0, 0, 0);
+            for (uint32_t k = lane; k < vecs; k += 32)
+                if (VOCAB_OK(kVocabWorkspace, dst + k, 16)) dst[k] = make_uint4(0, 0, 0, 0);
             continue;
         }
         const uint16_t *src = base + (uint64_t)at * p.dim;
@@ -1027,7 +1027,7 @@ __global__ void __launch_bounds__(kThreads) vocab_pack_kernel(const __grid_const
         for (uint32_t k = lane; k < vecs; k += 32) {
             const uint32_t n = min(p.dim - 8 * k, 8u);   // elements of this vector
             uint32_t w[4] = {0, 0, 0, 0};
-            if (VOCAB_OK(src + 8 * k, 2 * n, base, (uint64_t)have * p.dim * 2, 32 + r)) {
+            if (VOCAB_OK(h ? (int)kVocabHidden : kVocabRows + r, src + 8 * k, 2 * n)) {
                 const uint4 a = __ldg(blocks + k), b = off + 2 * n > 16 ? __ldg(blocks + k + 1) : make_uint4(0, 0, 0, 0);
                 const uint32_t v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
@@ -1044,7 +1044,7 @@ __global__ void __launch_bounds__(kThreads) vocab_pack_kernel(const __grid_const
                     else if (2 * q + 1 >= n) w[q] &= 0xFFFFu;
                 }
             }
-            dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
+            if (VOCAB_OK(kVocabWorkspace, dst + k, 16)) dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
         }
     }
     DT_TL_END_BLOCK(DT_TL_VOCAB);

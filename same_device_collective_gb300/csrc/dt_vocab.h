@@ -16,6 +16,13 @@ namespace dt {
 // rank r has units [unit_end[r - 1], unit_end[r]), its last one padded.
 constexpr uint32_t kVocabUnit = 256;
 
+// Buffers, as bounds-checked builds number them; then dweight 16 + r and the
+// ranks' rows that are laid out again 32 + r.
+enum VocabBuffer : int {
+    kVocabG, kVocabDh, kVocabTargets, kVocabLse, kVocabLosses, kVocabLoss, kVocabGrad, kVocabWorkspace, kVocabHidden,
+    kVocabDw = DT_MAX_RANKS, kVocabRows = 2 * DT_MAX_RANKS, kVocabBuffers = 3 * DT_MAX_RANKS
+};
+
 struct VocabParams {
     CUtensorMap h;                     // [tokens, dim]
     CUtensorMap g;                     // [tokens, gpitch]: a piece's p - [target]
@@ -60,6 +67,9 @@ struct VocabParams {
     uint16_t *dh;
     uint16_t *dw[DT_MAX_RANKS];
     ErrorSink sink;
+#ifdef DT_BOUNDS
+    Extent extent[kVocabBuffers];
+#endif
 };
 
 struct VocabFinish {
@@ -73,6 +83,9 @@ struct VocabFinish {
     uint32_t tokens, tiles, vocab;
     int32_t ignore, avg;
     ErrorSink sink;
+#ifdef DT_BOUNDS
+    Extent extent[kVocabBuffers];
+#endif
 };
 
 struct VocabPack {
@@ -86,6 +99,9 @@ struct VocabPack {
     uint32_t tokens, rows;             // hidden rows and vocabulary rows of this launch
     uint32_t dim, pitch;
     ErrorSink sink;
+#ifdef DT_BOUNDS
+    Extent extent[kVocabBuffers];
+#endif
 };
 
 cudaError_t launch_vocab_lse(VocabParams &p, int device, cudaStream_t s);

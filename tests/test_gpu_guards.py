@@ -276,3 +276,76 @@ def test_large_gathers_in_waves_write_only_their_outputs(dt, rows, shared):
     for q, o in enumerate(outs):
         assert o.intact(), f"output {q}"
         assert torch.equal(o.view(torch.uint8), want), f"output {q}"
+
+
+# ---------------------------------------------- layer norm, vocabulary loss
+def values(*shape, seed, dtype=torch.float32, std=1.0):
+    gen = torch.Generator("cuda").manual_seed(seed)
+    return (torch.randn(*shape, generator=gen, device="cuda") * std).to(dtype)
+
+
+@pytest.mark.parametrize("rows,cols,dtype,wdtype", [([3, 0, 5], 7, "bf16", "bf16"), ([400, 1, 30], 1024, "bf16", "f32"),
+                                                    ([40, 33, 0], 1021, "f32", "f32"), ([9, 300, 4], 64, "bf16", "f32"),
+                                                    ([350, 2, 3], 33, "f32", "bf16"), ([5, 3, 1], 9000, "f32", "f32"),
+                                                    ([3, 2, 1], 20001, "bf16", "bf16"), ([700, 80, 9], 4096, "f32", "f32")])
+@pytest.mark.parametrize("shift", [0, 4])
+def test_layer_norm_writes_only_its_outputs(dt, rows, cols, dtype, wdtype, shift):
+    P = len(rows)
+    x, dy = ([values(n, cols, seed=s + n, dtype=TORCH_DTYPE[dtype]) for n in rows] for s in (1, 2000))
+    w, b = (values(cols, seed=s, dtype=TORCH_DTYPE[wdtype]) for s in (5, 6))
+    inputs = [*x, *dy, w, b]
+    snap = snapshot(inputs)
+    y, dx = ([guarded_like(n * cols, dtype, shift) for n in rows] for _ in range(2))
+    mean, rstd = ([guarded_like(n, "f32", shift) for n in rows] for _ in range(2))
+    dw, db = (guarded_like(cols, wdtype, shift) for _ in range(2))
+    with group(P) as g:
+        ws = Guarded(dt.dt_layer_norm_workspace(g, cols))
+        dt.dt_layer_norm(g, x, w, b, [v for _, v in y], [v for _, v in mean], [v for _, v in rstd], rows, 0, cols, 1e-5,
+                         dtype, wdtype)
+        dt.dt_layer_norm_backward(g, x, dy, w, [v for _, v in mean], [v for _, v in rstd], [v for _, v in dx], dw[1],
+                                  db[1], rows, 0, cols, dtype, wdtype, "sum", ws.view(torch.uint8))
+        torch.cuda.synchronize()
+        assert dt.dt_group_check(g) == dt.DT_OK
+    assert unchanged(inputs, snap)
+    for what, outs in (("y", y), ("dx", dx), ("mean", mean), ("rstd", rstd), ("weights", [dw, db])):
+        for r, (guard, v) in enumerate(outs):
+            assert guard.intact(), (what, r)
+            assert torch.isfinite(v).all()
+    assert ws.intact()
+    h = [(x[r].double() - mean[r][1].double()[:, None]) * rstd[r][1].double()[:, None] for r in range(P)]
+    for r in range(P):
+        torch.testing.assert_close(y[r][1].view(rows[r], cols).double(), h[r] * w.double() + b.double(), rtol=2.0 ** -8,
+                                   atol=1e-4)
+    torch.testing.assert_close(dw[1].double(), sum((d.double() * k).sum(0) for d, k in zip(dy, h)), rtol=2.0 ** -8, atol=1e-2)
+
+
+@pytest.mark.parametrize("tokens,vocab,dim", [(1, [5, 0, 300], 8), (77, [1000, 30, 0], 333), (130, [257, 255, 1], 64),
+                                              (300, [700, 0, 900], 1100), (40, [64, 64, 64], 2050), (1000, [3000, 1, 2], 96)])
+@pytest.mark.parametrize("shift", [0, 4])
+def test_vocab_loss_writes_only_its_outputs(dt, tokens, vocab, dim, shift):
+    h = values(tokens, dim, seed=1, dtype=torch.bfloat16)
+    w = [values(v, dim, seed=2 + v, dtype=torch.bfloat16, std=dim ** -0.5) for v in vocab]
+    gen = torch.Generator("cuda").manual_seed(9)
+    t = torch.randint(0, sum(vocab), (tokens,), generator=gen, device="cuda", dtype=torch.int32)
+    t[1::5] = -100
+    inputs = [h, *w, t]
+    snap = snapshot(inputs)
+    losses, lse = (guarded_like(tokens, "f32", shift) for _ in range(2))
+    loss = guarded_like(1, "f32", shift)
+    dh = guarded_like(tokens * dim, "bf16", shift)
+    dw = [guarded_like(v * dim, "bf16", shift) for v in vocab]
+    with group(len(vocab)) as g:
+        ws = [Guarded(dt.dt_vocab_loss_workspace(g, vocab, 0, tokens, dim, "bf16", b)) for b in (False, True)]
+        dt.dt_vocab_loss(g, h, w, vocab, 0, t, tokens, dim, "bf16", "avg", -100, losses[1], lse[1], loss[1],
+                         ws[0].view(torch.uint8))
+        dt.dt_vocab_loss_backward(g, h, w, vocab, 0, t, lse[1], None, tokens, dim, "bf16", "avg", -100, dh[1],
+                                  [v for _, v in dw], ws[1].view(torch.uint8))
+        torch.cuda.synchronize()
+        assert dt.dt_group_check(g) == dt.DT_OK
+    assert unchanged(inputs, snap)
+    for k, (guard, v) in enumerate([losses, lse, loss, dh, *dw]):
+        assert guard.intact(), k
+        assert torch.isfinite(v).all()
+    assert all(x.intact() for x in ws)
+    l = h.double() @ torch.cat(w).double().t()
+    torch.testing.assert_close(lse[1].double(), torch.logsumexp(l, 1), rtol=0, atol=1e-3)
