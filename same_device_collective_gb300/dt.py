@@ -356,13 +356,38 @@ def _m_barrier(g: int, rank: int = DT_ALL_RANKS, stream=None) -> tuple:
     return (g, rank, _stream(stream))
 
 
-def _dense(*xs) -> None:
-    """The layer norm and loss calls describe dense buffers: refuse a tensor that is not one
-    (its address alone would be read as if it were)."""
+_TORCH_NAME = {DT_F32: "torch.float32", DT_BF16: "torch.bfloat16", DT_I32: "torch.int32"}
+
+
+def _dense(code: int | None, *xs) -> None:
+    """The layer norm and loss calls describe dense buffers of given types, of which they get the
+    address alone: refuse a tensor that is not contiguous, not of the type with this code (None: of
+    any), or neither on a GPU nor pinned."""
+    name = _TORCH_NAME.get(code)
     for x in xs:
         for t in x if isinstance(x, (list, tuple)) else (x,):
-            if hasattr(t, "is_contiguous") and not t.is_contiguous():
+            if not hasattr(t, "is_contiguous"):
+                continue
+            if not t.is_contiguous():
                 raise ValueError(f"tensor of shape {tuple(t.shape)} and strides {t.stride()} is not contiguous")
+            if name and str(t.dtype) != name:
+                raise ValueError(f"{t.dtype} tensor of shape {tuple(t.shape)} where the call reads or writes {name}")
+            if not t.is_cuda and t.numel() and not t.is_pinned():
+                raise ValueError(f"tensor of shape {tuple(t.shape)} is not in memory that a GPU reaches")
+
+
+def _ranks(g: int, *lists) -> None:
+    """Lists with an entry for each rank, of which the library reads as many as the group has."""
+    want = dt_group_size(g) if g else 0
+    for x in lists:
+        if x is not None and len(x) != (want if want > 0 else len(lists[0])):
+            raise ValueError(f"{len(x)} entries for {want if want > 0 else len(lists[0])} ranks")
+
+
+def _checked(dtype, *taken) -> int | None:
+    """The code of a type that the call takes, or None: the library refuses the others."""
+    code = _code(DTYPES, dtype)
+    return code if code in (taken or (DT_F32, DT_BF16)) else None
 
 
 def _workspace(ws) -> tuple:
@@ -387,7 +412,10 @@ def _m_layer_norm(g: int, x: Sequence, weight, bias, y: Sequence, mean, rstd, ro
     """Layer norm of every rank's rows: x[r], y[r] are rank r's [rows[r], cols] (or rows_equal
     rows); weight and bias (or None) serve all ranks; mean and rstd, lists of f32 tensors or
     None, receive what dt_layer_norm_backward reads."""
-    _dense(x, weight, bias, y, mean, rstd)
+    _ranks(g, x, y, mean, rstd, rows)
+    _dense(_checked(dtype), x, y)
+    _dense(_checked(weight_dtype), weight, bias)
+    _dense(DT_F32, mean, rstd)
     return (g, _ptr_array(x), _ptr(weight), _ptr(bias), _ptr_array(y), _opt_ptr_array(mean),
             _opt_ptr_array(rstd), _rows_array(rows), rows_equal, cols, eps, _code(DTYPES, dtype),
             _code(DTYPES, weight_dtype), _stream(stream))
@@ -398,7 +426,11 @@ def _m_layer_norm_backward(g: int, x: Sequence, dy: Sequence, weight, mean: Sequ
                            cols: int, dtype, weight_dtype, op, workspace, stream=None) -> tuple:
     """Backward pass: dx per rank, dweight and dbias (or None) reduced over every rank's rows
     (op "sum" or "avg").  workspace: a device tensor of dt_layer_norm_workspace(g, cols) bytes."""
-    _dense(x, dy, weight, mean, rstd, dx, dweight, dbias, workspace)
+    _ranks(g, x, dy, mean, rstd, dx, rows)
+    _dense(_checked(dtype), x, dy, dx)
+    _dense(_checked(weight_dtype), weight, dweight, dbias)
+    _dense(DT_F32, mean, rstd)
+    _dense(None, workspace)
     return (g, _ptr_array(x), _ptr_array(dy), _ptr(weight), _ptr_array(mean), _ptr_array(rstd),
             _ptr_array(dx), _ptr(dweight), _ptr(dbias), _rows_array(rows), rows_equal, cols,
             _code(DTYPES, dtype), _code(DTYPES, weight_dtype), _code(OPS, op), *_workspace(workspace),
@@ -411,7 +443,11 @@ def _m_vocab_loss(g: int, hidden, weight: Sequence, vocab: Sequence | None, voca
     """Softmax cross entropy of hidden [tokens, dim] under the ranks' vocabulary rows weight[r]
     [vocab[r], dim] (or vocab_equal rows each): losses and lse [tokens], loss [1], f32, or None.
     targets: int32 [tokens].  workspace: a device tensor of dt_vocab_loss_workspace bytes."""
-    _dense(hidden, weight, targets, losses, lse, loss, workspace)
+    _ranks(g, weight, vocab)
+    _dense(_checked(dtype, DT_BF16), hidden, weight)
+    _dense(DT_I32, targets)
+    _dense(DT_F32, losses, lse, loss)
+    _dense(None, workspace)
     return (g, _ptr(hidden), _ptr_array(weight), _rows_array(vocab), vocab_equal, _ptr(targets), tokens,
             dim, _code(DTYPES, dtype), _code(OPS, op), ignore_index, _ptr(losses), _ptr(lse), _ptr(loss),
             *_workspace(workspace), _stream(stream))
@@ -422,7 +458,11 @@ def _m_vocab_loss_backward(g: int, hidden, weight: Sequence, vocab: Sequence | N
                            dhidden, dweight: Sequence, workspace, stream=None) -> tuple:
     """The gradient of that loss: dhidden [tokens, dim], reduced over the ranks, and dweight[r]
     [vocab[r], dim].  lse as dt_vocab_loss wrote it; grad_loss: one f32 on the device, or None (1)."""
-    _dense(hidden, weight, targets, lse, grad_loss, dhidden, dweight, workspace)
+    _ranks(g, weight, vocab, dweight)
+    _dense(_checked(dtype, DT_BF16), hidden, weight, dhidden, dweight)
+    _dense(DT_I32, targets)
+    _dense(DT_F32, lse, grad_loss)
+    _dense(None, workspace)
     return (g, _ptr(hidden), _ptr_array(weight), _rows_array(vocab), vocab_equal, _ptr(targets), _ptr(lse),
             _ptr(grad_loss), tokens, dim, _code(DTYPES, dtype), _code(OPS, op), ignore_index,
             _ptr(dhidden), _ptr_array(dweight), *_workspace(workspace), _stream(stream))
@@ -463,6 +503,8 @@ dt_vocab_loss_backward = _entry("dt_vocab_loss_backward", _m_vocab_loss_backward
 def dt_vocab_loss_workspace(g: int, vocab: Sequence | None, vocab_equal: int, tokens: int, dim: int,
                             dtype, backward: bool) -> int:
     """Workspace bytes of dt_vocab_loss, or of dt_vocab_loss_backward (0: invalid argument)."""
+    if vocab is not None:
+        _ranks(g, vocab)
     return int(_lib.dt_vocab_loss_workspace(g, _rows_array(vocab), vocab_equal, tokens, dim,
                                             _code(DTYPES, dtype), int(bool(backward))))
 
