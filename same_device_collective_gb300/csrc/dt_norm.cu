@@ -1243,7 +1243,9 @@ NormShape norm_shape(NormParams &p, const NormPick &k, int dtype, bool vec, bool
     if (k.threads > 32) groups = std::min<uint64_t>(groups, 15);   // named barriers
     // rows of a stage: those summed at once, and more where they are short,
     // but not so many that groups go without
-    uint64_t per = std::max<uint64_t>(kStageTarget / row_bytes, k.rows);
+    // (at most 256 backward, whose means and reciprocals take 8 bytes a row: all
+    // groups' stages fit kSmemBytes then, or pass it by the stages' rounding)
+    uint64_t per = std::max<uint64_t>(kStageTarget / std::max<uint64_t>(row_bytes, back ? 16 : 1), k.rows);
     per = std::max<uint64_t>(1, std::min(per, p.rows / (groups * sms)));
     p.chunk_rows = (uint32_t)per;
     p.chunks = 0;

@@ -403,3 +403,17 @@ def test_a_rank_with_all_rows_costs_no_more_than_one_rank(dt):
 
     one, many = best(1), best(16)
     assert many <= 2 * one, (one, many)
+
+
+# Rows of a few bytes: a stage of them has as many means and reciprocals, which
+# take more room than the rows, and all groups' stages have to fit an SM.
+@pytest.mark.parametrize("rows,cols,dtype", [([5_100_000, 7], 1, "bf16"), ([1_300_000, 1_400_000], 2, "bf16"),
+                                             ([2_600_000], 1, "f32"), ([0, 1_800_000], 3, "bf16")])
+def test_millions_of_very_short_rows(dt, rows, cols, dtype):
+    x, dy, w, b = make(rows, cols, dtype, "f32", seed=cols)
+    with group(len(rows)) as g:
+        y, mean, rstd = forward(dt, g, x, w, b, rows, cols, dtype, "f32")
+        check_forward(x, w, b, y, mean, rstd, dtype)
+        dx, dw, db = backward(dt, g, x, dy, w, mean, rstd, rows, cols, dtype, "f32")
+        check_backward(x, dy, w, mean, rstd, dx, dw, db, dtype, "f32")
+        assert dt.dt_group_check(g) == dt.DT_OK
