@@ -329,7 +329,9 @@ dt_status dt_bucket_allreduce_static(int world_size, void *const *grads, const s
  *   eps            finite, >= 0
  * With mu the mean of a row and v the mean of (x - mu)^2, both fp32 and v from
  * the differences: rstd = 1 / sqrt(v + eps), y = (x - mu) * rstd * weight +
- * bias, rounded once.  A NaN or an infinity in a row makes that row NaN.
+ * bias, rounded once.  A NaN or an infinity in a row makes that row NaN.  The
+ * order of a row's sums depends on its width, type and alignment and on whether
+ * the call has more than two rows an SM: the same call gives the same bits.
  * Every pointer must be a multiple of its element size; rows that all start on
  * 16-byte boundaries move as vectors, others element by element.  cols is
  * 1..2^24.  A buffer may otherwise overlap no output. */
@@ -377,10 +379,11 @@ size_t dt_layer_norm_workspace(dt_group_t g, size_t cols);
  *   targets      [tokens] int32 vocabulary indices on the device, or
  *                ignore_index: that token's loss and dhidden are 0, it is not
  *                counted, and its hidden row enters dweight as a product with
- *                0 (so a NaN or an infinity there makes dweight NaN).  Any other value outside the vocabulary is
- *                treated the same way and recorded as DT_ERR_INVALID in the
- *                group's error word (dt_group_error_detail: rank -1, peer =
- *                the token, generation = the value).
+ *                0 (so a NaN or an infinity there makes dweight NaN).  Any
+ *                other value outside the vocabulary is treated the same way
+ *                and recorded as DT_ERR_INVALID in the group's error word
+ *                (dt_group_error_detail: rank -1, peer = the token,
+ *                generation = the value).
  *   dtype        of hidden and weight: DT_BF16 (products in the tensor cores,
  *                fp32 sums); DT_F32 is DT_ERR_UNSUPPORTED
  *   op           DT_SUM, or DT_AVG: the mean over the counted tokens (0 where
@@ -495,8 +498,8 @@ dt_status dt_debug_barrier_expect(dt_group_t g, int extra, uint32_t timeout_ms, 
 #define DT_TL_BUCKET_BARRIER 8  /* bucket all-reduce, the barrier block after a bucket */
 #define DT_TL_BARRIER 9         /* signal-window barrier kernel */
 #define DT_TL_MARK 10           /* dt_timeline_mark: block = the caller's tag */
-#define DT_TL_VOCAB 12          /* vocabulary loss, either pass */
 #define DT_TL_NORM 11           /* layer norm, either pass, and the join of its weight gradients */
+#define DT_TL_VOCAB 12          /* vocabulary loss, either pass */
 typedef struct {
     uint64_t grid;       /* the launch's %gridid */
     uint32_t kind;       /* DT_TL_* */

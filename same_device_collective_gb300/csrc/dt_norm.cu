@@ -14,7 +14,7 @@
 //
 // norm_rows_kernel  forward, rows of whole vectors: a row in the registers of
 //                   4, 8 or 16 lanes or of whole warps, blocks handed out by
-//                   the hardware (4 x 2048 rows of 4096 bf16: 27.7 us, 4.8
+//                   the hardware (4 x 2048 rows of 4096 bf16: 27.8 us, 4.8
 //                   TB/s; PyTorch's copy of the same bytes 23.2)
 // norm_kernel       forward, rows at other offsets or too long for that, and
 // norm_backward_kernel: resident blocks whose groups of threads each have a
@@ -22,13 +22,13 @@
 //                   up to 160 KB an SM are always under way.  A stage is a few
 //                   rows; rows of any alignment are copied with the 16-byte
 //                   blocks that their ends lie in, and then read element by
-//                   element (3 x 5000 rows of 1021 f32: 24.1 us, 5.1 TB/s; with
+//                   element (3 x 5000 rows of 1021 f32: 24.4 us, 5.0 TB/s; with
 //                   loads to registers 36).  A thread keeps its columns, 8 to
 //                   32 of them, over all of its rows, and with them their
 //                   weights and, backward, their shares of dw and db; up to four
 //                   rows are summed at a time, and the rows of a warp's teams of
 //                   lanes where rows are short.  Backward 4 x 2048 x 4096 bf16
-//                   43 us, 4.7 TB/s; 8 x 8192 x 4096 275 us, 5.9 TB/s: the
+//                   43 us, 4.7 TB/s; 8 x 8192 x 4096 272 us, 5.9 TB/s: the
 //                   smaller call's blocks spend 5 us on their way to the first
 //                   row and 3 between the first SM's end and the last's.
 // norm_join_kernel  adds the blocks' shares of dw and db in a fixed order, so
@@ -479,7 +479,8 @@ __host__ __device__ constexpr int rows_at_once()
 }
 
 // sum + low is the sum of what was added, to about twice fp32's digits: `low`
-// collects what each addition rounds off.
+// collects what each addition rounds off, as Knuth's two-sum gives it exactly
+// (The Art of Computer Programming, volume 2, section 4.2.2).
 template <typename V>
 __device__ __forceinline__ void exact_add(V &sum, V &low, V x, V minus_one)
 {
@@ -544,8 +545,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(const __grid_cons
     DT_TL_WAITED();
     const float inv = p.inv_cols;
     uint32_t phase = 0;
-    // the first stage's copies before the weights' loads, and the others, behind
-    // whose 25 MB the weights would take 6 us, after them
+    // the weights' loads before the stages' copies (Ring::load_first)
     V w[N][K], b[N][K];
     auto weights = [&](int n) {
         const uint32_t e = (n * tpr + t) * VEC;
@@ -739,9 +739,11 @@ norm_rows_kernel(const __grid_constant__ NormParams p)
         }
         float sum = both(add(add(s[0], s[1]), add(s[2], s[3]))), low = 0.0f;
         if constexpr (EARLY) {
-            // A mean near zero keeps few of its sum's digits: of a few rows a
-            // caller sees each, and a sum of twice the digits costs nothing here
-            // (4 x 1 x 4096 bf16: 4.0 us either way).
+            // A mean near zero keeps few of its sum's digits, and a sum of twice the
+            // digits costs nothing here (4 x 1 x 4096 bf16: 4.0 us either way), while
+            // kernels of many rows are nearly bound by issue.  So a row's statistics may
+            // differ in their last bits between a call of few rows and one of many, as
+            // they do by the threads that share the row.
             V hi = C::all(0.0f), lo = C::all(0.0f);
 #pragma unroll
             for (int n = 0; n < N; ++n) {
@@ -835,8 +837,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_kernel(const __
     DT_TL_WAITED();
     const float inv = p.inv_cols;
     uint32_t phase = 0;
-    // the first stage's copies before the weights' loads, and the others, behind
-    // whose 25 MB the weights would take 6 us, after them
+    // the weights' loads before the stages' copies (Ring::load_first)
     V dw[N][K], db[N][K], w[N][K];
     auto weights = [&](int n) {
         const uint32_t e = (n * tpr + t) * VEC;
@@ -1134,7 +1135,8 @@ using NormFn = void (*)(NormParams);
 // SM and one computes while another waits at its barrier (4 x 2048 x 4096
 // backward: over 512 threads 47.0 us, over 256 46.6).  Past 256 threads of 32
 // columns a row may have 512; beyond that, a thread's sums for its columns
-// would not fit in registers.  100 MB of rows of 64, 128, 384 bf16 backward: 8
+// would not fit in registers (32 columns of f32 spill 540 bytes as it is, of
+// bf16 94).  100 MB of rows of 64, 128, 384 bf16 backward: 8
 // columns and a warp to a row 161, 93, 100 us; this 61, 61, 75.
 struct NormPick {
     NormFn fn = nullptr;
@@ -1190,7 +1192,8 @@ NormPick pick_norm(int dtype, bool vec, uint32_t cols)
 // as many threads as a row has vectors.  Else, for rows of whole vectors, 4
 // vectors a thread in as few lanes of a warp as that takes, or 4 to 6 vectors
 // and whole warps, whichever leaves the fewest threads idle (100 MB of rows of
-// 2056 bf16: 4 and 5 vectors 58, 49 us; of 640 f32 40, 32).
+// 2056 bf16: 4 and 5 vectors 58, 49 us; of 640 f32 40, 32; 5 and 6 vectors of
+// bf16 spill 28 and 56 bytes of their 64 registers and are faster all the same).
 template <typename T, int VEC>
 NormPick pick_rows(uint32_t cols, bool few)
 {
