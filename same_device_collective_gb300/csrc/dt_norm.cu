@@ -1269,7 +1269,8 @@ NormShape norm_shape(NormParams &p, const NormPick &k, int dtype, bool vec, bool
 
 cudaError_t launch_rows(NormFn fn, const NormShape &n, const NormParams &p, cudaStream_t s)
 {
-    if (n.smem > 48 * 1024) {   // what a kernel may have without asking
+    // A kernel may have 48 KB without asking, its static part (up to 1 KB of these) included.
+    if (n.smem > 46 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(fn),
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024);
         if (e != cudaSuccess) return e;

@@ -417,3 +417,37 @@ def test_millions_of_very_short_rows(dt, rows, cols, dtype):
         dx, dw, db = backward(dt, g, x, dy, w, mean, rstd, rows, cols, dtype, "f32")
         check_backward(x, dy, w, mean, rstd, dx, dw, db, dtype, "f32")
         assert dt.dt_group_check(g) == dt.DT_OK
+
+
+# A kernel may have 48 KB of shared memory without asking, its static part
+# included: calls whose rings come near that, each the first of its kernel in a
+# process (once a larger call has asked, they all may).
+NEAR_48_KB = r"""
+import sys
+sys.path[:0] = [ROOT, TESTS]
+import torch
+import test_gpu_layer_norm as T
+from same_device_collective_gb300 import dt
+from gpu_util import group
+for rows, cols, dtype, offset in (([1], 6144, "bf16", 0), ([6, 7], 6112, "f32", 0), ([13], 6144, "bf16", 1), ([0, 13], 6104, "f32", 3),
+                                  ([13], 12256, "f32", 0), ([300], 12224, "bf16", 0), ([5000], 592, "bf16", 1),
+                                  ([2000], 592, "f32", 1), ([1000], 864, "bf16", 0), ([500], 1480, "f32", 0),
+                                  ([1000], 1465, "bf16", 1), ([500], 1465, "f32", 1), ([500], 6102, "bf16", 3)):
+    x, dy, w, b = T.make(rows, cols, dtype, "f32", seed=cols, offset=offset)
+    with group(len(rows)) as g:
+        y, mean, rstd = T.forward(dt, g, x, w, b, rows, cols, dtype, "f32", offset=offset)
+        T.check_forward(x, w, b, y, mean, rstd, dtype)
+        dx, dw, db = T.backward(dt, g, x, dy, w, mean, rstd, rows, cols, dtype, "f32", offset=offset)
+        T.check_backward(x, dy, w, mean, rstd, dx, dw, db, dtype, "f32")
+print("all right")
+"""
+
+
+def test_first_calls_that_need_nearly_48_kb(dt):
+    import os
+    import subprocess
+    import sys
+    tests = os.path.dirname(os.path.abspath(__file__))
+    code = NEAR_48_KB.replace("ROOT", repr(os.path.dirname(tests))).replace("TESTS", repr(tests))
+    out = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert out.returncode == 0 and "all right" in out.stdout, out.stderr[-3000:]
