@@ -154,7 +154,7 @@ print("RESULT " + json.dumps(res))
 """
 
 
-def test_checker_covers_every_output_of_the_norm_and_the_loss(dt):
+def test_trimmed_extents_of_every_output_of_the_norm_and_the_loss(dt):
     env = dict(os.environ, DT_BOUNDS_TRIM="16")
     code = OPERATORS.replace("ROOT", repr(ROOT)).replace("TESTS", repr(TESTS))
     out = subprocess.run([sys.executable, "-c", code], env=env, capture_output=True, text=True, timeout=300)
