@@ -84,5 +84,52 @@ inline uint64_t timeout_ns(const dt_group *g) { return (uint64_t)g->timeout_ms *
 
 inline ErrorSink error_sink(dt_group *g) { return ErrorSink{g->d_err, g->h_err_dev, timeout_ns(g)}; }
 
+inline bool float_dtype(int dtype) { return dtype == DT_F32 || dtype == DT_BF16; }
+
+inline bool multiple(const void *p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+
+inline uint64_t up(uint64_t n, uint64_t to) { return (n + to - 1) / to * to; }
+
+// The buffers of a call.  Outputs may overlap nothing, but for an output and
+// an input that carry the same tag (>= 0) and are the same buffer.
+struct Buffers {
+    Range in[6 * DT_MAX_RANKS + 4], out[3 * DT_MAX_RANKS + 4];
+    int nin = 0, nout = 0;
+
+    void read(const void *p, size_t bytes, int tag = -1)
+    {
+        if (p && bytes) in[nin++] = Range{(uintptr_t)p, (uintptr_t)p + bytes, tag, 0};
+    }
+    void write(const void *p, size_t bytes, int tag = -1)
+    {
+        if (p && bytes) out[nout++] = Range{(uintptr_t)p, (uintptr_t)p + bytes, tag, 1};
+    }
+    bool clash() const
+    {
+        for (int o = 0; o < nout; ++o) {
+            for (int k = o + 1; k < nout; ++k)
+                if (overlaps(out[o], out[k])) return true;
+            for (int i = 0; i < nin; ++i)
+                if (overlaps(out[o], in[i]) && !(out[o].rank >= 0 && out[o].rank == in[i].rank && out[o].lo == in[i].lo))
+                    return true;
+        }
+        return false;
+    }
+};
+
+// Every rank's row count; false where the counts or the bytes of all rows pass
+// what a size_t or a pointer can hold.
+inline bool row_counts(int P, const size_t *rows, size_t rows_equal, size_t row_bytes, size_t *n, size_t *total)
+{
+    *total = 0;
+    for (int r = 0; r < P; ++r) {
+        n[r] = rows ? rows[r] : rows_equal;
+        if (n[r] > SIZE_MAX / 64 / row_bytes) return false;
+        *total += n[r];
+        if (*total > SIZE_MAX / 64 / row_bytes) return false;
+    }
+    return true;
+}
+
 }  // namespace host
 }  // namespace dt

@@ -17,51 +17,6 @@ using namespace dt::host;
 
 constexpr size_t kMaxCols = (size_t)1 << 24;
 
-bool float_dtype(int dtype) { return dtype == DT_F32 || dtype == DT_BF16; }
-
-bool multiple(const void *p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
-
-// The buffers of a call.  Outputs may overlap nothing, but for an output and
-// an input that carry the same tag (>= 0) and are the same buffer.
-struct Buffers {
-    Range in[5 * DT_MAX_RANKS], out[3 * DT_MAX_RANKS + 4];
-    int nin = 0, nout = 0;
-
-    void read(const void *p, size_t bytes, int tag = -1)
-    {
-        if (p && bytes) in[nin++] = Range{(uintptr_t)p, (uintptr_t)p + bytes, tag, 0};
-    }
-    void write(const void *p, size_t bytes, int tag = -1)
-    {
-        if (p && bytes) out[nout++] = Range{(uintptr_t)p, (uintptr_t)p + bytes, tag, 1};
-    }
-    bool clash() const
-    {
-        for (int o = 0; o < nout; ++o) {
-            for (int k = o + 1; k < nout; ++k)
-                if (overlaps(out[o], out[k])) return true;
-            for (int i = 0; i < nin; ++i)
-                if (overlaps(out[o], in[i]) && !(out[o].rank >= 0 && out[o].rank == in[i].rank && out[o].lo == in[i].lo))
-                    return true;
-        }
-        return false;
-    }
-};
-
-// Every rank's row count; false where the counts or the bytes of all rows pass
-// what a size_t or a pointer can hold.
-bool row_counts(int P, const size_t *rows, size_t rows_equal, size_t row_bytes, size_t *n, size_t *total)
-{
-    *total = 0;
-    for (int r = 0; r < P; ++r) {
-        n[r] = rows ? rows[r] : rows_equal;
-        if (n[r] > SIZE_MAX / 64 / row_bytes) return false;
-        *total += n[r];
-        if (*total > SIZE_MAX / 64 / row_bytes) return false;
-    }
-    return true;
-}
-
 // What both passes of the layer norm check and set: x, the rows and the types.
 dt_status norm_common(dt_group *g, const void *const *x, void *const *out, const size_t *rows, size_t rows_equal,
                       size_t cols, int dtype, int weight_dtype, const void *weight, dt::NormParams &p, size_t *n,
@@ -106,8 +61,6 @@ constexpr uint64_t kPieceBytes = (uint64_t)512 << 20, kPackBytes = (uint64_t)128
 // Vocabulary tiles next to one another in the order of tiles: with 16, the
 // 76 pairs of CTAs work on about 5 x 16 tiles of 256 x 256.
 constexpr uint32_t kGroup = 16;
-
-uint64_t up(uint64_t n, uint64_t to) { return (n + to - 1) / to * to; }
 
 // How a call is cut up, and where its parts of the workspace lie.  Sizes that
 // the workspace query knows decide everything but `packed`.
@@ -278,15 +231,15 @@ cudaError_t vocab_maps(dt_group *g, const void *hidden, const void *const *weigh
     unsigned char *ws = static_cast<unsigned char *>(workspace);
     if (v.packed) {
         p.w_maps = 1;
-        const cudaError_t e = dt::vocab_map(&p.h, ws + v.pack_h, p.dim, p.tokens, v.pitch, rows_h);
+        const cudaError_t e = dt::matrix_map(&p.h, ws + v.pack_h, p.dim, p.tokens, v.pitch, rows_h);
         if (e != cudaSuccess) return e;
-        return dt::vocab_map(&p.w[0], ws + v.pack_w, p.dim, (uint64_t)v.piece * dt::kVocabUnit, v.pitch, rows_w);
+        return dt::matrix_map(&p.w[0], ws + v.pack_w, p.dim, (uint64_t)v.piece * dt::kVocabUnit, v.pitch, rows_w);
     }
-    cudaError_t e = dt::vocab_map(&p.h, hidden, p.dim, p.tokens, p.dim, rows_h);
+    cudaError_t e = dt::matrix_map(&p.h, hidden, p.dim, p.tokens, p.dim, rows_h);
     for (int r = 0; r < g->P && e == cudaSuccess; ++r) {
         if (p.rows[r] == 0) continue;
         p.w_maps |= 1u << r;
-        e = dt::vocab_map(&p.w[r], weight[r], p.dim, p.rows[r], p.dim, rows_w);
+        e = dt::matrix_map(&p.w[r], weight[r], p.dim, p.rows[r], p.dim, rows_w);
     }
     return e;
 }
@@ -580,7 +533,7 @@ dt_status dt_vocab_loss_backward(dt_group_t g, const void *hidden, const void *c
     vocab_prepare_pack(g, hidden, weight, workspace, v, p, pack);
     // few tokens: boxes of as many as there are, in whole K steps of 16
     p.rows_g = v.pairs ? 128 : (uint32_t)up(p.tokens, 16);
-    e = dt::vocab_map(&p.g, p.gbuf, p.gpitch, p.tokens, p.gpitch, p.rows_g);
+    e = dt::matrix_map(&p.g, p.gbuf, p.gpitch, p.tokens, p.gpitch, p.rows_g);
     for (uint32_t k = 0; k < v.pieces && e == cudaSuccess; ++k) {
         uint32_t units = 0;
         e = vocab_logit_maps(g, hidden, weight, workspace, v, p);

@@ -2,6 +2,7 @@
 // kernels.  Not part of the C ABI.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cstddef>
@@ -58,6 +59,10 @@ size_t norm_workspace(uint32_t cols, int device);
 // vec: every row of every buffer starts on a 16-byte boundary
 cudaError_t launch_norm(NormParams p, int dtype, bool vec, int device, cudaStream_t s);
 cudaError_t launch_norm_backward(NormParams p, int dtype, bool vec, int device, cudaStream_t s);
+
+// The tensor map of a row-major bf16 matrix, read in boxes of 64 columns.
+cudaError_t matrix_map(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows, uint64_t pitch,
+                       uint32_t box_rows);
 
 #ifdef DT_TIMELINE
 void bind_timeline_norm(const void *sink);

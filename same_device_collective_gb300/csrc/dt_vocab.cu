@@ -56,6 +56,7 @@
 #include "dt_device.cuh"
 #include "dt_math.cuh"
 #include "dt_tc.cuh"
+#include "dt_tile.cuh"
 #include "dt_timeline.cuh"
 #include "dt_vocab.h"
 
@@ -103,15 +104,6 @@ struct Tile {
     int r;               // rank and row there of the vocabulary rows that the tile covers (logits: n; dw: m)
     uint32_t vrow;
 };
-
-// n / d, where `inverse` is the least whole number above 2^32 / d (0 for 1): the
-// product's high word is at most one too large.
-__device__ __forceinline__ uint32_t quotient(uint32_t n, uint32_t d, uint32_t inverse)
-{
-    if (d == 1) return n;
-    const uint32_t q = __umulhi(n, inverse);
-    return q * d > n ? q - 1 : q;
-}
 
 // The rank of a unit of 256 vocabulary rows, and the unit's first row there.
 __device__ __forceinline__ int unit_rank(const VocabParams &p, uint32_t unit, uint32_t &row)
@@ -259,21 +251,7 @@ __device__ __forceinline__ void load_stage(const VocabParams &p, const Tile &t, 
     if (l.nb == 2) tma_box<CG>(b + kBoxBytes, l.b, l.bn + 64, row, bar);
 }
 
-// A finishing warp's 32 rows x 128 bytes in shared memory, 16-byte chunk c of
-// row r at chunk c ^ (r mod 8): a thread writes its row, and eight threads
-// read a row, without bank conflicts.
-__device__ __forceinline__ uint4 *out_chunk(unsigned char *buf, uint32_t row, uint32_t c)
-{
-    return reinterpret_cast<uint4 *>(buf + row * 128 + ((c ^ (row & 7)) << 4));
-}
-
 #define VOCAB_OK(buffer, a, n) DT_IN_EXTENT(p, kBoundsVocab, (buffer), (a), (n))
-
-// One instruction's worth of a row: N 16-bit elements.
-template <int N> struct Words;
-template <> struct Words<8> { using type = uint4; };
-template <> struct Words<4> { using type = uint2; };
-template <> struct Words<2> { using type = uint32_t; };
 
 // A warp's rows from `buf` to memory, N elements of a row to a lane and as
 // many rows at a time as that leaves lanes for.
@@ -368,32 +346,6 @@ __device__ __forceinline__ void join(float &top, float &sum, float2 v)
     sum = scaled(top, sum, most) + scaled(v.x, v.y, most);
     top = most;
 }
-
-// The state of the pipeline's waits: a wait that runs out is recorded once,
-// and every role then leaves its loop.
-struct Waits {
-    const ErrorSink &sink;
-    volatile uint32_t *gave_up;
-    // The timer is read only after 64 tries, each of which waits a while in the
-    // hardware: reading it on every wait cost a fifth of the time (2048 tokens of 32768 x 4096: 501 -> 397 us).
-    __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const
-    {
-        for (int k = 0; k < 64; ++k)
-            if (mbar_try_wait(bar, parity)) return true;
-        return slow(bar, parity);
-    }
-    __device__ __noinline__ bool slow(uint32_t bar, uint32_t parity) const
-    {
-        const uint64_t t0 = global_ns();
-        do {
-            for (int k = 0; k < 64; ++k)
-                if (mbar_try_wait(bar, parity)) return true;
-        } while (global_ns() - t0 <= sink.timeout_ns);
-        *gave_up = 1;
-        record_error(sink, DT_ERR_TIMEOUT, -1, blockIdx.x, 0);
-        return false;
-    }
-};
 
 template <int MODE, int CG>
 __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(tc_threads(MODE), 1)
@@ -1140,7 +1092,7 @@ cudaError_t launch_vocab_pack(const VocabPack &p, int device, cudaStream_t s)
                          dim3(kThreads), 0, s, false, p);
 }
 
-cudaError_t vocab_map(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows, uint64_t pitch, uint32_t box_rows)
+cudaError_t matrix_map(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows, uint64_t pitch, uint32_t box_rows)
 {
     static std::atomic<void *> entry{nullptr};
     void *fn = entry.load(std::memory_order_acquire);

@@ -115,8 +115,5 @@ uint32_t vocab_finish_blocks(uint32_t tokens);
 cudaError_t launch_vocab_pack(const VocabPack &p, int device, cudaStream_t s);
 // Blocks of an inner dimension of `inner`.
 uint32_t vocab_blocks(uint64_t inner);
-// The tensor map of a row-major bf16 matrix, read in boxes of 64 columns.
-cudaError_t vocab_map(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows, uint64_t pitch,
-                      uint32_t box_rows);
 
 }  // namespace dt
