@@ -428,6 +428,94 @@ dt_status dt_vocab_loss_backward(dt_group_t g, const void *hidden, const void *c
 size_t dt_vocab_loss_workspace(dt_group_t g, const size_t *vocab, size_t vocab_equal,
                                size_t tokens, size_t dim, int dtype, int backward);
 
+/* ------------------------------- linear layers over the ranks, group-wide */
+
+/* The two linear layers of a block whose tokens are S(0) over the ranks (rank r
+ * holds rows[r] of them, `dim` columns each) and whose inner features are S(0)
+ * over the ranks as well (rank r holds features[r]).  The first gathers: every
+ * rank's tokens meet every rank's features.  The second reduces: the ranks'
+ * features are summed over and each rank keeps its own tokens.  The gather and the
+ * reduce-scatter are part of the products: neither the gathered tokens nor the
+ * ranks' partial sums are stored, and the sum over the ranks is rounded once.
+ *
+ * Both.  rows NULL: rows_equal tokens on each rank; features NULL: features_equal.
+ * n is the sum of rows (n of them number the tokens in rank order); a rank may have
+ * no tokens or no features, all ranks together need a feature.  dtype is that of
+ * every tensor: DT_BF16, products in the tensor cores and fp32 sums; DT_F32 is
+ * DT_ERR_UNSUPPORTED.  Tensors are dense and 2-byte aligned.  Those whose rows start
+ * on 16-byte boundaries are read in place, others are laid out again in the workspace
+ * first, as are tokens whose ranks' pieces would leave more than a twentieth of the
+ * tiles of 256 rows (128 up to 128 tokens) to their ends.
+ * workspace: the query's bytes of device memory, 256-byte aligned, free for other use
+ * once `stream` has passed the call.  No output may overlap another buffer, but for
+ * the residual below.  n is at most 2^26, dim and the sum of features 2^22.  The
+ * tensor cores add 16 products at a time and round towards zero: sums of n terms of
+ * one sign are up to n * 2e-9 of themselves too small.  Repeated calls give the same
+ * bits. */
+#define DT_ACT_NONE 0
+#define DT_ACT_RELU 1
+#define DT_ACT_GELU 2 /* v * Phi(v), Phi the normal distribution (no tanh form) */
+#define DT_ACT_SILU 3 /* v / (1 + exp(-v)) */
+
+/* y[r] = act(X weight[r]^T + bias[r]), X [n, dim] the tokens of all ranks:
+ *   x[r]        rank r's tokens, [rows[r], dim]
+ *   weight[r]   [features[r], dim]
+ *   bias        NULL, or bias[r] [features[r]]
+ *   pre         NULL, or pre[r] [n, features[r]]: receives what act is taken of (itself
+ *               rounded to dtype; act is taken of the fp32 sum), for the backward call
+ *   y[r]        [n, features[r]] */
+dt_status dt_gather_linear(dt_group_t g, const void *const *x, const void *const *weight,
+                           const void *const *bias, void *const *pre, void *const *y,
+                           const size_t *rows, size_t rows_equal, size_t dim, const size_t *features,
+                           size_t features_equal, int dtype, int act, void *workspace,
+                           size_t workspace_bytes, void *stream);
+
+/* Its gradient.  With G_r = dy[r] act'(pre[r]) (dy[r] itself for DT_ACT_NONE, where pre
+ * may be NULL), rounded to dtype as the products' operand:
+ *   dx[r]       rank r's rows of sum_q G_q weight[q], reduced over the ranks
+ *   dweight[r]  G_r^T X
+ *   dbias       NULL, or dbias[r]: the sum of G_r over the tokens, before its rounding
+ * With no tokens at all dweight and dbias are 0. */
+dt_status dt_gather_linear_backward(dt_group_t g, const void *const *x, const void *const *weight,
+                                    const void *const *pre, const void *const *dy, void *const *dx,
+                                    void *const *dweight, void *const *dbias, const size_t *rows,
+                                    size_t rows_equal, size_t dim, const size_t *features,
+                                    size_t features_equal, int dtype, int act, void *workspace,
+                                    size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of either call; 0 for an invalid argument. */
+size_t dt_gather_linear_workspace(dt_group_t g, const size_t *rows, size_t rows_equal, size_t dim,
+                                  const size_t *features, size_t features_equal, int dtype,
+                                  int backward);
+
+/* y[r] = rank r's rows of (sum_q x[q] weight[q]^T + bias) + residual[r]:
+ *   x[q]        rank q's features of all tokens, [n, features[q]]
+ *   weight[q]   [dim, features[q]]
+ *   bias        NULL, or [dim], added once
+ *   residual    NULL, or residual[r] [rows[r], dim]
+ *   y[r]        [rows[r], dim]; may be residual[r] itself (in place) */
+dt_status dt_linear_reduce(dt_group_t g, const void *const *x, const void *const *weight,
+                           const void *bias, const void *const *residual, void *const *y,
+                           const size_t *rows, size_t rows_equal, size_t dim, const size_t *features,
+                           size_t features_equal, int dtype, void *workspace, size_t workspace_bytes,
+                           void *stream);
+
+/* Its gradient.  With Y [n, dim] the dy of all ranks:
+ *   dx[q]       Y weight[q], [n, features[q]]
+ *   dweight[q]  Y^T x[q]
+ *   dbias       NULL, or the sum of Y over the tokens, [dim]
+ * (the residual's gradient is dy).  With no tokens dweight and dbias are 0. */
+dt_status dt_linear_reduce_backward(dt_group_t g, const void *const *x, const void *const *weight,
+                                    const void *const *dy, void *const *dx, void *const *dweight,
+                                    void *dbias, const size_t *rows, size_t rows_equal, size_t dim,
+                                    const size_t *features, size_t features_equal, int dtype,
+                                    void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of either call; 0 for an invalid argument. */
+size_t dt_linear_reduce_workspace(dt_group_t g, const size_t *rows, size_t rows_equal, size_t dim,
+                                  const size_t *features, size_t features_equal, int dtype,
+                                  int backward);
+
 /* ----------------------------------------------------------- async work */
 
 /* Asynchronous collectives, after the async mode of "通信与互联（05）" §四.3
@@ -500,6 +588,7 @@ dt_status dt_debug_barrier_expect(dt_group_t g, int extra, uint32_t timeout_ms, 
 #define DT_TL_MARK 10           /* dt_timeline_mark: block = the caller's tag */
 #define DT_TL_NORM 11           /* layer norm, either pass, and the join of its weight gradients */
 #define DT_TL_VOCAB 12          /* vocabulary loss, either pass */
+#define DT_TL_LINEAR 13         /* linear layers over the ranks, either pass */
 typedef struct {
     uint64_t grid;       /* the launch's %gridid */
     uint32_t kind;       /* DT_TL_* */
@@ -558,6 +647,10 @@ dt_status dt_timeline_mark(void *stream, uint32_t tag);
  * loss 5, grad_loss 6, workspace 7, hidden rows laid out again 8, dweight 16 + r,
  * rank r's rows laid out again 32 + r.  (TMA's own loads stay in their tensor maps.) */
 #define DT_BOUNDS_VOCAB 10
+/* Linear layers over the ranks; buffers by rank r: y r, pre 16 + r, dx 32 + r, dweight
+ * 48 + r, dbias 64 + r, bias 80 + r, residual 96 + r, and those laid out again x 112 + r,
+ * weight 128 + r, dy 144 + r; workspace 160.  (TMA's own loads stay in their maps.) */
+#define DT_BOUNDS_LINEAR 11
 uint32_t dt_build_flags(void);
 
 #ifdef __cplusplus

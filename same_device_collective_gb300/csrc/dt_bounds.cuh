@@ -26,6 +26,7 @@ enum BoundsKernel : int {
     kBoundsBucket = DT_BOUNDS_BUCKET,
     kBoundsNorm = DT_BOUNDS_NORM,
     kBoundsVocab = DT_BOUNDS_VOCAB,
+    kBoundsLinear = DT_BOUNDS_LINEAR,
 };
 
 #ifdef DT_BOUNDS

@@ -1,0 +1,616 @@
+// C ABI entry points of the linear layers over the ranks: argument checks and
+// launch planning, by the conventions of the other calls (dt_ops.cpp).
+#include <algorithm>
+#include <cstring>
+
+#include "dt_group.h"
+#include "dt_host.h"
+#include "dt_linear.h"
+
+namespace {
+
+using namespace dt::host;
+using dt::LinearKind;
+
+constexpr size_t kMaxTokens = (size_t)1 << 26, kMaxWidth = (size_t)1 << 22;
+
+// How a call is cut up, and where its parts of the workspace lie.  The sizes
+// decide all of it; which matrices are laid out again is seen from the pointers.
+struct Plan {
+    LinearKind kind;
+    size_t n[DT_MAX_RANKS], f[DT_MAX_RANKS];
+    size_t tokens, features, dim;
+    bool pairs;                        // two CTAs share a tile
+    uint32_t high;                     // rows of a tile
+    uint64_t chunks;                   // of rows, whose column sums the bias' gradient adds
+    uint64_t tok, feat, w, sums, acc[2], bytes;
+};
+
+uint64_t tiles_of(uint64_t n, uint64_t size) { return (n + size - 1) / size; }
+
+bool back(LinearKind k) { return k == dt::kGatherBack || k == dt::kReduceBack; }
+bool gathers(LinearKind k) { return k == dt::kGather || k == dt::kGatherBack; }
+
+// The tokens' pieces that a product's tiles or blocks of `size` are cut from: each
+// rank's, or all of them as one.
+uint64_t token_tiles(const Plan &v, bool pieces, uint64_t size)
+{
+    if (!pieces) return tiles_of(v.tokens, size);
+    uint64_t t = 0;
+    for (size_t k : v.n) t += tiles_of(k, size);
+    return t;
+}
+
+uint64_t feature_tiles(const Plan &v, uint64_t size)
+{
+    uint64_t t = 0;
+    for (size_t k : v.f) t += tiles_of(k, size);
+    return t;
+}
+
+// Tiles across and down, and blocks of the inner axis, of a launch's products, with
+// the tokens' matrix in pieces or as one; the splits that leave no worker idle.
+struct Cut {
+    uint32_t bn;
+    uint64_t mt[2], nt[2], kblocks[2], splits[2];
+    uint64_t acc_bytes(const Plan &v, int k) const { return splits[k] > 1 ? splits[k] * mt[k] * v.high * nt[k] * bn * 4 : 0; }
+};
+
+bool cut(const dt_group *g, const Plan &v, bool pieces, Cut &c)
+{
+    const bool b = back(v.kind);
+    const uint64_t workers = dt::linear_workers(v.pairs, g->device), wide = v.pairs ? 256 : 128;
+    // the rows' axis of forward products is the tokens, which reducing are never in pieces
+    c.mt[0] = token_tiles(v, pieces && (v.kind == dt::kGather || v.kind == dt::kReduceBack), v.high);
+    const bool n_features = v.kind == dt::kGather || v.kind == dt::kReduceBack;
+    auto across = [&](uint64_t bn) { return n_features ? feature_tiles(v, bn) : tiles_of(v.dim, bn); };
+    // the narrower tile where it leaves the workers less to do one after the other; a
+    // tile costs about 64 columns more than it has
+    auto cost = [&](uint64_t bn) { return tiles_of(c.mt[0] * across(bn), workers) * (bn + 64); };
+    c.bn = (uint32_t)(!b && cost(wide / 2) < cost(wide) ? wide / 2 : wide);
+    c.nt[0] = across(c.bn);
+    c.kblocks[0] = n_features ? tiles_of(v.dim, 128) : feature_tiles(v, 128);
+    c.mt[1] = c.nt[1] = c.kblocks[1] = 0;
+    c.splits[0] = c.splits[1] = 1;
+    if (b) {
+        c.mt[1] = gathers(v.kind) ? feature_tiles(v, v.high) : tiles_of(v.dim, v.high);
+        c.nt[1] = c.nt[0];
+        c.kblocks[1] = token_tiles(v, pieces, 128);
+    }
+    uint64_t work = 0;
+    for (int k = 0; k < 2; ++k) {
+        if (c.mt[k] * c.nt[k] > 0x7FFFFFFF / workers) return false;   // tiles are counted in 32 bits
+        work += c.mt[k] * c.nt[k] * c.kblocks[k];
+    }
+    for (int k = 0; k < (b ? 2 : 1); ++k)
+        if (work) c.splits[k] = std::max<uint64_t>(1, std::min(c.kblocks[k] * workers / work, c.kblocks[k] / 4));
+    return true;
+}
+
+bool plan(const dt_group *g, LinearKind kind, const size_t *rows, size_t rows_equal, size_t dim, const size_t *features,
+          size_t features_equal, Plan &v)
+{
+    if (dim == 0 || dim > kMaxWidth) return false;
+    memset(&v, 0, sizeof v);
+    v.kind = kind;
+    v.dim = dim;
+    uint64_t padded = 0;
+    for (int r = 0; r < g->P; ++r) {
+        v.n[r] = rows ? rows[r] : rows_equal;
+        v.f[r] = features ? features[r] : features_equal;
+        if (v.n[r] > kMaxTokens || v.f[r] > kMaxWidth) return false;
+        v.tokens += v.n[r];
+        v.features += v.f[r];
+        padded += up(v.f[r], 8);
+        v.chunks += gathers(kind) ? 0 : tiles_of(v.n[r], dt::kPrepRows);
+    }
+    if (v.tokens > kMaxTokens || v.features > kMaxWidth || v.features == 0) return false;
+    if (gathers(kind)) v.chunks = tiles_of(v.tokens, dt::kPrepRows);
+    v.pairs = v.tokens > 128;
+    v.high = v.pairs ? 256 : 128;
+    uint64_t at = 0;
+    auto take = [&at](uint64_t n) {
+        const uint64_t from = at;
+        at = up(at + n, 256);
+        return from;
+    };
+    if (kind != dt::kReduce) v.tok = take((uint64_t)v.tokens * up(dim, 8) * 2);
+    if (kind != dt::kGather) v.feat = take((uint64_t)v.tokens * padded * 2);
+    v.w = take(gathers(kind) ? (uint64_t)v.features * up(dim, 8) * 2 : (uint64_t)dim * padded * 2);
+    if (back(kind)) v.sums = take(v.chunks * (gathers(kind) ? v.features : dim) * 4);
+    Cut c[2];
+    if (!cut(g, v, false, c[0]) || !cut(g, v, true, c[1])) return false;
+    for (int k = 0; k < 2; ++k) v.acc[k] = take(std::max(c[0].acc_bytes(v, k), c[1].acc_bytes(v, k)));
+    v.bytes = std::max<uint64_t>(at, 256);
+    return true;
+}
+
+size_t workspace_bytes_of(dt_group_t g, LinearKind fwd, const size_t *rows, size_t rows_equal, size_t dim,
+                          const size_t *features, size_t features_equal, int dtype, int backward)
+{
+    Plan v;
+    const LinearKind kind = !backward ? fwd : fwd == dt::kGather ? dt::kGatherBack : dt::kReduceBack;
+    if (!g || dtype != DT_BF16 || !plan(g, kind, rows, rows_equal, dim, features, features_equal, v)) return 0;
+    return (size_t)v.bytes;
+}
+
+// A call on its way: its plan, its buffers, and what goes before its products.
+struct Call {
+    dt_group *g;
+    Plan v;
+    Buffers b;
+    unsigned char *ws;
+    dt::LinearParams p;
+    dt::LinearPrep prep;
+    uint32_t pieces;                   // the tokens' matrix in the ranks' pieces (> 1), or as one
+    const void *tok[DT_MAX_RANKS];     // its pieces as TMA reads them
+    uint64_t tok_pitch;
+};
+
+template <typename Params>
+void workspace_extent(Params &p, const Call &c)
+{
+    dt::set_extent(p, dt::kLinearWorkspace, c.ws, c.v.bytes, false);
+}
+
+// A buffer for each rank that has something, of `width` columns, and its alignment.
+dt_status take_ranks(Call &c, const void *const *list, const size_t *n, const size_t *width, size_t equal, bool output,
+                     int buffer, int tag = -1)
+{
+    for (int r = 0; r < c.g->P; ++r) {
+        const size_t bytes = n[r] * (width ? width[r] : equal) * 2;
+        if (bytes == 0) continue;
+        if (!list || !list[r] || !multiple(list[r], 2)) return DT_ERR_INVALID;
+        if (output) c.b.write(list[r], bytes, tag >= 0 ? tag + r : -1);
+        else c.b.read(list[r], bytes, tag >= 0 ? tag + r : -1);
+        dt::set_extent(c.p, buffer + r, list[r], bytes, output);
+        dt::set_extent(c.prep, buffer + r, list[r], bytes, output);
+    }
+    return DT_OK;
+}
+
+uint32_t alignment(uint32_t least, const void *p, size_t width)
+{
+    while (width % least || !multiple(p, 2 * least)) least /= 2;
+    return least;
+}
+
+// A job of the launch before the products.
+void add_job(Call &c, const void *src, const void *pre, void *dst, float *sums, size_t rows, size_t cols, size_t pitch,
+             int src_buffer, int pre_buffer)
+{
+    if (rows == 0 || cols == 0) return;
+    dt::LinearPrepJob &j = c.prep.job[c.prep.jobs];
+    j.src = static_cast<const uint16_t *>(src);
+    j.pre = static_cast<const uint16_t *>(pre);
+    j.dst = static_cast<uint16_t *>(dst);
+    j.sums = sums;
+    j.rows = (uint32_t)rows;
+    j.cols = (uint32_t)cols;
+    j.pitch = (uint32_t)pitch;
+    j.strips = (uint32_t)tiles_of(cols, dt::kPrepCols);
+    j.block_end = (c.prep.jobs ? c.prep.job[c.prep.jobs - 1].block_end : 0) + j.strips * (uint32_t)tiles_of(rows, dt::kPrepRows);
+    j.src_buffer = src_buffer;
+    j.pre_buffer = pre_buffer;
+    ++c.prep.jobs;
+}
+
+bool addressable(const void *p, size_t width) { return width % 8 == 0 && aligned16(p); }
+
+// Checks what all calls share.
+dt_status begin(Call &c, LinearKind kind, const size_t *rows, size_t rows_equal, size_t dim, const size_t *features,
+                size_t features_equal, int dtype, void *workspace, size_t workspace_bytes)
+{
+    if (!valid_dtype(dtype)) return DT_ERR_INVALID;
+    if (dtype != DT_BF16) return DT_ERR_UNSUPPORTED;
+    if (!plan(c.g, kind, rows, rows_equal, dim, features, features_equal, c.v)) return DT_ERR_INVALID;
+    memset(&c.p, 0, sizeof c.p);
+    memset(&c.prep, 0, sizeof c.prep);
+    c.ws = static_cast<unsigned char *>(workspace);
+    if (c.v.tokens) {
+        if (!workspace || !multiple(workspace, 256) || workspace_bytes < c.v.bytes) return DT_ERR_INVALID;
+        c.b.write(workspace, workspace_bytes);
+    }
+    dt::LinearParams &p = c.p;
+    uint32_t end = 0;
+    for (int r = 0; r < c.g->P; ++r) {
+        p.f_len[r] = (uint32_t)c.v.f[r];
+        p.row_end[r] = end += (uint32_t)c.v.n[r];
+    }
+    p.P = c.g->P;
+    p.tokens = (uint32_t)c.v.tokens;
+    p.dim = (uint32_t)dim;
+    p.sink = c.prep.sink = error_sink(c.g);
+    workspace_extent(p, c);
+    workspace_extent(c.prep, c);
+    return DT_OK;
+}
+
+// How the tokens' matrix is read: as one where the ranks' rows follow one another in
+// memory, in the ranks' pieces where the tiles at their ends waste little, else laid
+// out again as one.  sums: column sums of its rows are wanted.
+void token_matrix(Call &c, const void *const *x, int buffer, float *sums)
+{
+    const Plan &v = c.v;
+    bool reads = true, follow = true, steps = true;
+    const unsigned char *next = nullptr;
+    uint64_t tiles = 0, before = 0;
+    uint32_t pieces = 0;
+    for (int r = 0; r < c.g->P; ++r) {
+        if (v.n[r] == 0) continue;
+        reads = reads && addressable(x[r], v.dim);
+        follow = follow && (!next || next == x[r]);
+        next = static_cast<const unsigned char *>(x[r]) + v.n[r] * v.dim * 2;
+        tiles += tiles_of(v.n[r], v.high);
+        // as the inner axis, each piece but the last has to be whole steps of 16: a step's
+        // other tokens would be the next rank's in the operand that is not in pieces
+        // (times zero, but an infinity times zero is not zero)
+        steps = steps && before % 16 == 0;
+        before = v.n[r];
+        c.tok[pieces] = x[r];
+        c.p.t_len[pieces++] = (uint32_t)v.n[r];
+    }
+    const bool in_pieces = reads && !follow && (!back(v.kind) || steps) && tiles * 20 <= tiles_of(v.tokens, v.high) * 21;
+    const bool again = !in_pieces && !(reads && follow);
+    c.tok_pitch = again ? up(v.dim, 8) : v.dim;
+    uint64_t first = 0, chunk = 0;
+    unsigned char *to = c.ws + v.tok;
+    for (int r = 0; r < c.g->P && (again || sums); ++r) {
+        add_job(c, x[r], nullptr, again ? to + first * c.tok_pitch * 2 : nullptr, sums ? sums + chunk * v.dim : nullptr, v.n[r],
+                v.dim, c.tok_pitch, buffer + r, 0);
+        chunk += tiles_of(v.n[r], dt::kPrepRows);
+        first += v.n[r];
+    }
+    if (again) c.tok[0] = to;
+    if (!in_pieces) {
+        pieces = 1;
+        c.p.t_len[0] = c.p.tokens;
+    }
+    for (uint32_t k = 1; k < pieces; ++k) c.p.t_first[k] = c.p.t_first[k - 1] + c.p.t_len[k - 1];
+    c.pieces = pieces;
+    c.p.t_pieces = (int32_t)pieces;
+}
+
+// A matrix for each rank, [rows, cols]: the map that reads it in place, or laid out
+// again at `to`.
+cudaError_t rank_matrix(Call &c, CUtensorMap *map, const void *src, size_t rows, size_t cols, unsigned char *&to, int buffer,
+                        uint32_t box, bool written = false)
+{
+    if (rows == 0 || cols == 0) return cudaSuccess;
+    const uint64_t pitch = up(cols, 8);
+    unsigned char *dst = to;
+    to += rows * pitch * 2;
+    if (written) return dt::matrix_map(map, dst, cols, rows, pitch, box);
+    if (addressable(src, cols)) return dt::matrix_map(map, src, cols, rows, cols, box);
+    add_job(c, src, nullptr, dst, nullptr, rows, cols, pitch, buffer, 0);
+    return dt::matrix_map(map, dst, cols, rows, pitch, box);
+}
+
+// The maps of all matrices, and the tiles.  feat: the ranks' [tokens, f] (written:
+// a job before the products makes it in the workspace).
+cudaError_t matrices(Call &c, const void *const *feat, int feat_buffer, bool written, const void *const *w)
+{
+    const Plan &v = c.v;
+    dt::LinearParams &p = c.p;
+    Cut t;
+    cut(c.g, v, c.pieces > 1, t);
+    const bool b = back(v.kind);
+    p.bn = t.bn;
+    // few tokens: boxes of as many as there are, in whole K steps of 16 where the
+    // tokens are the inner axis
+    p.rows_t = v.pairs ? 128 : (uint32_t)up(v.tokens, b ? 16 : 8);
+    p.rows_w = b ? 128 : t.bn / (v.pairs ? 2 : 1);
+    cudaError_t e = cudaSuccess;
+    if (v.kind != dt::kReduce)
+        for (uint32_t k = 0; k < c.pieces && e == cudaSuccess; ++k)
+            e = dt::matrix_map(&p.tok[k], c.tok[k], v.dim, p.t_len[k], c.tok_pitch, p.rows_t);
+    unsigned char *to = c.ws + v.feat, *to_w = c.ws + v.w;
+    for (int r = 0; r < c.g->P && e == cudaSuccess; ++r) {
+        if (v.kind != dt::kGather)
+            e = rank_matrix(c, &p.feat[r], feat[r], v.tokens, v.f[r], to, feat_buffer + r, p.rows_t, written);
+        if (e == cudaSuccess)
+            e = rank_matrix(c, &p.w[r], w[r], gathers(v.kind) ? v.f[r] : v.dim, gathers(v.kind) ? v.dim : v.f[r], to_w,
+                            dt::kLinearW + r, p.rows_w);
+    }
+    for (int k = 0; k < (b ? 2 : 1); ++k) {
+        dt::LinearProduct &q = p.product[k];
+        q.mt = (uint32_t)t.mt[k];
+        q.nt = (uint32_t)t.nt[k];
+        q.kblocks = (uint32_t)t.kblocks[k];
+        q.splits = (uint32_t)t.splits[k];
+        q.tiles = q.mt * q.nt * q.splits;
+        q.acc = reinterpret_cast<float *>(c.ws + v.acc[k]);
+        // the size of a tile or block along the features and the tokens in this product
+        const bool n_features = v.kind == dt::kGather || v.kind == dt::kReduceBack;
+        const uint64_t fs = n_features ? t.bn : k ? v.high : 128;
+        const uint64_t ts = k ? 128 : v.high;
+        uint32_t end = 0;
+        for (int r = 0; r < c.g->P; ++r) q.f_end[r] = end += (uint32_t)tiles_of(v.f[r], fs);
+        end = 0;
+        for (uint32_t r = 0; r < c.pieces; ++r) q.t_end[r] = end += (uint32_t)tiles_of(p.t_len[r], ts);
+    }
+    return e;
+}
+
+// The launches of a call: what goes before, the products, and the splits' joins.
+cudaError_t run(Call &c, cudaStream_t s)
+{
+    cudaError_t e = cudaSuccess;
+    const int device = c.g->device;
+    if (c.prep.jobs) e = dt::launch_linear_prep(c.prep, s);
+    if (e == cudaSuccess) e = dt::launch_linear(c.p, c.v.kind, c.v.pairs, device, s);
+    for (int k = 0; k < 2 && e == cudaSuccess; ++k)
+        if (c.p.product[k].splits > 1) e = dt::launch_linear_join(c.p, c.v.kind, k, c.v.pairs, device, s);
+    return e;
+}
+
+cudaError_t zero_ranks(const dt_group *g, void *const *list, const size_t *n, const size_t *width, size_t equal, cudaStream_t s)
+{
+    cudaError_t e = cudaSuccess;
+    for (int r = 0; r < g->P && e == cudaSuccess; ++r) {
+        const size_t bytes = n[r] * (width ? width[r] : equal) * 2;
+        if (bytes) e = cudaMemsetAsync(list[r], 0, bytes, s);
+    }
+    return e;
+}
+
+bool valid_act(int act) { return act >= DT_ACT_NONE && act <= DT_ACT_SILU; }
+
+}  // namespace
+
+extern "C" {
+
+dt_status dt_gather_linear(dt_group_t g, const void *const *x, const void *const *weight, const void *const *bias,
+                           void *const *pre, void *const *y, const size_t *rows, size_t rows_equal, size_t dim,
+                           const size_t *features, size_t features_equal, int dtype, int act, void *workspace,
+                           size_t workspace_bytes, void *stream)
+{
+    DT_TRACE();
+    if (!g) return DT_ERR_INVALID;
+    std::lock_guard<std::mutex> lock(g->mu);
+    dt_status st = take_device_error(g);
+    if (st != DT_OK) return st;
+    Call c;
+    c.g = g;
+    st = begin(c, dt::kGather, rows, rows_equal, dim, features, features_equal, dtype, workspace, workspace_bytes);
+    if (st != DT_OK) return st;
+    if (!valid_act(act)) return DT_ERR_INVALID;
+    const Plan &v = c.v;
+    size_t n[DT_MAX_RANKS], one[DT_MAX_RANKS];
+    std::fill(n, n + DT_MAX_RANKS, v.tokens);
+    std::fill(one, one + DT_MAX_RANKS, (size_t)1);
+    if ((st = take_ranks(c, x, v.n, nullptr, dim, false, dt::kLinearX)) != DT_OK) return st;
+    if ((st = take_ranks(c, weight, v.f, nullptr, dim, false, dt::kLinearW)) != DT_OK) return st;
+    if (bias && (st = take_ranks(c, bias, one, v.f, 0, false, dt::kLinearBias)) != DT_OK) return st;
+    if (pre && (st = take_ranks(c, pre, n, v.f, 0, true, dt::kLinearPre)) != DT_OK) return st;
+    if ((st = take_ranks(c, y, n, v.f, 0, true, dt::kLinearY)) != DT_OK) return st;
+    if (c.b.clash()) return DT_ERR_INVALID;
+    if (v.tokens == 0) return DT_OK;
+    c.p.act = act;
+    c.p.keep = pre != nullptr;
+    c.p.biased = bias != nullptr;
+    for (int r = 0; r < g->P; ++r) {
+        if (v.f[r] == 0) continue;
+        c.p.product[0].out[r] = static_cast<uint16_t *>(y[r]);
+        c.p.pre[r] = pre ? static_cast<uint16_t *>(pre[r]) : nullptr;
+        c.p.bias[r] = bias ? static_cast<const uint16_t *>(bias[r]) : nullptr;
+        c.p.product[0].align[r] = alignment(alignment(8, y[r], v.f[r]), c.p.pre[r], v.f[r]);
+    }
+    DeviceScope scope(g->device);
+    if (!scope.ok) return DT_ERR_CUDA;
+    token_matrix(c, x, dt::kLinearX, nullptr);
+    cudaError_t e = matrices(c, nullptr, 0, false, weight);
+    if (e == cudaSuccess) e = run(c, static_cast<cudaStream_t>(stream));
+    return cuda_status(e);
+}
+
+dt_status dt_gather_linear_backward(dt_group_t g, const void *const *x, const void *const *weight, const void *const *pre,
+                                    const void *const *dy, void *const *dx, void *const *dweight, void *const *dbias,
+                                    const size_t *rows, size_t rows_equal, size_t dim, const size_t *features,
+                                    size_t features_equal, int dtype, int act, void *workspace, size_t workspace_bytes,
+                                    void *stream)
+{
+    DT_TRACE();
+    if (!g) return DT_ERR_INVALID;
+    std::lock_guard<std::mutex> lock(g->mu);
+    dt_status st = take_device_error(g);
+    if (st != DT_OK) return st;
+    Call c;
+    c.g = g;
+    st = begin(c, dt::kGatherBack, rows, rows_equal, dim, features, features_equal, dtype, workspace, workspace_bytes);
+    if (st != DT_OK) return st;
+    if (!valid_act(act)) return DT_ERR_INVALID;
+    if (act == DT_ACT_NONE) pre = nullptr;
+    const Plan &v = c.v;
+    size_t n[DT_MAX_RANKS], one[DT_MAX_RANKS];
+    std::fill(n, n + DT_MAX_RANKS, v.tokens);
+    std::fill(one, one + DT_MAX_RANKS, (size_t)1);
+    if ((st = take_ranks(c, x, v.n, nullptr, dim, false, dt::kLinearX)) != DT_OK) return st;
+    if ((st = take_ranks(c, weight, v.f, nullptr, dim, false, dt::kLinearW)) != DT_OK) return st;
+    if (act != DT_ACT_NONE && (st = take_ranks(c, pre, n, v.f, 0, false, dt::kLinearPre)) != DT_OK) return st;
+    if ((st = take_ranks(c, dy, n, v.f, 0, false, dt::kLinearDy)) != DT_OK) return st;
+    if ((st = take_ranks(c, dx, v.n, nullptr, dim, true, dt::kLinearDx)) != DT_OK) return st;
+    if ((st = take_ranks(c, dweight, v.f, nullptr, dim, true, dt::kLinearDw)) != DT_OK) return st;
+    if (dbias && (st = take_ranks(c, dbias, one, v.f, 0, true, dt::kLinearDb)) != DT_OK) return st;
+    if (c.b.clash()) return DT_ERR_INVALID;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    DeviceScope scope(g->device);
+    if (!scope.ok) return DT_ERR_CUDA;
+    if (v.tokens == 0) {
+        cudaError_t e = zero_ranks(g, dweight, v.f, nullptr, dim, s);
+        if (e == cudaSuccess && dbias) e = zero_ranks(g, dbias, one, v.f, 0, s);
+        return cuda_status(e);
+    }
+    uint32_t tok_align = 8;
+    for (int r = 0; r < g->P; ++r) {
+        if (v.n[r]) {
+            c.p.product[0].out[r] = static_cast<uint16_t *>(dx[r]);
+            tok_align = alignment(tok_align, dx[r], dim);
+        }
+        if (v.f[r]) {
+            c.p.product[1].out[r] = static_cast<uint16_t *>(dweight[r]);
+            c.p.product[1].align[r] = alignment(8, dweight[r], dim);
+        }
+    }
+    c.p.product[0].align[0] = tok_align;
+    c.prep.act = act;
+    token_matrix(c, x, dt::kLinearX, nullptr);
+    // G: dy itself where nothing is done to it and TMA can read it
+    bool written = act != DT_ACT_NONE;
+    for (int r = 0; r < g->P; ++r)
+        if (v.f[r] && !addressable(dy[r], v.f[r])) written = true;
+    dt::LinearSums sums;
+    memset(&sums, 0, sizeof sums);
+    float *part = reinterpret_cast<float *>(c.ws + v.sums);
+    unsigned char *to = c.ws + v.feat;
+    for (int r = 0; r < g->P; ++r) {
+        const uint64_t pitch = up(v.f[r], 8);
+        if (written || dbias)
+            add_job(c, dy[r], pre ? pre[r] : nullptr, written ? to : nullptr, dbias ? part : nullptr, v.tokens, v.f[r], pitch,
+                    dt::kLinearDy + r, dt::kLinearPre + r);
+        to += v.tokens * pitch * 2;
+        if (dbias) {
+            sums.sums[r] = part;
+            sums.out[r] = static_cast<uint16_t *>(dbias[r]);
+            sums.cols[r] = (uint32_t)v.f[r];
+            sums.block_end[r] = (r ? sums.block_end[r - 1] : 0) + (uint32_t)tiles_of(v.f[r], 32);
+            dt::set_extent(sums, dt::kLinearDb + r, dbias[r], v.f[r] * 2, true);
+            part += v.chunks * v.f[r];
+        }
+    }
+    cudaError_t e = matrices(c, dy, dt::kLinearDy, written, weight);
+    if (e == cudaSuccess) e = run(c, s);
+    if (e == cudaSuccess && dbias) {
+        sums.n = g->P;
+        sums.chunks = (uint32_t)v.chunks;
+        sums.sink = c.p.sink;
+        workspace_extent(sums, c);
+        e = dt::launch_linear_sums(sums, s);
+    }
+    return cuda_status(e);
+}
+
+size_t dt_gather_linear_workspace(dt_group_t g, const size_t *rows, size_t rows_equal, size_t dim, const size_t *features,
+                                  size_t features_equal, int dtype, int backward)
+{
+    return workspace_bytes_of(g, dt::kGather, rows, rows_equal, dim, features, features_equal, dtype, backward);
+}
+
+dt_status dt_linear_reduce(dt_group_t g, const void *const *x, const void *const *weight, const void *bias,
+                           const void *const *residual, void *const *y, const size_t *rows, size_t rows_equal, size_t dim,
+                           const size_t *features, size_t features_equal, int dtype, void *workspace,
+                           size_t workspace_bytes, void *stream)
+{
+    DT_TRACE();
+    if (!g) return DT_ERR_INVALID;
+    std::lock_guard<std::mutex> lock(g->mu);
+    dt_status st = take_device_error(g);
+    if (st != DT_OK) return st;
+    Call c;
+    c.g = g;
+    st = begin(c, dt::kReduce, rows, rows_equal, dim, features, features_equal, dtype, workspace, workspace_bytes);
+    if (st != DT_OK) return st;
+    const Plan &v = c.v;
+    size_t n[DT_MAX_RANKS], d[DT_MAX_RANKS];
+    std::fill(n, n + DT_MAX_RANKS, v.tokens);
+    std::fill(d, d + DT_MAX_RANKS, dim);
+    if (!multiple(bias, 2)) return DT_ERR_INVALID;
+    c.b.read(bias, dim * 2);
+    dt::set_extent(c.p, dt::kLinearBias, bias, dim * 2, false);
+    if ((st = take_ranks(c, x, n, v.f, 0, false, dt::kLinearX)) != DT_OK) return st;
+    if ((st = take_ranks(c, weight, d, v.f, 0, false, dt::kLinearW)) != DT_OK) return st;
+    // y may be the residual: a thread reads an element before it writes it
+    if (residual && (st = take_ranks(c, residual, v.n, nullptr, dim, false, dt::kLinearResidual, 0)) != DT_OK) return st;
+    if ((st = take_ranks(c, y, v.n, nullptr, dim, true, dt::kLinearY, 0)) != DT_OK) return st;
+    if (c.b.clash()) return DT_ERR_INVALID;
+    if (v.tokens == 0) return DT_OK;
+    c.p.biased = bias != nullptr;
+    c.p.bias[0] = static_cast<const uint16_t *>(bias);
+    c.p.residuals = residual != nullptr;
+    uint32_t align = 8;
+    for (int r = 0; r < g->P; ++r) {
+        if (v.n[r] == 0) continue;
+        c.p.product[0].out[r] = static_cast<uint16_t *>(y[r]);
+        c.p.residual[r] = residual ? static_cast<const uint16_t *>(residual[r]) : nullptr;
+        align = alignment(alignment(align, y[r], dim), c.p.residual[r], dim);
+    }
+    c.p.product[0].align[0] = align;
+    DeviceScope scope(g->device);
+    if (!scope.ok) return DT_ERR_CUDA;
+    c.pieces = 1;
+    c.p.t_pieces = 1;
+    c.p.t_len[0] = c.p.tokens;
+    cudaError_t e = matrices(c, x, dt::kLinearX, false, weight);
+    if (e == cudaSuccess) e = run(c, static_cast<cudaStream_t>(stream));
+    return cuda_status(e);
+}
+
+dt_status dt_linear_reduce_backward(dt_group_t g, const void *const *x, const void *const *weight, const void *const *dy,
+                                    void *const *dx, void *const *dweight, void *dbias, const size_t *rows,
+                                    size_t rows_equal, size_t dim, const size_t *features, size_t features_equal, int dtype,
+                                    void *workspace, size_t workspace_bytes, void *stream)
+{
+    DT_TRACE();
+    if (!g) return DT_ERR_INVALID;
+    std::lock_guard<std::mutex> lock(g->mu);
+    dt_status st = take_device_error(g);
+    if (st != DT_OK) return st;
+    Call c;
+    c.g = g;
+    st = begin(c, dt::kReduceBack, rows, rows_equal, dim, features, features_equal, dtype, workspace, workspace_bytes);
+    if (st != DT_OK) return st;
+    const Plan &v = c.v;
+    size_t n[DT_MAX_RANKS], d[DT_MAX_RANKS];
+    std::fill(n, n + DT_MAX_RANKS, v.tokens);
+    std::fill(d, d + DT_MAX_RANKS, dim);
+    if ((st = take_ranks(c, x, n, v.f, 0, false, dt::kLinearX)) != DT_OK) return st;
+    if ((st = take_ranks(c, weight, d, v.f, 0, false, dt::kLinearW)) != DT_OK) return st;
+    if ((st = take_ranks(c, dy, v.n, nullptr, dim, false, dt::kLinearDy)) != DT_OK) return st;
+    if ((st = take_ranks(c, dx, n, v.f, 0, true, dt::kLinearDx)) != DT_OK) return st;
+    if ((st = take_ranks(c, dweight, d, v.f, 0, true, dt::kLinearDw)) != DT_OK) return st;
+    if (!multiple(dbias, 2)) return DT_ERR_INVALID;
+    c.b.write(dbias, dim * 2);
+    if (c.b.clash()) return DT_ERR_INVALID;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    DeviceScope scope(g->device);
+    if (!scope.ok) return DT_ERR_CUDA;
+    if (v.tokens == 0) {
+        cudaError_t e = zero_ranks(g, dweight, d, v.f, 0, s);
+        if (e == cudaSuccess && dbias) e = cudaMemsetAsync(dbias, 0, dim * 2, s);
+        return cuda_status(e);
+    }
+    for (int r = 0; r < g->P; ++r) {
+        if (v.f[r] == 0) continue;
+        c.p.product[0].out[r] = static_cast<uint16_t *>(dx[r]);
+        c.p.product[1].out[r] = static_cast<uint16_t *>(dweight[r]);
+        c.p.product[0].align[r] = alignment(8, dx[r], v.f[r]);
+        c.p.product[1].align[r] = alignment(8, dweight[r], v.f[r]);
+    }
+    float *part = reinterpret_cast<float *>(c.ws + v.sums);
+    token_matrix(c, dy, dt::kLinearDy, dbias ? part : nullptr);
+    cudaError_t e = matrices(c, x, dt::kLinearX, false, weight);
+    if (e == cudaSuccess) e = run(c, s);
+    if (e == cudaSuccess && dbias) {
+        dt::LinearSums sums;
+        memset(&sums, 0, sizeof sums);
+        sums.sums[0] = part;
+        sums.out[0] = static_cast<uint16_t *>(dbias);
+        sums.cols[0] = (uint32_t)dim;
+        sums.block_end[0] = (uint32_t)tiles_of(dim, 32);
+        sums.n = 1;
+        sums.chunks = (uint32_t)v.chunks;
+        sums.sink = c.p.sink;
+        workspace_extent(sums, c);
+        dt::set_extent(sums, dt::kLinearDb, dbias, dim * 2, true);
+        e = dt::launch_linear_sums(sums, s);
+    }
+    return cuda_status(e);
+}
+
+size_t dt_linear_reduce_workspace(dt_group_t g, const size_t *rows, size_t rows_equal, size_t dim, const size_t *features,
+                                  size_t features_equal, int dtype, int backward)
+{
+    return workspace_bytes_of(g, dt::kReduce, rows, rows_equal, dim, features, features_equal, dtype, backward);
+}
+
+}  // extern "C"

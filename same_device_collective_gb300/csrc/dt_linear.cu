@@ -1,0 +1,939 @@
+// Linear layers of a block whose tokens and features are both split over the
+// ranks, and their gradients (LinearKind).
+//
+//   gathering   y_r  = act(X W_r^T + b_r)            X: all ranks' tokens
+//               dx   = sum_r G_r W_r                 G_r = dy_r act'(pre_r)
+//               dW_r = G_r^T X,  db_r = sum_tokens G_r
+//   reducing    y    = sum_r H_r W_r^T + b + residual, each rank its own tokens
+//               dH_r = Y W_r
+//               dW_r = Y^T H_r,  db = sum_tokens Y       Y: all ranks' dy
+//
+// Every one of these is a product along one of three axes (tokens, columns of a
+// token, features) of two of three matrices: the ranks' tokens, the ranks'
+// features and the weights.  One persistent kernel serves all: tiles of 128 x
+// bn outputs, or of 256 x bn for two CTAs of a cluster, operands brought by TMA
+// into a ring of shared memory stages by one thread, multiplied by one thread
+// that issues tcgen05.mma into tensor memory, and finished by eight warps that
+// read the accumulator while the next tile's is made in the other half of tensor
+// memory.  A backward call's two products are one launch, so that one's tiles
+// fill what the other's leave of the last wave.
+//
+// The ranks are offsets and no more.  Along an output's axis a tile lies within
+// one rank's piece; along the inner axis the ranks' pieces follow one another in
+// blocks of 128, in the same accumulator: the gathered tokens and the partial sums
+// of the ranks, which a gather and a reduction around a library's product would
+// write and read, are never in memory, and the sum over the ranks is rounded once.
+// Past a piece's end TMA fills in zeros.
+//
+// Sums are fp32.  The tensor cores add 16 products at a time and round towards
+// zero: a sum of n terms of one sign comes out up to n * 2e-9 of itself too small
+// (3e-5 of 16384), where results are rounded by up to 2^-9 of themselves.
+#include <algorithm>
+#include <atomic>
+#include <type_traits>
+
+#include "dt_linear.h"
+
+#include "dt_bounds.cuh"
+#include "dt_device.cuh"
+#include "dt_math.cuh"
+#include "dt_tc.cuh"
+#include "dt_tile.cuh"
+#include "dt_timeline.cuh"
+
+namespace dt {
+namespace {
+
+constexpr uint32_t kM = 128;                       // rows of a tile in a CTA
+constexpr uint32_t kK = 128;                       // depth of a stage
+constexpr uint32_t kRingBytes = 192 * 1024;        // three stages of 128 rows and columns of A and B
+constexpr uint32_t kMaxStages = 8;
+constexpr uint32_t kTmemColumns = 512;             // two accumulators of 128 x 256 fp32
+constexpr uint32_t kFinishWarps = 8;
+constexpr int kTcThreads = (kFinishWarps + 2) * 32;
+constexpr uint32_t kStageOut = 4096;               // a finishing warp's 32 rows x 128 bytes
+constexpr uint32_t kOutBytes = kFinishWarps * kStageOut;
+constexpr uint32_t kBarBytes = 256, kBiasBytes = kFinishWarps * 128;
+constexpr size_t kTcSmem = 1024 + kRingBytes + kOutBytes + kBarBytes + kBiasBytes;
+static_assert(kTcSmem <= 227 * 1024, "shared memory above the per-block limit");
+constexpr uint32_t kGroup = 16;                    // columns of tiles that are worked on together
+
+#define LINEAR_OK(buffer, a, n) DT_IN_EXTENT(p, kBoundsLinear, (buffer), (a), (n))
+
+__host__ __device__ constexpr bool is_back(int kind) { return kind == kGatherBack || kind == kReduceBack; }
+
+// The matrices that TMA reads.
+enum Matrix : int { kTok, kFeat, kW };
+
+// What the rows, columns and inner axis of a product are, and its operands.  An
+// operand is MN-major where its rows run along the inner axis.
+template <int KIND, bool SECOND>
+struct Roles {
+    static constexpr int m = !SECOND ? kTokens : KIND == kGatherBack ? kFeatures : kDim;
+    static constexpr int n = KIND == kGather || KIND == kReduceBack ? kFeatures : kDim;
+    static constexpr int k = SECOND ? kTokens : n == kFeatures ? kDim : kFeatures;
+    static constexpr int a = KIND == kGather || KIND == kReduceBack ? kTok : kFeat;
+    static constexpr int b = !SECOND ? kW : KIND == kGatherBack ? kTok : kFeat;
+    static constexpr bool a_mn = SECOND, b_mn = is_back(KIND);
+    static constexpr bool tok = a == kTok || b == kTok;   // the token axis is cut as the tokens' matrices are
+    static constexpr bool w_by_feature = KIND == kGather || KIND == kGatherBack;   // rows of W_r are features
+};
+
+// A place along an axis: the rank's piece, the place there, and overall (tokens).
+struct Place {
+    uint32_t piece, at, all;
+};
+
+template <class R, int AXIS>
+__device__ __forceinline__ Place locate(const LinearParams &p, const LinearProduct &c, uint32_t i, uint32_t unit)
+{
+    if constexpr (AXIS == kDim) {
+        return Place{0, i * unit, 0};
+    } else if constexpr (AXIS == kFeatures) {
+        uint32_t r = 0, begin = 0;
+        while ((int)r + 1 < p.P && i >= c.f_end[r]) begin = c.f_end[r++];
+        return Place{r, (i - begin) * unit, 0};
+    } else if (!R::tok) {
+        return Place{0, i * unit, i * unit};
+    } else {
+        uint32_t r = 0, begin = 0;
+        while ((int)r + 1 < p.t_pieces && i >= c.t_end[r]) begin = c.t_end[r++];
+        const uint32_t at = (i - begin) * unit;
+        return Place{r, at, p.t_first[r] + at};
+    }
+}
+
+template <class R, int AXIS>
+__device__ __forceinline__ uint32_t length(const LinearParams &p, uint32_t piece)
+{
+    return AXIS == kDim ? p.dim : AXIS == kFeatures ? p.f_len[piece] : R::tok ? p.t_len[piece] : p.tokens;
+}
+
+// Walks over the blocks of the inner axis.
+template <class R>
+struct Inner {
+    Place at;
+    uint32_t len;
+    __device__ __forceinline__ Inner(const LinearParams &p, const LinearProduct &c, uint32_t kb)
+        : at(locate<R, R::k>(p, c, kb, kK)), len(length<R, R::k>(p, at.piece))
+    {
+    }
+    __device__ __forceinline__ void next(const LinearParams &p)
+    {
+        at.at += kK;
+        at.all += kK;
+        const uint32_t pieces = R::k == kFeatures ? (uint32_t)p.P : R::k == kTokens && R::tok ? (uint32_t)p.t_pieces : 1;
+        while (at.at >= len && at.piece + 1 < pieces) {
+            ++at.piece;
+            at.at = 0;
+            len = length<R, R::k>(p, at.piece);
+            if (R::k == kTokens) at.all = p.t_first[at.piece];
+        }
+    }
+};
+
+struct Tile {
+    bool second;
+    uint32_t m, n, kb0, kb1, split;
+};
+
+__device__ __forceinline__ void place_tile(const LinearProduct &c, uint32_t i, Tile &t)
+{
+    const uint32_t per_split = c.mt * c.nt;
+    t.split = i / per_split;
+    i -= t.split * per_split;
+    const uint32_t all = kGroup * c.mt, g = i / all;
+    i -= g * all;
+    const uint32_t width = min(kGroup, c.nt - g * kGroup);
+    t.m = i / width;
+    t.n = g * kGroup + i - t.m * width;
+    t.kb0 = (uint32_t)((uint64_t)c.kblocks * t.split / c.splits);
+    t.kb1 = (uint32_t)((uint64_t)c.kblocks * (t.split + 1) / c.splits);
+}
+
+// The k-th tile of worker q (a CTA or a pair) of W; false when it has no more.
+// Columns of tiles in groups of 16, rows slowest within a group, so that the tiles
+// in flight share few rows and columns and their operands come from L2.  First the
+// tiles of the first product, one by one to the workers.  While the first `rest`
+// workers still have one more of them, the others take `early` tiles of the second
+// product each; then all take the rest of those in turn.
+template <int KIND>
+__device__ __forceinline__ bool next_tile(const LinearParams &p, uint32_t q, uint32_t W, uint32_t k, Tile &t)
+{
+    const uint32_t tiles = p.product[0].tiles;
+    const uint32_t mine = q < tiles ? (tiles - q + W - 1) / W : 0;
+    t.second = false;
+    if (k < mine) {
+        place_tile(p.product[0], q + k * W, t);
+        return true;
+    }
+    if constexpr (!is_back(KIND)) return false;
+    k -= mine;
+    uint32_t i;
+    const uint32_t others = W - p.rest;
+    if (q >= p.rest && k < p.early) {
+        i = q - p.rest + k * others;
+    } else {
+        if (q >= p.rest) k -= p.early;
+        i = p.early * others + k * W + (q >= p.rest ? q - p.rest : q + others);
+    }
+    if (i >= p.product[1].tiles) return false;
+    t.second = true;
+    place_tile(p.product[1], i, t);
+    return true;
+}
+
+// The map of an operand, and the column and row of its first box, at these places.
+template <class R, int MATRIX>
+__device__ __forceinline__ const CUtensorMap *operand(const LinearParams &p, const Place (&at)[3], uint32_t &col,
+                                                      uint32_t &row)
+{
+    const Place &t = at[kTokens], &d = at[kDim], &f = at[kFeatures];
+    if (MATRIX == kTok) {
+        col = d.at;
+        row = t.at;
+        return &p.tok[t.piece];
+    }
+    if (MATRIX == kFeat) {
+        col = f.at;
+        row = t.all;
+        return &p.feat[f.piece];
+    }
+    col = R::w_by_feature ? d.at : f.at;
+    row = R::w_by_feature ? f.at : d.at;
+    return &p.w[f.piece];
+}
+
+// From operand A's first box to its second: K-major boxes of few tokens' rows lie
+// closer, MN-major ones are a fixed way apart.
+__host__ __device__ constexpr uint32_t a_box_bytes(bool back, uint32_t rows)
+{
+    return back ? kBoxBytes : (rows * 128 + 1023) / 1024 * 1024;
+}
+
+// One stage: two boxes of A, the second 64 columns further, and of B two, or one
+// to 64 columns of an MN-major operand.  What a stage holds beside its boxes is left
+// over from earlier loads and reaches only rows of the accumulator that are not
+// stored.
+template <class R, int CG>
+__device__ __forceinline__ void load_stage(const LinearParams &p, Place (&at)[3], const Place &k, uint32_t half, uint32_t a,
+                                           uint32_t a_box, uint32_t bar)
+{
+    at[R::k] = k;
+    const uint32_t bn = p.bn / CG, b = a + 2 * a_box;
+    const uint32_t b_boxes = R::b_mn ? bn / 64 : 2, b_rows = R::b_mn ? (R::b == kW ? kK : p.rows_t) : bn;
+    if (half == 0) mbar_expect_tx(bar, CG * (2 * p.rows_t + b_boxes * b_rows) * 128);
+    uint32_t col, row;
+    const CUtensorMap *map = operand<R, R::a>(p, at, col, row);
+    (R::a_mn ? col : row) += half * kM;
+    tma_box<CG>(a, map, col, row, bar);
+    tma_box<CG>(a + a_box, map, col + 64, row, bar);
+    map = operand<R, R::b>(p, at, col, row);
+    (R::b_mn ? col : row) += half * bn;
+    tma_box<CG>(b, map, col, row, bar);
+    if (b_boxes == 2) tma_box<CG>(b + (R::b_mn ? kBoxBytes : bn * 128), map, col + 64, row, bar);
+}
+
+// A tile's loads, or its products' issue, block after block.
+template <class R, int CG, class Wait>
+__device__ __forceinline__ bool load_tile(const LinearParams &p, const LinearProduct &c, const Tile &t, uint32_t half,
+                                          uint32_t ring, uint32_t stage_bytes, uint32_t a_box, uint32_t full,
+                                          uint32_t empty, const Wait &wait, uint32_t &s, uint32_t &round, uint32_t &n)
+{
+    Place at[3] = {};
+    at[R::m] = locate<R, R::m>(p, c, t.m, kM * CG);
+    at[R::n] = locate<R, R::n>(p, c, t.n, p.bn);
+    Inner<R> k(p, c, t.kb0);
+    for (uint32_t kb = t.kb0; kb < t.kb1; ++kb, ++n, k.next(p)) {
+        if (!wait(empty + 8 * s, round ^ 1)) return false;
+        load_stage<R, CG>(p, at, k.at, half, ring + s * stage_bytes, a_box, full + 8 * s);
+        if (++s == p.stages) s = 0, round ^= 1;
+    }
+    return true;
+}
+
+template <class R, int CG, class Wait>
+__device__ __forceinline__ bool multiply_tile(const LinearParams &p, const LinearProduct &c, const Tile &t, uint32_t acc,
+                                              uint32_t ring, uint32_t stage_bytes, uint32_t a_box, uint32_t full,
+                                              uint32_t empty, const Wait &wait, uint32_t &s, uint32_t &round)
+{
+    const uint32_t desc = mma_desc(kM * CG, p.bn, R::a_mn, R::b_mn);
+    // from a K step of 16 to the next: 16 rows of an MN-major box; 32 bytes of a
+    // K-major one, and from its fourth to the next box
+    const uint32_t a_step = R::a_mn ? 16 * 128 : 32, a_next = R::a_mn ? 4 * a_step : a_box;
+    const uint32_t b_step = R::b_mn ? 16 * 128 : 32, b_next = R::b_mn ? 4 * b_step : p.bn / CG * 128;
+    Inner<R> k(p, c, t.kb0);
+    for (uint32_t kb = t.kb0; kb < t.kb1; ++kb, k.next(p)) {
+        if (!wait(full + 8 * s, round)) return false;
+        tc_fence_after();
+        const uint32_t at = ring + s * stage_bytes;
+        const uint64_t a = smem_desc(at, R::a_mn), b = smem_desc(at + 2 * a_box, R::b_mn);
+        const uint32_t steps = min((k.len - k.at.at + 15) / 16, kK / 16);
+#pragma unroll
+        for (uint32_t j = 0; j < kK / 16; ++j)
+            if (j < steps)
+                mma_bf16<CG>(acc, a + ((j / 4 * a_next + j % 4 * a_step) >> 4), b + ((j / 4 * b_next + j % 4 * b_step) >> 4),
+                             desc, kb != t.kb0 || j != 0);
+        mma_commit<CG>(empty + 8 * s);
+        if (++s == p.stages) s = 0, round ^= 1;
+    }
+    return true;
+}
+
+// ---- what follows a sum ------------------------------------------------------
+
+__device__ constexpr float kTail[7] = {0.143713042f, 0.141772494f, 0.139719009f, 0.0265500601f, 0.180952892f, -0.179763854f, 0.0470560379f};
+
+// The upper tail of the normal distribution at z >= 0, and exp(-z^2 / 2).  The tail
+// is exp(-z^2 / 2) t (c0 + c1 t + ... + c6 t^6) with t = 1 / (1 + 0.36 z), the c a
+// minimax fit of the relative error over t from 1 to z = 14: 1e-6 of itself off
+// everywhere, where 1 - erf would have nothing left far out.  (Own fit; erfcf in its
+// place is some 40 instructions, 64 times over.)
+__device__ __forceinline__ float normal_tail(float z, float &bell)
+{
+    bell = exp2_fast(z * z * -0.72134752044448170368f);
+    const float t = __fdividef(1.0f, fmaf(0.36f, z, 1.0f));
+    float s = kTail[6];
+#pragma unroll
+    for (int i = 5; i >= 0; --i) s = fmaf(s, t, kTail[i]);
+    return s * t * bell;
+}
+
+// The activation; a NaN stays one.
+template <int ACT>
+__device__ __forceinline__ float activate(float v)
+{
+    if (ACT == DT_ACT_RELU) return v < 0.0f ? 0.0f : v;
+    if (ACT == DT_ACT_SILU) return __fdividef(v, 1.0f + __expf(-v));
+    if (ACT == DT_ACT_GELU) {
+        float bell;
+        const float q = normal_tail(fabsf(v), bell);
+        return v * (v > 0.0f ? 1.0f - q : q);
+    }
+    return v;
+}
+
+// Its derivative.
+template <int ACT>
+__device__ __forceinline__ float slope(float v)
+{
+    if (ACT == DT_ACT_RELU) return v > 0.0f ? 1.0f : 0.0f;
+    if (ACT == DT_ACT_SILU) {
+        const float s = __fdividef(1.0f, 1.0f + __expf(-v));
+        return s * fmaf(v, 1.0f - s, 1.0f);
+    }
+    if (ACT == DT_ACT_GELU) {
+        float bell;
+        const float q = normal_tail(fabsf(v), bell);
+        return fmaf(v * 0.39894228040143267794f, bell, v > 0.0f ? 1.0f - q : q);
+    }
+    return 1.0f;
+}
+
+// N values at a time, so that the choice is made once.
+template <int N>
+__device__ __forceinline__ void activate(float (&v)[N], int act)
+{
+    auto all = [&](auto of) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = activate<decltype(of)::value>(v[j]);
+    };
+    if (act == DT_ACT_RELU) all(std::integral_constant<int, DT_ACT_RELU>{});
+    else if (act == DT_ACT_GELU) all(std::integral_constant<int, DT_ACT_GELU>{});
+    else if (act == DT_ACT_SILU) all(std::integral_constant<int, DT_ACT_SILU>{});
+}
+
+__device__ __forceinline__ float activated(float x, int act)
+{
+    float v[1] = {x};
+    activate(v, act);
+    return v[0];
+}
+
+// g[j] times the derivative at v[j].
+template <int N>
+__device__ __forceinline__ void times_slope(float (&g)[N], const float (&v)[N], int act)
+{
+    auto all = [&](auto of) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) g[j] *= slope<decltype(of)::value>(v[j]);
+    };
+    if (act == DT_ACT_RELU) all(std::integral_constant<int, DT_ACT_RELU>{});
+    else if (act == DT_ACT_GELU) all(std::integral_constant<int, DT_ACT_GELU>{});
+    else if (act == DT_ACT_SILU) all(std::integral_constant<int, DT_ACT_SILU>{});
+}
+
+// Where row `row` (of the piece at.piece) of a product's output begins, its first
+// element at column n.at of its tile; and the number of the buffer, by rank.
+struct OutRow {
+    uint16_t *out;
+    uint64_t offset;   // elements from the buffer's start
+    uint32_t rank;
+};
+
+template <class R>
+__device__ __forceinline__ OutRow out_row(const LinearParams &p, const LinearProduct &c, const Place &m, const Place &n,
+                                          uint32_t row)
+{
+    OutRow o;
+    uint64_t at;
+    if (R::m == kTokens && R::n == kDim) {       // a token's row on its rank
+        const uint32_t t = m.all + row;
+        uint32_t begin = 0;
+        o.rank = 0;
+        while ((int)o.rank + 1 < p.P && t >= p.row_end[o.rank]) begin = p.row_end[o.rank++];
+        at = t - begin;
+    } else if (R::m == kFeatures) {              // dW_r: a feature's row
+        o.rank = m.piece;
+        at = m.at + row;
+    } else {                                     // a rank's features of a token, or of a column of W_r
+        o.rank = n.piece;
+        at = (R::m == kTokens ? m.all : m.at) + row;
+    }
+    o.offset = at * (R::n == kDim ? p.dim : p.f_len[n.piece]) + n.at;
+    o.out = c.out[o.rank];
+    return o;
+}
+
+// A pointer of another lane.
+__device__ __forceinline__ uint16_t *lane_pointer(uint16_t *v, uint32_t lane)
+{
+    return reinterpret_cast<uint16_t *>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<uint64_t>(v), lane));
+}
+
+// A warp's rows between `buf` and memory, N elements of a row to a lane and as many
+// rows at a time as that leaves lanes for.  row: where this lane's row begins, NULL
+// where there is none.
+template <int N, bool STORE>
+__device__ __forceinline__ void move_rows(const LinearParams &p, unsigned char *buf, uint16_t *row, uint32_t cols, int buffer)
+{
+    using W = typename Words<N>::type;
+    (void)p;
+    constexpr uint32_t kLanes = 64 / N, kRows = 32 / kLanes;
+    const uint32_t lane = threadIdx.x & 31, e = lane % kLanes * N, first = lane / kLanes;
+    W v[8];
+#pragma unroll
+    for (uint32_t k0 = 0; k0 < 32; k0 += 8 * kRows) {
+        uint16_t *at[8];
+#pragma unroll
+        for (uint32_t k = 0; k < 8; ++k) {
+            const uint32_t r = k0 + k * kRows + first;
+            at[k] = lane_pointer(row, r);
+            const int of = __shfl_sync(0xFFFFFFFFu, buffer, r);
+            const bool there = at[k] && e < cols && LINEAR_OK(of, at[k] + e, 2 * N);
+            (void)of;
+            W *word = reinterpret_cast<W *>(buf + r * 128 + ((((e >> 3) ^ r) & 7) << 4) + (e & 7) * 2);
+            if constexpr (STORE) {
+                if (there) *reinterpret_cast<W *>(at[k] + e) = *word;
+            } else if (there) {
+                v[k] = *reinterpret_cast<const W *>(at[k] + e);
+            }
+            if (!there) at[k] = nullptr;
+        }
+        if constexpr (!STORE) {
+#pragma unroll
+            for (uint32_t k = 0; k < 8; ++k) {
+                const uint32_t r = k0 + k * kRows + first;
+                    if (at[k]) *reinterpret_cast<W *>(buf + r * 128 + ((((e >> 3) ^ r) & 7) << 4) + (e & 7) * 2) = v[k];
+            }
+        }
+    }
+}
+
+// The same for rows that begin at any element: a row at a time, every element on
+// its own.
+template <bool STORE>
+__device__ __forceinline__ void move_rows_odd(const LinearParams &p, unsigned char *buf, uint16_t *row, uint32_t cols, int buffer)
+{
+    (void)p;
+    const uint32_t lane = threadIdx.x & 31;
+#pragma unroll 8
+    for (uint32_t r = 0; r < 32; ++r) {
+        uint16_t *at = lane_pointer(row, r);
+        const int of = __shfl_sync(0xFFFFFFFFu, buffer, r);
+        (void)of;
+        if (!at) continue;
+#pragma unroll
+        for (uint32_t e = lane; e < 64; e += 32) {
+            uint16_t *word = reinterpret_cast<uint16_t *>(buf + r * 128 + ((((e >> 3) ^ r) & 7) << 4) + (e & 7) * 2);
+            if (e < cols && LINEAR_OK(of, at + e, 2)) {
+                if constexpr (STORE) at[e] = *word;
+                else *word = at[e];
+            }
+        }
+    }
+}
+
+template <bool STORE>
+__device__ __forceinline__ void move_rows(const LinearParams &p, unsigned char *buf, uint16_t *row, uint32_t cols,
+                                          uint32_t align, int buffer)
+{
+    if (align == 8) move_rows<8, STORE>(p, buf, row, cols, buffer);
+    else if (align == 4) move_rows<4, STORE>(p, buf, row, cols, buffer);
+    else if (align == 2) move_rows<2, STORE>(p, buf, row, cols, buffer);
+    else move_rows_odd<STORE>(p, buf, row, cols, buffer);
+}
+
+// This lane's row of 64 columns to memory by way of `buf`.
+__device__ __forceinline__ void store_rows(const LinearParams &p, unsigned char *buf, const float (&v)[64], uint16_t *row,
+                                           uint32_t cols, uint32_t align, int buffer)
+{
+    const uint32_t lane = threadIdx.x & 31;
+    __syncwarp();
+#pragma unroll
+    for (uint32_t c = 0; c < 8; ++c)
+        *out_chunk(buf, lane, c) = make_uint4(pack_bf16x2(v[8 * c], v[8 * c + 1]), pack_bf16x2(v[8 * c + 2], v[8 * c + 3]),
+                                              pack_bf16x2(v[8 * c + 4], v[8 * c + 5]), pack_bf16x2(v[8 * c + 6], v[8 * c + 7]));
+    __syncwarp();
+    move_rows<true>(p, buf, row, cols, align, buffer);
+}
+
+// 64 sums of this lane's row, whose columns begin at column `c` of the tile: bias,
+// residual, activation, and to memory.
+template <int KIND, class R>
+__device__ __forceinline__ void finish_row(const LinearParams &p, unsigned char *buf, unsigned char *biases, float (&v)[64],
+                                           const OutRow &o, bool there, const Place &n, uint32_t c, uint32_t cols,
+                                           uint32_t align)
+{
+    const uint32_t lane = threadIdx.x & 31;
+    if (!is_back(KIND) && p.biased) {
+        // one bias for all ranks' tokens, or each rank's own for its features
+        const uint32_t r = KIND == kGather ? n.piece : 0;
+        const uint16_t *from = p.bias[r] + n.at + c;
+        uint32_t w = 0;
+        if (2 * lane < cols && LINEAR_OK(kLinearBias + r, from + 2 * lane, 2)) w = from[2 * lane];
+        if (2 * lane + 1 < cols && LINEAR_OK(kLinearBias + r, from + 2 * lane + 1, 2)) w |= (uint32_t)from[2 * lane + 1] << 16;
+        __syncwarp();
+        reinterpret_cast<uint32_t *>(biases)[lane] = w;
+        __syncwarp();
+#pragma unroll
+        for (uint32_t j = 0; j < 8; ++j) {
+            const uint4 b = reinterpret_cast<const uint4 *>(biases)[j];
+            const uint32_t w4[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (uint32_t q = 0; q < 4; ++q) {
+                v[8 * j + 2 * q] += bf16_lo(w4[q]);
+                v[8 * j + 2 * q + 1] += bf16_hi(w4[q]);
+            }
+        }
+    }
+    if (KIND == kReduce && p.residuals) {
+        uint16_t *from = there ? const_cast<uint16_t *>(p.residual[o.rank]) + o.offset + c : nullptr;
+        __syncwarp();
+        move_rows<false>(p, buf, from, cols, align, kLinearResidual + o.rank);
+        __syncwarp();
+#pragma unroll
+        for (uint32_t j = 0; j < 8; ++j) {
+            const uint4 b = *out_chunk(buf, lane, j);
+            const uint32_t w4[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (uint32_t q = 0; q < 4; ++q) {
+                v[8 * j + 2 * q] += bf16_lo(w4[q]);
+                v[8 * j + 2 * q + 1] += bf16_hi(w4[q]);
+            }
+        }
+    }
+    if (KIND == kGather && p.keep)
+        store_rows(p, buf, v, there ? p.pre[o.rank] + o.offset + c : nullptr, cols, align, kLinearPre + o.rank);
+    if (KIND == kGather) activate(v, p.act);
+    constexpr int kOut = !is_back(KIND) ? kLinearY : R::k == kTokens ? kLinearDw : kLinearDx;
+    store_rows(p, buf, v, there ? o.out + o.offset + c : nullptr, cols, align, kOut + o.rank);
+}
+
+// One tile's accumulator, by a warp whose 32 rows begin at row `quad` of the tile
+// and which takes the columns [c0, c1).
+template <int KIND, class R>
+__device__ __forceinline__ void finish_tile(const LinearParams &p, const LinearProduct &c, const Tile &t, uint32_t acc,
+                                            uint32_t high, uint32_t quad, uint32_t c0, uint32_t c1, unsigned char *buf,
+                                            unsigned char *biases)
+{
+    const Place m = locate<R, R::m>(p, c, t.m, high), n = locate<R, R::n>(p, c, t.n, p.bn);
+    const uint32_t lane = threadIdx.x & 31, row = quad + lane;
+    const uint32_t rows = length<R, R::m>(p, m.piece) - m.at, cols = length<R, R::n>(p, n.piece) - n.at;
+    const bool there = row < rows;
+    if (c.splits > 1) {
+        // fp32 sums: 32 columns a step, through shared memory so that eight threads
+        // take a row's line
+        const uint64_t pitch = (uint64_t)c.nt * p.bn;
+        float *part = c.acc + (((uint64_t)t.split * c.mt + t.m) * high + quad) * pitch + t.n * p.bn;
+        const uint32_t q = lane & 7, first = lane >> 3;
+        for (uint32_t b = c0; b < c1 && b < cols; b += 32) {
+            float v[32];
+            tmem_load32(acc + b, v);
+            __syncwarp();
+#pragma unroll
+            for (uint32_t j = 0; j < 8; ++j)
+                *out_chunk(buf, lane, j) = make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
+                                                      __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3]));
+            __syncwarp();
+#pragma unroll
+            for (uint32_t j = 0; j < 8; ++j) {
+                const uint32_t r = first + 4 * j;
+                float4 *to = reinterpret_cast<float4 *>(part + r * pitch + b + 4 * q);
+                if (quad + r < rows && LINEAR_OK(kLinearWorkspace, to, 16))
+                    *to = *reinterpret_cast<const float4 *>(out_chunk(buf, r, q));
+            }
+        }
+        return;
+    }
+    const OutRow o = out_row<R>(p, c, m, n, there ? row : 0);
+    // the rows of a warp may lie on several ranks, whose buffers are aligned alike (the host says how)
+    const uint32_t align = c.align[R::m == kTokens && R::n == kDim ? 0 : o.rank];
+    for (uint32_t b = c0; b < c1 && b < cols; b += 64) {
+        float v[64];
+        tmem_load32(acc + b, *reinterpret_cast<float(*)[32]>(v));
+        tmem_load32(acc + b + 32, *reinterpret_cast<float(*)[32]>(v + 32));
+        finish_row<KIND, R>(p, buf, biases, v, o, there, n, b, min(cols - b, 64u), align);
+    }
+}
+
+template <int KIND, int CG>
+__global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(kTcThreads, 1)
+linear_kernel(const __grid_constant__ LinearParams p)
+{
+    using First = Roles<KIND, false>;
+    using Second = Roles<KIND, is_back(KIND)>;
+    constexpr bool kBack = is_back(KIND);
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
+    const uint32_t ring = smem_addr(smem);
+    unsigned char *out_buf = smem + kRingBytes;
+    unsigned char *ctl = out_buf + kOutBytes;
+    const uint32_t bars = smem_addr(ctl);
+    const uint32_t full = bars, empty = bars + 8 * kMaxStages;         // stage loaded; stage consumed
+    const uint32_t acc_full = bars + 16 * kMaxStages, acc_empty = acc_full + 16, drained = acc_empty + 16;
+    volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(ctl + kBarBytes - 8);
+    volatile uint32_t *gave_up = tmem_slot + 1;
+    static_assert(16 * kMaxStages + 40 <= kBarBytes - 8, "room for the barriers");
+    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t half = CG == 2 ? cluster_rank() : 0;                // of the tile's rows
+    const uint32_t worker = blockIdx.x / CG, workers = gridDim.x / CG;
+
+    DT_TL_BEGIN();
+    if (threadIdx.x == 0) {
+        for (uint32_t s = 0; s < p.stages; ++s) {
+            mbar_init(full + 8 * s, 1);
+            mbar_init(empty + 8 * s, 1);
+        }
+        for (uint32_t s = 0; s < 2; ++s) {
+            mbar_init(acc_full + 8 * s, 1);
+            mbar_init(acc_empty + 8 * s, kFinishWarps * CG);
+        }
+        mbar_init(drained, 1);
+        *gave_up = 0;
+        mbar_init_fence();
+    }
+    if (warp == kFinishWarps + 1) tmem_alloc<CG>(smem_addr(const_cast<uint32_t *>(tmem_slot)), kTmemColumns);
+    tc_fence_before();
+    __syncwarp();
+    if (CG == 2) cluster_sync();
+    else __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    Tile t;
+    pdl_begin();
+    DT_TL_WAITED();
+    const Waits wait{p.sink, gave_up};
+    const uint32_t a_box = a_box_bytes(kBack, p.rows_t), stage_bytes = 2 * a_box + p.bn / CG * 256;
+
+    if (warp == kFinishWarps) {
+        if (lane == 0) {
+            uint32_t n = 0, s = 0, round = 0;   // loads issued; the next one's stage and its parity
+            bool ok = true;
+            for (uint32_t k = 0; ok && next_tile<KIND>(p, worker, workers, k, t); ++k) {
+                if (kBack && t.second)
+                    ok = load_tile<Second, CG>(p, p.product[1], t, half, ring, stage_bytes, a_box, full, empty, wait, s,
+                                               round, n);
+                else
+                    ok = load_tile<First, CG>(p, p.product[0], t, half, ring, stage_bytes, a_box, full, empty, wait, s,
+                                              round, n);
+            }
+            // leave nothing in flight: the stages are consumed or, where that
+            // was given up, at least loaded (a pair's loads complete on its
+            // first CTA's barriers, and neither CTA leaves before the other)
+            for (uint32_t k = n > p.stages ? n - p.stages : 0; k < n; ++k) {
+                const uint32_t at = k % p.stages, parity = (k / p.stages) & 1;
+                if ((*gave_up || !wait(empty + 8 * at, parity)) && half == 0) wait(full + 8 * at, parity);
+            }
+        }
+        __syncwarp();
+    } else if (warp == kFinishWarps + 1) {
+        if (lane == 0 && half == 0) {
+            uint32_t s = 0, round = 0;
+            bool ok = true;
+            for (uint32_t u = 0; ok && next_tile<KIND>(p, worker, workers, u, t); ++u) {
+                const uint32_t acc = tmem + (u & 1) * 256;
+                if (!(ok = wait(acc_empty + 8 * (u & 1), ((u >> 1) & 1) ^ 1))) break;
+                tc_fence_after();
+                if (kBack && t.second)
+                    ok = multiply_tile<Second, CG>(p, p.product[1], t, acc, ring, stage_bytes, a_box, full, empty, wait, s,
+                                                   round);
+                else
+                    ok = multiply_tile<First, CG>(p, p.product[0], t, acc, ring, stage_bytes, a_box, full, empty, wait, s,
+                                                  round);
+                if (ok) mma_commit<CG>(acc_full + 8 * (u & 1));
+            }
+            if (!ok) {   // the MMAs issued so far end before tensor memory is freed
+                mma_commit<CG>(drained);
+                wait(drained, 0);
+            }
+        }
+        __syncwarp();
+    } else {
+        // Warps w and w + 4 read the same 32 rows (a warp reaches the tensor memory
+        // lanes of its number modulo 4) and take half of the columns each, at least 64.
+        const uint32_t width = p.bn >= 128 ? p.bn / 2 : p.bn;
+        const uint32_t c0 = (warp >> 2) * width, c1 = min(c0 + width, p.bn);
+        const uint32_t quad = half * kM + (warp & 3) * 32;   // first of this warp's rows in the tile
+        unsigned char *buf = out_buf + warp * kStageOut, *biases = ctl + kBarBytes + warp * 128;
+        for (uint32_t u = 0; next_tile<KIND>(p, worker, workers, u, t); ++u) {
+            const bool ok = wait(acc_full + 8 * (u & 1), (u >> 1) & 1);
+            tc_fence_after();
+            if (__any_sync(0xFFFFFFFFu, !ok)) break;
+            const uint32_t acc = tmem + (u & 1) * 256 + ((warp & 3) * 32 << 16);
+            if (kBack && t.second)
+                finish_tile<KIND, Second>(p, p.product[1], t, acc, kM * CG, quad, c0, c1, buf, biases);
+            else
+                finish_tile<KIND, First>(p, p.product[0], t, acc, kM * CG, quad, c0, c1, buf, biases);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (CG == 2) mbar_arrive_first(acc_empty + 8 * (u & 1));
+                else mbar_arrive(acc_empty + 8 * (u & 1));
+            }
+        }
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (CG == 2) cluster_sync();
+    else __syncthreads();
+    tc_fence_after();
+    if (warp == kFinishWarps + 1) tmem_free<CG>(tmem, kTmemColumns);
+    DT_TL_END_BLOCK(DT_TL_LINEAR);
+}
+
+// The sums of a product's splits into one, four columns a thread, and what follows
+// a sum.  A row of blocks to a row of the output.
+template <int KIND, bool SECOND>
+__global__ void __launch_bounds__(kThreads) linear_join_kernel(const __grid_constant__ LinearParams p, uint32_t high)
+{
+    using R = Roles<KIND, SECOND>;
+    DT_TL_BEGIN();
+    pdl_begin();
+    DT_TL_WAITED();
+    const LinearProduct &c = p.product[SECOND];
+    const uint32_t pitch = c.nt * p.bn, col = (blockIdx.x * kThreads + threadIdx.x) * 4;
+    if (col < pitch) {
+        const Place m = locate<R, R::m>(p, c, blockIdx.y / high, high), n = locate<R, R::n>(p, c, col / p.bn, p.bn);
+        const uint32_t row = blockIdx.y % high, rows = length<R, R::m>(p, m.piece) - m.at;
+        const uint32_t e = col % p.bn, cols = length<R, R::n>(p, n.piece) - n.at;
+        if (row < rows && e < cols) {
+            const float4 *from = reinterpret_cast<const float4 *>(c.acc + (uint64_t)blockIdx.y * pitch + col);
+            const uint64_t step = (uint64_t)c.mt * high * pitch / 4;
+            float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
+            for (uint32_t k = 0; k < c.splits; ++k)
+                if (LINEAR_OK(kLinearWorkspace, from + k * step, 16)) {
+                    const float4 f = from[k * step];
+                    v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
+                }
+            const OutRow o = out_row<R>(p, c, m, n, row);
+            constexpr int kOut = !is_back(KIND) ? kLinearY : SECOND ? kLinearDw : kLinearDx;
+            const uint32_t r = KIND == kGather ? n.piece : 0;
+#pragma unroll
+            for (uint32_t j = 0; j < 4; ++j) {
+                if (e + j >= cols) continue;
+                const uint64_t at = o.offset + e + j;
+                if (!is_back(KIND) && p.biased && LINEAR_OK(kLinearBias + r, p.bias[r] + n.at + e + j, 2))
+                    v[j] += bf16_to_f32(p.bias[r][n.at + e + j]);
+                if (KIND == kReduce && p.residuals && LINEAR_OK(kLinearResidual + o.rank, p.residual[o.rank] + at, 2))
+                    v[j] += bf16_to_f32(p.residual[o.rank][at]);
+                if (KIND == kGather && p.keep && LINEAR_OK(kLinearPre + o.rank, p.pre[o.rank] + at, 2))
+                    p.pre[o.rank][at] = f32_to_bf16(v[j]);
+                v[j] = KIND == kGather ? activated(v[j], p.act) : v[j];
+                if (LINEAR_OK(kOut + o.rank, o.out + at, 2)) o.out[at] = f32_to_bf16(v[j]);
+            }
+        }
+    }
+    DT_TL_END_BLOCK(DT_TL_LINEAR);
+}
+
+// A strip of 256 columns of a chunk of 64 rows to a block: 32 threads across, eight
+// columns each, and eight rows at a time.
+__global__ void __launch_bounds__(kThreads) linear_prep_kernel(const __grid_constant__ LinearPrep p)
+{
+    __shared__ float part[8][kPrepCols + 4];
+    DT_TL_BEGIN();
+    pdl_begin();
+    DT_TL_WAITED();
+    int k = 0;
+    while (k + 1 < p.jobs && blockIdx.x >= p.job[k].block_end) ++k;
+    const LinearPrepJob &job = p.job[k];
+    const uint32_t block = blockIdx.x - (k ? p.job[k - 1].block_end : 0);
+    const uint32_t strip = block % job.strips, chunk = block / job.strips;
+    const uint32_t t = threadIdx.x % 32, r0 = threadIdx.x / 32, e = strip * kPrepCols + t * 8;
+    const uint32_t n = e < job.cols ? min(job.cols - e, 8u) : 0;
+    const uint32_t end = min((chunk + 1) * kPrepRows, job.rows);
+    auto load = [&](const uint16_t *base, uint32_t row, int buffer, uint32_t (&w)[4]) {
+        (void)buffer;
+        const uint16_t *at = base + (uint64_t)row * job.cols + e;
+        w[0] = w[1] = w[2] = w[3] = 0;
+        if (n == 0 || !LINEAR_OK(buffer, at, 2 * n)) return;
+        if (n == 8 && (reinterpret_cast<uintptr_t>(at) & 15) == 0) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(at);
+            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+        } else {
+#pragma unroll
+            for (uint32_t j = 0; j < 8; ++j)
+                if (j < n) w[j / 2] |= (uint32_t)at[j] << (j & 1) * 16;
+        }
+    };
+    float sum[8] = {};
+#pragma unroll 2
+    for (uint32_t row = chunk * kPrepRows + r0; row < end; row += 8) {
+        uint32_t w[4];
+        load(job.src, row, job.src_buffer, w);
+        if (job.pre || job.sums) {
+            float g[8], z[8];
+#pragma unroll
+            for (uint32_t j = 0; j < 8; ++j) g[j] = j & 1 ? bf16_hi(w[j / 2]) : bf16_lo(w[j / 2]);
+            if (job.pre) {
+                uint32_t u[4];
+                load(job.pre, row, job.pre_buffer, u);
+#pragma unroll
+                for (uint32_t j = 0; j < 8; ++j) z[j] = j & 1 ? bf16_hi(u[j / 2]) : bf16_lo(u[j / 2]);
+                times_slope(g, z, p.act);
+#pragma unroll
+                for (uint32_t j = 0; j < 4; ++j) w[j] = pack_bf16x2(g[2 * j], g[2 * j + 1]);
+            }
+#pragma unroll
+            for (uint32_t j = 0; j < 8; ++j) sum[j] += g[j];
+        }
+        uint4 *to = reinterpret_cast<uint4 *>(job.dst + (uint64_t)row * job.pitch + e);
+        if (job.dst && e < job.pitch && LINEAR_OK(kLinearWorkspace, to, 16)) *to = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    if (job.sums) {
+#pragma unroll
+        for (uint32_t j = 0; j < 8; ++j) part[r0][t * 8 + j] = sum[j];
+        __syncthreads();
+        const uint32_t c = strip * kPrepCols + threadIdx.x;
+        float all = 0.0f;
+#pragma unroll
+        for (uint32_t r = 0; r < 8; ++r) all += part[r][threadIdx.x];
+        float *to = job.sums + (uint64_t)chunk * job.cols + c;
+        if (c < job.cols && LINEAR_OK(kLinearWorkspace, to, 4)) *to = all;
+    }
+    DT_TL_END_BLOCK(DT_TL_LINEAR);
+}
+
+// Column sums over the chunks, in a fixed order: 32 columns a block, chunks k, k + 8,
+// ... to a row of threads.
+__global__ void __launch_bounds__(kThreads) linear_sums_kernel(const __grid_constant__ LinearSums p)
+{
+    __shared__ float part[8][33];
+    DT_TL_BEGIN();
+    pdl_begin();
+    DT_TL_WAITED();
+    int k = 0;
+    while (k + 1 < p.n && blockIdx.x >= p.block_end[k]) ++k;
+    const uint32_t lane = threadIdx.x % 32, slice = threadIdx.x / 32, cols = p.cols[k];
+    const uint32_t c = (blockIdx.x - (k ? p.block_end[k - 1] : 0)) * 32 + lane;
+    float sum = 0.0f;
+    if (c < cols) {
+#pragma unroll 8
+        for (uint32_t i = slice; i < p.chunks; i += 8) {
+            const float *from = p.sums[k] + (uint64_t)i * cols + c;
+            if (LINEAR_OK(kLinearWorkspace, from, 4)) sum += *from;
+        }
+    }
+    part[slice][lane] = sum;
+    __syncthreads();
+    if (slice == 0 && c < cols) {
+#pragma unroll
+        for (uint32_t i = 1; i < 8; ++i) sum += part[i][lane];
+        if (LINEAR_OK(kLinearDb + k, p.out[k] + c, 2)) p.out[k][c] = f32_to_bf16(sum);
+    }
+    DT_TL_END_BLOCK(DT_TL_LINEAR);
+}
+
+template <int KIND, int CG>
+cudaError_t launch_kind(LinearParams &p, int device, cudaStream_t s)
+{
+    static std::atomic<uint64_t> ready{0};   // devices whose shared memory limit is set
+    const uint64_t bit = device < 64 ? 1ull << device : 0;
+    if (!(ready.load(std::memory_order_acquire) & bit) || !bit) {
+        const cudaError_t e = cudaFuncSetAttribute(linear_kernel<KIND, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   (int)kTcSmem);
+        if (e != cudaSuccess) return e;
+        ready.fetch_or(bit, std::memory_order_release);
+    }
+    p.stages = std::min(kMaxStages, kRingBytes / (2 * a_box_bytes(is_back(KIND), p.rows_t) + p.bn / CG * 256));
+    return launch_kernel(linear_kernel<KIND, CG>, dim3(p.workers * CG), dim3(kTcThreads), kTcSmem, s, false, p);
+}
+
+template <int KIND>
+cudaError_t launch_kind(LinearParams &p, bool pairs, int device, cudaStream_t s)
+{
+    return pairs ? launch_kind<KIND, 2>(p, device, s) : launch_kind<KIND, 1>(p, device, s);
+}
+
+template <int KIND, bool SECOND>
+cudaError_t launch_join(const LinearParams &p, uint32_t high, cudaStream_t s)
+{
+    const LinearProduct &c = p.product[SECOND];
+    return launch_kernel(linear_join_kernel<KIND, SECOND>, dim3((c.nt * p.bn / 4 + kThreads - 1) / kThreads, c.mt * high),
+                         dim3(kThreads), 0, s, false, p, high);
+}
+
+}  // namespace
+
+DT_TL_BINDER(bind_timeline_linear)
+
+uint32_t linear_workers(bool pairs, int device) { return (uint32_t)std::max(1, sm_count(device) / (pairs ? 2 : 1)); }
+
+// A finished tile costs a worker about a block of the inner axis more than its
+// products.
+constexpr uint32_t kTileCost = 1;
+
+cudaError_t launch_linear(LinearParams &p, LinearKind kind, bool pairs, int device, cudaStream_t s)
+{
+    const uint32_t W = linear_workers(pairs, device);
+    const LinearProduct &a = p.product[0], &b = p.product[1];
+    const uint32_t second = is_back(kind) ? b.tiles : 0;
+    p.workers = std::min(W, a.tiles + second);
+    p.rest = p.early = 0;
+    if (second && a.tiles % p.workers) {
+        p.rest = a.tiles % p.workers;
+        p.early = std::min((a.kblocks / a.splits + kTileCost) / (b.kblocks / b.splits + kTileCost), second / (p.workers - p.rest));
+    }
+    switch (kind) {
+    case kGather: return launch_kind<kGather>(p, pairs, device, s);
+    case kGatherBack: return launch_kind<kGatherBack>(p, pairs, device, s);
+    case kReduce: return launch_kind<kReduce>(p, pairs, device, s);
+    default: return launch_kind<kReduceBack>(p, pairs, device, s);
+    }
+}
+
+cudaError_t launch_linear_join(const LinearParams &p, LinearKind kind, int k, bool pairs, int device, cudaStream_t s)
+{
+    const uint32_t high = pairs ? 2 * kM : kM;
+    (void)device;
+    switch (kind) {
+    case kGather: return launch_join<kGather, false>(p, high, s);
+    case kGatherBack: return k ? launch_join<kGatherBack, true>(p, high, s) : launch_join<kGatherBack, false>(p, high, s);
+    case kReduce: return launch_join<kReduce, false>(p, high, s);
+    default: return k ? launch_join<kReduceBack, true>(p, high, s) : launch_join<kReduceBack, false>(p, high, s);
+    }
+}
+
+cudaError_t launch_linear_prep(LinearPrep &p, cudaStream_t s)
+{
+    return launch_kernel(linear_prep_kernel, dim3(p.job[p.jobs - 1].block_end), dim3(kThreads), 0, s, false, p);
+}
+
+cudaError_t launch_linear_sums(LinearSums &p, cudaStream_t s)
+{
+    return launch_kernel(linear_sums_kernel, dim3(p.block_end[p.n - 1]), dim3(kThreads), 0, s, false, p);
+}
+
+}  // namespace dt

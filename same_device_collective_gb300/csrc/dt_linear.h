@@ -1,0 +1,115 @@
+// Parameter blocks and launchers of the linear layers over the ranks.  Not part
+// of the C ABI.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "dt.h"
+#include "dt_internal.h"
+#include "dt_ops.h"
+
+namespace dt {
+
+// What a launch computes.  With X [n, d] the ranks' tokens, W_r and f_r rank r's
+// weights and features, G_r [n, f_r] and Y [n, d]:
+//   kGather      y_r = act(X W_r^T + b_r)               W_r [f_r, d]
+//   kGatherBack  dx = sum_r G_r W_r, dW_r = G_r^T X
+//   kReduce      y = sum_r H_r W_r^T + b (+ residual)   W_r [d, f_r]
+//   kReduceBack  dH_r = Y W_r, dW_r = Y^T H_r
+enum LinearKind : int { kGather, kGatherBack, kReduce, kReduceBack };
+
+// The three axes of these products: tokens, columns of a token, features.
+enum LinearAxis : int { kTokens, kDim, kFeatures };
+
+// Buffers, as bounds-checked builds number them: by rank from these on.
+enum LinearBuffer : int {
+    kLinearY, kLinearPre = DT_MAX_RANKS, kLinearDx = 2 * DT_MAX_RANKS, kLinearDw = 3 * DT_MAX_RANKS,
+    kLinearDb = 4 * DT_MAX_RANKS, kLinearBias = 5 * DT_MAX_RANKS, kLinearResidual = 6 * DT_MAX_RANKS,
+    kLinearX = 7 * DT_MAX_RANKS, kLinearW = 8 * DT_MAX_RANKS, kLinearDy = 9 * DT_MAX_RANKS,
+    kLinearWorkspace = 10 * DT_MAX_RANKS, kLinearBuffers
+};
+
+// One product of a launch: its tiles, splits of its inner axis, and outputs.
+struct LinearProduct {
+    uint32_t mt, nt, splits, tiles;    // tiles = mt * nt * splits
+    uint32_t kblocks;                  // blocks of 128 of the inner axis
+    uint32_t f_end[DT_MAX_RANKS];      // the ranks' features and tokens in tiles or blocks, as their axis is cut
+    uint32_t t_end[DT_MAX_RANKS];      // here, numbered through: rank r's end at [r]
+    uint16_t *out[DT_MAX_RANKS];
+    uint32_t align[DT_MAX_RANKS];      // elements that the rows of out[r] (and pre[r], residual[r]) are a multiple of: 1, 2, 4, 8
+    float *acc;                        // splits > 1: sums [splits][mt tiles' rows][nt tiles' columns]
+};
+
+struct LinearParams {
+    CUtensorMap tok[DT_MAX_RANKS];     // the ranks' tokens [t_len, dim] (one map when they are one matrix)
+    CUtensorMap feat[DT_MAX_RANKS];    // [tokens, f_len]
+    CUtensorMap w[DT_MAX_RANKS];       // [f_len, dim], or reducing [dim, f_len]
+    LinearProduct product[2];
+    uint32_t f_len[DT_MAX_RANKS];
+    uint32_t t_len[DT_MAX_RANKS], t_first[DT_MAX_RANKS];   // pieces of the token axis in `tok`
+    uint32_t row_end[DT_MAX_RANKS];    // the ranks' tokens, numbered through
+    int32_t P, t_pieces;
+    uint32_t tokens, dim;
+    uint32_t bn;                       // tile width: 64 or 128, of pairs 128 or 256
+    uint32_t stages, workers;
+    uint32_t rows_t, rows_w;           // of the maps' boxes
+    uint32_t rest, early;              // the order of both products' tiles (next_tile)
+    uint16_t *pre[DT_MAX_RANKS];
+    const uint16_t *bias[DT_MAX_RANKS];
+    const uint16_t *residual[DT_MAX_RANKS];
+    int32_t act;
+    int32_t keep, biased, residuals;   // pre, bias, residual are there
+    ErrorSink sink;
+#ifdef DT_BOUNDS
+    Extent extent[kLinearBuffers];
+#endif
+};
+
+// What goes before the products: rows laid out again at a pitch that TMA can
+// address, the gradient before the activation, and column sums for the bias'.
+struct LinearPrepJob {
+    const uint16_t *src;               // [rows, cols]
+    const uint16_t *pre;               // NULL, or what act'(.) is taken of and src multiplied by
+    uint16_t *dst;                     // NULL, or [rows, pitch]
+    float *sums;                       // NULL, or [chunks of rows][cols]
+    uint32_t rows, cols, pitch;
+    uint32_t strips;                   // of kPrepCols columns
+    uint32_t block_end;                // of the launch's blocks
+    int32_t src_buffer, pre_buffer;    // numbers of LinearBuffer
+};
+constexpr uint32_t kPrepCols = 256, kPrepRows = 64;
+constexpr int kPrepJobs = 3 * DT_MAX_RANKS;
+struct LinearPrep {
+    LinearPrepJob job[kPrepJobs];
+    int32_t jobs, act;
+    ErrorSink sink;
+#ifdef DT_BOUNDS
+    Extent extent[kLinearBuffers];
+#endif
+};
+
+// The bias' gradient: column sums over chunks of rows into one.
+struct LinearSums {
+    const float *sums[DT_MAX_RANKS];   // [chunks][cols]
+    uint16_t *out[DT_MAX_RANKS];
+    uint32_t cols[DT_MAX_RANKS], chunks;
+    uint32_t block_end[DT_MAX_RANKS];
+    int32_t n;
+    ErrorSink sink;
+#ifdef DT_BOUNDS
+    Extent extent[kLinearBuffers];
+#endif
+};
+
+cudaError_t launch_linear(LinearParams &p, LinearKind kind, bool pairs, int device, cudaStream_t s);
+// The splits' sums into one, of product k.
+cudaError_t launch_linear_join(const LinearParams &p, LinearKind kind, int k, bool pairs, int device, cudaStream_t s);
+cudaError_t launch_linear_prep(LinearPrep &p, cudaStream_t s);
+cudaError_t launch_linear_sums(LinearSums &p, cudaStream_t s);
+// CTAs, or pairs of them, that run at once.
+uint32_t linear_workers(bool pairs, int device);
+
+}  // namespace dt

@@ -39,9 +39,11 @@ DT_DEFAULT_BUCKET_CAP_BYTES = 25 << 20
 DT_BUILD_NVTX, DT_BUILD_TIMELINE, DT_BUILD_BOUNDS = 1, 2, 4
 BOUNDS_KERNELS = {1: "reduce", 2: "reduce_shift", 3: "copy_bulk", 4: "copy_vec", 5: "copy_edge",
                   6: "copy_shift", 7: "copy_2d", 8: "bucket", 9: "norm",
-                  10: "vocab"}
+                  10: "vocab", 11: "linear"}
 
 DTYPES = {"f32": DT_F32, "bf16": DT_BF16, "i32": DT_I32}
+DT_ACT_NONE, DT_ACT_RELU, DT_ACT_GELU, DT_ACT_SILU = range(4)
+ACTS = {"none": DT_ACT_NONE, "relu": DT_ACT_RELU, "gelu": DT_ACT_GELU, "silu": DT_ACT_SILU}
 OPS = {"sum": DT_SUM, "avg": DT_AVG, "max": DT_MAX, "min": DT_MIN,
        "sum_stepwise": DT_SUM_STEPWISE}
 
@@ -83,6 +85,14 @@ _SIGS = {
     "dt_vocab_loss_backward": ([_vp, _vp, _vpp, _szp, _sz, _vp, _vp, _vp, _sz, _sz, _i, _i, _i32, _vp,
                                 _vpp, _vp, _sz, _vp], _i),
     "dt_vocab_loss_workspace": ([_vp, _szp, _sz, _sz, _sz, _i, _i], _sz),
+    "dt_gather_linear": ([_vp, _vpp, _vpp, _vpp, _vpp, _vpp, _szp, _sz, _sz, _szp, _sz, _i, _i, _vp, _sz, _vp], _i),
+    "dt_gather_linear_backward": ([_vp, _vpp, _vpp, _vpp, _vpp, _vpp, _vpp, _vpp, _szp, _sz, _sz, _szp, _sz, _i, _i,
+                                   _vp, _sz, _vp], _i),
+    "dt_gather_linear_workspace": ([_vp, _szp, _sz, _sz, _szp, _sz, _i, _i], _sz),
+    "dt_linear_reduce": ([_vp, _vpp, _vpp, _vp, _vpp, _vpp, _szp, _sz, _sz, _szp, _sz, _i, _vp, _sz, _vp], _i),
+    "dt_linear_reduce_backward": ([_vp, _vpp, _vpp, _vpp, _vpp, _vpp, _vp, _szp, _sz, _sz, _szp, _sz, _i, _vp, _sz,
+                                   _vp], _i),
+    "dt_linear_reduce_workspace": ([_vp, _szp, _sz, _sz, _szp, _sz, _i, _i], _sz),
     "dt_replicate_to_shard": ([_vp, _i, _vpp, _vpp, ctypes.POINTER(_i), _sz, _sz, _vp], _i),
     "dt_all_gather_into_vec": ([_vp, _i, _vpp, _vpp, _szp, _sz, _sz, _vp], _i),
     "dt_all_to_all_2d": ([_vp, _i, _vpp, _vpp, _sz, _sz, _sz, _i, _i, _vp], _i),
@@ -111,7 +121,7 @@ TIMELINE_DTYPE = np.dtype([("grid", np.uint64), ("kind", np.uint32), ("block", n
                            ("t_waited", np.uint64), ("t_end", np.uint64)])
 TIMELINE_KINDS = {1: "reduce", 2: "reduce_shift", 3: "copy_bulk", 4: "copy_vec", 5: "copy_shift",
                   6: "copy_2d", 7: "bucket", 8: "bucket_barrier", 9: "barrier", 10: "mark",
-                  11: "norm", 12: "vocab"}
+                  11: "norm", 12: "vocab", 13: "linear"}
 
 
 class DtError(RuntimeError):
@@ -360,7 +370,7 @@ _TORCH_NAME = {DT_F32: "torch.float32", DT_BF16: "torch.bfloat16", DT_I32: "torc
 
 
 def _dense(code: int | None, *xs) -> None:
-    """The layer norm and loss calls describe dense buffers of given types, of which they get the
+    """The operators' calls describe dense buffers of given types, of which they get the
     address alone: refuse a tensor that is not contiguous, not of the type with this code (None: of
     any), or neither on a GPU nor pinned."""
     name = _TORCH_NAME.get(code)
@@ -468,6 +478,61 @@ def _m_vocab_loss_backward(g: int, hidden, weight: Sequence, vocab: Sequence | N
             _ptr(dhidden), _ptr_array(dweight), *_workspace(workspace), _stream(stream))
 
 
+def _m_gather_linear(g: int, x: Sequence, weight: Sequence, bias: Sequence | None, pre: Sequence | None,
+                     y: Sequence, rows: Sequence | None, rows_equal: int, dim: int, features: Sequence | None,
+                     features_equal: int, dtype, act, workspace, stream=None) -> tuple:
+    """y[r] = act(X weight[r].T + bias[r]) [n, features[r]], X the tokens x[r] [rows[r], dim] of all
+    ranks; bias or pre may be None.  act: "none", "relu", "gelu", "silu".  pre[r] receives what act is
+    taken of.  workspace: a device tensor of dt_gather_linear_workspace bytes."""
+    _ranks(g, x, weight, bias, pre, y, rows, features)
+    _dense(_checked(dtype, DT_BF16), x, weight, bias, pre, y)
+    _dense(None, workspace)
+    return (g, _ptr_array(x), _ptr_array(weight), _opt_ptr_array(bias), _opt_ptr_array(pre), _ptr_array(y),
+            _rows_array(rows), rows_equal, dim, _rows_array(features), features_equal, _code(DTYPES, dtype),
+            _code(ACTS, act), *_workspace(workspace), _stream(stream))
+
+
+def _m_gather_linear_backward(g: int, x: Sequence, weight: Sequence, pre: Sequence | None, dy: Sequence, dx: Sequence,
+                              dweight: Sequence, dbias: Sequence | None, rows: Sequence | None, rows_equal: int,
+                              dim: int, features: Sequence | None, features_equal: int, dtype, act, workspace,
+                              stream=None) -> tuple:
+    """The gradient of that layer: dx[r] [rows[r], dim], reduced over the ranks, dweight[r] and dbias[r]
+    (or None).  pre as dt_gather_linear wrote it (None for "none"); workspace: backward=True bytes."""
+    _ranks(g, x, weight, pre, dy, dx, dweight, dbias, rows, features)
+    _dense(_checked(dtype, DT_BF16), x, weight, pre, dy, dx, dweight, dbias)
+    _dense(None, workspace)
+    return (g, _ptr_array(x), _ptr_array(weight), _opt_ptr_array(pre), _ptr_array(dy), _ptr_array(dx),
+            _ptr_array(dweight), _opt_ptr_array(dbias), _rows_array(rows), rows_equal, dim, _rows_array(features),
+            features_equal, _code(DTYPES, dtype), _code(ACTS, act), *_workspace(workspace), _stream(stream))
+
+
+def _m_linear_reduce(g: int, x: Sequence, weight: Sequence, bias, residual: Sequence | None, y: Sequence,
+                     rows: Sequence | None, rows_equal: int, dim: int, features: Sequence | None, features_equal: int,
+                     dtype, workspace, stream=None) -> tuple:
+    """y[r] = rank r's rows of (sum over q of x[q] weight[q].T, plus bias) + residual[r]: x[q]
+    [n, features[q]], weight[q] [dim, features[q]]; bias [dim] or residual may be None.  workspace: a
+    device tensor of dt_linear_reduce_workspace bytes."""
+    _ranks(g, x, weight, residual, y, rows, features)
+    _dense(_checked(dtype, DT_BF16), x, weight, bias, residual, y)
+    _dense(None, workspace)
+    return (g, _ptr_array(x), _ptr_array(weight), _ptr(bias), _opt_ptr_array(residual), _ptr_array(y),
+            _rows_array(rows), rows_equal, dim, _rows_array(features), features_equal, _code(DTYPES, dtype),
+            *_workspace(workspace), _stream(stream))
+
+
+def _m_linear_reduce_backward(g: int, x: Sequence, weight: Sequence, dy: Sequence, dx: Sequence, dweight: Sequence,
+                              dbias, rows: Sequence | None, rows_equal: int, dim: int, features: Sequence | None,
+                              features_equal: int, dtype, workspace, stream=None) -> tuple:
+    """The gradient of that layer: dx[q] [n, features[q]], dweight[q] and dbias [dim] (or None), from the
+    ranks' dy[r] [rows[r], dim].  workspace: backward=True bytes."""
+    _ranks(g, x, weight, dy, dx, dweight, rows, features)
+    _dense(_checked(dtype, DT_BF16), x, weight, dy, dx, dweight, dbias)
+    _dense(None, workspace)
+    return (g, _ptr_array(x), _ptr_array(weight), _ptr_array(dy), _ptr_array(dx), _ptr_array(dweight), _ptr(dbias),
+            _rows_array(rows), rows_equal, dim, _rows_array(features), features_equal, _code(DTYPES, dtype),
+            *_workspace(workspace), _stream(stream))
+
+
 _MARSHAL: dict = {}
 
 
@@ -498,6 +563,10 @@ dt_layer_norm = _entry("dt_layer_norm", _m_layer_norm)
 dt_layer_norm_backward = _entry("dt_layer_norm_backward", _m_layer_norm_backward)
 dt_vocab_loss = _entry("dt_vocab_loss", _m_vocab_loss)
 dt_vocab_loss_backward = _entry("dt_vocab_loss_backward", _m_vocab_loss_backward)
+dt_gather_linear = _entry("dt_gather_linear", _m_gather_linear)
+dt_gather_linear_backward = _entry("dt_gather_linear_backward", _m_gather_linear_backward)
+dt_linear_reduce = _entry("dt_linear_reduce", _m_linear_reduce)
+dt_linear_reduce_backward = _entry("dt_linear_reduce_backward", _m_linear_reduce_backward)
 
 
 def dt_vocab_loss_workspace(g: int, vocab: Sequence | None, vocab_equal: int, tokens: int, dim: int,
@@ -507,6 +576,26 @@ def dt_vocab_loss_workspace(g: int, vocab: Sequence | None, vocab_equal: int, to
         _ranks(g, vocab)
     return int(_lib.dt_vocab_loss_workspace(g, _rows_array(vocab), vocab_equal, tokens, dim,
                                             _code(DTYPES, dtype), int(bool(backward))))
+
+
+def _linear_workspace(name: str, g: int, rows, rows_equal, dim, features, features_equal, dtype, backward) -> int:
+    _ranks(g, *(x for x in (rows, features) if x is not None))
+    return int(getattr(_lib, name)(g, _rows_array(rows), rows_equal, dim, _rows_array(features), features_equal,
+                                   _code(DTYPES, dtype), int(bool(backward))))
+
+
+def dt_gather_linear_workspace(g: int, rows: Sequence | None, rows_equal: int, dim: int, features: Sequence | None,
+                               features_equal: int, dtype, backward: bool) -> int:
+    """Workspace bytes of dt_gather_linear, or of its backward call (0: invalid argument)."""
+    return _linear_workspace("dt_gather_linear_workspace", g, rows, rows_equal, dim, features, features_equal, dtype,
+                             backward)
+
+
+def dt_linear_reduce_workspace(g: int, rows: Sequence | None, rows_equal: int, dim: int, features: Sequence | None,
+                               features_equal: int, dtype, backward: bool) -> int:
+    """Workspace bytes of dt_linear_reduce, or of its backward call (0: invalid argument)."""
+    return _linear_workspace("dt_linear_reduce_workspace", g, rows, rows_equal, dim, features, features_equal, dtype,
+                             backward)
 
 
 def dt_layer_norm_workspace(g: int, cols: int) -> int:
