@@ -516,6 +516,60 @@ size_t dt_linear_reduce_workspace(dt_group_t g, const size_t *rows, size_t rows_
                                   const size_t *features, size_t features_equal, int dtype,
                                   int backward);
 
+/* ---------------------------------------- residual norm, group-wide */
+
+/* What stands between two blocks, for every rank's rows at once: the norm of the
+ * block's output, its gate, the residual sum, and the norm before the next block.
+ * With rstd(v) = 1 / sqrt(mean(v^2) + eps) over a row (no mean is taken off):
+ *   h = branch * rstd(branch)       y = residual_scale * x + gate * post_weight * h
+ *   z = y * rstd(y) * pre_weight
+ * x[r], branch[r], y[r], z[r] are rank r's [rows[r], cols] of dtype (rows NULL:
+ * rows_equal rows each); a rank may have none.  post_weight, gate and pre_weight, each
+ * [cols] of weight_dtype or NULL (1), serve all ranks.  dtype and weight_dtype are
+ * DT_F32 or DT_BF16.  All sums are fp32, the second norm is of y before its rounding,
+ * and y and z are rounded once.  rstd_post and rstd_pre, float arrays of rows[r] for
+ * each rank (or NULL: not wanted), receive both reciprocals for the backward call.  y[r] may be x[r]
+ * and z[r] may be branch[r] (in place); otherwise no output may overlap another buffer.
+ * Pointers are multiples of their element size; rows that all start on 16-byte boundaries
+ * move as vectors.  cols is 1..2^24, residual_scale any finite number.  A NaN or an
+ * infinity in a row makes results of that row NaN, and no other's.  The same call gives
+ * the same bits. */
+dt_status dt_residual_norm(dt_group_t g, const void *const *x, const void *const *branch,
+                           const void *post_weight, const void *gate, const void *pre_weight,
+                           float residual_scale, void *const *y, void *const *z,
+                           float *const *rstd_post, float *const *rstd_pre, const size_t *rows,
+                           size_t rows_equal, size_t cols, float eps, int dtype, int weight_dtype,
+                           void *stream);
+
+/* The backward pass.  y is as the forward call wrote it, dy the gradient that reaches y
+ * from further on (NULL: none), dz that of z.  With n = y * rstd_pre, q = dz * pre_weight,
+ * h = branch * rstd_post, d = dy + rstd_pre * (q - n * mean(q * n)) and c = d * gate *
+ * post_weight:
+ *   dx[r]         = residual_scale * d; may be dy[r] (in place)
+ *   dbranch[r]    = rstd_post * (c - h * mean(c * h)); may be dz[r]
+ *   dpost_weight  = gate * the sum over every row of every rank of d * h
+ *   dgate         = post_weight * that sum
+ *   dpre_weight   = the sum over every row of every rank of dz * n
+ * the last three of weight_dtype, each may be NULL; op DT_SUM, or DT_AVG: divided by the
+ * number of ranks.  With no rows at all they are 0.
+ *   workspace     at least dt_residual_norm_workspace(g, cols) bytes of device memory,
+ *                 16-byte aligned, free for other use once `stream` has passed the call;
+ *                 NULL when none of the three is wanted
+ * Sums are fp32 in an order that depends on the GPU and the shapes only. */
+dt_status dt_residual_norm_backward(dt_group_t g, const void *const *branch, const void *const *y,
+                                    const void *const *dy, const void *const *dz,
+                                    const void *post_weight, const void *gate, const void *pre_weight,
+                                    float residual_scale, const float *const *rstd_post,
+                                    const float *const *rstd_pre, void *const *dx,
+                                    void *const *dbranch, void *dpost_weight, void *dgate,
+                                    void *dpre_weight, const size_t *rows, size_t rows_equal,
+                                    size_t cols, int dtype, int weight_dtype, int op, void *workspace,
+                                    size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of dt_residual_norm_backward for rows of cols elements, any number of
+ * them; 0 for an invalid argument. */
+size_t dt_residual_norm_workspace(dt_group_t g, size_t cols);
+
 /* ----------------------------------------------------------- async work */
 
 /* Asynchronous collectives, after the async mode of "通信与互联（05）" §四.3
@@ -589,6 +643,7 @@ dt_status dt_debug_barrier_expect(dt_group_t g, int extra, uint32_t timeout_ms, 
 #define DT_TL_NORM 11           /* layer norm, either pass, and the join of its weight gradients */
 #define DT_TL_VOCAB 12          /* vocabulary loss, either pass */
 #define DT_TL_LINEAR 13         /* linear layers over the ranks, either pass */
+#define DT_TL_RESIDUAL 14       /* residual norm, either pass, and the join of its weight gradients */
 typedef struct {
     uint64_t grid;       /* the launch's %gridid */
     uint32_t kind;       /* DT_TL_* */
@@ -651,6 +706,10 @@ dt_status dt_timeline_mark(void *stream, uint32_t tag);
  * 48 + r, dbias 64 + r, bias 80 + r, residual 96 + r, and those laid out again x 112 + r,
  * weight 128 + r, dy 144 + r; workspace 160.  (TMA's own loads stay in their maps.) */
 #define DT_BOUNDS_LINEAR 11
+/* Residual norm; buffers: branch r, x or y 16 + r, dz 32 + r, dy 48 + r, y or dx 64 + r, z
+ * or dbranch 80 + r, rstd_post 96 + r, rstd_pre 112 + r, post_weight 128, gate 129,
+ * pre_weight 130, their gradients 131 to 133, workspace 134. */
+#define DT_BOUNDS_RESIDUAL 12
 uint32_t dt_build_flags(void);
 
 #ifdef __cplusplus

@@ -27,6 +27,7 @@ enum BoundsKernel : int {
     kBoundsNorm = DT_BOUNDS_NORM,
     kBoundsVocab = DT_BOUNDS_VOCAB,
     kBoundsLinear = DT_BOUNDS_LINEAR,
+    kBoundsResidual = DT_BOUNDS_RESIDUAL,
 };
 
 #ifdef DT_BOUNDS

@@ -39,7 +39,7 @@ DT_DEFAULT_BUCKET_CAP_BYTES = 25 << 20
 DT_BUILD_NVTX, DT_BUILD_TIMELINE, DT_BUILD_BOUNDS = 1, 2, 4
 BOUNDS_KERNELS = {1: "reduce", 2: "reduce_shift", 3: "copy_bulk", 4: "copy_vec", 5: "copy_edge",
                   6: "copy_shift", 7: "copy_2d", 8: "bucket", 9: "norm",
-                  10: "vocab", 11: "linear"}
+                  10: "vocab", 11: "linear", 12: "residual"}
 
 DTYPES = {"f32": DT_F32, "bf16": DT_BF16, "i32": DT_I32}
 DT_ACT_NONE, DT_ACT_RELU, DT_ACT_GELU, DT_ACT_SILU = range(4)
@@ -93,6 +93,11 @@ _SIGS = {
     "dt_linear_reduce_backward": ([_vp, _vpp, _vpp, _vpp, _vpp, _vpp, _vp, _szp, _sz, _sz, _szp, _sz, _i, _vp, _sz,
                                    _vp], _i),
     "dt_linear_reduce_workspace": ([_vp, _szp, _sz, _sz, _szp, _sz, _i, _i], _sz),
+    "dt_residual_norm": ([_vp, _vpp, _vpp, _vp, _vp, _vp, _f, _vpp, _vpp, _vpp, _vpp, _szp, _sz, _sz, _f, _i, _i, _vp],
+                         _i),
+    "dt_residual_norm_backward": ([_vp, _vpp, _vpp, _vpp, _vpp, _vp, _vp, _vp, _f, _vpp, _vpp, _vpp, _vpp, _vp, _vp,
+                                   _vp, _szp, _sz, _sz, _i, _i, _i, _vp, _sz, _vp], _i),
+    "dt_residual_norm_workspace": ([_vp, _sz], _sz),
     "dt_replicate_to_shard": ([_vp, _i, _vpp, _vpp, ctypes.POINTER(_i), _sz, _sz, _vp], _i),
     "dt_all_gather_into_vec": ([_vp, _i, _vpp, _vpp, _szp, _sz, _sz, _vp], _i),
     "dt_all_to_all_2d": ([_vp, _i, _vpp, _vpp, _sz, _sz, _sz, _i, _i, _vp], _i),
@@ -121,7 +126,7 @@ TIMELINE_DTYPE = np.dtype([("grid", np.uint64), ("kind", np.uint32), ("block", n
                            ("t_waited", np.uint64), ("t_end", np.uint64)])
 TIMELINE_KINDS = {1: "reduce", 2: "reduce_shift", 3: "copy_bulk", 4: "copy_vec", 5: "copy_shift",
                   6: "copy_2d", 7: "bucket", 8: "bucket_barrier", 9: "barrier", 10: "mark",
-                  11: "norm", 12: "vocab", 13: "linear"}
+                  11: "norm", 12: "vocab", 13: "linear", 14: "residual"}
 
 
 class DtError(RuntimeError):
@@ -533,6 +538,41 @@ def _m_linear_reduce_backward(g: int, x: Sequence, weight: Sequence, dy: Sequenc
             *_workspace(workspace), _stream(stream))
 
 
+def _m_residual_norm(g: int, x: Sequence, branch: Sequence, post_weight, gate, pre_weight, residual_scale: float,
+                     y: Sequence, z: Sequence, rstd_post, rstd_pre, rows: Sequence | None, rows_equal: int, cols: int,
+                     eps: float, dtype, weight_dtype, stream=None) -> tuple:
+    """The norm of a block's output, its gate, the residual sum and the next block's norm, for every
+    rank's rows [rows[r], cols]: y = residual_scale * x + gate * post_weight * branch * rstd(branch),
+    z = y * rstd(y) * pre_weight.  The weights serve all ranks, each may be None; rstd_post and
+    rstd_pre, lists of f32 tensors or None, receive what dt_residual_norm_backward reads."""
+    _ranks(g, x, branch, y, z, rstd_post, rstd_pre, rows)
+    _dense(_checked(dtype), x, branch, y, z)
+    _dense(_checked(weight_dtype), post_weight, gate, pre_weight)
+    _dense(DT_F32, rstd_post, rstd_pre)
+    return (g, _ptr_array(x), _ptr_array(branch), _ptr(post_weight), _ptr(gate), _ptr(pre_weight), residual_scale,
+            _ptr_array(y), _ptr_array(z), _opt_ptr_array(rstd_post), _opt_ptr_array(rstd_pre), _rows_array(rows),
+            rows_equal, cols, eps, _code(DTYPES, dtype), _code(DTYPES, weight_dtype), _stream(stream))
+
+
+def _m_residual_norm_backward(g: int, branch: Sequence, y: Sequence, dy: Sequence | None, dz: Sequence, post_weight,
+                              gate, pre_weight, residual_scale: float, rstd_post: Sequence, rstd_pre: Sequence,
+                              dx: Sequence, dbranch: Sequence, dpost_weight, dgate, dpre_weight, rows: Sequence | None,
+                              rows_equal: int, cols: int, dtype, weight_dtype, op, workspace, stream=None) -> tuple:
+    """Backward pass: dx and dbranch per rank, the weights' gradients (each may be None) reduced over
+    every rank's rows (op "sum" or "avg").  dy, the gradient that reaches y from further on, may be
+    None.  workspace: a device tensor of dt_residual_norm_workspace(g, cols) bytes."""
+    _ranks(g, branch, y, dy, dz, rstd_post, rstd_pre, dx, dbranch, rows)
+    _dense(_checked(dtype), branch, y, dy, dz, dx, dbranch)
+    _dense(_checked(weight_dtype), post_weight, gate, pre_weight, dpost_weight, dgate, dpre_weight)
+    _dense(DT_F32, rstd_post, rstd_pre)
+    _dense(None, workspace)
+    return (g, _ptr_array(branch), _ptr_array(y), _opt_ptr_array(dy), _ptr_array(dz), _ptr(post_weight), _ptr(gate),
+            _ptr(pre_weight), residual_scale, _ptr_array(rstd_post), _ptr_array(rstd_pre), _ptr_array(dx),
+            _ptr_array(dbranch), _ptr(dpost_weight), _ptr(dgate), _ptr(dpre_weight), _rows_array(rows), rows_equal,
+            cols, _code(DTYPES, dtype), _code(DTYPES, weight_dtype), _code(OPS, op), *_workspace(workspace),
+            _stream(stream))
+
+
 _MARSHAL: dict = {}
 
 
@@ -567,6 +607,8 @@ dt_gather_linear = _entry("dt_gather_linear", _m_gather_linear)
 dt_gather_linear_backward = _entry("dt_gather_linear_backward", _m_gather_linear_backward)
 dt_linear_reduce = _entry("dt_linear_reduce", _m_linear_reduce)
 dt_linear_reduce_backward = _entry("dt_linear_reduce_backward", _m_linear_reduce_backward)
+dt_residual_norm = _entry("dt_residual_norm", _m_residual_norm)
+dt_residual_norm_backward = _entry("dt_residual_norm_backward", _m_residual_norm_backward)
 
 
 def dt_vocab_loss_workspace(g: int, vocab: Sequence | None, vocab_equal: int, tokens: int, dim: int,
@@ -596,6 +638,11 @@ def dt_linear_reduce_workspace(g: int, rows: Sequence | None, rows_equal: int, d
     """Workspace bytes of dt_linear_reduce, or of its backward call (0: invalid argument)."""
     return _linear_workspace("dt_linear_reduce_workspace", g, rows, rows_equal, dim, features, features_equal, dtype,
                              backward)
+
+
+def dt_residual_norm_workspace(g: int, cols: int) -> int:
+    """Workspace bytes of dt_residual_norm_backward (0: invalid argument)."""
+    return int(_lib.dt_residual_norm_workspace(g, cols))
 
 
 def dt_layer_norm_workspace(g: int, cols: int) -> int:
