@@ -271,6 +271,41 @@ void token_matrix(Call &c, const void *const *x, int buffer, float *sums)
     c.p.t_pieces = (int32_t)pieces;
 }
 
+// The forward products of few tokens.
+cudaError_t run_few(Call &c, const void *const *x, const void *const *w, cudaStream_t s)
+{
+    const Plan &v = c.v;
+    const dt::LinearParams &p = c.p;
+    dt::LinearFew f;
+    memset(&f, 0, sizeof f);
+    bool vec = true;
+    const bool gather = v.kind == dt::kGather;
+    for (int r = 0; r < c.g->P; ++r) {
+        f.x[r] = static_cast<const uint16_t *>(x[r]);
+        f.w[r] = static_cast<const uint16_t *>(w[r]);
+        if (v.f[r]) vec = vec && addressable(w[r], gather ? v.dim : v.f[r]);
+        if (gather ? v.n[r] : v.f[r]) vec = vec && addressable(x[r], gather ? v.dim : v.f[r]);
+        f.out[r] = p.product[0].out[r];
+        f.pre[r] = p.pre[r];
+        f.bias[r] = p.bias[r];
+        f.residual[r] = p.residual[r];
+        f.f_len[r] = p.f_len[r];
+        f.row_end[r] = p.row_end[r];
+    }
+    f.P = p.P;
+    f.tokens = p.tokens;
+    f.dim = p.dim;
+    f.act = p.act;
+    f.keep = p.keep;
+    f.biased = p.biased;
+    f.residuals = p.residuals;
+    f.sink = p.sink;
+#ifdef DT_BOUNDS
+    memcpy(f.extent, p.extent, sizeof f.extent);
+#endif
+    return dt::launch_linear_few(f, v.kind, vec, c.g->device, s);
+}
+
 // A matrix for each rank, [rows, cols]: the map that reads it in place, or laid out
 // again at `to`.
 cudaError_t rank_matrix(Call &c, CUtensorMap *map, const void *src, size_t rows, size_t cols, unsigned char *&to, int buffer,
@@ -398,6 +433,7 @@ dt_status dt_gather_linear(dt_group_t g, const void *const *x, const void *const
     }
     DeviceScope scope(g->device);
     if (!scope.ok) return DT_ERR_CUDA;
+    if (v.tokens <= dt::kFewTokens) return cuda_status(run_few(c, x, weight, static_cast<cudaStream_t>(stream)));
     token_matrix(c, x, dt::kLinearX, nullptr);
     cudaError_t e = matrices(c, nullptr, 0, false, weight);
     if (e == cudaSuccess) e = run(c, static_cast<cudaStream_t>(stream));
@@ -537,6 +573,7 @@ dt_status dt_linear_reduce(dt_group_t g, const void *const *x, const void *const
     c.p.product[0].align[0] = align;
     DeviceScope scope(g->device);
     if (!scope.ok) return DT_ERR_CUDA;
+    if (v.tokens <= dt::kFewTokens) return cuda_status(run_few(c, x, weight, static_cast<cudaStream_t>(stream)));
     c.pieces = 1;
     c.p.t_pieces = 1;
     c.p.t_len[0] = c.p.tokens;

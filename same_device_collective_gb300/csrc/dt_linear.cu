@@ -758,6 +758,174 @@ __global__ void __launch_bounds__(kThreads) linear_join_kernel(const __grid_cons
     DT_TL_END_BLOCK(DT_TL_LINEAR);
 }
 
+// ---- few tokens --------------------------------------------------------------
+
+// Forward products of up to 16 tokens, which the weights' way from memory bounds: 16
+// rows of W to a group of warps that split the inner axis, with the weights straight
+// from memory into the registers of mma.sync.m16n8k16 as its A, the tokens as its eight
+// or sixteen columns.  (A tile of tcgen05 would be 128 rows of tokens, nearly all
+// empty, and its way through shared and tensor memory is longer than the whole of a
+// small call.)  A lane takes eight consecutive elements of a row, in one load, as its
+// elements of two products: which of the inner axis' elements stand together in a
+// product is free as long as both operands agree.  The warps' sums are added in shared
+// memory, then those of the C CTAs of a cluster, which split the inner axis where there
+// are few rows, in a fixed order.
+constexpr uint32_t kFewRows = 16, kFewWarps = kThreads / 32;
+constexpr uint32_t kFewDepth = 128;                // of the inner axis, to a step of a warp
+
+__device__ __forceinline__ void mma_16x8x16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Elements [k, k + 8) of a row of `len`; NULL: zeros.  The vector's load is volatile
+// so that a step's loads all go out before its products (the compiler, left to itself,
+// keeps a third of them under way, in 44 registers).
+template <bool VEC>
+__device__ __forceinline__ void few_load(const LinearFew &p, const uint16_t *row, uint32_t k, uint32_t len, int buffer,
+                                         uint32_t (&w)[4])
+{
+    (void)p, (void)buffer;
+    w[0] = w[1] = w[2] = w[3] = 0;
+    if (!row || k >= len) return;
+    if (VEC) {   // len is a multiple of 8
+        if (!LINEAR_OK(buffer, row + k, 16)) return;
+        asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(row + k));
+    } else {
+#pragma unroll
+        for (uint32_t j = 0; j < 8; ++j)
+            if (k + j < len && LINEAR_OK(buffer, row + k + j, 2)) w[j / 2] |= (uint32_t)row[k + j] << (j & 1) * 16;
+    }
+}
+
+// A float of another CTA of the cluster's shared memory.
+__device__ __forceinline__ float cluster_load(const float *here, uint32_t rank)
+{
+    float v;
+    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
+                 : "=f"(v)
+                 : "r"(smem_addr(here)), "r"(rank)
+                 : "memory");
+    return v;
+}
+
+template <int KIND, int NT, bool VEC, int C>
+__global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kThreads) linear_few_kernel(const __grid_constant__ LinearFew p)
+{
+    __shared__ float sums[kFewWarps][NT * 8][kFewRows + 1];
+    DT_TL_BEGIN();
+    pdl_begin();
+    DT_TL_WAITED();
+    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+    const uint32_t groups = kFewWarps / p.k_warps, group = warp / p.k_warps;
+    const uint32_t part = C > 1 ? cluster_rank() : 0, block = blockIdx.x / C;
+    // the block's rows of W: of one rank's features, or of the columns of a token
+    uint32_t r = 0, begin = 0;
+    if (KIND == kGather)
+        while ((int)r + 1 < p.P && block >= p.block_end[r]) begin = p.block_end[r++];
+    const uint32_t first = (block - begin) * groups * kFewRows, rows = KIND == kGather ? p.f_len[r] : p.dim;
+    const uint32_t row = first + group * kFewRows + g;   // this lane's rows: this and the eighth after it
+    // the tokens that this lane loads, and their rank
+    const uint16_t *token[NT];
+    int of[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const uint32_t t = n * 8 + g;
+        token[n] = nullptr;
+        of[n] = 0;
+        if (KIND == kGather && t < p.tokens) {
+            uint32_t at = 0;
+            while (of[n] + 1 < p.P && t >= p.row_end[of[n]]) at = p.row_end[of[n]++];
+            token[n] = p.x[of[n]] + (uint64_t)(t - at) * p.dim;
+        }
+    }
+    float c[NT][4] = {};
+    const uint32_t step = p.k_warps * C, mine = part * p.k_warps + warp % p.k_warps;
+    // steps of 128 of the inner axis, numbered through the ranks' pieces where it is features
+    uint32_t i = mine;
+    for (uint32_t f = KIND == kGather ? r : 0; f < (KIND == kGather ? r + 1 : (uint32_t)p.P); ++f) {
+        const uint32_t len = KIND == kGather ? p.dim : p.f_len[f], steps = (len + kFewDepth - 1) / kFewDepth;
+        const uint16_t *w0 = row < rows ? p.w[f] + (uint64_t)row * len : nullptr;
+        const uint16_t *w1 = row + 8 < rows ? p.w[f] + (uint64_t)(row + 8) * len : nullptr;
+        if (KIND == kReduce) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) token[n] = n * 8 + g < p.tokens ? p.x[f] + (uint64_t)(n * 8 + g) * len : nullptr;
+        }
+        for (; i < steps; i += step) {
+            uint32_t a0[4][4], a1[4][4], b[NT][4][4];
+#pragma unroll
+            for (uint32_t j = 0; j < 4; ++j) {
+                const uint32_t k = i * kFewDepth + j * 32 + q * 8;
+                few_load<VEC>(p, w0, k, len, kLinearW + f, a0[j]);
+                few_load<VEC>(p, w1, k, len, kLinearW + f, a1[j]);
+            }
+#pragma unroll
+            for (uint32_t j = 0; j < 4; ++j)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    few_load<VEC>(p, token[n], i * kFewDepth + j * 32 + q * 8, len, kLinearX + (KIND == kGather ? of[n] : (int)f),
+                                  b[n][j]);
+#pragma unroll
+            for (uint32_t j = 0; j < 4; ++j)
+#pragma unroll
+                for (uint32_t h = 0; h < 2; ++h) {
+                    const uint32_t a[4] = {a0[j][2 * h], a1[j][2 * h], a0[j][2 * h + 1], a1[j][2 * h + 1]};
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) mma_16x8x16(c[n], a, b[n][j][2 * h], b[n][j][2 * h + 1]);
+                }
+        }
+        i -= steps;
+    }
+    // a lane holds rows g and g + 8 of tokens 2 q and 2 q + 1
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        sums[warp][n * 8 + 2 * q][g] = c[n][0];
+        sums[warp][n * 8 + 2 * q + 1][g] = c[n][1];
+        sums[warp][n * 8 + 2 * q][g + 8] = c[n][2];
+        sums[warp][n * 8 + 2 * q + 1][g + 8] = c[n][3];
+    }
+    __syncthreads();
+    if (C > 1 && p.k_warps > 1) {   // the warps' sums into the first of each group
+        for (uint32_t o = threadIdx.x; o < groups * p.tokens * kFewRows; o += kThreads) {
+            const uint32_t at = o % kFewRows, t = o / kFewRows % p.tokens, w = o / kFewRows / p.tokens * p.k_warps;
+            float v = sums[w][t][at];
+            for (uint32_t k = 1; k < p.k_warps; ++k) v += sums[w + k][t][at];
+            sums[w][t][at] = v;
+        }
+    }
+    if (C > 1) cluster_sync();
+    for (uint32_t o = part * kThreads + threadIdx.x; o < groups * p.tokens * kFewRows; o += kThreads * C) {
+        const uint32_t at = o % kFewRows, t = o / kFewRows % p.tokens, w = o / kFewRows / p.tokens, f = first + w * kFewRows + at;
+        if (f >= rows) continue;
+        float v[1] = {0.0f};
+        if (C > 1) {
+            for (uint32_t k = 0; k < C; ++k) v[0] += cluster_load(&sums[w * p.k_warps][t][at], k);
+        } else {
+            for (uint32_t k = 0; k < p.k_warps; ++k) v[0] += sums[w * p.k_warps + k][t][at];
+        }
+        if (KIND == kGather) {
+            const uint64_t to = (uint64_t)t * rows + f;
+            if (p.biased && LINEAR_OK(kLinearBias + r, p.bias[r] + f, 2)) v[0] += bf16_to_f32(p.bias[r][f]);
+            if (p.keep && LINEAR_OK(kLinearPre + r, p.pre[r] + to, 2)) p.pre[r][to] = f32_to_bf16(v[0]);
+            activate(v, p.act);
+            if (LINEAR_OK(kLinearY + r, p.out[r] + to, 2)) p.out[r][to] = f32_to_bf16(v[0]);
+        } else {
+            uint32_t rank = 0, begin_row = 0;
+            while ((int)rank + 1 < p.P && t >= p.row_end[rank]) begin_row = p.row_end[rank++];
+            const uint64_t to = (uint64_t)(t - begin_row) * p.dim + f;
+            if (p.biased && LINEAR_OK(kLinearBias, p.bias[0] + f, 2)) v[0] += bf16_to_f32(p.bias[0][f]);
+            if (p.residuals && LINEAR_OK(kLinearResidual + rank, p.residual[rank] + to, 2))
+                v[0] += bf16_to_f32(p.residual[rank][to]);
+            if (LINEAR_OK(kLinearY + rank, p.out[rank] + to, 2)) p.out[rank][to] = f32_to_bf16(v[0]);
+        }
+    }
+    if (C > 1) cluster_sync();   // no CTA leaves while another reads its sums
+    DT_TL_END_BLOCK(DT_TL_LINEAR);
+}
+
 // A strip of 256 columns of a chunk of 64 rows to a block: 32 threads across, eight
 // columns each, and eight rows at a time.
 __global__ void __launch_bounds__(kThreads) linear_prep_kernel(const __grid_constant__ LinearPrep p)
@@ -885,6 +1053,25 @@ cudaError_t launch_join(const LinearParams &p, uint32_t high, cudaStream_t s)
                          dim3(kThreads), 0, s, false, p, high);
 }
 
+template <int KIND, int NT, bool VEC>
+cudaError_t launch_few(const LinearFew &p, uint32_t ctas, cudaStream_t s)
+{
+    const dim3 grid(p.blocks * ctas), block(kThreads);
+    switch (ctas) {
+    case 8: return launch_kernel(linear_few_kernel<KIND, NT, VEC, 8>, grid, block, 0, s, false, p);
+    case 4: return launch_kernel(linear_few_kernel<KIND, NT, VEC, 4>, grid, block, 0, s, false, p);
+    case 2: return launch_kernel(linear_few_kernel<KIND, NT, VEC, 2>, grid, block, 0, s, false, p);
+    default: return launch_kernel(linear_few_kernel<KIND, NT, VEC, 1>, grid, block, 0, s, false, p);
+    }
+}
+
+template <int KIND>
+cudaError_t launch_few(const LinearFew &p, bool vec, uint32_t ctas, cudaStream_t s)
+{
+    if (p.tokens <= 8) return vec ? launch_few<KIND, 1, true>(p, ctas, s) : launch_few<KIND, 1, false>(p, ctas, s);
+    return vec ? launch_few<KIND, 2, true>(p, ctas, s) : launch_few<KIND, 2, false>(p, ctas, s);
+}
+
 }  // namespace
 
 DT_TL_BINDER(bind_timeline_linear)
@@ -924,6 +1111,29 @@ cudaError_t launch_linear_join(const LinearParams &p, LinearKind kind, int k, bo
     case kReduce: return launch_join<kReduce, false>(p, high, s);
     default: return k ? launch_join<kReduceBack, true>(p, high, s) : launch_join<kReduceBack, false>(p, high, s);
     }
+}
+
+// Warps and CTAs that share a row of W: two steps of the inner axis to a warp at least,
+// and as many CTAs as give the SMs two each.
+cudaError_t launch_linear_few(LinearFew &p, LinearKind kind, bool vec, int device, cudaStream_t s)
+{
+    uint64_t steps = 0, rows = 0;
+    for (int r = 0; r < p.P; ++r) {
+        if (kind == kGather) rows += (p.f_len[r] + kFewRows - 1) / kFewRows;
+        else steps += (p.f_len[r] + kFewDepth - 1) / kFewDepth;
+    }
+    if (kind == kGather) steps = (p.dim + kFewDepth - 1) / kFewDepth;
+    else rows = (p.dim + kFewRows - 1) / kFewRows;
+    p.k_warps = 1;
+    while (p.k_warps < kFewWarps && p.k_warps * 2 <= steps) p.k_warps *= 2;
+    const uint32_t groups = kFewWarps / p.k_warps;
+    p.blocks = 0;
+    for (int r = 0; r < p.P; ++r)
+        p.block_end[r] = p.blocks += kind == kGather ? (p.f_len[r] + groups * kFewRows - 1) / (groups * kFewRows) : 0;
+    if (kind == kReduce) p.blocks = (uint32_t)((rows + groups - 1) / groups);
+    uint32_t ctas = 1;
+    while (ctas < 8 && p.blocks * ctas < 2u * sm_count(device) && (uint64_t)ctas * 4 * p.k_warps <= steps) ctas *= 2;
+    return kind == kGather ? launch_few<kGather>(p, vec, ctas, s) : launch_few<kReduce>(p, vec, ctas, s);
 }
 
 cudaError_t launch_linear_prep(LinearPrep &p, cudaStream_t s)

@@ -104,9 +104,30 @@ struct LinearSums {
 #endif
 };
 
+// Forward products of few tokens (linear_few_kernel).
+struct LinearFew {
+    const uint16_t *x[DT_MAX_RANKS];   // gathering: the ranks' tokens; reducing: the ranks' features
+    const uint16_t *w[DT_MAX_RANKS];
+    uint16_t *out[DT_MAX_RANKS], *pre[DT_MAX_RANKS];
+    const uint16_t *bias[DT_MAX_RANKS], *residual[DT_MAX_RANKS];
+    uint32_t f_len[DT_MAX_RANKS], row_end[DT_MAX_RANKS];
+    uint32_t block_end[DT_MAX_RANKS];  // gathering: blocks of each rank's features, numbered through
+    int32_t P;
+    uint32_t tokens, dim, blocks;
+    uint32_t k_warps;                  // warps of a block that share its rows' inner axis: 1, 2, 4 or 8
+    int32_t act, keep, biased, residuals;
+    ErrorSink sink;
+#ifdef DT_BOUNDS
+    Extent extent[kLinearBuffers];
+#endif
+};
+constexpr uint32_t kFewTokens = 16;
+
 cudaError_t launch_linear(LinearParams &p, LinearKind kind, bool pairs, int device, cudaStream_t s);
 // The splits' sums into one, of product k.
 cudaError_t launch_linear_join(const LinearParams &p, LinearKind kind, int k, bool pairs, int device, cudaStream_t s);
+// vec: every row of x and w starts on a 16-byte boundary.
+cudaError_t launch_linear_few(LinearFew &p, LinearKind kind, bool vec, int device, cudaStream_t s);
 cudaError_t launch_linear_prep(LinearPrep &p, cudaStream_t s);
 cudaError_t launch_linear_sums(LinearSums &p, cudaStream_t s);
 // CTAs, or pairs of them, that run at once.
