@@ -56,34 +56,63 @@ struct Cut {
     uint64_t acc_bytes(const Plan &v, int k) const { return splits[k] > 1 ? splits[k] * mt[k] * v.high * nt[k] * bn * 4 : 0; }
 };
 
-bool cut(const dt_group *g, const Plan &v, bool pieces, Cut &c)
+// What a launch takes, in microseconds, as far as its cut decides it: 16 of the inner
+// axis take the tensor cores 128 cycles whatever a tile's width (measured from 64 to 256
+// columns: reading 128 rows of A bounds it), a tile costs a microsecond beside that, and
+// splits cost a second launch and their sums' way to L2 and back.
+constexpr double kUsPer64 = 0.29, kUsTile = 1.0, kUsJoin = 3.0, kJoinBytesPerUs = 5e6;
+
+double join_cost(const Plan &v, const Cut &c)
+{
+    double us = 0.0;
+    for (int k = 0; k < 2; ++k)
+        if (c.splits[k] > 1) us += kUsJoin + 2.0 * c.acc_bytes(v, k) / kJoinBytesPerUs;
+    return us;
+}
+
+bool cut(const dt_group *g, const Plan &v, bool pieces, Cut &best)
 {
     const bool b = back(v.kind);
-    const uint64_t workers = dt::linear_workers(v.pairs, g->device), wide = v.pairs ? 256 : 128;
-    // the rows' axis of forward products is the tokens, which reducing are never in pieces
-    c.mt[0] = token_tiles(v, pieces && (v.kind == dt::kGather || v.kind == dt::kReduceBack), v.high);
+    const uint64_t workers = dt::linear_workers(v.pairs, g->device), depth = dt::linear_depth(b);
     const bool n_features = v.kind == dt::kGather || v.kind == dt::kReduceBack;
-    auto across = [&](uint64_t bn) { return n_features ? feature_tiles(v, bn) : tiles_of(v.dim, bn); };
-    // the narrower tile where it leaves the workers less to do one after the other; a
-    // tile costs about 64 columns more than it has
-    auto cost = [&](uint64_t bn) { return tiles_of(c.mt[0] * across(bn), workers) * (bn + 64); };
-    c.bn = (uint32_t)(!b && cost(wide / 2) < cost(wide) ? wide / 2 : wide);
-    c.nt[0] = across(c.bn);
-    c.kblocks[0] = n_features ? tiles_of(v.dim, 128) : feature_tiles(v, 128);
+    const double block_us = kUsPer64 * depth / 64;
+    Cut c;
+    // the rows' axis of forward products is the tokens, which reducing are never in pieces
+    c.mt[0] = token_tiles(v, pieces && n_features, v.high);
+    c.kblocks[0] = n_features ? tiles_of(v.dim, depth) : feature_tiles(v, depth);
     c.mt[1] = c.nt[1] = c.kblocks[1] = 0;
-    c.splits[0] = c.splits[1] = 1;
     if (b) {
         c.mt[1] = gathers(v.kind) ? feature_tiles(v, v.high) : tiles_of(v.dim, v.high);
-        c.nt[1] = c.nt[0];
-        c.kblocks[1] = token_tiles(v, pieces, 128);
+        c.kblocks[1] = token_tiles(v, pieces, depth);
     }
-    uint64_t work = 0;
-    for (int k = 0; k < 2; ++k) {
-        if (c.mt[k] * c.nt[k] > 0x7FFFFFFF / workers) return false;   // tiles are counted in 32 bits
-        work += c.mt[k] * c.nt[k] * c.kblocks[k];
+    double least = 1e300;
+    for (uint32_t bn = b && !v.pairs ? 128 : 256; bn >= 64; bn -= b ? 64 : 32) {
+        c.bn = bn;
+        c.nt[0] = n_features ? feature_tiles(v, bn) : tiles_of(v.dim, bn);
+        if (b) c.nt[1] = c.nt[0];
+        for (int k = 0; k < 2; ++k)
+            if (c.mt[k] * c.nt[k] > 0x7FFFFFFF / workers) return false;   // tiles are counted in 32 bits
+        const uint64_t most[2] = {std::max<uint64_t>(1, std::min<uint64_t>(16, c.kblocks[0] * depth / 512)),
+                                  std::max<uint64_t>(1, std::min<uint64_t>(16, c.kblocks[1] * depth / 512))};
+        for (c.splits[0] = 1; c.splits[0] <= most[0]; ++c.splits[0])
+            for (c.splits[1] = 1; c.splits[1] <= most[1]; ++c.splits[1]) {
+                double unit[2], longest = 0.0, all = 0.0;
+                uint64_t units = 0;
+                for (int k = 0; k < (b ? 2 : 1); ++k) {
+                    const uint64_t n = c.mt[k] * c.nt[k] * c.splits[k];
+                    unit[k] = tiles_of(c.kblocks[k], c.splits[k]) * block_us + kUsTile;
+                    longest = std::max(longest, unit[k]);
+                    all += n * unit[k];
+                    units += n;
+                }
+                // forward in whole waves; backward the second product's tiles fill the
+                // first one's last wave
+                const double us = (b ? std::max(all / workers, longest) : tiles_of(units, workers) * unit[0]) + join_cost(v, c);
+                if (us >= least) continue;
+                least = us;
+                best = c;
+            }
     }
-    for (int k = 0; k < (b ? 2 : 1); ++k)
-        if (work) c.splits[k] = std::max<uint64_t>(1, std::min(c.kblocks[k] * workers / work, c.kblocks[k] / 4));
     return true;
 }
 
@@ -132,6 +161,16 @@ size_t workspace_bytes_of(dt_group_t g, LinearKind fwd, const size_t *rows, size
     const LinearKind kind = !backward ? fwd : fwd == dt::kGather ? dt::kGatherBack : dt::kReduceBack;
     if (!g || dtype != DT_BF16 || !plan(g, kind, rows, rows_equal, dim, features, features_equal, v)) return 0;
     return (size_t)v.bytes;
+}
+
+// Whether the bias' gradient is summed down all rows by the warps beside the products, or
+// its rows are summed in chunks before them: a warp's loads of 32 rows of 32 columns are
+// about a microsecond under way, which should hide behind the products.
+bool sums_beside(const dt_group *g, const Plan &v)
+{
+    const uint64_t cols = gathers(v.kind) ? v.features : v.dim, warps = dt::linear_workers(v.pairs, g->device) * (v.pairs ? 4 : 2);
+    const double walk = (double)tiles_of(v.tokens, 32) * tiles_of(tiles_of(cols, 32), warps);
+    return walk <= 4.0 + 4.0 * v.tokens * v.dim * v.features / 1.6e9;
 }
 
 // A call on its way: its plan, its buffers, and what goes before its products.
@@ -357,8 +396,7 @@ cudaError_t matrices(Call &c, const void *const *feat, int feat_buffer, bool wri
         q.acc = reinterpret_cast<float *>(c.ws + v.acc[k]);
         // the size of a tile or block along the features and the tokens in this product
         const bool n_features = v.kind == dt::kGather || v.kind == dt::kReduceBack;
-        const uint64_t fs = n_features ? t.bn : k ? v.high : 128;
-        const uint64_t ts = k ? 128 : v.high;
+        const uint64_t depth = dt::linear_depth(b), fs = n_features ? t.bn : k ? v.high : depth, ts = k ? depth : v.high;
         uint32_t end = 0;
         for (int r = 0; r < c.g->P; ++r) q.f_end[r] = end += (uint32_t)tiles_of(v.f[r], fs);
         end = 0;
@@ -495,34 +533,29 @@ dt_status dt_gather_linear_backward(dt_group_t g, const void *const *x, const vo
     bool written = act != DT_ACT_NONE;
     for (int r = 0; r < g->P; ++r)
         if (v.f[r] && !addressable(dy[r], v.f[r])) written = true;
-    dt::LinearSums sums;
-    memset(&sums, 0, sizeof sums);
+    // the bias' gradient: from dy, or from sums over chunks of the rows
+    dt::LinearSums &sums = c.p.sums;
+    const bool beside = !pre && sums_beside(g, v);
     float *part = reinterpret_cast<float *>(c.ws + v.sums);
     unsigned char *to = c.ws + v.feat;
     for (int r = 0; r < g->P; ++r) {
         const uint64_t pitch = up(v.f[r], 8);
-        if (written || dbias)
-            add_job(c, dy[r], pre ? pre[r] : nullptr, written ? to : nullptr, dbias ? part : nullptr, v.tokens, v.f[r], pitch,
-                    dt::kLinearDy + r, dt::kLinearPre + r);
+        if (written || (dbias && !beside))
+            add_job(c, dy[r], pre ? pre[r] : nullptr, written ? to : nullptr, dbias && !beside ? part : nullptr, v.tokens, v.f[r],
+                    pitch, dt::kLinearDy + r, dt::kLinearPre + r);
         to += v.tokens * pitch * 2;
-        if (dbias) {
-            sums.sums[r] = part;
-            sums.out[r] = static_cast<uint16_t *>(dbias[r]);
-            sums.cols[r] = (uint32_t)v.f[r];
-            sums.block_end[r] = (r ? sums.block_end[r - 1] : 0) + (uint32_t)tiles_of(v.f[r], 32);
-            dt::set_extent(sums, dt::kLinearDb + r, dbias[r], v.f[r] * 2, true);
-            part += v.chunks * v.f[r];
-        }
+        if (!dbias) continue;
+        sums.src[r] = beside ? dy[r] : part;
+        sums.rows[r] = beside ? (uint32_t)v.tokens : (uint32_t)v.chunks;
+        sums.cols[r] = (uint32_t)v.f[r];
+        sums.out[r] = static_cast<uint16_t *>(dbias[r]);
+        sums.group_end[r] = sums.groups += (uint32_t)tiles_of(v.f[r], 32);
+        part += v.chunks * v.f[r];
     }
+    sums.n = sums.sources = g->P;
+    sums.f32 = !beside;
     cudaError_t e = matrices(c, dy, dt::kLinearDy, written, weight);
     if (e == cudaSuccess) e = run(c, s);
-    if (e == cudaSuccess && dbias) {
-        sums.n = g->P;
-        sums.chunks = (uint32_t)v.chunks;
-        sums.sink = c.p.sink;
-        workspace_extent(sums, c);
-        e = dt::launch_linear_sums(sums, s);
-    }
     return cuda_status(e);
 }
 
@@ -607,6 +640,7 @@ dt_status dt_linear_reduce_backward(dt_group_t g, const void *const *x, const vo
     if ((st = take_ranks(c, dweight, d, v.f, 0, true, dt::kLinearDw)) != DT_OK) return st;
     if (!multiple(dbias, 2)) return DT_ERR_INVALID;
     c.b.write(dbias, dim * 2);
+    dt::set_extent(c.p, dt::kLinearDb, dbias, dim * 2, true);
     if (c.b.clash()) return DT_ERR_INVALID;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     DeviceScope scope(g->device);
@@ -623,24 +657,27 @@ dt_status dt_linear_reduce_backward(dt_group_t g, const void *const *x, const vo
         c.p.product[0].align[r] = alignment(8, dx[r], v.f[r]);
         c.p.product[1].align[r] = alignment(8, dweight[r], v.f[r]);
     }
+    // the bias' gradient: from the ranks' dy, or from sums over chunks of the rows
     float *part = reinterpret_cast<float *>(c.ws + v.sums);
-    token_matrix(c, dy, dt::kLinearDy, dbias ? part : nullptr);
-    cudaError_t e = matrices(c, x, dt::kLinearX, false, weight);
-    if (e == cudaSuccess) e = run(c, s);
-    if (e == cudaSuccess && dbias) {
-        dt::LinearSums sums;
-        memset(&sums, 0, sizeof sums);
-        sums.sums[0] = part;
+    const bool beside = sums_beside(g, v);
+    token_matrix(c, dy, dt::kLinearDy, dbias && !beside ? part : nullptr);
+    if (dbias) {
+        dt::LinearSums &sums = c.p.sums;
         sums.out[0] = static_cast<uint16_t *>(dbias);
         sums.cols[0] = (uint32_t)dim;
-        sums.block_end[0] = (uint32_t)tiles_of(dim, 32);
-        sums.n = 1;
-        sums.chunks = (uint32_t)v.chunks;
-        sums.sink = c.p.sink;
-        workspace_extent(sums, c);
-        dt::set_extent(sums, dt::kLinearDb, dbias, dim * 2, true);
-        e = dt::launch_linear_sums(sums, s);
+        sums.group_end[0] = sums.groups = (uint32_t)tiles_of(dim, 32);
+        sums.n = sums.stacked = 1;
+        sums.sources = beside ? g->P : 1;
+        sums.f32 = !beside;
+        sums.src[0] = part;
+        sums.rows[0] = (uint32_t)v.chunks;
+        for (int r = 0; r < g->P && beside; ++r) {
+            sums.src[r] = dy[r];
+            sums.rows[r] = (uint32_t)v.n[r];
+        }
     }
+    cudaError_t e = matrices(c, x, dt::kLinearX, false, weight);
+    if (e == cudaSuccess) e = run(c, s);
     return cuda_status(e);
 }
 

@@ -45,18 +45,24 @@ namespace dt {
 namespace {
 
 constexpr uint32_t kM = 128;                       // rows of a tile in a CTA
-constexpr uint32_t kK = 128;                       // depth of a stage
-constexpr uint32_t kRingBytes = 192 * 1024;        // three stages of 128 rows and columns of A and B
-constexpr uint32_t kMaxStages = 8;
+constexpr uint32_t kRingBytes = 192 * 1024;        // three or six stages of 128 rows and columns of A and B
+constexpr uint32_t kMaxStages = 16;
 constexpr uint32_t kTmemColumns = 512;             // two accumulators of 128 x 256 fp32
-constexpr uint32_t kFinishWarps = 8;
-constexpr int kTcThreads = (kFinishWarps + 2) * 32;
-constexpr uint32_t kStageOut = 4096;               // a finishing warp's 32 rows x 128 bytes
+// Finishing warps (16 take as long), one for TMA, one for the products, and backward two
+// for the bias' gradient.
+constexpr uint32_t kFinishWarps = 8, kSumWarps = 2;
+__host__ __device__ constexpr int tc_threads(bool back) { return (kFinishWarps + 2 + (back ? kSumWarps : 0)) * 32; }
+constexpr uint32_t kColumnGroups = kFinishWarps / 4;
+constexpr uint32_t kStep = 32;                     // columns that a finishing warp takes at a time
+constexpr uint32_t kStageOut = 32 * kStep * 2;     // its 32 rows of them in bf16
 constexpr uint32_t kOutBytes = kFinishWarps * kStageOut;
-constexpr uint32_t kBarBytes = 256, kBiasBytes = kFinishWarps * 128;
+constexpr uint32_t kBarBytes = 384, kBiasBytes = kFinishWarps * kStep * 2;
 constexpr size_t kTcSmem = 1024 + kRingBytes + kOutBytes + kBarBytes + kBiasBytes;
 static_assert(kTcSmem <= 227 * 1024, "shared memory above the per-block limit");
-constexpr uint32_t kGroup = 16;                    // columns of tiles that are worked on together
+// Columns of tiles that are worked on together, rows fastest, so that the tiles in
+// flight share few rows and columns and their operands come from L2 (2048 tokens of 4096
+// to 16384: 16 columns, columns fastest 152 us, eight 142.5, rows fastest 141.5).
+constexpr uint32_t kGroup = 8;
 
 #define LINEAR_OK(buffer, a, n) DT_IN_EXTENT(p, kBoundsLinear, (buffer), (a), (n))
 
@@ -76,6 +82,7 @@ struct Roles {
     static constexpr int b = !SECOND ? kW : KIND == kGatherBack ? kTok : kFeat;
     static constexpr bool a_mn = SECOND, b_mn = is_back(KIND);
     static constexpr bool tok = a == kTok || b == kTok;   // the token axis is cut as the tokens' matrices are
+    static constexpr uint32_t depth = linear_depth(is_back(KIND));   // of a stage
     static constexpr bool w_by_feature = KIND == kGather || KIND == kGatherBack;   // rows of W_r are features
 };
 
@@ -109,26 +116,36 @@ __device__ __forceinline__ uint32_t length(const LinearParams &p, uint32_t piece
     return AXIS == kDim ? p.dim : AXIS == kFeatures ? p.f_len[piece] : R::tok ? p.t_len[piece] : p.tokens;
 }
 
-// Walks over the blocks of the inner axis.
+// Walks over the blocks of the inner axis, the blocks of one piece after the other.
 template <class R>
 struct Inner {
-    Place at;
-    uint32_t len;
-    __device__ __forceinline__ Inner(const LinearParams &p, const LinearProduct &c, uint32_t kb)
-        : at(locate<R, R::k>(p, c, kb, kK)), len(length<R, R::k>(p, at.piece))
+    Place at;            // of the piece's first block here
+    uint32_t blocks;     // of it from there on, at most as many as are left
+    uint32_t last;       // K steps of 16 in the piece's very last block
+    bool ends;           // that one is among them
+    uint32_t left;
+    __device__ __forceinline__ Inner(const LinearParams &p, const LinearProduct &c, uint32_t kb0, uint32_t kb1)
+        : at(locate<R, R::k>(p, c, kb0, R::depth)), left(kb1 - kb0)
     {
+        take(p);
     }
-    __device__ __forceinline__ void next(const LinearParams &p)
+    __device__ __forceinline__ void take(const LinearParams &p)
     {
-        at.at += kK;
-        at.all += kK;
-        const uint32_t pieces = R::k == kFeatures ? (uint32_t)p.P : R::k == kTokens && R::tok ? (uint32_t)p.t_pieces : 1;
-        while (at.at >= len && at.piece + 1 < pieces) {
-            ++at.piece;
-            at.at = 0;
-            len = length<R, R::k>(p, at.piece);
-            if (R::k == kTokens) at.all = p.t_first[at.piece];
-        }
+        const uint32_t len = length<R, R::k>(p, at.piece) - at.at, all = (len + R::depth - 1) / R::depth;
+        blocks = min(all, left);
+        ends = all <= left;
+        last = ((len - 1) % R::depth + 16) / 16;
+        left -= blocks;
+    }
+    // The next piece that has something; false at the end.
+    __device__ __forceinline__ bool next(const LinearParams &p)
+    {
+        if (left == 0) return false;
+        while (length<R, R::k>(p, ++at.piece) == 0) {}
+        at.at = 0;
+        if (R::k == kTokens) at.all = p.t_first[at.piece];
+        take(p);
+        return true;
     }
 };
 
@@ -144,17 +161,14 @@ __device__ __forceinline__ void place_tile(const LinearProduct &c, uint32_t i, T
     i -= t.split * per_split;
     const uint32_t all = kGroup * c.mt, g = i / all;
     i -= g * all;
-    const uint32_t width = min(kGroup, c.nt - g * kGroup);
-    t.m = i / width;
-    t.n = g * kGroup + i - t.m * width;
+    t.n = g * kGroup + i / c.mt;
+    t.m = i % c.mt;
     t.kb0 = (uint32_t)((uint64_t)c.kblocks * t.split / c.splits);
     t.kb1 = (uint32_t)((uint64_t)c.kblocks * (t.split + 1) / c.splits);
 }
 
 // The k-th tile of worker q (a CTA or a pair) of W; false when it has no more.
-// Columns of tiles in groups of 16, rows slowest within a group, so that the tiles
-// in flight share few rows and columns and their operands come from L2.  First the
-// tiles of the first product, one by one to the workers.  While the first `rest`
+// First the tiles of the first product, one by one to the workers.  While the first `rest`
 // workers still have one more of them, the others take `early` tiles of the second
 // product each; then all take the rest of those in turn.
 template <int KIND>
@@ -211,72 +225,96 @@ __host__ __device__ constexpr uint32_t a_box_bytes(bool back, uint32_t rows)
     return back ? kBoxBytes : (rows * 128 + 1023) / 1024 * 1024;
 }
 
-// One stage: two boxes of A, the second 64 columns further, and of B two, or one
-// to 64 columns of an MN-major operand.  What a stage holds beside its boxes is left
-// over from earlier loads and reaches only rows of the accumulator that are not
-// stored.
-template <class R, int CG>
-__device__ __forceinline__ void load_stage(const LinearParams &p, Place (&at)[3], const Place &k, uint32_t half, uint32_t a,
-                                           uint32_t a_box, uint32_t bar)
+// Boxes of 64 columns in a stage: one of a K-major operand, 64 deep, or as many as hold
+// the columns of an MN-major one; backward, where one operand at least is MN-major, a
+// K-major one has two.
+__host__ __device__ constexpr uint32_t a_boxes(bool back) { return back ? 2 : 1; }
+__host__ __device__ constexpr uint32_t b_boxes(bool back, uint32_t bn) { return back ? (bn + 63) / 64 : 1; }
+__host__ __device__ constexpr uint32_t stage_size(bool back, uint32_t rows_t, uint32_t bn)
 {
-    at[R::k] = k;
-    const uint32_t bn = p.bn / CG, b = a + 2 * a_box;
-    const uint32_t b_boxes = R::b_mn ? bn / 64 : 2, b_rows = R::b_mn ? (R::b == kW ? kK : p.rows_t) : bn;
-    if (half == 0) mbar_expect_tx(bar, CG * (2 * p.rows_t + b_boxes * b_rows) * 128);
-    uint32_t col, row;
-    const CUtensorMap *map = operand<R, R::a>(p, at, col, row);
-    (R::a_mn ? col : row) += half * kM;
-    tma_box<CG>(a, map, col, row, bar);
-    tma_box<CG>(a + a_box, map, col + 64, row, bar);
-    map = operand<R, R::b>(p, at, col, row);
-    (R::b_mn ? col : row) += half * bn;
-    tma_box<CG>(b, map, col, row, bar);
-    if (b_boxes == 2) tma_box<CG>(b + (R::b_mn ? kBoxBytes : bn * 128), map, col + 64, row, bar);
+    return a_boxes(back) * a_box_bytes(back, rows_t) + (back ? b_boxes(back, bn) * kBoxBytes : bn * 128);
 }
 
-// A tile's loads, or its products' issue, block after block.
+// A tile's loads.  A stage is the boxes of A, 64 columns apart, and those of B; what it
+// holds beside them is left over from earlier loads and reaches only rows of the
+// accumulator that are not stored.  Maps and coordinates are worked out once for a
+// piece of the inner axis: done for every stage they took the issuing thread longer
+// (680 cycles) than the products take (2048 tokens of 4096 to 16384: @G@ -> @H@ us).
 template <class R, int CG, class Wait>
 __device__ __forceinline__ bool load_tile(const LinearParams &p, const LinearProduct &c, const Tile &t, uint32_t half,
                                           uint32_t ring, uint32_t stage_bytes, uint32_t a_box, uint32_t full,
                                           uint32_t empty, const Wait &wait, uint32_t &s, uint32_t &round, uint32_t &n)
 {
+    constexpr bool kBack = R::b_mn;
     Place at[3] = {};
     at[R::m] = locate<R, R::m>(p, c, t.m, kM * CG);
     at[R::n] = locate<R, R::n>(p, c, t.n, p.bn);
-    Inner<R> k(p, c, t.kb0);
-    for (uint32_t kb = t.kb0; kb < t.kb1; ++kb, ++n, k.next(p)) {
-        if (!wait(empty + 8 * s, round ^ 1)) return false;
-        load_stage<R, CG>(p, at, k.at, half, ring + s * stage_bytes, a_box, full + 8 * s);
-        if (++s == p.stages) s = 0, round ^= 1;
-    }
+    const uint32_t bn = p.bn / CG, boxes = b_boxes(kBack, bn), b_rows = kBack ? (R::b == kW ? R::depth : p.rows_t) : bn;
+    const uint32_t bytes = CG * (a_boxes(kBack) * p.rows_t + boxes * b_rows) * 128, stages = p.stages;
+    Inner<R> k(p, c, t.kb0, t.kb1);
+    do {
+        at[R::k] = k.at;
+        uint32_t a_col, a_row, b_col, b_row;
+        const CUtensorMap *a_map = operand<R, R::a>(p, at, a_col, a_row), *b_map = operand<R, R::b>(p, at, b_col, b_row);
+        (R::a_mn ? a_col : a_row) += half * kM;
+        (R::b_mn ? b_col : b_row) += half * bn;
+        for (uint32_t i = 0; i < k.blocks; ++i, ++n) {
+            if (!wait(empty + 8 * s, round ^ 1)) return false;
+            const uint32_t bar = full + 8 * s, a = ring + s * stage_bytes, b = a + a_boxes(kBack) * a_box;
+            if (half == 0) mbar_expect_tx(bar, bytes);
+            tma_box<CG>(a, a_map, a_col, a_row, bar);
+            if (a_boxes(kBack) == 2) tma_box<CG>(a + a_box, a_map, a_col + 64, a_row, bar);
+            tma_box<CG>(b, b_map, b_col, b_row, bar);
+            if (boxes == 2) tma_box<CG>(b + kBoxBytes, b_map, b_col + 64, b_row, bar);
+            (R::a_mn ? a_row : a_col) += R::depth;
+            (R::b_mn ? b_row : b_col) += R::depth;
+            if (++s == stages) s = 0, round ^= 1;
+        }
+    } while (k.next(p));
     return true;
 }
 
+// A stage's products.
+template <class R, int CG>
+__device__ __forceinline__ void multiply_stage(uint32_t acc, uint64_t a, uint64_t b, uint32_t desc, bool add, uint32_t steps,
+                                               uint32_t a_box)
+{
+    // from a K step of 16 to the next: 16 rows of an MN-major box; 32 bytes of a
+    // K-major one, and from its fourth to the next box, where a stage is that deep (B
+    // is MN-major there)
+    const uint32_t a_step = R::a_mn ? 16 * 128 : 32, a_next = R::a_mn ? 4 * a_step : a_box;
+    const uint32_t b_step = R::b_mn ? 16 * 128 : 32, b_next = 4 * b_step;
+#pragma unroll
+    for (uint32_t j = 0; j < R::depth / 16; ++j)
+        if (j < steps)
+            mma_bf16<CG>(acc, a + ((j / 4 * a_next + j % 4 * a_step) >> 4), b + ((j / 4 * b_next + j % 4 * b_step) >> 4), desc,
+                         add || j != 0);
+}
+
+// A tile's products.
 template <class R, int CG, class Wait>
 __device__ __forceinline__ bool multiply_tile(const LinearParams &p, const LinearProduct &c, const Tile &t, uint32_t acc,
                                               uint32_t ring, uint32_t stage_bytes, uint32_t a_box, uint32_t full,
                                               uint32_t empty, const Wait &wait, uint32_t &s, uint32_t &round)
 {
-    const uint32_t desc = mma_desc(kM * CG, p.bn, R::a_mn, R::b_mn);
-    // from a K step of 16 to the next: 16 rows of an MN-major box; 32 bytes of a
-    // K-major one, and from its fourth to the next box
-    const uint32_t a_step = R::a_mn ? 16 * 128 : 32, a_next = R::a_mn ? 4 * a_step : a_box;
-    const uint32_t b_step = R::b_mn ? 16 * 128 : 32, b_next = R::b_mn ? 4 * b_step : p.bn / CG * 128;
-    Inner<R> k(p, c, t.kb0);
-    for (uint32_t kb = t.kb0; kb < t.kb1; ++kb, k.next(p)) {
-        if (!wait(full + 8 * s, round)) return false;
-        tc_fence_after();
-        const uint32_t at = ring + s * stage_bytes;
-        const uint64_t a = smem_desc(at, R::a_mn), b = smem_desc(at + 2 * a_box, R::b_mn);
-        const uint32_t steps = min((k.len - k.at.at + 15) / 16, kK / 16);
-#pragma unroll
-        for (uint32_t j = 0; j < kK / 16; ++j)
-            if (j < steps)
-                mma_bf16<CG>(acc, a + ((j / 4 * a_next + j % 4 * a_step) >> 4), b + ((j / 4 * b_next + j % 4 * b_step) >> 4),
-                             desc, kb != t.kb0 || j != 0);
-        mma_commit<CG>(empty + 8 * s);
-        if (++s == p.stages) s = 0, round ^= 1;
-    }
+    const uint32_t desc = mma_desc(kM * CG, p.bn, R::a_mn, R::b_mn), stages = p.stages;
+    const uint64_t a0 = smem_desc(ring, R::a_mn), b0 = smem_desc(ring + a_boxes(R::b_mn) * a_box, R::b_mn);
+    Inner<R> k(p, c, t.kb0, t.kb1);
+    bool add = false;
+    do {
+        for (uint32_t i = 0; i < k.blocks; ++i) {
+            if (!wait(full + 8 * s, round)) return false;
+            tc_fence_after();
+            const uint32_t at = s * (stage_bytes >> 4);
+            if (k.last < R::depth / 16 && k.ends && i + 1 == k.blocks)
+                multiply_stage<R, CG>(acc, a0 + at, b0 + at, desc, add, k.last, a_box);
+            else
+                multiply_stage<R, CG>(acc, a0 + at, b0 + at, desc, add, R::depth / 16, a_box);
+            add = true;
+            mma_commit<CG>(empty + 8 * s);
+            if (++s == stages) s = 0, round ^= 1;
+        }
+    } while (k.next(p));
     return true;
 }
 
@@ -284,70 +322,82 @@ __device__ __forceinline__ bool multiply_tile(const LinearParams &p, const Linea
 
 __device__ constexpr float kTail[7] = {0.143713042f, 0.141772494f, 0.139719009f, 0.0265500601f, 0.180952892f, -0.179763854f, 0.0470560379f};
 
-// The upper tail of the normal distribution at z >= 0, and exp(-z^2 / 2).  The tail
-// is exp(-z^2 / 2) t (c0 + c1 t + ... + c6 t^6) with t = 1 / (1 + 0.36 z), the c a
-// minimax fit of the relative error over t from 1 to z = 14: 1e-6 of itself off
+// The upper tail of the normal distribution at |v|, and exp(-v^2 / 2), two at a time.
+// The tail is exp(-z^2 / 2) t (c0 + c1 t + ... + c6 t^6) with t = 1 / (1 + 0.36 z), the c
+// a minimax fit of the relative error over t from 1 to z = 14: 1e-6 of itself off
 // everywhere, where 1 - erf would have nothing left far out.  (Own fit; erfcf in its
-// place is some 40 instructions, 64 times over.)
-__device__ __forceinline__ float normal_tail(float z, float &bell)
+// place is some 40 instructions, for every element.)
+__device__ __forceinline__ float2 normal_tail(float2 v, float2 &bell)
 {
-    bell = exp2_fast(z * z * -0.72134752044448170368f);
-    const float t = __fdividef(1.0f, fmaf(0.36f, z, 1.0f));
-    float s = kTail[6];
+    const float2 e = mul2(mul2(v, v), make_float2(-0.72134752044448170368f, -0.72134752044448170368f));
+    bell = make_float2(exp2_fast(e.x), exp2_fast(e.y));
+    const float2 d = fma2(make_float2(fabsf(v.x), fabsf(v.y)), make_float2(0.36f, 0.36f), make_float2(1.0f, 1.0f));
+    const float2 t = make_float2(rcp_fast(d.x), rcp_fast(d.y));
+    float2 s = make_float2(kTail[6], kTail[6]);
 #pragma unroll
-    for (int i = 5; i >= 0; --i) s = fmaf(s, t, kTail[i]);
-    return s * t * bell;
+    for (int i = 5; i >= 0; --i) s = fma2(s, t, make_float2(kTail[i], kTail[i]));
+    return mul2(mul2(s, t), bell);
+}
+
+// The normal distribution from its tail.
+__device__ __forceinline__ float2 normal_of(float2 v, float2 q)
+{
+    return make_float2(v.x > 0.0f ? 1.0f - q.x : q.x, v.y > 0.0f ? 1.0f - q.y : q.y);
+}
+
+// 1 / (1 + exp(-v)).
+__device__ __forceinline__ float2 logistic(float2 v)
+{
+    const float2 e = mul2(v, make_float2(-1.44269504088896340736f, -1.44269504088896340736f));
+    return make_float2(rcp_fast(1.0f + exp2_fast(e.x)), rcp_fast(1.0f + exp2_fast(e.y)));
 }
 
 // The activation; a NaN stays one.
 template <int ACT>
-__device__ __forceinline__ float activate(float v)
+__device__ __forceinline__ float2 activate(float2 v)
 {
-    if (ACT == DT_ACT_RELU) return v < 0.0f ? 0.0f : v;
-    if (ACT == DT_ACT_SILU) return __fdividef(v, 1.0f + __expf(-v));
+    if (ACT == DT_ACT_RELU) return make_float2(v.x < 0.0f ? 0.0f : v.x, v.y < 0.0f ? 0.0f : v.y);
+    if (ACT == DT_ACT_SILU) return mul2(v, logistic(v));
     if (ACT == DT_ACT_GELU) {
-        float bell;
-        const float q = normal_tail(fabsf(v), bell);
-        return v * (v > 0.0f ? 1.0f - q : q);
+        float2 bell;
+        const float2 q = normal_tail(v, bell);
+        return mul2(v, normal_of(v, q));
     }
     return v;
 }
 
 // Its derivative.
 template <int ACT>
-__device__ __forceinline__ float slope(float v)
+__device__ __forceinline__ float2 slope(float2 v)
 {
-    if (ACT == DT_ACT_RELU) return v > 0.0f ? 1.0f : 0.0f;
+    if (ACT == DT_ACT_RELU) return make_float2(v.x > 0.0f ? 1.0f : 0.0f, v.y > 0.0f ? 1.0f : 0.0f);
+    const float2 one = make_float2(1.0f, 1.0f);
     if (ACT == DT_ACT_SILU) {
-        const float s = __fdividef(1.0f, 1.0f + __expf(-v));
-        return s * fmaf(v, 1.0f - s, 1.0f);
+        const float2 s = logistic(v), rest = fma2(s, make_float2(-1.0f, -1.0f), one);
+        return mul2(s, fma2(v, rest, one));
     }
     if (ACT == DT_ACT_GELU) {
-        float bell;
-        const float q = normal_tail(fabsf(v), bell);
-        return fmaf(v * 0.39894228040143267794f, bell, v > 0.0f ? 1.0f - q : q);
+        float2 bell;
+        const float2 q = normal_tail(v, bell);
+        return fma2(mul2(v, make_float2(0.39894228040143267794f, 0.39894228040143267794f)), bell, normal_of(v, q));
     }
-    return 1.0f;
+    return one;
 }
 
-// N values at a time, so that the choice is made once.
+// All of N values, so that the choice is made once.
 template <int N>
 __device__ __forceinline__ void activate(float (&v)[N], int act)
 {
     auto all = [&](auto of) {
 #pragma unroll
-        for (int j = 0; j < N; ++j) v[j] = activate<decltype(of)::value>(v[j]);
+        for (int j = 0; j < N; j += 2) {
+            const float2 a = activate<decltype(of)::value>(make_float2(v[j], v[j + 1]));
+            v[j] = a.x, v[j + 1] = a.y;
+        }
     };
     if (act == DT_ACT_RELU) all(std::integral_constant<int, DT_ACT_RELU>{});
     else if (act == DT_ACT_GELU) all(std::integral_constant<int, DT_ACT_GELU>{});
     else if (act == DT_ACT_SILU) all(std::integral_constant<int, DT_ACT_SILU>{});
-}
-
-__device__ __forceinline__ float activated(float x, int act)
-{
-    float v[1] = {x};
-    activate(v, act);
-    return v[0];
 }
 
 // g[j] times the derivative at v[j].
@@ -356,7 +406,10 @@ __device__ __forceinline__ void times_slope(float (&g)[N], const float (&v)[N], 
 {
     auto all = [&](auto of) {
 #pragma unroll
-        for (int j = 0; j < N; ++j) g[j] *= slope<decltype(of)::value>(v[j]);
+        for (int j = 0; j < N; j += 2) {
+            const float2 a = mul2(make_float2(g[j], g[j + 1]), slope<decltype(of)::value>(make_float2(v[j], v[j + 1])));
+            g[j] = a.x, g[j + 1] = a.y;
+        }
     };
     if (act == DT_ACT_RELU) all(std::integral_constant<int, DT_ACT_RELU>{});
     else if (act == DT_ACT_GELU) all(std::integral_constant<int, DT_ACT_GELU>{});
@@ -401,47 +454,50 @@ __device__ __forceinline__ uint16_t *lane_pointer(uint16_t *v, uint32_t lane)
     return reinterpret_cast<uint16_t *>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<uint64_t>(v), lane));
 }
 
+// 16-byte chunk c (of four) of row r of a finishing warp's 32 x 64 bytes of shared
+// memory: a thread writes its row, and four threads read a row, without bank conflicts.
+__device__ __forceinline__ unsigned char *step_chunk(unsigned char *buf, uint32_t row, uint32_t c)
+{
+    return buf + row * 64 + ((c ^ (row >> 1 & 3)) << 4);
+}
+
 // A warp's rows between `buf` and memory, N elements of a row to a lane and as many
 // rows at a time as that leaves lanes for.  row: where this lane's row begins, NULL
-// where there is none.
+// where there is none.  Stores are marked as not soon read again, so that the operands
+// stay in L2 (as above with gelu and what it is taken of: 155.7 -> 154.7 us).
 template <int N, bool STORE>
 __device__ __forceinline__ void move_rows(const LinearParams &p, unsigned char *buf, uint16_t *row, uint32_t cols, int buffer)
 {
     using W = typename Words<N>::type;
     (void)p;
-    constexpr uint32_t kLanes = 64 / N, kRows = 32 / kLanes;
+    constexpr uint32_t kLanes = kStep / N, kRows = 32 / kLanes;
     const uint32_t lane = threadIdx.x & 31, e = lane % kLanes * N, first = lane / kLanes;
-    W v[8];
 #pragma unroll
-    for (uint32_t k0 = 0; k0 < 32; k0 += 8 * kRows) {
-        uint16_t *at[8];
+    for (uint32_t k0 = 0; k0 < 32; k0 += 4 * kRows) {
+        uint16_t *at[4];
+        W v[4];
 #pragma unroll
-        for (uint32_t k = 0; k < 8; ++k) {
+        for (uint32_t k = 0; k < 4; ++k) {
             const uint32_t r = k0 + k * kRows + first;
             at[k] = lane_pointer(row, r);
             const int of = __shfl_sync(0xFFFFFFFFu, buffer, r);
-            const bool there = at[k] && e < cols && LINEAR_OK(of, at[k] + e, 2 * N);
+            if (!at[k] || e >= cols || !LINEAR_OK(of, at[k] + e, 2 * N)) at[k] = nullptr;
             (void)of;
-            W *word = reinterpret_cast<W *>(buf + r * 128 + ((((e >> 3) ^ r) & 7) << 4) + (e & 7) * 2);
-            if constexpr (STORE) {
-                if (there) *reinterpret_cast<W *>(at[k] + e) = *word;
-            } else if (there) {
-                v[k] = *reinterpret_cast<const W *>(at[k] + e);
+            W *word = reinterpret_cast<W *>(step_chunk(buf, r, e >> 3) + (e & 7) * 2);
+            if (at[k]) {
+                if constexpr (STORE) __stcs(reinterpret_cast<W *>(at[k] + e), *word);
+                else v[k] = *reinterpret_cast<const W *>(at[k] + e);
             }
-            if (!there) at[k] = nullptr;
         }
         if constexpr (!STORE) {
 #pragma unroll
-            for (uint32_t k = 0; k < 8; ++k) {
-                const uint32_t r = k0 + k * kRows + first;
-                    if (at[k]) *reinterpret_cast<W *>(buf + r * 128 + ((((e >> 3) ^ r) & 7) << 4) + (e & 7) * 2) = v[k];
-            }
+            for (uint32_t k = 0; k < 4; ++k)
+                if (at[k]) *reinterpret_cast<W *>(step_chunk(buf, k0 + k * kRows + first, e >> 3) + (e & 7) * 2) = v[k];
         }
     }
 }
 
-// The same for rows that begin at any element: a row at a time, every element on
-// its own.
+// The same for rows that begin at any element: an element to a lane, a row at a time.
 template <bool STORE>
 __device__ __forceinline__ void move_rows_odd(const LinearParams &p, unsigned char *buf, uint16_t *row, uint32_t cols, int buffer)
 {
@@ -452,15 +508,10 @@ __device__ __forceinline__ void move_rows_odd(const LinearParams &p, unsigned ch
         uint16_t *at = lane_pointer(row, r);
         const int of = __shfl_sync(0xFFFFFFFFu, buffer, r);
         (void)of;
-        if (!at) continue;
-#pragma unroll
-        for (uint32_t e = lane; e < 64; e += 32) {
-            uint16_t *word = reinterpret_cast<uint16_t *>(buf + r * 128 + ((((e >> 3) ^ r) & 7) << 4) + (e & 7) * 2);
-            if (e < cols && LINEAR_OK(of, at + e, 2)) {
-                if constexpr (STORE) at[e] = *word;
-                else *word = at[e];
-            }
-        }
+        uint16_t *word = reinterpret_cast<uint16_t *>(step_chunk(buf, r, lane >> 3) + (lane & 7) * 2);
+        if (!at || lane >= cols || !LINEAR_OK(of, at + lane, 2)) continue;
+        if constexpr (STORE) at[lane] = *word;
+        else *word = at[lane];
     }
 }
 
@@ -474,64 +525,61 @@ __device__ __forceinline__ void move_rows(const LinearParams &p, unsigned char *
     else move_rows_odd<STORE>(p, buf, row, cols, buffer);
 }
 
-// This lane's row of 64 columns to memory by way of `buf`.
-__device__ __forceinline__ void store_rows(const LinearParams &p, unsigned char *buf, const float (&v)[64], uint16_t *row,
+// This lane's row of 32 columns to memory by way of `buf`.
+__device__ __forceinline__ void store_rows(const LinearParams &p, unsigned char *buf, const float (&v)[kStep], uint16_t *row,
                                            uint32_t cols, uint32_t align, int buffer)
 {
     const uint32_t lane = threadIdx.x & 31;
     __syncwarp();
 #pragma unroll
-    for (uint32_t c = 0; c < 8; ++c)
-        *out_chunk(buf, lane, c) = make_uint4(pack_bf16x2(v[8 * c], v[8 * c + 1]), pack_bf16x2(v[8 * c + 2], v[8 * c + 3]),
-                                              pack_bf16x2(v[8 * c + 4], v[8 * c + 5]), pack_bf16x2(v[8 * c + 6], v[8 * c + 7]));
+    for (uint32_t c = 0; c < kStep / 8; ++c)
+        *reinterpret_cast<uint4 *>(step_chunk(buf, lane, c)) =
+            make_uint4(pack_bf16x2(v[8 * c], v[8 * c + 1]), pack_bf16x2(v[8 * c + 2], v[8 * c + 3]),
+                       pack_bf16x2(v[8 * c + 4], v[8 * c + 5]), pack_bf16x2(v[8 * c + 6], v[8 * c + 7]));
     __syncwarp();
     move_rows<true>(p, buf, row, cols, align, buffer);
 }
 
-// 64 sums of this lane's row, whose columns begin at column `c` of the tile: bias,
+// v += 32 bf16 values in four chunks.
+template <class Chunk>
+__device__ __forceinline__ void add_chunks(float (&v)[kStep], const Chunk &chunk)
+{
+#pragma unroll
+    for (uint32_t j = 0; j < kStep / 8; ++j) {
+        const uint4 b = *reinterpret_cast<const uint4 *>(chunk(j));
+        const uint32_t w[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (uint32_t q = 0; q < 4; ++q) {
+            v[8 * j + 2 * q] += bf16_lo(w[q]);
+            v[8 * j + 2 * q + 1] += bf16_hi(w[q]);
+        }
+    }
+}
+
+// 32 sums of this lane's row, whose columns begin at column `c` of the tile: bias,
 // residual, activation, and to memory.
 template <int KIND, class R>
-__device__ __forceinline__ void finish_row(const LinearParams &p, unsigned char *buf, unsigned char *biases, float (&v)[64],
-                                           const OutRow &o, bool there, const Place &n, uint32_t c, uint32_t cols,
-                                           uint32_t align)
+__device__ __forceinline__ void finish_row(const LinearParams &p, unsigned char *buf, unsigned char *biases,
+                                           float (&v)[kStep], const OutRow &o, bool there, const Place &n, uint32_t c,
+                                           uint32_t cols, uint32_t align)
 {
     const uint32_t lane = threadIdx.x & 31;
     if (!is_back(KIND) && p.biased) {
         // one bias for all ranks' tokens, or each rank's own for its features
         const uint32_t r = KIND == kGather ? n.piece : 0;
-        const uint16_t *from = p.bias[r] + n.at + c;
-        uint32_t w = 0;
-        if (2 * lane < cols && LINEAR_OK(kLinearBias + r, from + 2 * lane, 2)) w = from[2 * lane];
-        if (2 * lane + 1 < cols && LINEAR_OK(kLinearBias + r, from + 2 * lane + 1, 2)) w |= (uint32_t)from[2 * lane + 1] << 16;
+        const uint16_t *from = p.bias[r] + n.at + c + lane;
+        const uint16_t w = lane < cols && LINEAR_OK(kLinearBias + r, from, 2) ? *from : 0;
         __syncwarp();
-        reinterpret_cast<uint32_t *>(biases)[lane] = w;
+        reinterpret_cast<uint16_t *>(biases)[lane] = w;
         __syncwarp();
-#pragma unroll
-        for (uint32_t j = 0; j < 8; ++j) {
-            const uint4 b = reinterpret_cast<const uint4 *>(biases)[j];
-            const uint32_t w4[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-            for (uint32_t q = 0; q < 4; ++q) {
-                v[8 * j + 2 * q] += bf16_lo(w4[q]);
-                v[8 * j + 2 * q + 1] += bf16_hi(w4[q]);
-            }
-        }
+        add_chunks(v, [&](uint32_t j) { return biases + 16 * j; });
     }
     if (KIND == kReduce && p.residuals) {
         uint16_t *from = there ? const_cast<uint16_t *>(p.residual[o.rank]) + o.offset + c : nullptr;
         __syncwarp();
         move_rows<false>(p, buf, from, cols, align, kLinearResidual + o.rank);
         __syncwarp();
-#pragma unroll
-        for (uint32_t j = 0; j < 8; ++j) {
-            const uint4 b = *out_chunk(buf, lane, j);
-            const uint32_t w4[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-            for (uint32_t q = 0; q < 4; ++q) {
-                v[8 * j + 2 * q] += bf16_lo(w4[q]);
-                v[8 * j + 2 * q + 1] += bf16_hi(w4[q]);
-            }
-        }
+        add_chunks(v, [&](uint32_t j) { return step_chunk(buf, lane, j); });
     }
     if (KIND == kGather && p.keep)
         store_rows(p, buf, v, there ? p.pre[o.rank] + o.offset + c : nullptr, cols, align, kLinearPre + o.rank);
@@ -540,55 +588,129 @@ __device__ __forceinline__ void finish_row(const LinearParams &p, unsigned char 
     store_rows(p, buf, v, there ? o.out + o.offset + c : nullptr, cols, align, kOut + o.rank);
 }
 
-// One tile's accumulator, by a warp whose 32 rows begin at row `quad` of the tile
-// and which takes the columns [c0, c1).
-template <int KIND, class R>
+// One tile's accumulator, by a warp whose 32 rows begin at row `quad` of the tile and
+// which takes steps of 32 columns in turn, from `group` on.  `give_back` hands the
+// accumulator over as soon as the warp has read its part.
+template <int KIND, class R, class GiveBack>
 __device__ __forceinline__ void finish_tile(const LinearParams &p, const LinearProduct &c, const Tile &t, uint32_t acc,
-                                            uint32_t high, uint32_t quad, uint32_t c0, uint32_t c1, unsigned char *buf,
-                                            unsigned char *biases)
+                                            uint32_t high, uint32_t quad, uint32_t group, unsigned char *buf,
+                                            unsigned char *biases, const GiveBack &give_back)
 {
     const Place m = locate<R, R::m>(p, c, t.m, high), n = locate<R, R::n>(p, c, t.n, p.bn);
     const uint32_t lane = threadIdx.x & 31, row = quad + lane;
-    const uint32_t rows = length<R, R::m>(p, m.piece) - m.at, cols = length<R, R::n>(p, n.piece) - n.at;
+    const uint32_t rows = length<R, R::m>(p, m.piece) - m.at, cols = min(length<R, R::n>(p, n.piece) - n.at, p.bn);
     const bool there = row < rows;
-    if (c.splits > 1) {
-        // fp32 sums: 32 columns a step, through shared memory so that eight threads
-        // take a row's line
-        const uint64_t pitch = (uint64_t)c.nt * p.bn;
-        float *part = c.acc + (((uint64_t)t.split * c.mt + t.m) * high + quad) * pitch + t.n * p.bn;
-        const uint32_t q = lane & 7, first = lane >> 3;
-        for (uint32_t b = c0; b < c1 && b < cols; b += 32) {
-            float v[32];
-            tmem_load32(acc + b, v);
-            __syncwarp();
-#pragma unroll
-            for (uint32_t j = 0; j < 8; ++j)
-                *out_chunk(buf, lane, j) = make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
-                                                      __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3]));
-            __syncwarp();
-#pragma unroll
-            for (uint32_t j = 0; j < 8; ++j) {
-                const uint32_t r = first + 4 * j;
-                float4 *to = reinterpret_cast<float4 *>(part + r * pitch + b + 4 * q);
-                if (quad + r < rows && LINEAR_OK(kLinearWorkspace, to, 16))
-                    *to = *reinterpret_cast<const float4 *>(out_chunk(buf, r, q));
-            }
-        }
+    const bool none = group * kStep >= cols || quad >= rows;
+    if (none) {
+        give_back();
         return;
     }
-    const OutRow o = out_row<R>(p, c, m, n, there ? row : 0);
+    const OutRow o = c.splits > 1 ? OutRow{} : out_row<R>(p, c, m, n, there ? row : 0);
     // the rows of a warp may lie on several ranks, whose buffers are aligned alike (the host says how)
     const uint32_t align = c.align[R::m == kTokens && R::n == kDim ? 0 : o.rank];
-    for (uint32_t b = c0; b < c1 && b < cols; b += 64) {
-        float v[64];
-        tmem_load32(acc + b, *reinterpret_cast<float(*)[32]>(v));
-        tmem_load32(acc + b + 32, *reinterpret_cast<float(*)[32]>(v + 32));
-        finish_row<KIND, R>(p, buf, biases, v, o, there, n, b, min(cols - b, 64u), align);
+    const uint64_t pitch = (uint64_t)c.nt * p.bn;
+    float *part = c.acc + (((uint64_t)t.split * c.mt + t.m) * high + quad) * pitch + t.n * p.bn;
+    for (uint32_t b = group * kStep; b < cols; b += kColumnGroups * kStep) {
+        float v[kStep];
+        tmem_load32(acc + b, v);
+        if (b + kColumnGroups * kStep >= cols) give_back();
+        if (c.splits == 1) {
+            finish_row<KIND, R>(p, buf, biases, v, o, there, n, b, min(cols - b, kStep), align);
+            continue;
+        }
+        // fp32 sums: 16 columns at a time through shared memory, so that four threads
+        // take a row's 64 bytes
+#pragma unroll
+        for (uint32_t h = 0; h < kStep; h += 16) {
+            __syncwarp();
+#pragma unroll
+            for (uint32_t j = 0; j < 4; ++j)
+                *reinterpret_cast<float4 *>(step_chunk(buf, lane, j)) =
+                    make_float4(v[h + 4 * j], v[h + 4 * j + 1], v[h + 4 * j + 2], v[h + 4 * j + 3]);
+            __syncwarp();
+#pragma unroll
+            for (uint32_t j = 0; j < 4; ++j) {
+                const uint32_t r = 8 * j + lane / 4;
+                float4 *to = reinterpret_cast<float4 *>(part + r * pitch + b + h + lane % 4 * 4);
+                if (quad + r < rows && LINEAR_OK(kLinearWorkspace, to, 16))
+                    *to = *reinterpret_cast<const float4 *>(step_chunk(buf, r, lane % 4));
+            }
+        }
+    }
+}
+
+// ---- the bias' gradient: column sums ---------------------------------------------
+
+// Eight values of a row of column sums' source, bf16 or floats, from its element e on.
+__device__ __forceinline__ void sum_load(const LinearParams &p, const LinearSums &c, int k, uint32_t row, uint32_t cols,
+                                         uint32_t e, float (&v)[8])
+{
+    const uint64_t at = (uint64_t)row * cols + e;
+    const uint32_t n = e < cols ? min(cols - e, 8u) : 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+    if (c.f32) {
+        const float *from = static_cast<const float *>(c.src[k]) + at;
+        if (n == 0 || !LINEAR_OK(kLinearWorkspace, from, 4 * n)) return;
+        if (n == 8 && (reinterpret_cast<uintptr_t>(from) & 15) == 0) {
+            const float4 a = reinterpret_cast<const float4 *>(from)[0], b = reinterpret_cast<const float4 *>(from)[1];
+            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j < n) v[j] = from[j];
+        }
+    } else {
+        const uint16_t *from = static_cast<const uint16_t *>(c.src[k]) + at;
+        if (n == 0 || !LINEAR_OK(kLinearDy + k, from, 2 * n)) return;
+        if (n == 8 && (reinterpret_cast<uintptr_t>(from) & 15) == 0) {
+            const uint4 u = *reinterpret_cast<const uint4 *>(from);
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = j & 1 ? bf16_hi(w[j / 2]) : bf16_lo(w[j / 2]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j < n) v[j] = bf16_to_f32(from[j]);
+        }
+    }
+}
+
+// 32 columns a warp, which walks down the rows eight at a time, four lanes to a row;
+// warp `i` of `all` takes the groups of 32 columns i, i + all, ...
+__device__ __forceinline__ void column_sums(const LinearParams &p, uint32_t i, uint32_t all)
+{
+    const LinearSums &c = p.sums;
+    const uint32_t lane = threadIdx.x & 31;
+    for (; i < c.groups; i += all) {
+        int k = 0;
+        uint32_t begin = 0;
+        while (k + 1 < c.n && i >= c.group_end[k]) begin = c.group_end[k++];
+        const uint32_t e = (i - begin) * 32 + lane % 4 * 8, cols = c.cols[k];
+        float sum[8] = {};
+        for (int q = c.stacked ? 0 : k; q < (c.stacked ? c.sources : k + 1); ++q)
+            for (uint32_t first = lane / 4; first < c.rows[q]; first += 32) {
+                float v[4][8];
+#pragma unroll
+                for (uint32_t j = 0; j < 4; ++j) sum_load(p, c, q, first + 8 * j, cols, first + 8 * j < c.rows[q] ? e : cols, v[j]);
+#pragma unroll
+                for (uint32_t j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int z = 0; z < 8; ++z) sum[z] += v[j][z];
+            }
+#pragma unroll
+        for (uint32_t o = 4; o < 32; o *= 2)
+#pragma unroll
+            for (int z = 0; z < 8; ++z) sum[z] += __shfl_xor_sync(0xFFFFFFFFu, sum[z], o);
+        if (lane < 4)
+#pragma unroll
+            for (int z = 0; z < 8; ++z)
+                if (e + z < cols && LINEAR_OK(kLinearDb + k, c.out[k] + e + z, 2)) c.out[k][e + z] = f32_to_bf16(sum[z]);
     }
 }
 
 template <int KIND, int CG>
-__global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(kTcThreads, 1)
+__global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(tc_threads(is_back(KIND)), 1)
 linear_kernel(const __grid_constant__ LinearParams p)
 {
     using First = Roles<KIND, false>;
@@ -634,7 +756,7 @@ linear_kernel(const __grid_constant__ LinearParams p)
     pdl_begin();
     DT_TL_WAITED();
     const Waits wait{p.sink, gave_up};
-    const uint32_t a_box = a_box_bytes(kBack, p.rows_t), stage_bytes = 2 * a_box + p.bn / CG * 256;
+    const uint32_t a_box = a_box_bytes(kBack, p.rows_t), stage_bytes = stage_size(kBack, p.rows_t, p.bn / CG);
 
     if (warp == kFinishWarps) {
         if (lane == 0) {
@@ -679,28 +801,30 @@ linear_kernel(const __grid_constant__ LinearParams p)
             }
         }
         __syncwarp();
+    } else if (kBack && warp >= kFinishWarps + 2) {
+        column_sums(p, blockIdx.x * kSumWarps + warp - kFinishWarps - 2, gridDim.x * kSumWarps);
     } else {
-        // Warps w and w + 4 read the same 32 rows (a warp reaches the tensor memory
-        // lanes of its number modulo 4) and take half of the columns each, at least 64.
-        const uint32_t width = p.bn >= 128 ? p.bn / 2 : p.bn;
-        const uint32_t c0 = (warp >> 2) * width, c1 = min(c0 + width, p.bn);
+        // Warps w, w + 4, ... read the same 32 rows (a warp reaches the tensor memory
+        // lanes of its number modulo 4) and take columns in turn.
         const uint32_t quad = half * kM + (warp & 3) * 32;   // first of this warp's rows in the tile
-        unsigned char *buf = out_buf + warp * kStageOut, *biases = ctl + kBarBytes + warp * 128;
+        unsigned char *buf = out_buf + warp * kStageOut, *biases = ctl + kBarBytes + warp * kStep * 2;
         for (uint32_t u = 0; next_tile<KIND>(p, worker, workers, u, t); ++u) {
             const bool ok = wait(acc_full + 8 * (u & 1), (u >> 1) & 1);
             tc_fence_after();
             if (__any_sync(0xFFFFFFFFu, !ok)) break;
             const uint32_t acc = tmem + (u & 1) * 256 + ((warp & 3) * 32 << 16);
+            auto give_back = [&] {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (CG == 2) mbar_arrive_first(acc_empty + 8 * (u & 1));
+                    else mbar_arrive(acc_empty + 8 * (u & 1));
+                }
+            };
             if (kBack && t.second)
-                finish_tile<KIND, Second>(p, p.product[1], t, acc, kM * CG, quad, c0, c1, buf, biases);
+                finish_tile<KIND, Second>(p, p.product[1], t, acc, kM * CG, quad, warp >> 2, buf, biases, give_back);
             else
-                finish_tile<KIND, First>(p, p.product[0], t, acc, kM * CG, quad, c0, c1, buf, biases);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                if (CG == 2) mbar_arrive_first(acc_empty + 8 * (u & 1));
-                else mbar_arrive(acc_empty + 8 * (u & 1));
-            }
+                finish_tile<KIND, First>(p, p.product[0], t, acc, kM * CG, quad, warp >> 2, buf, biases, give_back);
         }
     }
     tc_fence_before();
@@ -742,7 +866,7 @@ __global__ void __launch_bounds__(kThreads) linear_join_kernel(const __grid_cons
             const uint32_t r = KIND == kGather ? n.piece : 0;
 #pragma unroll
             for (uint32_t j = 0; j < 4; ++j) {
-                if (e + j >= cols) continue;
+                if (e + j >= cols) break;
                 const uint64_t at = o.offset + e + j;
                 if (!is_back(KIND) && p.biased && LINEAR_OK(kLinearBias + r, p.bias[r] + n.at + e + j, 2))
                     v[j] += bf16_to_f32(p.bias[r][n.at + e + j]);
@@ -750,8 +874,12 @@ __global__ void __launch_bounds__(kThreads) linear_join_kernel(const __grid_cons
                     v[j] += bf16_to_f32(p.residual[o.rank][at]);
                 if (KIND == kGather && p.keep && LINEAR_OK(kLinearPre + o.rank, p.pre[o.rank] + at, 2))
                     p.pre[o.rank][at] = f32_to_bf16(v[j]);
-                v[j] = KIND == kGather ? activated(v[j], p.act) : v[j];
-                if (LINEAR_OK(kOut + o.rank, o.out + at, 2)) o.out[at] = f32_to_bf16(v[j]);
+            }
+            if (KIND == kGather) activate(v, p.act);
+#pragma unroll
+            for (uint32_t j = 0; j < 4; ++j) {
+                const uint64_t at = o.offset + e + j;
+                if (e + j < cols && LINEAR_OK(kOut + o.rank, o.out + at, 2)) o.out[at] = f32_to_bf16(v[j]);
             }
         }
     }
@@ -900,7 +1028,7 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kThreads) linear_few
     for (uint32_t o = part * kThreads + threadIdx.x; o < groups * p.tokens * kFewRows; o += kThreads * C) {
         const uint32_t at = o % kFewRows, t = o / kFewRows % p.tokens, w = o / kFewRows / p.tokens, f = first + w * kFewRows + at;
         if (f >= rows) continue;
-        float v[1] = {0.0f};
+        float v[2] = {0.0f, 0.0f};
         if (C > 1) {
             for (uint32_t k = 0; k < C; ++k) v[0] += cluster_load(&sums[w * p.k_warps][t][at], k);
         } else {
@@ -957,28 +1085,37 @@ __global__ void __launch_bounds__(kThreads) linear_prep_kernel(const __grid_cons
         }
     };
     float sum[8] = {};
-#pragma unroll 2
-    for (uint32_t row = chunk * kPrepRows + r0; row < end; row += 8) {
-        uint32_t w[4];
-        load(job.src, row, job.src_buffer, w);
-        if (job.pre || job.sums) {
-            float g[8], z[8];
+    constexpr uint32_t kBatch = 4;   // rows whose loads are under way together
+    for (uint32_t row0 = chunk * kPrepRows + r0; row0 < end; row0 += 8 * kBatch) {
+        uint32_t w[kBatch][4], u[kBatch][4];
 #pragma unroll
-            for (uint32_t j = 0; j < 8; ++j) g[j] = j & 1 ? bf16_hi(w[j / 2]) : bf16_lo(w[j / 2]);
-            if (job.pre) {
-                uint32_t u[4];
-                load(job.pre, row, job.pre_buffer, u);
-#pragma unroll
-                for (uint32_t j = 0; j < 8; ++j) z[j] = j & 1 ? bf16_hi(u[j / 2]) : bf16_lo(u[j / 2]);
-                times_slope(g, z, p.act);
-#pragma unroll
-                for (uint32_t j = 0; j < 4; ++j) w[j] = pack_bf16x2(g[2 * j], g[2 * j + 1]);
-            }
-#pragma unroll
-            for (uint32_t j = 0; j < 8; ++j) sum[j] += g[j];
+        for (uint32_t k = 0; k < kBatch; ++k) {
+            const uint32_t row = row0 + 8 * k;
+            if (row < end) load(job.src, row, job.src_buffer, w[k]);
+            if (row < end && job.pre) load(job.pre, row, job.pre_buffer, u[k]);
         }
-        uint4 *to = reinterpret_cast<uint4 *>(job.dst + (uint64_t)row * job.pitch + e);
-        if (job.dst && e < job.pitch && LINEAR_OK(kLinearWorkspace, to, 16)) *to = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+        for (uint32_t k = 0; k < kBatch; ++k) {
+            const uint32_t row = row0 + 8 * k;
+            if (row >= end) break;
+            if (job.pre || job.sums) {
+                float g[8], z[8];
+#pragma unroll
+                for (uint32_t j = 0; j < 8; ++j) g[j] = j & 1 ? bf16_hi(w[k][j / 2]) : bf16_lo(w[k][j / 2]);
+                if (job.pre) {
+#pragma unroll
+                    for (uint32_t j = 0; j < 8; ++j) z[j] = j & 1 ? bf16_hi(u[k][j / 2]) : bf16_lo(u[k][j / 2]);
+                    times_slope(g, z, p.act);
+#pragma unroll
+                    for (uint32_t j = 0; j < 4; ++j) w[k][j] = pack_bf16x2(g[2 * j], g[2 * j + 1]);
+                }
+#pragma unroll
+                for (uint32_t j = 0; j < 8; ++j) sum[j] += g[j];
+            }
+            uint4 *to = reinterpret_cast<uint4 *>(job.dst + (uint64_t)row * job.pitch + e);
+            if (job.dst && e < job.pitch && LINEAR_OK(kLinearWorkspace, to, 16))
+                *to = make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
+        }
     }
     if (job.sums) {
 #pragma unroll
@@ -994,36 +1131,6 @@ __global__ void __launch_bounds__(kThreads) linear_prep_kernel(const __grid_cons
     DT_TL_END_BLOCK(DT_TL_LINEAR);
 }
 
-// Column sums over the chunks, in a fixed order: 32 columns a block, chunks k, k + 8,
-// ... to a row of threads.
-__global__ void __launch_bounds__(kThreads) linear_sums_kernel(const __grid_constant__ LinearSums p)
-{
-    __shared__ float part[8][33];
-    DT_TL_BEGIN();
-    pdl_begin();
-    DT_TL_WAITED();
-    int k = 0;
-    while (k + 1 < p.n && blockIdx.x >= p.block_end[k]) ++k;
-    const uint32_t lane = threadIdx.x % 32, slice = threadIdx.x / 32, cols = p.cols[k];
-    const uint32_t c = (blockIdx.x - (k ? p.block_end[k - 1] : 0)) * 32 + lane;
-    float sum = 0.0f;
-    if (c < cols) {
-#pragma unroll 8
-        for (uint32_t i = slice; i < p.chunks; i += 8) {
-            const float *from = p.sums[k] + (uint64_t)i * cols + c;
-            if (LINEAR_OK(kLinearWorkspace, from, 4)) sum += *from;
-        }
-    }
-    part[slice][lane] = sum;
-    __syncthreads();
-    if (slice == 0 && c < cols) {
-#pragma unroll
-        for (uint32_t i = 1; i < 8; ++i) sum += part[i][lane];
-        if (LINEAR_OK(kLinearDb + k, p.out[k] + c, 2)) p.out[k][c] = f32_to_bf16(sum);
-    }
-    DT_TL_END_BLOCK(DT_TL_LINEAR);
-}
-
 template <int KIND, int CG>
 cudaError_t launch_kind(LinearParams &p, int device, cudaStream_t s)
 {
@@ -1035,8 +1142,8 @@ cudaError_t launch_kind(LinearParams &p, int device, cudaStream_t s)
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit, std::memory_order_release);
     }
-    p.stages = std::min(kMaxStages, kRingBytes / (2 * a_box_bytes(is_back(KIND), p.rows_t) + p.bn / CG * 256));
-    return launch_kernel(linear_kernel<KIND, CG>, dim3(p.workers * CG), dim3(kTcThreads), kTcSmem, s, false, p);
+    p.stages = std::min(kMaxStages, kRingBytes / stage_size(is_back(KIND), p.rows_t, p.bn / CG));
+    return launch_kernel(linear_kernel<KIND, CG>, dim3(p.workers * CG), dim3(tc_threads(is_back(KIND))), kTcSmem, s, false, p);
 }
 
 template <int KIND>
@@ -1139,11 +1246,6 @@ cudaError_t launch_linear_few(LinearFew &p, LinearKind kind, bool vec, int devic
 cudaError_t launch_linear_prep(LinearPrep &p, cudaStream_t s)
 {
     return launch_kernel(linear_prep_kernel, dim3(p.job[p.jobs - 1].block_end), dim3(kThreads), 0, s, false, p);
-}
-
-cudaError_t launch_linear_sums(LinearSums &p, cudaStream_t s)
-{
-    return launch_kernel(linear_sums_kernel, dim3(p.block_end[p.n - 1]), dim3(kThreads), 0, s, false, p);
 }
 
 }  // namespace dt

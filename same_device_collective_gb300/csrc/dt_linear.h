@@ -32,15 +32,33 @@ enum LinearBuffer : int {
     kLinearWorkspace = 10 * DT_MAX_RANKS, kLinearBuffers
 };
 
+// The depth of a stage, and of the blocks that the inner axis is cut into: 64, or where
+// an operand's rows run along the inner axis 128, so that its boxes of 64 columns are
+// not short.  (Forward 128 deep, half as many stages: 2048 tokens of 4096 to 16384
+// @E@ -> @F@ us.)
+__host__ __device__ constexpr uint32_t linear_depth(bool back) { return back ? 128 : 64; }
+
 // One product of a launch: its tiles, splits of its inner axis, and outputs.
 struct LinearProduct {
     uint32_t mt, nt, splits, tiles;    // tiles = mt * nt * splits
-    uint32_t kblocks;                  // blocks of 128 of the inner axis
+    uint32_t kblocks;                  // blocks of the inner axis
     uint32_t f_end[DT_MAX_RANKS];      // the ranks' features and tokens in tiles or blocks, as their axis is cut
     uint32_t t_end[DT_MAX_RANKS];      // here, numbered through: rank r's end at [r]
     uint16_t *out[DT_MAX_RANKS];
     uint32_t align[DT_MAX_RANKS];      // elements that the rows of out[r] (and pre[r], residual[r]) are a multiple of: 1, 2, 4, 8
     float *acc;                        // splits > 1: sums [splits][mt tiles' rows][nt tiles' columns]
+};
+
+// The bias' gradient: column sums of bf16 matrices, or of the floats that were summed
+// over chunks of rows before, [rows, cols] each: of one matrix for each output, or of
+// all of them (`stacked`) for the only one.
+struct LinearSums {
+    const void *src[DT_MAX_RANKS];
+    uint16_t *out[DT_MAX_RANKS];
+    uint32_t rows[DT_MAX_RANKS], cols[DT_MAX_RANKS];   // of the sources, of the outputs
+    uint32_t group_end[DT_MAX_RANKS];  // groups of 32 columns, numbered through the outputs
+    uint32_t groups;
+    int32_t n, sources, stacked, f32;
 };
 
 struct LinearParams {
@@ -53,7 +71,7 @@ struct LinearParams {
     uint32_t row_end[DT_MAX_RANKS];    // the ranks' tokens, numbered through
     int32_t P, t_pieces;
     uint32_t tokens, dim;
-    uint32_t bn;                       // tile width: 64 or 128, of pairs 128 or 256
+    uint32_t bn;                       // tile width, a multiple of 32: up to 128, of pairs 256
     uint32_t stages, workers;
     uint32_t rows_t, rows_w;           // of the maps' boxes
     uint32_t rest, early;              // the order of both products' tiles (next_tile)
@@ -62,6 +80,7 @@ struct LinearParams {
     const uint16_t *residual[DT_MAX_RANKS];
     int32_t act;
     int32_t keep, biased, residuals;   // pre, bias, residual are there
+    LinearSums sums;                   // backward
     ErrorSink sink;
 #ifdef DT_BOUNDS
     Extent extent[kLinearBuffers];
@@ -85,19 +104,6 @@ constexpr int kPrepJobs = 3 * DT_MAX_RANKS;
 struct LinearPrep {
     LinearPrepJob job[kPrepJobs];
     int32_t jobs, act;
-    ErrorSink sink;
-#ifdef DT_BOUNDS
-    Extent extent[kLinearBuffers];
-#endif
-};
-
-// The bias' gradient: column sums over chunks of rows into one.
-struct LinearSums {
-    const float *sums[DT_MAX_RANKS];   // [chunks][cols]
-    uint16_t *out[DT_MAX_RANKS];
-    uint32_t cols[DT_MAX_RANKS], chunks;
-    uint32_t block_end[DT_MAX_RANKS];
-    int32_t n;
     ErrorSink sink;
 #ifdef DT_BOUNDS
     Extent extent[kLinearBuffers];
@@ -129,7 +135,6 @@ cudaError_t launch_linear_join(const LinearParams &p, LinearKind kind, int k, bo
 // vec: every row of x and w starts on a 16-byte boundary.
 cudaError_t launch_linear_few(LinearFew &p, LinearKind kind, bool vec, int device, cudaStream_t s);
 cudaError_t launch_linear_prep(LinearPrep &p, cudaStream_t s);
-cudaError_t launch_linear_sums(LinearSums &p, cudaStream_t s);
 // CTAs, or pairs of them, that run at once.
 uint32_t linear_workers(bool pairs, int device);
 

@@ -247,4 +247,12 @@ __device__ __forceinline__ float exp2_fast(float x)
     return y;
 }
 
+// 1 / x, at most 1 ulp off.
+__device__ __forceinline__ float rcp_fast(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 }  // namespace dt
