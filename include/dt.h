@@ -445,7 +445,7 @@ size_t dt_vocab_loss_workspace(dt_group_t g, const size_t *vocab, size_t vocab_e
  * DT_ERR_UNSUPPORTED.  Tensors are dense and 2-byte aligned.  Those whose rows start
  * on 16-byte boundaries are read in place, others are laid out again in the workspace
  * first, as are tokens whose ranks' pieces would leave more than a twentieth of the
- * tiles of 256 rows (128 up to 128 tokens) to their ends.
+ * tiles of 128 rows to their ends.
  * workspace: the query's bytes of device memory, 256-byte aligned, free for other use
  * once `stream` has passed the call.  No output may overlap another buffer, but for
  * the residual below.  n is at most 2^26, dim and the sum of features 2^22.  The

@@ -21,7 +21,7 @@ struct Plan {
     size_t n[DT_MAX_RANKS], f[DT_MAX_RANKS];
     size_t tokens, features, dim;
     bool pairs;                        // two CTAs share a tile
-    uint32_t high;                     // rows of a tile
+    uint32_t halves;                   // of 128 rows in a tile: 1 or 2, each within a rank's piece
     uint64_t chunks;                   // of rows, whose column sums the bias' gradient adds
     uint64_t tok, feat, w, sums, acc[2], bytes;
 };
@@ -53,7 +53,7 @@ uint64_t feature_tiles(const Plan &v, uint64_t size)
 struct Cut {
     uint32_t bn;
     uint64_t mt[2], nt[2], kblocks[2], splits[2];
-    uint64_t acc_bytes(const Plan &v, int k) const { return splits[k] > 1 ? splits[k] * mt[k] * v.high * nt[k] * bn * 4 : 0; }
+    uint64_t acc_bytes(const Plan &v, int k) const { return splits[k] > 1 ? splits[k] * mt[k] * v.halves * 128 * nt[k] * bn * 4 : 0; }
 };
 
 // What a launch takes, in microseconds, as far as its cut decides it: 16 of the inner
@@ -78,11 +78,11 @@ bool cut(const dt_group *g, const Plan &v, bool pieces, Cut &best)
     const double block_us = kUsPer64 * depth / 64;
     Cut c;
     // the rows' axis of forward products is the tokens, which reducing are never in pieces
-    c.mt[0] = token_tiles(v, pieces && n_features, v.high);
+    c.mt[0] = tiles_of(token_tiles(v, pieces && n_features, 128), v.halves);
     c.kblocks[0] = n_features ? tiles_of(v.dim, depth) : feature_tiles(v, depth);
     c.mt[1] = c.nt[1] = c.kblocks[1] = 0;
     if (b) {
-        c.mt[1] = gathers(v.kind) ? feature_tiles(v, v.high) : tiles_of(v.dim, v.high);
+        c.mt[1] = tiles_of(gathers(v.kind) ? feature_tiles(v, 128) : tiles_of(v.dim, 128), v.halves);
         c.kblocks[1] = token_tiles(v, pieces, depth);
     }
     double least = 1e300;
@@ -136,7 +136,7 @@ bool plan(const dt_group *g, LinearKind kind, const size_t *rows, size_t rows_eq
     if (v.tokens > kMaxTokens || v.features > kMaxWidth || v.features == 0) return false;
     if (gathers(kind)) v.chunks = tiles_of(v.tokens, dt::kPrepRows);
     v.pairs = v.tokens > 128;
-    v.high = v.pairs ? 256 : 128;
+    v.halves = v.pairs ? 2 : 1;
     uint64_t at = 0;
     auto take = [&at](uint64_t n) {
         const uint64_t from = at;
@@ -280,7 +280,7 @@ void token_matrix(Call &c, const void *const *x, int buffer, float *sums)
         reads = reads && addressable(x[r], v.dim);
         follow = follow && (!next || next == x[r]);
         next = static_cast<const unsigned char *>(x[r]) + v.n[r] * v.dim * 2;
-        tiles += tiles_of(v.n[r], v.high);
+        tiles += tiles_of(v.n[r], 128);
         // as the inner axis, each piece but the last has to be whole steps of 16: a step's
         // other tokens would be the next rank's in the operand that is not in pieces
         // (times zero, but an infinity times zero is not zero)
@@ -289,7 +289,7 @@ void token_matrix(Call &c, const void *const *x, int buffer, float *sums)
         c.tok[pieces] = x[r];
         c.p.t_len[pieces++] = (uint32_t)v.n[r];
     }
-    const bool in_pieces = reads && !follow && (!back(v.kind) || steps) && tiles * 20 <= tiles_of(v.tokens, v.high) * 21;
+    const bool in_pieces = reads && !follow && (!back(v.kind) || steps) && tiles * 20 <= tiles_of(v.tokens, 128) * 21;
     const bool again = !in_pieces && !(reads && follow);
     c.tok_pitch = again ? up(v.dim, 8) : v.dim;
     uint64_t first = 0, chunk = 0;
@@ -394,9 +394,9 @@ cudaError_t matrices(Call &c, const void *const *feat, int feat_buffer, bool wri
         q.splits = (uint32_t)t.splits[k];
         q.tiles = q.mt * q.nt * q.splits;
         q.acc = reinterpret_cast<float *>(c.ws + v.acc[k]);
-        // the size of a tile or block along the features and the tokens in this product
+        // the size of a tile (its rows: of a half) or block along the features and the tokens here
         const bool n_features = v.kind == dt::kGather || v.kind == dt::kReduceBack;
-        const uint64_t depth = dt::linear_depth(b), fs = n_features ? t.bn : k ? v.high : depth, ts = k ? depth : v.high;
+        const uint64_t depth = dt::linear_depth(b), fs = n_features ? t.bn : k ? 128 : depth, ts = k ? depth : 128;
         uint32_t end = 0;
         for (int r = 0; r < c.g->P; ++r) q.f_end[r] = end += (uint32_t)tiles_of(v.f[r], fs);
         end = 0;

@@ -247,7 +247,7 @@ __device__ __forceinline__ bool load_tile(const LinearParams &p, const LinearPro
 {
     constexpr bool kBack = R::b_mn;
     Place at[3] = {};
-    at[R::m] = locate<R, R::m>(p, c, t.m, kM * CG);
+    at[R::m] = locate<R, R::m>(p, c, t.m * CG + half, kM);
     at[R::n] = locate<R, R::n>(p, c, t.n, p.bn);
     const uint32_t bn = p.bn / CG, boxes = b_boxes(kBack, bn), b_rows = kBack ? (R::b == kW ? R::depth : p.rows_t) : bn;
     const uint32_t bytes = CG * (a_boxes(kBack) * p.rows_t + boxes * b_rows) * 128, stages = p.stages;
@@ -256,7 +256,6 @@ __device__ __forceinline__ bool load_tile(const LinearParams &p, const LinearPro
         at[R::k] = k.at;
         uint32_t a_col, a_row, b_col, b_row;
         const CUtensorMap *a_map = operand<R, R::a>(p, at, a_col, a_row), *b_map = operand<R, R::b>(p, at, b_col, b_row);
-        (R::a_mn ? a_col : a_row) += half * kM;
         (R::b_mn ? b_col : b_row) += half * bn;
         for (uint32_t i = 0; i < k.blocks; ++i, ++n) {
             if (!wait(empty + 8 * s, round ^ 1)) return false;
@@ -316,6 +315,29 @@ __device__ __forceinline__ bool multiply_tile(const LinearParams &p, const Linea
         }
     } while (k.next(p));
     return true;
+}
+
+// Eight elements of a row from any element on, of which `n` are there (the others come
+// out as zeros): from the aligned vectors that they lie in, neither of which reaches past
+// the 16-byte block of one of them.
+__device__ __forceinline__ void load_shifted(const uint16_t *from, uint32_t n, uint32_t (&w)[4])
+{
+    const uintptr_t at = reinterpret_cast<uintptr_t>(from);
+    const uint32_t off = (uint32_t)at & 15;
+    const uint4 *block = reinterpret_cast<const uint4 *>(at & ~(uintptr_t)15);
+    const uint4 a = __ldg(block), b = off + 2 * n > 16 ? __ldg(block + 1) : make_uint4(0, 0, 0, 0);
+    // by eight, four and two bytes
+    const bool s8 = off & 8, s4 = off & 4;
+    const uint32_t x[6] = {s8 ? a.z : a.x, s8 ? a.w : a.y, s8 ? b.x : a.z, s8 ? b.y : a.w, s8 ? b.z : b.x, s8 ? b.w : b.y};
+    uint32_t y[5];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) y[i] = s4 ? x[i + 1] : x[i];
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i) {
+        w[i] = __funnelshift_r(y[i], y[i + 1], (off & 2) * 8);
+        if (2 * i >= n) w[i] = 0;
+        else if (2 * i + 1 >= n) w[i] &= 0xFFFFu;
+    }
 }
 
 // ---- what follows a sum ------------------------------------------------------
@@ -588,17 +610,17 @@ __device__ __forceinline__ void finish_row(const LinearParams &p, unsigned char 
     store_rows(p, buf, v, there ? o.out + o.offset + c : nullptr, cols, align, kOut + o.rank);
 }
 
-// One tile's accumulator, by a warp whose 32 rows begin at row `quad` of the tile and
-// which takes steps of 32 columns in turn, from `group` on.  `give_back` hands the
+// One tile's accumulator, by a warp whose 32 rows begin at row `quad` of the CTA's 128
+// (number `unit` along the rows' axis) and which takes steps of 32 columns in turn, from `group` on.  `give_back` hands the
 // accumulator over as soon as the warp has read its part.
 template <int KIND, class R, class GiveBack>
 __device__ __forceinline__ void finish_tile(const LinearParams &p, const LinearProduct &c, const Tile &t, uint32_t acc,
-                                            uint32_t high, uint32_t quad, uint32_t group, unsigned char *buf,
+                                            uint32_t unit, uint32_t units, uint32_t quad, uint32_t group, unsigned char *buf,
                                             unsigned char *biases, const GiveBack &give_back)
 {
-    const Place m = locate<R, R::m>(p, c, t.m, high), n = locate<R, R::n>(p, c, t.n, p.bn);
-    const uint32_t lane = threadIdx.x & 31, row = quad + lane;
-    const uint32_t rows = length<R, R::m>(p, m.piece) - m.at, cols = min(length<R, R::n>(p, n.piece) - n.at, p.bn);
+    const Place m = locate<R, R::m>(p, c, unit, kM), n = locate<R, R::n>(p, c, t.n, p.bn);
+    const uint32_t lane = threadIdx.x & 31, row = quad + lane, len = length<R, R::m>(p, m.piece);
+    const uint32_t rows = m.at < len ? len - m.at : 0, cols = min(length<R, R::n>(p, n.piece) - n.at, p.bn);
     const bool there = row < rows;
     const bool none = group * kStep >= cols || quad >= rows;
     if (none) {
@@ -609,7 +631,7 @@ __device__ __forceinline__ void finish_tile(const LinearParams &p, const LinearP
     // the rows of a warp may lie on several ranks, whose buffers are aligned alike (the host says how)
     const uint32_t align = c.align[R::m == kTokens && R::n == kDim ? 0 : o.rank];
     const uint64_t pitch = (uint64_t)c.nt * p.bn;
-    float *part = c.acc + (((uint64_t)t.split * c.mt + t.m) * high + quad) * pitch + t.n * p.bn;
+    float *part = c.acc + (((uint64_t)t.split * units + unit) * kM + quad) * pitch + t.n * p.bn;
     for (uint32_t b = group * kStep; b < cols; b += kColumnGroups * kStep) {
         float v[kStep];
         tmem_load32(acc + b, v);
@@ -663,16 +685,10 @@ __device__ __forceinline__ void sum_load(const LinearParams &p, const LinearSums
     } else {
         const uint16_t *from = static_cast<const uint16_t *>(c.src[k]) + at;
         if (n == 0 || !LINEAR_OK(kLinearDy + k, from, 2 * n)) return;
-        if (n == 8 && (reinterpret_cast<uintptr_t>(from) & 15) == 0) {
-            const uint4 u = *reinterpret_cast<const uint4 *>(from);
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        uint32_t w[4];
+        load_shifted(from, n, w);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = j & 1 ? bf16_hi(w[j / 2]) : bf16_lo(w[j / 2]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (j < n) v[j] = bf16_to_f32(from[j]);
-        }
+        for (int j = 0; j < 8; ++j) v[j] = j & 1 ? bf16_hi(w[j / 2]) : bf16_lo(w[j / 2]);
     }
 }
 
@@ -806,7 +822,7 @@ linear_kernel(const __grid_constant__ LinearParams p)
     } else {
         // Warps w, w + 4, ... read the same 32 rows (a warp reaches the tensor memory
         // lanes of its number modulo 4) and take columns in turn.
-        const uint32_t quad = half * kM + (warp & 3) * 32;   // first of this warp's rows in the tile
+        const uint32_t quad = (warp & 3) * 32;   // first of this warp's rows in the CTA's
         unsigned char *buf = out_buf + warp * kStageOut, *biases = ctl + kBarBytes + warp * kStep * 2;
         for (uint32_t u = 0; next_tile<KIND>(p, worker, workers, u, t); ++u) {
             const bool ok = wait(acc_full + 8 * (u & 1), (u >> 1) & 1);
@@ -822,9 +838,9 @@ linear_kernel(const __grid_constant__ LinearParams p)
                 }
             };
             if (kBack && t.second)
-                finish_tile<KIND, Second>(p, p.product[1], t, acc, kM * CG, quad, warp >> 2, buf, biases, give_back);
+                finish_tile<KIND, Second>(p, p.product[1], t, acc, t.m * CG + half, p.product[1].mt * CG, quad, warp >> 2, buf, biases, give_back);
             else
-                finish_tile<KIND, First>(p, p.product[0], t, acc, kM * CG, quad, warp >> 2, buf, biases, give_back);
+                finish_tile<KIND, First>(p, p.product[0], t, acc, t.m * CG + half, p.product[0].mt * CG, quad, warp >> 2, buf, biases, give_back);
         }
     }
     tc_fence_before();
@@ -839,7 +855,7 @@ linear_kernel(const __grid_constant__ LinearParams p)
 // The sums of a product's splits into one, four columns a thread, and what follows
 // a sum.  A row of blocks to a row of the output.
 template <int KIND, bool SECOND>
-__global__ void __launch_bounds__(kThreads) linear_join_kernel(const __grid_constant__ LinearParams p, uint32_t high)
+__global__ void __launch_bounds__(kThreads) linear_join_kernel(const __grid_constant__ LinearParams p)
 {
     using R = Roles<KIND, SECOND>;
     DT_TL_BEGIN();
@@ -848,12 +864,12 @@ __global__ void __launch_bounds__(kThreads) linear_join_kernel(const __grid_cons
     const LinearProduct &c = p.product[SECOND];
     const uint32_t pitch = c.nt * p.bn, col = (blockIdx.x * kThreads + threadIdx.x) * 4;
     if (col < pitch) {
-        const Place m = locate<R, R::m>(p, c, blockIdx.y / high, high), n = locate<R, R::n>(p, c, col / p.bn, p.bn);
-        const uint32_t row = blockIdx.y % high, rows = length<R, R::m>(p, m.piece) - m.at;
+        const Place m = locate<R, R::m>(p, c, blockIdx.y / kM, kM), n = locate<R, R::n>(p, c, col / p.bn, p.bn);
+        const uint32_t row = blockIdx.y % kM, len = length<R, R::m>(p, m.piece), rows = m.at < len ? len - m.at : 0;
         const uint32_t e = col % p.bn, cols = length<R, R::n>(p, n.piece) - n.at;
         if (row < rows && e < cols) {
             const float4 *from = reinterpret_cast<const float4 *>(c.acc + (uint64_t)blockIdx.y * pitch + col);
-            const uint64_t step = (uint64_t)c.mt * high * pitch / 4;
+            const uint64_t step = (uint64_t)gridDim.y * pitch / 4;
             float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 8
             for (uint32_t k = 0; k < c.splits; ++k)
@@ -923,9 +939,8 @@ __device__ __forceinline__ void few_load(const LinearFew &p, const uint16_t *row
         if (!LINEAR_OK(buffer, row + k, 16)) return;
         asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(row + k));
     } else {
-#pragma unroll
-        for (uint32_t j = 0; j < 8; ++j)
-            if (k + j < len && LINEAR_OK(buffer, row + k + j, 2)) w[j / 2] |= (uint32_t)row[k + j] << (j & 1) * 16;
+        const uint32_t n = min(len - k, 8u);
+        if (LINEAR_OK(buffer, row + k, 2 * n)) load_shifted(row + k, n, w);
     }
 }
 
@@ -1075,14 +1090,7 @@ __global__ void __launch_bounds__(kThreads) linear_prep_kernel(const __grid_cons
         const uint16_t *at = base + (uint64_t)row * job.cols + e;
         w[0] = w[1] = w[2] = w[3] = 0;
         if (n == 0 || !LINEAR_OK(buffer, at, 2 * n)) return;
-        if (n == 8 && (reinterpret_cast<uintptr_t>(at) & 15) == 0) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(at);
-            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-        } else {
-#pragma unroll
-            for (uint32_t j = 0; j < 8; ++j)
-                if (j < n) w[j / 2] |= (uint32_t)at[j] << (j & 1) * 16;
-        }
+        load_shifted(at, n, w);
     };
     float sum[8] = {};
     constexpr uint32_t kBatch = 4;   // rows whose loads are under way together
@@ -1157,7 +1165,7 @@ cudaError_t launch_join(const LinearParams &p, uint32_t high, cudaStream_t s)
 {
     const LinearProduct &c = p.product[SECOND];
     return launch_kernel(linear_join_kernel<KIND, SECOND>, dim3((c.nt * p.bn / 4 + kThreads - 1) / kThreads, c.mt * high),
-                         dim3(kThreads), 0, s, false, p, high);
+                         dim3(kThreads), 0, s, false, p);
 }
 
 template <int KIND, int NT, bool VEC>

@@ -42,11 +42,11 @@ __host__ __device__ constexpr uint32_t linear_depth(bool back) { return back ? 1
 struct LinearProduct {
     uint32_t mt, nt, splits, tiles;    // tiles = mt * nt * splits
     uint32_t kblocks;                  // blocks of the inner axis
-    uint32_t f_end[DT_MAX_RANKS];      // the ranks' features and tokens in tiles or blocks, as their axis is cut
-    uint32_t t_end[DT_MAX_RANKS];      // here, numbered through: rank r's end at [r]
+    uint32_t f_end[DT_MAX_RANKS];      // the ranks' features and tokens in halves of 128 rows of a tile, its columns or
+    uint32_t t_end[DT_MAX_RANKS];      // blocks, as their axis is cut here, numbered through: rank r's end at [r]
     uint16_t *out[DT_MAX_RANKS];
     uint32_t align[DT_MAX_RANKS];      // elements that the rows of out[r] (and pre[r], residual[r]) are a multiple of: 1, 2, 4, 8
-    float *acc;                        // splits > 1: sums [splits][mt tiles' rows][nt tiles' columns]
+    float *acc;                        // splits > 1: sums [splits][tiles' rows][tiles' columns]
 };
 
 // The bias' gradient: column sums of bf16 matrices, or of the floats that were summed
