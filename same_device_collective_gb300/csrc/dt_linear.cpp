@@ -60,7 +60,7 @@ struct Cut {
 // axis take the tensor cores 128 cycles whatever a tile's width (measured from 64 to 256
 // columns: reading 128 rows of A bounds it), a tile costs a microsecond beside that, and
 // splits cost a second launch and their sums' way to L2 and back.
-constexpr double kUsPer64 = 0.29, kUsTile = 1.0, kUsJoin = 3.0, kJoinBytesPerUs = 5e6;
+constexpr double kUsPer64 = 0.34, kUsTile = 1.0, kUsJoin = 2.5, kJoinBytesPerUs = 8e6;
 
 double join_cost(const Plan &v, const Cut &c)
 {
@@ -164,13 +164,15 @@ size_t workspace_bytes_of(dt_group_t g, LinearKind fwd, const size_t *rows, size
 }
 
 // Whether the bias' gradient is summed down all rows by the warps beside the products, or
-// its rows are summed in chunks before them: a warp's loads of 32 rows of 32 columns are
-// about a microsecond under way, which should hide behind the products.
+// its rows are summed in chunks before them (a launch more): a warp's loads of 64 rows of
+// 32 columns are about two microseconds under way beside the products' own, which should
+// take half of the products' time at most (5000 tokens, 2000 columns: a walk of 79 steps
+// beside products of 200 us).
 bool sums_beside(const dt_group *g, const Plan &v)
 {
     const uint64_t cols = gathers(v.kind) ? v.features : v.dim, warps = dt::linear_workers(v.pairs, g->device) * (v.pairs ? 4 : 2);
-    const double walk = (double)tiles_of(v.tokens, 32) * tiles_of(tiles_of(cols, 32), warps);
-    return walk <= 4.0 + 4.0 * v.tokens * v.dim * v.features / 1.6e9;
+    const double walk = 2.0 * tiles_of(v.tokens, 64) * tiles_of(tiles_of(cols, 32), warps);
+    return walk <= 4.0 + 2.0 * v.tokens * v.dim * v.features / 1.6e9;
 }
 
 // A call on its way: its plan, its buffers, and what goes before its products.

@@ -519,21 +519,33 @@ __device__ __forceinline__ void move_rows(const LinearParams &p, unsigned char *
     }
 }
 
-// The same for rows that begin at any element: an element to a lane, a row at a time.
+// The same for rows that begin at any element: an element to a lane, a row at a time,
+// the loads of 16 rows under way together.
 template <bool STORE>
 __device__ __forceinline__ void move_rows_odd(const LinearParams &p, unsigned char *buf, uint16_t *row, uint32_t cols, int buffer)
 {
     (void)p;
     const uint32_t lane = threadIdx.x & 31;
-#pragma unroll 8
-    for (uint32_t r = 0; r < 32; ++r) {
-        uint16_t *at = lane_pointer(row, r);
-        const int of = __shfl_sync(0xFFFFFFFFu, buffer, r);
-        (void)of;
-        uint16_t *word = reinterpret_cast<uint16_t *>(step_chunk(buf, r, lane >> 3) + (lane & 7) * 2);
-        if (!at || lane >= cols || !LINEAR_OK(of, at + lane, 2)) continue;
-        if constexpr (STORE) at[lane] = *word;
-        else *word = at[lane];
+#pragma unroll
+    for (uint32_t r0 = 0; r0 < 32; r0 += 16) {
+        uint16_t v[16];
+#pragma unroll
+        for (uint32_t k = 0; k < 16; ++k) {
+            uint16_t *at = lane_pointer(row, r0 + k);
+            const int of = __shfl_sync(0xFFFFFFFFu, buffer, r0 + k);
+            (void)of;
+            const bool there = at && lane < cols && LINEAR_OK(of, at + lane, 2);
+            v[k] = 0;
+            if constexpr (STORE) {
+                if (there) at[lane] = *reinterpret_cast<uint16_t *>(step_chunk(buf, r0 + k, lane >> 3) + (lane & 7) * 2);
+            } else {
+                if (there) v[k] = at[lane];
+            }
+        }
+        if constexpr (!STORE)
+#pragma unroll
+            for (uint32_t k = 0; k < 16; ++k)
+                *reinterpret_cast<uint16_t *>(step_chunk(buf, r0 + k, lane >> 3) + (lane & 7) * 2) = v[k];
     }
 }
 
@@ -663,36 +675,7 @@ __device__ __forceinline__ void finish_tile(const LinearParams &p, const LinearP
 
 // ---- the bias' gradient: column sums ---------------------------------------------
 
-// Eight values of a row of column sums' source, bf16 or floats, from its element e on.
-__device__ __forceinline__ void sum_load(const LinearParams &p, const LinearSums &c, int k, uint32_t row, uint32_t cols,
-                                         uint32_t e, float (&v)[8])
-{
-    const uint64_t at = (uint64_t)row * cols + e;
-    const uint32_t n = e < cols ? min(cols - e, 8u) : 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-    if (c.f32) {
-        const float *from = static_cast<const float *>(c.src[k]) + at;
-        if (n == 0 || !LINEAR_OK(kLinearWorkspace, from, 4 * n)) return;
-        if (n == 8 && (reinterpret_cast<uintptr_t>(from) & 15) == 0) {
-            const float4 a = reinterpret_cast<const float4 *>(from)[0], b = reinterpret_cast<const float4 *>(from)[1];
-            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (j < n) v[j] = from[j];
-        }
-    } else {
-        const uint16_t *from = static_cast<const uint16_t *>(c.src[k]) + at;
-        if (n == 0 || !LINEAR_OK(kLinearDy + k, from, 2 * n)) return;
-        uint32_t w[4];
-        load_shifted(from, n, w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = j & 1 ? bf16_hi(w[j / 2]) : bf16_lo(w[j / 2]);
-    }
-}
-
-// 32 columns a warp, which walks down the rows eight at a time, four lanes to a row;
+// 32 columns a warp, which walks down the rows four lanes to a row;
 // warp `i` of `all` takes the groups of 32 columns i, i + all, ...
 __device__ __forceinline__ void column_sums(const LinearParams &p, uint32_t i, uint32_t all)
 {
@@ -703,17 +686,40 @@ __device__ __forceinline__ void column_sums(const LinearParams &p, uint32_t i, u
         uint32_t begin = 0;
         while (k + 1 < c.n && i >= c.group_end[k]) begin = c.group_end[k++];
         const uint32_t e = (i - begin) * 32 + lane % 4 * 8, cols = c.cols[k];
+        const uint32_t n = e < cols ? min(cols - e, 8u) : 0;
         float sum[8] = {};
-        for (int q = c.stacked ? 0 : k; q < (c.stacked ? c.sources : k + 1); ++q)
-            for (uint32_t first = lane / 4; first < c.rows[q]; first += 32) {
-                float v[4][8];
+        for (int q = c.stacked ? 0 : k; q < (c.stacked ? c.sources : k + 1); ++q) {
+            if (c.f32) {
+                for (uint32_t first = lane / 4; first < c.rows[q]; first += 32) {
+                    float v[4][8];
 #pragma unroll
-                for (uint32_t j = 0; j < 4; ++j) sum_load(p, c, q, first + 8 * j, cols, first + 8 * j < c.rows[q] ? e : cols, v[j]);
+                    for (uint32_t j = 0; j < 4; ++j) {
+                        const float *from = static_cast<const float *>(c.src[q]) + (uint64_t)(first + 8 * j) * cols + e;
 #pragma unroll
-                for (uint32_t j = 0; j < 4; ++j)
+                        for (uint32_t z = 0; z < 8; ++z)
+                            v[j][z] = first + 8 * j < c.rows[q] && z < n && LINEAR_OK(kLinearWorkspace, from + z, 4) ? from[z] : 0.0f;
+                    }
 #pragma unroll
-                    for (int z = 0; z < 8; ++z) sum[z] += v[j][z];
+                    for (uint32_t j = 0; j < 4; ++j)
+#pragma unroll
+                        for (uint32_t z = 0; z < 8; ++z) sum[z] += v[j][z];
+                }
+            } else {
+                for (uint32_t first = lane / 4; first < c.rows[q]; first += 64) {
+                    uint32_t w[8][4];
+#pragma unroll
+                    for (uint32_t j = 0; j < 8; ++j) {
+                        const uint16_t *from = static_cast<const uint16_t *>(c.src[q]) + (uint64_t)(first + 8 * j) * cols + e;
+                        w[j][0] = w[j][1] = w[j][2] = w[j][3] = 0;
+                        if (first + 8 * j < c.rows[q] && n && LINEAR_OK(kLinearDy + q, from, 2 * n)) load_shifted(from, n, w[j]);
+                    }
+#pragma unroll
+                    for (uint32_t j = 0; j < 8; ++j)
+#pragma unroll
+                        for (uint32_t z = 0; z < 8; ++z) sum[z] += z & 1 ? bf16_hi(w[j][z / 2]) : bf16_lo(w[j][z / 2]);
+                }
             }
+        }
 #pragma unroll
         for (uint32_t o = 4; o < 32; o *= 2)
 #pragma unroll
