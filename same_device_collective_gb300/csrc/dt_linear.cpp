@@ -22,7 +22,7 @@ struct Plan {
     size_t tokens, features, dim;
     bool pairs;                        // two CTAs share a tile
     uint32_t halves;                   // of 128 rows in a tile: 1 or 2, each within a rank's piece
-    uint64_t chunks;                   // of rows, whose column sums the bias' gradient adds
+    uint64_t chunk_rows, chunks;       // of rows, whose column sums the bias' gradient adds
     uint64_t tok, feat, w, sums, acc[2], bytes;
 };
 
@@ -124,6 +124,10 @@ bool plan(const dt_group *g, LinearKind kind, const size_t *rows, size_t rows_eq
     v.kind = kind;
     v.dim = dim;
     uint64_t padded = 0;
+    for (int r = 0; r < g->P; ++r) v.tokens += rows ? rows[r] : rows_equal;
+    // few rows: more blocks; many: fewer partial sums
+    v.chunk_rows = v.tokens <= 2048 ? 32 : 128;
+    v.tokens = 0;
     for (int r = 0; r < g->P; ++r) {
         v.n[r] = rows ? rows[r] : rows_equal;
         v.f[r] = features ? features[r] : features_equal;
@@ -131,10 +135,10 @@ bool plan(const dt_group *g, LinearKind kind, const size_t *rows, size_t rows_eq
         v.tokens += v.n[r];
         v.features += v.f[r];
         padded += up(v.f[r], 8);
-        v.chunks += gathers(kind) ? 0 : tiles_of(v.n[r], dt::kPrepRows);
+        v.chunks += gathers(kind) ? 0 : tiles_of(v.n[r], v.chunk_rows);
     }
     if (v.tokens > kMaxTokens || v.features > kMaxWidth || v.features == 0) return false;
-    if (gathers(kind)) v.chunks = tiles_of(v.tokens, dt::kPrepRows);
+    if (gathers(kind)) v.chunks = tiles_of(v.tokens, v.chunk_rows);
     v.pairs = v.tokens > 128;
     v.halves = v.pairs ? 2 : 1;
     uint64_t at = 0;
@@ -216,6 +220,9 @@ uint32_t alignment(uint32_t least, const void *p, size_t width)
     return least;
 }
 
+// TMA, and loads of vectors, can read a matrix of rows of `width`.
+bool addressable(const void *p, size_t width) { return width % 8 == 0 && aligned16(p); }
+
 // A job of the launch before the products.
 void add_job(Call &c, const void *src, const void *pre, void *dst, float *sums, size_t rows, size_t cols, size_t pitch,
              int src_buffer, int pre_buffer)
@@ -230,13 +237,12 @@ void add_job(Call &c, const void *src, const void *pre, void *dst, float *sums, 
     j.cols = (uint32_t)cols;
     j.pitch = (uint32_t)pitch;
     j.strips = (uint32_t)tiles_of(cols, dt::kPrepCols);
-    j.block_end = (c.prep.jobs ? c.prep.job[c.prep.jobs - 1].block_end : 0) + j.strips * (uint32_t)tiles_of(rows, dt::kPrepRows);
+    j.block_end = (c.prep.jobs ? c.prep.job[c.prep.jobs - 1].block_end : 0) + j.strips * (uint32_t)tiles_of(rows, c.v.chunk_rows);
     j.src_buffer = src_buffer;
     j.pre_buffer = pre_buffer;
+    j.vec = addressable(src, cols) && (!pre || addressable(pre, cols));
     ++c.prep.jobs;
 }
-
-bool addressable(const void *p, size_t width) { return width % 8 == 0 && aligned16(p); }
 
 // Checks what all calls share.
 dt_status begin(Call &c, LinearKind kind, const size_t *rows, size_t rows_equal, size_t dim, const size_t *features,
@@ -261,6 +267,7 @@ dt_status begin(Call &c, LinearKind kind, const size_t *rows, size_t rows_equal,
     p.P = c.g->P;
     p.tokens = (uint32_t)c.v.tokens;
     p.dim = (uint32_t)dim;
+    c.prep.chunk_rows = (uint32_t)c.v.chunk_rows;
     p.sink = c.prep.sink = error_sink(c.g);
     workspace_extent(p, c);
     workspace_extent(c.prep, c);
@@ -299,7 +306,7 @@ void token_matrix(Call &c, const void *const *x, int buffer, float *sums)
     for (int r = 0; r < c.g->P && (again || sums); ++r) {
         add_job(c, x[r], nullptr, again ? to + first * c.tok_pitch * 2 : nullptr, sums ? sums + chunk * v.dim : nullptr, v.n[r],
                 v.dim, c.tok_pitch, buffer + r, 0);
-        chunk += tiles_of(v.n[r], dt::kPrepRows);
+        chunk += tiles_of(v.n[r], v.chunk_rows);
         first += v.n[r];
     }
     if (again) c.tok[0] = to;

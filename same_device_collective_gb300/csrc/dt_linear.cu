@@ -48,15 +48,17 @@ constexpr uint32_t kM = 128;                       // rows of a tile in a CTA
 constexpr uint32_t kRingBytes = 192 * 1024;        // three or six stages of 128 rows and columns of A and B
 constexpr uint32_t kMaxStages = 16;
 constexpr uint32_t kTmemColumns = 512;             // two accumulators of 128 x 256 fp32
-// Finishing warps (16 take as long), one for TMA, one for the products, and backward two
-// for the bias' gradient.
-constexpr uint32_t kFinishWarps = 8, kSumWarps = 2;
-__host__ __device__ constexpr int tc_threads(bool back) { return (kFinishWarps + 2 + (back ? kSumWarps : 0)) * 32; }
-constexpr uint32_t kColumnGroups = kFinishWarps / 4;
+// Finishing warps, FW: eight, or of gathering layers with a short inner axis, whose finish
+// with its activation takes longer than the products, 16 (512 tokens of 1024 to 4 x 1024
+// with silu: 15.8 us, 14.1 with 16; 2048 of 4096 to 16384: 146 us, 149 with 16).  Then
+// one for TMA, one for the products, and backward two for the bias' gradient.
+constexpr uint32_t kShortBlocks = 16;              // of 64: blocks of a short inner axis, at most
+constexpr uint32_t kMostFinishWarps = 16, kSumWarps = 2;
+__host__ __device__ constexpr int tc_threads(bool back, uint32_t fw) { return (fw + 2 + (back ? kSumWarps : 0)) * 32; }
 constexpr uint32_t kStep = 32;                     // columns that a finishing warp takes at a time
 constexpr uint32_t kStageOut = 32 * kStep * 2;     // its 32 rows of them in bf16
-constexpr uint32_t kOutBytes = kFinishWarps * kStageOut;
-constexpr uint32_t kBarBytes = 384, kBiasBytes = kFinishWarps * kStep * 2;
+constexpr uint32_t kOutBytes = kMostFinishWarps * kStageOut;
+constexpr uint32_t kBarBytes = 384, kBiasBytes = kMostFinishWarps * kStep * 2;
 constexpr size_t kTcSmem = 1024 + kRingBytes + kOutBytes + kBarBytes + kBiasBytes;
 static_assert(kTcSmem <= 227 * 1024, "shared memory above the per-block limit");
 // Columns of tiles that are worked on together, rows fastest, so that the tiles in
@@ -361,6 +363,15 @@ __device__ __forceinline__ float2 normal_tail(float2 v, float2 &bell)
     return mul2(mul2(s, t), bell);
 }
 
+// v times the normal distribution at v, from its tail: max(v, 0) - |v| tail.  An infinite
+// |v| would make the product with a tail of zero no number; a NaN stays one.
+__device__ __forceinline__ float gelu_of(float v, float q)
+{
+    float a;
+    asm("{\n\t.reg .f32 t;\n\tabs.f32 t, %1;\n\tmin.NaN.f32 %0, t, 0f7F7FFFFF;\n\t}" : "=f"(a) : "f"(v));
+    return fmaf(-a, q, fmaxf(v, 0.0f));
+}
+
 // The normal distribution from its tail.
 __device__ __forceinline__ float2 normal_of(float2 v, float2 q)
 {
@@ -383,7 +394,7 @@ __device__ __forceinline__ float2 activate(float2 v)
     if (ACT == DT_ACT_GELU) {
         float2 bell;
         const float2 q = normal_tail(v, bell);
-        return mul2(v, normal_of(v, q));
+        return make_float2(gelu_of(v.x, q.x), gelu_of(v.y, q.y));
     }
     return v;
 }
@@ -574,47 +585,76 @@ __device__ __forceinline__ void store_rows(const LinearParams &p, unsigned char 
     move_rows<true>(p, buf, row, cols, align, buffer);
 }
 
-// v += 32 bf16 values in four chunks.
-template <class Chunk>
-__device__ __forceinline__ void add_chunks(float (&v)[kStep], const Chunk &chunk)
+// v += 32 bf16 values in four vectors.
+template <class Vector>
+__device__ __forceinline__ void add_vectors(float (&v)[kStep], const Vector &vector)
 {
 #pragma unroll
     for (uint32_t j = 0; j < kStep / 8; ++j) {
-        const uint4 b = *reinterpret_cast<const uint4 *>(chunk(j));
+        const uint4 b = vector(j);
         const uint32_t w[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
         for (uint32_t q = 0; q < 4; ++q) {
-            v[8 * j + 2 * q] += bf16_lo(w[q]);
-            v[8 * j + 2 * q + 1] += bf16_hi(w[q]);
+            const float2 f = add2(make_float2(v[8 * j + 2 * q], v[8 * j + 2 * q + 1]), make_float2(bf16_lo(w[q]), bf16_hi(w[q])));
+            v[8 * j + 2 * q] = f.x, v[8 * j + 2 * q + 1] = f.y;
         }
     }
 }
 
+// What a step of 32 columns adds to its sums, on its way while the accumulator is waited
+// for: the bias, a column to a lane, and, where rows are whole vectors, this lane's row
+// of the residual.
+struct Extra {
+    uint16_t bias;
+    uint4 residual[kStep / 8];
+};
+
+template <int KIND>
+__device__ __forceinline__ void fetch(const LinearParams &p, const OutRow &o, bool there, const Place &n, uint32_t c,
+                                      uint32_t cols, uint32_t align, Extra &x)
+{
+    if (!is_back(KIND) && p.biased) {
+        // one bias for all ranks' tokens, or each rank's own for its features
+        const uint32_t r = KIND == kGather ? n.piece : 0, lane = threadIdx.x & 31;
+        const uint16_t *from = p.bias[r] + n.at + c + lane;
+        x.bias = c + lane < cols && LINEAR_OK(kLinearBias + r, from, 2) ? *from : 0;
+    }
+    if (KIND == kReduce && p.residuals && align == 8) {
+        const uint16_t *from = p.residual[o.rank] + o.offset + c;
+#pragma unroll
+        for (uint32_t j = 0; j < kStep / 8; ++j)
+            x.residual[j] = there && c + 8 * j < cols && LINEAR_OK(kLinearResidual + o.rank, from + 8 * j, 16)
+                                ? *reinterpret_cast<const uint4 *>(from + 8 * j)
+                                : make_uint4(0, 0, 0, 0);
+    }
+}
+
 // 32 sums of this lane's row, whose columns begin at column `c` of the tile: bias,
-// residual, activation, and to memory.
-template <int KIND, class R>
+// residual, activation, and to memory.  `next` fetches what the next step adds.
+template <int KIND, class R, class Next>
 __device__ __forceinline__ void finish_row(const LinearParams &p, unsigned char *buf, unsigned char *biases,
-                                           float (&v)[kStep], const OutRow &o, bool there, const Place &n, uint32_t c,
-                                           uint32_t cols, uint32_t align)
+                                           float (&v)[kStep], const Extra &x, const OutRow &o, bool there, uint32_t c,
+                                           uint32_t cols, uint32_t align, const Next &next)
 {
     const uint32_t lane = threadIdx.x & 31;
     if (!is_back(KIND) && p.biased) {
-        // one bias for all ranks' tokens, or each rank's own for its features
-        const uint32_t r = KIND == kGather ? n.piece : 0;
-        const uint16_t *from = p.bias[r] + n.at + c + lane;
-        const uint16_t w = lane < cols && LINEAR_OK(kLinearBias + r, from, 2) ? *from : 0;
         __syncwarp();
-        reinterpret_cast<uint16_t *>(biases)[lane] = w;
+        reinterpret_cast<uint16_t *>(biases)[lane] = x.bias;
         __syncwarp();
-        add_chunks(v, [&](uint32_t j) { return biases + 16 * j; });
+        add_vectors(v, [&](uint32_t j) { return reinterpret_cast<const uint4 *>(biases)[j]; });
     }
     if (KIND == kReduce && p.residuals) {
-        uint16_t *from = there ? const_cast<uint16_t *>(p.residual[o.rank]) + o.offset + c : nullptr;
-        __syncwarp();
-        move_rows<false>(p, buf, from, cols, align, kLinearResidual + o.rank);
-        __syncwarp();
-        add_chunks(v, [&](uint32_t j) { return step_chunk(buf, lane, j); });
+        if (align == 8) {
+            add_vectors(v, [&](uint32_t j) { return x.residual[j]; });
+        } else {
+            uint16_t *from = there ? const_cast<uint16_t *>(p.residual[o.rank]) + o.offset + c : nullptr;
+            __syncwarp();
+            move_rows<false>(p, buf, from, cols, align, kLinearResidual + o.rank);
+            __syncwarp();
+            add_vectors(v, [&](uint32_t j) { return *reinterpret_cast<const uint4 *>(step_chunk(buf, lane, j)); });
+        }
     }
+    next();
     if (KIND == kGather && p.keep)
         store_rows(p, buf, v, there ? p.pre[o.rank] + o.offset + c : nullptr, cols, align, kLinearPre + o.rank);
     if (KIND == kGather) activate(v, p.act);
@@ -623,12 +663,13 @@ __device__ __forceinline__ void finish_row(const LinearParams &p, unsigned char 
 }
 
 // One tile's accumulator, by a warp whose 32 rows begin at row `quad` of the CTA's 128
-// (number `unit` along the rows' axis) and which takes steps of 32 columns in turn, from `group` on.  `give_back` hands the
-// accumulator over as soon as the warp has read its part.
-template <int KIND, class R, class GiveBack>
-__device__ __forceinline__ void finish_tile(const LinearParams &p, const LinearProduct &c, const Tile &t, uint32_t acc,
+// (number `unit` along the rows' axis) and which takes steps of 32 columns in turn, from `group` on.  `take` waits
+// for the accumulator (false: it gave up), `give_back` hands it over as soon as the warp
+// has read its part.
+template <int KIND, uint32_t FW, class R, class Take, class GiveBack>
+__device__ __forceinline__ bool finish_tile(const LinearParams &p, const LinearProduct &c, const Tile &t, uint32_t acc,
                                             uint32_t unit, uint32_t units, uint32_t quad, uint32_t group, unsigned char *buf,
-                                            unsigned char *biases, const GiveBack &give_back)
+                                            unsigned char *biases, const Take &take, const GiveBack &give_back)
 {
     const Place m = locate<R, R::m>(p, c, unit, kM), n = locate<R, R::n>(p, c, t.n, p.bn);
     const uint32_t lane = threadIdx.x & 31, row = quad + lane, len = length<R, R::m>(p, m.piece);
@@ -636,20 +677,26 @@ __device__ __forceinline__ void finish_tile(const LinearParams &p, const LinearP
     const bool there = row < rows;
     const bool none = group * kStep >= cols || quad >= rows;
     if (none) {
+        if (!take()) return false;
         give_back();
-        return;
+        return true;
     }
     const OutRow o = c.splits > 1 ? OutRow{} : out_row<R>(p, c, m, n, there ? row : 0);
     // the rows of a warp may lie on several ranks, whose buffers are aligned alike (the host says how)
     const uint32_t align = c.align[R::m == kTokens && R::n == kDim ? 0 : o.rank];
     const uint64_t pitch = (uint64_t)c.nt * p.bn;
     float *part = c.acc + (((uint64_t)t.split * units + unit) * kM + quad) * pitch + t.n * p.bn;
-    for (uint32_t b = group * kStep; b < cols; b += kColumnGroups * kStep) {
+    Extra x;
+    if (c.splits == 1) fetch<KIND>(p, o, there, n, group * kStep, cols, align, x);
+    if (!take()) return false;
+    for (uint32_t b = group * kStep; b < cols; b += FW / 4 * kStep) {
         float v[kStep];
         tmem_load32(acc + b, v);
-        if (b + kColumnGroups * kStep >= cols) give_back();
+        if (b + FW / 4 * kStep >= cols) give_back();
         if (c.splits == 1) {
-            finish_row<KIND, R>(p, buf, biases, v, o, there, n, b, min(cols - b, kStep), align);
+            finish_row<KIND, R>(p, buf, biases, v, x, o, there, b, min(cols - b, kStep), align, [&] {
+                if (b + FW / 4 * kStep < cols) fetch<KIND>(p, o, there, n, b + FW / 4 * kStep, cols, align, x);
+            });
             continue;
         }
         // fp32 sums: 16 columns at a time through shared memory, so that four threads
@@ -671,6 +718,7 @@ __device__ __forceinline__ void finish_tile(const LinearParams &p, const LinearP
             }
         }
     }
+    return true;
 }
 
 // ---- the bias' gradient: column sums ---------------------------------------------
@@ -731,8 +779,8 @@ __device__ __forceinline__ void column_sums(const LinearParams &p, uint32_t i, u
     }
 }
 
-template <int KIND, int CG>
-__global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(tc_threads(is_back(KIND)), 1)
+template <int KIND, int CG, uint32_t FW>
+__global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(tc_threads(is_back(KIND), FW), 1)
 linear_kernel(const __grid_constant__ LinearParams p)
 {
     using First = Roles<KIND, false>;
@@ -761,13 +809,13 @@ linear_kernel(const __grid_constant__ LinearParams p)
         }
         for (uint32_t s = 0; s < 2; ++s) {
             mbar_init(acc_full + 8 * s, 1);
-            mbar_init(acc_empty + 8 * s, kFinishWarps * CG);
+            mbar_init(acc_empty + 8 * s, FW * CG);
         }
         mbar_init(drained, 1);
         *gave_up = 0;
         mbar_init_fence();
     }
-    if (warp == kFinishWarps + 1) tmem_alloc<CG>(smem_addr(const_cast<uint32_t *>(tmem_slot)), kTmemColumns);
+    if (warp == FW + 1) tmem_alloc<CG>(smem_addr(const_cast<uint32_t *>(tmem_slot)), kTmemColumns);
     tc_fence_before();
     __syncwarp();
     if (CG == 2) cluster_sync();
@@ -780,7 +828,7 @@ linear_kernel(const __grid_constant__ LinearParams p)
     const Waits wait{p.sink, gave_up};
     const uint32_t a_box = a_box_bytes(kBack, p.rows_t), stage_bytes = stage_size(kBack, p.rows_t, p.bn / CG);
 
-    if (warp == kFinishWarps) {
+    if (warp == FW) {
         if (lane == 0) {
             uint32_t n = 0, s = 0, round = 0;   // loads issued; the next one's stage and its parity
             bool ok = true;
@@ -801,7 +849,7 @@ linear_kernel(const __grid_constant__ LinearParams p)
             }
         }
         __syncwarp();
-    } else if (warp == kFinishWarps + 1) {
+    } else if (warp == FW + 1) {
         if (lane == 0 && half == 0) {
             uint32_t s = 0, round = 0;
             bool ok = true;
@@ -823,18 +871,20 @@ linear_kernel(const __grid_constant__ LinearParams p)
             }
         }
         __syncwarp();
-    } else if (kBack && warp >= kFinishWarps + 2) {
-        column_sums(p, blockIdx.x * kSumWarps + warp - kFinishWarps - 2, gridDim.x * kSumWarps);
+    } else if (kBack && warp >= FW + 2) {
+        column_sums(p, blockIdx.x * kSumWarps + warp - FW - 2, gridDim.x * kSumWarps);
     } else {
         // Warps w, w + 4, ... read the same 32 rows (a warp reaches the tensor memory
         // lanes of its number modulo 4) and take columns in turn.
         const uint32_t quad = (warp & 3) * 32;   // first of this warp's rows in the CTA's
         unsigned char *buf = out_buf + warp * kStageOut, *biases = ctl + kBarBytes + warp * kStep * 2;
         for (uint32_t u = 0; next_tile<KIND>(p, worker, workers, u, t); ++u) {
-            const bool ok = wait(acc_full + 8 * (u & 1), (u >> 1) & 1);
-            tc_fence_after();
-            if (__any_sync(0xFFFFFFFFu, !ok)) break;
             const uint32_t acc = tmem + (u & 1) * 256 + ((warp & 3) * 32 << 16);
+            auto take = [&] {
+                const bool ok = wait(acc_full + 8 * (u & 1), (u >> 1) & 1);
+                tc_fence_after();
+                return !__any_sync(0xFFFFFFFFu, !ok);
+            };
             auto give_back = [&] {
                 tc_fence_before();
                 __syncwarp();
@@ -843,10 +893,12 @@ linear_kernel(const __grid_constant__ LinearParams p)
                     else mbar_arrive(acc_empty + 8 * (u & 1));
                 }
             };
-            if (kBack && t.second)
-                finish_tile<KIND, Second>(p, p.product[1], t, acc, t.m * CG + half, p.product[1].mt * CG, quad, warp >> 2, buf, biases, give_back);
-            else
-                finish_tile<KIND, First>(p, p.product[0], t, acc, t.m * CG + half, p.product[0].mt * CG, quad, warp >> 2, buf, biases, give_back);
+            const bool ok = kBack && t.second
+                                ? finish_tile<KIND, FW, Second>(p, p.product[1], t, acc, t.m * CG + half, p.product[1].mt * CG, quad,
+                                                            warp >> 2, buf, biases, take, give_back)
+                                : finish_tile<KIND, FW, First>(p, p.product[0], t, acc, t.m * CG + half, p.product[0].mt * CG, quad,
+                                                           warp >> 2, buf, biases, take, give_back);
+            if (!ok) break;
         }
     }
     tc_fence_before();
@@ -854,7 +906,7 @@ linear_kernel(const __grid_constant__ LinearParams p)
     if (CG == 2) cluster_sync();
     else __syncthreads();
     tc_fence_after();
-    if (warp == kFinishWarps + 1) tmem_free<CG>(tmem, kTmemColumns);
+    if (warp == FW + 1) tmem_free<CG>(tmem, kTmemColumns);
     DT_TL_END_BLOCK(DT_TL_LINEAR);
 }
 
@@ -1075,9 +1127,64 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kThreads) linear_few
     DT_TL_END_BLOCK(DT_TL_LINEAR);
 }
 
-// A strip of 256 columns of a chunk of 64 rows to a block: 32 threads across, eight
-// columns each, and eight rows at a time.
-__global__ void __launch_bounds__(kThreads) linear_prep_kernel(const __grid_constant__ LinearPrep p)
+// A strip of 256 columns of a chunk of rows to a block: 32 threads across, eight columns
+// each, and eight rows at a time, four of them under way for each thread.
+template <bool VEC>
+__device__ __forceinline__ void prep_rows(const LinearPrep &p, const LinearPrepJob &job, uint32_t first, uint32_t end, uint32_t e,
+                                          float (&sum)[8])
+{
+    constexpr uint32_t kBatch = 4;
+    const uint32_t n = e < job.cols ? min(job.cols - e, 8u) : 0;
+    auto load = [&](const uint16_t *base, uint32_t row, int buffer, uint32_t (&w)[4]) {
+        (void)buffer;
+        const uint16_t *at = base + (uint64_t)row * job.cols + e;
+        w[0] = w[1] = w[2] = w[3] = 0;
+        if (row >= end || n == 0 || !LINEAR_OK(buffer, at, 2 * n)) return;
+        if (VEC) {
+            const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(at));
+            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+        } else {
+            load_shifted(at, n, w);
+        }
+    };
+#pragma unroll 1
+    for (uint32_t row0 = first + threadIdx.x / 32; row0 < end; row0 += 8 * kBatch) {
+        uint32_t w[kBatch][4], u[kBatch][4];
+#pragma unroll
+        for (uint32_t k = 0; k < kBatch; ++k) {
+            load(job.src, row0 + 8 * k, job.src_buffer, w[k]);
+            if (job.pre) load(job.pre, row0 + 8 * k, job.pre_buffer, u[k]);
+        }
+#pragma unroll
+        for (uint32_t k = 0; k < kBatch; ++k) {
+            const uint32_t row = row0 + 8 * k;
+            if (row >= end) break;
+            if (job.pre || job.sums) {
+                float g[8];
+#pragma unroll
+                for (uint32_t j = 0; j < 8; ++j) g[j] = j & 1 ? bf16_hi(w[k][j / 2]) : bf16_lo(w[k][j / 2]);
+                if (job.pre) {
+                    float z[8];
+#pragma unroll
+                    for (uint32_t j = 0; j < 8; ++j) z[j] = j & 1 ? bf16_hi(u[k][j / 2]) : bf16_lo(u[k][j / 2]);
+                    times_slope(g, z, p.act);
+#pragma unroll
+                    for (uint32_t j = 0; j < 4; ++j) w[k][j] = pack_bf16x2(g[2 * j], g[2 * j + 1]);
+                }
+#pragma unroll
+                for (uint32_t j = 0; j < 8; j += 2) {
+                    const float2 f = add2(make_float2(sum[j], sum[j + 1]), make_float2(g[j], g[j + 1]));
+                    sum[j] = f.x, sum[j + 1] = f.y;
+                }
+            }
+            uint4 *to = reinterpret_cast<uint4 *>(job.dst + (uint64_t)row * job.pitch + e);
+            if (job.dst && e < job.pitch && LINEAR_OK(kLinearWorkspace, to, 16))
+                *to = make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kThreads, 4) linear_prep_kernel(const __grid_constant__ LinearPrep p)
 {
     __shared__ float part[8][kPrepCols + 4];
     DT_TL_BEGIN();
@@ -1088,52 +1195,14 @@ __global__ void __launch_bounds__(kThreads) linear_prep_kernel(const __grid_cons
     const LinearPrepJob &job = p.job[k];
     const uint32_t block = blockIdx.x - (k ? p.job[k - 1].block_end : 0);
     const uint32_t strip = block % job.strips, chunk = block / job.strips;
-    const uint32_t t = threadIdx.x % 32, r0 = threadIdx.x / 32, e = strip * kPrepCols + t * 8;
-    const uint32_t n = e < job.cols ? min(job.cols - e, 8u) : 0;
-    const uint32_t end = min((chunk + 1) * kPrepRows, job.rows);
-    auto load = [&](const uint16_t *base, uint32_t row, int buffer, uint32_t (&w)[4]) {
-        (void)buffer;
-        const uint16_t *at = base + (uint64_t)row * job.cols + e;
-        w[0] = w[1] = w[2] = w[3] = 0;
-        if (n == 0 || !LINEAR_OK(buffer, at, 2 * n)) return;
-        load_shifted(at, n, w);
-    };
+    const uint32_t first = chunk * p.chunk_rows, end = min(first + p.chunk_rows, job.rows);
+    const uint32_t t = threadIdx.x % 32, e = strip * kPrepCols + t * 8;
     float sum[8] = {};
-    constexpr uint32_t kBatch = 4;   // rows whose loads are under way together
-    for (uint32_t row0 = chunk * kPrepRows + r0; row0 < end; row0 += 8 * kBatch) {
-        uint32_t w[kBatch][4], u[kBatch][4];
-#pragma unroll
-        for (uint32_t k = 0; k < kBatch; ++k) {
-            const uint32_t row = row0 + 8 * k;
-            if (row < end) load(job.src, row, job.src_buffer, w[k]);
-            if (row < end && job.pre) load(job.pre, row, job.pre_buffer, u[k]);
-        }
-#pragma unroll
-        for (uint32_t k = 0; k < kBatch; ++k) {
-            const uint32_t row = row0 + 8 * k;
-            if (row >= end) break;
-            if (job.pre || job.sums) {
-                float g[8], z[8];
-#pragma unroll
-                for (uint32_t j = 0; j < 8; ++j) g[j] = j & 1 ? bf16_hi(w[k][j / 2]) : bf16_lo(w[k][j / 2]);
-                if (job.pre) {
-#pragma unroll
-                    for (uint32_t j = 0; j < 8; ++j) z[j] = j & 1 ? bf16_hi(u[k][j / 2]) : bf16_lo(u[k][j / 2]);
-                    times_slope(g, z, p.act);
-#pragma unroll
-                    for (uint32_t j = 0; j < 4; ++j) w[k][j] = pack_bf16x2(g[2 * j], g[2 * j + 1]);
-                }
-#pragma unroll
-                for (uint32_t j = 0; j < 8; ++j) sum[j] += g[j];
-            }
-            uint4 *to = reinterpret_cast<uint4 *>(job.dst + (uint64_t)row * job.pitch + e);
-            if (job.dst && e < job.pitch && LINEAR_OK(kLinearWorkspace, to, 16))
-                *to = make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
-        }
-    }
+    if (job.vec) prep_rows<true>(p, job, first, end, e, sum);
+    else prep_rows<false>(p, job, first, end, e, sum);
     if (job.sums) {
 #pragma unroll
-        for (uint32_t j = 0; j < 8; ++j) part[r0][t * 8 + j] = sum[j];
+        for (uint32_t j = 0; j < 8; ++j) part[threadIdx.x / 32][t * 8 + j] = sum[j];
         __syncthreads();
         const uint32_t c = strip * kPrepCols + threadIdx.x;
         float all = 0.0f;
@@ -1145,25 +1214,29 @@ __global__ void __launch_bounds__(kThreads) linear_prep_kernel(const __grid_cons
     DT_TL_END_BLOCK(DT_TL_LINEAR);
 }
 
-template <int KIND, int CG>
+template <int KIND, int CG, uint32_t FW>
 cudaError_t launch_kind(LinearParams &p, int device, cudaStream_t s)
 {
     static std::atomic<uint64_t> ready{0};   // devices whose shared memory limit is set
     const uint64_t bit = device < 64 ? 1ull << device : 0;
     if (!(ready.load(std::memory_order_acquire) & bit) || !bit) {
-        const cudaError_t e = cudaFuncSetAttribute(linear_kernel<KIND, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        const cudaError_t e = cudaFuncSetAttribute(linear_kernel<KIND, CG, FW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    (int)kTcSmem);
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit, std::memory_order_release);
     }
     p.stages = std::min(kMaxStages, kRingBytes / stage_size(is_back(KIND), p.rows_t, p.bn / CG));
-    return launch_kernel(linear_kernel<KIND, CG>, dim3(p.workers * CG), dim3(tc_threads(is_back(KIND))), kTcSmem, s, false, p);
+    return launch_kernel(linear_kernel<KIND, CG, FW>, dim3(p.workers * CG), dim3(tc_threads(is_back(KIND), FW)), kTcSmem, s,
+                         false, p);
 }
 
 template <int KIND>
 cudaError_t launch_kind(LinearParams &p, bool pairs, int device, cudaStream_t s)
 {
-    return pairs ? launch_kind<KIND, 2>(p, device, s) : launch_kind<KIND, 1>(p, device, s);
+    if constexpr (KIND == kGather)
+        if (p.product[0].kblocks <= kShortBlocks)
+            return pairs ? launch_kind<KIND, 2, 16>(p, device, s) : launch_kind<KIND, 1, 16>(p, device, s);
+    return pairs ? launch_kind<KIND, 2, 8>(p, device, s) : launch_kind<KIND, 1, 8>(p, device, s);
 }
 
 template <int KIND, bool SECOND>

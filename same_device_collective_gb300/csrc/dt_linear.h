@@ -98,11 +98,13 @@ struct LinearPrepJob {
     uint32_t strips;                   // of kPrepCols columns
     uint32_t block_end;                // of the launch's blocks
     int32_t src_buffer, pre_buffer;    // numbers of LinearBuffer
+    int32_t vec;                       // rows of src and pre are whole vectors
 };
-constexpr uint32_t kPrepCols = 256, kPrepRows = 64;
+constexpr uint32_t kPrepCols = 256;
 constexpr int kPrepJobs = 3 * DT_MAX_RANKS;
 struct LinearPrep {
     LinearPrepJob job[kPrepJobs];
+    uint32_t chunk_rows;               // of a block: a multiple of 32
     int32_t jobs, act;
     ErrorSink sink;
 #ifdef DT_BOUNDS
