@@ -10,8 +10,8 @@
 //   G = sum_rows d h    dpost = G gate    dgate = G post    dpre = sum_rows dz n
 //
 // Two weights' gradients come from one column sum, and both of a row's means from
-// one reduction: with g = gate post, sum(c h) = sum(g h dy) + r2 (sum(g h q) -
-// mean(q n) sum(g h n)), so that the four sums of a row cross its threads together.
+// one reduction: with g = gate post and e = dy + r2 q, sum(c h) = sum(g h e) - r2
+// mean(q n) sum(g h n), so that the three sums of a row cross its threads together.
 //
 // HBM bounds both directions (4 and 6 passes over the rows at 2 to 4 flops a byte), so
 // every row is read once.  Resident blocks, whose groups of threads each have a ring of
@@ -224,7 +224,7 @@ template <typename T, int VEC, int N, int L, bool BACK>
 __host__ __device__ constexpr int rows_at_once()
 {
     constexpr int raw = N * (VEC == 1 ? 1 : 4), cols = N * VEC;
-    constexpr int held = (BACK ? 4 : 2) * cols, row = BACK ? 4 * raw : 2 * raw + cols;
+    constexpr int held = (BACK ? 4 : 2) * cols, row = 2 * raw + cols;
     constexpr int most = BACK && L < 16 ? L / 4 : 4;   // row_sum: a value to a lane at least
     constexpr int room = BACK ? 72 : 96;
     return most >= 4 && held + 4 * row <= room ? 4 : most >= 2 && held + 2 * row <= room ? 2 : 1;
@@ -383,41 +383,45 @@ __global__ void __launch_bounds__(kNormThreads, 1) residual_backward_kernel(cons
         ring.wait();
         // this team's rows are the stage's k, k + S, ...
         for (uint32_t k = team.team; k - team.team < rows; k += B * S) {
-            // B rows at a time; the last ones of a stage may stand beside rows of zeros
-            C v[kResidualSources][B][N];
+            // B rows at a time; the last ones of a stage may stand beside rows of zeros.  Of
+            // dz and dy only e = dy + rstd_pre q is kept, in fp32.
+            C o[B][N], y[B][N];
+            V e[B][N][K];
             float s[4 * B], r1[B], r2[B];
 #pragma unroll
             for (int j = 0; j < B; ++j) {
                 const bool there = k + j * S < rows;
                 r1[j] = there ? r1s[k + j * S] : 0.0f;
                 r2[j] = there ? r2s[k + j * S] : 0.0f;
-#pragma unroll
-                for (int a = 0; a < kResidualSources; ++a)
-                    read_row<T, VEC, N>(v[a][j], cols, src[a] + j * S * cols, tpr, t, there && (a != kDy || p.has_dy));
-                // sums of q y, g o dy, g o q and g o y: the rstd factors come afterwards
-                V qn = C::all(0.0f), hd = qn, hq = qn, hn = qn;
+                read_row<T, VEC, N>(o[j], cols, src[kBranch] + j * S * cols, tpr, t, there);
+                read_row<T, VEC, N>(y[j], cols, src[kY] + j * S * cols, tpr, t, there);
+                C z[N], d[N];
+                read_row<T, VEC, N>(z, cols, src[kDz] + j * S * cols, tpr, t, there);
+                read_row<T, VEC, N>(d, cols, src[kDy] + j * S * cols, tpr, t, there && p.has_dy);
+                // sums of q y, g e and g y, with g = gate post o: the other rstd factors come afterwards
+                V qn = C::all(0.0f), he = qn, hn = qn;
                 const V scale2 = C::all(r2[j]);
 #pragma unroll
                 for (int n = 0; n < N; ++n) {
-                    V o[K], y[K], z[K], d[K];
-                    v[kBranch][j][n].get(o);
-                    v[kY][j][n].get(y);
-                    v[kDz][j][n].get(z);
-                    v[kDy][j][n].get(d);
+                    V of[K], yf[K], zf[K], df[K];
+                    o[j][n].get(of);
+                    y[j][n].get(yf);
+                    z[n].get(zf);
+                    d[n].get(df);
 #pragma unroll
                     for (int i = 0; i < K; ++i) {
-                        const V q = mul(z[i], pre[n][i]), g = mul(o[i], gp[n][i]);
-                        qn = fma(q, y[i], qn);
-                        hd = fma(g, d[i], hd);
-                        hq = fma(g, q, hq);
-                        hn = fma(g, y[i], hn);
-                        dn[n][i] = fma(z[i], mul(y[i], scale2), dn[n][i]);
+                        const V q = mul(zf[i], pre[n][i]), g = mul(of[i], gp[n][i]);
+                        e[j][n][i] = fma(q, scale2, df[i]);
+                        qn = fma(q, yf[i], qn);
+                        he = fma(g, e[j][n][i], he);
+                        hn = fma(g, yf[i], hn);
+                        dn[n][i] = fma(zf[i], mul(yf[i], scale2), dn[n][i]);
                     }
                 }
                 s[4 * j] = both(qn);
-                s[4 * j + 1] = both(hd);
-                s[4 * j + 2] = both(hq);
-                s[4 * j + 3] = both(hn);
+                s[4 * j + 1] = both(he);
+                s[4 * j + 2] = both(hn);
+                s[4 * j + 3] = 0.0f;
             }
             row_sum<4 * B>(s, red, phase, team);
             if (tpr <= 32) __syncwarp();
@@ -427,31 +431,29 @@ __global__ void __launch_bounds__(kNormThreads, 1) residual_backward_kernel(cons
 #pragma unroll
             for (int j = 0; j < B; ++j) {
                 if (k + j * S >= rows) continue;
-                // d = dy + r2 q - y r2^2 mean(q n);  do = r1 c - o r1^2 mean(c h)
+                // d = e - y r2^2 mean(q n);  do = r1 c - o r1^2 mean(c h)
                 const float m2 = s[4 * j] * r2[j] * inv;
-                const float ch = r1[j] * fmaf(r2[j], fmaf(-m2 * r2[j], s[4 * j + 3], s[4 * j + 2]), s[4 * j + 1]);
-                const V scale2 = C::all(r2[j]), back2 = C::all(-r2[j] * r2[j] * m2);
-                const V scale1 = C::all(r1[j]), back1 = C::all(-r1[j] * r1[j] * (ch * inv)), scale = C::all(p.scale);
+                const float ch = r1[j] * fmaf(-m2 * r2[j] * r2[j], s[4 * j + 2], s[4 * j + 1]);
+                const V back2 = C::all(-r2[j] * r2[j] * m2);
+                const V scale1 = C::all(r1[j]), back1 = C::all(-r1[j] * (ch * inv)), scale = C::all(p.scale);
                 const uint64_t at = row + k + j * S;
                 T *to_x = static_cast<T *>(p.out[0][r]) + at * cols, *to_o = static_cast<T *>(p.out[1][r]) + at * cols;
 #pragma unroll
                 for (int n = 0; n < N; ++n) {
-                    const uint32_t e = (n * tpr + t) * VEC;
-                    if (e >= cols) continue;
-                    V o[K], y[K], z[K], d[K], dx[K];
-                    v[kBranch][j][n].get(o);
-                    v[kY][j][n].get(y);
-                    v[kDz][j][n].get(z);
-                    v[kDy][j][n].get(d);
+                    const uint32_t c = (n * tpr + t) * VEC;
+                    if (c >= cols) continue;
+                    V of[K], yf[K], dx[K];
+                    o[j][n].get(of);
+                    y[j][n].get(yf);
 #pragma unroll
                     for (int i = 0; i < K; ++i) {
-                        d[i] = add(d[i], fma(mul(z[i], pre[n][i]), scale2, mul(y[i], back2)));
-                        dx[i] = mul(d[i], scale);
-                        dh[n][i] = fma(d[i], mul(o[i], scale1), dh[n][i]);
-                        o[i] = fma(mul(d[i], gp[n][i]), scale1, mul(o[i], back1));
+                        const V d = fma(yf[i], back2, e[j][n][i]), h = mul(of[i], scale1);
+                        dx[i] = mul(d, scale);
+                        dh[n][i] = fma(d, h, dh[n][i]);
+                        of[i] = fma(mul(d, gp[n][i]), scale1, mul(h, back1));
                     }
-                    if (RESIDUAL_OK(kResidualOut + r, to_x + e, VEC * sizeof(T))) C::store(to_x + e, dx);
-                    if (RESIDUAL_OK(kResidualOut + DT_MAX_RANKS + r, to_o + e, VEC * sizeof(T))) C::store(to_o + e, o);
+                    if (RESIDUAL_OK(kResidualOut + r, to_x + c, VEC * sizeof(T))) C::store(to_x + c, dx);
+                    if (RESIDUAL_OK(kResidualOut + DT_MAX_RANKS + r, to_o + c, VEC * sizeof(T))) C::store(to_o + c, of);
                 }
             }
 #pragma unroll
@@ -661,7 +663,7 @@ __global__ void __launch_bounds__(kLongThreads) residual_long_kernel(const __gri
 template <typename T>
 __global__ void __launch_bounds__(kLongThreads) residual_backward_long_kernel(const __grid_constant__ ResidualParams p)
 {
-    __shared__ float red[kLongThreads / 32][4];
+    __shared__ float red[kLongThreads / 32][3];
     DT_TL_BEGIN();
     pdl_begin();
     DT_TL_WAITED();
@@ -678,19 +680,18 @@ __global__ void __launch_bounds__(kLongThreads) residual_backward_long_kernel(co
         const float r1 = RESIDUAL_OK(kResidualRstd + r, p.rstd[0][r] + local, 4) ? p.rstd[0][r][local] : 0.0f;
         const float r2 = RESIDUAL_OK(kResidualRstd + DT_MAX_RANKS + r, p.rstd[1][r] + local, 4) ? p.rstd[1][r][local] : 0.0f;
         auto gp = [&](uint32_t e) { return weight(p, p.post, kResidualPost, e) * weight(p, p.gate, kResidualGate, e); };
-        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        float s[3] = {0.0f, 0.0f, 0.0f};
         for (uint32_t e = threadIdx.x; e < p.cols; e += kLongThreads) {
             const uint64_t at = first + e;
             const float q = element<T>(p, kDz, r, at) * weight(p, p.pre, kResidualPre, e), y = element<T>(p, kY, r, at);
             const float g = element<T>(p, kBranch, r, at) * gp(e), d = p.has_dy ? element<T>(p, kDy, r, at) : 0.0f;
             s[0] = fmaf(q, y, s[0]);
-            s[1] = fmaf(g, d, s[1]);
-            s[2] = fmaf(g, q, s[2]);
-            s[3] = fmaf(g, y, s[3]);
+            s[1] = fmaf(g, fmaf(q, r2, d), s[1]);
+            s[2] = fmaf(g, y, s[2]);
         }
         block_sum(s, red);
         const float m2 = s[0] * r2 * p.inv_cols;
-        const float m1 = r1 * fmaf(r2, fmaf(-m2 * r2, s[3], s[2]), s[1]) * p.inv_cols;
+        const float m1 = r1 * fmaf(-m2 * r2 * r2, s[2], s[1]) * p.inv_cols;
         for (uint32_t e = threadIdx.x; e < p.cols; e += kLongThreads) {
             const uint64_t at = first + e;
             const float z = element<T>(p, kDz, r, at), y = element<T>(p, kY, r, at), o = element<T>(p, kBranch, r, at);
