@@ -504,6 +504,85 @@ __global__ void __launch_bounds__(kNormThreads, 1) residual_backward_kernel(cons
     DT_TL_END_BLOCK(DT_TL_RESIDUAL);
 }
 
+// Forward, few rows of whole vectors: a block to a row, whose threads load their vectors of
+// it and their weights straight from memory, all at once (a decoding step of 4 rows of 4096
+// bf16: by way of a ring 5.0 us, this @F@).
+template <typename T, int VEC, int N>
+__global__ void __launch_bounds__(kNormThreads) residual_few_kernel(const __grid_constant__ ResidualParams p)
+{
+    using C = Chunk<T, VEC>;
+    using V = typename C::V;
+    constexpr int K = C::K;
+    __shared__ float red[2][1][kNormThreads / 32];
+    DT_TL_BEGIN();
+    pdl_begin();
+    DT_TL_WAITED();
+    const Team<32> team(p.tpr);
+    int r = 0;
+    uint64_t begin = 0;
+    while (r + 1 < p.P && blockIdx.x >= p.row_end[r]) begin = p.row_end[r++];
+    const uint64_t row = blockIdx.x - begin, first = row * p.cols;
+    const T *os = static_cast<const T *>(p.src[kBranch][r]) + first, *xs = static_cast<const T *>(p.src[kX][r]) + first;
+    C o[N], x[N];
+    V gp[N][K], pre[N][K];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const uint32_t e = (n * team.tpr + team.t) * VEC;
+        o[n].zero();
+        x[n].zero();
+        if (e < p.cols && RESIDUAL_OK(kBranch * DT_MAX_RANKS + r, os + e, 16)) o[n].load(os + e);
+        if (e < p.cols && RESIDUAL_OK(kX * DT_MAX_RANKS + r, xs + e, 16)) x[n].load(xs + e);
+#pragma unroll
+        for (int i = 0; i < K; ++i) gp[n][i] = pre[n][i] = C::all(0.0f);
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const uint32_t e = (n * team.tpr + team.t) * VEC;
+        if (e < p.cols) weights<C, VEC>(p, e, gp[n], pre[n]);
+    }
+    uint32_t phase = 0;
+    V sum = C::all(0.0f), y[N][K];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        o[n].get(y[n]);
+#pragma unroll
+        for (int i = 0; i < K; ++i) sum = fma(y[n][i], y[n][i], sum);
+    }
+    float s[1] = {both(sum)};
+    row_sum<1>(s, red, phase, team);
+    const float r1 = rstd_of(s[0], p.inv_cols, p.eps);
+    sum = C::all(0.0f);
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        V a[K];
+        x[n].get(a);
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+            y[n][i] = fma(mul(y[n][i], C::all(r1)), gp[n][i], mul(a[i], C::all(p.scale)));
+            sum = fma(y[n][i], y[n][i], sum);
+        }
+    }
+    s[0] = both(sum);
+    row_sum<1>(s, red, phase, team);
+    const float r2 = rstd_of(s[0], p.inv_cols, p.eps);
+    T *to_y = static_cast<T *>(p.out[0][r]) + first, *to_z = static_cast<T *>(p.out[1][r]) + first;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const uint32_t e = (n * team.tpr + team.t) * VEC;
+        if (e >= p.cols) continue;
+        V z[K];
+#pragma unroll
+        for (int i = 0; i < K; ++i) z[i] = mul(mul(y[n][i], C::all(r2)), pre[n][i]);
+        if (RESIDUAL_OK(kResidualOut + r, to_y + e, 16)) C::store(to_y + e, y[n]);
+        if (RESIDUAL_OK(kResidualOut + DT_MAX_RANKS + r, to_z + e, 16)) C::store(to_z + e, z);
+    }
+    if (threadIdx.x == 0) {
+        if (p.rstd[0][r] && RESIDUAL_OK(kResidualRstd + r, p.rstd[0][r] + row, 4)) p.rstd[0][r][row] = r1;
+        if (p.rstd[1][r] && RESIDUAL_OK(kResidualRstd + DT_MAX_RANKS + r, p.rstd[1][r] + row, 4)) p.rstd[1][r][row] = r2;
+    }
+    DT_TL_END_BLOCK(DT_TL_RESIDUAL);
+}
+
 // The weights' gradients from the blocks' shares: of dpost and dgate (blockIdx.y 0) or
 // dpre (1).  Thread (c, s) adds shares s, s + 16, ... of its column, then the 16 sums
 // are added in a tree.
@@ -748,6 +827,22 @@ Pick pick(int dtype, bool vec, uint32_t cols)
     return vec ? pick<float, 4, BACK>(cols) : pick<float, 1, BACK>(cols);
 }
 
+// The kernel for few rows of whole vectors, and the threads of a row.
+template <typename T, int VEC>
+Pick pick_few(uint32_t cols)
+{
+    Pick k;
+    const uint32_t vecs = (cols + VEC - 1) / VEC;
+    if (vecs <= kNormThreads) {
+        k.fn = residual_few_kernel<T, VEC, 1>;
+        k.tpr = (vecs + 31) / 32 * 32;
+    } else if (vecs <= 2 * kNormThreads) {
+        k.fn = residual_few_kernel<T, VEC, 2>;
+        k.tpr = ((vecs + 1) / 2 + 31) / 32 * 32;
+    }
+    return k;
+}
+
 // The grid, the groups and the rings of a call.
 cudaError_t launch_rows(const Pick &k, ResidualParams &p, int dtype, bool vec, bool back, int device, cudaStream_t s)
 {
@@ -809,6 +904,11 @@ size_t residual_workspace(uint32_t cols, int device)
 
 cudaError_t launch_residual(ResidualParams p, int dtype, bool vec, int device, cudaStream_t s)
 {
+    if (vec && p.rows <= 2 * (uint64_t)sm_count(device)) {
+        const Pick few = dtype == DT_BF16 ? pick_few<uint16_t, 8>(p.cols) : pick_few<float, 4>(p.cols);
+        p.tpr = few.tpr;
+        if (few.fn) return launch_kernel(few.fn, dim3((unsigned)p.rows), dim3(few.tpr), 0, s, false, p);
+    }
     const Pick k = pick<false>(dtype, vec, p.cols);
     if (k.fn) return launch_rows(k, p, dtype, vec, false, device, s);
     const uint64_t grid = std::min<uint64_t>(p.rows, (uint64_t)sm_count(device) * 4);
