@@ -23,10 +23,10 @@ STEP_TOOL = os.path.join(PKG, "rank_local_step")
 
 SOURCES = ["dt_group.cpp", "dt_reduce.cu", "dt_reduce_shift.cu", "dt_copy.cu", "dt_bucket.cu",
            "dt_barrier.cu", "dt_static.cu", "dt_norm.cu", "dt_vocab.cu", "dt_ops.cpp",
-           "dt_linear.cu", "dt_linear.cpp", "dt_residual.cu", "dt_residual.cpp"]
+           "dt_linear.cu", "dt_linear_small.cu", "dt_linear.cpp", "dt_residual.cu", "dt_residual.cpp"]
 HEADERS = ["dt_internal.h", "dt_group.h", "dt_host.h", "dt_math.cuh", "dt_device.cuh", "dt_shift.cuh",
            "dt_reduce_shift.h", "dt_timeline.cuh", "dt_timeline.h", "dt_bounds.cuh", "dt_ops.h", "dt_tc.cuh", "dt_tile.cuh", "dt_rows.cuh", "dt_vocab.h",
-           "dt_linear.h", "dt_residual.h"]
+           "dt_linear.h", "dt_linear.cuh", "dt_residual.h"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 # -fmad=false: no multiply-add contraction anywhere (the reductions use

@@ -1456,6 +1456,7 @@ dt_status dt_timeline_start(size_t max_records)
     dt::bind_timeline_norm(&sink);
     dt::bind_timeline_vocab(&sink);
     dt::bind_timeline_linear(&sink);
+    dt::bind_timeline_linear_small(&sink);
     dt::bind_timeline_residual(&sink);
     return cudaDeviceSynchronize() == cudaSuccess ? DT_OK : DT_ERR_CUDA;
 #else

@@ -53,14 +53,16 @@ uint64_t feature_tiles(const Plan &v, uint64_t size)
 struct Cut {
     uint32_t bn;
     uint64_t mt[2], nt[2], kblocks[2], splits[2];
+    double us;                         // what it takes, about
     uint64_t acc_bytes(const Plan &v, int k) const { return splits[k] > 1 ? splits[k] * mt[k] * v.halves * 128 * nt[k] * bn * 4 : 0; }
 };
 
 // What a launch takes, in microseconds, as far as its cut decides it: 16 of the inner
 // axis take the tensor cores 128 cycles whatever a tile's width (measured from 64 to 256
-// columns: reading 128 rows of A bounds it), a tile costs a microsecond beside that, and
-// splits cost a second launch and their sums' way to L2 and back.
-constexpr double kUsPer64 = 0.34, kUsTile = 1.0, kUsJoin = 2.5, kJoinBytesPerUs = 8e6;
+// columns: reading 128 rows of A bounds it), a tile costs half a microsecond beside that
+// and the last one's finish half of one for each 64 columns, and splits cost a second
+// launch and their sums' way to L2 and back.
+constexpr double kUsPer64 = 0.34, kUsTile = 0.5, kUsFinish64 = 0.45, kUsJoin = 2.5, kJoinBytesPerUs = 8e6;
 
 double join_cost(const Plan &v, const Cut &c)
 {
@@ -107,9 +109,10 @@ bool cut(const dt_group *g, const Plan &v, bool pieces, Cut &best)
                 }
                 // forward in whole waves; backward the second product's tiles fill the
                 // first one's last wave
-                const double us = (b ? std::max(all / workers, longest) : tiles_of(units, workers) * unit[0]) + join_cost(v, c);
+                const double us = (b ? std::max(all / workers, longest) : tiles_of(units, workers) * unit[0]) +
+                                  tiles_of(bn, 64) * kUsFinish64 + join_cost(v, c);
                 if (us >= least) continue;
-                least = us;
+                least = c.us = us;
                 best = c;
             }
     }
@@ -319,6 +322,116 @@ void token_matrix(Call &c, const void *const *x, int buffer, float *sums)
     c.p.t_pieces = (int32_t)pieces;
 }
 
+// How small products are cut: CTAs of a cluster, and whether they share a tile's inner axis.
+struct SmallCut {
+    uint64_t mt[2], nt[2], kblocks[2], strips;
+    uint32_t ctas, shared[2];
+    double us;
+};
+
+// What they take, in microseconds: a launch, the longest CTA's round trips to memory, and
+// in all so much for each step of a tile (measured at 17 to 1000 tokens of 100 to 1024,
+// to 200 to 4096 features; rows at any element and an activation's derivative cost
+// instructions).
+constexpr double kUsSmall = 5.0, kUsSmallStep = 0.45;
+
+void small_cut(const dt_group *g, const Plan &v, bool sums, bool vec, bool slope, SmallCut &c)
+{
+    const bool b = back(v.kind), n_features = v.kind == dt::kGather || v.kind == dt::kReduceBack;
+    const uint64_t tile = dt::kSmallTile, t = tiles_of(v.tokens, tile), d = tiles_of(v.dim, tile), f = feature_tiles(v, tile);
+    c.mt[0] = t;
+    c.nt[0] = c.nt[1] = n_features ? f : d;
+    c.kblocks[0] = n_features ? d : f;
+    c.mt[1] = b ? (gathers(v.kind) ? f : d) : 0;
+    c.kblocks[1] = b ? t : 0;
+    c.strips = sums ? (gathers(v.kind) ? f : d) : 0;
+    uint64_t most = 0, steps = c.strips * t, longest = sums ? t : 0;
+    for (int k = 0; k < 2; ++k) {
+        c.shared[k] = c.kblocks[k] >= 4;
+        if (c.shared[k]) most = std::max(most, c.kblocks[k]);
+        steps += c.mt[k] * c.nt[k] * c.kblocks[k];
+    }
+    // two steps to a CTA at least; forward no more CTAs than SMs, which clusters of many
+    // slow down (512 tokens of 512 to 512: 1, 2, 4, 8 CTAs 7.9, 8.5, 9.9, 12.6 us)
+    c.ctas = 1;
+    while (c.ctas < (b ? 8u : 4u) && c.ctas * 4 <= most &&
+           (b || c.mt[0] * c.nt[0] * c.ctas * 2 <= dt::linear_workers(false, g->device)))
+        c.ctas *= 2;
+    for (int k = 0; k < 2; ++k) longest = std::max(longest, c.shared[k] ? tiles_of(c.kblocks[k], c.ctas) : c.kblocks[k]);
+    const double step = b ? (slope ? 0.0135 : 0.009) + (vec ? 0.0 : 0.004) : vec ? 0.0045 : 0.011;
+    c.us = kUsSmall + std::max(longest * kUsSmallStep, steps * step);
+}
+
+// What goes before the tensor core kernels' products, in microseconds: matrices that are
+// laid out again, or (`written`) the ranks' features, which a job makes.
+double prep_us(const Call &c, const void *const *tok, const void *const *feat, const void *const *w, bool written)
+{
+    const Plan &v = c.v;
+    double bytes = 0.0;
+    bool tok_again = false, feat_again = written, w_again = false;
+    const unsigned char *next = nullptr;
+    for (int r = 0; r < c.g->P; ++r) {
+        if (tok && v.n[r]) {
+            tok_again = tok_again || !addressable(tok[r], v.dim) || (next && next != tok[r] && v.n[r] % 128);
+            next = static_cast<const unsigned char *>(tok[r]) + v.n[r] * v.dim * 2;
+        }
+        if (feat && v.f[r]) feat_again = feat_again || !addressable(feat[r], v.f[r]);
+        if (v.f[r]) w_again = w_again || !addressable(w[r], gathers(v.kind) ? v.dim : v.f[r]);
+    }
+    if (tok_again) bytes += 4.0 * v.tokens * v.dim;
+    if (feat_again) bytes += (written ? 6.0 : 4.0) * v.tokens * v.features;
+    if (w_again) bytes += 4.0 * v.features * v.dim;
+    return bytes > 0.0 ? 3.0 + bytes / 4e6 : 0.0;
+}
+
+// Small products where they are likely to take less time than the tensor core kernels':
+// true where they were launched.  z: what act'(.) is taken of.
+bool run_small(Call &c, const void *const *tok, const void *const *feat, const void *const *w, const void *const *z, int act,
+               bool sums, bool written, cudaStream_t s, cudaError_t &e)
+{
+    const Plan &v = c.v;
+    bool vec = true;
+    for (int r = 0; r < c.g->P; ++r) {
+        if (tok && v.n[r]) vec = vec && addressable(tok[r], v.dim);
+        if (v.f[r] == 0) continue;
+        if (feat) vec = vec && addressable(feat[r], v.f[r]) && (!z || addressable(z[r], v.f[r]));
+        vec = vec && addressable(w[r], gathers(v.kind) ? v.dim : v.f[r]);
+    }
+    SmallCut t;
+    small_cut(c.g, v, sums, vec, z != nullptr, t);
+    Cut big;
+    cut(c.g, v, false, big);
+    if (t.us >= big.us + 4.0 + prep_us(c, tok, feat, w, written)) return false;
+    dt::LinearSmall p;
+    memset(&p, 0, sizeof p);
+    static_cast<dt::LinearCall &>(p) = c.p;
+    for (int r = 0; r < c.g->P; ++r) {
+        p.tok[r] = tok ? static_cast<const uint16_t *>(tok[r]) : nullptr;
+        p.feat[r] = feat ? static_cast<const uint16_t *>(feat[r]) : nullptr;
+        p.weight[r] = static_cast<const uint16_t *>(w[r]);
+        p.z[r] = z ? static_cast<const uint16_t *>(z[r]) : nullptr;
+    }
+    p.act = act;
+    p.ctas = t.ctas;
+    p.strips = (uint32_t)t.strips;
+    uint32_t end = 0;
+    for (int r = 0; r < c.g->P; ++r) {
+        end += (uint32_t)tiles_of(v.f[r], dt::kSmallTile);
+        p.product[0].f_end[r] = p.product[1].f_end[r] = end;
+    }
+    for (int k = 0; k < 2; ++k) {
+        dt::LinearProduct &q = p.product[k];
+        q.mt = (uint32_t)t.mt[k];
+        q.nt = (uint32_t)t.nt[k];
+        q.kblocks = (uint32_t)t.kblocks[k];
+        p.shared[k] = t.shared[k];
+        const uint32_t tiles = q.mt * q.nt;
+        p.clusters[k] = t.shared[k] ? tiles : (tiles + t.ctas - 1) / t.ctas;
+    }
+    e = dt::launch_linear_small(p, v.kind, vec, s);
+    return true;
+}
+
 // The forward products of few tokens.
 cudaError_t run_few(Call &c, const void *const *x, const void *const *w, cudaStream_t s)
 {
@@ -481,8 +594,10 @@ dt_status dt_gather_linear(dt_group_t g, const void *const *x, const void *const
     DeviceScope scope(g->device);
     if (!scope.ok) return DT_ERR_CUDA;
     if (v.tokens <= dt::kFewTokens) return cuda_status(run_few(c, x, weight, static_cast<cudaStream_t>(stream)));
+    cudaError_t e = cudaSuccess;
+    if (run_small(c, x, nullptr, weight, nullptr, act, false, false, static_cast<cudaStream_t>(stream), e)) return cuda_status(e);
     token_matrix(c, x, dt::kLinearX, nullptr);
-    cudaError_t e = matrices(c, nullptr, 0, false, weight);
+    e = matrices(c, nullptr, 0, false, weight);
     if (e == cudaSuccess) e = run(c, static_cast<cudaStream_t>(stream));
     return cuda_status(e);
 }
@@ -536,6 +651,9 @@ dt_status dt_gather_linear_backward(dt_group_t g, const void *const *x, const vo
         }
     }
     c.p.product[0].align[0] = tok_align;
+    cudaError_t e = cudaSuccess;
+    for (int r = 0; r < g->P; ++r) c.p.sums.out[r] = dbias ? static_cast<uint16_t *>(dbias[r]) : nullptr;
+    if (run_small(c, x, dy, weight, pre, act, dbias != nullptr, act != DT_ACT_NONE, s, e)) return cuda_status(e);
     c.prep.act = act;
     token_matrix(c, x, dt::kLinearX, nullptr);
     // G: dy itself where nothing is done to it and TMA can read it
@@ -557,13 +675,12 @@ dt_status dt_gather_linear_backward(dt_group_t g, const void *const *x, const vo
         sums.src[r] = beside ? dy[r] : part;
         sums.rows[r] = beside ? (uint32_t)v.tokens : (uint32_t)v.chunks;
         sums.cols[r] = (uint32_t)v.f[r];
-        sums.out[r] = static_cast<uint16_t *>(dbias[r]);
         sums.group_end[r] = sums.groups += (uint32_t)tiles_of(v.f[r], 32);
         part += v.chunks * v.f[r];
     }
     sums.n = sums.sources = g->P;
     sums.f32 = !beside;
-    cudaError_t e = matrices(c, dy, dt::kLinearDy, written, weight);
+    e = matrices(c, dy, dt::kLinearDy, written, weight);
     if (e == cudaSuccess) e = run(c, s);
     return cuda_status(e);
 }
@@ -616,10 +733,13 @@ dt_status dt_linear_reduce(dt_group_t g, const void *const *x, const void *const
     DeviceScope scope(g->device);
     if (!scope.ok) return DT_ERR_CUDA;
     if (v.tokens <= dt::kFewTokens) return cuda_status(run_few(c, x, weight, static_cast<cudaStream_t>(stream)));
+    cudaError_t e = cudaSuccess;
+    if (run_small(c, nullptr, x, weight, nullptr, DT_ACT_NONE, false, false, static_cast<cudaStream_t>(stream), e))
+        return cuda_status(e);
     c.pieces = 1;
     c.p.t_pieces = 1;
     c.p.t_len[0] = c.p.tokens;
-    cudaError_t e = matrices(c, x, dt::kLinearX, false, weight);
+    e = matrices(c, x, dt::kLinearX, false, weight);
     if (e == cudaSuccess) e = run(c, static_cast<cudaStream_t>(stream));
     return cuda_status(e);
 }
@@ -666,13 +786,15 @@ dt_status dt_linear_reduce_backward(dt_group_t g, const void *const *x, const vo
         c.p.product[0].align[r] = alignment(8, dx[r], v.f[r]);
         c.p.product[1].align[r] = alignment(8, dweight[r], v.f[r]);
     }
+    cudaError_t e = cudaSuccess;
+    c.p.sums.out[0] = static_cast<uint16_t *>(dbias);
+    if (run_small(c, dy, x, weight, nullptr, DT_ACT_NONE, dbias != nullptr, false, s, e)) return cuda_status(e);
     // the bias' gradient: from the ranks' dy, or from sums over chunks of the rows
     float *part = reinterpret_cast<float *>(c.ws + v.sums);
     const bool beside = sums_beside(g, v);
     token_matrix(c, dy, dt::kLinearDy, dbias && !beside ? part : nullptr);
     if (dbias) {
         dt::LinearSums &sums = c.p.sums;
-        sums.out[0] = static_cast<uint16_t *>(dbias);
         sums.cols[0] = (uint32_t)dim;
         sums.group_end[0] = sums.groups = (uint32_t)tiles_of(dim, 32);
         sums.n = sums.stacked = 1;
@@ -685,7 +807,7 @@ dt_status dt_linear_reduce_backward(dt_group_t g, const void *const *x, const vo
             sums.rows[r] = (uint32_t)v.n[r];
         }
     }
-    cudaError_t e = matrices(c, x, dt::kLinearX, false, weight);
+    e = matrices(c, x, dt::kLinearX, false, weight);
     if (e == cudaSuccess) e = run(c, s);
     return cuda_status(e);
 }

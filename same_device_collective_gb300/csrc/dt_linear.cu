@@ -32,7 +32,7 @@
 #include <atomic>
 #include <type_traits>
 
-#include "dt_linear.h"
+#include "dt_linear.cuh"
 
 #include "dt_bounds.cuh"
 #include "dt_device.cuh"
@@ -65,58 +65,6 @@ static_assert(kTcSmem <= 227 * 1024, "shared memory above the per-block limit");
 // flight share few rows and columns and their operands come from L2 (2048 tokens of 4096
 // to 16384: 16 columns, columns fastest 152 us, eight 142.5, rows fastest 141.5).
 constexpr uint32_t kGroup = 8;
-
-#define LINEAR_OK(buffer, a, n) DT_IN_EXTENT(p, kBoundsLinear, (buffer), (a), (n))
-
-__host__ __device__ constexpr bool is_back(int kind) { return kind == kGatherBack || kind == kReduceBack; }
-
-// The matrices that TMA reads.
-enum Matrix : int { kTok, kFeat, kW };
-
-// What the rows, columns and inner axis of a product are, and its operands.  An
-// operand is MN-major where its rows run along the inner axis.
-template <int KIND, bool SECOND>
-struct Roles {
-    static constexpr int m = !SECOND ? kTokens : KIND == kGatherBack ? kFeatures : kDim;
-    static constexpr int n = KIND == kGather || KIND == kReduceBack ? kFeatures : kDim;
-    static constexpr int k = SECOND ? kTokens : n == kFeatures ? kDim : kFeatures;
-    static constexpr int a = KIND == kGather || KIND == kReduceBack ? kTok : kFeat;
-    static constexpr int b = !SECOND ? kW : KIND == kGatherBack ? kTok : kFeat;
-    static constexpr bool a_mn = SECOND, b_mn = is_back(KIND);
-    static constexpr bool tok = a == kTok || b == kTok;   // the token axis is cut as the tokens' matrices are
-    static constexpr uint32_t depth = linear_depth(is_back(KIND));   // of a stage
-    static constexpr bool w_by_feature = KIND == kGather || KIND == kGatherBack;   // rows of W_r are features
-};
-
-// A place along an axis: the rank's piece, the place there, and overall (tokens).
-struct Place {
-    uint32_t piece, at, all;
-};
-
-template <class R, int AXIS>
-__device__ __forceinline__ Place locate(const LinearParams &p, const LinearProduct &c, uint32_t i, uint32_t unit)
-{
-    if constexpr (AXIS == kDim) {
-        return Place{0, i * unit, 0};
-    } else if constexpr (AXIS == kFeatures) {
-        uint32_t r = 0, begin = 0;
-        while ((int)r + 1 < p.P && i >= c.f_end[r]) begin = c.f_end[r++];
-        return Place{r, (i - begin) * unit, 0};
-    } else if (!R::tok) {
-        return Place{0, i * unit, i * unit};
-    } else {
-        uint32_t r = 0, begin = 0;
-        while ((int)r + 1 < p.t_pieces && i >= c.t_end[r]) begin = c.t_end[r++];
-        const uint32_t at = (i - begin) * unit;
-        return Place{r, at, p.t_first[r] + at};
-    }
-}
-
-template <class R, int AXIS>
-__device__ __forceinline__ uint32_t length(const LinearParams &p, uint32_t piece)
-{
-    return AXIS == kDim ? p.dim : AXIS == kFeatures ? p.f_len[piece] : R::tok ? p.t_len[piece] : p.tokens;
-}
 
 // Walks over the blocks of the inner axis, the blocks of one piece after the other.
 template <class R>
@@ -317,168 +265,6 @@ __device__ __forceinline__ bool multiply_tile(const LinearParams &p, const Linea
         }
     } while (k.next(p));
     return true;
-}
-
-// Eight elements of a row from any element on, of which `n` are there (the others come
-// out as zeros): from the aligned vectors that they lie in, neither of which reaches past
-// the 16-byte block of one of them.
-__device__ __forceinline__ void load_shifted(const uint16_t *from, uint32_t n, uint32_t (&w)[4])
-{
-    const uintptr_t at = reinterpret_cast<uintptr_t>(from);
-    const uint32_t off = (uint32_t)at & 15;
-    const uint4 *block = reinterpret_cast<const uint4 *>(at & ~(uintptr_t)15);
-    const uint4 a = __ldg(block), b = off + 2 * n > 16 ? __ldg(block + 1) : make_uint4(0, 0, 0, 0);
-    // by eight, four and two bytes
-    const bool s8 = off & 8, s4 = off & 4;
-    const uint32_t x[6] = {s8 ? a.z : a.x, s8 ? a.w : a.y, s8 ? b.x : a.z, s8 ? b.y : a.w, s8 ? b.z : b.x, s8 ? b.w : b.y};
-    uint32_t y[5];
-#pragma unroll
-    for (int i = 0; i < 5; ++i) y[i] = s4 ? x[i + 1] : x[i];
-#pragma unroll
-    for (uint32_t i = 0; i < 4; ++i) {
-        w[i] = __funnelshift_r(y[i], y[i + 1], (off & 2) * 8);
-        if (2 * i >= n) w[i] = 0;
-        else if (2 * i + 1 >= n) w[i] &= 0xFFFFu;
-    }
-}
-
-// ---- what follows a sum ------------------------------------------------------
-
-__device__ constexpr float kTail[7] = {0.143713042f, 0.141772494f, 0.139719009f, 0.0265500601f, 0.180952892f, -0.179763854f, 0.0470560379f};
-
-// The upper tail of the normal distribution at |v|, and exp(-v^2 / 2), two at a time.
-// The tail is exp(-z^2 / 2) t (c0 + c1 t + ... + c6 t^6) with t = 1 / (1 + 0.36 z), the c
-// a minimax fit of the relative error over t from 1 to z = 14: 1e-6 of itself off
-// everywhere, where 1 - erf would have nothing left far out.  (Own fit; erfcf in its
-// place is some 40 instructions, for every element.)
-__device__ __forceinline__ float2 normal_tail(float2 v, float2 &bell)
-{
-    const float2 e = mul2(mul2(v, v), make_float2(-0.72134752044448170368f, -0.72134752044448170368f));
-    bell = make_float2(exp2_fast(e.x), exp2_fast(e.y));
-    const float2 d = fma2(make_float2(fabsf(v.x), fabsf(v.y)), make_float2(0.36f, 0.36f), make_float2(1.0f, 1.0f));
-    const float2 t = make_float2(rcp_fast(d.x), rcp_fast(d.y));
-    float2 s = make_float2(kTail[6], kTail[6]);
-#pragma unroll
-    for (int i = 5; i >= 0; --i) s = fma2(s, t, make_float2(kTail[i], kTail[i]));
-    return mul2(mul2(s, t), bell);
-}
-
-// v times the normal distribution at v, from its tail: max(v, 0) - |v| tail.  An infinite
-// |v| would make the product with a tail of zero no number; a NaN stays one.
-__device__ __forceinline__ float gelu_of(float v, float q)
-{
-    float a;
-    asm("{\n\t.reg .f32 t;\n\tabs.f32 t, %1;\n\tmin.NaN.f32 %0, t, 0f7F7FFFFF;\n\t}" : "=f"(a) : "f"(v));
-    return fmaf(-a, q, fmaxf(v, 0.0f));
-}
-
-// The normal distribution from its tail.
-__device__ __forceinline__ float2 normal_of(float2 v, float2 q)
-{
-    return make_float2(v.x > 0.0f ? 1.0f - q.x : q.x, v.y > 0.0f ? 1.0f - q.y : q.y);
-}
-
-// 1 / (1 + exp(-v)).
-__device__ __forceinline__ float2 logistic(float2 v)
-{
-    const float2 e = mul2(v, make_float2(-1.44269504088896340736f, -1.44269504088896340736f));
-    return make_float2(rcp_fast(1.0f + exp2_fast(e.x)), rcp_fast(1.0f + exp2_fast(e.y)));
-}
-
-// The activation; a NaN stays one.
-template <int ACT>
-__device__ __forceinline__ float2 activate(float2 v)
-{
-    if (ACT == DT_ACT_RELU) return make_float2(v.x < 0.0f ? 0.0f : v.x, v.y < 0.0f ? 0.0f : v.y);
-    if (ACT == DT_ACT_SILU) return mul2(v, logistic(v));
-    if (ACT == DT_ACT_GELU) {
-        float2 bell;
-        const float2 q = normal_tail(v, bell);
-        return make_float2(gelu_of(v.x, q.x), gelu_of(v.y, q.y));
-    }
-    return v;
-}
-
-// Its derivative.
-template <int ACT>
-__device__ __forceinline__ float2 slope(float2 v)
-{
-    if (ACT == DT_ACT_RELU) return make_float2(v.x > 0.0f ? 1.0f : 0.0f, v.y > 0.0f ? 1.0f : 0.0f);
-    const float2 one = make_float2(1.0f, 1.0f);
-    if (ACT == DT_ACT_SILU) {
-        const float2 s = logistic(v), rest = fma2(s, make_float2(-1.0f, -1.0f), one);
-        return mul2(s, fma2(v, rest, one));
-    }
-    if (ACT == DT_ACT_GELU) {
-        float2 bell;
-        const float2 q = normal_tail(v, bell);
-        return fma2(mul2(v, make_float2(0.39894228040143267794f, 0.39894228040143267794f)), bell, normal_of(v, q));
-    }
-    return one;
-}
-
-// All of N values, so that the choice is made once.
-template <int N>
-__device__ __forceinline__ void activate(float (&v)[N], int act)
-{
-    auto all = [&](auto of) {
-#pragma unroll
-        for (int j = 0; j < N; j += 2) {
-            const float2 a = activate<decltype(of)::value>(make_float2(v[j], v[j + 1]));
-            v[j] = a.x, v[j + 1] = a.y;
-        }
-    };
-    if (act == DT_ACT_RELU) all(std::integral_constant<int, DT_ACT_RELU>{});
-    else if (act == DT_ACT_GELU) all(std::integral_constant<int, DT_ACT_GELU>{});
-    else if (act == DT_ACT_SILU) all(std::integral_constant<int, DT_ACT_SILU>{});
-}
-
-// g[j] times the derivative at v[j].
-template <int N>
-__device__ __forceinline__ void times_slope(float (&g)[N], const float (&v)[N], int act)
-{
-    auto all = [&](auto of) {
-#pragma unroll
-        for (int j = 0; j < N; j += 2) {
-            const float2 a = mul2(make_float2(g[j], g[j + 1]), slope<decltype(of)::value>(make_float2(v[j], v[j + 1])));
-            g[j] = a.x, g[j + 1] = a.y;
-        }
-    };
-    if (act == DT_ACT_RELU) all(std::integral_constant<int, DT_ACT_RELU>{});
-    else if (act == DT_ACT_GELU) all(std::integral_constant<int, DT_ACT_GELU>{});
-    else if (act == DT_ACT_SILU) all(std::integral_constant<int, DT_ACT_SILU>{});
-}
-
-// Where row `row` (of the piece at.piece) of a product's output begins, its first
-// element at column n.at of its tile; and the number of the buffer, by rank.
-struct OutRow {
-    uint16_t *out;
-    uint64_t offset;   // elements from the buffer's start
-    uint32_t rank;
-};
-
-template <class R>
-__device__ __forceinline__ OutRow out_row(const LinearParams &p, const LinearProduct &c, const Place &m, const Place &n,
-                                          uint32_t row)
-{
-    OutRow o;
-    uint64_t at;
-    if (R::m == kTokens && R::n == kDim) {       // a token's row on its rank
-        const uint32_t t = m.all + row;
-        uint32_t begin = 0;
-        o.rank = 0;
-        while ((int)o.rank + 1 < p.P && t >= p.row_end[o.rank]) begin = p.row_end[o.rank++];
-        at = t - begin;
-    } else if (R::m == kFeatures) {              // dW_r: a feature's row
-        o.rank = m.piece;
-        at = m.at + row;
-    } else {                                     // a rank's features of a token, or of a column of W_r
-        o.rank = n.piece;
-        at = (R::m == kTokens ? m.all : m.at) + row;
-    }
-    o.offset = at * (R::n == kDim ? p.dim : p.f_len[n.piece]) + n.at;
-    o.out = c.out[o.rank];
-    return o;
 }
 
 // A pointer of another lane.
@@ -735,6 +521,7 @@ __device__ __forceinline__ void column_sums(const LinearParams &p, uint32_t i, u
         while (k + 1 < c.n && i >= c.group_end[k]) begin = c.group_end[k++];
         const uint32_t e = (i - begin) * 32 + lane % 4 * 8, cols = c.cols[k];
         const uint32_t n = e < cols ? min(cols - e, 8u) : 0;
+        constexpr uint32_t kSumRows = 6;   // loads under way
         float sum[8] = {};
         for (int q = c.stacked ? 0 : k; q < (c.stacked ? c.sources : k + 1); ++q) {
             if (c.f32) {
@@ -753,18 +540,21 @@ __device__ __forceinline__ void column_sums(const LinearParams &p, uint32_t i, u
                         for (uint32_t z = 0; z < 8; ++z) sum[z] += v[j][z];
                 }
             } else {
-                for (uint32_t first = lane / 4; first < c.rows[q]; first += 64) {
-                    uint32_t w[8][4];
+                for (uint32_t first = lane / 4; first < c.rows[q]; first += 8 * kSumRows) {
+                    Shifted v[kSumRows];
 #pragma unroll
-                    for (uint32_t j = 0; j < 8; ++j) {
+                    for (uint32_t j = 0; j < kSumRows; ++j) {
                         const uint16_t *from = static_cast<const uint16_t *>(c.src[q]) + (uint64_t)(first + 8 * j) * cols + e;
-                        w[j][0] = w[j][1] = w[j][2] = w[j][3] = 0;
-                        if (first + 8 * j < c.rows[q] && n && LINEAR_OK(kLinearDy + q, from, 2 * n)) load_shifted(from, n, w[j]);
+                        const bool there = first + 8 * j < c.rows[q] && n && LINEAR_OK(kLinearDy + q, from, 2 * n);
+                        v[j].load(from, there ? n : 0);
                     }
 #pragma unroll
-                    for (uint32_t j = 0; j < 8; ++j)
+                    for (uint32_t j = 0; j < kSumRows; ++j) {
+                        uint32_t w[4];
+                        v[j].get(w);
 #pragma unroll
-                        for (uint32_t z = 0; z < 8; ++z) sum[z] += z & 1 ? bf16_hi(w[j][z / 2]) : bf16_lo(w[j][z / 2]);
+                        for (uint32_t z = 0; z < 8; ++z) sum[z] += z & 1 ? bf16_hi(w[z / 2]) : bf16_lo(w[z / 2]);
+                    }
                 }
             }
         }
@@ -960,216 +750,46 @@ __global__ void __launch_bounds__(kThreads) linear_join_kernel(const __grid_cons
     DT_TL_END_BLOCK(DT_TL_LINEAR);
 }
 
-// ---- few tokens --------------------------------------------------------------
-
-// Forward products of up to 16 tokens, which the weights' way from memory bounds: 16
-// rows of W to a group of warps that split the inner axis, with the weights straight
-// from memory into the registers of mma.sync.m16n8k16 as its A, the tokens as its eight
-// or sixteen columns.  (A tile of tcgen05 would be 128 rows of tokens, nearly all
-// empty, and its way through shared and tensor memory is longer than the whole of a
-// small call.)  A lane takes eight consecutive elements of a row, in one load, as its
-// elements of two products: which of the inner axis' elements stand together in a
-// product is free as long as both operands agree.  The warps' sums are added in shared
-// memory, then those of the C CTAs of a cluster, which split the inner axis where there
-// are few rows, in a fixed order.
-constexpr uint32_t kFewRows = 16, kFewWarps = kThreads / 32;
-constexpr uint32_t kFewDepth = 128;                // of the inner axis, to a step of a warp
-
-__device__ __forceinline__ void mma_16x8x16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
-{
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-                 "{%0, %1, %2, %3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// Elements [k, k + 8) of a row of `len`; NULL: zeros.  The vector's load is volatile
-// so that a step's loads all go out before its products (the compiler, left to itself,
-// keeps a third of them under way, in 44 registers).
-template <bool VEC>
-__device__ __forceinline__ void few_load(const LinearFew &p, const uint16_t *row, uint32_t k, uint32_t len, int buffer,
-                                         uint32_t (&w)[4])
-{
-    (void)p, (void)buffer;
-    w[0] = w[1] = w[2] = w[3] = 0;
-    if (!row || k >= len) return;
-    if (VEC) {   // len is a multiple of 8
-        if (!LINEAR_OK(buffer, row + k, 16)) return;
-        asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(row + k));
-    } else {
-        const uint32_t n = min(len - k, 8u);
-        if (LINEAR_OK(buffer, row + k, 2 * n)) load_shifted(row + k, n, w);
-    }
-}
-
-// A float of another CTA of the cluster's shared memory.
-__device__ __forceinline__ float cluster_load(const float *here, uint32_t rank)
-{
-    float v;
-    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
-                 : "=f"(v)
-                 : "r"(smem_addr(here)), "r"(rank)
-                 : "memory");
-    return v;
-}
-
-template <int KIND, int NT, bool VEC, int C>
-__global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kThreads) linear_few_kernel(const __grid_constant__ LinearFew p)
-{
-    __shared__ float sums[kFewWarps][NT * 8][kFewRows + 1];
-    DT_TL_BEGIN();
-    pdl_begin();
-    DT_TL_WAITED();
-    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-    const uint32_t groups = kFewWarps / p.k_warps, group = warp / p.k_warps;
-    const uint32_t part = C > 1 ? cluster_rank() : 0, block = blockIdx.x / C;
-    // the block's rows of W: of one rank's features, or of the columns of a token
-    uint32_t r = 0, begin = 0;
-    if (KIND == kGather)
-        while ((int)r + 1 < p.P && block >= p.block_end[r]) begin = p.block_end[r++];
-    const uint32_t first = (block - begin) * groups * kFewRows, rows = KIND == kGather ? p.f_len[r] : p.dim;
-    const uint32_t row = first + group * kFewRows + g;   // this lane's rows: this and the eighth after it
-    // the tokens that this lane loads, and their rank
-    const uint16_t *token[NT];
-    int of[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const uint32_t t = n * 8 + g;
-        token[n] = nullptr;
-        of[n] = 0;
-        if (KIND == kGather && t < p.tokens) {
-            uint32_t at = 0;
-            while (of[n] + 1 < p.P && t >= p.row_end[of[n]]) at = p.row_end[of[n]++];
-            token[n] = p.x[of[n]] + (uint64_t)(t - at) * p.dim;
-        }
-    }
-    float c[NT][4] = {};
-    const uint32_t step = p.k_warps * C, mine = part * p.k_warps + warp % p.k_warps;
-    // steps of 128 of the inner axis, numbered through the ranks' pieces where it is features
-    uint32_t i = mine;
-    for (uint32_t f = KIND == kGather ? r : 0; f < (KIND == kGather ? r + 1 : (uint32_t)p.P); ++f) {
-        const uint32_t len = KIND == kGather ? p.dim : p.f_len[f], steps = (len + kFewDepth - 1) / kFewDepth;
-        const uint16_t *w0 = row < rows ? p.w[f] + (uint64_t)row * len : nullptr;
-        const uint16_t *w1 = row + 8 < rows ? p.w[f] + (uint64_t)(row + 8) * len : nullptr;
-        if (KIND == kReduce) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n) token[n] = n * 8 + g < p.tokens ? p.x[f] + (uint64_t)(n * 8 + g) * len : nullptr;
-        }
-        for (; i < steps; i += step) {
-            uint32_t a0[4][4], a1[4][4], b[NT][4][4];
-#pragma unroll
-            for (uint32_t j = 0; j < 4; ++j) {
-                const uint32_t k = i * kFewDepth + j * 32 + q * 8;
-                few_load<VEC>(p, w0, k, len, kLinearW + f, a0[j]);
-                few_load<VEC>(p, w1, k, len, kLinearW + f, a1[j]);
-            }
-#pragma unroll
-            for (uint32_t j = 0; j < 4; ++j)
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-                    few_load<VEC>(p, token[n], i * kFewDepth + j * 32 + q * 8, len, kLinearX + (KIND == kGather ? of[n] : (int)f),
-                                  b[n][j]);
-#pragma unroll
-            for (uint32_t j = 0; j < 4; ++j)
-#pragma unroll
-                for (uint32_t h = 0; h < 2; ++h) {
-                    const uint32_t a[4] = {a0[j][2 * h], a1[j][2 * h], a0[j][2 * h + 1], a1[j][2 * h + 1]};
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) mma_16x8x16(c[n], a, b[n][j][2 * h], b[n][j][2 * h + 1]);
-                }
-        }
-        i -= steps;
-    }
-    // a lane holds rows g and g + 8 of tokens 2 q and 2 q + 1
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        sums[warp][n * 8 + 2 * q][g] = c[n][0];
-        sums[warp][n * 8 + 2 * q + 1][g] = c[n][1];
-        sums[warp][n * 8 + 2 * q][g + 8] = c[n][2];
-        sums[warp][n * 8 + 2 * q + 1][g + 8] = c[n][3];
-    }
-    __syncthreads();
-    if (C > 1 && p.k_warps > 1) {   // the warps' sums into the first of each group
-        for (uint32_t o = threadIdx.x; o < groups * p.tokens * kFewRows; o += kThreads) {
-            const uint32_t at = o % kFewRows, t = o / kFewRows % p.tokens, w = o / kFewRows / p.tokens * p.k_warps;
-            float v = sums[w][t][at];
-            for (uint32_t k = 1; k < p.k_warps; ++k) v += sums[w + k][t][at];
-            sums[w][t][at] = v;
-        }
-    }
-    if (C > 1) cluster_sync();
-    for (uint32_t o = part * kThreads + threadIdx.x; o < groups * p.tokens * kFewRows; o += kThreads * C) {
-        const uint32_t at = o % kFewRows, t = o / kFewRows % p.tokens, w = o / kFewRows / p.tokens, f = first + w * kFewRows + at;
-        if (f >= rows) continue;
-        float v[2] = {0.0f, 0.0f};
-        if (C > 1) {
-            for (uint32_t k = 0; k < C; ++k) v[0] += cluster_load(&sums[w * p.k_warps][t][at], k);
-        } else {
-            for (uint32_t k = 0; k < p.k_warps; ++k) v[0] += sums[w * p.k_warps + k][t][at];
-        }
-        if (KIND == kGather) {
-            const uint64_t to = (uint64_t)t * rows + f;
-            if (p.biased && LINEAR_OK(kLinearBias + r, p.bias[r] + f, 2)) v[0] += bf16_to_f32(p.bias[r][f]);
-            if (p.keep && LINEAR_OK(kLinearPre + r, p.pre[r] + to, 2)) p.pre[r][to] = f32_to_bf16(v[0]);
-            activate(v, p.act);
-            if (LINEAR_OK(kLinearY + r, p.out[r] + to, 2)) p.out[r][to] = f32_to_bf16(v[0]);
-        } else {
-            uint32_t rank = 0, begin_row = 0;
-            while ((int)rank + 1 < p.P && t >= p.row_end[rank]) begin_row = p.row_end[rank++];
-            const uint64_t to = (uint64_t)(t - begin_row) * p.dim + f;
-            if (p.biased && LINEAR_OK(kLinearBias, p.bias[0] + f, 2)) v[0] += bf16_to_f32(p.bias[0][f]);
-            if (p.residuals && LINEAR_OK(kLinearResidual + rank, p.residual[rank] + to, 2))
-                v[0] += bf16_to_f32(p.residual[rank][to]);
-            if (LINEAR_OK(kLinearY + rank, p.out[rank] + to, 2)) p.out[rank][to] = f32_to_bf16(v[0]);
-        }
-    }
-    if (C > 1) cluster_sync();   // no CTA leaves while another reads its sums
-    DT_TL_END_BLOCK(DT_TL_LINEAR);
-}
-
 // A strip of 256 columns of a chunk of rows to a block: 32 threads across, eight columns
-// each, and eight rows at a time, four of them under way for each thread.
-template <bool VEC>
+// each, and eight rows at a time, two or four of them under way for each thread.
+template <bool VEC, bool PRE>
 __device__ __forceinline__ void prep_rows(const LinearPrep &p, const LinearPrepJob &job, uint32_t first, uint32_t end, uint32_t e,
                                           float (&sum)[8])
 {
-    constexpr uint32_t kBatch = 4;
+    constexpr uint32_t kBatch = !VEC && PRE ? 2 : 4;
     const uint32_t n = e < job.cols ? min(job.cols - e, 8u) : 0;
-    auto load = [&](const uint16_t *base, uint32_t row, int buffer, uint32_t (&w)[4]) {
+    auto load = [&](const uint16_t *base, uint32_t row, int buffer, Eight<VEC> &v) {
         (void)buffer;
         const uint16_t *at = base + (uint64_t)row * job.cols + e;
-        w[0] = w[1] = w[2] = w[3] = 0;
-        if (row >= end || n == 0 || !LINEAR_OK(buffer, at, 2 * n)) return;
-        if (VEC) {
-            const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(at));
-            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-        } else {
-            load_shifted(at, n, w);
-        }
+        v.load(at, row < end && n && LINEAR_OK(buffer, at, 2 * n) ? n : 0);
     };
 #pragma unroll 1
     for (uint32_t row0 = first + threadIdx.x / 32; row0 < end; row0 += 8 * kBatch) {
-        uint32_t w[kBatch][4], u[kBatch][4];
+        Eight<VEC> src[kBatch], pre[PRE ? kBatch : 1];
 #pragma unroll
         for (uint32_t k = 0; k < kBatch; ++k) {
-            load(job.src, row0 + 8 * k, job.src_buffer, w[k]);
-            if (job.pre) load(job.pre, row0 + 8 * k, job.pre_buffer, u[k]);
+            load(job.src, row0 + 8 * k, job.src_buffer, src[k]);
+            if (PRE) load(job.pre, row0 + 8 * k, job.pre_buffer, pre[PRE ? k : 0]);
         }
 #pragma unroll
         for (uint32_t k = 0; k < kBatch; ++k) {
             const uint32_t row = row0 + 8 * k;
             if (row >= end) break;
-            if (job.pre || job.sums) {
+            uint32_t w[4];
+            src[k].get(w);
+            if (PRE || job.sums) {
                 float g[8];
 #pragma unroll
-                for (uint32_t j = 0; j < 8; ++j) g[j] = j & 1 ? bf16_hi(w[k][j / 2]) : bf16_lo(w[k][j / 2]);
-                if (job.pre) {
+                for (uint32_t j = 0; j < 8; ++j) g[j] = j & 1 ? bf16_hi(w[j / 2]) : bf16_lo(w[j / 2]);
+                if (PRE) {
+                    uint32_t u[4];
                     float z[8];
+                    pre[PRE ? k : 0].get(u);
 #pragma unroll
-                    for (uint32_t j = 0; j < 8; ++j) z[j] = j & 1 ? bf16_hi(u[k][j / 2]) : bf16_lo(u[k][j / 2]);
+                    for (uint32_t j = 0; j < 8; ++j) z[j] = j & 1 ? bf16_hi(u[j / 2]) : bf16_lo(u[j / 2]);
                     times_slope(g, z, p.act);
 #pragma unroll
-                    for (uint32_t j = 0; j < 4; ++j) w[k][j] = pack_bf16x2(g[2 * j], g[2 * j + 1]);
+                    for (uint32_t j = 0; j < 4; ++j) w[j] = pack_bf16x2(g[2 * j], g[2 * j + 1]);
                 }
 #pragma unroll
                 for (uint32_t j = 0; j < 8; j += 2) {
@@ -1179,12 +799,12 @@ __device__ __forceinline__ void prep_rows(const LinearPrep &p, const LinearPrepJ
             }
             uint4 *to = reinterpret_cast<uint4 *>(job.dst + (uint64_t)row * job.pitch + e);
             if (job.dst && e < job.pitch && LINEAR_OK(kLinearWorkspace, to, 16))
-                *to = make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
+                *to = make_uint4(w[0], w[1], w[2], w[3]);
         }
     }
 }
 
-__global__ void __launch_bounds__(kThreads, 4) linear_prep_kernel(const __grid_constant__ LinearPrep p)
+__global__ void __launch_bounds__(kThreads, 3) linear_prep_kernel(const __grid_constant__ LinearPrep p)
 {
     __shared__ float part[8][kPrepCols + 4];
     DT_TL_BEGIN();
@@ -1198,8 +818,10 @@ __global__ void __launch_bounds__(kThreads, 4) linear_prep_kernel(const __grid_c
     const uint32_t first = chunk * p.chunk_rows, end = min(first + p.chunk_rows, job.rows);
     const uint32_t t = threadIdx.x % 32, e = strip * kPrepCols + t * 8;
     float sum[8] = {};
-    if (job.vec) prep_rows<true>(p, job, first, end, e, sum);
-    else prep_rows<false>(p, job, first, end, e, sum);
+    if (job.pre && job.vec) prep_rows<true, true>(p, job, first, end, e, sum);
+    else if (job.pre) prep_rows<false, true>(p, job, first, end, e, sum);
+    else if (job.vec) prep_rows<true, false>(p, job, first, end, e, sum);
+    else prep_rows<false, false>(p, job, first, end, e, sum);
     if (job.sums) {
 #pragma unroll
         for (uint32_t j = 0; j < 8; ++j) part[threadIdx.x / 32][t * 8 + j] = sum[j];
@@ -1247,25 +869,6 @@ cudaError_t launch_join(const LinearParams &p, uint32_t high, cudaStream_t s)
                          dim3(kThreads), 0, s, false, p);
 }
 
-template <int KIND, int NT, bool VEC>
-cudaError_t launch_few(const LinearFew &p, uint32_t ctas, cudaStream_t s)
-{
-    const dim3 grid(p.blocks * ctas), block(kThreads);
-    switch (ctas) {
-    case 8: return launch_kernel(linear_few_kernel<KIND, NT, VEC, 8>, grid, block, 0, s, false, p);
-    case 4: return launch_kernel(linear_few_kernel<KIND, NT, VEC, 4>, grid, block, 0, s, false, p);
-    case 2: return launch_kernel(linear_few_kernel<KIND, NT, VEC, 2>, grid, block, 0, s, false, p);
-    default: return launch_kernel(linear_few_kernel<KIND, NT, VEC, 1>, grid, block, 0, s, false, p);
-    }
-}
-
-template <int KIND>
-cudaError_t launch_few(const LinearFew &p, bool vec, uint32_t ctas, cudaStream_t s)
-{
-    if (p.tokens <= 8) return vec ? launch_few<KIND, 1, true>(p, ctas, s) : launch_few<KIND, 1, false>(p, ctas, s);
-    return vec ? launch_few<KIND, 2, true>(p, ctas, s) : launch_few<KIND, 2, false>(p, ctas, s);
-}
-
 }  // namespace
 
 DT_TL_BINDER(bind_timeline_linear)
@@ -1305,29 +908,6 @@ cudaError_t launch_linear_join(const LinearParams &p, LinearKind kind, int k, bo
     case kReduce: return launch_join<kReduce, false>(p, high, s);
     default: return k ? launch_join<kReduceBack, true>(p, high, s) : launch_join<kReduceBack, false>(p, high, s);
     }
-}
-
-// Warps and CTAs that share a row of W: two steps of the inner axis to a warp at least,
-// and as many CTAs as give the SMs two each.
-cudaError_t launch_linear_few(LinearFew &p, LinearKind kind, bool vec, int device, cudaStream_t s)
-{
-    uint64_t steps = 0, rows = 0;
-    for (int r = 0; r < p.P; ++r) {
-        if (kind == kGather) rows += (p.f_len[r] + kFewRows - 1) / kFewRows;
-        else steps += (p.f_len[r] + kFewDepth - 1) / kFewDepth;
-    }
-    if (kind == kGather) steps = (p.dim + kFewDepth - 1) / kFewDepth;
-    else rows = (p.dim + kFewRows - 1) / kFewRows;
-    p.k_warps = 1;
-    while (p.k_warps < kFewWarps && p.k_warps * 2 <= steps) p.k_warps *= 2;
-    const uint32_t groups = kFewWarps / p.k_warps;
-    p.blocks = 0;
-    for (int r = 0; r < p.P; ++r)
-        p.block_end[r] = p.blocks += kind == kGather ? (p.f_len[r] + groups * kFewRows - 1) / (groups * kFewRows) : 0;
-    if (kind == kReduce) p.blocks = (uint32_t)((rows + groups - 1) / groups);
-    uint32_t ctas = 1;
-    while (ctas < 8 && p.blocks * ctas < 2u * sm_count(device) && (uint64_t)ctas * 4 * p.k_warps <= steps) ctas *= 2;
-    return kind == kGather ? launch_few<kGather>(p, vec, ctas, s) : launch_few<kReduce>(p, vec, ctas, s);
 }
 
 cudaError_t launch_linear_prep(LinearPrep &p, cudaStream_t s)

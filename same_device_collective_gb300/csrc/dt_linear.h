@@ -61,20 +61,14 @@ struct LinearSums {
     int32_t n, sources, stacked, f32;
 };
 
-struct LinearParams {
-    CUtensorMap tok[DT_MAX_RANKS];     // the ranks' tokens [t_len, dim] (one map when they are one matrix)
-    CUtensorMap feat[DT_MAX_RANKS];    // [tokens, f_len]
-    CUtensorMap w[DT_MAX_RANKS];       // [f_len, dim], or reducing [dim, f_len]
+// What every kernel of a call knows.
+struct LinearCall {
     LinearProduct product[2];
     uint32_t f_len[DT_MAX_RANKS];
-    uint32_t t_len[DT_MAX_RANKS], t_first[DT_MAX_RANKS];   // pieces of the token axis in `tok`
+    uint32_t t_len[DT_MAX_RANKS], t_first[DT_MAX_RANKS];   // pieces of the token axis in the tokens' matrix
     uint32_t row_end[DT_MAX_RANKS];    // the ranks' tokens, numbered through
     int32_t P, t_pieces;
     uint32_t tokens, dim;
-    uint32_t bn;                       // tile width, a multiple of 32: up to 128, of pairs 256
-    uint32_t stages, workers;
-    uint32_t rows_t, rows_w;           // of the maps' boxes
-    uint32_t rest, early;              // the order of both products' tiles (next_tile)
     uint16_t *pre[DT_MAX_RANKS];
     const uint16_t *bias[DT_MAX_RANKS];
     const uint16_t *residual[DT_MAX_RANKS];
@@ -86,6 +80,30 @@ struct LinearParams {
     Extent extent[kLinearBuffers];
 #endif
 };
+
+// The tensor core kernels (linear_kernel).
+struct LinearParams : LinearCall {
+    CUtensorMap tok[DT_MAX_RANKS];     // the ranks' tokens [t_len, dim] (one map when they are one matrix)
+    CUtensorMap feat[DT_MAX_RANKS];    // [tokens, f_len]
+    CUtensorMap w[DT_MAX_RANKS];       // [f_len, dim], or reducing [dim, f_len]
+    uint32_t bn;                       // tile width, a multiple of 32: up to 256
+    uint32_t stages, workers;
+    uint32_t rows_t, rows_w;           // of the maps' boxes
+    uint32_t rest, early;              // the order of both products' tiles (next_tile)
+};
+
+// Small products, in place (linear_small_kernel): tiles of 64 x 64.
+struct LinearSmall : LinearCall {
+    const uint16_t *tok[DT_MAX_RANKS];     // the ranks' tokens
+    const uint16_t *feat[DT_MAX_RANKS];    // [tokens, f_len]
+    const uint16_t *weight[DT_MAX_RANKS];
+    const uint16_t *z[DT_MAX_RANKS];       // gathering, backward: what act'(.) is taken of, where act is not none
+    uint32_t ctas;                     // of a cluster: 1, 2, 4 or 8
+    uint32_t shared[2];                // they share a tile's inner axis; else each has a tile
+    uint32_t clusters[2];              // the first product's, and the second's after them; then those of the sums
+    uint32_t strips;                   // of 64 columns of the bias' gradient
+};
+constexpr uint32_t kSmallTile = 64;
 
 // What goes before the products: rows laid out again at a pitch that TMA can
 // address, the gradient before the activation, and column sums for the bias'.
@@ -134,8 +152,9 @@ constexpr uint32_t kFewTokens = 16;
 cudaError_t launch_linear(LinearParams &p, LinearKind kind, bool pairs, int device, cudaStream_t s);
 // The splits' sums into one, of product k.
 cudaError_t launch_linear_join(const LinearParams &p, LinearKind kind, int k, bool pairs, int device, cudaStream_t s);
-// vec: every row of x and w starts on a 16-byte boundary.
+// vec: every row that is read starts on a 16-byte boundary.
 cudaError_t launch_linear_few(LinearFew &p, LinearKind kind, bool vec, int device, cudaStream_t s);
+cudaError_t launch_linear_small(const LinearSmall &p, LinearKind kind, bool vec, cudaStream_t s);
 cudaError_t launch_linear_prep(LinearPrep &p, cudaStream_t s);
 // CTAs, or pairs of them, that run at once.
 uint32_t linear_workers(bool pairs, int device);

@@ -68,6 +68,7 @@ cudaError_t matrix_map(CUtensorMap *map, const void *base, uint64_t cols, uint64
 void bind_timeline_norm(const void *sink);
 void bind_timeline_vocab(const void *sink);
 void bind_timeline_linear(const void *sink);
+void bind_timeline_linear_small(const void *sink);
 void bind_timeline_residual(const void *sink);
 #endif
 
