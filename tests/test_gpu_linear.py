@@ -468,3 +468,57 @@ def test_f32_is_unsupported(dt):
         with pytest.raises(dt.DtError) as e:
             dt.dt_linear_reduce(g, [f(4, 8)], [f(8, 8)], None, None, [f(4, 8)], [4], 0, 8, [8], 0, "f32", ws)
         assert e.value.status == dt.DT_ERR_UNSUPPORTED
+
+
+# sizes that the tensor cores' tiles take: one CTA and pairs, widths that TMA cannot address, ranks' pieces that are read
+# in place, as one, or laid out again, tiles that end inside a rank, and inner axes that are split over the SMs
+LARGE = [
+    ([100], 2048, [4000]),
+    ([60, 0, 61], 1999, [3001, 0, 2001]),
+    ([128], 4096, [512]),
+    ([256, 128, 384], 1024, [1024, 512, 640]),
+    ([700, 521], 1021, [2003, 1000]),
+    ([300, 900, 100, 260], 1500, [515, 700, 1030, 129]),
+    ([1, 1300, 0, 11], 1024, [1500, 8, 0, 800]),
+    ([2000, 2100], 136, [3000, 1000]),
+    ([9000, 7000], 72, [100, 30]),
+    ([20000], 64, [64]),
+    ([512], 6000, [100, 100]),
+    ([160, 96], 64, [9000, 7000]),
+]
+
+
+@pytest.mark.parametrize("which", WHICH)
+@pytest.mark.parametrize("offset", [0, 3])
+@pytest.mark.parametrize("shape", LARGE, ids=str)
+def test_large_products(dt, which, shape, offset):
+    rows, dim, features = padded(shape, max(len(shape[0]), len(shape[2])))
+    a = Layer(dt, which, rows, dim, features, seed=dim + 2, offset=offset)
+    with group(a.P) as g:
+        act = ACTS[(sum(rows) + dim) % 4] if which == "gather_linear" else "none"
+        a.check_forward(a.forward(g, act) if which == "gather_linear" else a.forward(g), act)
+        a.check_backward(a.backward(g, act), act)
+        assert dt.dt_group_check(g) == dt.DT_OK
+
+
+def test_ends_of_the_activations(dt):
+    """Zeros, infinities and NaN before each activation: relu and gelu of infinities are their limits (gelu
+    of minus infinity 0), a NaN stays one, and silu of minus infinity is no number, as its formula says."""
+    inf, nan = float("inf"), float("nan")
+    x = torch.tensor([0.0, -0.0, inf, -inf, nan, 300.0, -300.0, 1e-30], device="cuda").to(BF16)
+    for n in (8, 40, 20000):   # tokens of one column: a kernel each
+        with group(1) as g:
+            for act in ACTS:
+                X = x[torch.arange(n, device="cuda") % 8][:, None].contiguous()
+                y = torch.empty(n, 8, dtype=BF16, device="cuda")
+                ws = workspace(dt, "gather_linear", g, [n], 1, [8], False)
+                dt.dt_gather_linear(g, [X], [torch.ones(8, 1, dtype=BF16, device="cuda")], None, None, [y], [n], 0, 1, [8], 0,
+                                    "bf16", act, ws)
+                want = act64(X.double(), act).repeat(1, 8)
+                if act == "gelu":
+                    want[X[:, 0] == -inf] = 0.0
+                assert torch.equal(y.isnan(), want.isnan())
+                ok = ~want.isnan()
+                assert torch.equal(y.double().isinf()[ok], want.isinf()[ok])
+                fin = ok & ~want.isinf()
+                assert ((y.double() - want).abs()[fin] <= (2 * R * want.abs() + 1e-37)[fin]).all()
