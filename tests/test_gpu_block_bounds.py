@@ -36,11 +36,12 @@ res = {}
 gen = torch.Generator("cuda").manual_seed(3)
 bf16, f32 = torch.bfloat16, torch.float32
 def made(*shape, dtype=bf16): return torch.randn(*shape, generator=gen, device="cuda").to(dtype)
-def sevens(*shape, dtype=bf16): return torch.full(shape, 7.0, dtype=dtype, device="cuda")
+MARK = 2.0 ** 100   # what no result is (results of bf16 do come out as a round number)
+def marked(*shape, dtype=bf16): return torch.full(shape, MARK, dtype=dtype, device="cuda")
 def tail(t, n):
     # the last n elements kept their value, all others were written
     t = t.reshape(-1)
-    return bool((t[len(t) - n:] == 7).all()) and bool((t[:len(t) - n] != 7).all())
+    return bool((t[len(t) - n:] == MARK).all()) and bool((t[:len(t) - n] != MARK).all())
 
 P = 2
 g = dt.dt_group_create(P, 0)
@@ -58,26 +59,26 @@ for name, rows, dim, features in (("few", [3, 2], 64, [40, 24]), ("small", [20, 
     w1, w2, b1, b2 = [made(f, dim) for f in features], [made(dim, f) for f in features], [made(f) for f in features], made(dim)
     args = (rows, 0, dim, features, 0, "bf16")
     ws = torch.empty(max(q(g, *args, b) for q in (dt.dt_gather_linear_workspace, dt.dt_linear_reduce_workspace) for b in (False, True)), dtype=torch.uint8, device="cuda")
-    y, pre = ([sevens(n, f) for f in features] for _ in range(2))
+    y, pre = ([marked(n, f) for f in features] for _ in range(2))
     dt.dt_gather_linear(g, x, w1, b1, pre, y, *args, "silu", ws)
     record(name + " gather", lambda: all(tail(t, 8) for t in (*y, *pre)))
-    dx, dw, db = [sevens(k, dim) for k in rows], [sevens(f, dim) for f in features], [sevens(f) for f in features]
+    dx, dw, db = [marked(k, dim) for k in rows], [marked(f, dim) for f in features], [marked(f) for f in features]
     dt.dt_gather_linear_backward(g, x, w1, h, h, dx, dw, db, *args, "gelu", ws)
     record(name + " gather_bwd", lambda: all(tail(t, 8) for t in (*dx, *dw, *db)))
-    z = [sevens(k, dim) for k in rows]
+    z = [marked(k, dim) for k in rows]
     dt.dt_linear_reduce(g, h, w2, b2, x, z, *args, ws)
     record(name + " reduce", lambda: all(tail(t, 8) for t in z))
-    dx, dw, db = [sevens(n, f) for f in features], [sevens(dim, f) for f in features], sevens(dim)
+    dx, dw, db = [marked(n, f) for f in features], [marked(dim, f) for f in features], marked(dim)
     dt.dt_linear_reduce_backward(g, h, w2, x, dx, dw, db, *args, ws)
     record(name + " reduce_bwd", lambda: all(tail(t, 8) for t in (*dx, *dw, db)))
 
 for name, rows, cols in (("few", [3, 2], 256), ("rings", [400, 200], 256), ("long", [2, 3], 9000)):
     x, o, dy, dz = ([made(k, cols) for k in rows] for _ in range(4))
     w = [made(cols, dtype=f32) for _ in range(3)]
-    y, z, r1, r2 = [sevens(k, cols) for k in rows], [sevens(k, cols) for k in rows], [made(k, dtype=f32) for k in rows], [made(k, dtype=f32) for k in rows]
+    y, z, r1, r2 = [marked(k, cols) for k in rows], [marked(k, cols) for k in rows], [made(k, dtype=f32) for k in rows], [made(k, dtype=f32) for k in rows]
     dt.dt_residual_norm(g, x, o, *w, 1.0, y, z, None, None, rows, 0, cols, 1e-6, "bf16", "f32")
     record(name + " norm", lambda: all(tail(t, 8) for t in (*y, *z)))
-    dx, do, dw = [sevens(k, cols) for k in rows], [sevens(k, cols) for k in rows], [sevens(cols, dtype=f32) for _ in range(3)]
+    dx, do, dw = [marked(k, cols) for k in rows], [marked(k, cols) for k in rows], [marked(cols, dtype=f32) for _ in range(3)]
     ws = torch.empty(dt.dt_residual_norm_workspace(g, cols), dtype=torch.uint8, device="cuda")
     dt.dt_residual_norm_backward(g, o, x, dy, dz, *w, 1.0, r1, r2, dx, do, *dw, rows, 0, cols, "bf16", "f32", "sum", ws)
     record(name + " norm_bwd", lambda: all(tail(t, 8) for t in (*dx, *do)) and all(tail(t, 4) for t in dw))

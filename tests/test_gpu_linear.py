@@ -522,3 +522,17 @@ def test_ends_of_the_activations(dt):
                 assert torch.equal(y.double().isinf()[ok], want.isinf()[ok])
                 fin = ok & ~want.isinf()
                 assert ((y.double() - want).abs()[fin] <= (2 * R * want.abs() + 1e-37)[fin]).all()
+
+
+@pytest.mark.parametrize("which", WHICH)
+@pytest.mark.parametrize("rows", [[1], [2, 0, 3], [7, 5], [16]])
+@pytest.mark.parametrize("long,short", [(4096, 64), (9001, 33), (33000, 40), (20000, 1000)])
+def test_few_tokens_of_a_long_inner_axis(dt, which, rows, long, short):
+    """Single tokens whose inner axis is shared by the CTAs of a cluster."""
+    P = len(rows)
+    cut = lambda n: [n * (r + 1) // P - n * r // P for r in range(P)]
+    dim, features = (long, cut(short)) if which == "gather_linear" else (short, cut(long))
+    a = Layer(dt, which, rows, dim, features, seed=long)
+    with group(P) as g:
+        a.check_forward(a.forward(g, "relu") if which == "gather_linear" else a.forward(g), "relu")
+        assert dt.dt_group_check(g) == dt.DT_OK

@@ -339,3 +339,14 @@ def test_refusals(dt):
             call(x=a.x[:1])
         assert dt.dt_residual_norm_workspace(g, 0) == 0
         assert dt.dt_group_check(g) == dt.DT_OK
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,cols", [([500, 1, 200], 8192), ([700], 4104), ([400, 9], 5001), ([1000], 101), ([3, 400], 8191),
+                                       ([20000], 8), ([5000, 3000], 24), ([160, 200], 20000)])
+def test_many_rows_of_other_widths(dt, rows, cols, dtype):
+    a = Rows(dt, rows, cols, dtype, "f32", seed=cols)
+    with group(len(rows)) as g:
+        a.check_forward(a.forward(g))
+        a.check_backward(a.backward(g))
+        assert dt.dt_group_check(g) == dt.DT_OK
