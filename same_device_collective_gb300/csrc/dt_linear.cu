@@ -273,6 +273,17 @@ __device__ __forceinline__ uint16_t *lane_pointer(uint16_t *v, uint32_t lane)
     return reinterpret_cast<uint16_t *>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<uint64_t>(v), lane));
 }
 
+// The number of the buffer of another lane's row, which checks of bounds alone ask for
+// (8192 tokens of 512 to 8192 with a bias: with these shuffles 63 us, 57.6 without).
+__device__ __forceinline__ int lane_buffer(int buffer, uint32_t lane)
+{
+#ifdef DT_BOUNDS
+    return __shfl_sync(0xFFFFFFFFu, buffer, lane);
+#else
+    return (void)lane, buffer;
+#endif
+}
+
 // 16-byte chunk c (of four) of row r of a finishing warp's 32 x 64 bytes of shared
 // memory: a thread writes its row, and four threads read a row, without bank conflicts.
 __device__ __forceinline__ unsigned char *step_chunk(unsigned char *buf, uint32_t row, uint32_t c)
@@ -299,7 +310,7 @@ __device__ __forceinline__ void move_rows(const LinearParams &p, unsigned char *
         for (uint32_t k = 0; k < 4; ++k) {
             const uint32_t r = k0 + k * kRows + first;
             at[k] = lane_pointer(row, r);
-            const int of = __shfl_sync(0xFFFFFFFFu, buffer, r);
+            const int of = lane_buffer(buffer, r);
             if (!at[k] || e >= cols || !LINEAR_OK(of, at[k] + e, 2 * N)) at[k] = nullptr;
             (void)of;
             W *word = reinterpret_cast<W *>(step_chunk(buf, r, e >> 3) + (e & 7) * 2);
@@ -329,7 +340,7 @@ __device__ __forceinline__ void move_rows_odd(const LinearParams &p, unsigned ch
 #pragma unroll
         for (uint32_t k = 0; k < 16; ++k) {
             uint16_t *at = lane_pointer(row, r0 + k);
-            const int of = __shfl_sync(0xFFFFFFFFu, buffer, r0 + k);
+            const int of = lane_buffer(buffer, r0 + k);
             (void)of;
             const bool there = at && lane < cols && LINEAR_OK(of, at + lane, 2);
             v[k] = 0;
