@@ -94,8 +94,12 @@ bool cut(const dt_group *g, const Plan &v, bool pieces, Cut &best)
         if (b) c.nt[1] = c.nt[0];
         for (int k = 0; k < 2; ++k)
             if (c.mt[k] * c.nt[k] > 0x7FFFFFFF / workers) return false;   // tiles are counted in 32 bits
-        const uint64_t most[2] = {std::max<uint64_t>(1, std::min<uint64_t>(16, c.kblocks[0] * depth / 512)),
-                                  std::max<uint64_t>(1, std::min<uint64_t>(16, c.kblocks[1] * depth / 512))};
+        // splits of 512 at least; none where a join would have more rows of blocks than a grid can
+        uint64_t most[2];
+        for (int k = 0; k < 2; ++k)
+            most[k] = c.mt[k] * v.halves * 128 > 65535
+                          ? 1
+                          : std::max<uint64_t>(1, std::min<uint64_t>(16, c.kblocks[k] * depth / 512));
         for (c.splits[0] = 1; c.splits[0] <= most[0]; ++c.splits[0])
             for (c.splits[1] = 1; c.splits[1] <= most[1]; ++c.splits[1]) {
                 double unit[2], longest = 0.0, all = 0.0;

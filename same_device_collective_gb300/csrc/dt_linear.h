@@ -34,8 +34,7 @@ enum LinearBuffer : int {
 
 // The depth of a stage, and of the blocks that the inner axis is cut into: 64, or where
 // an operand's rows run along the inner axis 128, so that its boxes of 64 columns are
-// not short.  (Forward 128 deep, half as many stages: 2048 tokens of 4096 to 16384
-// @E@ -> @F@ us.)
+// not short.  Forward, more and shorter stages ride out the loads' latency.
 __host__ __device__ constexpr uint32_t linear_depth(bool back) { return back ? 128 : 64; }
 
 // One product of a launch: its tiles, splits of its inner axis, and outputs.

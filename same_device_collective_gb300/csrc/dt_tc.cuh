@@ -167,8 +167,8 @@ __device__ __forceinline__ void tmem_load8(uint32_t tmem, float (&v)[8])
 // One box of a row-major matrix at (column, row) into this CTA's shared
 // memory; what lies outside the matrix is filled with zeros and counts towards
 // the barrier's bytes.  Of a pair, both CTAs' loads complete on the barrier
-// at this place in the first CTA.  The column is a multiple of 64, so the copy
-// starts on a 16-byte boundary.
+// at this place in the first CTA.  The column is a multiple of eight 16-bit
+// elements, so the copy starts on a 16-byte boundary.
 template <int CG>
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap *map, int32_t col, int32_t row, uint32_t bar)
 {

@@ -53,7 +53,7 @@ def record(name, tails):
 
 # few tokens, small products, the tensor cores' tiles, and those with the inner axis split
 for name, rows, dim, features in (("few", [3, 2], 64, [40, 24]), ("small", [20, 30], 64, [48, 96]),
-                                  ("tiles", [400, 700], 1024, [1000, 1048]), ("splits", [40, 30], 8192, [2048, 1024])):
+                                  ("tiles", [400, 700], 1024, [1000, 1048]), ("splits", [40, 30], 8192, [2048, 1000])):
     n = sum(rows)
     x, h = [made(k, dim) for k in rows], [made(n, f) for f in features]
     w1, w2, b1, b2 = [made(f, dim) for f in features], [made(dim, f) for f in features], [made(f) for f in features], made(dim)

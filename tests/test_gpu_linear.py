@@ -501,6 +501,21 @@ def test_large_products(dt, which, shape, offset):
         assert dt.dt_group_check(g) == dt.DT_OK
 
 
+def test_many_tokens_of_few_features_and_a_long_inner_axis(dt):
+    """More rows than a grid has in its second dimension, where splits of the inner axis would pay."""
+    rows, dim, features = [60001, 5999], 16384, [200, 0]
+    layer = Layer(dt, "gather_linear", rows, dim, features, bias=False)
+    with group(2) as g:
+        pre, y = layer.forward(g)
+    x = torch.cat(layer.x)
+    some = torch.cat([torch.arange(0, 80), torch.arange(32700, 32800), torch.arange(59990, 60010),
+                      torch.arange(65500, 66000)]).cuda()
+    want = x[some].double() @ layer.w[0].double().T
+    tol = sum_error(dim, 2) * (x[some].double().abs() @ layer.w[0].double().abs().T)
+    check(y[0][some], want, tol, "y")
+    check(pre[0][some], want, tol, "pre")
+
+
 def test_ends_of_the_activations(dt):
     """Zeros, infinities and NaN before each activation: relu and gelu of infinities are their limits (gelu
     of minus infinity 0), a NaN stays one, and silu of minus infinity is no number, as its formula says."""
