@@ -436,6 +436,20 @@ bool run_small(Call &c, const void *const *tok, const void *const *feat, const v
     return true;
 }
 
+// Whether few tokens' forward products go straight from memory to mma.sync: up to eight tokens
+// until the weights are many times L2 (8 of 4096 to 16384, 134 MB: 27.9 us, in tensor core
+// tiles 28.5; of 8192 to 28672, 470 MB: 77.5 and 73.5), up to 16, whose sums take registers
+// from the loads in flight, while they are half of it (12 of 4096 to 8192: 12.7 and 13.9; to
+// 16384: 32.7 and 29.0), and weights that TMA cannot read always.
+bool few(const Call &c, const void *const *w)
+{
+    const Plan &v = c.v;
+    if (v.tokens > dt::kFewTokens) return false;
+    for (int r = 0; r < c.g->P; ++r)
+        if (v.f[r] && !addressable(w[r], gathers(v.kind) ? v.dim : v.f[r])) return true;
+    return 2.0 * v.features * v.dim <= (v.tokens <= 8 ? 256e6 : 72e6);
+}
+
 // The forward products of few tokens.
 cudaError_t run_few(Call &c, const void *const *x, const void *const *w, cudaStream_t s)
 {
@@ -597,7 +611,7 @@ dt_status dt_gather_linear(dt_group_t g, const void *const *x, const void *const
     }
     DeviceScope scope(g->device);
     if (!scope.ok) return DT_ERR_CUDA;
-    if (v.tokens <= dt::kFewTokens) return cuda_status(run_few(c, x, weight, static_cast<cudaStream_t>(stream)));
+    if (few(c, weight)) return cuda_status(run_few(c, x, weight, static_cast<cudaStream_t>(stream)));
     cudaError_t e = cudaSuccess;
     if (run_small(c, x, nullptr, weight, nullptr, act, false, false, static_cast<cudaStream_t>(stream), e)) return cuda_status(e);
     token_matrix(c, x, dt::kLinearX, nullptr);
@@ -736,7 +750,7 @@ dt_status dt_linear_reduce(dt_group_t g, const void *const *x, const void *const
     c.p.product[0].align[0] = align;
     DeviceScope scope(g->device);
     if (!scope.ok) return DT_ERR_CUDA;
-    if (v.tokens <= dt::kFewTokens) return cuda_status(run_few(c, x, weight, static_cast<cudaStream_t>(stream)));
+    if (few(c, weight)) return cuda_status(run_few(c, x, weight, static_cast<cudaStream_t>(stream)));
     cudaError_t e = cudaSuccess;
     if (run_small(c, nullptr, x, weight, nullptr, DT_ACT_NONE, false, false, static_cast<cudaStream_t>(stream), e))
         return cuda_status(e);

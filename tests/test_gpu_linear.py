@@ -501,6 +501,47 @@ def test_large_products(dt, which, shape, offset):
         assert dt.dt_group_check(g) == dt.DT_OK
 
 
+@pytest.mark.parametrize("which", WHICH)
+@pytest.mark.parametrize("shape", [([7, 5], 4096, [5000, 4600]), ([2, 1], 8192, [16000, 400])], ids=str)
+def test_few_tokens_of_large_weights(dt, which, shape):
+    a = Layer(dt, which, *shape, seed=21)
+    with group(2) as g:
+        a.check_forward(a.forward(g, "gelu") if which == "gather_linear" else a.forward(g),
+                        "gelu" if which == "gather_linear" else "none")
+        assert dt.dt_group_check(g) == dt.DT_OK
+
+
+@pytest.mark.parametrize("rows,dim,features", [([3, 2], 72, [40, 24]), ([40, 30], 200, [64, 24]),
+                                               ([300, 84], 64, [4096, 4096]), ([700, 324], 2048, [512, 512])])
+def test_residual_in_place_of_every_size(dt, rows, dim, features):
+    """y in the residual's place: few tokens, small products, splits of the inner axis, and large ones."""
+    a = Layer(dt, "linear_reduce", rows, dim, features, seed=9)
+    with group(2) as g:
+        want = a.forward(g)
+        a.check_forward(want)
+        a.forward(g, y=a.res)
+        assert all(torch.equal(got, w) for got, w in zip(a.res, want))
+
+
+@pytest.mark.parametrize("which", WHICH)
+def test_two_calls_at_once(dt, which):
+    """Calls on two streams, each with its own workspace and outputs, as a group's calls may run."""
+    layers = [Layer(dt, which, [300, 212], 520, [600, 136], seed=s) for s in (31, 32)]
+    with group(2) as g:
+        streams = [torch.cuda.Stream() for _ in layers]
+        torch.cuda.synchronize()
+        outs = []
+        for _ in range(3):
+            for a, s in zip(layers, streams):
+                with torch.cuda.stream(s):
+                    outs.append((a, a.forward(g), a.backward(g)))
+        torch.cuda.synchronize()
+        for a, fwd, bwd in outs:
+            a.check_forward(fwd)
+            a.check_backward(bwd)
+        assert dt.dt_group_check(g) == dt.DT_OK
+
+
 def test_many_tokens_of_few_features_and_a_long_inner_axis(dt):
     """More rows than a grid has in its second dimension, where splits of the inner axis would pay."""
     rows, dim, features = [60001, 5999], 16384, [200, 0]
