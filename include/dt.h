@@ -442,10 +442,10 @@ size_t dt_vocab_loss_workspace(dt_group_t g, const size_t *vocab, size_t vocab_e
  * n is the sum of rows (n of them number the tokens in rank order); a rank may have
  * no tokens or no features, all ranks together need a feature.  dtype is that of
  * every tensor: DT_BF16, products in the tensor cores and fp32 sums; DT_F32 is
- * DT_ERR_UNSUPPORTED.  Tensors are dense and 2-byte aligned.  Those whose rows start
- * on 16-byte boundaries are read in place, others are laid out again in the workspace
- * first, as are tokens whose ranks' pieces would leave more than a twentieth of the
- * tiles of 128 rows to their ends.
+ * DT_ERR_UNSUPPORTED.  Tensors are dense and 2-byte aligned.  Few tokens and small
+ * products read them in place; of larger ones those whose rows start on 16-byte
+ * boundaries are, others are laid out again in the workspace first, as are tokens whose
+ * ranks' pieces would leave more than a twentieth of the tiles of 128 rows to their ends.
  * workspace: the query's bytes of device memory, 256-byte aligned, free for other use
  * once `stream` has passed the call.  No output may overlap another buffer, but for
  * the residual below.  n is at most 2^26, dim and the sum of features 2^22.  The
@@ -528,8 +528,9 @@ size_t dt_linear_reduce_workspace(dt_group_t g, const size_t *rows, size_t rows_
  * [cols] of weight_dtype or NULL (1), serve all ranks.  dtype and weight_dtype are
  * DT_F32 or DT_BF16.  All sums are fp32, the second norm is of y before its rounding,
  * and y and z are rounded once.  rstd_post and rstd_pre, float arrays of rows[r] for
- * each rank (or NULL: not wanted), receive both reciprocals for the backward call.  y[r] may be x[r]
- * and z[r] may be branch[r] (in place); otherwise no output may overlap another buffer.
+ * each rank (or NULL: not wanted), receive both reciprocals for the backward call.  y[r]
+ * may be x[r] and z[r] may be branch[r] (in place); otherwise no output may overlap another
+ * buffer.
  * Pointers are multiples of their element size; rows that all start on 16-byte boundaries
  * move as vectors.  cols is 1..2^24, residual_scale any finite number.  A NaN or an
  * infinity in a row makes results of that row NaN, and no other's.  The same call gives
