@@ -109,14 +109,17 @@ struct Tile {
 __device__ __forceinline__ void place_tile(const LinearProduct &c, uint32_t i, Tile &t)
 {
     const uint32_t per_split = c.mt * c.nt;
-    t.split = i / per_split;
-    i -= t.split * per_split;
+    t.split = 0, t.kb0 = 0, t.kb1 = c.kblocks;
+    if (c.splits > 1) {   // at most 16 splits of 2^20 blocks
+        t.split = i / per_split;
+        i -= t.split * per_split;
+        t.kb0 = c.kblocks * t.split / c.splits;
+        t.kb1 = c.kblocks * (t.split + 1) / c.splits;
+    }
     const uint32_t all = kGroup * c.mt, g = i / all;
     i -= g * all;
     t.n = g * kGroup + i / c.mt;
     t.m = i % c.mt;
-    t.kb0 = (uint32_t)((uint64_t)c.kblocks * t.split / c.splits);
-    t.kb1 = (uint32_t)((uint64_t)c.kblocks * (t.split + 1) / c.splits);
 }
 
 // The k-th tile of worker q (a CTA or a pair) of W; false when it has no more.
@@ -210,13 +213,15 @@ __device__ __forceinline__ bool load_tile(const LinearParams &p, const LinearPro
         const CUtensorMap *a_map = operand<R, R::a>(p, at, a_col, a_row), *b_map = operand<R, R::b>(p, at, b_col, b_row);
         (R::b_mn ? b_col : b_row) += half * bn;
         for (uint32_t i = 0; i < k.blocks; ++i, ++n) {
-            if (!wait(empty + 8 * s, round ^ 1)) return false;
+            if (!__all_sync(0xFFFFFFFFu, wait(empty + 8 * s, round ^ 1))) return false;
             const uint32_t bar = full + 8 * s, a = ring + s * stage_bytes, b = a + a_boxes(kBack) * a_box;
-            if (half == 0) mbar_expect_tx(bar, bytes);
-            tma_box<CG>(a, a_map, a_col, a_row, bar);
-            if (a_boxes(kBack) == 2) tma_box<CG>(a + a_box, a_map, a_col + 64, a_row, bar);
-            tma_box<CG>(b, b_map, b_col, b_row, bar);
-            if (boxes == 2) tma_box<CG>(b + kBoxBytes, b_map, b_col + 64, b_row, bar);
+            if (elect_one()) {
+                if (half == 0) mbar_expect_tx(bar, bytes);
+                tma_box<CG>(a, a_map, a_col, a_row, bar);
+                if (a_boxes(kBack) == 2) tma_box<CG>(a + a_box, a_map, a_col + 64, a_row, bar);
+                tma_box<CG>(b, b_map, b_col, b_row, bar);
+                if (boxes == 2) tma_box<CG>(b + kBoxBytes, b_map, b_col + 64, b_row, bar);
+            }
             (R::a_mn ? a_row : a_col) += R::depth;
             (R::b_mn ? b_row : b_col) += R::depth;
             if (++s == stages) s = 0, round ^= 1;
@@ -254,15 +259,16 @@ __device__ __forceinline__ bool multiply_tile(const LinearParams &p, const Linea
     bool add = false;
     do {
         for (uint32_t i = 0; i < k.blocks; ++i) {
-            if (!wait(full + 8 * s, round)) return false;
+            if (!__all_sync(0xFFFFFFFFu, wait(full + 8 * s, round))) return false;
             tc_fence_after();
             const uint32_t at = s * (stage_bytes >> 4);
-            if (k.last < R::depth / 16 && k.ends && i + 1 == k.blocks)
-                multiply_stage<R, CG>(acc, a0 + at, b0 + at, desc, add, k.last, a_box);
-            else
-                multiply_stage<R, CG>(acc, a0 + at, b0 + at, desc, add, R::depth / 16, a_box);
+            const bool whole = k.last == R::depth / 16 || !k.ends || i + 1 < k.blocks;
+            if (elect_one()) {
+                if (whole) multiply_stage<R, CG>(acc, a0 + at, b0 + at, desc, add, R::depth / 16, a_box);
+                else multiply_stage<R, CG>(acc, a0 + at, b0 + at, desc, add, k.last, a_box);
+                mma_commit<CG>(empty + 8 * s);
+            }
             add = true;
-            mma_commit<CG>(empty + 8 * s);
             if (++s == stages) s = 0, round ^= 1;
         }
     } while (k.next(p));
@@ -600,7 +606,8 @@ linear_kernel(const __grid_constant__ LinearParams p)
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(ctl + kBarBytes - 8);
     volatile uint32_t *gave_up = tmem_slot + 1;
     static_assert(16 * kMaxStages + 40 <= kBarBytes - 8, "room for the barriers");
-    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // (the shuffle tells the compiler that a warp is one's whole)
+    const uint32_t warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t half = CG == 2 ? cluster_rank() : 0;                // of the tile's rows
     const uint32_t worker = blockIdx.x / CG, workers = gridDim.x / CG;
 
@@ -624,7 +631,7 @@ linear_kernel(const __grid_constant__ LinearParams p)
     if (CG == 2) cluster_sync();
     else __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
     Tile t;
     pdl_begin();
     DT_TL_WAITED();
@@ -632,33 +639,30 @@ linear_kernel(const __grid_constant__ LinearParams p)
     const uint32_t a_box = a_box_bytes(kBack, p.rows_t), stage_bytes = stage_size(kBack, p.rows_t, p.bn / CG);
 
     if (warp == FW) {
-        if (lane == 0) {
-            uint32_t n = 0, s = 0, round = 0;   // loads issued; the next one's stage and its parity
-            bool ok = true;
-            for (uint32_t k = 0; ok && next_tile<KIND>(p, worker, workers, k, t); ++k) {
-                if (kBack && t.second)
-                    ok = load_tile<Second, CG>(p, p.product[1], t, half, ring, stage_bytes, a_box, full, empty, wait, s,
-                                               round, n);
-                else
-                    ok = load_tile<First, CG>(p, p.product[0], t, half, ring, stage_bytes, a_box, full, empty, wait, s,
-                                              round, n);
-            }
-            // leave nothing in flight: the stages are consumed or, where that
-            // was given up, at least loaded (a pair's loads complete on its
-            // first CTA's barriers, and neither CTA leaves before the other)
+        uint32_t n = 0, s = 0, round = 0;   // loads issued; the next one's stage and its parity
+        bool ok = true;
+        for (uint32_t k = 0; ok && next_tile<KIND>(p, worker, workers, k, t); ++k) {
+            if (kBack && t.second)
+                ok = load_tile<Second, CG>(p, p.product[1], t, half, ring, stage_bytes, a_box, full, empty, wait, s, round, n);
+            else
+                ok = load_tile<First, CG>(p, p.product[0], t, half, ring, stage_bytes, a_box, full, empty, wait, s, round, n);
+        }
+        // leave nothing in flight: the stages are consumed or, where that
+        // was given up, at least loaded (a pair's loads complete on its
+        // first CTA's barriers, and neither CTA leaves before the other)
+        if (lane == 0)
             for (uint32_t k = n > p.stages ? n - p.stages : 0; k < n; ++k) {
                 const uint32_t at = k % p.stages, parity = (k / p.stages) & 1;
                 if ((*gave_up || !wait(empty + 8 * at, parity)) && half == 0) wait(full + 8 * at, parity);
             }
-        }
         __syncwarp();
     } else if (warp == FW + 1) {
-        if (lane == 0 && half == 0) {
+        if (half == 0) {
             uint32_t s = 0, round = 0;
             bool ok = true;
             for (uint32_t u = 0; ok && next_tile<KIND>(p, worker, workers, u, t); ++u) {
                 const uint32_t acc = tmem + (u & 1) * 256;
-                if (!(ok = wait(acc_empty + 8 * (u & 1), ((u >> 1) & 1) ^ 1))) break;
+                if (!(ok = __all_sync(0xFFFFFFFFu, wait(acc_empty + 8 * (u & 1), ((u >> 1) & 1) ^ 1)))) break;
                 tc_fence_after();
                 if (kBack && t.second)
                     ok = multiply_tile<Second, CG>(p, p.product[1], t, acc, ring, stage_bytes, a_box, full, empty, wait, s,
@@ -666,10 +670,10 @@ linear_kernel(const __grid_constant__ LinearParams p)
                 else
                     ok = multiply_tile<First, CG>(p, p.product[0], t, acc, ring, stage_bytes, a_box, full, empty, wait, s,
                                                   round);
-                if (ok) mma_commit<CG>(acc_full + 8 * (u & 1));
+                if (ok && elect_one()) mma_commit<CG>(acc_full + 8 * (u & 1));
             }
             if (!ok) {   // the MMAs issued so far end before tensor memory is freed
-                mma_commit<CG>(drained);
+                if (elect_one()) mma_commit<CG>(drained);
                 wait(drained, 0);
             }
         }
