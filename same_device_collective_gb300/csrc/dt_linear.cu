@@ -108,7 +108,7 @@ struct Tile {
 
 __device__ __forceinline__ void place_tile(const LinearProduct &c, uint32_t i, Tile &t)
 {
-    const uint32_t per_split = c.mt * c.nt;
+    const uint32_t per_split = c.mt * c.nt, all = kGroup * c.mt;
     t.split = 0, t.kb0 = 0, t.kb1 = c.kblocks;
     if (c.splits > 1) {   // at most 16 splits of 2^20 blocks
         t.split = i / per_split;
@@ -116,10 +116,11 @@ __device__ __forceinline__ void place_tile(const LinearProduct &c, uint32_t i, T
         t.kb0 = c.kblocks * t.split / c.splits;
         t.kb1 = c.kblocks * (t.split + 1) / c.splits;
     }
-    const uint32_t all = kGroup * c.mt, g = i / all;
+    const uint32_t g = quotient(i, all, c.group_inverse);
     i -= g * all;
-    t.n = g * kGroup + i / c.mt;
-    t.m = i % c.mt;
+    const uint32_t n = quotient(i, c.mt, c.mt_inverse);
+    t.n = g * kGroup + n;
+    t.m = i - n * c.mt;
 }
 
 // The k-th tile of worker q (a CTA or a pair) of W; false when it has no more.
@@ -625,6 +626,8 @@ linear_kernel(const __grid_constant__ LinearParams p)
         *gave_up = 0;
         mbar_init_fence();
     }
+    Tile t;
+    const bool any = next_tile<KIND>(p, worker, workers, 0, t);
     if (warp == FW + 1) tmem_alloc<CG>(smem_addr(const_cast<uint32_t *>(tmem_slot)), kTmemColumns);
     tc_fence_before();
     __syncwarp();
@@ -632,7 +635,6 @@ linear_kernel(const __grid_constant__ LinearParams p)
     else __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
-    Tile t;
     pdl_begin();
     DT_TL_WAITED();
     const Waits wait{p.sink, gave_up};
@@ -640,8 +642,8 @@ linear_kernel(const __grid_constant__ LinearParams p)
 
     if (warp == FW) {
         uint32_t n = 0, s = 0, round = 0;   // loads issued; the next one's stage and its parity
-        bool ok = true;
-        for (uint32_t k = 0; ok && next_tile<KIND>(p, worker, workers, k, t); ++k) {
+        bool ok = any;
+        for (uint32_t k = 1; ok; ok = ok && next_tile<KIND>(p, worker, workers, k++, t)) {
             if (kBack && t.second)
                 ok = load_tile<Second, CG>(p, p.product[1], t, half, ring, stage_bytes, a_box, full, empty, wait, s, round, n);
             else
@@ -660,7 +662,8 @@ linear_kernel(const __grid_constant__ LinearParams p)
         if (half == 0) {
             uint32_t s = 0, round = 0;
             bool ok = true;
-            for (uint32_t u = 0; ok && next_tile<KIND>(p, worker, workers, u, t); ++u) {
+            bool more = any;
+            for (uint32_t u = 0; ok && more; more = next_tile<KIND>(p, worker, workers, ++u, t)) {
                 const uint32_t acc = tmem + (u & 1) * 256;
                 if (!(ok = __all_sync(0xFFFFFFFFu, wait(acc_empty + 8 * (u & 1), ((u >> 1) & 1) ^ 1)))) break;
                 tc_fence_after();
@@ -685,7 +688,8 @@ linear_kernel(const __grid_constant__ LinearParams p)
         // lanes of its number modulo 4) and take columns in turn.
         const uint32_t quad = (warp & 3) * 32;   // first of this warp's rows in the CTA's
         unsigned char *buf = out_buf + warp * kStageOut, *biases = ctl + kBarBytes + warp * kStep * 2;
-        for (uint32_t u = 0; next_tile<KIND>(p, worker, workers, u, t); ++u) {
+        bool more = any;
+        for (uint32_t u = 0; more; more = next_tile<KIND>(p, worker, workers, ++u, t)) {
             const uint32_t acc = tmem + (u & 1) * 256 + ((warp & 3) * 32 << 16);
             auto take = [&] {
                 const bool ok = wait(acc_full + 8 * (u & 1), (u >> 1) & 1);
@@ -906,6 +910,11 @@ cudaError_t launch_linear(LinearParams &p, LinearKind kind, bool pairs, int devi
     if (second && a.tiles % p.workers) {
         p.rest = a.tiles % p.workers;
         p.early = std::min((a.kblocks / a.splits + kTileCost) / (b.kblocks / b.splits + kTileCost), second / (p.workers - p.rest));
+    }
+    for (LinearProduct &c : p.product) {
+        const uint64_t g = (uint64_t)kGroup * c.mt;
+        c.group_inverse = g ? (uint32_t)((1ull << 32) / g + 1) : 0;
+        c.mt_inverse = c.mt > 1 ? (uint32_t)((1ull << 32) / c.mt + 1) : 0;
     }
     switch (kind) {
     case kGather: return launch_kind<kGather>(p, pairs, device, s);

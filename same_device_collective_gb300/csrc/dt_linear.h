@@ -41,6 +41,7 @@ __host__ __device__ constexpr uint32_t linear_depth(bool back) { return back ? 1
 struct LinearProduct {
     uint32_t mt, nt, splits, tiles;    // tiles = mt * nt * splits
     uint32_t kblocks;                  // blocks of the inner axis
+    uint32_t group_inverse, mt_inverse;   // for divisions by a group of tiles and by mt
     uint32_t f_end[DT_MAX_RANKS];      // the ranks' features and tokens in halves of 128 rows of a tile, its columns or
     uint32_t t_end[DT_MAX_RANKS];      // blocks, as their axis is cut here, numbered through: rank r's end at [r]
     uint16_t *out[DT_MAX_RANKS];
