@@ -57,12 +57,20 @@ struct Cut {
     uint64_t acc_bytes(const Plan &v, int k) const { return splits[k] > 1 ? splits[k] * mt[k] * v.halves * 128 * nt[k] * bn * 4 : 0; }
 };
 
-// What a launch takes, in microseconds, as far as its cut decides it: 16 of the inner
-// axis take the tensor cores 128 cycles whatever a tile's width (measured from 64 to 256
-// columns: reading 128 rows of A bounds it), a tile costs half a microsecond beside that
+// What a launch takes, in microseconds, as far as its cut decides it: a stage takes the
+// tensor cores as long as it has columns, and at least what its loads and products take to
+// issue (forward, 64 deep, 512 tokens of 4096 to 4096 with 256, 192, 128 columns: 0.28, 0.22,
+// 0.21; backward, 128 deep, 1024 tokens of 4096 to 4096 with 256, 128, 64: 0.67, 0.38, 0.32),
+// and one CTA's loads longer than a pair's; a tile costs half a microsecond beside that
 // and the last one's finish half of one for each 64 columns, and splits cost a second
 // launch and their sums' way to L2 and back.
-constexpr double kUsPer64 = 0.34, kUsTile = 0.5, kUsFinish64 = 0.45, kUsJoin = 2.5, kJoinBytesPerUs = 8e6;
+constexpr double kUsTile = 0.5, kUsFinish64 = 0.45, kUsJoin = 2.5, kJoinBytesPerUs = 8e6;
+
+double stage_us(bool back, bool pairs, uint32_t bn)
+{
+    if (back) return pairs ? 0.2 + 0.47 * bn / 256 : 0.68;
+    return pairs ? std::max(0.2, 0.28 * bn / 256) : 0.19 + 0.15 * bn / 256;
+}
 
 double join_cost(const Plan &v, const Cut &c)
 {
@@ -77,7 +85,6 @@ bool cut(const dt_group *g, const Plan &v, bool pieces, Cut &best)
     const bool b = back(v.kind);
     const uint64_t workers = dt::linear_workers(v.pairs, g->device), depth = dt::linear_depth(b);
     const bool n_features = v.kind == dt::kGather || v.kind == dt::kReduceBack;
-    const double block_us = kUsPer64 * depth / 64;
     Cut c;
     // the rows' axis of forward products is the tokens, which reducing are never in pieces
     c.mt[0] = tiles_of(token_tiles(v, pieces && n_features, 128), v.halves);
@@ -90,6 +97,7 @@ bool cut(const dt_group *g, const Plan &v, bool pieces, Cut &best)
     double least = 1e300;
     for (uint32_t bn = b && !v.pairs ? 128 : 256; bn >= 64; bn -= b ? 64 : 32) {
         c.bn = bn;
+        const double block_us = stage_us(b, v.pairs, bn);
         c.nt[0] = n_features ? feature_tiles(v, bn) : tiles_of(v.dim, bn);
         if (b) c.nt[1] = c.nt[0];
         for (int k = 0; k < 2; ++k)
@@ -405,7 +413,7 @@ bool run_small(Call &c, const void *const *tok, const void *const *feat, const v
     small_cut(c.g, v, sums, vec, z != nullptr, t);
     Cut big;
     cut(c.g, v, false, big);
-    if (t.us >= big.us + 4.0 + prep_us(c, tok, feat, w, written)) return false;
+    if (t.us >= big.us + 3.0 + prep_us(c, tok, feat, w, written)) return false;
     dt::LinearSmall p;
     memset(&p, 0, sizeof p);
     static_cast<dt::LinearCall &>(p) = c.p;
