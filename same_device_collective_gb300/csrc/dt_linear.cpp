@@ -57,13 +57,13 @@ struct Cut {
     uint64_t acc_bytes(const Plan &v, int k) const { return splits[k] > 1 ? splits[k] * mt[k] * v.halves * 128 * nt[k] * bn * 4 : 0; }
 };
 
-// What a launch takes, in microseconds, as far as its cut decides it: a stage takes the
+// What a launch takes, in microseconds, as far as its cut decides it.  A stage takes the
 // tensor cores as long as it has columns, and at least what its loads and products take to
-// issue (forward, 64 deep, 512 tokens of 4096 to 4096 with 256, 192, 128 columns: 0.28, 0.22,
-// 0.21; backward, 128 deep, 1024 tokens of 4096 to 4096 with 256, 128, 64: 0.67, 0.38, 0.32),
-// and one CTA's loads longer than a pair's; a tile costs half a microsecond beside that
-// and the last one's finish half of one for each 64 columns, and splits cost a second
-// launch and their sums' way to L2 and back.
+// issue: forward, 64 deep, 0.28, 0.22, 0.21 with 256, 192, 128 columns (512 tokens of 4096 to
+// 4096); backward, 128 deep, 0.67, 0.38, 0.32 with 256, 128, 64 (1024 tokens of it), where 64
+// never paid (81 us, 49 with 128).  One CTA's loads take longer than a pair's.  A tile costs
+// half a microsecond beside that and the last one's finish half of one for each 64 columns,
+// and splits cost a second launch and their sums' way to L2 and back.
 constexpr double kUsTile = 0.5, kUsFinish64 = 0.45, kUsJoin = 2.5, kJoinBytesPerUs = 8e6;
 
 double stage_us(bool back, bool pairs, uint32_t bn)
@@ -95,7 +95,7 @@ bool cut(const dt_group *g, const Plan &v, bool pieces, Cut &best)
         c.kblocks[1] = token_tiles(v, pieces, depth);
     }
     double least = 1e300;
-    for (uint32_t bn = b && !v.pairs ? 128 : 256; bn >= 64; bn -= b ? 64 : 32) {
+    for (uint32_t bn = b && !v.pairs ? 128 : 256; bn >= (b ? 128u : 64u); bn -= b ? 64 : 32) {
         c.bn = bn;
         const double block_us = stage_us(b, v.pairs, bn);
         c.nt[0] = n_features ? feature_tiles(v, bn) : tiles_of(v.dim, bn);
