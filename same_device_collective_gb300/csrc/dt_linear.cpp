@@ -59,8 +59,8 @@ struct Cut {
 
 // What a launch takes, in microseconds, as far as its cut decides it.  A stage takes the
 // tensor cores as long as it has columns, and at least what its loads and products take to
-// issue: forward, 64 deep, 0.28, 0.22, 0.21 with 256, 192, 128 columns (512 tokens of 4096 to
-// 4096); backward, 128 deep, 0.67, 0.38, 0.32 with 256, 128, 64 (1024 tokens of it), where 64
+// issue: forward, for 64 of the inner axis, 0.28, 0.22, 0.15 with 256, 192, 128 columns (512
+// tokens of 4096 to 4096); backward, 128 deep, 0.67, 0.38, 0.32 with 256, 128, 64 (1024 tokens of it), where 64
 // never paid (81 us, 49 with 128).  One CTA's loads take longer than a pair's.  A tile costs
 // half a microsecond beside that and the last one's finish half of one for each 64 columns,
 // and splits cost a second launch and their sums' way to L2 and back.
@@ -69,7 +69,8 @@ constexpr double kUsTile = 0.5, kUsFinish64 = 0.45, kUsJoin = 2.5, kJoinBytesPer
 double stage_us(bool back, bool pairs, uint32_t bn)
 {
     if (back) return pairs ? 0.2 + 0.47 * bn / 256 : 0.68;
-    return pairs ? std::max(0.2, 0.28 * bn / 256) : 0.19 + 0.15 * bn / 256;
+    const double least = bn <= 128 ? 0.11 : 0.19;   // two blocks to a stage, or one
+    return pairs ? std::max(least + 0.04, 0.28 * bn / 256) : least + 0.15 * bn / 256;
 }
 
 double join_cost(const Plan &v, const Cut &c)

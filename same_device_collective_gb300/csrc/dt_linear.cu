@@ -47,6 +47,9 @@ namespace {
 constexpr uint32_t kM = 128;                       // rows of a tile in a CTA
 // Three stages of 128 rows and columns of A and B, or six of 64 columns (2048 tokens of
 // 4096 to 16384 with four, five, six of them: 171, 157, 150 us).
+// Forward tiles of up to 128 columns, whose products take less time than a stage takes to
+// issue, have two such blocks to a stage (512 tokens of 4096 to 4096: 17.7 -> 14.7 us; wider
+// tiles no faster, 512 of 4096 to 16384: 42.4 -> 45.3).
 constexpr uint32_t kRingBytes = 192 * 1024;
 constexpr uint32_t kMaxStages = 16;
 constexpr uint32_t kTmemColumns = 512;             // two accumulators of 128 x 256 fp32
@@ -191,14 +194,14 @@ __host__ __device__ constexpr uint32_t stage_size(bool back, uint32_t rows_t, ui
     return a_boxes(back) * a_box_bytes(back, rows_t) + (back ? b_boxes(back, bn) * kBoxBytes : bn * 128);
 }
 
-// A tile's loads.  A stage is the boxes of A, 64 columns apart, and those of B; what it
+// A tile's loads.  A block of a stage is the boxes of A, 64 columns apart, and those of B; what it
 // holds beside them is left over from earlier loads and reaches only rows of the
 // accumulator that are not stored.  Maps and coordinates are worked out once for a
 // piece of the inner axis: done for every stage they took the issuing thread longer
 // (680 cycles) than the products take (2048 tokens of 4096 to 16384: 168 -> 162 us).
 template <class R, int CG, class Wait>
 __device__ __forceinline__ bool load_tile(const LinearParams &p, const LinearProduct &c, const Tile &t, uint32_t half,
-                                          uint32_t ring, uint32_t stage_bytes, uint32_t a_box, uint32_t full,
+                                          uint32_t ring, uint32_t block_bytes, uint32_t a_box, uint32_t full,
                                           uint32_t empty, const Wait &wait, uint32_t &s, uint32_t &round, uint32_t &n)
 {
     constexpr bool kBack = R::b_mn;
@@ -207,24 +210,30 @@ __device__ __forceinline__ bool load_tile(const LinearParams &p, const LinearPro
     at[R::n] = locate<R, R::n>(p, c, t.n, p.bn);
     const uint32_t bn = p.bn / CG, boxes = b_boxes(kBack, bn), b_rows = kBack ? (R::b == kW ? R::depth : p.rows_t) : bn;
     const uint32_t bytes = CG * (a_boxes(kBack) * p.rows_t + boxes * b_rows) * 128, stages = p.stages;
+    const uint32_t step = kBack ? 1 : p.step;
     Inner<R> k(p, c, t.kb0, t.kb1);
     do {
         at[R::k] = k.at;
         uint32_t a_col, a_row, b_col, b_row;
         const CUtensorMap *a_map = operand<R, R::a>(p, at, a_col, a_row), *b_map = operand<R, R::b>(p, at, b_col, b_row);
         (R::b_mn ? b_col : b_row) += half * bn;
-        for (uint32_t i = 0; i < k.blocks; ++i, ++n) {
+        for (uint32_t i = 0; i < k.blocks; i += step, ++n) {
             if (!__all_sync(0xFFFFFFFFu, wait(empty + 8 * s, round ^ 1))) return false;
-            const uint32_t bar = full + 8 * s, a = ring + s * stage_bytes, b = a + a_boxes(kBack) * a_box;
+            const uint32_t bar = full + 8 * s, a = ring + s * step * block_bytes, b = a + a_boxes(kBack) * a_box;
+            const bool two = step == 2 && i + 1 < k.blocks;
             if (elect_one()) {
-                if (half == 0) mbar_expect_tx(bar, bytes);
+                if (half == 0) mbar_expect_tx(bar, two ? 2 * bytes : bytes);
                 tma_box<CG>(a, a_map, a_col, a_row, bar);
                 if (a_boxes(kBack) == 2) tma_box<CG>(a + a_box, a_map, a_col + 64, a_row, bar);
                 tma_box<CG>(b, b_map, b_col, b_row, bar);
                 if (boxes == 2) tma_box<CG>(b + kBoxBytes, b_map, b_col + 64, b_row, bar);
+                if (two) {   // (forward: K-major)
+                    tma_box<CG>(a + block_bytes, a_map, a_col + R::depth, a_row, bar);
+                    tma_box<CG>(b + block_bytes, b_map, b_col + R::depth, b_row, bar);
+                }
             }
-            (R::a_mn ? a_row : a_col) += R::depth;
-            (R::b_mn ? b_row : b_col) += R::depth;
+            (R::a_mn ? a_row : a_col) += step * R::depth;
+            (R::b_mn ? b_row : b_col) += step * R::depth;
             if (++s == stages) s = 0, round ^= 1;
         }
     } while (k.next(p));
@@ -251,22 +260,28 @@ __device__ __forceinline__ void multiply_stage(uint32_t acc, uint64_t a, uint64_
 // A tile's products.
 template <class R, int CG, class Wait>
 __device__ __forceinline__ bool multiply_tile(const LinearParams &p, const LinearProduct &c, const Tile &t, uint32_t acc,
-                                              uint32_t ring, uint32_t stage_bytes, uint32_t a_box, uint32_t full,
+                                              uint32_t ring, uint32_t block_bytes, uint32_t a_box, uint32_t full,
                                               uint32_t empty, const Wait &wait, uint32_t &s, uint32_t &round)
 {
-    const uint32_t desc = mma_desc(kM * CG, p.bn, R::a_mn, R::b_mn), stages = p.stages;
+    const uint32_t desc = mma_desc(kM * CG, p.bn, R::a_mn, R::b_mn), stages = p.stages, step = R::b_mn ? 1 : p.step;
     const uint64_t a0 = smem_desc(ring, R::a_mn), b0 = smem_desc(ring + a_boxes(R::b_mn) * a_box, R::b_mn);
     Inner<R> k(p, c, t.kb0, t.kb1);
     bool add = false;
     do {
-        for (uint32_t i = 0; i < k.blocks; ++i) {
+        for (uint32_t i = 0; i < k.blocks; i += step) {
             if (!__all_sync(0xFFFFFFFFu, wait(full + 8 * s, round))) return false;
             tc_fence_after();
-            const uint32_t at = s * (stage_bytes >> 4);
-            const bool whole = k.last == R::depth / 16 || !k.ends || i + 1 < k.blocks;
+            const uint32_t block = block_bytes >> 4, at = s * step * block;
+            const uint32_t last = k.ends ? k.last : R::depth / 16;   // K steps of the piece's last block here
+            const bool two = step == 2 && i + 1 < k.blocks;
             if (elect_one()) {
-                if (whole) multiply_stage<R, CG>(acc, a0 + at, b0 + at, desc, add, R::depth / 16, a_box);
-                else multiply_stage<R, CG>(acc, a0 + at, b0 + at, desc, add, k.last, a_box);
+                if (i + 1 < k.blocks || last == R::depth / 16)
+                    multiply_stage<R, CG>(acc, a0 + at, b0 + at, desc, add, R::depth / 16, a_box);
+                else
+                    multiply_stage<R, CG>(acc, a0 + at, b0 + at, desc, add, last, a_box);
+                if (two)
+                    multiply_stage<R, CG>(acc, a0 + at + block, b0 + at + block, desc, true,
+                                          i + 2 < k.blocks ? R::depth / 16 : last, a_box);
                 mma_commit<CG>(empty + 8 * s);
             }
             add = true;
@@ -638,16 +653,16 @@ linear_kernel(const __grid_constant__ LinearParams p)
     pdl_begin();
     DT_TL_WAITED();
     const Waits wait{p.sink, gave_up};
-    const uint32_t a_box = a_box_bytes(kBack, p.rows_t), stage_bytes = stage_size(kBack, p.rows_t, p.bn / CG);
+    const uint32_t a_box = a_box_bytes(kBack, p.rows_t), block_bytes = stage_size(kBack, p.rows_t, p.bn / CG);
 
     if (warp == FW) {
         uint32_t n = 0, s = 0, round = 0;   // loads issued; the next one's stage and its parity
         bool ok = any;
         for (uint32_t k = 1; ok; ok = ok && next_tile<KIND>(p, worker, workers, k++, t)) {
             if (kBack && t.second)
-                ok = load_tile<Second, CG>(p, p.product[1], t, half, ring, stage_bytes, a_box, full, empty, wait, s, round, n);
+                ok = load_tile<Second, CG>(p, p.product[1], t, half, ring, block_bytes, a_box, full, empty, wait, s, round, n);
             else
-                ok = load_tile<First, CG>(p, p.product[0], t, half, ring, stage_bytes, a_box, full, empty, wait, s, round, n);
+                ok = load_tile<First, CG>(p, p.product[0], t, half, ring, block_bytes, a_box, full, empty, wait, s, round, n);
         }
         // leave nothing in flight: the stages are consumed or, where that
         // was given up, at least loaded (a pair's loads complete on its
@@ -668,10 +683,10 @@ linear_kernel(const __grid_constant__ LinearParams p)
                 if (!(ok = __all_sync(0xFFFFFFFFu, wait(acc_empty + 8 * (u & 1), ((u >> 1) & 1) ^ 1)))) break;
                 tc_fence_after();
                 if (kBack && t.second)
-                    ok = multiply_tile<Second, CG>(p, p.product[1], t, acc, ring, stage_bytes, a_box, full, empty, wait, s,
+                    ok = multiply_tile<Second, CG>(p, p.product[1], t, acc, ring, block_bytes, a_box, full, empty, wait, s,
                                                    round);
                 else
-                    ok = multiply_tile<First, CG>(p, p.product[0], t, acc, ring, stage_bytes, a_box, full, empty, wait, s,
+                    ok = multiply_tile<First, CG>(p, p.product[0], t, acc, ring, block_bytes, a_box, full, empty, wait, s,
                                                   round);
                 if (ok && elect_one()) mma_commit<CG>(acc_full + 8 * (u & 1));
             }
@@ -868,7 +883,8 @@ cudaError_t launch_kind(LinearParams &p, int device, cudaStream_t s)
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit, std::memory_order_release);
     }
-    p.stages = std::min(kMaxStages, kRingBytes / stage_size(is_back(KIND), p.rows_t, p.bn / CG));
+    p.step = !is_back(KIND) && p.bn <= 128 ? 2 : 1;
+    p.stages = std::min(kMaxStages, kRingBytes / (p.step * stage_size(is_back(KIND), p.rows_t, p.bn / CG)));
     return launch_kernel(linear_kernel<KIND, CG, FW>, dim3(p.workers * CG), dim3(tc_threads(is_back(KIND), FW)), kTcSmem, s,
                          false, p);
 }

@@ -88,6 +88,7 @@ struct LinearParams : LinearCall {
     CUtensorMap w[DT_MAX_RANKS];       // [f_len, dim], or reducing [dim, f_len]
     uint32_t bn;                       // tile width, a multiple of 32: up to 256
     uint32_t stages, workers;
+    uint32_t step;                     // forward: blocks of the inner axis to a stage, 1 or 2
     uint32_t rows_t, rows_w;           // of the maps' boxes
     uint32_t rest, early;              // the order of both products' tiles (next_tile)
 };
