@@ -155,7 +155,11 @@ bool plan(const dt_group *g, LinearKind kind, const size_t *rows, size_t rows_eq
     }
     if (v.tokens > kMaxTokens || v.features > kMaxWidth || v.features == 0) return false;
     if (gathers(kind)) v.chunks = tiles_of(v.tokens, v.chunk_rows);
-    v.pairs = v.tokens > 128;
+    // Two CTAs to a tile share its operands, and wait for one another at its start and end:
+    // forward products of a wave or less and short inner axes go without (512 tokens of 1024 to
+    // 4096: 8.2 us, without 7.8; 300 of 512 to 2048: 5.8 and 5.1; 512 of 4096 to 4096: 14.7 and 16.4)
+    const uint64_t inner = gathers(kind) ? dim : v.features, outer = gathers(kind) ? v.features : dim;
+    v.pairs = v.tokens > 128 && (back(kind) || inner > 1024 || v.tokens * outer > (1ull << 21));
     v.halves = v.pairs ? 2 : 1;
     uint64_t at = 0;
     auto take = [&at](uint64_t n) {
@@ -521,7 +525,7 @@ cudaError_t matrices(Call &c, const void *const *feat, int feat_buffer, bool wri
     p.bn = t.bn;
     // few tokens: boxes of as many as there are, in whole K steps of 16 where the
     // tokens are the inner axis
-    p.rows_t = v.pairs ? 128 : (uint32_t)up(v.tokens, b ? 16 : 8);
+    p.rows_t = v.pairs ? 128 : (uint32_t)std::min<uint64_t>(128, up(v.tokens, b ? 16 : 8));
     p.rows_w = b ? 128 : t.bn / (v.pairs ? 2 : 1);
     cudaError_t e = cudaSuccess;
     if (v.kind != dt::kReduce)

@@ -485,6 +485,8 @@ LARGE = [
     ([20000], 64, [64]),
     ([512], 6000, [100, 100]),
     ([160, 96], 64, [9000, 7000]),
+    ([500, 12], 2000, [600, 400]),
+    ([300, 0, 33], 1000, [1400, 700, 8]),
 ]
 
 
