@@ -471,7 +471,8 @@ dt_status dt_gather_linear(dt_group_t g, const void *const *x, const void *const
                            size_t workspace_bytes, void *stream);
 
 /* Its gradient.  With G_r = dy[r] act'(pre[r]) (dy[r] itself for DT_ACT_NONE, where pre
- * may be NULL), rounded to dtype as the products' operand:
+ * may be NULL), rounded to dtype as the products' operand (small products, a few
+ * tokens of narrow layers among them, take what the rounding leaves as an operand too):
  *   dx[r]       rank r's rows of sum_q G_q weight[q], reduced over the ranks
  *   dweight[r]  G_r^T X
  *   dbias       NULL, or dbias[r]: the sum of G_r over the tokens, before its rounding

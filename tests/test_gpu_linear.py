@@ -525,6 +525,22 @@ def test_residual_in_place_of_every_size(dt, rows, dim, features):
         assert all(torch.equal(got, w) for got, w in zip(a.res, want))
 
 
+@pytest.mark.parametrize("act", ["relu", "gelu", "silu"])
+@pytest.mark.parametrize("rows,dim,features", [([1, 0], 424, [192, 100]), ([3, 2], 70, [33, 500]), ([60, 40], 200, [96, 24])])
+def test_small_gradients_are_as_near_as_their_rounding(dt, act, rows, dim, features):
+    """The gradient before the activation enters small products as its rounding and what that left: off by
+    2^-17 of itself, and by what the derivative is off, 2^-16."""
+    a = Layer(dt, "gather_linear", rows, dim, features, seed=17)
+    with group(2) as g:
+        dx, dw, _ = a.backward(g, act)
+    G = torch.cat([d.double() * slope64(v.double(), act) for d, v in zip(a.dy, a.pre)], 1)
+    M = torch.cat([d.double().abs() * 1.2 for d in a.dy], 1)   # a derivative is 1.13 at most
+    X, W = torch.cat(a.x).double(), torch.cat(a.w).double()
+    near = lambda k: 2.0 ** -16 + 2.0 ** -17 + sum_error(2 * k, 2)
+    check(torch.cat(dx), G @ W, near(sum(features)) * (M @ W.abs()), "dx")
+    check(torch.cat(dw), G.t() @ X, near(sum(rows)) * (M.t() @ X.abs()), "dw")
+
+
 @pytest.mark.parametrize("which", WHICH)
 def test_two_calls_at_once(dt, which):
     """Calls on two streams, each with its own workspace and outputs, as a group's calls may run."""
