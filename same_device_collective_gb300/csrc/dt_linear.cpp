@@ -418,7 +418,11 @@ bool run_small(Call &c, const void *const *tok, const void *const *feat, const v
     small_cut(c.g, v, sums, vec, z != nullptr, t);
     Cut big;
     cut(c.g, v, false, big);
-    if (t.us >= big.us + 3.0 + prep_us(c, tok, feat, w, written)) return false;
+    // a weight's gradient of few products: the large kernels' rounding of what stands before the
+    // activation, which does not average out there, is worth up to as much time again
+    bool near = false;
+    for (int r = 0; r < c.g->P && written; ++r) near = near || (v.f[r] && v.f[r] * v.tokens < 2048);
+    if (t.us >= (near ? 2.0 : 1.0) * (big.us + 3.0 + prep_us(c, tok, feat, w, written))) return false;
     dt::LinearSmall p;
     memset(&p, 0, sizeof p);
     static_cast<dt::LinearCall &>(p) = c.p;
