@@ -53,9 +53,10 @@ constexpr uint32_t kM = 128;                       // rows of a tile in a CTA
 constexpr uint32_t kRingBytes = 192 * 1024;
 constexpr uint32_t kMaxStages = 16;
 constexpr uint32_t kTmemColumns = 512;             // two accumulators of 128 x 256 fp32
-// Finishing warps, FW: eight, or of gathering layers with a short inner axis, whose finish
-// with its activation takes longer than the products, 16 (512 tokens of 1024 to 4 x 1024
-// with silu: 15.8 us, 14.1 with 16; 2048 of 4096 to 16384: 146 us, 149 with 16).  Then
+// Finishing warps, FW: eight, or 16 of gathering layers with a short inner axis and an
+// activation, whose finish takes longer than the products, where each worker has several tiles
+// (8192 tokens of 512 to 8192, gelu and what it is taken of: 106 us with eight, 100 with 16;
+// without an activation 54 and 55; 1024 tokens of 1024 to 1024 with gelu 6.8 and 7.6).  Then
 // one for TMA, one for the products, and backward two for the bias' gradient.
 constexpr uint32_t kShortBlocks = 16;              // of 64: blocks of a short inner axis, at most
 constexpr uint32_t kMostFinishWarps = 16, kSumWarps = 2;
@@ -893,7 +894,7 @@ template <int KIND>
 cudaError_t launch_kind(LinearParams &p, bool pairs, int device, cudaStream_t s)
 {
     if constexpr (KIND == kGather)
-        if (p.product[0].kblocks <= kShortBlocks)
+        if (p.product[0].kblocks <= kShortBlocks && p.act != DT_ACT_NONE && p.product[0].tiles > 2 * p.workers)
             return pairs ? launch_kind<KIND, 2, 16>(p, device, s) : launch_kind<KIND, 1, 16>(p, device, s);
     return pairs ? launch_kind<KIND, 2, 8>(p, device, s) : launch_kind<KIND, 1, 8>(p, device, s);
 }
