@@ -444,8 +444,8 @@ size_t dt_vocab_loss_workspace(dt_group_t g, const size_t *vocab, size_t vocab_e
  * every tensor: DT_BF16, products in the tensor cores and fp32 sums; DT_F32 is
  * DT_ERR_UNSUPPORTED.  Tensors are dense and 2-byte aligned.  Few tokens and small
  * products read them in place; of larger ones those whose rows start on 16-byte
- * boundaries are, others are laid out again in the workspace first, as are tokens whose
- * ranks' pieces would leave more than a twentieth of the tiles of 128 rows to their ends.
+ * boundaries are, others are laid out again in the workspace first, as are tokens where the
+ * tiles of 128 rows that the ranks' pieces end inside would cost more than that.
  * workspace: the query's bytes of device memory, 256-byte aligned, free for other use
  * once `stream` has passed the call.  No output may overlap another buffer, but for
  * the residual below.  n is at most 2^26, dim and the sum of features 2^22.  The

@@ -208,6 +208,7 @@ struct Call {
     dt::LinearParams p;
     dt::LinearPrep prep;
     uint32_t pieces;                   // the tokens' matrix in the ranks' pieces (> 1), or as one
+    bool in_pieces, again;             // which of these, and whether it is laid out again first
     const void *tok[DT_MAX_RANKS];     // its pieces as TMA reads them
     uint64_t tok_pitch;
 };
@@ -294,43 +295,60 @@ dt_status begin(Call &c, LinearKind kind, const size_t *rows, size_t rows_equal,
     return DT_OK;
 }
 
+// What laying `bytes` out again takes before the products, in microseconds, in and out.
+double again_us(double bytes) { return 3.0 + 2.0 * bytes / 4e6; }
+
 // How the tokens' matrix is read: as one where the ranks' rows follow one another in
-// memory, in the ranks' pieces where the tiles at their ends waste little, else laid
-// out again as one.  sums: column sums of its rows are wanted.
-void token_matrix(Call &c, const void *const *x, int buffer, float *sums)
+// memory, in the ranks' pieces where that takes no longer than laying them out again as one
+// (77 tokens of 512 to 512 over 3 ranks: 5.7 us, in pieces 4.5).
+void plan_tokens(Call &c, const void *const *x)
 {
     const Plan &v = c.v;
     bool reads = true, follow = true, steps = true;
     const unsigned char *next = nullptr;
-    uint64_t tiles = 0, before = 0;
-    uint32_t pieces = 0;
+    uint64_t before = 0;
     for (int r = 0; r < c.g->P; ++r) {
         if (v.n[r] == 0) continue;
         reads = reads && addressable(x[r], v.dim);
         follow = follow && (!next || next == x[r]);
         next = static_cast<const unsigned char *>(x[r]) + v.n[r] * v.dim * 2;
-        tiles += tiles_of(v.n[r], 128);
         // as the inner axis, each piece but the last has to be whole steps of 16: a step's
         // other tokens would be the next rank's in the operand that is not in pieces
         // (times zero, but an infinity times zero is not zero)
         steps = steps && before % 16 == 0;
         before = v.n[r];
-        c.tok[pieces] = x[r];
-        c.p.t_len[pieces++] = (uint32_t)v.n[r];
     }
-    const bool in_pieces = reads && !follow && (!back(v.kind) || steps) && tiles * 20 <= tiles_of(v.tokens, 128) * 21;
-    const bool again = !in_pieces && !(reads && follow);
-    c.tok_pitch = again ? up(v.dim, 8) : v.dim;
+    c.in_pieces = false;
+    c.again = !(reads && follow);
+    if (reads && !follow && (!back(v.kind) || steps)) {
+        Cut one, pieces;
+        cut(c.g, v, false, one);
+        cut(c.g, v, true, pieces);
+        c.in_pieces = pieces.us <= one.us + again_us(2.0 * v.tokens * v.dim);
+        c.again = !c.in_pieces;
+    }
+}
+
+// Its pieces, and what lays it out again.  sums: column sums of its rows are wanted.
+void token_matrix(Call &c, const void *const *x, int buffer, float *sums)
+{
+    const Plan &v = c.v;
+    uint32_t pieces = 0;
+    c.tok_pitch = c.again ? up(v.dim, 8) : v.dim;
     uint64_t first = 0, chunk = 0;
     unsigned char *to = c.ws + v.tok;
-    for (int r = 0; r < c.g->P && (again || sums); ++r) {
-        add_job(c, x[r], nullptr, again ? to + first * c.tok_pitch * 2 : nullptr, sums ? sums + chunk * v.dim : nullptr, v.n[r],
-                v.dim, c.tok_pitch, buffer + r, 0);
+    for (int r = 0; r < c.g->P; ++r) {
+        if (v.n[r] == 0) continue;
+        c.tok[pieces] = x[r];
+        c.p.t_len[pieces++] = (uint32_t)v.n[r];
+        if (c.again || sums)
+            add_job(c, x[r], nullptr, c.again ? to + first * c.tok_pitch * 2 : nullptr, sums ? sums + chunk * v.dim : nullptr,
+                    v.n[r], v.dim, c.tok_pitch, buffer + r, 0);
         chunk += tiles_of(v.n[r], v.chunk_rows);
         first += v.n[r];
     }
-    if (again) c.tok[0] = to;
-    if (!in_pieces) {
+    if (c.again) c.tok[0] = to;
+    if (!c.in_pieces) {
         pieces = 1;
         c.p.t_len[0] = c.p.tokens;
     }
@@ -381,24 +399,19 @@ void small_cut(const dt_group *g, const Plan &v, bool sums, bool vec, bool slope
 
 // What goes before the tensor core kernels' products, in microseconds: matrices that are
 // laid out again, or (`written`) the ranks' features, which a job makes.
-double prep_us(const Call &c, const void *const *tok, const void *const *feat, const void *const *w, bool written)
+double prep_us(const Call &c, bool tok_again, const void *const *feat, const void *const *w, bool written)
 {
     const Plan &v = c.v;
     double bytes = 0.0;
-    bool tok_again = false, feat_again = written, w_again = false;
-    const unsigned char *next = nullptr;
+    bool feat_again = written, w_again = false;
     for (int r = 0; r < c.g->P; ++r) {
-        if (tok && v.n[r]) {
-            tok_again = tok_again || !addressable(tok[r], v.dim) || (next && next != tok[r] && v.n[r] % 128);
-            next = static_cast<const unsigned char *>(tok[r]) + v.n[r] * v.dim * 2;
-        }
         if (feat && v.f[r]) feat_again = feat_again || !addressable(feat[r], v.f[r]);
         if (v.f[r]) w_again = w_again || !addressable(w[r], gathers(v.kind) ? v.dim : v.f[r]);
     }
-    if (tok_again) bytes += 4.0 * v.tokens * v.dim;
-    if (feat_again) bytes += (written ? 6.0 : 4.0) * v.tokens * v.features;
-    if (w_again) bytes += 4.0 * v.features * v.dim;
-    return bytes > 0.0 ? 3.0 + bytes / 4e6 : 0.0;
+    if (tok_again) bytes += 2.0 * v.tokens * v.dim;
+    if (feat_again) bytes += (written ? 3.0 : 2.0) * v.tokens * v.features;
+    if (w_again) bytes += 2.0 * v.features * v.dim;
+    return bytes > 0.0 ? again_us(bytes) : 0.0;
 }
 
 // Small products where they are likely to take less time than the tensor core kernels':
@@ -417,12 +430,12 @@ bool run_small(Call &c, const void *const *tok, const void *const *feat, const v
     SmallCut t;
     small_cut(c.g, v, sums, vec, z != nullptr, t);
     Cut big;
-    cut(c.g, v, false, big);
+    cut(c.g, v, tok && c.in_pieces, big);
     // a weight's gradient of few products: the large kernels' rounding of what stands before the
     // activation, which does not average out there, is worth up to as much time again
     bool near = false;
     for (int r = 0; r < c.g->P && written; ++r) near = near || (v.f[r] && v.f[r] * v.tokens < 2048);
-    if (t.us >= (near ? 2.0 : 1.0) * (big.us + 3.0 + prep_us(c, tok, feat, w, written))) return false;
+    if (t.us >= (near ? 2.0 : 1.0) * (big.us + 3.0 + prep_us(c, tok && c.again, feat, w, written))) return false;
     dt::LinearSmall p;
     memset(&p, 0, sizeof p);
     static_cast<dt::LinearCall &>(p) = c.p;
@@ -630,6 +643,7 @@ dt_status dt_gather_linear(dt_group_t g, const void *const *x, const void *const
     if (!scope.ok) return DT_ERR_CUDA;
     if (few(c, weight)) return cuda_status(run_few(c, x, weight, static_cast<cudaStream_t>(stream)));
     cudaError_t e = cudaSuccess;
+    plan_tokens(c, x);
     if (run_small(c, x, nullptr, weight, nullptr, act, false, false, static_cast<cudaStream_t>(stream), e)) return cuda_status(e);
     token_matrix(c, x, dt::kLinearX, nullptr);
     e = matrices(c, nullptr, 0, false, weight);
@@ -688,6 +702,7 @@ dt_status dt_gather_linear_backward(dt_group_t g, const void *const *x, const vo
     c.p.product[0].align[0] = tok_align;
     cudaError_t e = cudaSuccess;
     for (int r = 0; r < g->P; ++r) c.p.sums.out[r] = dbias ? static_cast<uint16_t *>(dbias[r]) : nullptr;
+    plan_tokens(c, x);
     if (run_small(c, x, dy, weight, pre, act, dbias != nullptr, act != DT_ACT_NONE, s, e)) return cuda_status(e);
     c.prep.act = act;
     token_matrix(c, x, dt::kLinearX, nullptr);
@@ -823,6 +838,7 @@ dt_status dt_linear_reduce_backward(dt_group_t g, const void *const *x, const vo
     }
     cudaError_t e = cudaSuccess;
     c.p.sums.out[0] = static_cast<uint16_t *>(dbias);
+    plan_tokens(c, dy);
     if (run_small(c, dy, x, weight, nullptr, DT_ACT_NONE, dbias != nullptr, false, s, e)) return cuda_status(e);
     // the bias' gradient: from the ranks' dy, or from sums over chunks of the rows
     float *part = reinterpret_cast<float *>(c.ws + v.sums);
