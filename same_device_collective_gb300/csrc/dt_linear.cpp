@@ -366,9 +366,10 @@ struct SmallCut {
 
 // What they take, in microseconds: a launch, the longest CTA's round trips to memory, and
 // in all so much for each step of a tile (measured at 17 to 1000 tokens of 100 to 1024,
-// to 200 to 4096 features; rows at any element and an activation's derivative cost
-// instructions).
-constexpr double kUsSmall = 5.0, kUsSmallStep = 0.45;
+// to 200 to 4096 features; rows at any element and an activation's derivative, whose two
+// operands are two products, cost more: the gradient of 3 tokens of 164 to 4680 with gelu
+// takes 26.6 us so and 11.4 in large tiles).
+constexpr double kUsSmall = 5.0, kUsSmallStep = 0.45, kUsSmallSlope = 1.1, kUsSmallOdd = 0.35;
 
 void small_cut(const dt_group *g, const Plan &v, bool sums, bool vec, bool slope, SmallCut &c)
 {
@@ -393,8 +394,8 @@ void small_cut(const dt_group *g, const Plan &v, bool sums, bool vec, bool slope
            (b || c.mt[0] * c.nt[0] * c.ctas * 2 <= dt::linear_workers(false, g->device)))
         c.ctas *= 2;
     for (int k = 0; k < 2; ++k) longest = std::max(longest, c.shared[k] ? tiles_of(c.kblocks[k], c.ctas) : c.kblocks[k]);
-    const double step = b ? (slope ? 0.0135 : 0.009) + (vec ? 0.0 : 0.004) : vec ? 0.0045 : 0.011;
-    c.us = kUsSmall + std::max(longest * kUsSmallStep, steps * step);
+    const double step = b ? (slope ? 0.018 : 0.009) + (vec ? 0.0 : 0.004) : vec ? 0.0045 : 0.011;
+    c.us = kUsSmall + std::max(longest * ((slope ? kUsSmallSlope : kUsSmallStep) + (vec ? 0.0 : kUsSmallOdd)), steps * step);
 }
 
 // What goes before the tensor core kernels' products, in microseconds: matrices that are
