@@ -91,21 +91,31 @@ inline bool multiple(const void *p, size_t n) { return ((uintptr_t)p & (n - 1)) 
 inline uint64_t up(uint64_t n, uint64_t to) { return (n + to - 1) / to * to; }
 
 // The buffers of a call.  Outputs may overlap nothing, but for an output and
-// an input that carry the same tag (>= 0) and are the same buffer.
+// an input that carry the same tag (>= 0) and are the same buffer.  The most
+// that a call has: six lists of a buffer to a rank and three weights that the
+// residual norm's gradient reads, four such lists that the norm writes.  A call
+// with more clashes.
 struct Buffers {
-    Range in[6 * DT_MAX_RANKS + 4], out[3 * DT_MAX_RANKS + 4];
+    static constexpr int kIn = 6 * DT_MAX_RANKS + 4, kOut = 4 * DT_MAX_RANKS + 4;
+    Range in[kIn], out[kOut];
     int nin = 0, nout = 0;
+    bool full = false;
 
     void read(const void *p, size_t bytes, int tag = -1)
     {
-        if (p && bytes) in[nin++] = Range{(uintptr_t)p, (uintptr_t)p + bytes, tag, 0};
+        if (!p || !bytes) return;
+        if (nin == kIn) full = true;
+        else in[nin++] = Range{(uintptr_t)p, (uintptr_t)p + bytes, tag, 0};
     }
     void write(const void *p, size_t bytes, int tag = -1)
     {
-        if (p && bytes) out[nout++] = Range{(uintptr_t)p, (uintptr_t)p + bytes, tag, 1};
+        if (!p || !bytes) return;
+        if (nout == kOut) full = true;
+        else out[nout++] = Range{(uintptr_t)p, (uintptr_t)p + bytes, tag, 1};
     }
     bool clash() const
     {
+        if (full) return true;
         for (int o = 0; o < nout; ++o) {
             for (int k = o + 1; k < nout; ++k)
                 if (overlaps(out[o], out[k])) return true;
