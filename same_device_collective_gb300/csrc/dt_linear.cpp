@@ -284,6 +284,7 @@ dt_status begin(Call &c, LinearKind kind, const size_t *rows, size_t rows_equal,
     for (int r = 0; r < c.g->P; ++r) {
         p.f_len[r] = (uint32_t)c.v.f[r];
         p.row_end[r] = end += (uint32_t)c.v.n[r];
+        if (c.v.f[r]) p.f_pieces = r + 1;
     }
     p.P = c.g->P;
     p.tokens = (uint32_t)c.v.tokens;

@@ -37,19 +37,21 @@ struct Roles {
     static constexpr bool w_by_feature = KIND == kGather || KIND == kGatherBack;   // rows of W_r are features
 };
 
-// A place along an axis: the rank's piece, the place there, and overall (tokens).
+// A place along an axis: the rank's piece, the place there, and overall (tokens).  A pair's
+// second half may lie past the end of all: that is past the end of the last piece that has
+// something, whose tensor map fills in zeros.
 struct Place {
     uint32_t piece, at, all;
 };
 
 template <class R, int AXIS>
-__device__ __forceinline__ Place locate(const LinearCall &p, const LinearProduct &c, uint32_t i, uint32_t unit)
+__host__ __device__ __forceinline__ Place locate(const LinearCall &p, const LinearProduct &c, uint32_t i, uint32_t unit)
 {
     if constexpr (AXIS == kDim) {
         return Place{0, i * unit, 0};
     } else if constexpr (AXIS == kFeatures) {
         uint32_t r = 0, begin = 0;
-        while ((int)r + 1 < p.P && i >= c.f_end[r]) begin = c.f_end[r++];
+        while ((int)r + 1 < p.f_pieces && i >= c.f_end[r]) begin = c.f_end[r++];
         return Place{r, (i - begin) * unit, 0};
     } else if (!R::tok) {
         return Place{0, i * unit, i * unit};
@@ -62,7 +64,7 @@ __device__ __forceinline__ Place locate(const LinearCall &p, const LinearProduct
 }
 
 template <class R, int AXIS>
-__device__ __forceinline__ uint32_t length(const LinearCall &p, uint32_t piece)
+__host__ __device__ __forceinline__ uint32_t length(const LinearCall &p, uint32_t piece)
 {
     return AXIS == kDim ? p.dim : AXIS == kFeatures ? p.f_len[piece] : R::tok ? p.t_len[piece] : p.tokens;
 }

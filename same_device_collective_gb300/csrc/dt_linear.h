@@ -68,6 +68,7 @@ struct LinearCall {
     uint32_t t_len[DT_MAX_RANKS], t_first[DT_MAX_RANKS];   // pieces of the token axis in the tokens' matrix
     uint32_t row_end[DT_MAX_RANKS];    // the ranks' tokens, numbered through
     int32_t P, t_pieces;
+    int32_t f_pieces;                  // ranks up to the last that has features
     uint32_t tokens, dim;
     uint16_t *pre[DT_MAX_RANKS];
     const uint16_t *bias[DT_MAX_RANKS];

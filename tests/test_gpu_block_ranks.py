@@ -7,6 +7,7 @@ import pytest
 import torch
 
 from gpu_util import group
+from test_gpu_linear import WHICH, Layer
 from test_gpu_residual_norm import Rows
 
 pytestmark = pytest.mark.gpu
@@ -28,4 +29,19 @@ def test_residual_norm_of_many_ranks(dt, rows, cols, dtype):
         a.check_forward(a.forward(g))
         a.check_backward(a.backward(g, op="avg"), op="avg")
         a.check_forward(a.forward(g, stats=False))
+        assert dt.dt_group_check(g) == dt.DT_OK
+
+
+# last ranks without features beside an odd number of 128 features: the second half of a pair's last tile has none
+@pytest.mark.parametrize("which", WHICH)
+@pytest.mark.parametrize("offset", [0, 1])
+@pytest.mark.parametrize("rows,dim,features", [([1024, 1024], 512, [1100, 0]), ([2000, 0, 48, 0], 264, [1500, 700, 0, 0]),
+                                               ([300, 212, 1], 1030, [129, 0, 0]), ([0, 700, 0, 333], 1000, [0, 40, 0, 0]),
+                                               ([2, 1], 64, [72, 0]), ([60, 17], 200, [0, 130])], ids=str)
+def test_last_ranks_without_features(dt, which, offset, rows, dim, features):
+    a = Layer(dt, which, rows, dim, features, seed=dim + offset, offset=offset)
+    act = "gelu" if which == "gather_linear" else "none"
+    with group(a.P) as g:
+        a.check_forward(a.forward(g, act) if which == "gather_linear" else a.forward(g), act)
+        a.check_backward(a.backward(g, act), act)
         assert dt.dt_group_check(g) == dt.DT_OK
