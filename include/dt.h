@@ -533,9 +533,17 @@ size_t dt_linear_reduce_workspace(dt_group_t g, const size_t *rows, size_t rows_
  * may be x[r] and z[r] may be branch[r] (in place); otherwise no output may overlap another
  * buffer.
  * Pointers are multiples of their element size; rows that all start on 16-byte boundaries
- * move as vectors.  cols is 1..2^24, residual_scale any finite number.  A NaN or an
- * infinity in a row makes results of that row NaN, and no other's.  The same call gives
- * the same bits. */
+ * move as vectors.  cols is 1..2^24, residual_scale any finite number.  The same call gives
+ * the same bits.
+ * A NaN or an infinity goes through the formulas as it stands and reaches its own row's
+ * results only.  A NaN in branch makes all of y and z and both reciprocals NaN; one in x its
+ * element of y, all of z, and rstd_pre.  Of an infinity the reciprocal is 0 and its own norm
+ * NaN: one in branch makes rstd_post 0, its element of y NaN and the others
+ * residual_scale * x, all of z and rstd_pre NaN; one in x makes its element of y infinite
+ * and of z NaN, rstd_pre and the rest of z 0.  Squares are summed in fp32: where the sum
+ * passes it (a root mean square of 1.8e19 / sqrt(cols)) the reciprocal is 0 as well.  With
+ * an eps of 0 a row whose squares are all 0 there, below 1e-23, has an infinite one, and NaN
+ * or infinities for its norm. */
 dt_status dt_residual_norm(dt_group_t g, const void *const *x, const void *const *branch,
                            const void *post_weight, const void *gate, const void *pre_weight,
                            float residual_scale, void *const *y, void *const *z,
@@ -553,7 +561,9 @@ dt_status dt_residual_norm(dt_group_t g, const void *const *x, const void *const
  *   dgate         = post_weight * that sum
  *   dpre_weight   = the sum over every row of every rank of dz * n
  * the last three of weight_dtype, each may be NULL; op DT_SUM, or DT_AVG: divided by the
- * number of ranks.  With no rows at all they are 0.
+ * number of ranks.  With no rows at all they are 0.  A NaN or an infinity reaches its own
+ * row's results and the weights' gradients only.  Reciprocals are squared in fp32: one of
+ * 1.8e19 or more, which no eps of 1e-38 or more leaves, makes NaN or infinities.
  *   workspace     at least dt_residual_norm_workspace(g, cols) bytes of device memory,
  *                 16-byte aligned, free for other use once `stream` has passed the call;
  *                 NULL when none of the three is wanted

@@ -1,0 +1,107 @@
+"""NaN, infinities and the ends of fp32's range in the residual norm's rows: what the header says of them, for
+each of its kernels (few rows, rings of vectors and of single elements, rows too long for registers)."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from gpu_util import group
+from test_gpu_residual_norm import EPS, Rows
+
+pytestmark = pytest.mark.gpu
+INF, NAN = float("inf"), float("nan")
+# a case to a row: the input, the value
+CASES = [("x", INF), ("x", -INF), ("x", NAN), ("branch", INF), ("branch", -INF), ("branch", NAN)]
+
+
+@pytest.fixture(scope="module")
+def dt():
+    from same_device_collective_gb300 import dt as mod
+    assert torch.cuda.is_available()
+    return mod
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("cols", [8, 96, 777, 4096, 9000])
+@pytest.mark.parametrize("rows", [[5, 6], [700, 5]], ids=str)
+def test_a_value_that_is_not_finite(dt, rows, cols, dtype):
+    a = Rows(dt, rows, cols, dtype, "f32", seed=3)
+    j = cols // 3
+    with group(2) as g:
+        clean = [torch.cat(t) for t in a.forward(g)]
+        n = rows[0]
+        at = [(0, 1), (0, n - 1), (1, 0), (1, 1), (1, 3), (1, 4)]
+        for (name, v), (r, i) in zip(CASES, at):
+            getattr(a, name)[r][i, j] = v
+        y, z, r1, r2 = (torch.cat(t) for t in a.forward(g))
+        assert dt.dt_group_check(g) == dt.DT_OK
+    rest = torch.ones(sum(rows), dtype=torch.bool, device="cuda")
+    other = torch.arange(cols, device="cuda") != j
+    scaled = a.scale * torch.cat(a.x).double()
+    half = torch.finfo(y.dtype).eps / 2
+    for (name, v), (r, i) in zip(CASES, at):
+        k = i + r * n
+        rest[k] = False
+        if name == "x":
+            assert torch.equal(y[k][other], clean[0][k][other]) and r1[k] == clean[2][k]
+            if v != v:
+                assert y[k, j].isnan() and z[k].isnan().all() and r2[k].isnan()
+            else:
+                assert y[k, j] == v and z[k, j].isnan() and (z[k][other] == 0).all() and r2[k] == 0
+        elif v != v:
+            assert y[k].isnan().all() and z[k].isnan().all() and r1[k].isnan() and r2[k].isnan()
+        else:
+            # (scale x is rounded to fp32 and to the rows' type)
+            off = (y[k].double() - scaled[k]).abs()[other]
+            assert r1[k] == 0 and y[k, j].isnan() and (off <= (half + 2.0 ** -23) * scaled[k].abs()[other]).all()
+            assert z[k].isnan().all() and r2[k].isnan()
+    for got, want in zip((y, z, r1, r2), clean):
+        assert torch.equal(got[rest], want[rest])
+
+
+@pytest.mark.parametrize("cols", [8, 777, 4096, 9000])
+@pytest.mark.parametrize("rows", [3, 400])
+def test_squares_past_the_range(dt, rows, cols):
+    """Rows of 1e20, and with an eps of 0 rows of zeros and of 1e-30."""
+    a = Rows(dt, [rows], cols, "f32", "f32", seed=4)
+    with group(1) as g:
+        clean = a.forward(g)
+        a.branch[0][0], a.x[0][1] = 1e20, 1e20
+        y, z, r1, r2 = (t[0] for t in a.forward(g))
+        assert r1[0] == 0 and r2[1] == 0 and (z[1] == 0).all() and y.isfinite().all()
+        assert ((y[0].double() - a.scale * a.x[0][0].double()).abs() <= 2.0 ** -23 * a.scale * a.x[0][0].abs()).all()
+        for got, want in zip((y, z, r1, r2), clean):
+            assert torch.equal(got[2:], want[0][2:])
+        a.branch[0][0], a.branch[0][1] = 0, 1e-30
+        y, z, r1, r2 = (torch.empty_like(t) for t in (y, z, r1, r2))
+        dt.dt_residual_norm(g, a.x, a.branch, a.post, a.gate, a.pre, a.scale, [y], [z], [r1], [r2], [rows], 0, cols, 0.0,
+                            "f32", "f32")
+        assert (r1[:2] == INF).all() and y[0].isnan().all() and y[1].isinf().all()
+        # other rows, with the least eps that matters nowhere
+        o, x = a.branch[0][2:].double(), a.x[0][2:].double()
+        want = a.scale * x + a.gate.double() * a.post.double() * o / o.square().mean(1, keepdim=True).sqrt()
+        if rows > 2:
+            tol = 2.0 ** -24 * (64 + cols / 256 + 16)   # (a row's sum, and a few operations)
+            assert ((y[2:].double() - want).abs() <= tol * (want.abs() + (a.scale * x).abs() + (want - a.scale * x).abs())).all()
+
+
+@pytest.mark.parametrize("value", [INF, -INF, NAN])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("cols", [8, 777, 4096, 9000])
+def test_backward_of_a_value_that_is_not_finite(dt, cols, dtype, value):
+    """It reaches its own row's dx and dbranch only, and the weights' gradients."""
+    a = Rows(dt, [40, 9], cols, dtype, "f32", seed=5)
+    with group(2) as g:
+        clean = [torch.cat(t) for t in a.backward(g)[:2]]
+        rest = torch.ones(49, dtype=torch.bool, device="cuda")
+        for k, name in enumerate(("branch", "y", "dy", "dz")):
+            getattr(a, name)[k % 2][3 + k, cols - 1] = value
+            rest[3 + k + 40 * (k % 2)] = False
+        dx, do = (torch.cat(t) for t in a.backward(g)[:2])
+    for got, want in zip((dx, do), clean):
+        assert torch.equal(got[rest], want[rest])
+    finite = lambda t: t.isfinite()
+    assert torch.equal(dx[3], clean[0][3]) and not finite(do[3]).any()              # branch
+    assert not finite(dx[44]).any() and not finite(do[44]).any()                    # y
+    assert torch.equal(dx[5][:-1], clean[0][5][:-1]) and not finite(dx[5, -1]) and not finite(do[5]).any()   # dy
+    assert not finite(dx[46]).any() and not finite(do[46]).any()                    # dz
