@@ -414,8 +414,9 @@ dt_status dt_vocab_loss(dt_group_t g, const void *hidden, const void *const *wei
  * The logits are computed again as the loss computes them, a piece of the
  * vocabulary at a time; p - [target] is held in bf16 for that piece (at most 512
  * MiB, or 256 vocabulary rows' worth), every sum in fp32, and results are
- * rounded once.  The tensor cores add 16 products at a time and round towards
- * zero: sums of n terms are up to n * 2e-9 of themselves too small beside that.
+ * rounded once.  The tensor cores cut off what of a product lies below a quarter of
+ * the sum's last place: sums of n terms of one sign are about n * 5e-9 of themselves too
+ * small beside that, and any n * 2^-25 of their largest part sum at most.
  * Repeated calls give the same bits. */
 dt_status dt_vocab_loss_backward(dt_group_t g, const void *hidden, const void *const *weight,
                                  const size_t *vocab, size_t vocab_equal, const int32_t *targets,
@@ -449,9 +450,10 @@ size_t dt_vocab_loss_workspace(dt_group_t g, const size_t *vocab, size_t vocab_e
  * workspace: the query's bytes of device memory, 256-byte aligned, free for other use
  * once `stream` has passed the call.  No output may overlap another buffer, but for
  * the residual below.  n is at most 2^26, dim and the sum of features 2^22.  The
- * tensor cores add 16 products at a time and round towards zero: sums of n terms of
- * one sign are up to n * 2e-9 of themselves too small.  Repeated calls give the same
- * bits. */
+ * tensor cores cut off what of a product lies below a quarter of the sum's last place:
+ * a sum of n terms is off by n * 2^-25 of its largest part sum at most.  Terms of one
+ * sign and like size come out n * 5e-9 of their sum too small, terms of both signs as
+ * near as fp32's rounding.  Repeated calls give the same bits. */
 #define DT_ACT_NONE 0
 #define DT_ACT_RELU 1
 #define DT_ACT_GELU 2 /* v * Phi(v), Phi the normal distribution (no tanh form) */

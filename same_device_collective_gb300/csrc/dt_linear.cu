@@ -25,9 +25,12 @@
 // write and read, are never in memory, and the sum over the ranks is rounded once.
 // Past a piece's end TMA fills in zeros.
 //
-// Sums are fp32.  The tensor cores add 16 products at a time and round towards
-// zero: a sum of n terms of one sign comes out up to n * 2e-9 of itself too small
-// (3e-5 of 16384), where results are rounded by up to 2^-9 of themselves.
+// Sums are fp32.  The tensor cores add 16 products at a time, each aligned to the largest
+// of them and the sum so far and cut off two bits below its last place: at most 2^-25 of
+// the sum is lost to a term, n * 2^-25 to n of them (3.97 of 4 units of 2^-23 for 16 terms of
+// 1.99 * 2^-25 beside a 1).  Terms of one sign, uniform from 0 to 1, lose n * 4.4e-9 to 5.3e-9 of
+// their sum (16384, 65536 of them; 7e-5 of it at 16384), where results are rounded by up to
+// 2^-8 of themselves; normal ones nothing that shows (rms 1.4e-11 n of the sum of magnitudes).
 #include <algorithm>
 #include <atomic>
 #include <type_traits>

@@ -1,11 +1,13 @@
-"""NaN, infinities and the ends of fp32's range in the residual norm's rows: what the header says of them, for
-each of its kernels (few rows, rings of vectors and of single elements, rows too long for registers)."""
+"""What the header says of values at the ends: NaN, infinities and squares past fp32's range in the residual
+norm's rows, for each of its kernels (few rows, rings of vectors and of single elements, rows too long for
+registers), and what the tensor cores cut off of the linear layers' sums."""
 from __future__ import annotations
 
 import pytest
 import torch
 
 from gpu_util import group
+from test_gpu_linear import workspace
 from test_gpu_residual_norm import EPS, Rows
 
 pytestmark = pytest.mark.gpu
@@ -105,3 +107,30 @@ def test_backward_of_a_value_that_is_not_finite(dt, cols, dtype, value):
     assert not finite(dx[44]).any() and not finite(do[44]).any()                    # y
     assert torch.equal(dx[5][:-1], clean[0][5][:-1]) and not finite(dx[5, -1]) and not finite(do[5]).any()   # dy
     assert not finite(dx[46]).any() and not finite(do[46]).any()                    # dz
+
+
+@pytest.mark.parametrize("terms", ["uniform", "small"])
+@pytest.mark.parametrize("n,features,dim", [(2048, 4096, 16384), (300, 200, 65536), (64, 64, 2048), (4, 4096, 16384)])
+def test_sums_of_one_sign(dt, n, features, dim, terms):
+    """Sums that a bias takes off again, so that the result shows their error: terms of one size, and terms
+    of one to two quarters of the last place of the 1 that they follow.  A term loses 2^-25 of the
+    largest part sum at most, here the sum; a sum's splits, the bias and the conversions take 64 roundings
+    of 2^-23 of it, and the result is rounded to bf16."""
+    gen = torch.Generator("cuda").manual_seed(dim)
+    x, w = (torch.rand(k, dim, generator=gen, device="cuda") for k in (n, features))
+    if terms == "small":
+        x, w = torch.ones_like(x), (1 + w) * 2.0 ** -25
+        w[:, 0] = 1
+    x, w = x.bfloat16(), w.bfloat16()
+    exact = x[:8].double() @ w.double().t()
+    bias = (-exact[0]).bfloat16()
+    y = torch.empty(n, features, dtype=torch.bfloat16, device="cuda")
+    with group(1) as g:
+        ws = workspace(dt, "gather_linear", g, [n], dim, [features], False)
+        dt.dt_gather_linear(g, [x], [w], [bias], None, [y], [n], 0, dim, [features], 0, "bf16", "none", ws)
+        assert dt.dt_group_check(g) == dt.DT_OK
+    want = exact + bias.double()
+    off = (y[:8].double() - want).abs()
+    assert (off <= (dim * 2.0 ** -25 + 64 * 2.0 ** -23) * exact + 2.0 ** -8 * want.abs()).all()
+    if terms == "uniform":   # what the header calls usual, with half of it to spare
+        assert (off <= (dim * 7.5e-9 + 64 * 2.0 ** -23) * exact + 2.0 ** -8 * want.abs()).all()
