@@ -453,7 +453,9 @@ size_t dt_vocab_loss_workspace(dt_group_t g, const size_t *vocab, size_t vocab_e
  * tensor cores cut off what of a product lies below a quarter of the sum's last place:
  * a sum of n terms is off by n * 2^-25 of its largest part sum at most.  Terms of one
  * sign and like size come out n * 5e-9 of their sum too small, terms of both signs as
- * near as fp32's rounding.  Repeated calls give the same bits. */
+ * near as fp32's rounding.  Calls repeated on the same buffers give the same bits; the same
+ * values in others, aligned otherwise or with ranks' rows that follow one another where these
+ * do not, may be summed in another order. */
 #define DT_ACT_NONE 0
 #define DT_ACT_RELU 1
 #define DT_ACT_GELU 2 /* v * Phi(v), Phi the normal distribution (no tanh form) */

@@ -1,7 +1,7 @@
 // The linear layers' entry points with their launches taken out: what a call hands to the
 // tensor core kernels, on the host alone.  Every tile's loads have to go through a tensor map
-// that was made, the tiles have to cover every output once, and the parts of the workspace lie
-// within it.  Prints what it saw; nothing is launched.
+// that was made, the tiles have to cover every output once, and what a call lays out in the
+// workspace lies within it and apart.  Prints what it saw; nothing is launched.
 #include <cuda_runtime.h>
 
 static cudaError_t no_get_device(int *d) { *d = 0; return cudaSuccess; }
@@ -16,6 +16,7 @@ static cudaError_t no_memset(void *, int, size_t, cudaStream_t) { return cudaSuc
 
 #include <cstdio>
 #include <cstdlib>
+#include <vector>
 
 // What stands in a map's 128 bytes here; a map that was not made is zeros.
 struct Map {
@@ -27,10 +28,41 @@ static const unsigned char *workspace;
 static size_t workspace_bytes;
 static int launches, past_the_end, failures;
 
+// What a call writes to its workspace before and between its products.
+struct Part {
+    uint64_t from, to;
+};
+static std::vector<Part> parts;
+
 #define EXPECT(ok)                                                                    \
     do {                                                                              \
         if (!(ok) && ++failures <= 5) printf("line %d: %s\n", __LINE__, #ok);          \
     } while (0)
+
+static void part(const void *from, uint64_t bytes)
+{
+    if (bytes) parts.push_back(Part{(uint64_t)from, (uint64_t)from + bytes});
+}
+
+static void check_parts()
+{
+    const uint64_t lo = (uint64_t)workspace, hi = lo + workspace_bytes;
+    for (size_t i = 0; i < parts.size(); ++i) {
+        EXPECT(parts[i].from >= lo && parts[i].to <= hi);
+        for (size_t j = 0; j < i; ++j) EXPECT(parts[i].from >= parts[j].to || parts[j].from >= parts[i].to);
+    }
+}
+
+// A map of the workspace reads what was laid out there, which may be several ranks' rows as one.
+static void check_map(const Map &m)
+{
+    const uint64_t lo = (uint64_t)workspace, hi = lo + workspace_bytes, end = m.base + ((m.rows - 1) * m.pitch + m.cols) * 2;
+    if (m.made != kMade || m.base + 1 <= lo || m.base >= hi) return;
+    uint64_t at = m.base;
+    for (size_t i = 0; i < parts.size() && at < end; ++i)
+        if (parts[i].from <= at && at < parts[i].to) at = parts[i].to;
+    EXPECT(at >= end);
+}
 
 static const Map &of(const CUtensorMap &m) { return reinterpret_cast<const Map &>(m); }
 
@@ -42,6 +74,14 @@ static const Map &operand(const dt::LinearParams &p, int matrix, const dt::Place
     col = matrix == dt::kTok ? d.at : matrix == dt::kFeat ? f.at : R::w_by_feature ? d.at : f.at;
     row = matrix == dt::kTok ? t.at : matrix == dt::kFeat ? t.all : R::w_by_feature ? f.at : d.at;
     return of(matrix == dt::kTok ? p.tok[t.piece] : matrix == dt::kFeat ? p.feat[f.piece] : p.w[f.piece]);
+}
+
+static bool sums_at(const void *from, uint64_t bytes)
+{
+    uint64_t at = (uint64_t)from;
+    for (size_t i = 0; i < parts.size() && at < (uint64_t)from + bytes; ++i)
+        if (parts[i].from <= at && at < parts[i].to) at = parts[i].to;
+    return at >= (uint64_t)from + bytes;
 }
 
 template <class R>
@@ -78,10 +118,7 @@ static void walk(const dt::LinearParams &p, const dt::LinearProduct &c, bool pai
     for (int r = 0; r < p.P; ++r) features += p.f_len[r];
     auto all = [&](int axis) { return axis == dt::kDim ? (uint64_t)p.dim : axis == dt::kTokens ? (uint64_t)p.tokens : features; };
     EXPECT(rows == all(R::m) && cols == all(R::n) && deep == all(R::k));
-    if (c.splits > 1) {
-        const uint64_t from = reinterpret_cast<const unsigned char *>(c.acc) - workspace;
-        EXPECT(from + (uint64_t)c.splits * c.mt * halves * 128 * c.nt * p.bn * 4 <= workspace_bytes);
-    }
+    if (c.splits > 1) part(c.acc, (uint64_t)c.splits * c.mt * halves * 128 * c.nt * p.bn * 4);
 }
 
 namespace dt {
@@ -94,6 +131,13 @@ cudaError_t matrix_map(CUtensorMap *map, const void *base, uint64_t cols, uint64
 cudaError_t launch_linear(LinearParams &p, LinearKind kind, bool pairs, int, cudaStream_t)
 {
     ++launches;
+    for (int r = 0; r < p.P; ++r) {
+        check_map(of(p.tok[r]));
+        check_map(of(p.feat[r]));
+        check_map(of(p.w[r]));
+        if (p.sums.f32 && r < (p.sums.stacked ? 1 : p.sums.n) && p.sums.groups)   // sums of chunks are all there
+            EXPECT(!p.sums.cols[r] || sums_at(p.sums.src[r], (uint64_t)p.sums.rows[r] * p.sums.cols[r] * 4));
+    }
     switch (kind) {
     case kGather: walk<Roles<kGather, false>>(p, p.product[0], pairs); break;
     case kReduce: walk<Roles<kReduce, false>>(p, p.product[0], pairs); break;
@@ -105,12 +149,28 @@ cudaError_t launch_linear(LinearParams &p, LinearKind kind, bool pairs, int, cud
         walk<Roles<kReduceBack, false>>(p, p.product[0], pairs);
         walk<Roles<kReduceBack, true>>(p, p.product[1], pairs);
     }
+    check_parts();
+    parts.clear();
     return cudaSuccess;
 }
 cudaError_t launch_linear_join(const LinearParams &, LinearKind, int, bool, int, cudaStream_t) { return cudaSuccess; }
 cudaError_t launch_linear_few(LinearFew &, LinearKind, bool, int, cudaStream_t) { return cudaSuccess; }
 cudaError_t launch_linear_small(const LinearSmall &, LinearKind, bool, cudaStream_t) { return cudaSuccess; }
-cudaError_t launch_linear_prep(LinearPrep &, cudaStream_t) { return cudaSuccess; }
+cudaError_t launch_linear_prep(LinearPrep &p, cudaStream_t)
+{
+    EXPECT(p.jobs >= 1 && p.jobs <= kPrepJobs && p.chunk_rows % 32 == 0);
+    uint32_t blocks = 0;
+    for (int k = 0; k < p.jobs; ++k) {
+        const LinearPrepJob &j = p.job[k];
+        const uint32_t chunks = (j.rows + p.chunk_rows - 1) / p.chunk_rows;
+        EXPECT(j.rows && j.cols && j.pitch >= j.cols && j.pitch % 8 == 0 && j.strips == (j.cols + kPrepCols - 1) / kPrepCols);
+        EXPECT(j.block_end - blocks == chunks * j.strips && (j.dst || j.sums));
+        blocks = j.block_end;
+        if (j.dst) part(j.dst, (uint64_t)j.rows * j.pitch * 2);
+        if (j.sums) part(j.sums, (uint64_t)chunks * j.cols * 4);
+    }
+    return cudaSuccess;
+}
 uint32_t linear_workers(bool pairs, int) { return pairs ? 76 : 152; }
 
 }  // namespace dt

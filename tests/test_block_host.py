@@ -25,9 +25,12 @@ def test_residual_norm_of_every_number_of_ranks(tmp_path):
 
 def test_linear_layers_load_through_maps_that_were_made(tmp_path):
     """Each load of each tile of the four large products, for groups with ranks that have no tokens or no
-    features: a load through a tensor map that was never made would be an illegal instruction on a GPU."""
+    features: a load through a tensor map that was never made would be an illegal instruction on a GPU.
+    What a call lays out in its workspace lies within the query's bytes, apart, and where it is read."""
     exe = str(tmp_path / "host_linear")
-    res = subprocess.run([b.nvcc(), *b.ARCH, "-std=c++17", "-O1", "-I", b.INCLUDE, "-I", b.CSRC,
+    res = subprocess.run([b.nvcc(), *b.ARCH, "-std=c++17", "-O1",
+                          "-Xcompiler", "-fsanitize=bounds", "-Xcompiler", "-fsanitize-undefined-trap-on-error",
+                          "-I", b.INCLUDE, "-I", b.CSRC,
                           os.path.join(HERE, "host_linear.cu"), "-o", exe], capture_output=True, text=True)
     assert res.returncode == 0, res.stdout + res.stderr
     run = subprocess.run([exe], capture_output=True, text=True, timeout=300)
