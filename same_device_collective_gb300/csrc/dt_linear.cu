@@ -947,10 +947,9 @@ cudaError_t launch_linear(LinearParams &p, LinearKind kind, bool pairs, int devi
     }
 }
 
-cudaError_t launch_linear_join(const LinearParams &p, LinearKind kind, int k, bool pairs, int device, cudaStream_t s)
+cudaError_t launch_linear_join(const LinearParams &p, LinearKind kind, int k, bool pairs, cudaStream_t s)
 {
     const uint32_t high = pairs ? 2 * kM : kM;
-    (void)device;
     switch (kind) {
     case kGather: return launch_join<kGather, false>(p, high, s);
     case kGatherBack: return k ? launch_join<kGatherBack, true>(p, high, s) : launch_join<kGatherBack, false>(p, high, s);

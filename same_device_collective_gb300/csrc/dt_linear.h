@@ -153,7 +153,7 @@ constexpr uint32_t kFewTokens = 16;
 
 cudaError_t launch_linear(LinearParams &p, LinearKind kind, bool pairs, int device, cudaStream_t s);
 // The splits' sums into one, of product k.
-cudaError_t launch_linear_join(const LinearParams &p, LinearKind kind, int k, bool pairs, int device, cudaStream_t s);
+cudaError_t launch_linear_join(const LinearParams &p, LinearKind kind, int k, bool pairs, cudaStream_t s);
 // vec: every row that is read starts on a 16-byte boundary.
 cudaError_t launch_linear_few(LinearFew &p, LinearKind kind, bool vec, int device, cudaStream_t s);
 cudaError_t launch_linear_small(const LinearSmall &p, LinearKind kind, bool vec, cudaStream_t s);

@@ -153,7 +153,7 @@ cudaError_t launch_linear(LinearParams &p, LinearKind kind, bool pairs, int, cud
     parts.clear();
     return cudaSuccess;
 }
-cudaError_t launch_linear_join(const LinearParams &, LinearKind, int, bool, int, cudaStream_t) { return cudaSuccess; }
+cudaError_t launch_linear_join(const LinearParams &, LinearKind, int, bool, cudaStream_t) { return cudaSuccess; }
 cudaError_t launch_linear_few(LinearFew &, LinearKind, bool, int, cudaStream_t) { return cudaSuccess; }
 cudaError_t launch_linear_small(const LinearSmall &, LinearKind, bool, cudaStream_t) { return cudaSuccess; }
 cudaError_t launch_linear_prep(LinearPrep &p, cudaStream_t)
