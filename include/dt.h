@@ -459,7 +459,7 @@ size_t dt_vocab_loss_workspace(dt_group_t g, const size_t *vocab, size_t vocab_e
 #define DT_ACT_NONE 0
 #define DT_ACT_RELU 1
 #define DT_ACT_GELU 2 /* v * Phi(v), Phi the normal distribution (no tanh form) */
-#define DT_ACT_SILU 3 /* v / (1 + exp(-v)) */
+#define DT_ACT_SILU 3 /* v / (1 + exp(-v)); 0 below v = -87.3, where it is -1.1e-36 and nearer to 0 */
 
 /* y[r] = act(X weight[r]^T + bias[r]), X [n, dim] the tokens of all ranks:
  *   x[r]        rank r's tokens, [rows[r], dim]

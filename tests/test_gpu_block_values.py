@@ -134,3 +134,20 @@ def test_sums_of_one_sign(dt, n, features, dim, terms):
     assert (off <= (dim * 2.0 ** -25 + 64 * 2.0 ** -23) * exact + 2.0 ** -8 * want.abs()).all()
     if terms == "uniform":   # what the header calls usual, with half of it to spare
         assert (off <= (dim * 7.5e-9 + 64 * 2.0 ** -23) * exact + 2.0 ** -8 * want.abs()).all()
+
+
+@pytest.mark.parametrize("act,least", [("gelu", 1.2e-38), ("silu", 1.1e-36)])
+@pytest.mark.parametrize("n", [4, 70, 3000])
+def test_far_below_zero(dt, n, act, least):
+    """Every bf16 value from -120 to -2: an activation's exponential is off by 2^-16 of itself, its result is
+    rounded to bf16, and what lies below `least` may be 0."""
+    v = torch.arange(-2 ** 15, 0, device="cuda").to(torch.int16).view(torch.bfloat16)
+    v = v[(v >= -120) & (v <= -2)]
+    x = torch.ones(n, 1, dtype=torch.bfloat16, device="cuda")
+    y = torch.empty(n, len(v), dtype=torch.bfloat16, device="cuda")
+    with group(1) as g:
+        ws = workspace(dt, "gather_linear", g, [n], 1, [len(v)], False)
+        dt.dt_gather_linear(g, [x], [v[:, None].contiguous()], None, None, [y], [n], 0, 1, [len(v)], 0, "bf16", act, ws)
+    d = v.double()
+    want = d * torch.exp(torch.special.log_ndtr(d)) if act == "gelu" else d * torch.sigmoid(d)
+    assert ((y.double() - want).abs() <= (2.0 ** -8 + 2.0 ** -15) * want.abs() + least).all() and (y <= 0).all()
