@@ -416,7 +416,7 @@ dt_status dt_vocab_loss(dt_group_t g, const void *hidden, const void *const *wei
  * MiB, or 256 vocabulary rows' worth), every sum in fp32, and results are
  * rounded once.  The tensor cores cut off what of a product lies below a quarter of
  * the sum's last place: sums of n terms of one sign are about n * 5e-9 of themselves too
- * small beside that, and any n * 2^-25 of their largest part sum at most.
+ * small beside that, and any n * 2^-25 of their largest part sum or term at most.
  * Repeated calls give the same bits. */
 dt_status dt_vocab_loss_backward(dt_group_t g, const void *hidden, const void *const *weight,
                                  const size_t *vocab, size_t vocab_equal, const int32_t *targets,
@@ -451,8 +451,8 @@ size_t dt_vocab_loss_workspace(dt_group_t g, const size_t *vocab, size_t vocab_e
  * once `stream` has passed the call.  No output may overlap another buffer, but for
  * the residual below.  n is at most 2^26, dim and the sum of features 2^22.  The
  * tensor cores cut off what of a product lies below a quarter of the sum's last place:
- * a sum of n terms is off by n * 2^-25 of its largest part sum at most.  Terms of one
- * sign and like size come out n * 5e-9 of their sum too small, terms of both signs as
+ * a sum of n terms is off by n * 2^-25 of its largest part sum or term at most.  Terms of
+ * one sign and like size come out n * 5e-9 of their sum too small, terms of both signs as
  * near as fp32's rounding.  Calls repeated on the same buffers give the same bits; the same
  * values in others, aligned otherwise or with ranks' rows that follow one another where these
  * do not, may be summed in another order. */
